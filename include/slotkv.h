@@ -308,6 +308,174 @@ int decode_batch_attn_paged(slotkv_t handle, uint32_t B, uint32_t n_head, const 
                             slotkv_stream_t stream);
 
 /*
+ * slotkv_scores -- how a scored call treats its scores and which keys a row
+ * attends (soft-capped scores and sliding windows of the Gemma models,
+ * distance biases, packed documents, prefixes attended in both directions).
+ * For a row at position p, a key at position t and query head h:
+ *   s = scale * <q', K[t]>;
+ *   cap > 0:        s = cap * tanh(s / cap);
+ *   slopes given:   s = s - slopes[h] * |p - t|;
+ *   the row attends t iff lo <= t <= hi, where
+ *     lo = max(doc_start[row], p + 1 - window), each where given, else 0;
+ *     hi = p, or in a prefill with prefix_end: max(p, prefix_end[row] - 1).
+ * The sink logits are neither capped nor biased.  A row whose mask leaves
+ * nothing (doc_start[row] > hi) gets zeros; its K and V are written all the
+ * same.  Keys a row does not attend never affect it, whatever they hold
+ * (infinities and NaN included), unless noted at a call.
+ *   cap         0: none; else 1e-30 .. 1e30.
+ *   window      0: none; else keys t with p - t < window.
+ *   slopes      device [n_head], or NULL.
+ *   doc_start   device u32[rows], or NULL: the first key of the row's document.
+ *   prefix_end  device u32[rows], or NULL; prefills only (SLOTKV_ERR_ARG
+ *               elsewhere): the row attends every key below prefix_end[row]
+ *               (from lo on), later ones than its own included.  Those must
+ *               be in the slot or tokens of the call.  0: no prefix.  A row
+ *               with prefix_end[row] > slot_ctx is out of range.
+ * A NULL slotkv_scores pointer is the plain rule.  The struct is read during
+ * the call; its arrays are read by the kernels.
+ */
+typedef struct {
+    float cap;
+    uint32_t window;
+    const float* slopes;
+    const uint32_t* doc_start;
+    const uint32_t* prefix_end;
+} slotkv_scores;
+
+/*
+ * decode_batch_attn_scored, decode_batch_attn_paged_scored,
+ * prefill_batch_attn_scored -- the three calls above with a score rule.  The
+ * other arguments, their alignment, the options of slot_kv_set_options, the
+ * device flags and the errors are those of the plain call.  Only keys a row
+ * may attend are read (up to tile boundaries: a row's first tile starts at a
+ * multiple of 4096/head_dim keys), so a window bounds the work; in the paged
+ * call, table entries of blocks before the one holding the row's first key
+ * are not read, and those blocks may have been given away.
+ *
+ * The prefill runs head dims 64 and 128 on the tensor cores with tiles as
+ * prefill_batch_attn's, each reading the union of its rows' keys.  A call of
+ * few tiles (a chunk of a long prompt) also cuts each tile's keys into splits
+ * and joins them with one more kernel, so results depend on the batch in the
+ * last bits.  Its workspace is allocated by the handle's first such call
+ * (queries, items, and 128 * 4 partial rows per SM), at the size of max_rows
+ * and max_n_head: make one before capturing into a graph (a call under
+ * capture that would have to allocate returns SLOTKV_ERR_STATE and captures
+ * nothing).  Head dim 256 runs the scored decode kernel once per token.
+ */
+int decode_batch_attn_scored(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
+                             const float* k_new, const float* v_new, const uint32_t* positions,
+                             const uint32_t* slots, const float* q_norm_w,
+                             const float* k_norm_w, const float* inv_freq, const float* sinks,
+                             const slotkv_scores* scores, float* out, float eps, float scale,
+                             slotkv_stream_t stream);
+int decode_batch_attn_paged_scored(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
+                                   const float* k_new, const float* v_new,
+                                   const uint32_t* positions, const uint32_t* block_tables,
+                                   uint32_t bt_stride, const float* q_norm_w,
+                                   const float* k_norm_w, const float* inv_freq,
+                                   const float* sinks, const slotkv_scores* scores, float* out,
+                                   float eps, float scale, slotkv_stream_t stream);
+int prefill_batch_attn_scored(slotkv_t handle, uint32_t n_tok, uint32_t n_head, const float* q,
+                              const float* k_new, const float* v_new, const uint32_t* positions,
+                              const uint32_t* slots, const float* q_norm_w,
+                              const float* k_norm_w, const float* inv_freq, const float* sinks,
+                              const slotkv_scores* scores, float* out, float eps, float scale,
+                              slotkv_stream_t stream);
+
+/*
+ * decode_batch_attn_shared -- the decode step for rows that share long
+ * prefixes (a system prompt, a document): each prefix is kept once and its
+ * keys are read once for all the rows on it, by the tensor cores.
+ *
+ *   prefix        a handle that holds the prefixes, one per slot, filled by
+ *                 prefill_batch_attn or decode steps as any slot is; it has
+ *                 the same n_kv_head, head_dim and device as `handle`, its
+ *                 own n_slots and slot_ctx, and may be `handle` itself.  It
+ *                 is only read.
+ *   prefix_slots  device u32[B]: the prefix handle's slot with the row's prefix.
+ *   prefix_lens   device u32[B]: how many of the row's keys are there, positions
+ *                 0 .. prefix_lens[b] - 1 of that slot.  0: none (a plain row;
+ *                 prefix_slots[b] is then not read).
+ *   positions     the row's whole position p, prefix included; q' and k' are
+ *                 rotated at it.  Key p goes to position p - prefix_lens[b] of
+ *                 the row's own slot, which holds the keys after the prefix.
+ *   scores        a score rule, or NULL; positions in it count the prefix.
+ * The result is decode_batch_attn_scored's for a slot that held the prefix
+ * and the row's own keys one after the other, up to f32 rounding.  Rows of
+ * one prefix are best given one after another: consecutive rows with the same
+ * prefix slot are attended together, up to 128 / G of them (their lengths may
+ * differ); any order is correct.  Out of range, hence skipped with
+ * SLOTKV_DEV_RANGE: a row with slots[b] >= n_slots, positions[b] <
+ * prefix_lens[b], positions[b] - prefix_lens[b] >= slot_ctx, prefix_lens[b] >
+ * the prefix handle's slot_ctx, or, with prefix_lens[b] > 0, prefix_slots[b]
+ * >= its n_slots.  Flags are raised on `handle`.
+ *
+ * Head dims 64 and 128 (SLOTKV_ERR_UNSUPPORTED otherwise).  The prefix pass
+ * keeps a workspace in `handle`, allocated by the first call as
+ * prefill_batch_attn_scored's is (the same rule for captures), with a partial
+ * result per row and head besides.  Other errors as decode_batch_attn, and
+ * SLOTKV_ERR_ARG for a prefix handle of another shape, SLOTKV_ERR_STATE for
+ * one that is not allocated or on another device.
+ */
+int decode_batch_attn_shared(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
+                             const float* k_new, const float* v_new, const uint32_t* positions,
+                             const uint32_t* slots, slotkv_t prefix,
+                             const uint32_t* prefix_slots, const uint32_t* prefix_lens,
+                             const float* q_norm_w, const float* k_norm_w,
+                             const float* inv_freq, const float* sinks,
+                             const slotkv_scores* scores, float* out, float eps, float scale,
+                             slotkv_stream_t stream);
+
+/*
+ * slot_kv_token_map -- the index arrays of a batched prefill from the
+ * requests' lengths, on the device.  Request r adds fresh[r] tokens to slot
+ * slots[r], which holds past[r] positions; the requests' tokens follow one
+ * another.  Writes, for every r and i < fresh[r], with t = starts[r] + i:
+ *   starts[r] = fresh[0] + .. + fresh[r-1], and starts[n_req] the total;
+ *   tok_slots[t] = slots[r], tok_positions[t] = past[r] + i,
+ * what prefill_batch_attn takes as slots and positions.
+ *   n_req   requests, 0 .. SLOTKV_MAX_REQUESTS; slots, past, fresh: device u32[n_req].
+ *   n_tok   entries that tok_slots and tok_positions hold (device u32[n_tok]);
+ *           entries past the total are left as they are.
+ *   starts  device u32[n_req + 1].
+ * SLOTKV_DEV_RANGE is raised for a request with new tokens whose slot is >=
+ * n_slots or whose past[r] + fresh[r] passes slot_ctx (its tokens get slot
+ * 0xFFFFFFFF, which a prefill skips, so the others keep their places), and
+ * when the total passes n_tok (the tokens that fit are written).  Asynchronous,
+ * one kernel; errors SLOTKV_ERR_ARG (NULL or misaligned pointer, n_req too
+ * large), SLOTKV_ERR_STATE, SLOTKV_ERR_CUDA.
+ */
+#define SLOTKV_MAX_REQUESTS (1u << 20)
+int slot_kv_token_map(slotkv_t handle, uint32_t n_req, const uint32_t* slots,
+                      const uint32_t* past, const uint32_t* fresh, uint32_t n_tok,
+                      uint32_t* starts, uint32_t* tok_slots, uint32_t* tok_positions,
+                      slotkv_stream_t stream);
+
+/*
+ * slot_kv_extend_tables -- block tables extended from a free list, on the
+ * device, for decode_batch_attn_paged: the handle is the pool, slot_ctx its
+ * block size bs.  Request r has past[r] keys in ceil(past[r] / bs) blocks and
+ * is about to add fresh[r] (1 for a decode step).  In request order, the
+ * entries ceil(past[r] / bs) .. ceil((past[r] + fresh[r]) / bs) - 1 of its row
+ * of block_tables take the next ids of the free list:
+ *   block_tables  device u32[n_req][bt_stride], in place; no other entry is
+ *                 written.
+ *   free_blocks   device u32[n_free]; ids are taken from free_blocks[head[0]]
+ *                 on, as they stand (a paged call checks them).
+ *   head          device u32[1]; head_out, device u32[1], receives head[0] plus
+ *                 the ids taken.  head_out may be head, so that a captured
+ *                 step can be replayed.
+ * A request whose blocks would pass bt_stride takes none; one that the rest
+ * of the free list cannot serve whole takes none either, nor does any later
+ * one that needs some.  Each raises SLOTKV_DEV_RANGE.  Asynchronous, one
+ * kernel; errors as slot_kv_token_map, and SLOTKV_ERR_ARG for bt_stride = 0.
+ */
+int slot_kv_extend_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
+                          const uint32_t* fresh, uint32_t* block_tables, uint32_t bt_stride,
+                          const uint32_t* free_blocks, uint32_t n_free, const uint32_t* head,
+                          uint32_t* head_out, slotkv_stream_t stream);
+
+/*
  * decode_batch_attn_host -- decode_batch_attn for callers whose per-step
  * inputs and output live in host memory.  q, k_new, v_new, positions, slots
  * and out are HOST pointers with the layouts above; q_norm_w, k_norm_w,

@@ -13,7 +13,11 @@ The functions mirror the C ABI in ``include/slotkv.h`` name for name
 ``prefill_batch_attn`` and its host-buffer form ``prefill_batch_attn_host``
 (with ``slot_kv_prefill_host_parts``), ``decode_batch_attn_paged`` and its
 host-buffer form ``decode_batch_attn_paged_host``, the allocation-free
-``decode_batch_attn_noalloc``), multi-step support
+``decode_batch_attn_noalloc``), the step with a score rule (``Scores``:
+``decode_batch_attn_scored``, ``decode_batch_attn_paged_scored``,
+``prefill_batch_attn_scored``) and over shared prefixes
+(``decode_batch_attn_shared``), index arrays from request lengths
+(``slot_kv_token_map``, ``slot_kv_extend_tables``), multi-step support
 (``slot_kv_advance_positions``), and control (``slot_kv_get_status``,
 ``slot_kv_set_split``, ``slot_kv_set_options``, ``slot_kv_call_shape``).
 ``SlotKV`` wraps a handle.
@@ -26,7 +30,9 @@ __all__ = [
     "slot_kv_reset", "decode_batch_attn", "decode_batch_attn_host", "prefill_batch_attn",
     "prefill_batch_attn_host", "slot_kv_prefill_host_parts", "PREFILL_HOST_MAX_PARTS",
     "decode_batch_attn_paged", "decode_batch_attn_paged_host", "decode_batch_attn_noalloc",
-    "slot_kv_advance_positions",
+    "Scores", "decode_batch_attn_scored", "decode_batch_attn_paged_scored",
+    "prefill_batch_attn_scored", "decode_batch_attn_shared", "slot_kv_token_map",
+    "slot_kv_extend_tables", "slot_kv_advance_positions",
     "slot_kv_get_status", "slot_kv_set_split", "HostCall", "LIB_PATH", "EXPORTS", "DEV_RANGE",
     "DEV_TIMEOUT", "OPT_VNORM", "OPT_NORM_PLUS_ONE", "OPT_TEST_STALL",
 ]
@@ -41,6 +47,15 @@ PREFILL_HOST_MAX_PARTS = 8  # SLOTKV_PREFILL_HOST_MAX_PARTS
 SIZE_MAX = ctypes.c_size_t(-1).value
 
 _u32, _f32, _vp, _int = ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+
+
+class _CScores(ctypes.Structure):
+    """slotkv_scores"""
+    _fields_ = [("cap", _f32), ("window", _u32), ("slopes", _vp), ("doc_start", _vp),
+                ("prefix_end", _vp)]
+
+
+_SCP = ctypes.POINTER(_CScores)
 _DECODE_ARGS = [_vp, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                 _f32, _f32, _vp]
 EXPORTS = {
@@ -62,6 +77,16 @@ EXPORTS = {
                                  _vp, _vp, _f32, _f32, _vp], _int),
     "decode_batch_attn_paged_host": ([_vp, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _u32, _vp, _vp,
                                       _vp, _vp, _vp, _f32, _f32, _vp], _int),
+    "decode_batch_attn_scored": ([_vp, _u32, _u32] + [_vp] * 9 + [_SCP, _vp, _f32, _f32, _vp],
+                                 _int),
+    "decode_batch_attn_paged_scored": ([_vp, _u32, _u32] + [_vp] * 5 + [_u32] + [_vp] * 4 +
+                                       [_SCP, _vp, _f32, _f32, _vp], _int),
+    "prefill_batch_attn_scored": ([_vp, _u32, _u32] + [_vp] * 9 + [_SCP, _vp, _f32, _f32, _vp],
+                                  _int),
+    "decode_batch_attn_shared": ([_vp, _u32, _u32] + [_vp] * 12 +
+                                 [_SCP, _vp, _f32, _f32, _vp], _int),
+    "slot_kv_token_map": ([_vp, _u32, _vp, _vp, _vp, _u32, _vp, _vp, _vp, _vp], _int),
+    "slot_kv_extend_tables": ([_vp, _u32, _vp, _vp, _vp, _u32, _vp, _u32, _vp, _vp, _vp], _int),
     "slot_kv_get_status": ([_vp, _vp, ctypes.POINTER(_u32)], _int),
     "slot_kv_set_split": ([_vp, _u32, _u32], _int),
     "slot_kv_call_shape": ([_vp, _u32, _u32, _u32, ctypes.POINTER(_u32), ctypes.POINTER(_u32),
@@ -172,6 +197,40 @@ def _stream_ptr(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+class Scores:
+    """A score rule (slotkv_scores): tanh cap, window, per-head slopes of the
+    distance bias (float32 [n_head]), the rows' document starts and, in a
+    prefill, prefix ends (int32 [rows]); CUDA tensors, kept referenced."""
+
+    def __init__(self, cap=0.0, window=0, slopes=None, doc_start=None, prefix_end=None):
+        import torch
+        if not 0 <= int(window) < 2 ** 32:
+            raise ValueError("window must be 0 .. 2^32 - 1")
+        self.slopes, self.doc_start, self.prefix_end = slopes, doc_start, prefix_end
+        self._c = _CScores(cap, int(window), _ptr(slopes, torch.float32, "slopes"),
+                           _ptr(doc_start, torch.int32, "doc_start"),
+                           _ptr(prefix_end, torch.int32, "prefix_end"))
+
+    @property
+    def cap(self):
+        return self._c.cap
+
+    @property
+    def window(self):
+        return self._c.window
+
+
+def _scores(sc, rows, n_head):
+    """The struct pointer of a Scores for a step of ``rows`` rows; None stays NULL."""
+    if sc is None:
+        return None
+    for name, t, n in (("slopes", sc.slopes, n_head), ("doc_start", sc.doc_start, rows),
+                       ("prefix_end", sc.prefix_end, rows)):
+        if t is not None and _shape(t) != (n,):
+            raise ValueError(f"{name} has shape {_shape(t)}, expected {(n,)}")
+    return ctypes.byref(sc._c)
 
 
 class SlotKV:
@@ -327,6 +386,122 @@ class SlotKV:
             "decode_batch_attn_paged_host")
         return out
 
+    def decode_batch_attn_scored(self, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                                 inv_freq, sinks, scores, out, eps, scale, stream=None):
+        """As decode_batch_attn, with a score rule (Scores, or None)."""
+        return self._slot_step_scored("decode_batch_attn_scored", q, k_new, v_new, positions,
+                                      slots, q_norm_w, k_norm_w, inv_freq, sinks, scores, out,
+                                      eps, scale, stream)
+
+    def prefill_batch_attn_scored(self, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                                  inv_freq, sinks, scores, out, eps, scale, stream=None):
+        """As prefill_batch_attn, with a score rule (Scores, or None)."""
+        return self._slot_step_scored("prefill_batch_attn_scored", q, k_new, v_new, positions,
+                                      slots, q_norm_w, k_norm_w, inv_freq, sinks, scores, out,
+                                      eps, scale, stream)
+
+    def _slot_step_scored(self, name, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                          inv_freq, sinks, scores, out, eps, scale, stream):
+        import torch
+        B, n_head = _check_step(q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w,
+                                inv_freq, sinks, self.n_kv_head, self.head_dim)
+        f, u = torch.float32, torch.int32
+        _check(getattr(_lib, name)(
+            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
+            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"), _ptr(slots, u, "slots"),
+            _ptr(q_norm_w, f, "q_norm_w"), _ptr(k_norm_w, f, "k_norm_w"),
+            _ptr(inv_freq, f, "inv_freq"), _ptr(sinks, f, "sinks"),
+            _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale, _stream_ptr(stream)),
+            name)
+        return out
+
+    def decode_batch_attn_paged_scored(self, q, k_new, v_new, positions, block_tables, q_norm_w,
+                                       k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                                       stream=None):
+        """As decode_batch_attn_paged, with a score rule (Scores, or None)."""
+        import torch
+        B, n_head = _check_step(q, k_new, v_new, positions, block_tables, out, q_norm_w,
+                                k_norm_w, inv_freq, sinks, self.n_kv_head, self.head_dim,
+                                idx_name="block_tables")
+        f, u = torch.float32, torch.int32
+        if block_tables.dim() != 2 or int(block_tables.shape[0]) != B:
+            raise ValueError("block_tables must be [B][max_blocks]")
+        _check(_lib.decode_batch_attn_paged_scored(
+            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
+            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"),
+            _ptr(block_tables, u, "block_tables"), int(block_tables.shape[1]),
+            _ptr(q_norm_w, f, "q_norm_w"), _ptr(k_norm_w, f, "k_norm_w"),
+            _ptr(inv_freq, f, "inv_freq"), _ptr(sinks, f, "sinks"),
+            _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale, _stream_ptr(stream)),
+            "decode_batch_attn_paged_scored")
+        return out
+
+    def decode_batch_attn_shared(self, q, k_new, v_new, positions, slots, prefix, prefix_slots,
+                                 prefix_lens, q_norm_w, k_norm_w, inv_freq, sinks, scores, out,
+                                 eps, scale, stream=None):
+        """The decode step for rows on shared prefixes: row b's positions
+        0 .. prefix_lens[b] - 1 are in slot prefix_slots[b] of the SlotKV
+        ``prefix``, the later ones in its own slot from position 0 on."""
+        import torch
+        B, n_head = _check_step(q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w,
+                                inv_freq, sinks, self.n_kv_head, self.head_dim)
+        for name, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
+            if t is None or _shape(t) != (B,):
+                raise ValueError(f"{name} must be [B]")
+        if not isinstance(prefix, SlotKV):
+            raise TypeError("prefix must be a SlotKV")
+        f, u = torch.float32, torch.int32
+        _check(_lib.decode_batch_attn_shared(
+            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
+            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"), _ptr(slots, u, "slots"),
+            prefix._h, _ptr(prefix_slots, u, "prefix_slots"),
+            _ptr(prefix_lens, u, "prefix_lens"), _ptr(q_norm_w, f, "q_norm_w"),
+            _ptr(k_norm_w, f, "k_norm_w"), _ptr(inv_freq, f, "inv_freq"),
+            _ptr(sinks, f, "sinks"), _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale,
+            _stream_ptr(stream)), "decode_batch_attn_shared")
+        return out
+
+    def token_map(self, slots, past, fresh, starts, tok_slots, tok_positions, stream=None):
+        """slot_kv_token_map: the slots and positions of a prefill's tokens from
+        the requests' (slot, cached length, new length), int32 CUDA tensors."""
+        import torch
+        u, n = torch.int32, int(slots.numel())
+        for name, t, shape in (("slots", slots, (n,)), ("past", past, (n,)),
+                               ("fresh", fresh, (n,)), ("starts", starts, (n + 1,)),
+                               ("tok_positions", tok_positions, _shape(tok_slots))):
+            if _shape(t) != shape or len(shape) != 1:
+                raise ValueError(f"{name} has shape {_shape(t)}, expected {shape}")
+        _check(_lib.slot_kv_token_map(
+            self._h, n, _ptr(slots, u, "slots"), _ptr(past, u, "past"), _ptr(fresh, u, "fresh"),
+            int(tok_slots.numel()), _ptr(starts, u, "starts"), _ptr(tok_slots, u, "tok_slots"),
+            _ptr(tok_positions, u, "tok_positions"), _stream_ptr(stream)), "slot_kv_token_map")
+        return starts, tok_slots, tok_positions
+
+    def extend_tables(self, past, fresh, block_tables, free_blocks, head, head_out=None,
+                      stream=None):
+        """slot_kv_extend_tables: block_tables (int32 [requests][max_blocks], in
+        place) extended from the free list; head_out None advances ``head``
+        itself.  int32 CUDA tensors."""
+        import torch
+        u, n = torch.int32, int(past.numel())
+        if head_out is None:
+            head_out = head
+        if block_tables.dim() != 2 or int(block_tables.shape[0]) != n:
+            raise ValueError("block_tables must be [requests][max_blocks]")
+        for name, t, shape in (("past", past, (n,)), ("fresh", fresh, (n,)),
+                               ("head", head, (1,)), ("head_out", head_out, (1,))):
+            if _shape(t) != shape:
+                raise ValueError(f"{name} has shape {_shape(t)}, expected {shape}")
+        if free_blocks.dim() != 1:
+            raise ValueError("free_blocks must be [n_free]")
+        _check(_lib.slot_kv_extend_tables(
+            self._h, n, _ptr(past, u, "past"), _ptr(fresh, u, "fresh"),
+            _ptr(block_tables, u, "block_tables"), int(block_tables.shape[1]),
+            _ptr(free_blocks, u, "free_blocks"), int(free_blocks.numel()),
+            _ptr(head, u, "head"), _ptr(head_out, u, "head_out"), _stream_ptr(stream)),
+            "slot_kv_extend_tables")
+        return block_tables, head_out
+
     def prepare_host_call(self, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
                           inv_freq, sinks, out, eps, scale, block_tables=None):
         """A prepared host step (slot_kv_host_call_create): the arguments of
@@ -446,6 +621,43 @@ def decode_batch_attn_paged(h, q, k_new, v_new, positions, block_tables, q_norm_
                             inv_freq, sinks, out, eps, scale, stream=None):
     return h.decode_batch_attn_paged(q, k_new, v_new, positions, block_tables, q_norm_w,
                                      k_norm_w, inv_freq, sinks, out, eps, scale, stream)
+
+
+def decode_batch_attn_scored(h, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w, inv_freq,
+                             sinks, scores, out, eps, scale, stream=None):
+    return h.decode_batch_attn_scored(q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                                      inv_freq, sinks, scores, out, eps, scale, stream)
+
+
+def decode_batch_attn_paged_scored(h, q, k_new, v_new, positions, block_tables, q_norm_w,
+                                   k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                                   stream=None):
+    return h.decode_batch_attn_paged_scored(q, k_new, v_new, positions, block_tables, q_norm_w,
+                                            k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                                            stream)
+
+
+def prefill_batch_attn_scored(h, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w, inv_freq,
+                              sinks, scores, out, eps, scale, stream=None):
+    return h.prefill_batch_attn_scored(q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                                       inv_freq, sinks, scores, out, eps, scale, stream)
+
+
+def decode_batch_attn_shared(h, q, k_new, v_new, positions, slots, prefix, prefix_slots,
+                             prefix_lens, q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps,
+                             scale, stream=None):
+    return h.decode_batch_attn_shared(q, k_new, v_new, positions, slots, prefix, prefix_slots,
+                                      prefix_lens, q_norm_w, k_norm_w, inv_freq, sinks, scores,
+                                      out, eps, scale, stream)
+
+
+def slot_kv_token_map(h, slots, past, fresh, starts, tok_slots, tok_positions, stream=None):
+    return h.token_map(slots, past, fresh, starts, tok_slots, tok_positions, stream)
+
+
+def slot_kv_extend_tables(h, past, fresh, block_tables, free_blocks, head, head_out=None,
+                          stream=None):
+    return h.extend_tables(past, fresh, block_tables, free_blocks, head, head_out, stream)
 
 
 class HostCall:

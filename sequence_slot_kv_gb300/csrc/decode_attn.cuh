@@ -53,6 +53,15 @@
 // (looked up one tile ahead), and the plan (or, for a static item, the
 // producer warp) checks every used table entry.
 //
+// Scored calls (template parameter SC; parameters ScoredDecodeParams) are the
+// same kernels with the score rule of score_rule.cuh: a row's keys start at
+// the tile holding its first attended key instead of key 0, keys before that
+// first key are masked, and each score is capped and biased once it has been
+// reduced, on the lanes that hold it.  In a shared call (shared.lens set) the
+// row's slot holds its positions from prefix_lens[b] on, q and k' are rotated
+// at positions[b], and the consumers of a row's split 0 fold in the partials
+// that the prefix pass left (params.h, Partials).
+//
 // Every wait on an mbarrier is bounded; on expiry the CTA raises
 // SLOTKV_DEV_TIMEOUT, drains its own copies in flight (bounded) and returns.
 #pragma once
@@ -65,6 +74,7 @@
 #include <atomic>
 
 #include "params.h"
+#include "score_rule.cuh"
 
 namespace slotkv {
 
@@ -184,8 +194,9 @@ struct KCfg {
 
 // What the producer tells the other warps about an item.
 // prow: row of key p in the [rows][kv_dim] view of the K and V buffers.
+// lo: first key attended (scored calls only).
 struct ItemDesc {
-    uint32_t b, kvh, split, nsplit, p, prow, k0, hist_end, ntiles, is_last, end, pad;
+    uint32_t b, kvh, split, nsplit, p, prow, k0, hist_end, ntiles, is_last, end, lo;
 };
 
 // A finished multi-split partial handed to the merge warp.
@@ -344,13 +355,25 @@ __device__ __forceinline__ void scale_e(float c, float (&acc)[E]) {
     }
 }
 
-template <int HD, int G, int E, int L, int NR>
+// How a scored call's lane treats its scores: the cap's constants, the
+// distance p - t of each key row of the tile at hand as p minus (key of row
+// 0) minus the row, and the slopes of the lane's heads (times log2 e).
+template <int N>
+struct LaneRule {
+    float cap_in, cap_out;
+    bool bias;
+    int d0;
+    float slope[N];
+};
+
+template <int HD, int G, int E, int L, int NR, bool SC = false>
 __device__ __forceinline__ void attend_rows(const float* __restrict__ Kt,
                                             const float* __restrict__ Vt,
                                             const int (&row)[NR], const bool (&valid)[NR],
                                             const int li, const float (&q)[G][E],
                                             float (&m)[G], float (&l)[G],
-                                            float (&acc)[G][E]) {
+                                            float (&acc)[G][E],
+                                            const LaneRule<G>* rule = nullptr) {
     float s[NR][G];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -378,7 +401,12 @@ __device__ __forceinline__ void attend_rows(const float* __restrict__ Kt,
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) s[r][h] = valid[r] ? s[r][h] : -CUDART_INF_F;
+        for (int h = 0; h < G; ++h) {
+            if constexpr (SC)
+                s[r][h] = apply_rule(s[r][h], rule->cap_in, rule->cap_out, rule->slope[h],
+                                     rule->bias, rule->d0 - row[r]);
+            s[r][h] = valid[r] ? s[r][h] : -CUDART_INF_F;
+        }
     }
     // online softmax in base 2: rescale only when the running max grows
 #pragma unroll
@@ -408,7 +436,8 @@ __device__ __forceinline__ void attend_rows(const float* __restrict__ Kt,
             }
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-                const float pr = exp2f(s[r][h] - m[h]);
+                // (a bias may take a score to -inf, and a first one at that)
+                const float pr = SC && s[r][h] == -CUDART_INF_F ? 0.f : exp2f(s[r][h] - m[h]);
                 l[h] += pr;
                 axpy_e<E>(pr, vv, acc[h]);
             }
@@ -430,14 +459,15 @@ __device__ __forceinline__ void attend_rows(const float* __restrict__ Kt,
 // across the lanes holding the same heads for other keys), acc as usual.
 // The running max is lazy: it is raised (and acc, l rescaled) only when a
 // score exceeds it by more than 2^8, so every probability stays <= 2^8.
-template <int HD, int G, int E, int L, int NR, int GP, int CNT>
+template <int HD, int G, int E, int L, int NR, int GP, int CNT, bool SC = false>
 __device__ __forceinline__ void attend_rows_tr(const float* __restrict__ Kt,
                                                const float* __restrict__ Vt,
                                                const int (&row)[NR], const bool (&valid)[NR],
                                                const int li, const int lane,
                                                const float (&q)[G][E], float (&m_t)[CNT],
                                                float (&l_t)[CNT], float (&acc)[G][E],
-                                               float* __restrict__ pg) {
+                                               float* __restrict__ pg,
+                                               const LaneRule<CNT>* rule = nullptr) {
     constexpr int NV = NR * GP;
     constexpr int REP = NV >= L ? 1 : L / NV;  // lanes holding each score
     constexpr float kLazy = 8.0f;
@@ -478,9 +508,18 @@ __device__ __forceinline__ void attend_rows_tr(const float* __restrict__ Kt,
 #pragma unroll
     for (int r = 1; r < NR; ++r)
         if (my_r == r) my_valid = valid[r];
+    int my_d = 0;
+    if constexpr (SC) {
+        my_d = rule->d0 - row[0];
+#pragma unroll
+        for (int r = 1; r < NR; ++r)
+            if (my_r == r) my_d = rule->d0 - row[r];
+    }
     float mx[CNT];
 #pragma unroll
     for (int j = 0; j < CNT; ++j) {
+        if constexpr (SC)
+            s[j] = apply_rule(s[j], rule->cap_in, rule->cap_out, rule->slope[j], rule->bias, my_d);
         s[j] = my_valid ? s[j] : -CUDART_INF_F;
         mx[j] = s[j];
     }
@@ -545,6 +584,22 @@ __device__ __forceinline__ void attend_rows_tr(const float* __restrict__ Kt,
             for (int h = 0; h < G; ++h) axpy_e<E>(pr[r * GP + h], vv, acc[h]);
         }
     }
+}
+
+// The lane rule of a scored call for kv head kvh: in the transposed scheme
+// the slopes of the CNT heads this lane's scores belong to (GP-padded heads
+// get none), in the replicated one those of all G heads.
+template <int G, int N>
+__device__ __forceinline__ LaneRule<N> lane_rule(const ScoreRule& r, uint32_t kvh, int h0) {
+    LaneRule<N> x;
+    x.cap_in = r.cap_in;
+    x.cap_out = r.cap_out;
+    x.bias = r.slopes != nullptr;
+    x.d0 = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        x.slope[j] = x.bias && h0 + j < G ? __ldg(r.slopes + kvh * G + h0 + j) * kRuleLog2e : 0.f;
+    return x;
 }
 
 // The per-lane state of attend_rows_tr turned into the replicated form of
@@ -628,6 +683,40 @@ __device__ __forceinline__ void merge_stats(const float* ml0, size_t hstride, in
 // empty partial (m = -inf) weighing 0 even when M is -inf too.
 __device__ __forceinline__ float partial_weight(float m, float M) {
     return m == -CUDART_INF_F ? 0.f : exp2f(m - M);
+}
+
+// Fold prefix partials first, first + step, ... of row b into a warp's merged
+// state (merge_warp_groups done: lane holds EF elements at dims dim(t) of each
+// head), in that order.  A row without a prefix has no splits.
+template <int HD, int G, int EF, int E, typename Dim>
+__device__ __forceinline__ void fold_partials(const Partials& part, uint4 rec, uint32_t n_head,
+                                              uint32_t hq0, uint32_t first, uint32_t step,
+                                              float (&m)[G], float (&l)[G], float (&acc)[G][E],
+                                              Dim dim) {
+    for (uint32_t s = first; s < rec.z; s += step) {
+        const size_t at = (static_cast<size_t>(rec.x) + static_cast<size_t>(s) * rec.y) * n_head + hq0;
+        float2 ml[G];
+        float2 v[G][EF / 2];
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            ml[h] = __ldcg(reinterpret_cast<const float2*>(part.ml) + at + h);
+#pragma unroll
+            for (int t = 0; t < EF; t += 2)
+                v[h][t / 2] = __ldcg(reinterpret_cast<const float2*>(part.acc + (at + h) * HD + dim(t)));
+        }
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const float M = fmaxf(m[h], ml[h].x);
+            const float c1 = partial_weight(m[h], M), c2 = partial_weight(ml[h].x, M);
+            l[h] = __fmaf_rn(l[h], c1, __fmul_rn(ml[h].y, c2));
+#pragma unroll
+            for (int t = 0; t < EF; t += 2) {
+                acc[h][t] = __fmaf_rn(acc[h][t], c1, __fmul_rn(v[h][t / 2].x, c2));
+                acc[h][t + 1] = __fmaf_rn(acc[h][t + 1], c1, __fmul_rn(v[h][t / 2].y, c2));
+            }
+            m[h] = M;
+        }
+    }
 }
 
 // Merge the (m, l, acc) states of a warp's 32 / L key groups by halving: at
@@ -751,14 +840,16 @@ __device__ __forceinline__ void warp_rms_norm_plain(const float* src, float* dst
 constexpr int kPlanBins = 64;
 constexpr int kPlanMaxRows = 65536;
 
-template <int T>
-__global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const DecodeParams P) {
+template <int T, bool SC = false>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    slotkv_plan_kernel(const decode_params_t<SC> P) {
     __shared__ uint32_t bin_count[kPlanBins];
     __shared__ uint32_t bin_cursor[kPlanBins];
     __shared__ uint32_t total;
     __shared__ uint32_t row_bad[kPlanMaxRows / 32];  // paged mode: rows failing the check
     // one round of rows (one per thread) handed from reservation to writing
     __shared__ uint32_t sh_p[kPlanThreads], sh_prow[kPlanThreads], sh_meta[kPlanThreads];
+    __shared__ uint32_t sh_lo[SC ? kPlanThreads : 1];
     __shared__ uint32_t sh_fb[kPlanThreads], sh_lb[kPlanThreads];
     __shared__ uint32_t sh_nf[kPlanThreads], sh_nl[kPlanThreads];
     // The plan kernel is a programmatic dependent of whatever precedes it on
@@ -779,6 +870,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
         constexpr int RW = 4;
         for (uint32_t b0 = warp * RW; b0 < P.B; b0 += (kPlanThreads / 32) * RW) {
             uint32_t used[RW];
+            [[maybe_unused]] uint32_t first[RW];  // scored: blocks before a row's keys are not read
             bool bad[RW];
             const uint32_t* tab[RW];
             uint32_t most = 0;
@@ -789,6 +881,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
                 bad[u] = b < P.B && static_cast<uint64_t>(p) >=
                                         static_cast<uint64_t>(P.bt_stride) * P.slot_ctx;
                 used[u] = (b < P.B && !bad[u]) ? p / P.slot_ctx + 1 : 0u;
+                if constexpr (SC)
+                    first[u] = used[u] ? row_base(rule_first(P.rule, b, p), p, T) / P.slot_ctx : 0u;
                 tab[u] = P.block_tables + static_cast<size_t>(b < P.B ? b : 0) * P.bt_stride;
                 most = used[u] > most ? used[u] : most;
             }
@@ -799,7 +893,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         const uint32_t i = i0 + v * 32 + lane;
-                        id[u][v] = i < used[u] ? __ldg(tab[u] + i) : 0u;
+                        bool need = i < used[u];
+                        if constexpr (SC) need = need && i >= first[u];
+                        id[u][v] = need ? __ldg(tab[u] + i) : 0u;
                     }
 #pragma unroll
                 for (int u = 0; u < RW; ++u) bad[u] |= id[u][0] >= P.n_slots || id[u][1] >= P.n_slots;
@@ -820,22 +916,42 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
     // static_second pairs when the row has a second split).
     struct Shape {
         uint32_t p, prow, nsplit, ft, lt, nfull, nlast, ns, ns1;
+        uint32_t lo;  // scored: first key attended
     };
     auto row_shape = [&](uint32_t b, Shape& r) {
+        [[maybe_unused]] uint32_t hi = 0;
         r.p = P.positions[b];
         if (paged) {
             if (row_bad[b >> 5] & (1u << (b & 31))) return false;
             r.prow = __ldg(P.block_tables + static_cast<size_t>(b) * P.bt_stride +
                            r.p / P.slot_ctx) * P.slot_ctx + r.p % P.slot_ctx;
+            r.lo = 0;
+            if constexpr (SC) r.lo = rule_first(P.rule, b, r.p);
         } else {
             const uint32_t slot = P.slots[b];
-            if (slot >= P.n_slots || r.p >= P.slot_ctx) return false;
+            if constexpr (SC) {
+                const ScoredRow x = scored_row(P.rule, P.shared, b, r.p, P.slot_ctx,
+                                               slot < P.n_slots, P.prefill != 0);
+                if (!x.ok) return false;
+                r.p = x.p;
+                r.lo = x.lo;
+                hi = x.hi;
+            } else {
+                if (slot >= P.n_slots || r.p >= P.slot_ctx) return false;
+            }
             r.prow = slot * P.slot_ctx + r.p;
         }
-        const uint32_t chunk = split_chunk(r.p + 1, P.chunk_min, P.max_splits, T);
-        r.nsplit = (r.p + 1 + chunk - 1) / chunk;
+        uint32_t end = r.p;  // keys [base, end], plus none past key p
+        uint32_t base = 0;
+        if constexpr (SC) {
+            if (!paged) end = hi;
+            base = row_base(r.lo, end, T);
+        }
+        const uint32_t n = end + 1 - base;
+        const uint32_t chunk = split_chunk(n, P.chunk_min, P.max_splits, T);
+        r.nsplit = (n + chunk - 1) / chunk;
         r.ft = chunk / T;
-        r.lt = (r.p + (P.prefill ? 1u : 0u) - (r.nsplit - 1) * chunk + T - 1) / T;
+        r.lt = (n - (P.prefill ? 0u : 1u) - (r.nsplit - 1) * chunk + T - 1) / T;
         const uint32_t first = b * nkv;
         r.ns = P.static_items > first
                    ? (P.static_items - first < nkv ? P.static_items - first : nkv)
@@ -898,6 +1014,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
             if (ok) {
                 sh_p[tid] = r.p;
                 sh_prow[tid] = r.prow;
+                if constexpr (SC) sh_lo[tid] = r.lo;
                 sh_nf[tid] = r.nfull;
                 sh_nl[tid] = r.nlast;
                 sh_fb[tid] = r.nfull ? atomicAdd(&bin_cursor[bin_of(r.ft)], r.nfull) : 0u;
@@ -915,6 +1032,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
             const uint32_t row = r0 + i, nsplit = m & 511u, ns = (m >> 9) & 511u, ns1 = m >> 18;
             const uint32_t p = sh_p[i], prow = sh_prow[i];
             const uint32_t nfull = sh_nf[i], nlast = sh_nl[i], fb = sh_fb[i], lb = sh_lb[i];
+            const uint32_t lo = SC ? sh_lo[SC ? i : 0] : 0u;
             // listed full splits, in (split, kv head) order: split 0 from kv
             // head ns, split 1 from ns1 (when it is not the last split), the
             // rest whole; listed last splits: kv heads nkv - nlast .. nkv - 1
@@ -931,10 +1049,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
                     split = 2 + kvh / nkv;
                     kvh %= nkv;
                 }
-                recs[fb + j] = make_uint4(pack_item(row, split, kvh), p, prow, 0u);
+                recs[fb + j] = make_uint4(pack_item(row, split, kvh), p, prow, lo);
             }
             for (uint32_t j = lane; j < nlast; j += 32)
-                recs[lb + j] = make_uint4(pack_item(row, nsplit - 1, j + (nkv - nlast)), p, prow, 0u);
+                recs[lb + j] = make_uint4(pack_item(row, nsplit - 1, j + (nkv - nlast)), p, prow, lo);
         }
         __syncthreads();
     }
@@ -945,11 +1063,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) slotkv_plan_kernel(const Deco
 }
 
 // ------------------------------------------------------------------ decode
-template <int HD, int G>
+template <int HD, int G, bool SC = false>
 __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
     slotkv_decode_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                               const __grid_constant__ CUtensorMap tmV,
-                              const DecodeParams P) {
+                              const decode_params_t<SC> P) {
     using C = KCfg<HD, G>;
     constexpr int E = C::E, L = C::L, NG = C::NG, R = C::R, T = C::T, S = C::S, W = C::W;
     constexpr int NMS = C::NMS;
@@ -992,9 +1110,17 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
     const uint32_t st_split = blockIdx.x < P.static_items ? 0u : 1u;
     const uint32_t st_row = (blockIdx.x - st_split * P.static_items) / P.n_kv_head;
     uint32_t pre_p = 0, pre_slot = 0;
+    [[maybe_unused]] ScoredRow pre_row{};
     if (warp == C::WARP_TMA && has_static) {
         pre_p = __ldg(P.positions + st_row);
         if (!P.block_tables) pre_slot = __ldg(P.slots + st_row);
+        if constexpr (SC) {
+            const bool paged = P.block_tables != nullptr;
+            pre_row = scored_row(P.rule, P.shared, st_row, pre_p,
+                                 paged ? static_cast<uint64_t>(P.bt_stride) * P.slot_ctx : P.slot_ctx,
+                                 paged || pre_slot < P.n_slots, P.prefill != 0);
+            pre_p = pre_row.p;
+        }
     }
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
@@ -1036,8 +1162,11 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
             const uint32_t* tab = P.block_tables + static_cast<size_t>(st_row) * P.bt_stride;
             bool bad = static_cast<uint64_t>(pre_p) >=
                        static_cast<uint64_t>(P.bt_stride) * P.slot_ctx;
+            if constexpr (SC) bad = !pre_row.ok;
             const uint32_t used = bad ? 0u : pre_p / P.slot_ctx + 1;
-            for (uint32_t i0 = 0; i0 < used; i0 += 128) {
+            uint32_t first = 0;
+            if constexpr (SC) first = row_base(pre_row.lo, pre_p, T) / P.slot_ctx;
+            for (uint32_t i0 = first; i0 < used; i0 += 128) {
                 uint32_t id[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -1081,13 +1210,27 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
                 }
                 const uint32_t b = rec.x >> 16, split = (rec.x >> 8) & 255u, kvh = rec.x & 255u;
                 const uint32_t p = rec.y, prow = rec.z;
-                const uint32_t chunk = split_chunk(p + 1, P.chunk_min, P.max_splits, T);
-                const uint32_t nsplit = (p + 1 + chunk - 1) / chunk;
-                const uint32_t k0 = split * chunk;
+                // keys [base, base + n): from key 0, or in a scored call from
+                // the tile of the first key attended (rec.w)
+                uint32_t base = 0, n = p + 1;
+                if constexpr (SC) {
+                    uint32_t hi = p;
+                    if (P.prefill && P.rule.prefix_end) {
+                        const uint32_t e = __ldg(P.rule.prefix_end + b);
+                        hi = e > p + 1 ? e - 1 : p;
+                    }
+                    base = row_base(rec.w, hi, T);
+                    n = hi + 1 - base;
+                    d->lo = rec.w;
+                }
+                const uint32_t chunk = split_chunk(n, P.chunk_min, P.max_splits, T);
+                const uint32_t nsplit = (n + chunk - 1) / chunk;
+                const uint32_t k0 = base + split * chunk;
                 // in prefill mode every key, p included, is read from the slot
                 // (the KV-write kernel has written the new rows already)
                 const bool is_last = !P.prefill && split == nsplit - 1;
-                const uint32_t hist_end = is_last ? p : (k0 + chunk < p + 1 ? k0 + chunk : p + 1);
+                const uint32_t hist_end =
+                    is_last ? p : (k0 + chunk < base + n ? k0 + chunk : base + n);
                 const uint32_t n_hist = hist_end > k0 ? hist_end - k0 : 0;
                 const uint32_t ntiles = (n_hist + T - 1) / T;
                 d->b = b;
@@ -1136,11 +1279,17 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
             if (has_static) {
                 const uint32_t kvh = (blockIdx.x - st_split * P.static_items) % P.n_kv_head;
                 const uint32_t p = pre_p, slot = pre_slot;
-                const bool in_range = paged ? pg_ok != 0u : (slot < P.n_slots && p < P.slot_ctx);
+                bool in_range = paged ? pg_ok != 0u : (slot < P.n_slots && p < P.slot_ctx);
+                uint32_t n = p + 1, lo = 0;
+                if constexpr (SC) {
+                    if (!paged) in_range = pre_row.ok;
+                    lo = pre_row.lo;
+                    n = pre_row.hi + 1 - row_base(lo, pre_row.hi, T);
+                }
                 const uint32_t prow = paged ? pg_prow : slot * P.slot_ctx + p;
                 first_ok = in_range &&
-                           (st_split == 0 || p + 1 > split_chunk(p + 1, P.chunk_min, P.max_splits, T));
-                if (first_ok) rec = make_uint4(pack_item(st_row, st_split, kvh), p, prow, 0u);
+                           (st_split == 0 || n > split_chunk(n, P.chunk_min, P.max_splits, T));
+                if (first_ok) rec = make_uint4(pack_item(st_row, st_split, kvh), p, prow, lo);
                 // without a plan kernel (split-0 items only), the range flag
                 // is raised here
                 if (!in_range && P.no_plan) atomicOr(P.status, kDevRange);
@@ -1275,7 +1424,9 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
                 }
                 if (misc[0]) break;
                 const bool end = desc[is].end != 0;
-                const uint32_t p = desc[is].p;
+                uint32_t p = desc[is].p;
+                if constexpr (SC)  // a shared call's row rotates at its whole position
+                    if (!end && P.shared.lens) p += __ldg(P.shared.lens + desc[is].b);
                 const bool is_last = desc[is].is_last != 0;
                 if (!end) {
                     float cs[PPL], sn[PPL];
@@ -1502,6 +1653,20 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
         const uint32_t k0 = desc[is].k0, hist_end = desc[is].hist_end;
         const uint32_t ntiles = desc[is].ntiles;
         const bool is_last = desc[is].is_last != 0;
+        uint32_t lo = 0;
+        [[maybe_unused]] uint4 prec = make_uint4(0, 0, 0, 0);
+        [[maybe_unused]] LaneRule<C::CNT> rule_t;
+        [[maybe_unused]] LaneRule<G> rule_h;
+        if constexpr (SC) {
+            lo = desc[is].lo;
+            if (P.shared.lens && split == 0)
+                prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+            if constexpr (C::TR) {
+                constexpr int REP = C::NV >= L ? 1 : L / C::NV;
+                rule_t = lane_rule<G, C::CNT>(P.rule, kvh, li / REP * C::CNT % C::GP);
+            }
+            if (!C::TR || (is_last && warp == 0)) rule_h = lane_rule<G, G>(P.rule, kvh, 0);
+        }
         const float* qs = qbuf + is * G * HD;
         const float* ks = kbuf + is * HD;
         const float* vs = vbuf + is * HD;
@@ -1548,13 +1713,19 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
                 for (int r = 0; r < C::RC; ++r) {
                     row[r] = gid + NG * (r0 + r);
                     valid[r] = kbase + static_cast<uint32_t>(row[r]) < hist_end;
+                    if constexpr (SC)
+                        valid[r] = valid[r] && kbase + static_cast<uint32_t>(row[r]) >= lo;
                 }
-                if constexpr (C::TR)
-                    attend_rows_tr<HD, G, E, L, C::RC, C::GP, C::CNT>(
+                if constexpr (C::TR) {
+                    if constexpr (SC) rule_t.d0 = static_cast<int>(p - kbase);
+                    attend_rows_tr<HD, G, E, L, C::RC, C::GP, C::CNT, SC>(
                         Kt, Vt, row, valid, li, lane, q, m_t, l_t, acc,
-                        reinterpret_cast<float*>(smem + C::OFF_PBUF) + gid * C::NV);
-                else
-                    attend_rows<HD, G, E, L, C::RC>(Kt, Vt, row, valid, li, q, m, l, acc);
+                        reinterpret_cast<float*>(smem + C::OFF_PBUF) + gid * C::NV, &rule_t);
+                } else {
+                    if constexpr (SC) rule_h.d0 = static_cast<int>(p - kbase);
+                    attend_rows<HD, G, E, L, C::RC, SC>(Kt, Vt, row, valid, li, q, m, l, acc,
+                                                        &rule_h);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
@@ -1566,8 +1737,9 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
 
         if (is_last && warp == 0) {
             const int row1[1] = {0};
-            const bool valid1[1] = {gid == 0};
-            attend_rows<HD, G, E, L, 1>(ks, vs, row1, valid1, li, q, m, l, acc);
+            const bool valid1[1] = {gid == 0 && (!SC || lo <= p)};
+            if constexpr (SC) rule_h.d0 = 0;
+            attend_rows<HD, G, E, L, 1, SC>(ks, vs, row1, valid1, li, q, m, l, acc, &rule_h);
             // key p's K and V rows go to row prow: (slot*slot_ctx + p) in a slot,
             // (block*block_size + p % block_size) in paged mode
             const size_t at = static_cast<size_t>(prow) * P.n_kv_head + kvh;
@@ -1585,6 +1757,10 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
         // element t < EF of this lane's slice sits at dimension dim(t) of a head
         // (pairs t, t + 1 are adjacent: EF and e0 are even)
         auto dim = [&](int t) { return ((e0 + t) >> 2) * 4 * L + 4 * li + ((e0 + t) & 3); };
+        // a shared call's prefix partials join split 0, spread over the warps
+        if constexpr (SC) {
+            if (prec.z) fold_partials<HD, G, EF>(P.part, prec, P.n_head, kvh * G, warp, W, m, l, acc, dim);
+        }
         // ------------------------------------ chain the four warps: 0 -> 1 -> 2 -> 3
         for (int w2 = 0; w2 < W; ++w2) {
             if (warp == w2) {
@@ -1636,7 +1812,8 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
                         Ls = Ls * c + exp2f(sk - M2);
                     }
                     float* o = P.out + (static_cast<size_t>(b) * P.n_head + hq0 + h) * HD;
-                    const float f = __fmul_rn(c, __frcp_rn(Ls));  // one reciprocal per head
+                    float f = __fmul_rn(c, __frcp_rn(Ls));  // one reciprocal per head
+                    if (SC && m[h] == -CUDART_INF_F) f = 0.f;  // no key: zeros
 #pragma unroll
                     for (int t = 0; t < EF; t += 2)
                         *reinterpret_cast<float2*>(o + dim(t)) =
@@ -1689,14 +1866,16 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
 // One warp per (token, kv head): k' = RoPE(RMSnorm(k_new)) and v (or its
 // weightless norm) into the slot row (slot*slot_ctx + pos).  Out-of-range
 // tokens are skipped (the plan kernel raises the flag).
-template <int HD>
-__global__ void __launch_bounds__(128) slotkv_write_kv_kernel(const DecodeParams P) {
+template <int HD, bool SC = false>
+__global__ void __launch_bounds__(128) slotkv_write_kv_kernel(const decode_params_t<SC> P) {
     const int lane = threadIdx.x & 31;
     const uint32_t wg = blockIdx.x * 4 + (threadIdx.x >> 5);
     const uint32_t tok = wg / P.n_kv_head, kvh = wg % P.n_kv_head;
     if (tok >= P.B) return;
     const uint32_t p = P.positions[tok], slot = P.slots[tok];
     if (slot >= P.n_slots || p >= P.slot_ctx) return;
+    if constexpr (SC)
+        if (P.rule.prefix_end && __ldg(P.rule.prefix_end + tok) > P.slot_ctx) return;
     float cs[HD / 64], sn[HD / 64];
     warp_rope_angles<HD>(p, P.inv_freq, cs, sn, lane);
     const float w1 = (P.flags & kOptNormPlusOne) ? 1.0f : 0.0f;
@@ -1711,8 +1890,8 @@ __global__ void __launch_bounds__(128) slotkv_write_kv_kernel(const DecodeParams
     }
 }
 
-template <int HD, int G>
-int launch_one(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+template <int HD, int G, bool SC = false>
+int launch_one(const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                unsigned ctas, cudaStream_t stream) {
     using C = KCfg<HD, G>;
     // kernel attributes belong to each device's copy of the kernels: set them
@@ -1722,32 +1901,32 @@ int launch_one(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap&
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (!(configured.load(std::memory_order_acquire) & bit) || bit == 0) {
-        cudaError_t e = cudaFuncSetAttribute(slotkv_decode_attn_kernel<HD, G>,
+        cudaError_t e = cudaFuncSetAttribute(slotkv_decode_attn_kernel<HD, G, SC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return static_cast<int>(e);
         // one shared-memory carve-out for every kernel of a call, so the SMs
         // need no reconfiguration between them
         const int carve = cudaSharedmemCarveoutMaxShared;
-        if ((e = cudaFuncSetAttribute(slotkv_decode_attn_kernel<HD, G>,
+        if ((e = cudaFuncSetAttribute(slotkv_decode_attn_kernel<HD, G, SC>,
                                       cudaFuncAttributePreferredSharedMemoryCarveout, carve)) !=
                 cudaSuccess ||
-            (e = cudaFuncSetAttribute(slotkv_plan_kernel<C::T>,
+            (e = cudaFuncSetAttribute(slotkv_plan_kernel<C::T, SC>,
                                       cudaFuncAttributePreferredSharedMemoryCarveout, carve)) !=
                 cudaSuccess ||
-            (e = cudaFuncSetAttribute(slotkv_write_kv_kernel<HD>,
+            (e = cudaFuncSetAttribute(slotkv_write_kv_kernel<HD, SC>,
                                       cudaFuncAttributePreferredSharedMemoryCarveout, carve)) !=
                 cudaSuccess)
             return static_cast<int>(e);
         // the register hand-over assumes the launch gives every thread 128
         // registers; with fewer, the consumers' request could never be met
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, slotkv_decode_attn_kernel<HD, G>);
+        e = cudaFuncGetAttributes(&fa, slotkv_decode_attn_kernel<HD, G, SC>);
         if (e != cudaSuccess) return static_cast<int>(e);
         if (fa.numRegs != 128) return static_cast<int>(cudaErrorInvalidConfiguration);
         // the grid (two CTAs per SM) and its static items assume that both
         // CTAs of an SM are resident at once
         int per_sm = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, slotkv_decode_attn_kernel<HD, G>,
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, slotkv_decode_attn_kernel<HD, G, SC>,
                                                           C::THREADS, C::SMEM);
         if (e != cudaSuccess) return static_cast<int>(e);
         if (per_sm < 2) return static_cast<int>(cudaErrorInvalidConfiguration);
@@ -1755,7 +1934,7 @@ int launch_one(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap&
     }
     if (p.prefill) {
         const uint32_t warps = p.B * p.n_kv_head;
-        slotkv_write_kv_kernel<HD><<<(warps + 3) / 4, 128, 0, stream>>>(p);
+        slotkv_write_kv_kernel<HD, SC><<<(warps + 3) / 4, 128, 0, stream>>>(p);
     }
     cudaError_t e;
     cudaLaunchAttribute attr[1];
@@ -1769,7 +1948,7 @@ int launch_one(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap&
         pc.stream = stream;
         pc.attrs = attr;
         pc.numAttrs = 1;
-        e = cudaLaunchKernelEx(&pc, slotkv_plan_kernel<C::T>, p);
+        e = cudaLaunchKernelEx(&pc, slotkv_plan_kernel<C::T, SC>, p);
         if (e != cudaSuccess) return static_cast<int>(e);
     }
     cudaLaunchConfig_t cfg = {};
@@ -1779,22 +1958,22 @@ int launch_one(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap&
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = p.no_plan ? 0 : 1;  // programmatic dependent of the plan kernel
-    e = cudaLaunchKernelEx(&cfg, slotkv_decode_attn_kernel<HD, G>, tmK, tmV, p);
+    e = cudaLaunchKernelEx(&cfg, slotkv_decode_attn_kernel<HD, G, SC>, tmK, tmV, p);
     return static_cast<int>(e);
 }
 
-template <int HD>
-int launch_hd(int G, const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+template <int HD, bool SC = false>
+int launch_hd(int G, const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
               unsigned ctas, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_one<HD, 1>(p, tmK, tmV, ctas, stream);
-        case 2: return launch_one<HD, 2>(p, tmK, tmV, ctas, stream);
-        case 3: return launch_one<HD, 3>(p, tmK, tmV, ctas, stream);
-        case 4: return launch_one<HD, 4>(p, tmK, tmV, ctas, stream);
-        case 5: return launch_one<HD, 5>(p, tmK, tmV, ctas, stream);
-        case 6: return launch_one<HD, 6>(p, tmK, tmV, ctas, stream);
-        case 7: return launch_one<HD, 7>(p, tmK, tmV, ctas, stream);
-        case 8: return launch_one<HD, 8>(p, tmK, tmV, ctas, stream);
+        case 1: return launch_one<HD, 1, SC>(p, tmK, tmV, ctas, stream);
+        case 2: return launch_one<HD, 2, SC>(p, tmK, tmV, ctas, stream);
+        case 3: return launch_one<HD, 3, SC>(p, tmK, tmV, ctas, stream);
+        case 4: return launch_one<HD, 4, SC>(p, tmK, tmV, ctas, stream);
+        case 5: return launch_one<HD, 5, SC>(p, tmK, tmV, ctas, stream);
+        case 6: return launch_one<HD, 6, SC>(p, tmK, tmV, ctas, stream);
+        case 7: return launch_one<HD, 7, SC>(p, tmK, tmV, ctas, stream);
+        case 8: return launch_one<HD, 8, SC>(p, tmK, tmV, ctas, stream);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

@@ -28,6 +28,9 @@
 //   6. each warp merges its key groups by halving (merge_warp_groups), the
 //      four warps' (m, l, acc) merge through shared memory, the sink joins
 //      the max and the denominator, and out is written.
+// Scored calls (SC) start at the chunk of the row's first attended key and
+// apply the score rule where the persistent kernel does; in a shared call the
+// prefix partials join in step 6, spread over the four warps.
 // No spin-waits: only __syncthreads and cp.async groups.
 #pragma once
 
@@ -78,8 +81,8 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int HD, int G>
-__global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodeParams P) {
+template <int HD, int G, bool SC = false>
+__global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_params_t<SC> P) {
     using C = SCfg<HD, G>;
     using KC = KCfg<HD, G>;
     constexpr int T = C::T, W = C::W, E = KC::E, L = KC::L;
@@ -98,10 +101,24 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t b = blockIdx.x / P.n_kv_head, g = blockIdx.x % P.n_kv_head;
-    const uint32_t p = __ldg(P.positions + b);
+    const uint32_t pos = __ldg(P.positions + b);
     const uint32_t* tab = P.block_tables ? P.block_tables + static_cast<size_t>(b) * P.bt_stride
                                          : nullptr;
     const uint32_t slot = tab ? 0u : __ldg(P.slots + b);
+    // p: the position in the row's own slot; lo: the first key attended; c0:
+    // the chunk it is in
+    uint32_t p = pos, lo = 0, c0 = 0;
+    [[maybe_unused]] bool row_ok = true;
+    if constexpr (SC) {
+        const ScoredRow r = scored_row(
+            P.rule, P.shared, b, pos,
+            tab ? static_cast<uint64_t>(P.bt_stride) * P.slot_ctx : P.slot_ctx,
+            tab || slot < P.n_slots, false);
+        p = r.p;
+        lo = r.lo;
+        c0 = row_base(lo, p, T) / T;
+        row_ok = r.ok;
+    }
     // the row's vectors and the call's weights (none depends on p): q, k_new
     // and v_new are 16-byte aligned, the others 4-byte aligned
     {
@@ -123,11 +140,12 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
     bool ok;
     if (tab) {  // p within the table, every used entry (blocks 0 .. p / block) in the pool
         bool bad = static_cast<uint64_t>(p) >= static_cast<uint64_t>(P.bt_stride) * P.slot_ctx;
+        if constexpr (SC) bad = !row_ok;
         const uint32_t used = bad ? 0u : p / P.slot_ctx + 1;
-        for (uint32_t i = lane; i < used; i += 32) bad |= __ldg(tab + i) >= P.n_slots;
+        for (uint32_t i = c0 * T / P.slot_ctx + lane; i < used; i += 32) bad |= __ldg(tab + i) >= P.n_slots;
         ok = !__any_sync(0xffffffffu, bad);
     } else {
-        ok = slot < P.n_slots && p < P.slot_ctx;
+        ok = SC ? row_ok : slot < P.n_slots && p < P.slot_ctx;
     }
     if (!ok) {
         cp_async_wait<0>();  // no copy outlives the CTA
@@ -142,7 +160,7 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
                    : static_cast<size_t>(slot) * P.slot_ctx + t;
     };
     const size_t kvd = static_cast<size_t>(P.n_kv_head) * HD;
-    const uint32_t nchunks = (p + T - 1) / T;  // chunks of keys [0, p)
+    const uint32_t nchunks = (p + T - 1) / T;  // chunks of keys [0, p), from c0 on
     // history chunk c into buffer c & 1: keys [c T, min((c + 1) T, p))
     auto issue = [&](uint32_t c) {
         const uint32_t k0 = c * T;
@@ -158,19 +176,19 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
         }
         cp_async_commit();
     };
-    if (nchunks > 0) issue(0);
-    if (nchunks > 1) issue(1);
+    if (nchunks > c0) issue(c0);
+    if (nchunks > c0 + 1) issue(c0 + 1);
     // the vectors' group is the oldest: wait until at most the chunks' groups
     // are in flight
-    if (nchunks > 1) cp_async_wait<2>();
-    else if (nchunks == 1) cp_async_wait<1>();
+    if (nchunks > c0 + 1) cp_async_wait<2>();
+    else if (nchunks == c0 + 1) cp_async_wait<1>();
     else cp_async_wait<0>();
     __syncthreads();
 
     // the row's vectors (bit for bit as the decode kernel's prep warp forms them)
     {
         float cs[HD / 64], sn[HD / 64];
-        warp_rope_angles<HD>(p, ifr, cs, sn, lane);
+        warp_rope_angles<HD>(pos, ifr, cs, sn, lane);
         const float w1 = (P.flags & kOptNormPlusOne) ? 1.0f : 0.0f;
         if (warp == 0) {
             warp_norm_rope<HD>(k1, k1, kw, w1, 1.0f, P.eps, cs, sn, lane);
@@ -216,7 +234,18 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
     }
-    for (uint32_t c = 0; c < nchunks; ++c) {
+    [[maybe_unused]] uint4 prec = make_uint4(0, 0, 0, 0);
+    [[maybe_unused]] LaneRule<KC::CNT> rule_t;
+    [[maybe_unused]] LaneRule<G> rule_h;
+    if constexpr (SC) {
+        if (P.shared.lens) prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+        if constexpr (KC::TR) {
+            constexpr int REP = KC::NV >= L ? 1 : L / KC::NV;
+            rule_t = lane_rule<G, KC::CNT>(P.rule, g, li / REP * KC::CNT % KC::GP);
+        }
+        if (!KC::TR || warp == 0) rule_h = lane_rule<G, G>(P.rule, g, 0);
+    }
+    for (uint32_t c = c0; c < nchunks; ++c) {
         if (c + 1 < nchunks) cp_async_wait<1>();
         else cp_async_wait<0>();
         __syncthreads();  // chunk c is in shared memory for every thread
@@ -231,13 +260,18 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
             for (int r = 0; r < KC::RC; ++r) {
                 row[r] = gid + KC::NG * (r0 + r);
                 valid[r] = static_cast<uint32_t>(row[r]) < nk;
+                if constexpr (SC)
+                    valid[r] = valid[r] && c * T + static_cast<uint32_t>(row[r]) >= lo;
             }
-            if constexpr (KC::TR)
-                attend_rows_tr<HD, G, E, L, KC::RC, KC::GP, KC::CNT>(Kt, Vt, row, valid, li, lane,
-                                                                     q, m_t, l_t, acc,
-                                                                     pgs + gid * KC::NV);
-            else
-                attend_rows<HD, G, E, L, KC::RC>(Kt, Vt, row, valid, li, q, m, l, acc);
+            if constexpr (KC::TR) {
+                if constexpr (SC) rule_t.d0 = static_cast<int>(p - c * T);
+                attend_rows_tr<HD, G, E, L, KC::RC, KC::GP, KC::CNT, SC>(
+                    Kt, Vt, row, valid, li, lane, q, m_t, l_t, acc, pgs + gid * KC::NV, &rule_t);
+            } else {
+                if constexpr (SC) rule_h.d0 = static_cast<int>(p - c * T);
+                attend_rows<HD, G, E, L, KC::RC, SC>(Kt, Vt, row, valid, li, q, m, l, acc,
+                                                     &rule_h);
+            }
         }
         __syncthreads();  // buffer c & 1 is free again
         if (c + 2 < nchunks) issue(c + 2);
@@ -245,13 +279,18 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
     if constexpr (KC::TR) tr_state_to_heads<G, L, KC::RC, KC::GP, KC::CNT>(li, lane, m_t, l_t, m, l);
     if (warp == 0) {  // key p: the row's own k' and v
         const int row1[1] = {0};
-        const bool valid1[1] = {gid == 0};
-        attend_rows<HD, G, E, L, 1>(k1, v1, row1, valid1, li, q, m, l, acc);
+        const bool valid1[1] = {gid == 0 && (!SC || lo <= p)};
+        if constexpr (SC) rule_h.d0 = 0;
+        attend_rows<HD, G, E, L, 1, SC>(k1, v1, row1, valid1, li, q, m, l, acc, &rule_h);
     }
     // merge the key groups of each warp, then the four warps through shared
     // memory (the chunk space): acc [W][G][HD], m, l [W][G]
     constexpr int EF = HD / 32;
     const int e0 = merge_warp_groups<G, E, L>(lane, m, l, acc);
+    if constexpr (SC) {
+        auto dim = [&](int t) { return ((e0 + t) >> 2) * 4 * L + 4 * li + ((e0 + t) & 3); };
+        if (prec.z) fold_partials<HD, G, EF>(P.part, prec, P.n_head, g * G, warp, W, m, l, acc, dim);
+    }
     float* macc = reinterpret_cast<float*>(smem);
     float* mm = macc + W * G * HD;
     float* ml = mm + W * G;
@@ -293,41 +332,42 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const DecodePa
             cs = exp2f(M - M2);
             Ls = __fmaf_rn(Ls, cs, exp2f(sk - M2));
         }
-        const float f = __fmul_rn(cs, __frcp_rn(Ls));
+        float f = __fmul_rn(cs, __frcp_rn(Ls));
+        if (SC && M == -CUDART_INF_F) f = 0.f;  // no key: zeros
         reinterpret_cast<float4*>(P.out + (static_cast<size_t>(b) * P.n_head + g * G + h) * HD)[d4] =
             make_float4(__fmul_rn(o.x, f), __fmul_rn(o.y, f), __fmul_rn(o.z, f),
                         __fmul_rn(o.w, f));
     }
 }
 
-template <int HD, int G>
-int launch_small_one(const DecodeParams& p, cudaStream_t stream) {
+template <int HD, int G, bool SC = false>
+int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream) {
     using C = SCfg<HD, G>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (!(configured.load(std::memory_order_acquire) & bit) || bit == 0) {
-        cudaError_t e = cudaFuncSetAttribute(slotkv_decode_small_kernel<HD, G>,
+        cudaError_t e = cudaFuncSetAttribute(slotkv_decode_small_kernel<HD, G, SC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return static_cast<int>(e);
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    slotkv_decode_small_kernel<HD, G><<<p.B * p.n_kv_head, 128, C::SMEM, stream>>>(p);
+    slotkv_decode_small_kernel<HD, G, SC><<<p.B * p.n_kv_head, 128, C::SMEM, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 
-template <int HD>
-int launch_small_hd(int G, const DecodeParams& p, cudaStream_t stream) {
+template <int HD, bool SC = false>
+int launch_small_hd(int G, const decode_params_t<SC>& p, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_small_one<HD, 1>(p, stream);
-        case 2: return launch_small_one<HD, 2>(p, stream);
-        case 3: return launch_small_one<HD, 3>(p, stream);
-        case 4: return launch_small_one<HD, 4>(p, stream);
-        case 5: return launch_small_one<HD, 5>(p, stream);
-        case 6: return launch_small_one<HD, 6>(p, stream);
-        case 7: return launch_small_one<HD, 7>(p, stream);
-        case 8: return launch_small_one<HD, 8>(p, stream);
+        case 1: return launch_small_one<HD, 1, SC>(p, stream);
+        case 2: return launch_small_one<HD, 2, SC>(p, stream);
+        case 3: return launch_small_one<HD, 3, SC>(p, stream);
+        case 4: return launch_small_one<HD, 4, SC>(p, stream);
+        case 5: return launch_small_one<HD, 5, SC>(p, stream);
+        case 6: return launch_small_one<HD, 6, SC>(p, stream);
+        case 7: return launch_small_one<HD, 7, SC>(p, stream);
+        case 8: return launch_small_one<HD, 8, SC>(p, stream);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace slotkv {
 
 struct DecodeParams {
@@ -81,6 +83,61 @@ struct PrefillParams {
     uint32_t flags;          // SLOTKV_OPT_* norm options
 };
 
+// The score rule of a scored call (include/slotkv.h, slotkv_scores), in the
+// kernels' base-2 units: a score s is log2(e) times the natural one, so the
+// cap reads c tanh(s_nat / c) log2(e) = cap_out * tanh(s * cap_in).
+struct ScoreRule {
+    float cap_in = 0.f, cap_out = 0.f;      // ln 2 / c, c log2(e); cap_out 0: no cap
+    uint32_t window = 0;                    // keys t with p - t < window; 0: all
+    const float* slopes = nullptr;          // [n_head], natural units, or null
+    const uint32_t* doc_start = nullptr;    // [rows]: first key of the row's document, or null
+    const uint32_t* prefix_end = nullptr;   // [rows]: keys below it are attended whatever the
+                                            // row's position (prefill only), or null
+};
+
+// The rows of a shared call: row b's positions 0 .. lens[b] - 1 live in slot
+// slots[b] of another handle's buffers (n_slots slots of slot_ctx positions),
+// the rest in its own slot from position 0 on.  lens null: not a shared call.
+struct SharedRows {
+    const uint32_t* slots = nullptr;
+    const uint32_t* lens = nullptr;
+    uint32_t n_slots = 0, slot_ctx = 0;
+};
+
+// What the prefix pass of a shared call leaves for the decode kernel, and the
+// splits of a scored prefill for its combine kernel.  rec[b] = (first partial
+// row, stride, splits, 0): split s of row b, head h, is partial
+// (rec.x + s * rec.y) * n_head + h, (m, l) and an unnormalised accumulator.
+struct Partials {
+    uint32_t* rec = nullptr;  // [rows][4]
+    float* ml = nullptr;      // [partials][2]
+    float* acc = nullptr;     // [partials][hd]
+};
+
+struct ScoredDecodeParams : DecodeParams {
+    ScoreRule rule;
+    SharedRows shared;
+    Partials part;
+};
+
+struct ScoredPrefillParams : PrefillParams {
+    ScoreRule rule;
+    SharedRows shared;       // shared call: K, V, n_slots and slot_ctx are the prefix handle's,
+                             // own_* the rows' own slots and their geometry
+    const uint32_t* own_slots = nullptr;
+    uint32_t own_n_slots = 0, own_ctx = 0;
+    Partials part;
+    uint32_t* tile_lo = nullptr;  // workspace [n_tok]: each tile's smallest key
+    uint32_t* list = nullptr;     // workspace: (split << 16 | tile) of each (tile, split)
+    uint32_t list_cap = 0;
+    uint32_t sms = 0;             // SMs, for the split choice
+};
+
+template <bool SC>
+using decode_params_t = std::conditional_t<SC, ScoredDecodeParams, DecodeParams>;
+template <bool SC>
+using prefill_params_t = std::conditional_t<SC, ScoredPrefillParams, PrefillParams>;
+
 // Keys per split chunk for a row with n_keys keys (p + 1).  Depends only on
 // n_keys and the geometry so that a row's result never depends on the batch.
 __host__ __device__ inline uint32_t split_chunk(uint32_t n_keys, uint32_t chunk_min,
@@ -134,6 +191,28 @@ int launch_prefill_tc_hd64(int G, const PrefillParams& p, const CUtensorMap& tmK
                            const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream);
 int launch_prefill_tc_hd128(int G, const PrefillParams& p, const CUtensorMap& tmK,
                             const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream);
+
+// The scored forms (capped scores, distance bias, masks; see score_rule.cuh)
+// of the three kinds above, and the prefix pass of a shared decode call
+// (plan, q preparation, attention into partials).
+int launch_scored_hd64(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
+                       const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+int launch_scored_hd128(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+int launch_scored_hd256(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+int launch_scored_prefill_hd64(int G, const ScoredPrefillParams& p, const CUtensorMap& tmK,
+                               const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream);
+int launch_scored_prefill_hd128(int G, const ScoredPrefillParams& p, const CUtensorMap& tmK,
+                                const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream);
+
+// (tile, split) items per SM and kv head that the scored prefill's plan may
+// make by splitting; a call with more tiles than kSplitBelow items per SM is
+// never split.
+constexpr uint32_t kSplitBelow = 2, kSplitMost = 4, kMaxSplits = 64;
+// rows (tokens) of partials a call can need beyond one per row of a shared
+// call: 128 query rows per split item
+inline size_t partial_head_rows(uint32_t sms) { return (size_t)128 * kSplitMost * sms; }
 
 // Keys per pipeline stage of the tensor-core prefill.
 __host__ __device__ constexpr int prefill_tile_keys(int) { return 64; }

@@ -57,6 +57,30 @@
 // producer for its copies before tensor memory is freed.  The test option
 // SLOTKV_OPT_TEST_STALL withholds each CTA's first score-ready signal to
 // exercise that path.
+//
+// Scored calls (template parameter SC; parameters ScoredPrefillParams) are
+// the same three kernels with the score rule of score_rule.cuh, and also the
+// prefix pass of a shared decode call, whose rows attend the first
+// prefix_lens[b] keys of another handle's slot.  What differs:
+//   * each row has a key range [lo, hi]; a tile reads the union of its rows'
+//     ranges, and scores outside a row's own range are masked;
+//   * a call with few tiles cuts each tile's keys into splits (the plan picks
+//     the chunk, see below): an item is then (tile, split, kv head), and it
+//     leaves (m, l, O) in the partials instead of out.  The splits of a
+//     prefill are joined by slotkv_combine_kernel, those of a prefix pass by
+//     the decode kernel;
+//   * sums that stay at f32 accuracy however many keys there are: the tensor
+//     core's accumulation drops bits at every step, always toward zero, so a
+//     long chain drifts (1.2e-4 relative over 16 thousand keys).  Each key
+//     tile's P V therefore starts a new accumulator, which the softmax warps
+//     add to a register copy of O with rounded f32 adds -- O(t) is read while
+//     the tensor core forms the next scores -- and within a chain the products
+//     with a low part come first, while the partial sum is still small.  Q
+//     and P are split with a rounded high part, so the dropped lo x lo terms
+//     have no common sign;
+//   * a V value that is not finite is taken as 0 by the tensor core (0 times
+//     it would poison every masked row of the tile), and rows that do attend
+//     it get it added in the epilogue from the slot itself.
 #pragma once
 
 #include "decode_attn.cuh"
@@ -86,11 +110,21 @@ struct PCfg {
     static constexpr int WARP_TMA = 8, WARP_MMA = 9, WARP_CONV = 10, NCONV = 4;
     static constexpr int SB_PER_WARP = KB * NB / NCONV;  // V sub-blocks per converter warp
     static constexpr int THREADS = 32 * (WARP_CONV + NCONV);
+    // scored calls: whole warpgroups (two warps only hand registers over),
+    // launched at 128 registers a thread; the two softmax warpgroups, with O in
+    // registers, take them from the other two: 256 * 160 + 256 * 96 = 512 * 128
+    static constexpr int THREADS_SC = 512, REG_SOFTMAX = 160, REG_OTHER = 96;
+    static_assert(256 * REG_SOFTMAX + 256 * REG_OTHER == THREADS_SC * 128,
+                  "register hand-over must add up to the launch's registers");
     // tensor memory columns: Q hi | Q lo | O | NBUF buffers of (S, then P hi
     // over it | P lo)
     static constexpr uint32_t C_QHI = 0, C_QLO = HD, C_O = 2 * HD, C_S = 3 * HD;
     static constexpr uint32_t C_BUF = 2 * BK;   // columns per score buffer
     static constexpr int NBUF = (512 - 3 * HD) / (2 * BK) >= 2 ? 2 : 1;
+    // scored calls: with two score buffers PV(t) may run while O(t - 1) is
+    // still to be read, so O has a second buffer after the score buffers
+    static constexpr uint32_t C_O2 = 3 * HD + NBUF * 2 * BK;
+    static_assert(NBUF == 1 || C_O2 + HD <= 512, "tensor memory columns");
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(3 * HD + NBUF * 2 * BK <= 512, "tensor memory columns");
     static_assert(BK % 32 == 0 && HD % 32 == 0, "32-column tensor memory accesses");
@@ -104,7 +138,8 @@ struct PCfg {
     static constexpr int NBAR = 3 * NSLOT + 12;
     static constexpr int OFF_TSLOT = OFF_BAR + NBAR * 8;
     static constexpr int OFF_MISC = OFF_TSLOT + 16;
-    // misc[0]: abort; misc[2 + w]: converter warp w's stop flag
+    // misc[0]: abort; misc[2 + w]: converter warp w's stop flag; misc[8]: see
+    // the kernel
     // the softmax halves' exchange: row maxima [2 parities][2 halves][M],
     // row sums [2 halves][M], and a stop flag beside each
     static constexpr int OFF_XCH = OFF_MISC + 64;
@@ -139,6 +174,14 @@ __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) 
     lo = __float_as_uint(x - __uint_as_float(h));
 }
 
+// The same with the high part rounded to nearest, so the remainder is at most
+// half a TF32 step and takes either sign.
+__device__ __forceinline__ void tf32_split_rn(float x, uint32_t& hi, uint32_t& lo) {
+    const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    hi = h;
+    lo = __float_as_uint(x - __uint_as_float(h));
+}
+
 // ------------------------------------------------------------------ prep
 // One warp per (token, group of heads): kPrepHeads query heads, or
 // kPrepKvHeads kv heads (their k_new and v_new rows), so that every warp
@@ -155,6 +198,34 @@ __device__ __forceinline__ void prep_cp_async16(void* smem_dst, const void* gmem
                  : "memory");
 }
 
+// Row i of a scored call as the tensor-core kernels see it: the slot it reads
+// (its own, or its prefix's), its key range there, its position; ok: in
+// range; keys: it has keys in that slot for the tensor cores to attend (a
+// prefill row always belongs to a tile, be its mask empty).
+struct PrefillRow {
+    uint32_t slot, pos, lo, hi;
+    bool ok, keys;
+};
+__device__ __forceinline__ PrefillRow prefill_row(const ScoredPrefillParams& P, uint32_t i) {
+    PrefillRow r;
+    r.pos = __ldg(P.positions + i);
+    r.slot = __ldg(P.slots + i);
+    r.lo = rule_first(P.rule, i, r.pos);
+    if (P.shared.lens) {
+        const ScoredRow x = scored_row(P.rule, P.shared, i, r.pos, P.own_ctx,
+                                       __ldg(P.own_slots + i) < P.own_n_slots, false);
+        r.ok = x.ok;
+        r.keys = x.ok && x.len != 0u && r.lo < x.len;
+        r.hi = r.keys ? x.len - 1u : 0u;
+    } else {
+        const ScoredRow x = scored_row(P.rule, P.shared, i, r.pos, P.slot_ctx,
+                                       r.slot < P.n_slots, true);
+        r.ok = r.keys = x.ok;
+        r.hi = x.hi;
+    }
+    return r;
+}
+
 template <int HD>
 __host__ __device__ constexpr int prep_smem_bytes() {
     return 4 * kPrepHeads * HD * 4;  // four warps x kPrepHeads rows
@@ -168,16 +239,24 @@ __host__ __device__ inline uint32_t prep_groups(uint32_t n_head, uint32_t n_kv_h
     return prep_q_groups(n_head) + (n_kv_head + kPrepKvHeads - 1) / kPrepKvHeads;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(128) slotkv_prefill_prep_kernel(const PrefillParams P) {
+template <int HD, bool SC = false>
+__global__ void __launch_bounds__(128)
+    slotkv_prefill_prep_kernel(const prefill_params_t<SC> P) {
     extern __shared__ __align__(16) uint8_t prep_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t qg = prep_q_groups(P.n_head), groups = prep_groups(P.n_head, P.n_kv_head);
+    const uint32_t qg = prep_q_groups(P.n_head);
+    uint32_t groups = prep_groups(P.n_head, P.n_kv_head);
+    if constexpr (SC)
+        if (P.shared.lens) groups = qg;  // the decode kernel forms and writes k' and v
     const uint32_t wg = blockIdx.x * 4 + warp;
     const uint32_t tok = wg / groups, grp = wg % groups;
     if (tok >= P.n_tok) return;
     const uint32_t p = P.positions[tok], slot = P.slots[tok];
-    if (slot >= P.n_slots || p >= P.slot_ctx) return;  // the plan raises the flag
+    if constexpr (SC) {
+        if (!prefill_row(P, tok).ok) return;
+    } else {
+        if (slot >= P.n_slots || p >= P.slot_ctx) return;  // the plan raises the flag
+    }
     const bool is_q = grp < qg;
     // the group's first head (a query head, or a kv head) and its size
     const uint32_t x0 = is_q ? grp * kPrepHeads : (grp - qg) * kPrepKvHeads;
@@ -225,14 +304,144 @@ __global__ void __launch_bounds__(128) slotkv_prefill_prep_kernel(const PrefillP
 }
 
 // ------------------------------------------------------------------ plan
+// Scored calls: the splits of the tiles and the item list (split << 16 |
+// tile), whole CTA.  With enough tiles to fill the GPU twice nothing is
+// split.  Otherwise one chunk length serves every tile, so that all items
+// are about equal: of the lengths that cut the longest tile into 1 ..
+// kMaxSplits splits (at least four key tiles each), the one with the least
+// estimated time, waves of items over the SMs times key tiles per item plus
+// a fixed cost per item (its q load, its epilogue and the join of its
+// partial, about four key tiles' time).  Items are listed split by split, the
+// tiles from last to first, so CTAs that run together share a split's keys
+// in L2, and a prefill's largest tiles come first.
+constexpr uint32_t kItemCost = 4;  // key tiles
+
+template <int BK>
+__device__ __forceinline__ uint32_t tile_split_count(uint32_t lo, uint32_t hi, uint32_t chunk) {
+    const uint32_t kt = (hi - lo) / BK + 1;  // key tiles
+    return (kt + chunk - 1) / chunk;
+}
+
+template <int BK>
+__device__ void plan_splits(const ScoredPrefillParams& P, uint32_t n_tiles) {
+    __shared__ uint32_t longest, best_chunk;
+    __shared__ unsigned long long best;
+    __shared__ uint32_t scan[32], carry_items, carry_part;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
+    if (tid == 0) {
+        longest = 1;
+        best = ~0ull;
+        best_chunk = 0x7FFFFFFFu;
+        carry_items = carry_part = 0;
+    }
+    __syncthreads();
+    const bool split = static_cast<uint64_t>(n_tiles) * P.n_kv_head <
+                       static_cast<uint64_t>(kSplitBelow) * P.sms;
+    if (split) {
+        for (uint32_t t = tid; t < n_tiles; t += 1024)
+            atomicMax(&longest, (__ldcg(&tiles[t].w) - __ldcg(P.tile_lo + t)) / BK + 1);
+        __syncthreads();
+        // warp w tries w + 1 and w + 33 splits of the longest tile
+        for (uint32_t s = warp + 1; s <= kMaxSplits; s += 32) {
+            const uint32_t chunk = (longest + s - 1) / s;
+            if (s > 1 && chunk < 4) continue;
+            uint32_t items = 0;
+            for (uint32_t t = lane; t < n_tiles; t += 32)
+                items += tile_split_count<BK>(__ldcg(P.tile_lo + t), __ldcg(&tiles[t].w), chunk);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) items += __shfl_xor_sync(0xffffffffu, items, off);
+            items *= P.n_kv_head;
+            if (s > 1 && items > kSplitMost * P.sms) continue;
+            const uint64_t waves = (items + P.sms - 1) / P.sms;
+            const uint64_t cost = waves * (chunk + (s > 1 ? kItemCost : 0u));
+            // (of equal costs the longest chunk, so the fewest partials)
+            if (lane == 0) atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - chunk));
+        }
+        __syncthreads();
+        if (tid == 0) best_chunk = 0xFFFFFFFFu - static_cast<uint32_t>(best & 0xFFFFFFFFu);
+        __syncthreads();
+    }
+    const uint32_t chunk = best_chunk;
+    // items per tile and partial rows per tile, both as exclusive sums over
+    // the tiles from last to first (order of the partials is of no account)
+    for (uint32_t r0 = 0; r0 < n_tiles; r0 += 1024) {
+        const uint32_t i = r0 + tid;
+        uint32_t ns = 0, rows = 0, tile = 0, first = 0;
+        if (i < n_tiles) {
+            tile = n_tiles - 1 - i;
+            const uint4 rec = __ldcg(tiles + tile);
+            first = rec.x;
+            rows = rec.y;
+            ns = split ? tile_split_count<BK>(__ldcg(P.tile_lo + tile), rec.w, chunk) : 1u;
+        }
+        const uint32_t pr = (ns > 1 || P.shared.lens) ? ns * rows : 0u;
+        uint32_t a = pr;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, a, off);
+            if (lane >= static_cast<uint32_t>(off)) a += o;
+        }
+        if (lane == 31) scan[warp] = a;
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t v = scan[lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
+                if (lane >= static_cast<uint32_t>(off)) v += o;
+            }
+            scan[lane] = v;
+        }
+        __syncthreads();
+        const uint32_t base = carry_part + (warp ? scan[warp - 1] : 0u) + a - pr;
+        if (pr)
+            for (uint32_t j = 0; j < rows; ++j)
+                reinterpret_cast<uint4*>(P.part.rec)[first + j] = make_uint4(base + j, rows, ns, 0u);
+        __syncthreads();
+        if (tid == 1023) carry_part = base + pr;
+        __syncthreads();
+    }
+    // the list, split by split: tiles with more than s splits, last to first
+    const uint32_t most = split ? (longest + chunk - 1) / chunk : 1u;
+    for (uint32_t s = 0; s < most; ++s) {
+        for (uint32_t r0 = 0; r0 < n_tiles; r0 += 1024) {
+            const uint32_t i = r0 + tid;
+            bool in = false;
+            uint32_t tile = 0;
+            if (i < n_tiles) {
+                tile = n_tiles - 1 - i;
+                in = s == 0 || tile_split_count<BK>(__ldcg(P.tile_lo + tile),
+                                                    __ldcg(&tiles[tile].w), chunk) > s;
+            }
+            const uint32_t ballot = __ballot_sync(0xffffffffu, in);
+            if (lane == 0) scan[warp] = __popc(ballot);
+            __syncthreads();
+            uint32_t before = carry_items;
+            for (uint32_t w = 0; w < warp; ++w) before += scan[w];
+            const uint32_t at = before + __popc(ballot & ((1u << lane) - 1u));
+            if (in && at < P.list_cap) P.list[at] = s << 16 | tile;
+            __syncthreads();
+            if (tid == 1023) carry_items = at + (in ? 1u : 0u);
+            __syncthreads();
+        }
+    }
+    if (tid == 0) {
+        P.plan[0] = carry_items * P.n_kv_head;
+        P.plan[1] = 0;
+        P.plan[2] = chunk;
+    }
+}
+
 // One CTA of 1024 threads, tokens in rounds of 1024.  A run is a maximal
 // sequence of consecutive in-range tokens with the same slot; token i starts
 // a tile when its index within its run is a multiple of MT.  Tile records:
 // (first token, tokens, slot, largest position).  Out-of-range tokens raise
 // SLOTKV_DEV_RANGE and belong to no tile.  Then the tiles' hand-out order.
 
-template <int MT>
-__global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const PrefillParams P) {
+template <int MT, int BK, bool SC = false>
+__global__ void __launch_bounds__(1024, 1)
+    slotkv_prefill_plan_kernel(const prefill_params_t<SC> P) {
     __shared__ int warp_max[32];
     __shared__ uint32_t warp_sum[32];
     __shared__ int carry_start;
@@ -252,7 +461,25 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
         const uint32_t i = r0 + tid;
         bool valid = false, start = false;
         uint32_t slot = 0;
-        if (i < P.n_tok) {
+        [[maybe_unused]] uint32_t lo = 0, hi = 0;
+        if constexpr (SC) {
+            if (i < P.n_tok) {
+                const PrefillRow r = prefill_row(P, i);
+                if (!r.ok) atomicOr(P.status, kDevRange);
+                valid = r.keys;
+                slot = r.slot;
+                hi = r.hi;
+                lo = r.lo < hi ? r.lo : hi;
+                reinterpret_cast<uint4*>(P.part.rec)[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (valid) {
+                    start = i == 0;
+                    if (i > 0) {
+                        const PrefillRow prev = prefill_row(P, i - 1);
+                        start = !prev.keys || prev.slot != slot;
+                    }
+                }
+            }
+        } else if (i < P.n_tok) {
             slot = P.slots[i];
             valid = slot < P.n_slots && P.positions[i] < P.slot_ctx;
             if (!valid) atomicOr(P.status, kDevRange);
@@ -309,6 +536,8 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
         __syncthreads();
         const uint32_t incl = c + (warp > 0 ? warp_sum[warp - 1] : 0u) + carry_tiles;
         if (tflag) tiles[incl - 1] = make_uint4(i, 0u, slot, 0u);
+        if constexpr (SC)
+            if (tflag) P.tile_lo[incl - 1] = 0xFFFFFFFFu;
         if (i < P.n_tok) P.tile_of[i] = valid ? incl - 1 : 0xFFFFFFFFu;
         __syncthreads();  // every thread has read the carries
         if (tid == 1023) {
@@ -323,9 +552,19 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
         if (t == 0xFFFFFFFFu) continue;
         uint32_t* rec = P.tiles + 4 * static_cast<size_t>(t);
         atomicAdd(rec + 1, 1u);
-        atomicMax(rec + 3, P.positions[i]);
+        if constexpr (SC) {
+            const PrefillRow r = prefill_row(P, i);
+            atomicMax(rec + 3, r.hi);
+            atomicMin(P.tile_lo + t, r.lo < r.hi ? r.lo : r.hi);
+        } else {
+            atomicMax(rec + 3, P.positions[i]);
+        }
     }
     __syncthreads();
+    if constexpr (SC) {
+        plan_splits<BK>(P, carry_tiles);
+        return;
+    }
     // The hand-out order, into tile_of (its per-token use is over): the
     // tiles in reverse, so each run is handed out from its last tile (the
     // most keys, when its positions increase) to its first, one run after
@@ -344,10 +583,11 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
 // ------------------------------------------------------------------ attention
 // Half-tile h of the CTA's stream of key tiles: h = 2g is tile g's K, h = 2g + 1
 // its V; it lives in slot h % NSLOT.
-template <int HD, int G>
-__global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
+template <int HD, int G, bool SC = false>
+__global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::THREADS, 1)
     slotkv_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK,
-                             const __grid_constant__ CUtensorMap tmV, const PrefillParams P) {
+                             const __grid_constant__ CUtensorMap tmV,
+                             const prefill_params_t<SC> P) {
     using C = PCfg<HD, G>;
     constexpr int BK = C::BK, NB = C::NB, NSLOT = C::NSLOT, NBUF = C::NBUF;
     constexpr float kLog2e = 1.4426950408889634f;
@@ -384,6 +624,7 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
         mbar_init(QREADY, C::NSW);
         mbar_init(DRAIN, 1);
         misc[0] = 0;
+        misc[8] = 0;  // scored calls: a V value of this CTA's tiles was not finite
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -400,264 +641,335 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
         misc[0] = 1;
     };
 
-    if (warp == C::WARP_TMA) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            const uint32_t n_items = __ldcg(P.plan);
-            const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
-            uint32_t h = 0;  // half-tiles issued
-            // wait until slot h % NSLOT is free again
-            auto slot_free = [&](uint32_t hh) {
-                return hh < static_cast<uint32_t>(NSLOT) ||
-                       mbar_wait(EMPTY + 8 * (hh % NSLOT), ((hh / NSLOT) - 1) & 1);
-            };
-            for (uint32_t k = 0;; ++k) {
-                const uint32_t is = k & 1;
-                if (k >= 2 && !mbar_wait(IFREE + 8 * is, ((k >> 1) - 1) & 1)) {
-                    timeout();
-                    break;
-                }
-                if (misc[0]) break;
-                volatile uint32_t* d = desc + 8 * is;
-                const uint32_t it = atomicAdd(P.plan + 1, 1u);
-                if (it >= n_items) {
-                    d[6] = 1;
-                    mbar_arrive(IFULL + 8 * is);
-                    // tell the converters: an end marker in the next slot
-                    if (!slot_free(h)) {
+    if (warp >= C::NSW) {
+        if constexpr (SC) regs_decrease<C::REG_OTHER>();
+        if (warp == C::WARP_TMA) {
+            // ------------------------------------------------------------ producer
+            if (lane == 0) {
+                const uint32_t n_items = __ldcg(P.plan);
+                const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
+                uint32_t h = 0;  // half-tiles issued
+                // wait until slot h % NSLOT is free again
+                auto slot_free = [&](uint32_t hh) {
+                    return hh < static_cast<uint32_t>(NSLOT) ||
+                           mbar_wait(EMPTY + 8 * (hh % NSLOT), ((hh / NSLOT) - 1) & 1);
+                };
+                for (uint32_t k = 0;; ++k) {
+                    const uint32_t is = k & 1;
+                    if (k >= 2 && !mbar_wait(IFREE + 8 * is, ((k >> 1) - 1) & 1)) {
                         timeout();
                         break;
                     }
-                    meta[4 * (h % NSLOT) + 1] = 1;
-                    mbar_arrive(FULL + 8 * (h % NSLOT));
-                    break;
-                }
-                // in the plan's hand-out order
-                const uint4 rec = __ldcg(tiles + __ldcg(P.tile_of + it / P.n_kv_head));
-                const uint32_t kvh = it % P.n_kv_head;
-                const uint32_t max_pos = rec.w;
-                const uint32_t ntiles = (max_pos + BK) / BK;  // keys 0 .. max_pos
-                d[0] = rec.x;
-                d[1] = rec.y;
-                d[2] = rec.z;
-                d[3] = max_pos;
-                d[4] = kvh;
-                d[5] = ntiles;
-                d[6] = 0;
-                mbar_arrive(IFULL + 8 * is);
-                const int y0 = static_cast<int>(rec.z * P.slot_ctx);
-                for (uint32_t t = 0; t < ntiles && !misc[0]; ++t) {
-                    const uint32_t left = max_pos + 1 - t * BK;
-                    const int y = y0 + static_cast<int>(t * BK);
-                    for (int which = 0; which < 2; ++which, ++h) {  // K, then V
+                    if (misc[0]) break;
+                    volatile uint32_t* d = desc + 8 * is;
+                    const uint32_t it = atomicAdd(P.plan + 1, 1u);
+                    if (it >= n_items) {
+                        d[6] = 1;
+                        mbar_arrive(IFULL + 8 * is);
+                        // tell the converters: an end marker in the next slot
                         if (!slot_free(h)) {
                             timeout();
                             break;
                         }
-                        const uint32_t sl = h % NSLOT;
-                        meta[4 * sl + 0] = left < static_cast<uint32_t>(BK) ? left : BK;
-                        meta[4 * sl + 1] = 0;
-                        mbar_expect_tx(FULL + 8 * sl, C::BUF);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c)
-                            tma_load_2d(slot_hi(sl) + c * C::BLK, which ? &tmV : &tmK,
-                                        static_cast<int>(kvh * HD) + 32 * c, y, FULL + 8 * sl);
-                    }
-                }
-                if (misc[0]) break;
-            }
-            if (misc[0]) {
-                // drain this CTA's copies that may still be in flight
-                for (uint32_t u = h > static_cast<uint32_t>(NSLOT) ? h - NSLOT : 0; u < h; ++u)
-                    mbar_wait(FULL + 8 * (u % NSLOT), (u / NSLOT) & 1, 1ll << 28);
-            }
-        }
-    } else if (warp >= C::WARP_CONV) {
-        // ------------------------------------------------------------ converters
-        const int ct = tid - C::WARP_CONV * 32;
-        const int w = ct >> 5;
-        constexpr int NT = C::NCONV * 32;
-        for (uint32_t h = 0;; ++h) {
-            const uint32_t sl = h % NSLOT;
-            // The converter warps meet at named barriers below, so they must
-            // all stop at the same half-tile: each publishes its own reason
-            // to stop (a wait that expired, an abort, the end marker) and all
-            // decide from the published flags.
-            const bool ok = mbar_wait(FULL + 8 * sl, (h / NSLOT) & 1);
-            if (!ok) timeout();
-            if (lane == 0) misc[2 + w] = (!ok || misc[0] || meta[4 * sl + 1]) ? 1 : 0;
-            named_sync_conv<NT>();
-            int stop = 0;
-#pragma unroll
-            for (int w2 = 0; w2 < C::NCONV; ++w2) stop |= misc[2 + w2];
-            if (stop) break;
-            const uint32_t rows = meta[4 * sl + 0];
-            uint8_t* hib = smem + sl * C::SLOT;
-            uint8_t* lob = hib + C::BUF;
-            if ((h & 1) == 0) {
-                // K: the landed f32 tile is its own hi part (the tensor core
-                // reads a TF32 operand's f32 bits with the low 13 mantissa
-                // bits ignored, i.e. as x & 0xFFFFE000), so only the lo part
-                // is written beside it (K-major, as TMA laid the tile out);
-                // rows past the item's last key are zeroed in both
-                float4* hi = reinterpret_cast<float4*>(hib);
-                float4* lo = reinterpret_cast<float4*>(lob);
-#pragma unroll
-                for (int i = ct; i < C::BUF / 16; i += NT) {
-                    // each 128-byte row of a column block is 8 float4s
-                    const uint32_t row = static_cast<uint32_t>(i % (C::BLK / 16)) / 8;
-                    if (row >= rows) {
-                        hi[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        lo[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        continue;
-                    }
-                    const float4 x = hi[i];
-                    uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
-                    tf32_split(x.x, h0, l0);
-                    tf32_split(x.y, h1, l1);
-                    tf32_split(x.z, h2, l2);
-                    tf32_split(x.w, h3, l3);
-                    lo[i] = make_float4(__uint_as_float(l0), __uint_as_float(l1),
-                                        __uint_as_float(l2), __uint_as_float(l3));
-                }
-            } else {
-                // V: every 32 x 32 sub-block transposed (keys along the
-                // 128-byte rows), hi in place, lo into the lo buffer.  All
-                // converter threads read their sub-blocks (lane = dim, one
-                // key per load) before any writes, so the in-place
-                // permutation is safe whatever its cycles.
-                float x[C::SB_PER_WARP][32];
-#pragma unroll
-                for (int j = 0; j < C::SB_PER_WARP; ++j) {
-                    const int sb = w + C::NCONV * j;
-                    const int kb = sb / NB, db = sb % NB;
-                    const uint8_t* src = hib + db * C::BLK + kb * 4096;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const uint32_t off = (k / 8) * 1024 + (k % 8) * 128 +
-                                             (((lane / 4) ^ (k % 8)) * 16) + (lane % 4) * 4;
-                        const float v = *reinterpret_cast<const float*>(src + off);
-                        x[j][k] = static_cast<uint32_t>(kb * 32 + k) < rows ? v : 0.f;
-                    }
-                }
-                named_sync_conv<NT>();
-#pragma unroll
-                for (int j = 0; j < C::SB_PER_WARP; ++j) {
-                    const int sb = w + C::NCONV * j;
-                    const int kb = sb / NB, db = sb % NB;
-                    const uint32_t base = kb * C::VT_BLK + db * 4096 + (lane / 8) * 1024 +
-                                          (lane % 8) * 128;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t hh[4], ll[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) tf32_split(x[j][4 * c + e], hh[e], ll[e]);
-                        const uint32_t off = base + ((c ^ (lane % 8)) * 16);
-                        *reinterpret_cast<uint4*>(hib + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-                        *reinterpret_cast<uint4*>(lob + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
-                    }
-                }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(CONV + 8 * sl);
-        }
-    } else if (warp == C::WARP_MMA) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            uint32_t g = 0;  // key tiles whose QK was issued
-            bool ok = true;
-            auto converted = [&](uint32_t hh) {
-                return mbar_wait(CONV + 8 * (hh % NSLOT), (hh / NSLOT) & 1);
-            };
-            // O += P V for tile t of the item (global tile gp)
-            auto issue_pv = [&](uint32_t t, uint32_t gp) {
-                const uint32_t hv = 2 * gp + 1;
-                if (!converted(hv) || !mbar_wait(PREADY + 8 * (gp & 1), (gp >> 1) & 1)) {
-                    timeout();
-                    return false;
-                }
-                tc::fence_after_sync();
-                const uint32_t sl = hv % NSLOT;
-                const uint32_t pcol0 = C::C_S + (gp % NBUF) * C::C_BUF;
-                // O += P_lo V_hi + P_hi V_hi + P_hi V_lo, K-step by K-step
-                // (consecutive products share their B, then their A, slice)
-#pragma unroll
-                for (int kk = 0; kk < BK / 8; ++kk) {
-                    const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
-                    const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
-                    const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
-                    tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + BK + kk * 8, bh, C::IDESC_PV,
-                                    (t | kk) != 0 ? 1u : 0u);
-                    tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + kk * 8, bh, C::IDESC_PV, 1u);
-                    tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + kk * 8, bl, C::IDESC_PV, 1u);
-                }
-                tc::mma_commit(PVDONE + 8 * (gp & 1));
-                tc::mma_commit(EMPTY + 8 * sl);
-                return true;
-            };
-            for (uint32_t k = 0; ok; ++k) {
-                const uint32_t is = k & 1;
-                if (!mbar_wait(IFULL + 8 * is, (k >> 1) & 1)) {
-                    timeout();
-                    break;
-                }
-                const uint32_t ntiles = desc[8 * is + 5], end = desc[8 * is + 6];
-                mbar_arrive(IFREE + 8 * is);
-                if (end || misc[0]) break;
-                if (!mbar_wait(QREADY, k & 1)) {
-                    timeout();
-                    break;
-                }
-                tc::fence_after_sync();
-                for (uint32_t t = 0; t < ntiles; ++t, ++g) {
-                    const uint32_t hk = 2 * g;
-                    if (!converted(hk)) {
-                        timeout();
-                        ok = false;
+                        meta[4 * (h % NSLOT) + 1] = 1;
+                        mbar_arrive(FULL + 8 * (h % NSLOT));
                         break;
                     }
-                    if (misc[0]) {
-                        ok = false;
+                    // in the plan's hand-out order
+                    uint32_t tile, split = 0;
+                    if constexpr (SC) {
+                        const uint32_t entry = __ldcg(P.list + it / P.n_kv_head);
+                        tile = entry & 0xFFFFu;
+                        split = entry >> 16;
+                    } else {
+                        tile = __ldcg(P.tile_of + it / P.n_kv_head);
+                    }
+                    const uint4 rec = __ldcg(tiles + tile);
+                    const uint32_t kvh = it % P.n_kv_head;
+                    // keys k_begin .. max_pos: 0 .. the tile's largest position,
+                    // or in a scored call the split's part of the tile's range
+                    uint32_t k_begin = 0, max_pos = rec.w;
+                    if constexpr (SC) {
+                        const uint32_t chunk = __ldcg(P.plan + 2);
+                        k_begin = __ldcg(P.tile_lo + tile) + split * chunk * BK;
+                        const uint32_t left = (max_pos - k_begin) / BK;  // further key tiles
+                        if (left >= chunk) max_pos = k_begin + chunk * BK - 1;
+                    }
+                    const uint32_t ntiles = (max_pos - k_begin + BK) / BK;
+                    d[0] = rec.x;
+                    d[1] = rec.y;
+                    d[2] = SC ? k_begin : rec.z;
+                    d[3] = SC ? split : max_pos;
+                    d[4] = kvh;
+                    d[5] = ntiles;
+                    d[6] = 0;
+                    mbar_arrive(IFULL + 8 * is);
+                    const int y0 = static_cast<int>(rec.z * P.slot_ctx + k_begin);
+                    for (uint32_t t = 0; t < ntiles && !misc[0]; ++t) {
+                        const uint32_t left = max_pos - k_begin + 1 - t * BK;
+                        const int y = y0 + static_cast<int>(t * BK);
+                        for (int which = 0; which < 2; ++which, ++h) {  // K, then V
+                            if (!slot_free(h)) {
+                                timeout();
+                                break;
+                            }
+                            const uint32_t sl = h % NSLOT;
+                            meta[4 * sl + 0] = left < static_cast<uint32_t>(BK) ? left : BK;
+                            meta[4 * sl + 1] = 0;
+                            mbar_expect_tx(FULL + 8 * sl, C::BUF);
+    #pragma unroll
+                            for (int c = 0; c < NB; ++c)
+                                tma_load_2d(slot_hi(sl) + c * C::BLK, which ? &tmV : &tmK,
+                                            static_cast<int>(kvh * HD) + 32 * c, y, FULL + 8 * sl);
+                        }
+                    }
+                    if (misc[0]) break;
+                }
+                if (misc[0]) {
+                    // drain this CTA's copies that may still be in flight
+                    for (uint32_t u = h > static_cast<uint32_t>(NSLOT) ? h - NSLOT : 0; u < h; ++u)
+                        mbar_wait(FULL + 8 * (u % NSLOT), (u / NSLOT) & 1, 1ll << 28);
+                }
+            }
+        } else if (warp >= C::WARP_CONV + C::NCONV) {
+            // (scored calls: warps that only complete a warpgroup)
+        } else if (warp >= C::WARP_CONV) {
+            // ------------------------------------------------------------ converters
+            const int ct = tid - C::WARP_CONV * 32;
+            const int w = ct >> 5;
+            constexpr int NT = C::NCONV * 32;
+            for (uint32_t h = 0;; ++h) {
+                const uint32_t sl = h % NSLOT;
+                // The converter warps meet at named barriers below, so they must
+                // all stop at the same half-tile: each publishes its own reason
+                // to stop (a wait that expired, an abort, the end marker) and all
+                // decide from the published flags.
+                const bool ok = mbar_wait(FULL + 8 * sl, (h / NSLOT) & 1);
+                if (!ok) timeout();
+                if (lane == 0) misc[2 + w] = (!ok || misc[0] || meta[4 * sl + 1]) ? 1 : 0;
+                named_sync_conv<NT>();
+                int stop = 0;
+    #pragma unroll
+                for (int w2 = 0; w2 < C::NCONV; ++w2) stop |= misc[2 + w2];
+                if (stop) break;
+                const uint32_t rows = meta[4 * sl + 0];
+                uint8_t* hib = smem + sl * C::SLOT;
+                uint8_t* lob = hib + C::BUF;
+                if ((h & 1) == 0) {
+                    // K: the landed f32 tile is its own hi part (the tensor core
+                    // reads a TF32 operand's f32 bits with the low 13 mantissa
+                    // bits ignored, i.e. as x & 0xFFFFE000), so only the lo part
+                    // is written beside it (K-major, as TMA laid the tile out);
+                    // rows past the item's last key are zeroed in both
+                    float4* hi = reinterpret_cast<float4*>(hib);
+                    float4* lo = reinterpret_cast<float4*>(lob);
+    #pragma unroll
+                    for (int i = ct; i < C::BUF / 16; i += NT) {
+                        // each 128-byte row of a column block is 8 float4s
+                        const uint32_t row = static_cast<uint32_t>(i % (C::BLK / 16)) / 8;
+                        if (row >= rows) {
+                            hi[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            lo[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            continue;
+                        }
+                        const float4 x = hi[i];
+                        uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
+                        tf32_split(x.x, h0, l0);
+                        tf32_split(x.y, h1, l1);
+                        tf32_split(x.z, h2, l2);
+                        tf32_split(x.w, h3, l3);
+                        lo[i] = make_float4(__uint_as_float(l0), __uint_as_float(l1),
+                                            __uint_as_float(l2), __uint_as_float(l3));
+                    }
+                } else {
+                    // V: every 32 x 32 sub-block transposed (keys along the
+                    // 128-byte rows), hi in place, lo into the lo buffer.  All
+                    // converter threads read their sub-blocks (lane = dim, one
+                    // key per load) before any writes, so the in-place
+                    // permutation is safe whatever its cycles.
+                    float x[C::SB_PER_WARP][32];
+    #pragma unroll
+                    for (int j = 0; j < C::SB_PER_WARP; ++j) {
+                        const int sb = w + C::NCONV * j;
+                        const int kb = sb / NB, db = sb % NB;
+                        const uint8_t* src = hib + db * C::BLK + kb * 4096;
+    #pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const uint32_t off = (k / 8) * 1024 + (k % 8) * 128 +
+                                                 (((lane / 4) ^ (k % 8)) * 16) + (lane % 4) * 4;
+                            const float v = *reinterpret_cast<const float*>(src + off);
+                            x[j][k] = static_cast<uint32_t>(kb * 32 + k) < rows ? v : 0.f;
+                        }
+                    }
+                    if constexpr (SC) {
+                        // the largest magnitude's bits tell whether every value is finite
+                        uint32_t top = 0;
+    #pragma unroll
+                        for (int j = 0; j < C::SB_PER_WARP; ++j)
+    #pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const uint32_t u = __float_as_uint(x[j][k]) & 0x7FFFFFFFu;
+                                top = top > u ? top : u;
+                            }
+                        if (top >= 0x7F800000u) {
+                            misc[8] = 1;  // seen by the epilogue through this tile's barriers
+    #pragma unroll
+                            for (int j = 0; j < C::SB_PER_WARP; ++j)
+    #pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if ((__float_as_uint(x[j][k]) & 0x7F800000u) == 0x7F800000u)
+                                        x[j][k] = 0.f;
+                        }
+                    }
+                    named_sync_conv<NT>();
+    #pragma unroll
+                    for (int j = 0; j < C::SB_PER_WARP; ++j) {
+                        const int sb = w + C::NCONV * j;
+                        const int kb = sb / NB, db = sb % NB;
+                        const uint32_t base = kb * C::VT_BLK + db * 4096 + (lane / 8) * 1024 +
+                                              (lane % 8) * 128;
+    #pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t hh[4], ll[4];
+    #pragma unroll
+                            for (int e = 0; e < 4; ++e) tf32_split(x[j][4 * c + e], hh[e], ll[e]);
+                            const uint32_t off = base + ((c ^ (lane % 8)) * 16);
+                            *reinterpret_cast<uint4*>(hib + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                            *reinterpret_cast<uint4*>(lob + off) = make_uint4(ll[0], ll[1], ll[2], ll[3]);
+                        }
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(CONV + 8 * sl);
+            }
+        } else if (warp == C::WARP_MMA) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                uint32_t g = 0;  // key tiles whose QK was issued
+                bool ok = true;
+                auto converted = [&](uint32_t hh) {
+                    return mbar_wait(CONV + 8 * (hh % NSLOT), (hh / NSLOT) & 1);
+                };
+                // O += P V for tile t of the item (global tile gp)
+                auto issue_pv = [&](uint32_t t, uint32_t gp) {
+                    const uint32_t hv = 2 * gp + 1;
+                    if (!converted(hv) || !mbar_wait(PREADY + 8 * (gp & 1), (gp >> 1) & 1)) {
+                        timeout();
+                        return false;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t sl = hv % NSLOT;
+                    const uint32_t pcol0 = C::C_S + (gp % NBUF) * C::C_BUF;
+                    if constexpr (SC) {
+                        // the tile's own O: products with a low part first
+                        const uint32_t ocol = NBUF == 2 && (gp & 1) ? C::C_O2 : C::C_O;
+    #pragma unroll
+                        for (int kk = 0; kk < BK / 8; ++kk) {
+                            const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
+                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + BK + kk * 8, bh, C::IDESC_PV,
+                                            kk != 0 ? 1u : 0u);
+                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + kk * 8, bl, C::IDESC_PV, 1u);
+                        }
+    #pragma unroll
+                        for (int kk = 0; kk < BK / 8; ++kk) {
+                            const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
+                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + kk * 8, bh, C::IDESC_PV, 1u);
+                        }
+                    } else {
+                        // O += P_lo V_hi + P_hi V_hi + P_hi V_lo, K-step by K-step
+                        // (consecutive products share their B, then their A, slice)
+        #pragma unroll
+                        for (int kk = 0; kk < BK / 8; ++kk) {
+                            const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
+                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + BK + kk * 8, bh, C::IDESC_PV,
+                                            (t | kk) != 0 ? 1u : 0u);
+                            tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + kk * 8, bh, C::IDESC_PV, 1u);
+                            tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + kk * 8, bl, C::IDESC_PV, 1u);
+                        }
+                    }
+                    tc::mma_commit(PVDONE + 8 * (gp & 1));
+                    tc::mma_commit(EMPTY + 8 * sl);
+                    return true;
+                };
+                for (uint32_t k = 0; ok; ++k) {
+                    const uint32_t is = k & 1;
+                    if (!mbar_wait(IFULL + 8 * is, (k >> 1) & 1)) {
+                        timeout();
+                        break;
+                    }
+                    const uint32_t ntiles = desc[8 * is + 5], end = desc[8 * is + 6];
+                    mbar_arrive(IFREE + 8 * is);
+                    if (end || misc[0]) break;
+                    if (!mbar_wait(QREADY, k & 1)) {
+                        timeout();
                         break;
                     }
                     tc::fence_after_sync();
-                    // S = Q_lo K_hi + Q_hi K_hi + Q_hi K_lo, K-step by K-step
-                    // (consecutive products share their B, then their A, slice)
-                    const uint32_t sl = hk % NSLOT;
-                    const uint32_t scol = C::C_S + (g % NBUF) * C::C_BUF;
-#pragma unroll
-                    for (int kk = 0; kk < HD / 8; ++kk) {
-                        const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
-                        const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
-                        const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
-                        tc::mma_tf32_ts(tbase + scol, tbase + C::C_QLO + kk * 8, bh, C::IDESC_QK,
-                                        kk != 0 ? 1u : 0u);
-                        tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bh, C::IDESC_QK, 1u);
-                        tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bl, C::IDESC_QK, 1u);
-                    }
-                    // (the failure-path test option withholds the CTA's first
-                    // score-ready signal, so the softmax's bounded wait runs out)
-                    if (!(g == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SFULL + 8 * (g & 1));
-                    tc::mma_commit(EMPTY + 8 * sl);  // K slot free once QK has read it
-                    // one buffer: this tile's PV next; two: the previous tile's
-                    if (NBUF == 1) {
-                        if (!issue_pv(t, g)) {
+                    for (uint32_t t = 0; t < ntiles; ++t, ++g) {
+                        const uint32_t hk = 2 * g;
+                        if (!converted(hk)) {
+                            timeout();
                             ok = false;
                             break;
                         }
-                    } else if (t >= 1 && !issue_pv(t - 1, g - 1)) {
-                        ok = false;
-                        break;
+                        if (misc[0]) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        // S = Q_lo K_hi + Q_hi K_hi + Q_hi K_lo, K-step by K-step
+                        // (consecutive products share their B, then their A, slice)
+                        const uint32_t sl = hk % NSLOT;
+                        const uint32_t scol = C::C_S + (g % NBUF) * C::C_BUF;
+    #pragma unroll
+                        for (int kk = 0; kk < HD / 8; ++kk) {
+                            const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
+                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
+                            tc::mma_tf32_ts(tbase + scol, tbase + C::C_QLO + kk * 8, bh, C::IDESC_QK,
+                                            kk != 0 ? 1u : 0u);
+                            if constexpr (!SC)
+                                tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bh, C::IDESC_QK, 1u);
+                            tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bl, C::IDESC_QK, 1u);
+                        }
+                        if constexpr (SC) {  // the high products last
+    #pragma unroll
+                            for (int kk = 0; kk < HD / 8; ++kk) {
+                                const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
+                                const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                                tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bh, C::IDESC_QK, 1u);
+                            }
+                        }
+                        // (the failure-path test option withholds the CTA's first
+                        // score-ready signal, so the softmax's bounded wait runs out)
+                        if (!(g == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SFULL + 8 * (g & 1));
+                        tc::mma_commit(EMPTY + 8 * sl);  // K slot free once QK has read it
+                        // one buffer: this tile's PV next; two: the previous tile's
+                        if (NBUF == 1) {
+                            if (!issue_pv(t, g)) {
+                                ok = false;
+                                break;
+                            }
+                        } else if (t >= 1 && !issue_pv(t - 1, g - 1)) {
+                            ok = false;
+                            break;
+                        }
                     }
+                    if (NBUF == 2 && ok && ntiles && !misc[0] && !issue_pv(ntiles - 1, g - 1)) ok = false;
                 }
-                if (NBUF == 2 && ok && ntiles && !misc[0] && !issue_pv(ntiles - 1, g - 1)) ok = false;
+                // every MMA issued above has completed before tensor memory is freed
+                tc::mma_commit(DRAIN);
+                mbar_wait(DRAIN, 0, 1ll << 28);
             }
-            // every MMA issued above has completed before tensor memory is freed
-            tc::mma_commit(DRAIN);
-            mbar_wait(DRAIN, 0, 1ll << 28);
         }
     } else {
+        if constexpr (SC) regs_increase<C::REG_SOFTMAX>();
         // ------------------------------------------------------------ softmax
         // Warps q and q + 4 share tensor-memory lane quarter q (rows 32 q ..
         // 32 q + 31); half hf = warp / 4 takes columns [hf BK/2, (hf+1) BK/2)
@@ -694,11 +1006,12 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
             return buf[(1 - hf) * C::M + r];
         };
         uint32_t g = 0;  // key tiles processed
+        constexpr int ND = SC ? 7 : 5;
         // Meeting 1 opens item k: both halves hold its descriptor (xsum is
         // free: every meeting on it is followed by a pair barrier).  stop
         // carries a failure not yet published and becomes the pair's
         // decision; on success the descriptor's slot is released.
-        auto open_item = [&](uint32_t k, bool stop, uint32_t (&d)[5]) {
+        auto open_item = [&](uint32_t k, bool stop, uint32_t (&d)[ND]) {
             const uint32_t is = k & 1;
             stop = stop || misc[0];
             if (!stop && !mbar_wait(IFULL + 8 * is, (k >> 1) & 1)) {
@@ -712,6 +1025,10 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
             d[2] = desc[8 * is + 4];  // kv head
             d[3] = desc[8 * is + 5];  // key tiles
             d[4] = desc[8 * is + 6];  // end marker
+            if constexpr (SC) {
+                d[5] = desc[8 * is + 2];  // first key
+                d[6] = desc[8 * is + 3];  // split
+            }
             pair_sync();  // both have read meeting 1 before xsum is written again
             __syncwarp();
             if (lane == 0) mbar_arrive(IFREE + 8 * is);
@@ -720,13 +1037,23 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
         struct ItemRow {
             bool valid;
             uint32_t tok, pos, head;
+            uint32_t lo, hi;  // scored calls: the row's keys (none: lo > hi)
         };
-        auto row_of = [&](const uint32_t (&d)[5]) {
+        auto row_of = [&](const uint32_t (&d)[ND]) {
             ItemRow w;
             w.valid = r < static_cast<uint32_t>(C::ROWS) && t_local < d[1];
             w.tok = d[0] + t_local;
             w.pos = w.valid ? __ldg(P.positions + w.tok) : 0u;
             w.head = d[2] * G + h_local;
+            if constexpr (SC) {
+                w.lo = 1;
+                w.hi = 0;
+                if (w.valid) {
+                    const PrefillRow x = prefill_row(P, w.tok);
+                    w.lo = x.lo;
+                    w.hi = x.hi;
+                }
+            }
             return w;
         };
         // this half of the item's q rows into tensor memory, split hi / lo
@@ -739,10 +1066,17 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                 for (int c = 0; c < 32; c += 4) {
                     const float4 x = w.valid ? __ldcg(reinterpret_cast<const float4*>(qrow + c0 + c))
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-                    tf32_split(x.x, hi[c + 0], lo[c + 0]);
-                    tf32_split(x.y, hi[c + 1], lo[c + 1]);
-                    tf32_split(x.z, hi[c + 2], lo[c + 2]);
-                    tf32_split(x.w, hi[c + 3], lo[c + 3]);
+                    if constexpr (SC) {
+                        tf32_split_rn(x.x, hi[c + 0], lo[c + 0]);
+                        tf32_split_rn(x.y, hi[c + 1], lo[c + 1]);
+                        tf32_split_rn(x.z, hi[c + 2], lo[c + 2]);
+                        tf32_split_rn(x.w, hi[c + 3], lo[c + 3]);
+                    } else {
+                        tf32_split(x.x, hi[c + 0], lo[c + 0]);
+                        tf32_split(x.y, hi[c + 1], lo[c + 1]);
+                        tf32_split(x.z, hi[c + 2], lo[c + 2]);
+                        tf32_split(x.w, hi[c + 3], lo[c + 3]);
+                    }
                 }
                 tc::tmem_st32(lrow + C::C_QHI + c0, hi);
                 tc::tmem_st32(lrow + C::C_QLO + c0, lo);
@@ -752,15 +1086,55 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(QREADY);
         };
-        uint32_t d[5];
+        // Scored calls: this half's columns of O for its row, in registers.
+        // Key tile j's own O (from global tile j's PV) is added once PV(j) has
+        // completed; c is the correction of the running max since P(j).
+        [[maybe_unused]] float acc[SC ? HH : 1];
+        [[maybe_unused]] auto add_tile = [&](uint32_t j, float c) {
+            if (!mbar_wait(PVDONE + 8 * (j & 1), (j >> 1) & 1)) {
+                timeout();
+                return false;
+            }
+            tc::fence_after_sync();
+            const uint32_t ocol = NBUF == 2 && (j & 1) ? C::C_O2 : C::C_O;
+#pragma unroll
+            for (int c0 = 0; c0 < HH; c0 += 32) {
+                uint32_t v[32];
+                tc::tmem_ld32(lrow + ocol + hf * HH + c0, v);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    acc[SC ? c0 + i : 0] = fmaf(__uint_as_float(v[i]), c, acc[SC ? c0 + i : 0]);
+            }
+            return true;
+        };
+        uint32_t d[ND];
         if (open_item(0, false, d) && !d[4]) {
             ItemRow cur = row_of(d);
             load_q(cur);
             for (uint32_t k = 0;; ++k) {
                 const uint32_t ntiles = d[3];
+                [[maybe_unused]] uint32_t k_begin = 0, split = 0;
+                [[maybe_unused]] float slope2 = 0.f;
+                if constexpr (SC) {
+                    k_begin = d[5];
+                    split = d[6];
+                    if (P.rule.slopes) slope2 = __ldg(P.rule.slopes + cur.head) * kRuleLog2e;
+                }
                 float m = -CUDART_INF_F, l = 0.f;  // l: this half's share of the row sum
                 bool failed = false;
+                [[maybe_unused]] float corr_prev = 1.f;  // the last tile's correction of the max
+                if constexpr (SC) {
+#pragma unroll
+                    for (int i = 0; i < HH; ++i) acc[i] = 0.f;
+                }
                 for (uint32_t t = 0; t < ntiles; ++t, ++g) {
+                    // the O of tile t - NBUF, while the tensor core forms S(t)
+                    if constexpr (SC) {
+                        if (t >= static_cast<uint32_t>(NBUF) &&
+                            !add_tile(g - NBUF, NBUF == 2 ? corr_prev : 1.f))
+                            failed = true;
+                    }
                     if (!mbar_wait(SFULL + 8 * (g & 1), (g >> 1) & 1)) {
                         timeout();
                         failed = true;
@@ -776,9 +1150,33 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                         for (int c = 0; c < HB; ++c) s[c] = __uint_as_float(v[c]);
                     }
                     // causal mask: key kbase + c is attended iff it is <= cur.pos
-                    const uint32_t kbase = t * BK + hf * HB;
+                    uint32_t kbase = t * BK + hf * HB;
                     float mx = -CUDART_INF_F;
-                    if (kbase + HB - 1 <= cur.pos) {
+                    if constexpr (SC) {
+                        kbase += k_begin;
+                        if (P.rule.cap_out != 0.f) {
+#pragma unroll
+                            for (int c = 0; c < HB; ++c)
+                                s[c] = P.rule.cap_out * cap_tanh(s[c] * P.rule.cap_in);
+                        }
+                        if (P.rule.slopes) {
+                            const int d0 = static_cast<int>(cur.pos - kbase);
+#pragma unroll
+                            for (int c = 0; c < HB; ++c)
+                                s[c] = fmaf(-slope2, fabsf(static_cast<float>(d0 - c)), s[c]);
+                        }
+                        if (kbase >= cur.lo && kbase + HB - 1 <= cur.hi) {
+#pragma unroll
+                            for (int c = 0; c < HB; ++c) mx = fmaxf(mx, s[c]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < HB; ++c) {
+                                const uint32_t key = kbase + static_cast<uint32_t>(c);
+                                s[c] = key >= cur.lo && key <= cur.hi ? s[c] : -CUDART_INF_F;
+                                mx = fmaxf(mx, s[c]);
+                            }
+                        }
+                    } else if (kbase + HB - 1 <= cur.pos) {
 #pragma unroll
                         for (int c = 0; c < HB; ++c) mx = fmaxf(mx, s[c]);
                     } else {
@@ -813,6 +1211,15 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                         s[c] = s[c] == -CUDART_INF_F ? 0.f : fast_exp2(s[c] - m);
                         l += s[c];
                     }
+                    if constexpr (SC) {
+                        // O is in registers; the tile whose O is still to be
+                        // read takes the correction then
+                        if (rescale) {
+#pragma unroll
+                            for (int i = 0; i < HH; ++i) acc[i] *= corr;
+                        }
+                        corr_prev = rescale ? corr : 1.f;
+                    }
                     // O may be rescaled only once the previous tile's O += P V
                     // (global tile g - 1) has completed.  PV(j) completes a phase
                     // of pv_done[j % 2]; at any wait for PV(j), PV(j - 2) has
@@ -824,7 +1231,7 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                     // PV(j), and its parity would read as already complete.)
                     // Both halves of a row take the same decision; a wait that
                     // runs out is published at the next meeting.
-                    if (__any_sync(0xffffffffu, rescale)) {
+                    if (!SC && __any_sync(0xffffffffu, rescale)) {
                         if (!mbar_wait(PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1)) {
                             timeout();
                             failed = true;
@@ -845,7 +1252,10 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                     {
                         uint32_t hi[32], lo[32];
 #pragma unroll
-                        for (int c = 0; c < HB; ++c) tf32_split(s[c], hi[c], lo[c]);
+                        for (int c = 0; c < HB; ++c) {
+                            if constexpr (SC) tf32_split_rn(s[c], hi[c], lo[c]);
+                            else tf32_split(s[c], hi[c], lo[c]);
+                        }
                         tc::tmem_st32(lrow + scol, hi);
                         tc::tmem_st32(lrow + scol + BK, lo);
                     }
@@ -873,26 +1283,77 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
                 // covers every earlier MMA), then out = O / l (both halves'
                 // sums, sink included).  Meeting 3, the sums, publishes a
                 // wait that ran out.
-                bool stop3 = !mbar_wait(PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1);
-                if (stop3) timeout();
+                bool stop3;
+                if constexpr (SC) {
+                    stop3 = NBUF == 2 && ntiles >= 2 && !add_tile(g - 2, corr_prev);
+                    stop3 = !add_tile(g - 1, 1.f) || stop3;
+                } else {
+                    stop3 = !mbar_wait(PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                    if (stop3) timeout();
+                }
                 const float l_other = exchange(xsum, l, stop3);
                 pair_sync();  // both have read the sums before xsum is written again
                 if (stop3) break;
                 tc::fence_after_sync();
                 const float lt = l + l_other;
                 float f = 1.f / lt;
-                if (P.sinks) {
+                float* orow = P.out + (static_cast<size_t>(cur.tok) * P.n_head + cur.head) * HD;
+                bool direct = true;  // the row's output, not a split's partial
+                if constexpr (SC) {
+                    if (cur.valid) {
+                        const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + cur.tok);
+                        if (rec.z != 0u) {
+                            direct = false;
+                            f = 1.f;
+                            const size_t prow = (static_cast<size_t>(rec.x) +
+                                                 static_cast<size_t>(split) * rec.y) *
+                                                    P.n_head + cur.head;
+                            orow = P.part.acc + prow * HD;
+                            if (hf == 0)
+                                reinterpret_cast<float2*>(P.part.ml)[prow] = make_float2(m, lt);
+                        } else if (m == -CUDART_INF_F) {
+                            direct = false;
+                            f = 0.f;  // no key: zeros
+                        }
+                    }
+                }
+                if (direct && P.sinks) {
                     const float sk = __ldg(P.sinks + cur.head) * kLog2e;
                     const float M2 = fmaxf(m, sk);
                     const float c = exp2f(m - M2);
                     f = c / (lt * c + exp2f(sk - M2));
                 }
-                float* orow = P.out + (static_cast<size_t>(cur.tok) * P.n_head + cur.head) * HD;
+                [[maybe_unused]] const bool rescan = SC && misc[8] != 0;
 #pragma unroll
                 for (int c0 = hf * HH; c0 < (hf + 1) * HH; c0 += 32) {
                     uint32_t v[32];
-                    tc::tmem_ld32(lrow + C::C_O + c0, v);
-                    tc::tmem_ld_wait();
+                    if constexpr (SC) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            v[c] = __float_as_uint(acc[(c0 - hf * HH) + c]);
+                    } else {
+                        tc::tmem_ld32(lrow + C::C_O + c0, v);
+                        tc::tmem_ld_wait();
+                    }
+                    if constexpr (SC) {
+                        // the values the tensor core took as 0, for the keys
+                        // of this item that the row attends
+                        if (rescan && cur.valid) {
+                            const uint32_t slot = __ldg(P.slots + cur.tok);
+                            const uint32_t k_end = k_begin + ntiles * BK;  // past the item's keys
+                            for (uint32_t key = cur.lo > k_begin ? cur.lo : k_begin;
+                                 key <= cur.hi && key < k_end; ++key) {
+                                const float* vr = P.V + ((static_cast<size_t>(slot) * P.slot_ctx + key) *
+                                                             P.n_kv_head + cur.head / G) * HD + c0;
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) {
+                                    const float x = vr[c];
+                                    if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u)
+                                        v[c] = __float_as_uint(__uint_as_float(v[c]) + x);
+                                }
+                            }
+                        }
+                    }
                     if (cur.valid) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)
@@ -914,8 +1375,77 @@ __global__ void __launch_bounds__(PCfg<HD, G>::THREADS, 1)
     if (warp == 0) tc::tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
-template <int HD, int G>
-int launch_prefill_one(const PrefillParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+// Join the splits of a scored prefill: one warp per (token, head), splits in
+// order; rows the attention kernel has finished itself have no partials.
+template <int HD>
+__global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefillParams P) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t wg = blockIdx.x * 4 + (threadIdx.x >> 5);
+    grid_dependency_wait();
+    const uint32_t tok = wg / P.n_head, head = wg % P.n_head;
+    if (tok >= P.n_tok) return;
+    const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + tok);
+    if (rec.z == 0u) return;
+    const size_t at0 = static_cast<size_t>(rec.x) * P.n_head + head;
+    const size_t step = static_cast<size_t>(rec.y) * P.n_head;
+    // lanes take splits lane and lane + 32 (kMaxSplits is 64)
+    float2 c[2];
+    float M = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t s = lane + 32 * j;
+        c[j] = s < rec.z ? __ldcg(reinterpret_cast<const float2*>(P.part.ml) + at0 + s * step)
+                         : make_float2(-CUDART_INF_F, 0.f);
+        M = fmaxf(M, c[j].x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float w[2], L = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        w[j] = partial_weight(c[j].x, M);
+        L = __fmaf_rn(c[j].y, w[j], L);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    float f = 1.f / L;
+    if (M == -CUDART_INF_F) {
+        f = 0.f;  // no key: zeros
+    } else if (P.sinks) {
+        const float sk = __ldg(P.sinks + head) * kRuleLog2e;
+        const float M2 = fmaxf(M, sk);
+        const float cm = exp2f(M - M2);
+        f = cm / (L * cm + exp2f(sk - M2));
+    }
+    constexpr int EL = HD / 32;  // elements per lane
+    float a[EL] = {};
+    for (uint32_t s0 = 0; s0 < rec.z; s0 += 4) {
+        float v[4][EL];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2* src = reinterpret_cast<const float2*>(P.part.acc + (at0 + (s0 + u) * step) * HD);
+#pragma unroll
+            for (int e = 0; e < EL / 2; ++e) {
+                const float2 x = s0 + u < rec.z ? __ldcg(src + lane + 32 * e) : make_float2(0.f, 0.f);
+                v[u][2 * e] = x.x;
+                v[u][2 * e + 1] = x.y;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t s = s0 + u;
+            const float wu = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
+#pragma unroll
+            for (int e = 0; e < EL; ++e) a[e] = __fmaf_rn(wu, v[u][e], a[e]);
+        }
+    }
+    float2* o = reinterpret_cast<float2*>(P.out + (static_cast<size_t>(tok) * P.n_head + head) * HD);
+#pragma unroll
+    for (int e = 0; e < EL / 2; ++e) o[lane + 32 * e] = make_float2(a[2 * e] * f, a[2 * e + 1] * f);
+}
+
+template <int HD, int G, bool SC = false>
+int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        unsigned ctas, cudaStream_t stream) {
     using C = PCfg<HD, G>;
     static std::atomic<uint64_t> configured{0};
@@ -923,18 +1453,29 @@ int launch_prefill_one(const PrefillParams& p, const CUtensorMap& tmK, const CUt
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (!(configured.load(std::memory_order_acquire) & bit) || bit == 0) {
-        cudaError_t e = cudaFuncSetAttribute(slotkv_prefill_tc_kernel<HD, G>,
+        cudaError_t e = cudaFuncSetAttribute(slotkv_prefill_tc_kernel<HD, G, SC>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return static_cast<int>(e);
+        if constexpr (SC) {
+            // the register hand-over assumes 128 registers a thread; with
+            // fewer the softmax warps' request could never be met
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, slotkv_prefill_tc_kernel<HD, G, SC>);
+            if (e != cudaSuccess) return static_cast<int>(e);
+            if (fa.numRegs != 128) return static_cast<int>(cudaErrorInvalidConfiguration);
+        }
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    const uint32_t warps = p.n_tok * prep_groups(p.n_head, p.n_kv_head);
+    uint32_t groups = prep_groups(p.n_head, p.n_kv_head);
+    if constexpr (SC)
+        if (p.shared.lens) groups = prep_q_groups(p.n_head);
+    const uint32_t warps = p.n_tok * groups;
     // the plan (one CTA) first, then prep beside it as its programmatic
     // dependent; the attention kernel, launched in stream order, waits for
     // both.  Prep starts only once the plan runs, hence after the previous
     // call's attention kernel has finished reading the rows and q workspace
     // that prep overwrites.
-    slotkv_prefill_plan_kernel<C::MT><<<1, 1024, 0, stream>>>(p);
+    slotkv_prefill_plan_kernel<C::MT, C::BK, SC><<<1, 1024, 0, stream>>>(p);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -945,24 +1486,38 @@ int launch_prefill_one(const PrefillParams& p, const CUtensorMap& tmK, const CUt
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD>, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD, SC>, p);
     if (e != cudaSuccess) return static_cast<int>(e);
-    slotkv_prefill_tc_kernel<HD, G><<<ctas, C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
+    slotkv_prefill_tc_kernel<HD, G, SC>
+        <<<ctas, SC ? C::THREADS_SC : C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
+    if constexpr (SC) {
+        // a prefill that the plan may split: join the splits (at least
+        // ceil(n_tok / MT) tiles; the plan splits below kSplitBelow items per SM)
+        if (!p.shared.lens && static_cast<uint64_t>((p.n_tok + C::MT - 1) / C::MT) * p.n_kv_head <
+                                  static_cast<uint64_t>(kSplitBelow) * p.sms) {
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return static_cast<int>(e);
+            cfg.gridDim = dim3((p.n_tok * p.n_head + 3) / 4);
+            cfg.dynamicSmemBytes = 0;
+            e = cudaLaunchKernelEx(&cfg, slotkv_combine_kernel<HD>, p);
+            if (e != cudaSuccess) return static_cast<int>(e);
+        }
+    }
     return static_cast<int>(cudaGetLastError());
 }
 
-template <int HD>
-int launch_prefill_hd(int G, const PrefillParams& p, const CUtensorMap& tmK,
+template <int HD, bool SC = false>
+int launch_prefill_hd(int G, const prefill_params_t<SC>& p, const CUtensorMap& tmK,
                       const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_prefill_one<HD, 1>(p, tmK, tmV, ctas, stream);
-        case 2: return launch_prefill_one<HD, 2>(p, tmK, tmV, ctas, stream);
-        case 3: return launch_prefill_one<HD, 3>(p, tmK, tmV, ctas, stream);
-        case 4: return launch_prefill_one<HD, 4>(p, tmK, tmV, ctas, stream);
-        case 5: return launch_prefill_one<HD, 5>(p, tmK, tmV, ctas, stream);
-        case 6: return launch_prefill_one<HD, 6>(p, tmK, tmV, ctas, stream);
-        case 7: return launch_prefill_one<HD, 7>(p, tmK, tmV, ctas, stream);
-        case 8: return launch_prefill_one<HD, 8>(p, tmK, tmV, ctas, stream);
+        case 1: return launch_prefill_one<HD, 1, SC>(p, tmK, tmV, ctas, stream);
+        case 2: return launch_prefill_one<HD, 2, SC>(p, tmK, tmV, ctas, stream);
+        case 3: return launch_prefill_one<HD, 3, SC>(p, tmK, tmV, ctas, stream);
+        case 4: return launch_prefill_one<HD, 4, SC>(p, tmK, tmV, ctas, stream);
+        case 5: return launch_prefill_one<HD, 5, SC>(p, tmK, tmV, ctas, stream);
+        case 6: return launch_prefill_one<HD, 6, SC>(p, tmK, tmV, ctas, stream);
+        case 7: return launch_prefill_one<HD, 7, SC>(p, tmK, tmV, ctas, stream);
+        case 8: return launch_prefill_one<HD, 8, SC>(p, tmK, tmV, ctas, stream);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

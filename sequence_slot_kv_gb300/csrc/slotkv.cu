@@ -3,6 +3,7 @@
 // TMA descriptors for the slot buffers, and kernel dispatch.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -15,6 +16,7 @@
 #include <vector>
 
 #include "../../include/slotkv.h"
+#include "maps.h"
 #include "params.h"
 
 using slotkv::DecodeParams;
@@ -97,6 +99,14 @@ struct slotkv_s {
     uint32_t* pf_tile_of = nullptr;  // [tokens]
     uint32_t* pf_plan = nullptr;     // item count, hand-out counter
     size_t pf_q_elems = 0, pf_tok = 0;
+    // scored prefill and shared decode: a workspace of its own, allocated by
+    // the first such call at the size of the largest one the handle allows
+    // (so a captured call's pointers stay good until slot_kv_free); the
+    // splits' partials of a prefill and those of a prefix pass apart
+    float* sc_q = nullptr;            // [max_rows][max_n_head][hd] rotated q
+    uint32_t* sc_idx = nullptr;       // rec, tiles, tile_of, tile_lo, list, plan
+    float* sc_part[2] = {};           // (m, l) then acc, each partial_rows() head rows
+    uint32_t* map_scratch = nullptr;  // slot_kv_extend_tables: CTA counter, new head
     std::vector<slotkv_host_call_s*> calls;  // prepared host calls on this handle
     cudaStream_t copy_stream = nullptr;      // their enqueued input copies (created on demand)
     // prefill_batch_attn_host in parts: its outputs' copies, the second
@@ -169,6 +179,11 @@ void release(slotkv_s* h) {
     cudaFree(h->pf_tiles);
     cudaFree(h->pf_tile_of);
     cudaFree(h->pf_plan);
+    cudaFree(h->sc_q);
+    cudaFree(h->sc_idx);
+    cudaFree(h->sc_part[0]);
+    cudaFree(h->sc_part[1]);
+    cudaFree(h->map_scratch);
     if (h->owns_kv) {
         cudaFree(h->K);
         cudaFree(h->V);
@@ -354,13 +369,14 @@ CallShape call_shape(const slotkv_s* h, uint32_t B, uint64_t max_keys, bool pref
     return c;
 }
 
-int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float* k_new,
-           const float* v_new, const uint32_t* positions, const uint32_t* slots,
-           const float* q_norm_w, const float* k_norm_w, const float* inv_freq,
-           const float* sinks, float* out, float eps, float scale, cudaStream_t stream,
-           bool prefill = false, const uint32_t* block_tables = nullptr,
-           uint32_t bt_stride = 0) {
-    DecodeParams P;
+// A step's parameters and the shape of a call whose rows have at most
+// max_keys keys each.
+CallShape fill_params(slotkv_s* h, DecodeParams& P, uint32_t B, uint32_t n_head, const float* q,
+                      const float* k_new, const float* v_new, const uint32_t* positions,
+                      const uint32_t* slots, const float* q_norm_w, const float* k_norm_w,
+                      const float* inv_freq, const float* sinks, float* out, float eps,
+                      float scale, bool prefill, const uint32_t* block_tables,
+                      uint32_t bt_stride, uint64_t max_keys) {
     P.prefill = prefill ? 1u : 0u;
     P.block_tables = block_tables;
     P.bt_stride = bt_stride;
@@ -387,18 +403,31 @@ int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float
     P.n_head = n_head;
     P.n_kv_head = h->n_kv_head;
     P.B = B;
-    const uint64_t max_keys = block_tables ? (uint64_t)bt_stride * h->slot_ctx : h->slot_ctx;
     const CallShape cs = call_shape(h, B, max_keys, prefill);
     P.chunk_min = cs.chunk;
     P.max_splits = h->max_splits;
     P.eps = eps;
     P.scale_log2 = scale * 1.4426950408889634f;
     P.flags = h->options;
-    const int G = (int)(n_head / h->n_kv_head);
-    const unsigned ctas = cs.ctas;
     P.static_items = cs.static_items;
     P.static_second = cs.static_second;
     P.no_plan = cs.no_plan;
+    return cs;
+}
+
+int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float* k_new,
+           const float* v_new, const uint32_t* positions, const uint32_t* slots,
+           const float* q_norm_w, const float* k_norm_w, const float* inv_freq,
+           const float* sinks, float* out, float eps, float scale, cudaStream_t stream,
+           bool prefill = false, const uint32_t* block_tables = nullptr,
+           uint32_t bt_stride = 0) {
+    DecodeParams P;
+    const uint64_t max_keys = block_tables ? (uint64_t)bt_stride * h->slot_ctx : h->slot_ctx;
+    const CallShape cs =
+        fill_params(h, P, B, n_head, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                    inv_freq, sinks, out, eps, scale, prefill, block_tables, bt_stride, max_keys);
+    const int G = (int)(n_head / h->n_kv_head);
+    const unsigned ctas = cs.ctas;
     int rc;
     if (cs.small) {
         switch (h->head_dim) {
@@ -416,6 +445,131 @@ int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float
         default: return fail(SLOTKV_ERR_UNSUPPORTED, "head_dim %u", h->head_dim);
     }
     if (rc != 0) return cuda_fail((cudaError_t)rc, "decode kernel launch");
+    return SLOTKV_OK;
+}
+
+// ------------------------------------------------------------ scored calls
+int check_scores(const slotkv_scores* sc, bool prefill) {
+    if (!sc) return SLOTKV_OK;
+    // (the kernels divide by the cap and multiply by it: both stay normal)
+    if (!(sc->cap >= 0.f) || sc->cap > 1e30f || (sc->cap > 0.f && sc->cap < 1e-30f))
+        return fail(SLOTKV_ERR_ARG, "scores: cap=%g must be 0 or in 1e-30 .. 1e30",
+                    (double)sc->cap);
+    if (((uintptr_t)sc->slopes | (uintptr_t)sc->doc_start | (uintptr_t)sc->prefix_end) & 3)
+        return fail(SLOTKV_ERR_ARG, "scores: arrays must be 4-byte aligned");
+    if (sc->prefix_end && !prefill)
+        return fail(SLOTKV_ERR_ARG, "scores: prefix_end belongs to a prefill");
+    return SLOTKV_OK;
+}
+
+slotkv::ScoreRule score_rule(const slotkv_scores* sc) {
+    slotkv::ScoreRule r;
+    if (!sc) return r;
+    if (sc->cap > 0.f) {
+        r.cap_in = (float)(0.69314718055994531 / sc->cap);
+        r.cap_out = (float)(1.4426950408889634 * sc->cap);
+    }
+    r.window = sc->window;
+    r.slopes = sc->slopes;
+    r.doc_start = sc->doc_start;
+    r.prefix_end = sc->prefix_end;
+    return r;
+}
+
+// The first call that needs a buffer allocates it (cudaMalloc may synchronise
+// the device); a stream under capture cannot.
+int first_use(float** p, size_t floats, cudaStream_t stream, const char* what) {
+    if (*p) return SLOTKV_OK;
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &st);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    if (st != cudaStreamCaptureStatusNone)
+        return fail(SLOTKV_ERR_STATE, "%s is not allocated yet: make one such call before "
+                                      "capturing", what);
+    if ((e = cudaMalloc(p, floats * sizeof(float))) != cudaSuccess) {
+        *p = nullptr;
+        return cuda_fail(e, what);
+    }
+    return SLOTKV_OK;
+}
+
+uint32_t sm_total(const slotkv_s* h) { return (uint32_t)(h->sm_count > 0 ? h->sm_count : 1); }
+
+// Head rows of partials: what splits can need, and one per row and head of a
+// shared call that is not split.
+size_t partial_rows(const slotkv_s* h, bool shared) {
+    return slotkv::partial_head_rows(sm_total(h)) +
+           (shared ? (size_t)h->max_rows * h->max_n_head : 0);
+}
+
+// Workspace of the tensor-core kernels of a scored prefill (shared false) or
+// of the prefix pass of a shared call, into P.
+int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
+                     cudaStream_t stream) {
+    const size_t R = h->max_rows;
+    const size_t list = R + (size_t)slotkv::kSplitMost * sm_total(h);
+    const size_t pr = partial_rows(h, shared);
+    int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, stream, "scored workspace (q)");
+    if (rc == SLOTKV_OK)
+        rc = first_use(reinterpret_cast<float**>(&h->sc_idx), 10 * R + list + 4, stream,
+                       "scored workspace (items)");
+    if (rc == SLOTKV_OK)
+        rc = first_use(&h->sc_part[shared ? 1 : 0], pr * (2 + h->head_dim), stream,
+                       "scored workspace (partials)");
+    if (rc != SLOTKV_OK) return rc;
+    P.q_rot = h->sc_q;
+    P.part.rec = h->sc_idx;
+    P.tiles = h->sc_idx + 4 * R;
+    P.tile_of = h->sc_idx + 8 * R;
+    P.tile_lo = h->sc_idx + 9 * R;
+    P.list = h->sc_idx + 10 * R;
+    P.list_cap = (uint32_t)list;
+    P.plan = P.list + list;
+    P.sms = sm_total(h);
+    // acc first: its rows are read and written 16 bytes at a time
+    P.part.acc = h->sc_part[shared ? 1 : 0];
+    P.part.ml = P.part.acc + pr * h->head_dim;
+    return SLOTKV_OK;
+}
+
+int launch_scored(slotkv_s* h, const slotkv_scores* sc, const slotkv::SharedRows& shared,
+                  const slotkv::Partials& part, uint32_t B, uint32_t n_head, const float* q,
+                  const float* k_new, const float* v_new, const uint32_t* positions,
+                  const uint32_t* slots, const float* q_norm_w, const float* k_norm_w,
+                  const float* inv_freq, const float* sinks, float* out, float eps, float scale,
+                  cudaStream_t stream, bool prefill, const uint32_t* block_tables,
+                  uint32_t bt_stride) {
+    slotkv::ScoredDecodeParams P;
+    P.rule = score_rule(sc);
+    P.shared = shared;
+    P.part = part;
+    uint64_t max_keys = block_tables ? (uint64_t)bt_stride * h->slot_ctx : h->slot_ctx;
+    // a window bounds a row's keys, from its first key's tile on
+    const uint64_t T = (uint64_t)slotkv::tile_keys((int)h->head_dim);
+    if (P.rule.window && !P.rule.prefix_end)
+        max_keys = std::min<uint64_t>(max_keys, P.rule.window + T - 1);
+    const CallShape cs =
+        fill_params(h, P, B, n_head, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                    inv_freq, sinks, out, eps, scale, prefill, block_tables, bt_stride, max_keys);
+    const int G = (int)(n_head / h->n_kv_head);
+    const bool small = cs.small != 0;
+    int rc;
+    switch (h->head_dim) {
+        case 64: rc = slotkv::launch_scored_hd64(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
+        case 128: rc = slotkv::launch_scored_hd128(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
+        default: rc = slotkv::launch_scored_hd256(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
+    }
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "scored decode kernel launch");
+    return SLOTKV_OK;
+}
+
+int launch_scored_prefill(slotkv_s* h, const slotkv::ScoredPrefillParams& P,
+                          const CUtensorMap& tmK, const CUtensorMap& tmV, cudaStream_t stream) {
+    const int G = (int)(P.n_head / P.n_kv_head);
+    const int rc = h->head_dim == 64
+                       ? slotkv::launch_scored_prefill_hd64(G, P, tmK, tmV, P.sms, stream)
+                       : slotkv::launch_scored_prefill_hd128(G, P, tmK, tmV, P.sms, stream);
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "scored prefill kernel launch");
     return SLOTKV_OK;
 }
 
@@ -666,6 +820,11 @@ int slot_kv_alloc(slotkv_t* handle, uint32_t n_slots, uint32_t slot_ctx, uint32_
         if ((e = cudaMalloc(&h->status, sizeof(uint32_t))) != cudaSuccess ||
             (e = cudaMemset(h->status, 0, sizeof(uint32_t))) != cudaSuccess)
             rc = cuda_fail(e, "status word");
+    }
+    if (rc == SLOTKV_OK) {
+        if ((e = cudaMalloc(&h->map_scratch, 2 * sizeof(uint32_t))) != cudaSuccess ||
+            (e = cudaMemset(h->map_scratch, 0, 2 * sizeof(uint32_t))) != cudaSuccess)
+            rc = cuda_fail(e, "table scratch");
     }
     if (rc == SLOTKV_OK) {
         const size_t nq = (size_t)max_rows * max_n_head * head_dim;
@@ -1023,6 +1182,204 @@ int decode_batch_attn_paged(slotkv_t h, uint32_t B, uint32_t n_head, const float
     return launch(h, B, n_head, q, k_new, v_new, positions, nullptr, q_norm_w, k_norm_w,
                   inv_freq, sinks, out, eps, scale, (cudaStream_t)stream, false, block_tables,
                   bt_stride);
+}
+
+int decode_batch_attn_scored(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
+                             const float* k_new, const float* v_new, const uint32_t* positions,
+                             const uint32_t* slots, const float* q_norm_w,
+                             const float* k_norm_w, const float* inv_freq, const float* sinks,
+                             const slotkv_scores* scores, float* out, float eps, float scale,
+                             slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, B, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                               k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, false);
+    if (rc != SLOTKV_OK || B == 0) return rc;
+    return launch_scored(h, scores, {}, {}, B, n_head, q, k_new, v_new, positions, slots,
+                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale,
+                         (cudaStream_t)stream, false, nullptr, 0);
+}
+
+int decode_batch_attn_paged_scored(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
+                                   const float* k_new, const float* v_new,
+                                   const uint32_t* positions, const uint32_t* block_tables,
+                                   uint32_t bt_stride, const float* q_norm_w,
+                                   const float* k_norm_w, const float* inv_freq,
+                                   const float* sinks, const slotkv_scores* scores, float* out,
+                                   float eps, float scale, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, B, n_head, q, k_new, v_new, positions, block_tables,
+                               q_norm_w, k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, false);
+    if (rc != SLOTKV_OK) return rc;
+    const uint32_t T = (uint32_t)slotkv::tile_keys((int)h->head_dim);
+    if (h->slot_ctx % T != 0)
+        return fail(SLOTKV_ERR_UNSUPPORTED, "block size %u is not a multiple of %u keys",
+                    h->slot_ctx, T);
+    if (bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
+    if (B == 0) return SLOTKV_OK;
+    return launch_scored(h, scores, {}, {}, B, n_head, q, k_new, v_new, positions, nullptr,
+                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale,
+                         (cudaStream_t)stream, false, block_tables, bt_stride);
+}
+
+int prefill_batch_attn_scored(slotkv_t h, uint32_t n_tok, uint32_t n_head, const float* q,
+                              const float* k_new, const float* v_new, const uint32_t* positions,
+                              const uint32_t* slots, const float* q_norm_w,
+                              const float* k_norm_w, const float* inv_freq, const float* sinks,
+                              const slotkv_scores* scores, float* out, float eps, float scale,
+                              slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, n_tok, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                               k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, true);
+    if (rc != SLOTKV_OK || n_tok == 0) return rc;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (!h->tc_prefill)  // head dim 256: the decode kernel in prefill mode
+        return launch_scored(h, scores, {}, {}, n_tok, n_head, q, k_new, v_new, positions, slots,
+                             q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale, s, true,
+                             nullptr, 0);
+    slotkv::ScoredPrefillParams P;
+    rc = scored_workspace(h, false, P, s);
+    if (rc != SLOTKV_OK) return rc;
+    P.q = q;
+    P.k_new = k_new;
+    P.v_new = v_new;
+    P.positions = positions;
+    P.slots = slots;
+    P.q_norm_w = q_norm_w;
+    P.k_norm_w = k_norm_w;
+    P.inv_freq = inv_freq;
+    P.sinks = sinks;
+    P.out = out;
+    P.K = h->K;
+    P.V = h->V;
+    P.status = h->status;
+    P.n_slots = h->n_slots;
+    P.slot_ctx = h->slot_ctx;
+    P.n_head = n_head;
+    P.n_kv_head = h->n_kv_head;
+    P.n_tok = n_tok;
+    P.eps = eps;
+    P.scale_log2 = scale * 1.4426950408889634f;
+    P.flags = h->options;
+    P.rule = score_rule(scores);
+    return launch_scored_prefill(h, P, h->tmKs, h->tmVs, s);
+}
+
+int decode_batch_attn_shared(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
+                             const float* k_new, const float* v_new, const uint32_t* positions,
+                             const uint32_t* slots, slotkv_t prefix,
+                             const uint32_t* prefix_slots, const uint32_t* prefix_lens,
+                             const float* q_norm_w, const float* k_norm_w,
+                             const float* inv_freq, const float* sinks,
+                             const slotkv_scores* scores, float* out, float eps, float scale,
+                             slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, B, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                               k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, false);
+    if (rc != SLOTKV_OK) return rc;
+    if (!valid_handle(prefix)) return fail(SLOTKV_ERR_STATE, "prefix handle is not allocated");
+    if (prefix->device != h->device)
+        return fail(SLOTKV_ERR_STATE, "the prefix handle belongs to device %d, the rows' to %d",
+                    prefix->device, h->device);
+    if (prefix->n_kv_head != h->n_kv_head || prefix->head_dim != h->head_dim)
+        return fail(SLOTKV_ERR_ARG, "the prefix handle has %u kv heads of %u, the rows' %u of %u",
+                    prefix->n_kv_head, prefix->head_dim, h->n_kv_head, h->head_dim);
+    if (!h->tc_prefill)
+        return fail(SLOTKV_ERR_UNSUPPORTED, "a shared call needs head_dim 64 or 128, not %u",
+                    h->head_dim);
+    if (B == 0) return SLOTKV_OK;
+    if (!prefix_slots || !prefix_lens) return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (((uintptr_t)prefix_slots | (uintptr_t)prefix_lens) & 3)
+        return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    const cudaStream_t s = (cudaStream_t)stream;
+    slotkv::ScoredPrefillParams P;
+    rc = scored_workspace(h, true, P, s);
+    if (rc != SLOTKV_OK) return rc;
+    slotkv::SharedRows shared;
+    shared.slots = prefix_slots;
+    shared.lens = prefix_lens;
+    shared.n_slots = prefix->n_slots;
+    shared.slot_ctx = prefix->slot_ctx;
+    // the prefix pass: the rows' queries against their prefixes' slots
+    P.q = q;
+    P.k_new = P.v_new = nullptr;  // the decode kernel writes k' and v
+    P.positions = positions;
+    P.slots = prefix_slots;
+    P.q_norm_w = q_norm_w;
+    P.k_norm_w = k_norm_w;
+    P.inv_freq = inv_freq;
+    P.sinks = nullptr;
+    P.out = nullptr;
+    P.K = prefix->K;
+    P.V = prefix->V;
+    P.status = h->status;
+    P.n_slots = prefix->n_slots;
+    P.slot_ctx = prefix->slot_ctx;
+    P.n_head = n_head;
+    P.n_kv_head = h->n_kv_head;
+    P.n_tok = B;
+    P.eps = eps;
+    P.scale_log2 = scale * 1.4426950408889634f;
+    P.flags = h->options;
+    P.rule = score_rule(scores);
+    P.shared = shared;
+    P.own_slots = slots;
+    P.own_n_slots = h->n_slots;
+    P.own_ctx = h->slot_ctx;
+    rc = launch_scored_prefill(h, P, prefix->tmKs, prefix->tmVs, s);
+    if (rc != SLOTKV_OK) return rc;
+    return launch_scored(h, scores, shared, P.part, B, n_head, q, k_new, v_new, positions, slots,
+                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale, s, false, nullptr,
+                         0);
+}
+
+int slot_kv_token_map(slotkv_t h, uint32_t n_req, const uint32_t* slots, const uint32_t* past,
+                      const uint32_t* fresh, uint32_t n_tok, uint32_t* starts,
+                      uint32_t* tok_slots, uint32_t* tok_positions, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    if (!valid_handle(h)) return fail(SLOTKV_ERR_STATE, "handle is not allocated");
+    if (check_device(h) != SLOTKV_OK) return SLOTKV_ERR_STATE;
+    if (n_req > SLOTKV_MAX_REQUESTS)
+        return fail(SLOTKV_ERR_ARG, "n_req=%u exceeds %u", n_req, SLOTKV_MAX_REQUESTS);
+    if (!starts || (n_req && (!slots || !past || !fresh)) ||
+        (n_tok && (!tok_slots || !tok_positions)))
+        return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (((uintptr_t)slots | (uintptr_t)past | (uintptr_t)fresh | (uintptr_t)starts |
+         (uintptr_t)tok_slots | (uintptr_t)tok_positions) & 3)
+        return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    const slotkv::TokenMapParams P{slots,         past,      fresh, starts, tok_slots,
+                                   tok_positions, h->status, n_req, n_tok,  h->n_slots,
+                                   h->slot_ctx};
+    const int rc = slotkv::launch_token_map(P, (cudaStream_t)stream);
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "token map kernel launch");
+    return SLOTKV_OK;
+}
+
+int slot_kv_extend_tables(slotkv_t h, uint32_t n_req, const uint32_t* past,
+                          const uint32_t* fresh, uint32_t* block_tables, uint32_t bt_stride,
+                          const uint32_t* free_blocks, uint32_t n_free, const uint32_t* head,
+                          uint32_t* head_out, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    if (!valid_handle(h)) return fail(SLOTKV_ERR_STATE, "handle is not allocated");
+    if (check_device(h) != SLOTKV_OK) return SLOTKV_ERR_STATE;
+    if (n_req > SLOTKV_MAX_REQUESTS)
+        return fail(SLOTKV_ERR_ARG, "n_req=%u exceeds %u", n_req, SLOTKV_MAX_REQUESTS);
+    if (bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
+    if (!head || !head_out || (n_req && (!past || !fresh || !block_tables)) ||
+        (n_free && !free_blocks))
+        return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (((uintptr_t)past | (uintptr_t)fresh | (uintptr_t)block_tables | (uintptr_t)free_blocks |
+         (uintptr_t)head | (uintptr_t)head_out) & 3)
+        return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    const slotkv::ExtendTablesParams P{past,     fresh,          block_tables, free_blocks, head,
+                                       head_out, h->map_scratch, h->status,    n_req,       bt_stride,
+                                       h->slot_ctx, n_free};
+    const int rc = slotkv::launch_extend_tables(P, sm_total(h), (cudaStream_t)stream);
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "block table kernel launch");
+    return SLOTKV_OK;
 }
 
 int decode_batch_attn_host(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
