@@ -322,7 +322,7 @@ int decode_batch_attn_paged(slotkv_t handle, uint32_t B, uint32_t n_head, const 
  * nothing (doc_start[row] > hi) gets zeros; its K and V are written all the
  * same.  Keys a row does not attend never affect it, whatever they hold
  * (infinities and NaN included), unless noted at a call.
- *   cap         0: none; else 1e-30 .. 1e30.
+ *   cap         0: none; else 1e-6 .. 1e6.
  *   window      0: none; else keys t with p - t < window.
  *   slopes      device [n_head], or NULL.
  *   doc_start   device u32[rows], or NULL: the first key of the row's document.

@@ -199,6 +199,78 @@ def _stream_ptr(stream):
     return stream.cuda_stream
 
 
+class _Unlike(Exception):
+    """An argument is not what the fast path takes; the slow path says why."""
+
+
+def _addr(t, dtype, dev, shape):
+    """Address of a contiguous tensor of this type and shape on CUDA device
+    ``dev``.  A step's calls come every few microseconds, so the checks of a
+    good argument are a handful of attribute reads; anything else raises
+    _Unlike and is looked at again by _check_step and _ptr for its message."""
+    if (t.dtype is dtype and t.get_device() == dev and t.shape == shape and
+            t.is_contiguous()):
+        return t.data_ptr()
+    raise _Unlike
+
+
+def _step_addrs(kv, q, k_new, v_new, positions, rows_idx, out, q_norm_w, k_norm_w, inv_freq,
+                sinks, idx_name="slots"):
+    """(B, n_head, addresses of q, k_new, v_new, positions, the row index,
+    q_norm_w, k_norm_w, inv_freq, sinks, out, current device) of one step on
+    the current device."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    f, u = torch.float32, torch.int32
+    try:
+        B, n_head, hd = q.shape
+        row, kv_row = (B, n_head, hd), (B, kv.n_kv_head, hd)
+        if hd != kv.head_dim:
+            raise _Unlike
+        idx_shape = (B,) if idx_name == "slots" else (B, rows_idx.shape[1])
+        return (B, n_head, _addr(q, f, dev, row), _addr(k_new, f, dev, kv_row),
+                _addr(v_new, f, dev, kv_row), _addr(positions, u, dev, (B,)),
+                _addr(rows_idx, u, dev, idx_shape), _addr(q_norm_w, f, dev, (hd,)),
+                _addr(k_norm_w, f, dev, (hd,)), _addr(inv_freq, f, dev, (hd // 2,)),
+                None if sinks is None else _addr(sinks, f, dev, (n_head,)),
+                _addr(out, f, dev, row), dev)
+    except (_Unlike, AttributeError, TypeError, ValueError, IndexError):
+        pass
+    B, n_head = _check_step(q, k_new, v_new, positions, rows_idx, out, q_norm_w, k_norm_w,
+                            inv_freq, sinks, kv.n_kv_head, kv.head_dim, idx_name)
+    if idx_name != "slots" and (rows_idx.dim() != 2 or int(rows_idx.shape[0]) != B):
+        raise ValueError("block_tables must be [B][max_blocks]")
+    for name, t, dt in (("q", q, f), ("k_new", k_new, f), ("v_new", v_new, f),
+                        ("positions", positions, u), (idx_name, rows_idx, u),
+                        ("q_norm_w", q_norm_w, f), ("k_norm_w", k_norm_w, f),
+                        ("inv_freq", inv_freq, f), ("sinks", sinks, f), ("out", out, f)):
+        _ptr(t, dt, name)
+        _on_device(t, dev, name)
+    raise ValueError("the step's tensors cannot be used")
+
+
+def _on_device(t, dev, what):
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"{what} is on device {t.get_device()}, but device {dev} is current")
+
+
+def _int_addr(t, dev, what):
+    """Address of a contiguous int32 tensor on CUDA device ``dev`` (its shape
+    has been checked)."""
+    import torch
+    if t.get_device() != dev or t.dtype is not torch.int32 or not t.is_contiguous():
+        _ptr(t, torch.int32, what)
+        _on_device(t, dev, what)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 class Scores:
     """A score rule (slotkv_scores): tanh cap, window, per-head slopes of the
     distance bias (float32 [n_head]), the rows' document starts and, in a
@@ -209,9 +281,11 @@ class Scores:
         if not 0 <= int(window) < 2 ** 32:
             raise ValueError("window must be 0 .. 2^32 - 1")
         self.slopes, self.doc_start, self.prefix_end = slopes, doc_start, prefix_end
+        self._arrays = slopes is not None or doc_start is not None or prefix_end is not None
         self._c = _CScores(cap, int(window), _ptr(slopes, torch.float32, "slopes"),
                            _ptr(doc_start, torch.int32, "doc_start"),
                            _ptr(prefix_end, torch.int32, "prefix_end"))
+        self._ref = ctypes.byref(self._c)
 
     @property
     def cap(self):
@@ -222,15 +296,19 @@ class Scores:
         return self._c.window
 
 
-def _scores(sc, rows, n_head):
-    """The struct pointer of a Scores for a step of ``rows`` rows; None stays NULL."""
+def _scores(sc, rows, n_head, dev):
+    """The struct pointer of a Scores for a step of ``rows`` rows on device
+    ``dev``; None stays NULL."""
     if sc is None:
         return None
-    for name, t, n in (("slopes", sc.slopes, n_head), ("doc_start", sc.doc_start, rows),
-                       ("prefix_end", sc.prefix_end, rows)):
-        if t is not None and _shape(t) != (n,):
-            raise ValueError(f"{name} has shape {_shape(t)}, expected {(n,)}")
-    return ctypes.byref(sc._c)
+    if sc._arrays:
+        for name, t, n in (("slopes", sc.slopes, n_head), ("doc_start", sc.doc_start, rows),
+                           ("prefix_end", sc.prefix_end, rows)):
+            if t is not None:
+                if t.shape != (n,):
+                    raise ValueError(f"{name} has shape {_shape(t)}, expected {(n,)}")
+                _on_device(t, dev, name)
+    return sc._ref
 
 
 class SlotKV:
@@ -402,37 +480,23 @@ class SlotKV:
 
     def _slot_step_scored(self, name, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
                           inv_freq, sinks, scores, out, eps, scale, stream):
-        import torch
-        B, n_head = _check_step(q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w,
-                                inv_freq, sinks, self.n_kv_head, self.head_dim)
-        f, u = torch.float32, torch.int32
-        _check(getattr(_lib, name)(
-            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
-            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"), _ptr(slots, u, "slots"),
-            _ptr(q_norm_w, f, "q_norm_w"), _ptr(k_norm_w, f, "k_norm_w"),
-            _ptr(inv_freq, f, "inv_freq"), _ptr(sinks, f, "sinks"),
-            _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale, _stream_ptr(stream)),
-            name)
+        (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
+            self, q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w, inv_freq, sinks)
+        _check(getattr(_lib, name)(self._h, B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn,
+                                   _scores(scores, B, n_head, dev), ao, eps, scale,
+                                   _raw_stream(stream, dev)), name)
         return out
 
     def decode_batch_attn_paged_scored(self, q, k_new, v_new, positions, block_tables, q_norm_w,
                                        k_norm_w, inv_freq, sinks, scores, out, eps, scale,
                                        stream=None):
         """As decode_batch_attn_paged, with a score rule (Scores, or None)."""
-        import torch
-        B, n_head = _check_step(q, k_new, v_new, positions, block_tables, out, q_norm_w,
-                                k_norm_w, inv_freq, sinks, self.n_kv_head, self.head_dim,
-                                idx_name="block_tables")
-        f, u = torch.float32, torch.int32
-        if block_tables.dim() != 2 or int(block_tables.shape[0]) != B:
-            raise ValueError("block_tables must be [B][max_blocks]")
+        (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
+            self, q, k_new, v_new, positions, block_tables, out, q_norm_w, k_norm_w, inv_freq,
+            sinks, "block_tables")
         _check(_lib.decode_batch_attn_paged_scored(
-            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
-            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"),
-            _ptr(block_tables, u, "block_tables"), int(block_tables.shape[1]),
-            _ptr(q_norm_w, f, "q_norm_w"), _ptr(k_norm_w, f, "k_norm_w"),
-            _ptr(inv_freq, f, "inv_freq"), _ptr(sinks, f, "sinks"),
-            _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale, _stream_ptr(stream)),
+            self._h, B, n_head, aq, ak, av, ap, ai, int(block_tables.shape[1]), aqw, akw, af, asn,
+            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)),
             "decode_batch_attn_paged_scored")
         return out
 
@@ -442,39 +506,40 @@ class SlotKV:
         """The decode step for rows on shared prefixes: row b's positions
         0 .. prefix_lens[b] - 1 are in slot prefix_slots[b] of the SlotKV
         ``prefix``, the later ones in its own slot from position 0 on."""
-        import torch
-        B, n_head = _check_step(q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w,
-                                inv_freq, sinks, self.n_kv_head, self.head_dim)
-        for name, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
-            if t is None or _shape(t) != (B,):
-                raise ValueError(f"{name} must be [B]")
         if not isinstance(prefix, SlotKV):
             raise TypeError("prefix must be a SlotKV")
-        f, u = torch.float32, torch.int32
+        for name, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
+            if t is None or t.dim() != 1 or t.shape != positions.shape:
+                raise ValueError(f"{name} must be [B]")
+        (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
+            self, q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w, inv_freq, sinks)
         _check(_lib.decode_batch_attn_shared(
-            self._h, B, n_head, _ptr(q, f, "q"), _ptr(k_new, f, "k_new"),
-            _ptr(v_new, f, "v_new"), _ptr(positions, u, "positions"), _ptr(slots, u, "slots"),
-            prefix._h, _ptr(prefix_slots, u, "prefix_slots"),
-            _ptr(prefix_lens, u, "prefix_lens"), _ptr(q_norm_w, f, "q_norm_w"),
-            _ptr(k_norm_w, f, "k_norm_w"), _ptr(inv_freq, f, "inv_freq"),
-            _ptr(sinks, f, "sinks"), _scores(scores, B, n_head), _ptr(out, f, "out"), eps, scale,
-            _stream_ptr(stream)), "decode_batch_attn_shared")
+            self._h, B, n_head, aq, ak, av, ap, ai, prefix._h,
+            _int_addr(prefix_slots, dev, "prefix_slots"),
+            _int_addr(prefix_lens, dev, "prefix_lens"), aqw, akw, af, asn,
+            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)),
+            "decode_batch_attn_shared")
         return out
 
     def token_map(self, slots, past, fresh, starts, tok_slots, tok_positions, stream=None):
         """slot_kv_token_map: the slots and positions of a prefill's tokens from
         the requests' (slot, cached length, new length), int32 CUDA tensors."""
         import torch
-        u, n = torch.int32, int(slots.numel())
-        for name, t, shape in (("slots", slots, (n,)), ("past", past, (n,)),
-                               ("fresh", fresh, (n,)), ("starts", starts, (n + 1,)),
-                               ("tok_positions", tok_positions, _shape(tok_slots))):
-            if _shape(t) != shape or len(shape) != 1:
-                raise ValueError(f"{name} has shape {_shape(t)}, expected {shape}")
+        n, n_tok = slots.numel(), tok_slots.numel()
+        if not (slots.shape == past.shape == fresh.shape == (n,) and starts.shape == (n + 1,) and
+                tok_slots.shape == tok_positions.shape == (n_tok,)):
+            for name, t, m in (("slots", slots, n), ("past", past, n), ("fresh", fresh, n),
+                               ("starts", starts, n + 1), ("tok_slots", tok_slots, n_tok),
+                               ("tok_positions", tok_positions, n_tok)):
+                if t.shape != (m,):
+                    raise ValueError(f"{name} has shape {_shape(t)}, expected {(m,)}")
+        dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
         _check(_lib.slot_kv_token_map(
-            self._h, n, _ptr(slots, u, "slots"), _ptr(past, u, "past"), _ptr(fresh, u, "fresh"),
-            int(tok_slots.numel()), _ptr(starts, u, "starts"), _ptr(tok_slots, u, "tok_slots"),
-            _ptr(tok_positions, u, "tok_positions"), _stream_ptr(stream)), "slot_kv_token_map")
+            self._h, n, _int_addr(slots, dev, "slots"), _int_addr(past, dev, "past"),
+            _int_addr(fresh, dev, "fresh"), n_tok, _int_addr(starts, dev, "starts"),
+            _int_addr(tok_slots, dev, "tok_slots"),
+            _int_addr(tok_positions, dev, "tok_positions"), _raw_stream(stream, dev)),
+            "slot_kv_token_map")
         return starts, tok_slots, tok_positions
 
     def extend_tables(self, past, fresh, block_tables, free_blocks, head, head_out=None,
@@ -483,23 +548,26 @@ class SlotKV:
         place) extended from the free list; head_out None advances ``head``
         itself.  int32 CUDA tensors."""
         import torch
-        u, n = torch.int32, int(past.numel())
+        n = past.numel()
         if head_out is None:
             head_out = head
-        if block_tables.dim() != 2 or int(block_tables.shape[0]) != n:
+        if block_tables.dim() != 2 or block_tables.shape[0] != n:
             raise ValueError("block_tables must be [requests][max_blocks]")
-        for name, t, shape in (("past", past, (n,)), ("fresh", fresh, (n,)),
-                               ("head", head, (1,)), ("head_out", head_out, (1,))):
-            if _shape(t) != shape:
-                raise ValueError(f"{name} has shape {_shape(t)}, expected {shape}")
         if free_blocks.dim() != 1:
             raise ValueError("free_blocks must be [n_free]")
+        if not (past.shape == fresh.shape == (n,) and head.shape == head_out.shape == (1,)):
+            for name, t, m in (("past", past, n), ("fresh", fresh, n), ("head", head, 1),
+                               ("head_out", head_out, 1)):
+                if t.shape != (m,):
+                    raise ValueError(f"{name} has shape {_shape(t)}, expected {(m,)}")
+        dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+        n_free = free_blocks.shape[0]
         _check(_lib.slot_kv_extend_tables(
-            self._h, n, _ptr(past, u, "past"), _ptr(fresh, u, "fresh"),
-            _ptr(block_tables, u, "block_tables"), int(block_tables.shape[1]),
-            _ptr(free_blocks, u, "free_blocks"), int(free_blocks.numel()),
-            _ptr(head, u, "head"), _ptr(head_out, u, "head_out"), _stream_ptr(stream)),
-            "slot_kv_extend_tables")
+            self._h, n, _int_addr(past, dev, "past"), _int_addr(fresh, dev, "fresh"),
+            _int_addr(block_tables, dev, "block_tables"), block_tables.shape[1],
+            _int_addr(free_blocks, dev, "free_blocks"), n_free,
+            _int_addr(head, dev, "head"), _int_addr(head_out, dev, "head_out"),
+            _raw_stream(stream, dev)), "slot_kv_extend_tables")
         return block_tables, head_out
 
     def prepare_host_call(self, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,

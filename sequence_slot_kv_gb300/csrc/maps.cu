@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kMapThreads) slotkv_token_map_kernel(const Tok
     uint32_t r0, r1;
     my_part(P.R, r0, r1);
     uint64_t sum = 0, total;
+#pragma unroll 8
     for (uint32_t r = r0; r < r1; ++r) sum += __ldg(P.fresh + r);
     uint64_t at = block_exclusive(sum, sums, total);
     const bool head = blockIdx.x == 0;
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kMapThreads)
     my_part(P.R, r0, r1);
     if (threadIdx.x == 0) used = 0;
     uint64_t sum = 0, total;
+#pragma unroll 8
     for (uint32_t r = r0; r < r1; ++r) {
         uint32_t have, need;
         blocks_needed(P, r, have, need);

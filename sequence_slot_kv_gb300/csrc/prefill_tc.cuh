@@ -110,9 +110,11 @@ struct PCfg {
     static constexpr int WARP_TMA = 8, WARP_MMA = 9, WARP_CONV = 10, NCONV = 4;
     static constexpr int SB_PER_WARP = KB * NB / NCONV;  // V sub-blocks per converter warp
     static constexpr int THREADS = 32 * (WARP_CONV + NCONV);
-    // scored calls: whole warpgroups (two warps only hand registers over),
-    // launched at 128 registers a thread; the two softmax warpgroups, with O in
-    // registers, take them from the other two: 256 * 160 + 256 * 96 = 512 * 128
+    // scored calls: two more warps convert K while the four take V, so K(t + 1)
+    // and V(t) are converted side by side; that makes whole warpgroups,
+    // launched at 128 registers a thread, of which the two softmax ones, with O
+    // in registers, take from the other two: 256 * 160 + 256 * 96 = 512 * 128
+    static constexpr int NKCONV = 2;
     static constexpr int THREADS_SC = 512, REG_SOFTMAX = 160, REG_OTHER = 96;
     static_assert(256 * REG_SOFTMAX + 256 * REG_OTHER == THREADS_SC * 128,
                   "register hand-over must add up to the launch's registers");
@@ -180,6 +182,17 @@ __device__ __forceinline__ void tf32_split_rn(float x, uint32_t& hi, uint32_t& l
     const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
     hi = h;
     lo = __float_as_uint(x - __uint_as_float(h));
+}
+
+// Two at a time (one packed subtraction).
+__device__ __forceinline__ void tf32_split_rn2(float x, float y, uint32_t& hx, uint32_t& hy,
+                                               uint32_t& lx, uint32_t& ly) {
+    hx = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    hy = (__float_as_uint(y) + 0x1000u) & 0xFFFFE000u;
+    const float2 d = __ffma2_rn(make_float2(__uint_as_float(hx), __uint_as_float(hy)),
+                                make_float2(-1.f, -1.f), make_float2(x, y));
+    lx = __float_as_uint(d.x);
+    ly = __float_as_uint(d.y);
 }
 
 // ------------------------------------------------------------------ prep
@@ -673,6 +686,15 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                         }
                         meta[4 * (h % NSLOT) + 1] = 1;
                         mbar_arrive(FULL + 8 * (h % NSLOT));
+                        if constexpr (SC) {  // and one for the V converters
+                            ++h;
+                            if (!slot_free(h)) {
+                                timeout();
+                                break;
+                            }
+                            meta[4 * (h % NSLOT) + 1] = 1;
+                            mbar_arrive(FULL + 8 * (h % NSLOT));
+                        }
                         break;
                     }
                     // in the plan's hand-out order
@@ -732,13 +754,54 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 }
             }
         } else if (warp >= C::WARP_CONV + C::NCONV) {
-            // (scored calls: warps that only complete a warpgroup)
+            // ------------------------------------------------------------ K converters
+            // (scored calls; the others below then only take V).  K's lo part
+            // beside it, as below, with all of a thread's loads of a batch in
+            // flight before its stores; no warp waits for another.
+            constexpr int NT = C::NKCONV * 32, PER = C::BUF / 16 / NT, BATCH = 8;
+            static_assert(PER % BATCH == 0, "whole batches");
+            const int ct = tid - (C::WARP_CONV + C::NCONV) * 32;
+            for (uint32_t h = 0;; h += 2) {
+                const uint32_t sl = h % NSLOT;
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(FULL + 8 * sl, (h / NSLOT) & 1));
+                if (!ok) timeout();
+                if (__any_sync(0xffffffffu, !ok || misc[0] || meta[4 * sl + 1])) break;
+                const uint32_t rows = meta[4 * sl + 0];
+                float4* hi = reinterpret_cast<float4*>(smem + sl * C::SLOT);
+                float4* lo = reinterpret_cast<float4*>(smem + sl * C::SLOT + C::BUF);
+#pragma unroll
+                for (int b = 0; b < PER; b += BATCH) {
+                    float4 x[BATCH];
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) x[j] = hi[ct + (b + j) * NT];
+#pragma unroll
+                    for (int j = 0; j < BATCH; ++j) {
+                        const int i = ct + (b + j) * NT;
+                        const uint32_t row = static_cast<uint32_t>(i % (C::BLK / 16)) / 8;
+                        if (row >= rows) {  // past the item's last key
+                            x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            hi[i] = x[j];
+                        }
+                        uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
+                        tf32_split(x[j].x, h0, l0);
+                        tf32_split(x[j].y, h1, l1);
+                        tf32_split(x[j].z, h2, l2);
+                        tf32_split(x[j].w, h3, l3);
+                        lo[i] = make_float4(__uint_as_float(l0), __uint_as_float(l1),
+                                            __uint_as_float(l2), __uint_as_float(l3));
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane < C::NCONV / C::NKCONV) mbar_arrive(CONV + 8 * sl);
+            }
         } else if (warp >= C::WARP_CONV) {
             // ------------------------------------------------------------ converters
             const int ct = tid - C::WARP_CONV * 32;
             const int w = ct >> 5;
             constexpr int NT = C::NCONV * 32;
-            for (uint32_t h = 0;; ++h) {
+            // (scored calls: V only, the odd half-tiles)
+            for (uint32_t h = SC ? 1 : 0;; h += SC ? 2 : 1) {
                 const uint32_t sl = h % NSLOT;
                 // The converter warps meet at named barriers below, so they must
                 // all stop at the same half-tile: each publishes its own reason
@@ -755,7 +818,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 const uint32_t rows = meta[4 * sl + 0];
                 uint8_t* hib = smem + sl * C::SLOT;
                 uint8_t* lob = hib + C::BUF;
-                if ((h & 1) == 0) {
+                if (!SC && (h & 1) == 0) {
                     // K: the landed f32 tile is its own hi part (the tensor core
                     // reads a TF32 operand's f32 bits with the low 13 mantissa
                     // bits ignored, i.e. as x & 0xFFFFE000), so only the lo part
@@ -845,16 +908,33 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
             }
         } else if (warp == C::WARP_MMA) {
             // ------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
+            // Plain calls: one thread runs the role.  Scored calls: the whole
+            // warp does, in step, and one elected lane issues -- what an MMA
+            // instruction takes (tensor memory columns, descriptors) is then
+            // known to be the same in all lanes, so the compiler keeps it in
+            // uniform registers instead of moving it there for each MMA
+            if (SC || lane == 0) {
+                const uint32_t tb = SC ? __shfl_sync(0xffffffffu, tbase, 0) : tbase;
+                const bool lead = !SC || tc::elect_one();
                 uint32_t g = 0;  // key tiles whose QK was issued
                 bool ok = true;
+                // a wait's outcome and the abort flag, the same for the whole
+                // warp (the lanes meet again below, so they leave together)
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    const bool done = mbar_wait(bar, parity);
+                    return SC ? __all_sync(0xffffffffu, done) != 0 : done;
+                };
+                auto aborted = [&]() {
+                    const bool a = misc[0] != 0;
+                    return SC ? __any_sync(0xffffffffu, a) != 0 : a;
+                };
                 auto converted = [&](uint32_t hh) {
-                    return mbar_wait(CONV + 8 * (hh % NSLOT), (hh / NSLOT) & 1);
+                    return wait(CONV + 8 * (hh % NSLOT), (hh / NSLOT) & 1);
                 };
                 // O += P V for tile t of the item (global tile gp)
                 auto issue_pv = [&](uint32_t t, uint32_t gp) {
                     const uint32_t hv = 2 * gp + 1;
-                    if (!converted(hv) || !mbar_wait(PREADY + 8 * (gp & 1), (gp >> 1) & 1)) {
+                    if (!converted(hv) || !wait(PREADY + 8 * (gp & 1), (gp >> 1) & 1)) {
                         timeout();
                         return false;
                     }
@@ -863,21 +943,22 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     const uint32_t pcol0 = C::C_S + (gp % NBUF) * C::C_BUF;
                     if constexpr (SC) {
                         // the tile's own O: products with a low part first
-                        const uint32_t ocol = NBUF == 2 && (gp & 1) ? C::C_O2 : C::C_O;
-    #pragma unroll
-                        for (int kk = 0; kk < BK / 8; ++kk) {
-                            const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
-                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
-                            const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
-                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + BK + kk * 8, bh, C::IDESC_PV,
-                                            kk != 0 ? 1u : 0u);
-                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + kk * 8, bl, C::IDESC_PV, 1u);
-                        }
-    #pragma unroll
-                        for (int kk = 0; kk < BK / 8; ++kk) {
-                            const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
-                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
-                            tc::mma_tf32_ts(tbase + ocol, tbase + pcol0 + kk * 8, bh, C::IDESC_PV, 1u);
+                        const uint32_t ocol = tb + (NBUF == 2 && (gp & 1) ? C::C_O2 : C::C_O);
+                        const uint32_t phi = tb + pcol0, plo = phi + BK;
+                        const uint64_t bh = tc::smem_desc(slot_hi(sl), 16, 1024, tc::kSwizzle128B);
+                        const uint64_t bl = tc::smem_desc(slot_lo(sl), 16, 1024, tc::kSwizzle128B);
+                        if (lead) {
+#pragma unroll
+                            for (int kk = 0; kk < BK / 8; ++kk) {
+                                const uint32_t off = ((kk / 4) * C::VT_BLK + (kk % 4) * 32) >> 4;
+                                tc::mma_tf32_ts(ocol, plo + kk * 8, bh + off, C::IDESC_PV, kk != 0 ? 1u : 0u);
+                                tc::mma_tf32_ts(ocol, phi + kk * 8, bl + off, C::IDESC_PV, 1u);
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < BK / 8; ++kk) {
+                                const uint32_t off = ((kk / 4) * C::VT_BLK + (kk % 4) * 32) >> 4;
+                                tc::mma_tf32_ts(ocol, phi + kk * 8, bh + off, C::IDESC_PV, 1u);
+                            }
                         }
                     } else {
                         // O += P_lo V_hi + P_hi V_hi + P_hi V_lo, K-step by K-step
@@ -893,20 +974,27 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             tc::mma_tf32_ts(tbase + C::C_O, tbase + pcol0 + kk * 8, bl, C::IDESC_PV, 1u);
                         }
                     }
-                    tc::mma_commit(PVDONE + 8 * (gp & 1));
-                    tc::mma_commit(EMPTY + 8 * sl);
+                    if (lead) {
+                        tc::mma_commit(PVDONE + 8 * (gp & 1));
+                        tc::mma_commit(EMPTY + 8 * sl);
+                    }
+                    __syncwarp(SC ? 0xffffffffu : 1u);
                     return true;
                 };
                 for (uint32_t k = 0; ok; ++k) {
                     const uint32_t is = k & 1;
-                    if (!mbar_wait(IFULL + 8 * is, (k >> 1) & 1)) {
+                    if (!wait(IFULL + 8 * is, (k >> 1) & 1)) {
                         timeout();
                         break;
                     }
-                    const uint32_t ntiles = desc[8 * is + 5], end = desc[8 * is + 6];
-                    mbar_arrive(IFREE + 8 * is);
-                    if (end || misc[0]) break;
-                    if (!mbar_wait(QREADY, k & 1)) {
+                    uint32_t ntiles = desc[8 * is + 5], end = desc[8 * is + 6];
+                    if constexpr (SC) {
+                        ntiles = __shfl_sync(0xffffffffu, ntiles, 0);
+                        end = __shfl_sync(0xffffffffu, end, 0);
+                    }
+                    if (lead) mbar_arrive(IFREE + 8 * is);
+                    if (end || aborted()) break;
+                    if (!wait(QREADY, k & 1)) {
                         timeout();
                         break;
                     }
@@ -918,38 +1006,52 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             ok = false;
                             break;
                         }
-                        if (misc[0]) {
+                        if (aborted()) {
                             ok = false;
                             break;
                         }
                         tc::fence_after_sync();
-                        // S = Q_lo K_hi + Q_hi K_hi + Q_hi K_lo, K-step by K-step
-                        // (consecutive products share their B, then their A, slice)
                         const uint32_t sl = hk % NSLOT;
                         const uint32_t scol = C::C_S + (g % NBUF) * C::C_BUF;
-    #pragma unroll
-                        for (int kk = 0; kk < HD / 8; ++kk) {
-                            const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
-                            const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
-                            const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
-                            tc::mma_tf32_ts(tbase + scol, tbase + C::C_QLO + kk * 8, bh, C::IDESC_QK,
-                                            kk != 0 ? 1u : 0u);
-                            if constexpr (!SC)
-                                tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bh, C::IDESC_QK, 1u);
-                            tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bl, C::IDESC_QK, 1u);
-                        }
-                        if constexpr (SC) {  // the high products last
-    #pragma unroll
+                        if constexpr (SC) {
+                            // S: products with a low part first, the high ones last
+                            const uint64_t bh = tc::smem_desc(slot_hi(sl), 16, 1024, tc::kSwizzle128B);
+                            const uint64_t bl = tc::smem_desc(slot_lo(sl), 16, 1024, tc::kSwizzle128B);
+                            if (lead) {
+#pragma unroll
+                                for (int kk = 0; kk < HD / 8; ++kk) {
+                                    const uint32_t off = ((kk / 4) * C::BLK + (kk % 4) * 32) >> 4;
+                                    tc::mma_tf32_ts(tb + scol, tb + C::C_QLO + kk * 8, bh + off, C::IDESC_QK,
+                                                    kk != 0 ? 1u : 0u);
+                                    tc::mma_tf32_ts(tb + scol, tb + C::C_QHI + kk * 8, bl + off, C::IDESC_QK, 1u);
+                                }
+#pragma unroll
+                                for (int kk = 0; kk < HD / 8; ++kk) {
+                                    const uint32_t off = ((kk / 4) * C::BLK + (kk % 4) * 32) >> 4;
+                                    tc::mma_tf32_ts(tb + scol, tb + C::C_QHI + kk * 8, bh + off, C::IDESC_QK, 1u);
+                                }
+                            }
+                        } else {
+                            // S = Q_lo K_hi + Q_hi K_hi + Q_hi K_lo, K-step by K-step
+                            // (consecutive products share their B, then their A, slice)
+#pragma unroll
                             for (int kk = 0; kk < HD / 8; ++kk) {
                                 const uint32_t off = (kk / 4) * C::BLK + (kk % 4) * 32;
                                 const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
+                                const uint64_t bl = tc::smem_desc(slot_lo(sl) + off, 16, 1024, tc::kSwizzle128B);
+                                tc::mma_tf32_ts(tbase + scol, tbase + C::C_QLO + kk * 8, bh, C::IDESC_QK,
+                                                kk != 0 ? 1u : 0u);
                                 tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bh, C::IDESC_QK, 1u);
+                                tc::mma_tf32_ts(tbase + scol, tbase + C::C_QHI + kk * 8, bl, C::IDESC_QK, 1u);
                             }
                         }
                         // (the failure-path test option withholds the CTA's first
                         // score-ready signal, so the softmax's bounded wait runs out)
-                        if (!(g == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SFULL + 8 * (g & 1));
-                        tc::mma_commit(EMPTY + 8 * sl);  // K slot free once QK has read it
+                        if (lead) {
+                            if (!(g == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SFULL + 8 * (g & 1));
+                            tc::mma_commit(EMPTY + 8 * sl);  // K slot free once QK has read it
+                        }
+                        __syncwarp(SC ? 0xffffffffu : 1u);
                         // one buffer: this tile's PV next; two: the previous tile's
                         if (NBUF == 1) {
                             if (!issue_pv(t, g)) {
@@ -961,10 +1063,10 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             break;
                         }
                     }
-                    if (NBUF == 2 && ok && ntiles && !misc[0] && !issue_pv(ntiles - 1, g - 1)) ok = false;
+                    if (NBUF == 2 && ok && ntiles && !aborted() && !issue_pv(ntiles - 1, g - 1)) ok = false;
                 }
                 // every MMA issued above has completed before tensor memory is freed
-                tc::mma_commit(DRAIN);
+                if (lead) tc::mma_commit(DRAIN);
                 mbar_wait(DRAIN, 0, 1ll << 28);
             }
         }
@@ -992,6 +1094,17 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
         int* xflag = reinterpret_cast<int*>(xmax + 6 * C::M);       // beside each value
         auto pair_sync = [&]() {
             asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory");
+        };
+        // Meet, and return whether any of the pair's 64 threads says so.
+        [[maybe_unused]] auto pair_any = [&](bool x) {
+            uint32_t any;
+            asm volatile(
+                "{\n\t.reg .pred P, Q;\n\tsetp.ne.u32 P, %1, 0;\n\t"
+                "bar.red.or.pred Q, %2, 64, P;\n\tselp.u32 %0, 1, 0, Q;\n\t}"
+                : "=r"(any)
+                : "r"(x ? 1u : 0u), "r"(3 + quarter)
+                : "memory");
+            return any != 0;
         };
         // Publish v and this warp's stop flag (any lane's) in slot [hf][r] of
         // buf, meet, and return the partner's value; stop becomes the pair's
@@ -1090,6 +1203,17 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
         // Key tile j's own O (from global tile j's PV) is added once PV(j) has
         // completed; c is the correction of the running max since P(j).
         [[maybe_unused]] float acc[SC ? HH : 1];
+        [[maybe_unused]] auto add_o = [&](int c0, const uint32_t (&v)[32], float c) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const int at = SC ? c0 + i : 0, at1 = SC ? c0 + i + 1 : 0;
+                const float2 a = __ffma2_rn(
+                    make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                    make_float2(c, c), make_float2(acc[at], acc[at1]));
+                acc[at] = a.x;
+                acc[at1] = a.y;
+            }
+        };
         [[maybe_unused]] auto add_tile = [&](uint32_t j, float c) {
             if (!mbar_wait(PVDONE + 8 * (j & 1), (j >> 1) & 1)) {
                 timeout();
@@ -1102,12 +1226,12 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 uint32_t v[32];
                 tc::tmem_ld32(lrow + ocol + hf * HH + c0, v);
                 tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    acc[SC ? c0 + i : 0] = fmaf(__uint_as_float(v[i]), c, acc[SC ? c0 + i : 0]);
+                add_o(c0, v, c);
             }
             return true;
         };
+        [[maybe_unused]] CapSeries cap_k{};
+        if constexpr (SC) cap_k = cap_series(P.rule.cap_in);
         uint32_t d[ND];
         if (open_item(0, false, d) && !d[4]) {
             ItemRow cur = row_of(d);
@@ -1129,11 +1253,10 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     for (int i = 0; i < HH; ++i) acc[i] = 0.f;
                 }
                 for (uint32_t t = 0; t < ntiles; ++t, ++g) {
-                    // the O of tile t - NBUF, while the tensor core forms S(t)
-                    if constexpr (SC) {
-                        if (t >= static_cast<uint32_t>(NBUF) &&
-                            !add_tile(g - NBUF, NBUF == 2 ? corr_prev : 1.f))
-                            failed = true;
+                    // one score buffer: the O of tile t - 1, while the tensor
+                    // core forms S(t)
+                    if constexpr (SC && NBUF == 1) {
+                        if (t >= 1 && !add_tile(g - 1, 1.f)) failed = true;
                     }
                     if (!mbar_wait(SFULL + 8 * (g & 1), (g >> 1) & 1)) {
                         timeout();
@@ -1145,6 +1268,17 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     {
                         uint32_t v[32];
                         tc::tmem_ld32(lrow + scol, v);
+                        if constexpr (SC && NBUF == 2) {
+                            // two: the O of tile t - 2 with S(t), whose commit
+                            // covers its PV
+                            static_assert(NBUF == 1 || HH == 32, "one access per half of O");
+                            if (t >= 2) {
+                                uint32_t o[32];
+                                tc::tmem_ld32(lrow + (g & 1 ? C::C_O2 : C::C_O) + hf * HH, o);
+                                tc::tmem_ld_wait();
+                                add_o(0, o, corr_prev);
+                            }
+                        }
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int c = 0; c < HB; ++c) s[c] = __uint_as_float(v[c]);
@@ -1154,28 +1288,24 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     float mx = -CUDART_INF_F;
                     if constexpr (SC) {
                         kbase += k_begin;
-                        if (P.rule.cap_out != 0.f) {
-#pragma unroll
-                            for (int c = 0; c < HB; ++c)
-                                s[c] = P.rule.cap_out * cap_tanh(s[c] * P.rule.cap_in);
-                        }
+                        if (P.rule.cap_out != 0.f) cap_scores(s, P.rule, cap_k);
                         if (P.rule.slopes) {
-                            const int d0 = static_cast<int>(cur.pos - kbase);
+                            const float d0 = static_cast<float>(static_cast<int>(cur.pos - kbase));
 #pragma unroll
                             for (int c = 0; c < HB; ++c)
-                                s[c] = fmaf(-slope2, fabsf(static_cast<float>(d0 - c)), s[c]);
+                                s[c] = fmaf(-slope2, fabsf(d0 - static_cast<float>(c)), s[c]);
                         }
-                        if (kbase >= cur.lo && kbase + HB - 1 <= cur.hi) {
-#pragma unroll
-                            for (int c = 0; c < HB; ++c) mx = fmaxf(mx, s[c]);
-                        } else {
+                        if (kbase < cur.lo || kbase + HB - 1 > cur.hi) {
 #pragma unroll
                             for (int c = 0; c < HB; ++c) {
                                 const uint32_t key = kbase + static_cast<uint32_t>(c);
                                 s[c] = key >= cur.lo && key <= cur.hi ? s[c] : -CUDART_INF_F;
-                                mx = fmaxf(mx, s[c]);
                             }
                         }
+                        float m4[4] = {s[0], s[1], s[2], s[3]};  // four short chains
+#pragma unroll
+                        for (int c = 4; c < HB; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     } else if (kbase + HB - 1 <= cur.pos) {
 #pragma unroll
                         for (int c = 0; c < HB; ++c) mx = fmaxf(mx, s[c]);
@@ -1191,12 +1321,16 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     // again only after the next meeting, which its partner
                     // reaches after reading p)
                     bool stop2 = failed || misc[0];
-                    const float other = exchange(xmax + (g & 1) * 2 * C::M, mx, stop2);
-                    if (stop2) {
-                        failed = true;
-                        break;
+                    // (scored calls: the values are exchanged only when some
+                    // row of the pair would raise its max, or to stop)
+                    if (!SC || pair_any(stop2 || mx > m + 8.f)) {
+                        const float other = exchange(xmax + (g & 1) * 2 * C::M, mx, stop2);
+                        if (stop2) {
+                            failed = true;
+                            break;
+                        }
+                        mx = fmaxf(mx, other);
                     }
-                    mx = fmaxf(mx, other);
                     // lazy running max: raised only when a score passes it by 2^8
                     float corr = 1.f;
                     bool rescale = false;
@@ -1206,10 +1340,25 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                         l *= corr;
                         m = mx;
                     }
+                    if constexpr (SC) {
+                        // (a row without a key so far: every score is -inf, every weight 0)
+                        const float m0 = m == -CUDART_INF_F ? 0.f : m;
+                        const float2 mm = make_float2(-m0, -m0);
+                        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < HB; ++c) {
-                        s[c] = s[c] == -CUDART_INF_F ? 0.f : fast_exp2(s[c] - m);
-                        l += s[c];
+                        for (int c = 0; c < HB; c += 2) {
+                            const float2 x = __fadd2_rn(make_float2(s[c], s[c + 1]), mm);
+                            s[c] = fast_exp2(x.x);
+                            s[c + 1] = fast_exp2(x.y);
+                            l2[(c >> 1) & 1] = __fadd2_rn(l2[(c >> 1) & 1], make_float2(s[c], s[c + 1]));
+                        }
+                        l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < HB; ++c) {
+                            s[c] = s[c] == -CUDART_INF_F ? 0.f : fast_exp2(s[c] - m);
+                            l += s[c];
+                        }
                     }
                     if constexpr (SC) {
                         // O is in registers; the tile whose O is still to be
@@ -1252,9 +1401,13 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     {
                         uint32_t hi[32], lo[32];
 #pragma unroll
-                        for (int c = 0; c < HB; ++c) {
-                            if constexpr (SC) tf32_split_rn(s[c], hi[c], lo[c]);
-                            else tf32_split(s[c], hi[c], lo[c]);
+                        for (int c = 0; c < HB; c += 2) {
+                            if constexpr (SC) {
+                                tf32_split_rn2(s[c], s[c + 1], hi[c], hi[c + 1], lo[c], lo[c + 1]);
+                            } else {
+                                tf32_split(s[c], hi[c], lo[c]);
+                                tf32_split(s[c + 1], hi[c + 1], lo[c + 1]);
+                            }
                         }
                         tc::tmem_st32(lrow + scol, hi);
                         tc::tmem_st32(lrow + scol + BK, lo);

@@ -34,6 +34,47 @@ __device__ __forceinline__ float cap_tanh(float y) {
     return copysignf(__fdividef(num, den), y);
 }
 
+// Cap N scores of one thread, all 32 lanes of the warp together.  The
+// tensor-core prefill's softmax has little time for it and cap_tanh is some
+// twenty instructions, so scores well inside the cap -- the usual case: caps
+// are several times the scores -- take the Taylor series tanh(y) / y = 1 -
+// u / 3 + 2 u^2 / 15 - 17 u^3 / 315, u = y^2, two scores per instruction and
+// the cap's constant folded into the coefficients; for |y| <= 1/8 the first
+// term left out is below 2^-29.  (cap_in cap_out = 1, so cap_out tanh(y) = s
+// tanh(y) / y.)  One score outside sends the warp's part of the tile to
+// cap_tanh.  (Caps are 1e-6 .. 1e6: nothing here overflows.)
+struct CapSeries {
+    float c1, c2, c3;
+};
+__device__ __forceinline__ CapSeries cap_series(float cap_in) {
+    const float k = cap_in * cap_in;
+    return {k * (-1.f / 3.f), k * k * (2.f / 15.f), k * k * k * (-17.f / 315.f)};
+}
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&s)[N], const ScoreRule& r, const CapSeries& k) {
+    float t4[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains
+#pragma unroll
+    for (int c = 0; c < N; ++c) t4[c & 3] = fmaxf(t4[c & 3], fabsf(s[c]));
+    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+    if (__any_sync(0xffffffffu, top * r.cap_in > 0.125f)) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] = r.cap_out * cap_tanh(s[c] * r.cap_in);
+        return;
+    }
+    auto both = [](float x) { return make_float2(x, x); };
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 x = make_float2(s[c], s[c + 1]);
+        const float2 u = __fmul2_rn(x, x);
+        float2 t = __ffma2_rn(u, both(k.c3), both(k.c2));
+        t = __ffma2_rn(u, t, both(k.c1));
+        t = __ffma2_rn(u, t, both(1.f));
+        const float2 y = __fmul2_rn(x, t);
+        s[c] = y.x;
+        s[c + 1] = y.y;
+    }
+}
+
 // One score after cap and bias; slope2 = slope_h log2 e (0: no bias), d = p - t.
 __device__ __forceinline__ float apply_rule(float s, float cap_in, float cap_out, float slope2,
                                             bool bias, int d) {

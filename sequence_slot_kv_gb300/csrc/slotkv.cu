@@ -451,9 +451,9 @@ int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float
 // ------------------------------------------------------------ scored calls
 int check_scores(const slotkv_scores* sc, bool prefill) {
     if (!sc) return SLOTKV_OK;
-    // (the kernels divide by the cap and multiply by it: both stay normal)
-    if (!(sc->cap >= 0.f) || sc->cap > 1e30f || (sc->cap > 0.f && sc->cap < 1e-30f))
-        return fail(SLOTKV_ERR_ARG, "scores: cap=%g must be 0 or in 1e-30 .. 1e30",
+    // (the kernels use powers of the cap's reciprocal: they stay normal)
+    if (!(sc->cap >= 0.f) || sc->cap > 1e6f || (sc->cap > 0.f && sc->cap < 1e-6f))
+        return fail(SLOTKV_ERR_ARG, "scores: cap=%g must be 0 or in 1e-6 .. 1e6",
                     (double)sc->cap);
     if (((uintptr_t)sc->slopes | (uintptr_t)sc->doc_start | (uintptr_t)sc->prefix_end) & 3)
         return fail(SLOTKV_ERR_ARG, "scores: arrays must be 4-byte aligned");

@@ -71,9 +71,9 @@ def test_binding_refuses_scores():
         skv.Scores(window=1 << 32)
     sc = skv.Scores(cap=2.0, window=9)
     assert sc.cap == 2.0 and sc.window == 9
-    sc.doc_start = torch.zeros(4, dtype=torch.int32)
+    sc.doc_start, sc._arrays = torch.zeros(4, dtype=torch.int32), True
     with pytest.raises(ValueError, match="doc_start"):
-        skv._scores(sc, 3, 8)
+        skv._scores(sc, 3, 8, 0)
 
 
 def test_binding_refuses_request_arrays():
