@@ -394,8 +394,8 @@ int prefill_batch_attn_scored(slotkv_t handle, uint32_t n_tok, uint32_t n_head, 
  *                 is only read.
  *   prefix_slots  device u32[B]: the prefix handle's slot with the row's prefix.
  *   prefix_lens   device u32[B]: how many of the row's keys are there, positions
- *                 0 .. prefix_lens[b] - 1 of that slot.  0: none (a plain row;
- *                 prefix_slots[b] is then not read).
+ *                 0 .. prefix_lens[b] - 1 of that slot.  0: none (a plain row,
+ *                 whatever prefix_slots[b] holds).
  *   positions     the row's whole position p, prefix included; q' and k' are
  *                 rotated at it.  Key p goes to position p - prefix_lens[b] of
  *                 the row's own slot, which holds the keys after the prefix.

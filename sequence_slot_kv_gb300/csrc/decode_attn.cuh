@@ -1191,7 +1191,11 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
             uint32_t n_items = 0;
             auto await_plan = [&]() {
                 if (!P.no_plan) {
-                    grid_dependency_wait();
+                    // (a shared call's plan ended before the prefix pass, this
+                    // kernel's predecessor, began)
+                    bool wait = true;
+                    if constexpr (SC) wait = P.shared.lens == nullptr;
+                    if (wait) grid_dependency_wait();
                     n_items = __ldcg(P.plan);
                 }
                 planned = true;
@@ -1544,6 +1548,7 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
     const int gid = warp * (32 / L) + lane / L;  // key group
     const int li = lane % L;                     // lane within the group
     uint32_t tile_g = 0, handed = 0;
+    [[maybe_unused]] bool prefix_done = false;
     for (uint32_t k = 0;; ++k) {
         const uint32_t is = k & 1;
         if (!misc[0] && !mbar_wait(prepared0 + 8 * is, (k >> 1) & 1)) {
@@ -1659,7 +1664,8 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
         [[maybe_unused]] LaneRule<G> rule_h;
         if constexpr (SC) {
             lo = desc[is].lo;
-            if (P.shared.lens && split == 0)
+            // (before the first one is needed, the prefix pass may still run)
+            if (P.shared.lens && split == 0 && prefix_done)
                 prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
             if constexpr (C::TR) {
                 constexpr int REP = C::NV >= L ? 1 : L / C::NV;
@@ -1759,7 +1765,14 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
         auto dim = [&](int t) { return ((e0 + t) >> 2) * 4 * L + 4 * li + ((e0 + t) & 3); };
         // a shared call's prefix partials join split 0, spread over the warps
         if constexpr (SC) {
-            if (prec.z) fold_partials<HD, G, EF>(P.part, prec, P.n_head, kvh * G, warp, W, m, l, acc, dim);
+            if (P.shared.lens && split == 0) {
+                if (!prefix_done) {
+                    grid_dependency_wait();
+                    prefix_done = true;
+                    prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+                }
+                fold_partials<HD, G, EF>(P.part, prec, P.n_head, kvh * G, warp, W, m, l, acc, dim);
+            }
         }
         // ------------------------------------ chain the four warps: 0 -> 1 -> 2 -> 3
         for (int w2 = 0; w2 < W; ++w2) {
@@ -1847,6 +1860,9 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
         if (lane == 0) mbar_arrive(free0 + 8 * is);  // this warp is done with the slot
     }
 
+    // a shared call's decode ends after its prefix pass, whatever it had to do
+    if constexpr (SC)
+        if (P.shared.lens) grid_dependency_wait();
     if (misc[0]) {
         // drain this CTA's own copies that may still be in flight: the newest
         // tile of each stage and the newest staged items
@@ -1892,7 +1908,7 @@ __global__ void __launch_bounds__(128) slotkv_write_kv_kernel(const decode_param
 
 template <int HD, int G, bool SC = false>
 int launch_one(const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-               unsigned ctas, cudaStream_t stream) {
+               unsigned ctas, cudaStream_t stream, ScoredPart part = ScoredPart::whole) {
     using C = KCfg<HD, G>;
     // kernel attributes belong to each device's copy of the kernels: set them
     // once per device (bit d of the mask; devices past 63 set them every time)
@@ -1932,7 +1948,7 @@ int launch_one(const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUten
         if (per_sm < 2) return static_cast<int>(cudaErrorInvalidConfiguration);
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    if (p.prefill) {
+    if (p.prefill && part != ScoredPart::attention) {
         const uint32_t warps = p.B * p.n_kv_head;
         slotkv_write_kv_kernel<HD, SC><<<(warps + 3) / 4, 128, 0, stream>>>(p);
     }
@@ -1940,7 +1956,7 @@ int launch_one(const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUten
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    if (!p.no_plan) {
+    if (!p.no_plan && part != ScoredPart::attention) {
         // a programmatic dependent of the preceding work (see the plan kernel)
         cudaLaunchConfig_t pc = {};
         pc.gridDim = dim3(1);
@@ -1951,29 +1967,31 @@ int launch_one(const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUten
         e = cudaLaunchKernelEx(&pc, slotkv_plan_kernel<C::T, SC>, p);
         if (e != cudaSuccess) return static_cast<int>(e);
     }
+    if (part == ScoredPart::plan) return static_cast<int>(cudaGetLastError());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = p.no_plan ? 0 : 1;  // programmatic dependent of the plan kernel
+    // programmatic dependent of the plan kernel, or of a prefix pass
+    cfg.numAttrs = p.no_plan && part == ScoredPart::whole ? 0 : 1;
     e = cudaLaunchKernelEx(&cfg, slotkv_decode_attn_kernel<HD, G, SC>, tmK, tmV, p);
     return static_cast<int>(e);
 }
 
 template <int HD, bool SC = false>
 int launch_hd(int G, const decode_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-              unsigned ctas, cudaStream_t stream) {
+              unsigned ctas, cudaStream_t stream, ScoredPart part = ScoredPart::whole) {
     switch (G) {
-        case 1: return launch_one<HD, 1, SC>(p, tmK, tmV, ctas, stream);
-        case 2: return launch_one<HD, 2, SC>(p, tmK, tmV, ctas, stream);
-        case 3: return launch_one<HD, 3, SC>(p, tmK, tmV, ctas, stream);
-        case 4: return launch_one<HD, 4, SC>(p, tmK, tmV, ctas, stream);
-        case 5: return launch_one<HD, 5, SC>(p, tmK, tmV, ctas, stream);
-        case 6: return launch_one<HD, 6, SC>(p, tmK, tmV, ctas, stream);
-        case 7: return launch_one<HD, 7, SC>(p, tmK, tmV, ctas, stream);
-        case 8: return launch_one<HD, 8, SC>(p, tmK, tmV, ctas, stream);
+        case 1: return launch_one<HD, 1, SC>(p, tmK, tmV, ctas, stream, part);
+        case 2: return launch_one<HD, 2, SC>(p, tmK, tmV, ctas, stream, part);
+        case 3: return launch_one<HD, 3, SC>(p, tmK, tmV, ctas, stream, part);
+        case 4: return launch_one<HD, 4, SC>(p, tmK, tmV, ctas, stream, part);
+        case 5: return launch_one<HD, 5, SC>(p, tmK, tmV, ctas, stream, part);
+        case 6: return launch_one<HD, 6, SC>(p, tmK, tmV, ctas, stream, part);
+        case 7: return launch_one<HD, 7, SC>(p, tmK, tmV, ctas, stream, part);
+        case 8: return launch_one<HD, 8, SC>(p, tmK, tmV, ctas, stream, part);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
     if (!ok) {
         cp_async_wait<0>();  // no copy outlives the CTA
         if (tid == 0) atomicOr(P.status, kDevRange);
+        if constexpr (SC)
+            if (P.shared.lens) grid_dependency_wait();  // this grid ends after the prefix pass
         return;
     }
     // row of key t in the [rows][n_kv_head * HD] view of K and V; keys t .. t + T - 1
@@ -234,11 +236,9 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
     }
-    [[maybe_unused]] uint4 prec = make_uint4(0, 0, 0, 0);
     [[maybe_unused]] LaneRule<KC::CNT> rule_t;
     [[maybe_unused]] LaneRule<G> rule_h;
     if constexpr (SC) {
-        if (P.shared.lens) prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
         if constexpr (KC::TR) {
             constexpr int REP = KC::NV >= L ? 1 : L / KC::NV;
             rule_t = lane_rule<G, KC::CNT>(P.rule, g, li / REP * KC::CNT % KC::GP);
@@ -289,7 +289,12 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
     const int e0 = merge_warp_groups<G, E, L>(lane, m, l, acc);
     if constexpr (SC) {
         auto dim = [&](int t) { return ((e0 + t) >> 2) * 4 * L + 4 * li + ((e0 + t) & 3); };
-        if (prec.z) fold_partials<HD, G, EF>(P.part, prec, P.n_head, g * G, warp, W, m, l, acc, dim);
+        if (P.shared.lens) {
+            // everything above ran beside the prefix pass; its partials here
+            grid_dependency_wait();
+            const uint4 prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+            fold_partials<HD, G, EF>(P.part, prec, P.n_head, g * G, warp, W, m, l, acc, dim);
+        }
     }
     float* macc = reinterpret_cast<float*>(smem);
     float* mm = macc + W * G * HD;
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
 }
 
 template <int HD, int G, bool SC = false>
-int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream) {
+int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream, bool after_pass = false) {
     using C = SCfg<HD, G>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
@@ -353,21 +358,35 @@ int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream) {
         if (e != cudaSuccess) return static_cast<int>(e);
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
+    if (after_pass) {  // a programmatic dependent of a shared call's prefix pass
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(p.B * p.n_kv_head);
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return static_cast<int>(cudaLaunchKernelEx(&cfg, slotkv_decode_small_kernel<HD, G, SC>, p));
+    }
     slotkv_decode_small_kernel<HD, G, SC><<<p.B * p.n_kv_head, 128, C::SMEM, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 
 template <int HD, bool SC = false>
-int launch_small_hd(int G, const decode_params_t<SC>& p, cudaStream_t stream) {
+int launch_small_hd(int G, const decode_params_t<SC>& p, cudaStream_t stream,
+                    bool after_pass = false) {
     switch (G) {
-        case 1: return launch_small_one<HD, 1, SC>(p, stream);
-        case 2: return launch_small_one<HD, 2, SC>(p, stream);
-        case 3: return launch_small_one<HD, 3, SC>(p, stream);
-        case 4: return launch_small_one<HD, 4, SC>(p, stream);
-        case 5: return launch_small_one<HD, 5, SC>(p, stream);
-        case 6: return launch_small_one<HD, 6, SC>(p, stream);
-        case 7: return launch_small_one<HD, 7, SC>(p, stream);
-        case 8: return launch_small_one<HD, 8, SC>(p, stream);
+        case 1: return launch_small_one<HD, 1, SC>(p, stream, after_pass);
+        case 2: return launch_small_one<HD, 2, SC>(p, stream, after_pass);
+        case 3: return launch_small_one<HD, 3, SC>(p, stream, after_pass);
+        case 4: return launch_small_one<HD, 4, SC>(p, stream, after_pass);
+        case 5: return launch_small_one<HD, 5, SC>(p, stream, after_pass);
+        case 6: return launch_small_one<HD, 6, SC>(p, stream, after_pass);
+        case 7: return launch_small_one<HD, 7, SC>(p, stream, after_pass);
+        case 8: return launch_small_one<HD, 8, SC>(p, stream, after_pass);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

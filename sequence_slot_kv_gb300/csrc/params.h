@@ -129,8 +129,8 @@ struct ScoredPrefillParams : PrefillParams {
     Partials part;
     uint32_t* tile_lo = nullptr;  // workspace [n_tok]: each tile's smallest key
     uint32_t* list = nullptr;     // workspace: (split << 16 | tile) of each (tile, split)
-    uint32_t list_cap = 0;
     uint32_t sms = 0;             // SMs, for the split choice
+    uint32_t after_plan = 0;      // 1: a decode plan kernel precedes on the stream
 };
 
 template <bool SC>
@@ -194,13 +194,19 @@ int launch_prefill_tc_hd128(int G, const PrefillParams& p, const CUtensorMap& tm
 
 // The scored forms (capped scores, distance bias, masks; see score_rule.cuh)
 // of the three kinds above, and the prefix pass of a shared decode call
-// (plan, q preparation, attention into partials).
+// (plan, q preparation, attention into partials).  A shared decode call is
+// launched in two parts around its prefix pass, first the decode plan (if
+// its shape has one), then the attention, a programmatic dependent of the pass.
+enum class ScoredPart { whole, plan, attention };
 int launch_scored_hd64(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
-                       const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+                       const CUtensorMap& tmV, unsigned ctas, bool small, ScoredPart part,
+                       cudaStream_t stream);
 int launch_scored_hd128(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
-                        const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+                        const CUtensorMap& tmV, unsigned ctas, bool small, ScoredPart part,
+                       cudaStream_t stream);
 int launch_scored_hd256(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
-                        const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream);
+                        const CUtensorMap& tmV, unsigned ctas, bool small, ScoredPart part,
+                       cudaStream_t stream);
 int launch_scored_prefill_hd64(int G, const ScoredPrefillParams& p, const CUtensorMap& tmK,
                                const CUtensorMap& tmV, unsigned ctas, cudaStream_t stream);
 int launch_scored_prefill_hd128(int G, const ScoredPrefillParams& p, const CUtensorMap& tmK,
@@ -209,7 +215,7 @@ int launch_scored_prefill_hd128(int G, const ScoredPrefillParams& p, const CUten
 // (tile, split) items per SM and kv head that the scored prefill's plan may
 // make by splitting; a call with more tiles than kSplitBelow items per SM is
 // never split.
-constexpr uint32_t kSplitBelow = 2, kSplitMost = 4, kMaxSplits = 64;
+constexpr uint32_t kSplitBelow = 2, kSplitMost = 8, kMaxSplits = 64;
 // rows (tokens) of partials a call can need beyond one per row of a shared
 // call: 128 query rows per split item
 inline size_t partial_head_rows(uint32_t sms) { return (size_t)128 * kSplitMost * sms; }

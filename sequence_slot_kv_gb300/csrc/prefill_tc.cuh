@@ -225,8 +225,9 @@ __device__ __forceinline__ PrefillRow prefill_row(const ScoredPrefillParams& P, 
     r.slot = __ldg(P.slots + i);
     r.lo = rule_first(P.rule, i, r.pos);
     if (P.shared.lens) {
+        const uint32_t own = __ldg(P.own_slots + i);
         const ScoredRow x = scored_row(P.rule, P.shared, i, r.pos, P.own_ctx,
-                                       __ldg(P.own_slots + i) < P.own_n_slots, false);
+                                       own < P.own_n_slots, false);
         r.ok = x.ok;
         r.keys = x.ok && x.len != 0u && r.lo < x.len;
         r.hi = r.keys ? x.len - 1u : 0u;
@@ -252,9 +253,8 @@ __host__ __device__ inline uint32_t prep_groups(uint32_t n_head, uint32_t n_kv_h
     return prep_q_groups(n_head) + (n_kv_head + kPrepKvHeads - 1) / kPrepKvHeads;
 }
 
-template <int HD, bool SC = false>
-__global__ void __launch_bounds__(128)
-    slotkv_prefill_prep_kernel(const prefill_params_t<SC> P) {
+template <int HD, bool SC>
+__device__ __forceinline__ void prefill_prep(const prefill_params_t<SC>& P) {
     extern __shared__ __align__(16) uint8_t prep_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t qg = prep_q_groups(P.n_head);
@@ -316,145 +316,27 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+template <int HD, bool SC = false>
+__global__ void __launch_bounds__(128)
+    slotkv_prefill_prep_kernel(const prefill_params_t<SC> P) {
+    // scored calls: the attention kernel may be set up beside this one's end,
+    // and the last CTA ends after the plan, this kernel's programmatic
+    // predecessor
+    if constexpr (SC) grid_launch_dependents();
+    prefill_prep<HD, SC>(P);
+    if constexpr (SC)
+        if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+}
+
 // ------------------------------------------------------------------ plan
-// Scored calls: the splits of the tiles and the item list (split << 16 |
-// tile), whole CTA.  With enough tiles to fill the GPU twice nothing is
-// split.  Otherwise one chunk length serves every tile, so that all items
-// are about equal: of the lengths that cut the longest tile into 1 ..
-// kMaxSplits splits (at least four key tiles each), the one with the least
-// estimated time, waves of items over the SMs times key tiles per item plus
-// a fixed cost per item (its q load, its epilogue and the join of its
-// partial, about four key tiles' time).  Items are listed split by split, the
-// tiles from last to first, so CTAs that run together share a split's keys
-// in L2, and a prefill's largest tiles come first.
-constexpr uint32_t kItemCost = 4;  // key tiles
-
-template <int BK>
-__device__ __forceinline__ uint32_t tile_split_count(uint32_t lo, uint32_t hi, uint32_t chunk) {
-    const uint32_t kt = (hi - lo) / BK + 1;  // key tiles
-    return (kt + chunk - 1) / chunk;
-}
-
-template <int BK>
-__device__ void plan_splits(const ScoredPrefillParams& P, uint32_t n_tiles) {
-    __shared__ uint32_t longest, best_chunk;
-    __shared__ unsigned long long best;
-    __shared__ uint32_t scan[32], carry_items, carry_part;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
-    if (tid == 0) {
-        longest = 1;
-        best = ~0ull;
-        best_chunk = 0x7FFFFFFFu;
-        carry_items = carry_part = 0;
-    }
-    __syncthreads();
-    const bool split = static_cast<uint64_t>(n_tiles) * P.n_kv_head <
-                       static_cast<uint64_t>(kSplitBelow) * P.sms;
-    if (split) {
-        for (uint32_t t = tid; t < n_tiles; t += 1024)
-            atomicMax(&longest, (__ldcg(&tiles[t].w) - __ldcg(P.tile_lo + t)) / BK + 1);
-        __syncthreads();
-        // warp w tries w + 1 and w + 33 splits of the longest tile
-        for (uint32_t s = warp + 1; s <= kMaxSplits; s += 32) {
-            const uint32_t chunk = (longest + s - 1) / s;
-            if (s > 1 && chunk < 4) continue;
-            uint32_t items = 0;
-            for (uint32_t t = lane; t < n_tiles; t += 32)
-                items += tile_split_count<BK>(__ldcg(P.tile_lo + t), __ldcg(&tiles[t].w), chunk);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) items += __shfl_xor_sync(0xffffffffu, items, off);
-            items *= P.n_kv_head;
-            if (s > 1 && items > kSplitMost * P.sms) continue;
-            const uint64_t waves = (items + P.sms - 1) / P.sms;
-            const uint64_t cost = waves * (chunk + (s > 1 ? kItemCost : 0u));
-            // (of equal costs the longest chunk, so the fewest partials)
-            if (lane == 0) atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - chunk));
-        }
-        __syncthreads();
-        if (tid == 0) best_chunk = 0xFFFFFFFFu - static_cast<uint32_t>(best & 0xFFFFFFFFu);
-        __syncthreads();
-    }
-    const uint32_t chunk = best_chunk;
-    // items per tile and partial rows per tile, both as exclusive sums over
-    // the tiles from last to first (order of the partials is of no account)
-    for (uint32_t r0 = 0; r0 < n_tiles; r0 += 1024) {
-        const uint32_t i = r0 + tid;
-        uint32_t ns = 0, rows = 0, tile = 0, first = 0;
-        if (i < n_tiles) {
-            tile = n_tiles - 1 - i;
-            const uint4 rec = __ldcg(tiles + tile);
-            first = rec.x;
-            rows = rec.y;
-            ns = split ? tile_split_count<BK>(__ldcg(P.tile_lo + tile), rec.w, chunk) : 1u;
-        }
-        const uint32_t pr = (ns > 1 || P.shared.lens) ? ns * rows : 0u;
-        uint32_t a = pr;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, a, off);
-            if (lane >= static_cast<uint32_t>(off)) a += o;
-        }
-        if (lane == 31) scan[warp] = a;
-        __syncthreads();
-        if (warp == 0) {
-            uint32_t v = scan[lane];
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
-                if (lane >= static_cast<uint32_t>(off)) v += o;
-            }
-            scan[lane] = v;
-        }
-        __syncthreads();
-        const uint32_t base = carry_part + (warp ? scan[warp - 1] : 0u) + a - pr;
-        if (pr)
-            for (uint32_t j = 0; j < rows; ++j)
-                reinterpret_cast<uint4*>(P.part.rec)[first + j] = make_uint4(base + j, rows, ns, 0u);
-        __syncthreads();
-        if (tid == 1023) carry_part = base + pr;
-        __syncthreads();
-    }
-    // the list, split by split: tiles with more than s splits, last to first
-    const uint32_t most = split ? (longest + chunk - 1) / chunk : 1u;
-    for (uint32_t s = 0; s < most; ++s) {
-        for (uint32_t r0 = 0; r0 < n_tiles; r0 += 1024) {
-            const uint32_t i = r0 + tid;
-            bool in = false;
-            uint32_t tile = 0;
-            if (i < n_tiles) {
-                tile = n_tiles - 1 - i;
-                in = s == 0 || tile_split_count<BK>(__ldcg(P.tile_lo + tile),
-                                                    __ldcg(&tiles[tile].w), chunk) > s;
-            }
-            const uint32_t ballot = __ballot_sync(0xffffffffu, in);
-            if (lane == 0) scan[warp] = __popc(ballot);
-            __syncthreads();
-            uint32_t before = carry_items;
-            for (uint32_t w = 0; w < warp; ++w) before += scan[w];
-            const uint32_t at = before + __popc(ballot & ((1u << lane) - 1u));
-            if (in && at < P.list_cap) P.list[at] = s << 16 | tile;
-            __syncthreads();
-            if (tid == 1023) carry_items = at + (in ? 1u : 0u);
-            __syncthreads();
-        }
-    }
-    if (tid == 0) {
-        P.plan[0] = carry_items * P.n_kv_head;
-        P.plan[1] = 0;
-        P.plan[2] = chunk;
-    }
-}
-
 // One CTA of 1024 threads, tokens in rounds of 1024.  A run is a maximal
 // sequence of consecutive in-range tokens with the same slot; token i starts
 // a tile when its index within its run is a multiple of MT.  Tile records:
 // (first token, tokens, slot, largest position).  Out-of-range tokens raise
 // SLOTKV_DEV_RANGE and belong to no tile.  Then the tiles' hand-out order.
 
-template <int MT, int BK, bool SC = false>
-__global__ void __launch_bounds__(1024, 1)
-    slotkv_prefill_plan_kernel(const prefill_params_t<SC> P) {
+template <int MT>
+__global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const PrefillParams P) {
     __shared__ int warp_max[32];
     __shared__ uint32_t warp_sum[32];
     __shared__ int carry_start;
@@ -474,25 +356,7 @@ __global__ void __launch_bounds__(1024, 1)
         const uint32_t i = r0 + tid;
         bool valid = false, start = false;
         uint32_t slot = 0;
-        [[maybe_unused]] uint32_t lo = 0, hi = 0;
-        if constexpr (SC) {
-            if (i < P.n_tok) {
-                const PrefillRow r = prefill_row(P, i);
-                if (!r.ok) atomicOr(P.status, kDevRange);
-                valid = r.keys;
-                slot = r.slot;
-                hi = r.hi;
-                lo = r.lo < hi ? r.lo : hi;
-                reinterpret_cast<uint4*>(P.part.rec)[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (valid) {
-                    start = i == 0;
-                    if (i > 0) {
-                        const PrefillRow prev = prefill_row(P, i - 1);
-                        start = !prev.keys || prev.slot != slot;
-                    }
-                }
-            }
-        } else if (i < P.n_tok) {
+        if (i < P.n_tok) {
             slot = P.slots[i];
             valid = slot < P.n_slots && P.positions[i] < P.slot_ctx;
             if (!valid) atomicOr(P.status, kDevRange);
@@ -549,8 +413,6 @@ __global__ void __launch_bounds__(1024, 1)
         __syncthreads();
         const uint32_t incl = c + (warp > 0 ? warp_sum[warp - 1] : 0u) + carry_tiles;
         if (tflag) tiles[incl - 1] = make_uint4(i, 0u, slot, 0u);
-        if constexpr (SC)
-            if (tflag) P.tile_lo[incl - 1] = 0xFFFFFFFFu;
         if (i < P.n_tok) P.tile_of[i] = valid ? incl - 1 : 0xFFFFFFFFu;
         __syncthreads();  // every thread has read the carries
         if (tid == 1023) {
@@ -565,19 +427,9 @@ __global__ void __launch_bounds__(1024, 1)
         if (t == 0xFFFFFFFFu) continue;
         uint32_t* rec = P.tiles + 4 * static_cast<size_t>(t);
         atomicAdd(rec + 1, 1u);
-        if constexpr (SC) {
-            const PrefillRow r = prefill_row(P, i);
-            atomicMax(rec + 3, r.hi);
-            atomicMin(P.tile_lo + t, r.lo < r.hi ? r.lo : r.hi);
-        } else {
-            atomicMax(rec + 3, P.positions[i]);
-        }
+        atomicMax(rec + 3, P.positions[i]);
     }
     __syncthreads();
-    if constexpr (SC) {
-        plan_splits<BK>(P, carry_tiles);
-        return;
-    }
     // The hand-out order, into tile_of (its per-token use is over): the
     // tiles in reverse, so each run is handed out from its last tile (the
     // most keys, when its positions increase) to its first, one run after
@@ -591,6 +443,267 @@ __global__ void __launch_bounds__(1024, 1)
         P.plan[0] = carry_tiles * P.n_kv_head;
         P.plan[1] = 0;
     }
+}
+
+// The scored calls' plan (one CTA of 1024 threads, PER consecutive tokens per
+// thread and round: one for a call of up to 1024 rows, whose time is the
+// latency of code run once, so the least of it; else eight).  Runs and tiles as above, over the rows that
+// have keys for the tensor cores (PrefillRow); a tile's record is the same,
+// with its smallest key in tile_lo.  The first kPlanTiles tiles are kept in
+// shared memory until the end.
+//
+// With few tiles their keys are cut into splits, which fills the GPU and
+// evens its items out: one chunk length for every tile, of the lengths that
+// cut the longest tile into 1 .. kMaxSplits splits the one with the least
+// estimated time -- waves of items over the SMs, times key tiles per item plus
+// kItemCost for its q load, its epilogue and the join of its partial.  Items
+// are listed split by split, so CTAs that run together share a split's keys
+// in L2; unsplit tiles are listed last to first, as above.  The order has no
+// part in any result: a split's partial has a place of its own.
+constexpr uint32_t kPlanTiles = 512;
+constexpr uint32_t kItemCost = 2, kMinChunk = 2;  // key tiles
+
+// Inclusive scan of one value per thread over 1024 threads.
+template <typename T, typename Op>
+__device__ T block_inclusive(T v, T* warp_vals, Op op, T zero) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const T o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v = op(v, o);
+    }
+    if (lane == 31) warp_vals[warp] = v;
+    __syncthreads();
+    T w = lane < warp ? warp_vals[lane] : zero;  // the warps before this one
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) w = op(w, __shfl_xor_sync(0xffffffffu, w, off));
+    return op(v, w);
+}
+
+template <int MT, int BK, uint32_t PER>
+__global__ void __launch_bounds__(1024, 1)
+    slotkv_scored_plan_kernel(const ScoredPrefillParams P) {
+    __shared__ uint32_t t_first[kPlanTiles], t_rows[kPlanTiles], t_slot[kPlanTiles];
+    __shared__ uint32_t t_lo[kPlanTiles], t_hi[kPlanTiles], t_ns[kPlanTiles], t_part[kPlanTiles];
+    __shared__ int scan_i[32];
+    __shared__ uint32_t scan_u[32], hist[kMaxSplits + 1], at[kMaxSplits + 1];
+    __shared__ uint32_t carry_tiles, longest;
+    __shared__ int carry_start;
+    __shared__ unsigned long long best;
+    // Prep, launched next as a programmatic dependent, may start at once: it
+    // reads nothing of what this kernel writes, and its last CTA waits for
+    // this kernel, so the attention kernel after it waits for both.
+    grid_launch_dependents();
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint4* tiles = reinterpret_cast<uint4*>(P.tiles);
+    uint4* rec = reinterpret_cast<uint4*>(P.part.rec);
+    if (tid == 0) {
+        carry_tiles = 0;
+        carry_start = -1;
+        longest = 1;
+        best = ~0ull;
+    }
+    if (tid <= kMaxSplits) hist[tid] = at[tid] = 0;
+    __syncthreads();
+    auto max_op = [](int a, int b) { return a > b ? a : b; };
+    auto add_op = [](uint32_t a, uint32_t b) { return a + b; };
+    for (uint32_t r0 = 0; r0 < P.n_tok; r0 += 1024 * PER) {
+        const uint32_t i0 = r0 + tid * PER;
+        uint32_t slot[PER], lo[PER], hi[PER];
+        uint32_t keys = 0, starts = 0;  // bit j: token i0 + j
+        uint32_t last_slot = 0, last_keys = 0;  // of the thread's last token
+        uint32_t first_prev_slot = 0, first_prev = 0;
+        if (lane == 0 && i0 > 0 && i0 < P.n_tok) {
+            const PrefillRow r = prefill_row(P, i0 - 1);
+            first_prev = r.keys ? 1u : 0u;
+            first_prev_slot = r.slot;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+            slot[j] = lo[j] = hi[j] = 0;
+            if (i0 + j < P.n_tok) {
+                const PrefillRow r = prefill_row(P, i0 + j);
+                if (!r.ok) atomicOr(P.status, kDevRange);
+                keys |= (r.keys ? 1u : 0u) << j;
+                slot[j] = r.slot;
+                hi[j] = r.hi;
+                lo[j] = r.lo < r.hi ? r.lo : r.hi;
+                last_slot = r.slot;
+                last_keys = r.keys ? 1u : 0u;
+            }
+        }
+        uint32_t prev_slot = __shfl_up_sync(0xffffffffu, last_slot, 1);
+        uint32_t prev = __shfl_up_sync(0xffffffffu, last_keys, 1);
+        if (lane == 0) {
+            prev_slot = first_prev_slot;
+            prev = first_prev;
+        }
+        int last_start = -1;
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+            if (keys >> j & 1u) {
+                const bool follows = j ? (keys >> (j - 1) & 1u) && slot[j - 1] == slot[j]
+                                       : prev && prev_slot == slot[j];
+                if (!follows) {
+                    starts |= 1u << j;
+                    last_start = static_cast<int>(i0 + j);
+                }
+            }
+        }
+        // the run start before this thread's tokens, then its tile starts
+        const int incl_start = block_inclusive(last_start, scan_i, max_op, -1);
+        int before = __shfl_up_sync(0xffffffffu, incl_start, 1);
+        if (lane == 0) {
+            before = carry_start;
+            for (uint32_t w = 0; w < warp; ++w) before = max_op(before, scan_i[w]);
+        }
+        before = max_op(before, carry_start);
+        uint32_t opens = 0;
+        int run = before;
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+            if (starts >> j & 1u) run = static_cast<int>(i0 + j);
+            if ((keys >> j & 1u) && (i0 + j - static_cast<uint32_t>(run)) % MT == 0) opens |= 1u << j;
+        }
+        const uint32_t incl = block_inclusive(static_cast<uint32_t>(__popc(opens)), scan_u, add_op, 0u);
+        uint32_t t = carry_tiles + incl - __popc(opens);  // tiles opened before
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+            if (opens >> j & 1u) {
+                if (t < kPlanTiles) {
+                    t_first[t] = i0 + j;
+                    t_slot[t] = slot[j];
+                    t_rows[t] = 0;
+                    t_lo[t] = 0xFFFFFFFFu;
+                    t_hi[t] = 0;
+                } else {
+                    tiles[t] = make_uint4(i0 + j, 0u, slot[j], 0u);
+                    P.tile_lo[t] = 0xFFFFFFFFu;
+                }
+                ++t;
+            }
+        }
+        __syncthreads();
+        // each tile's rows, smallest and largest key: this thread's tokens
+        // tile by tile; when one tile takes the whole warp, once for all
+        t = carry_tiles + incl - __popc(opens);
+        uint32_t n = 0, tlo = 0xFFFFFFFFu, thi = 0;
+        auto flush = [&](uint32_t tile) {
+            if (n == 0) return;
+            uint32_t* rows = tile < kPlanTiles ? t_rows + tile : P.tiles + 4 * static_cast<size_t>(tile) + 1;
+            uint32_t* plo = tile < kPlanTiles ? t_lo + tile : P.tile_lo + tile;
+            uint32_t* phi = tile < kPlanTiles ? t_hi + tile : P.tiles + 4 * static_cast<size_t>(tile) + 3;
+            atomicAdd(rows, n);
+            atomicMin(plo, tlo);
+            atomicMax(phi, thi);
+            n = 0;
+            tlo = 0xFFFFFFFFu;
+            thi = 0;
+        };
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) {
+            if (opens >> j & 1u) {
+                flush(t - 1);
+                ++t;
+            }
+            const bool in = keys >> j & 1u;
+            if (in) {
+                ++n;
+                tlo = tlo < lo[j] ? tlo : lo[j];
+                thi = thi > hi[j] ? thi : hi[j];
+            }
+            if (i0 + j < P.n_tok) P.tile_of[i0 + j] = in ? t - 1 : 0xFFFFFFFFu;
+        }
+        const uint32_t t_of_0 = __shfl_sync(0xffffffffu, t, 0);  // (every lane takes part)
+        const bool one = __all_sync(0xffffffffu, n != 0 && t == t_of_0);
+        if (one) {
+            n = __reduce_add_sync(0xffffffffu, n);
+            tlo = __reduce_min_sync(0xffffffffu, tlo);
+            thi = __reduce_max_sync(0xffffffffu, thi);
+            if (lane != 0) n = 0;
+        }
+        flush(t - 1);
+        __syncthreads();  // every thread has read the carries
+        if (tid == 1023) {
+            carry_tiles += incl;
+            carry_start = max_op(incl_start, before);
+        }
+        __syncthreads();
+    }
+    const uint32_t n_tiles = carry_tiles;
+    const uint32_t kept = n_tiles < kPlanTiles ? n_tiles : kPlanTiles;
+    const bool split = n_tiles <= kPlanTiles && static_cast<uint64_t>(n_tiles) * P.n_kv_head <
+                                                    static_cast<uint64_t>(kSplitBelow) * P.sms;
+    uint32_t ktiles = 0, rows = 0;  // of tile tid
+    if (tid < kept) {
+        rows = t_rows[tid];
+        tiles[tid] = make_uint4(t_first[tid], rows, t_slot[tid], t_hi[tid]);
+        P.tile_lo[tid] = t_lo[tid];
+        ktiles = (t_hi[tid] - t_lo[tid]) / BK + 1;
+        if (split) t_part[tid] = ktiles;
+    }
+    uint32_t chunk = 0x7FFFFFFFu;
+    if (split) {
+        const uint32_t wmax = __reduce_max_sync(0xffffffffu, ktiles);
+        if (lane == 0) atomicMax(&longest, wmax);
+        __syncthreads();
+        // warp w tries w + 1 and w + 33 splits of the longest tile; of equal
+        // costs the longest chunk, so the fewest partials
+        for (uint32_t s = warp + 1; s <= kMaxSplits; s += 32) {
+            const uint32_t c = (longest + s - 1) / s;
+            if (s > 1 && c < kMinChunk) continue;
+            uint32_t items = 0;
+            for (uint32_t t = lane; t < n_tiles; t += 32) items += (t_part[t] + c - 1) / c;
+            items = __reduce_add_sync(0xffffffffu, items) * P.n_kv_head;
+            if (s > 1 && items > kSplitMost * P.sms) continue;
+            const uint64_t waves = (items + P.sms - 1) / P.sms;
+            const uint64_t cost = waves * (c + kItemCost + (s > 1 ? 1u : 0u));
+            if (lane == 0) atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - c));
+        }
+        __syncthreads();
+        chunk = 0xFFFFFFFFu - static_cast<uint32_t>(best & 0xFFFFFFFFu);
+        const uint32_t ns = tid < n_tiles ? (ktiles + chunk - 1) / chunk : 0u;
+        const uint32_t mine = ns > 1 || P.shared.lens ? ns * rows : 0u;  // partial rows
+        const uint32_t base = block_inclusive(mine, scan_u, add_op, 0u) - mine;
+        if (tid < n_tiles) {
+            t_ns[tid] = mine ? ns : 0u;
+            t_part[tid] = base;
+            atomicAdd(&hist[ns], 1u);
+        }
+        __syncthreads();
+        // split s begins in the list after the tiles with more than s' splits
+        // of every s' < s
+        if (tid == 0) {
+            uint32_t left = n_tiles, sum = 0;
+            for (uint32_t s = 0; s < kMaxSplits && left; ++s) {
+                left -= hist[s];  // (hist[0] is 0)
+                at[s] = sum;
+                sum += left;
+            }
+            at[kMaxSplits] = sum;
+        }
+        __syncthreads();
+        for (uint32_t s = 0; s < ns; ++s) P.list[atomicAdd(&at[s], 1u)] = s << 16 | tid;
+        for (uint32_t i = tid; i < P.n_tok; i += 1024) {
+            const uint32_t t = P.tile_of[i];
+            rec[i] = t == 0xFFFFFFFFu || t_ns[t] == 0
+                         ? make_uint4(0u, 0u, 0u, 0u)
+                         : make_uint4(t_part[t] + (i - t_first[t]), t_rows[t], t_ns[t], 0u);
+        }
+    } else {
+        for (uint32_t t = tid; t < n_tiles; t += 1024) P.list[t] = n_tiles - 1 - t;
+        // a shared call's unsplit rows have one partial each
+        for (uint32_t i = tid; i < P.n_tok; i += 1024)
+            rec[i] = make_uint4(i, 0u, P.shared.lens && P.tile_of[i] != 0xFFFFFFFFu ? 1u : 0u, 0u);
+    }
+    if (tid == 0) {
+        P.plan[0] = (split ? at[kMaxSplits] : n_tiles) * P.n_kv_head;
+        P.plan[1] = 0;
+        P.plan[2] = chunk;
+    }
+    // a shared call's decode plan runs before this kernel, which may have
+    // started beside it: this kernel ends after it
+    grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ attention
@@ -649,6 +762,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = *tslot;
+    // (scored calls: set up beside the kernels before it)
+    if constexpr (SC) grid_dependency_wait();
     auto timeout = [&]() {
         atomicOr(P.status, kDevTimeout);
         misc[0] = 1;
@@ -677,6 +792,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     volatile uint32_t* d = desc + 8 * is;
                     const uint32_t it = atomicAdd(P.plan + 1, 1u);
                     if (it >= n_items) {
+                        // nothing left for this CTA: what follows may be launched
+                        if constexpr (SC) grid_launch_dependents();
                         d[6] = 1;
                         mbar_arrive(IFULL + 8 * is);
                         // tell the converters: an end marker in the next slot
@@ -1628,33 +1745,52 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
     // both.  Prep starts only once the plan runs, hence after the previous
     // call's attention kernel has finished reading the rows and q workspace
     // that prep overwrites.
-    slotkv_prefill_plan_kernel<C::MT, C::BK, SC><<<1, 1024, 0, stream>>>(p);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((warps + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = prep_smem_bytes<HD>();
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD, SC>, p);
-    if (e != cudaSuccess) return static_cast<int>(e);
-    slotkv_prefill_tc_kernel<HD, G, SC>
-        <<<ctas, SC ? C::THREADS_SC : C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
+    cudaError_t e;
     if constexpr (SC) {
+        // Scored calls: a chain of programmatic dependents.  In a shared call
+        // the decode plan comes first, and this plan runs beside it (it has
+        // waited for the work before the call); otherwise this plan starts
+        // the chain in stream order.
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(1024);
+        cfg.numAttrs = p.after_plan ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1>
+                                                     : slotkv_scored_plan_kernel<C::MT, C::BK, 8>, p);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        cfg.numAttrs = 1;
+    } else {
+        slotkv_prefill_plan_kernel<C::MT><<<1, 1024, 0, stream>>>(p);
+    }
+    cfg.gridDim = dim3((warps + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = prep_smem_bytes<HD>();
+    e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD, SC>, p);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if constexpr (SC) {
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(C::THREADS_SC);
+        cfg.dynamicSmemBytes = C::SMEM;
+        e = cudaLaunchKernelEx(&cfg, slotkv_prefill_tc_kernel<HD, G, SC>, tmK, tmV, p);
+        if (e != cudaSuccess) return static_cast<int>(e);
         // a prefill that the plan may split: join the splits (at least
         // ceil(n_tok / MT) tiles; the plan splits below kSplitBelow items per SM)
         if (!p.shared.lens && static_cast<uint64_t>((p.n_tok + C::MT - 1) / C::MT) * p.n_kv_head <
                                   static_cast<uint64_t>(kSplitBelow) * p.sms) {
-            e = cudaGetLastError();
-            if (e != cudaSuccess) return static_cast<int>(e);
             cfg.gridDim = dim3((p.n_tok * p.n_head + 3) / 4);
+            cfg.blockDim = dim3(128);
             cfg.dynamicSmemBytes = 0;
             e = cudaLaunchKernelEx(&cfg, slotkv_combine_kernel<HD>, p);
             if (e != cudaSuccess) return static_cast<int>(e);
         }
+    } else {
+        slotkv_prefill_tc_kernel<HD, G, SC><<<ctas, C::THREADS, C::SMEM, stream>>>(tmK, tmV, p);
     }
     return static_cast<int>(cudaGetLastError());
 }

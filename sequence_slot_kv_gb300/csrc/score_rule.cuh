@@ -105,21 +105,18 @@ struct ScoredRow {
 __device__ __forceinline__ ScoredRow scored_row(const ScoreRule& rule, const SharedRows& sh,
                                                 uint32_t b, uint32_t pos, uint64_t cap,
                                                 bool slot_ok, bool prefill) {
-    ScoredRow r;
-    r.len = sh.lens ? __ldg(sh.lens + b) : 0u;
-    r.ok = slot_ok && pos >= r.len;
-    if (sh.lens && r.len)
-        r.ok = r.ok && r.len <= sh.slot_ctx && __ldg(sh.slots + b) < sh.n_slots;
-    r.p = r.ok ? pos - r.len : 0u;
-    r.ok = r.ok && static_cast<uint64_t>(r.p) < cap;
+    // (every load first: they are in flight together)
+    const uint32_t len = sh.lens ? __ldg(sh.lens + b) : 0u;
+    const uint32_t pslot = sh.lens ? __ldg(sh.slots + b) : 0u;
     const uint32_t first = rule_first(rule, b, pos);
-    r.lo = first > r.len ? first - r.len : 0u;
-    r.hi = r.p;
-    if (prefill && rule.prefix_end) {
-        const uint32_t e = __ldg(rule.prefix_end + b);
-        if (e > cap) r.ok = false;
-        if (e > r.p + 1u) r.hi = e - 1u;
-    }
+    const uint32_t end = prefill && rule.prefix_end ? __ldg(rule.prefix_end + b) : 0u;
+    ScoredRow r;
+    r.len = len;
+    r.ok = slot_ok && pos >= len && (len == 0u || (len <= sh.slot_ctx && pslot < sh.n_slots));
+    r.p = r.ok ? pos - len : 0u;
+    r.ok = r.ok && static_cast<uint64_t>(r.p) < cap && static_cast<uint64_t>(end) <= cap;
+    r.lo = first > len ? first - len : 0u;
+    r.hi = end > r.p + 1u ? end - 1u : r.p;
     return r;
 }
 

@@ -8,9 +8,11 @@
 namespace slotkv {
 
 int launch_scored_hd128(int G, const ScoredDecodeParams& p, const CUtensorMap& tmK,
-                       const CUtensorMap& tmV, unsigned ctas, bool small, cudaStream_t stream) {
-    return small ? launch_small_hd<128, true>(G, p, stream)
-                 : launch_hd<128, true>(G, p, tmK, tmV, ctas, stream);
+                       const CUtensorMap& tmV, unsigned ctas, bool small, ScoredPart part,
+                       cudaStream_t stream) {
+    if (!small) return launch_hd<128, true>(G, p, tmK, tmV, ctas, stream, part);
+    if (part == ScoredPart::plan) return 0;  // one kernel, no plan
+    return launch_small_hd<128, true>(G, p, stream, part == ScoredPart::attention);
 }
 
 }  // namespace slotkv

@@ -523,7 +523,6 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     P.tile_of = h->sc_idx + 8 * R;
     P.tile_lo = h->sc_idx + 9 * R;
     P.list = h->sc_idx + 10 * R;
-    P.list_cap = (uint32_t)list;
     P.plan = P.list + list;
     P.sms = sm_total(h);
     // acc first: its rows are read and written 16 bytes at a time
@@ -532,33 +531,32 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     return SLOTKV_OK;
 }
 
-int launch_scored(slotkv_s* h, const slotkv_scores* sc, const slotkv::SharedRows& shared,
-                  const slotkv::Partials& part, uint32_t B, uint32_t n_head, const float* q,
-                  const float* k_new, const float* v_new, const uint32_t* positions,
-                  const uint32_t* slots, const float* q_norm_w, const float* k_norm_w,
-                  const float* inv_freq, const float* sinks, float* out, float eps, float scale,
-                  cudaStream_t stream, bool prefill, const uint32_t* block_tables,
-                  uint32_t bt_stride) {
-    slotkv::ScoredDecodeParams P;
+// A scored decode call's parameters and shape.
+CallShape fill_scored(slotkv_s* h, slotkv::ScoredDecodeParams& P, const slotkv_scores* sc,
+                      uint32_t B, uint32_t n_head, const float* q, const float* k_new,
+                      const float* v_new, const uint32_t* positions, const uint32_t* slots,
+                      const float* q_norm_w, const float* k_norm_w, const float* inv_freq,
+                      const float* sinks, float* out, float eps, float scale, bool prefill,
+                      const uint32_t* block_tables, uint32_t bt_stride) {
     P.rule = score_rule(sc);
-    P.shared = shared;
-    P.part = part;
     uint64_t max_keys = block_tables ? (uint64_t)bt_stride * h->slot_ctx : h->slot_ctx;
     // a window bounds a row's keys, from its first key's tile on
     const uint64_t T = (uint64_t)slotkv::tile_keys((int)h->head_dim);
     if (P.rule.window && !P.rule.prefix_end)
         max_keys = std::min<uint64_t>(max_keys, P.rule.window + T - 1);
-    const CallShape cs =
-        fill_params(h, P, B, n_head, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
-                    inv_freq, sinks, out, eps, scale, prefill, block_tables, bt_stride, max_keys);
-    const int G = (int)(n_head / h->n_kv_head);
+    return fill_params(h, P, B, n_head, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
+                       inv_freq, sinks, out, eps, scale, prefill, block_tables, bt_stride,
+                       max_keys);
+}
+
+int launch_scored(slotkv_s* h, const slotkv::ScoredDecodeParams& P, const CallShape& cs,
+                  slotkv::ScoredPart part, cudaStream_t stream) {
+    const int G = (int)(P.n_head / P.n_kv_head);
     const bool small = cs.small != 0;
-    int rc;
-    switch (h->head_dim) {
-        case 64: rc = slotkv::launch_scored_hd64(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
-        case 128: rc = slotkv::launch_scored_hd128(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
-        default: rc = slotkv::launch_scored_hd256(G, P, h->tmK, h->tmV, cs.ctas, small, stream); break;
-    }
+    auto run = h->head_dim == 64    ? slotkv::launch_scored_hd64
+               : h->head_dim == 128 ? slotkv::launch_scored_hd128
+                                    : slotkv::launch_scored_hd256;
+    const int rc = run(G, P, h->tmK, h->tmV, cs.ctas, small, part, stream);
     if (rc != 0) return cuda_fail((cudaError_t)rc, "scored decode kernel launch");
     return SLOTKV_OK;
 }
@@ -1195,9 +1193,11 @@ int decode_batch_attn_scored(slotkv_t h, uint32_t B, uint32_t n_head, const floa
                                k_norm_w, inv_freq, out);
     if (rc == SLOTKV_OK) rc = check_scores(scores, false);
     if (rc != SLOTKV_OK || B == 0) return rc;
-    return launch_scored(h, scores, {}, {}, B, n_head, q, k_new, v_new, positions, slots,
-                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale,
-                         (cudaStream_t)stream, false, nullptr, 0);
+    slotkv::ScoredDecodeParams P;
+    const CallShape cs =
+        fill_scored(h, P, scores, B, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                    k_norm_w, inv_freq, sinks, out, eps, scale, false, nullptr, 0);
+    return launch_scored(h, P, cs, slotkv::ScoredPart::whole, (cudaStream_t)stream);
 }
 
 int decode_batch_attn_paged_scored(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
@@ -1218,9 +1218,11 @@ int decode_batch_attn_paged_scored(slotkv_t h, uint32_t B, uint32_t n_head, cons
                     h->slot_ctx, T);
     if (bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
     if (B == 0) return SLOTKV_OK;
-    return launch_scored(h, scores, {}, {}, B, n_head, q, k_new, v_new, positions, nullptr,
-                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale,
-                         (cudaStream_t)stream, false, block_tables, bt_stride);
+    slotkv::ScoredDecodeParams P;
+    const CallShape cs =
+        fill_scored(h, P, scores, B, n_head, q, k_new, v_new, positions, nullptr, q_norm_w,
+                    k_norm_w, inv_freq, sinks, out, eps, scale, false, block_tables, bt_stride);
+    return launch_scored(h, P, cs, slotkv::ScoredPart::whole, (cudaStream_t)stream);
 }
 
 int prefill_batch_attn_scored(slotkv_t h, uint32_t n_tok, uint32_t n_head, const float* q,
@@ -1235,10 +1237,13 @@ int prefill_batch_attn_scored(slotkv_t h, uint32_t n_tok, uint32_t n_head, const
     if (rc == SLOTKV_OK) rc = check_scores(scores, true);
     if (rc != SLOTKV_OK || n_tok == 0) return rc;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (!h->tc_prefill)  // head dim 256: the decode kernel in prefill mode
-        return launch_scored(h, scores, {}, {}, n_tok, n_head, q, k_new, v_new, positions, slots,
-                             q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale, s, true,
-                             nullptr, 0);
+    if (!h->tc_prefill) {  // head dim 256: the decode kernel in prefill mode
+        slotkv::ScoredDecodeParams D;
+        const CallShape cs =
+            fill_scored(h, D, scores, n_tok, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                        k_norm_w, inv_freq, sinks, out, eps, scale, true, nullptr, 0);
+        return launch_scored(h, D, cs, slotkv::ScoredPart::whole, s);
+    }
     slotkv::ScoredPrefillParams P;
     rc = scored_workspace(h, false, P, s);
     if (rc != SLOTKV_OK) return rc;
@@ -1303,6 +1308,16 @@ int decode_batch_attn_shared(slotkv_t h, uint32_t B, uint32_t n_head, const floa
     shared.lens = prefix_lens;
     shared.n_slots = prefix->n_slots;
     shared.slot_ctx = prefix->slot_ctx;
+    // the decode step's plan, the prefix pass, the step itself
+    slotkv::ScoredDecodeParams D;
+    const CallShape cs =
+        fill_scored(h, D, scores, B, n_head, q, k_new, v_new, positions, slots, q_norm_w,
+                    k_norm_w, inv_freq, sinks, out, eps, scale, false, nullptr, 0);
+    D.shared = shared;
+    D.part = P.part;
+    rc = launch_scored(h, D, cs, slotkv::ScoredPart::plan, s);
+    if (rc != SLOTKV_OK) return rc;
+    P.after_plan = cs.no_plan ? 0u : 1u;
     // the prefix pass: the rows' queries against their prefixes' slots
     P.q = q;
     P.k_new = P.v_new = nullptr;  // the decode kernel writes k' and v
@@ -1331,9 +1346,7 @@ int decode_batch_attn_shared(slotkv_t h, uint32_t B, uint32_t n_head, const floa
     P.own_ctx = h->slot_ctx;
     rc = launch_scored_prefill(h, P, prefix->tmKs, prefix->tmVs, s);
     if (rc != SLOTKV_OK) return rc;
-    return launch_scored(h, scores, shared, P.part, B, n_head, q, k_new, v_new, positions, slots,
-                         q_norm_w, k_norm_w, inv_freq, sinks, out, eps, scale, s, false, nullptr,
-                         0);
+    return launch_scored(h, D, cs, slotkv::ScoredPart::attention, s);
 }
 
 int slot_kv_token_map(slotkv_t h, uint32_t n_req, const uint32_t* slots, const uint32_t* past,
