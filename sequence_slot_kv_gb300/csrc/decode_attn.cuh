@@ -1666,7 +1666,7 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
             lo = desc[is].lo;
             // (before the first one is needed, the prefix pass may still run)
             if (P.shared.lens && split == 0 && prefix_done)
-                prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+                prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + 2 * static_cast<size_t>(b));
             if constexpr (C::TR) {
                 constexpr int REP = C::NV >= L ? 1 : L / C::NV;
                 rule_t = lane_rule<G, C::CNT>(P.rule, kvh, li / REP * C::CNT % C::GP);
@@ -1769,7 +1769,7 @@ __global__ void __launch_bounds__(KCfg<HD, G>::THREADS, 2)
                 if (!prefix_done) {
                     grid_dependency_wait();
                     prefix_done = true;
-                    prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + b);
+                    prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + 2 * static_cast<size_t>(b));
                 }
                 fold_partials<HD, G, EF>(P.part, prec, P.n_head, kvh * G, warp, W, m, l, acc, dim);
             }

@@ -106,10 +106,11 @@ struct SharedRows {
 
 // What the prefix pass of a shared call leaves for the decode kernel, and the
 // splits of a scored prefill for its combine kernel.  rec[b] = (first partial
-// row, stride, splits, 0): split s of row b, head h, is partial
+// row, stride, splits, 0), then the row's position and the first and last key
+// it attends, for the attention kernel: split s of row b, head h, is partial
 // (rec.x + s * rec.y) * n_head + h, (m, l) and an unnormalised accumulator.
 struct Partials {
-    uint32_t* rec = nullptr;  // [rows][4]
+    uint32_t* rec = nullptr;  // [rows][8]
     float* ml = nullptr;      // [partials][2]
     float* acc = nullptr;     // [partials][hd]
 };

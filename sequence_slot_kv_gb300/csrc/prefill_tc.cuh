@@ -147,7 +147,10 @@ struct PCfg {
     static constexpr int OFF_XCH = OFF_MISC + 64;
     static constexpr int SMEM_USED = OFF_XCH + 2 * 6 * M * 4;
     static constexpr int SMEM = SMEM_USED + 1024;   // slack to align the ring to 1 KiB
-    static_assert(SMEM <= 227 * 1024, "shared memory");
+    // scored calls: 2 KB for each softmax warp to stage rows in
+    static constexpr int OFF_STAGE = (SMEM_USED + 15) / 16 * 16;
+    static constexpr int SMEM_SC = OFF_STAGE + NSW * 2048 + 1024;
+    static_assert(SMEM <= 227 * 1024 && SMEM_SC <= 227 * 1024, "shared memory");
     static_assert(BLK % 1024 == 0 && SLOT % 1024 == 0, "128-byte swizzle atoms stay 1 KiB aligned");
     static constexpr uint32_t IDESC_QK = tc::idesc_tf32(M, BK, false);
     static constexpr uint32_t IDESC_PV = tc::idesc_tf32(M, HD, false);
@@ -176,15 +179,9 @@ __device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) 
     lo = __float_as_uint(x - __uint_as_float(h));
 }
 
-// The same with the high part rounded to nearest, so the remainder is at most
-// half a TF32 step and takes either sign.
-__device__ __forceinline__ void tf32_split_rn(float x, uint32_t& hi, uint32_t& lo) {
-    const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
-    hi = h;
-    lo = __float_as_uint(x - __uint_as_float(h));
-}
-
-// Two at a time (one packed subtraction).
+// The same for two values, with the high parts rounded to nearest, so a
+// remainder is at most half a TF32 step and takes either sign (one packed
+// subtraction).
 __device__ __forceinline__ void tf32_split_rn2(float x, float y, uint32_t& hx, uint32_t& hy,
                                                uint32_t& lx, uint32_t& ly) {
     hx = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
@@ -525,6 +522,7 @@ __global__ void __launch_bounds__(1024, 1)
                 const PrefillRow r = prefill_row(P, i0 + j);
                 if (!r.ok) atomicOr(P.status, kDevRange);
                 keys |= (r.keys ? 1u : 0u) << j;
+                rec[2 * (i0 + j) + 1] = make_uint4(r.pos, r.lo, r.hi, 0u);
                 slot[j] = r.slot;
                 hi[j] = r.hi;
                 lo[j] = r.lo < r.hi ? r.lo : r.hi;
@@ -686,15 +684,15 @@ __global__ void __launch_bounds__(1024, 1)
         for (uint32_t s = 0; s < ns; ++s) P.list[atomicAdd(&at[s], 1u)] = s << 16 | tid;
         for (uint32_t i = tid; i < P.n_tok; i += 1024) {
             const uint32_t t = P.tile_of[i];
-            rec[i] = t == 0xFFFFFFFFu || t_ns[t] == 0
-                         ? make_uint4(0u, 0u, 0u, 0u)
-                         : make_uint4(t_part[t] + (i - t_first[t]), t_rows[t], t_ns[t], 0u);
+            rec[2 * i] = t == 0xFFFFFFFFu || t_ns[t] == 0
+                             ? make_uint4(0u, 0u, 0u, 0u)
+                             : make_uint4(t_part[t] + (i - t_first[t]), t_rows[t], t_ns[t], 0u);
         }
     } else {
         for (uint32_t t = tid; t < n_tiles; t += 1024) P.list[t] = n_tiles - 1 - t;
         // a shared call's unsplit rows have one partial each
         for (uint32_t i = tid; i < P.n_tok; i += 1024)
-            rec[i] = make_uint4(i, 0u, P.shared.lens && P.tile_of[i] != 0xFFFFFFFFu ? 1u : 0u, 0u);
+            rec[2 * i] = make_uint4(i, 0u, P.shared.lens && P.tile_of[i] != 0xFFFFFFFFu ? 1u : 0u, 0u);
     }
     if (tid == 0) {
         P.plan[0] = (split ? at[kMaxSplits] : n_tiles) * P.n_kv_head;
@@ -1268,25 +1266,74 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
             bool valid;
             uint32_t tok, pos, head;
             uint32_t lo, hi;  // scored calls: the row's keys (none: lo > hi)
+            uint4 part;       // and its partials' record
         };
         auto row_of = [&](const uint32_t (&d)[ND]) {
             ItemRow w;
             w.valid = r < static_cast<uint32_t>(C::ROWS) && t_local < d[1];
             w.tok = d[0] + t_local;
-            w.pos = w.valid ? __ldg(P.positions + w.tok) : 0u;
             w.head = d[2] * G + h_local;
             if constexpr (SC) {
-                w.lo = 1;
-                w.hi = 0;
-                if (w.valid) {
-                    const PrefillRow x = prefill_row(P, w.tok);
-                    w.lo = x.lo;
-                    w.hi = x.hi;
-                }
+                const uint4* r8 = reinterpret_cast<const uint4*>(P.part.rec) + 2 * w.tok;
+                const uint4 x = w.valid ? __ldcg(r8 + 1) : make_uint4(0u, 1u, 0u, 0u);
+                w.part = w.valid ? __ldcg(r8) : make_uint4(0u, 0u, 0u, 0u);
+                w.pos = x.x;
+                w.lo = x.y;
+                w.hi = x.z;
+            } else {
+                w.pos = w.valid ? __ldg(P.positions + w.tok) : 0u;
             }
             return w;
         };
         // this half of the item's q rows into tensor memory, split hi / lo
+        // Scored calls stage q and out rows through 2 KB of shared memory per
+        // warp, 32 rows x 16 columns at a time, rows of 64 bytes with their
+        // four chunks rotated: lanes then move whole 64-byte pieces of rows
+        // to and from memory, four lanes a row.  (A thread reading or writing
+        // its own row touches 32 lines per instruction, which cost 7 us of q
+        // and 3 of out per item.)
+        [[maybe_unused]] float4* stage = reinterpret_cast<float4*>(smem + C::OFF_STAGE) + warp * 128;
+        [[maybe_unused]] auto stage_at = [&](int row, int chunk) { return row * 4 + ((chunk + (row >> 1)) & 3); };
+        [[maybe_unused]] auto load_q_staged = [&](const uint32_t (&d)[ND]) {
+            const int sub = lane >> 2, ch = lane & 3;  // row of eight, chunk
+            const float* src[4];                       // rows sub, sub + 8, ..
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t rr = static_cast<uint32_t>(quarter * 32 + i * 8 + sub);
+                const bool in = rr < static_cast<uint32_t>(C::ROWS) && rr / G < d[1];
+                src[i] = in ? P.q_rot + (static_cast<size_t>(d[0] + rr / G) * P.n_head + d[2] * G + rr % G) * HD +
+                                  hf * HH + ch * 4
+                            : nullptr;
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < HH; c0 += 32) {
+                float4 x[8];  // 32 columns in flight
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = src[j & 3] ? __ldcg(reinterpret_cast<const float4*>(src[j & 3] + c0 + (j >> 2) * 16))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) stage[stage_at(i * 8 + sub, ch)] = x[p * 4 + i];
+                    __syncwarp();
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 y = stage[stage_at(lane, c)];
+                        tf32_split_rn2(y.x, y.y, hi[4 * c], hi[4 * c + 1], lo[4 * c], lo[4 * c + 1]);
+                        tf32_split_rn2(y.z, y.w, hi[4 * c + 2], hi[4 * c + 3], lo[4 * c + 2], lo[4 * c + 3]);
+                    }
+                    tc::tmem_st16(lrow + C::C_QHI + hf * HH + c0 + p * 16, hi);
+                    tc::tmem_st16(lrow + C::C_QLO + hf * HH + c0 + p * 16, lo);
+                }
+            }
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(QREADY);
+        };
         auto load_q = [&](const ItemRow& w) {
             const float* qrow = P.q_rot + (static_cast<size_t>(w.valid ? w.tok : 0) * P.n_head + w.head) * HD;
 #pragma unroll
@@ -1296,17 +1343,10 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 for (int c = 0; c < 32; c += 4) {
                     const float4 x = w.valid ? __ldcg(reinterpret_cast<const float4*>(qrow + c0 + c))
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-                    if constexpr (SC) {
-                        tf32_split_rn(x.x, hi[c + 0], lo[c + 0]);
-                        tf32_split_rn(x.y, hi[c + 1], lo[c + 1]);
-                        tf32_split_rn(x.z, hi[c + 2], lo[c + 2]);
-                        tf32_split_rn(x.w, hi[c + 3], lo[c + 3]);
-                    } else {
-                        tf32_split(x.x, hi[c + 0], lo[c + 0]);
-                        tf32_split(x.y, hi[c + 1], lo[c + 1]);
-                        tf32_split(x.z, hi[c + 2], lo[c + 2]);
-                        tf32_split(x.w, hi[c + 3], lo[c + 3]);
-                    }
+                    tf32_split(x.x, hi[c + 0], lo[c + 0]);
+                    tf32_split(x.y, hi[c + 1], lo[c + 1]);
+                    tf32_split(x.z, hi[c + 2], lo[c + 2]);
+                    tf32_split(x.w, hi[c + 3], lo[c + 3]);
                 }
                 tc::tmem_st32(lrow + C::C_QHI + c0, hi);
                 tc::tmem_st32(lrow + C::C_QLO + c0, lo);
@@ -1352,7 +1392,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
         uint32_t d[ND];
         if (open_item(0, false, d) && !d[4]) {
             ItemRow cur = row_of(d);
-            load_q(cur);
+            if constexpr (SC) load_q_staged(d);
+            else load_q(cur);
             for (uint32_t k = 0;; ++k) {
                 const uint32_t ntiles = d[3];
                 [[maybe_unused]] uint32_t k_begin = 0, split = 0;
@@ -1547,7 +1588,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 ItemRow nxt{};
                 if (!last) {
                     nxt = row_of(d);
-                    load_q(nxt);
+                    if constexpr (SC) load_q_staged(d);
+                    else load_q(nxt);
                 }
                 // This item's last O += P V (global tile g - 1; its commit
                 // covers every earlier MMA), then out = O / l (both halves'
@@ -1571,7 +1613,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 bool direct = true;  // the row's output, not a split's partial
                 if constexpr (SC) {
                     if (cur.valid) {
-                        const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + cur.tok);
+                        const uint4 rec = cur.part;
                         if (rec.z != 0u) {
                             direct = false;
                             f = 1.f;
@@ -1593,43 +1635,61 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     const float c = exp2f(m - M2);
                     f = c / (lt * c + exp2f(sk - M2));
                 }
-                [[maybe_unused]] const bool rescan = SC && misc[8] != 0;
+                if constexpr (SC) {
+                    // the values the tensor core took as 0, for the keys of
+                    // this item that the row attends
+                    if (misc[8] != 0 && cur.valid) {
+                        const uint32_t slot = __ldg(P.slots + cur.tok);
+                        const uint32_t k_end = k_begin + ntiles * BK;  // past the item's keys
+                        for (uint32_t key = cur.lo > k_begin ? cur.lo : k_begin;
+                             key <= cur.hi && key < k_end; ++key) {
+                            const float* vr = P.V + ((static_cast<size_t>(slot) * P.slot_ctx + key) *
+                                                         P.n_kv_head + cur.head / G) * HD + hf * HH;
 #pragma unroll
-                for (int c0 = hf * HH; c0 < (hf + 1) * HH; c0 += 32) {
-                    uint32_t v[32];
-                    if constexpr (SC) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            v[c] = __float_as_uint(acc[(c0 - hf * HH) + c]);
-                    } else {
-                        tc::tmem_ld32(lrow + C::C_O + c0, v);
-                        tc::tmem_ld_wait();
-                    }
-                    if constexpr (SC) {
-                        // the values the tensor core took as 0, for the keys
-                        // of this item that the row attends
-                        if (rescan && cur.valid) {
-                            const uint32_t slot = __ldg(P.slots + cur.tok);
-                            const uint32_t k_end = k_begin + ntiles * BK;  // past the item's keys
-                            for (uint32_t key = cur.lo > k_begin ? cur.lo : k_begin;
-                                 key <= cur.hi && key < k_end; ++key) {
-                                const float* vr = P.V + ((static_cast<size_t>(slot) * P.slot_ctx + key) *
-                                                             P.n_kv_head + cur.head / G) * HD + c0;
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) {
-                                    const float x = vr[c];
-                                    if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u)
-                                        v[c] = __float_as_uint(__uint_as_float(v[c]) + x);
-                                }
+                            for (int c = 0; c < HH; ++c) {
+                                const float x = vr[c];
+                                if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) acc[c] += x;
                             }
                         }
                     }
-                    if (cur.valid) {
+                    // rows to memory by way of the stage; each lane has the
+                    // destinations of the four rows it writes pieces of
+                    const int sub = lane >> 2, ch = lane & 3;
+                    const uint64_t mine = cur.valid ? reinterpret_cast<uint64_t>(orow) : 0ull;
+                    float* dst[4];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4*>(orow + c0 + c) =
-                                make_float4(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f,
-                                            __uint_as_float(v[c + 2]) * f, __uint_as_float(v[c + 3]) * f);
+                    for (int i = 0; i < 4; ++i) {
+                        dst[i] = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, mine, i * 8 + sub));
+                        if (dst[i]) dst[i] += hf * HH + ch * 4;
+                    }
+#pragma unroll
+                    for (int c0 = 0; c0 < HH; c0 += 16) {
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            stage[stage_at(lane, c)] =
+                                make_float4(acc[c0 + 4 * c] * f, acc[c0 + 4 * c + 1] * f,
+                                            acc[c0 + 4 * c + 2] * f, acc[c0 + 4 * c + 3] * f);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 y = stage[stage_at(i * 8 + sub, ch)];
+                            if (dst[i]) *reinterpret_cast<float4*>(dst[i] + c0) = y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c0 = hf * HH; c0 < (hf + 1) * HH; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(lrow + C::C_O + c0, v);
+                        tc::tmem_ld_wait();
+                        if (cur.valid) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4)
+                                *reinterpret_cast<float4*>(orow + c0 + c) =
+                                    make_float4(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f,
+                                                __uint_as_float(v[c + 2]) * f, __uint_as_float(v[c + 3]) * f);
+                        }
                     }
                 }
                 tc::fence_before_sync();
@@ -1654,7 +1714,7 @@ __global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefill
     grid_dependency_wait();
     const uint32_t tok = wg / P.n_head, head = wg % P.n_head;
     if (tok >= P.n_tok) return;
-    const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + tok);
+    const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + 2 * tok);
     if (rec.z == 0u) return;
     const size_t at0 = static_cast<size_t>(rec.x) * P.n_head + head;
     const size_t step = static_cast<size_t>(rec.y) * P.n_head;
@@ -1724,7 +1784,8 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (!(configured.load(std::memory_order_acquire) & bit) || bit == 0) {
         cudaError_t e = cudaFuncSetAttribute(slotkv_prefill_tc_kernel<HD, G, SC>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             SC ? C::SMEM_SC : C::SMEM);
         if (e != cudaSuccess) return static_cast<int>(e);
         if constexpr (SC) {
             // the register hand-over assumes 128 registers a thread; with
@@ -1776,7 +1837,7 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
     if constexpr (SC) {
         cfg.gridDim = dim3(ctas);
         cfg.blockDim = dim3(C::THREADS_SC);
-        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.dynamicSmemBytes = C::SMEM_SC;
         e = cudaLaunchKernelEx(&cfg, slotkv_prefill_tc_kernel<HD, G, SC>, tmK, tmV, p);
         if (e != cudaSuccess) return static_cast<int>(e);
         // a prefill that the plan may split: join the splits (at least

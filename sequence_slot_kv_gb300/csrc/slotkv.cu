@@ -511,7 +511,7 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     const size_t pr = partial_rows(h, shared);
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, stream, "scored workspace (q)");
     if (rc == SLOTKV_OK)
-        rc = first_use(reinterpret_cast<float**>(&h->sc_idx), 10 * R + list + 4, stream,
+        rc = first_use(reinterpret_cast<float**>(&h->sc_idx), 14 * R + list + 4, stream,
                        "scored workspace (items)");
     if (rc == SLOTKV_OK)
         rc = first_use(&h->sc_part[shared ? 1 : 0], pr * (2 + h->head_dim), stream,
@@ -519,10 +519,10 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     if (rc != SLOTKV_OK) return rc;
     P.q_rot = h->sc_q;
     P.part.rec = h->sc_idx;
-    P.tiles = h->sc_idx + 4 * R;
-    P.tile_of = h->sc_idx + 8 * R;
-    P.tile_lo = h->sc_idx + 9 * R;
-    P.list = h->sc_idx + 10 * R;
+    P.tiles = h->sc_idx + 8 * R;
+    P.tile_of = h->sc_idx + 12 * R;
+    P.tile_lo = h->sc_idx + 13 * R;
+    P.list = h->sc_idx + 14 * R;
     P.plan = P.list + list;
     P.sms = sm_total(h);
     // acc first: its rows are read and written 16 bytes at a time
