@@ -199,6 +199,24 @@ def _stream_ptr(stream):
     return stream.cuda_stream
 
 
+_call = None  # the compiled calls: None not looked for yet, False not built
+
+
+def _compiled():
+    """The module of the compiled calls (csrc/call.cpp), which check a call's
+    tensors and make it in one go; False if it is not built.  A call it
+    declines (returning None) goes through the checks here, for their message."""
+    global _call
+    if _call is None:
+        import torch  # noqa: F401 -- its libraries first
+        try:
+            from . import _slotkv_call
+            _call = _slotkv_call
+        except ImportError:
+            _call = False
+    return _call
+
+
 class _Unlike(Exception):
     """An argument is not what the fast path takes; the slow path says why."""
 
@@ -264,6 +282,18 @@ def _int_addr(t, dev, what):
     return t.data_ptr()
 
 
+def _stream_arg(stream):
+    """A stream argument for the compiled calls: an address, or None for torch's."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
+def _done(rc, name):
+    """Whether a compiled call was made (None: declined); raises for its status."""
+    if rc:
+        _check(rc, name)
+    return rc is not None
+
+
 def _raw_stream(stream, dev):
     if stream is None:
         import torch
@@ -286,6 +316,7 @@ class Scores:
                            _ptr(doc_start, torch.int32, "doc_start"),
                            _ptr(prefix_end, torch.int32, "prefix_end"))
         self._ref = ctypes.byref(self._c)
+        self._args = (float(cap), int(window), slopes, doc_start, prefix_end)
 
     @property
     def cap(self):
@@ -480,6 +511,12 @@ class SlotKV:
 
     def _slot_step_scored(self, name, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
                           inv_freq, sinks, scores, out, eps, scale, stream):
+        c = _compiled()
+        if c and _done(getattr(c, name)(
+                self._h.value, self.n_kv_head, self.head_dim, q, k_new, v_new, positions, slots,
+                q_norm_w, k_norm_w, inv_freq, sinks, None if scores is None else scores._args, out,
+                eps, scale, _stream_arg(stream)), name):
+            return out
         (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
             self, q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w, inv_freq, sinks)
         _check(getattr(_lib, name)(self._h, B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn,
@@ -491,13 +528,19 @@ class SlotKV:
                                        k_norm_w, inv_freq, sinks, scores, out, eps, scale,
                                        stream=None):
         """As decode_batch_attn_paged, with a score rule (Scores, or None)."""
+        c, name = _compiled(), "decode_batch_attn_paged_scored"
+        if c and _done(c.decode_batch_attn_paged_scored(
+                self._h.value, self.n_kv_head, self.head_dim, q, k_new, v_new, positions,
+                block_tables, q_norm_w, k_norm_w, inv_freq, sinks,
+                None if scores is None else scores._args, out, eps, scale, _stream_arg(stream)),
+                name):
+            return out
         (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
             self, q, k_new, v_new, positions, block_tables, out, q_norm_w, k_norm_w, inv_freq,
             sinks, "block_tables")
         _check(_lib.decode_batch_attn_paged_scored(
             self._h, B, n_head, aq, ak, av, ap, ai, int(block_tables.shape[1]), aqw, akw, af, asn,
-            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)),
-            "decode_batch_attn_paged_scored")
+            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)), name)
         return out
 
     def decode_batch_attn_shared(self, q, k_new, v_new, positions, slots, prefix, prefix_slots,
@@ -508,6 +551,13 @@ class SlotKV:
         ``prefix``, the later ones in its own slot from position 0 on."""
         if not isinstance(prefix, SlotKV):
             raise TypeError("prefix must be a SlotKV")
+        c, name = _compiled(), "decode_batch_attn_shared"
+        if c and _done(c.decode_batch_attn_shared(
+                self._h.value, self.n_kv_head, self.head_dim, q, k_new, v_new, positions, slots,
+                prefix._h.value, prefix_slots, prefix_lens, q_norm_w, k_norm_w, inv_freq, sinks,
+                None if scores is None else scores._args, out, eps, scale, _stream_arg(stream)),
+                name):
+            return out
         for name, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
             if t is None or t.dim() != 1 or t.shape != positions.shape:
                 raise ValueError(f"{name} must be [B]")
@@ -517,13 +567,17 @@ class SlotKV:
             self._h, B, n_head, aq, ak, av, ap, ai, prefix._h,
             _int_addr(prefix_slots, dev, "prefix_slots"),
             _int_addr(prefix_lens, dev, "prefix_lens"), aqw, akw, af, asn,
-            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)),
-            "decode_batch_attn_shared")
+            _scores(scores, B, n_head, dev), ao, eps, scale, _raw_stream(stream, dev)), name)
         return out
 
     def token_map(self, slots, past, fresh, starts, tok_slots, tok_positions, stream=None):
         """slot_kv_token_map: the slots and positions of a prefill's tokens from
         the requests' (slot, cached length, new length), int32 CUDA tensors."""
+        c = _compiled()
+        if c and _done(c.slot_kv_token_map(self._h.value, slots, past, fresh, starts, tok_slots,
+                                           tok_positions, _stream_arg(stream)),
+                       "slot_kv_token_map"):
+            return starts, tok_slots, tok_positions
         import torch
         n, n_tok = slots.numel(), tok_slots.numel()
         if not (slots.shape == past.shape == fresh.shape == (n,) and starts.shape == (n + 1,) and
@@ -547,10 +601,15 @@ class SlotKV:
         """slot_kv_extend_tables: block_tables (int32 [requests][max_blocks], in
         place) extended from the free list; head_out None advances ``head``
         itself.  int32 CUDA tensors."""
-        import torch
-        n = past.numel()
         if head_out is None:
             head_out = head
+        c = _compiled()
+        if c and _done(c.slot_kv_extend_tables(self._h.value, past, fresh, block_tables,
+                                               free_blocks, head, head_out, _stream_arg(stream)),
+                       "slot_kv_extend_tables"):
+            return block_tables, head_out
+        import torch
+        n = past.numel()
         if block_tables.dim() != 2 or block_tables.shape[0] != n:
             raise ValueError("block_tables must be [requests][max_blocks]")
         if free_blocks.dim() != 1:

@@ -4,14 +4,17 @@ The translation units compile in parallel (one per head dim for the decode
 and the tensor-core prefill kernels and their scored forms, the request-length
 kernels, the host side, the allocation-free entry point), then link into ``sequence_slot_kv_gb300/libslotkv.so``.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libslotkv.so")
+CALL = os.path.join(HERE, "_slotkv_call.so")  # the compiled calls of the Python binding
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["slotkv.cu", "decode_attn_hd64.cu", "decode_attn_hd128.cu", "decode_attn_hd256.cu",
            "noalloc.cu", "prefill_tc_hd64.cu", "prefill_tc_hd128.cu", "scored_decode_hd64.cu",
@@ -34,6 +37,27 @@ def _stale(out, srcs):
     return any(os.path.getmtime(s) > t for s in srcs)
 
 
+def _call_flags():
+    """Compile and link flags of the compiled calls, from the installed torch
+    (found without importing it) and Python; None where their headers are
+    missing, and the binding then makes the calls through ctypes alone."""
+    spec = importlib.util.find_spec("torch")
+    inc = sysconfig.get_paths()["include"]
+    if spec is None or not os.path.exists(os.path.join(inc, "Python.h")):
+        return None
+    root = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(root, "include", "torch", "csrc", "autograd",
+                                       "python_variable.h")):
+        return None
+    lib = os.path.join(root, "lib")
+    cflags = ["-O2", "-std=c++17", "-fPIC", "-I", inc, "-I", os.path.join(root, "include"),
+              "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              "-I", os.path.join(_cuda_home(), "include")]
+    ldflags = ["-L" + HERE, "-lslotkv", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib]
+    return cflags, ldflags
+
+
 def build(force=False, verbose_ptxas=False):
     os.makedirs(OBJDIR, exist_ok=True)
     header = os.path.join(INCLUDE, "slotkv.h")
@@ -49,6 +73,14 @@ def build(force=False, verbose_ptxas=False):
                 cmd += ["-Xptxas", "-v"]
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT, text=True)))
+    flags = _call_flags()
+    call_src, call_obj = os.path.join(CSRC, "call.cpp"), os.path.join(OBJDIR, "call.o")
+    if flags is None:
+        print("no headers of Python or torch: the compiled calls are not built")
+    elif force or _stale(call_obj, [call_src, header]):
+        procs.append(("call.cpp", subprocess.Popen(
+            ["g++"] + flags[0] + ["-c", call_src, "-o", call_obj], stdout=subprocess.PIPE,
+            stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -57,12 +89,14 @@ def build(force=False, verbose_ptxas=False):
         if pr.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     if force or _stale(LIB, objs):
         cuda_lib = os.path.join(_cuda_home(), "lib64")
         cmd = ["nvcc", "-shared", "-o", LIB] + objs + ARCH + [
             "-cudart", "shared", "-Xlinker", "-rpath=" + cuda_lib]
         subprocess.run(cmd, check=True)
+    if flags is not None and (force or _stale(CALL, [call_obj, LIB])):
+        subprocess.run(["g++", "-shared", "-o", CALL, call_obj] + flags[1], check=True)
     return LIB
 
 

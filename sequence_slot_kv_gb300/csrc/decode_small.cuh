@@ -87,6 +87,15 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
     using KC = KCfg<HD, G>;
     constexpr int T = C::T, W = C::W, E = KC::E, L = KC::L;
     constexpr float kLog2e = 1.4426950408889634f;
+    if constexpr (SC) {
+        // launched as a programmatic dependent, and lets its own launch: the
+        // set-up of back-to-back small calls overlaps (a shared call's waits
+        // for its prefix pass below)
+        if (!P.shared.lens) {
+            grid_dependency_wait();
+            grid_launch_dependents();
+        }
+    }
     extern __shared__ __align__(1024) uint8_t smem[];
     float* kc = reinterpret_cast<float*>(smem);                // [2][T][HD]
     float* vc = reinterpret_cast<float*>(smem + C::OFF_V);     // [2][T][HD]
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
 }
 
 template <int HD, int G, bool SC = false>
-int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream, bool after_pass = false) {
+int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream) {
     using C = SCfg<HD, G>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
@@ -358,7 +367,7 @@ int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream, bool aft
         if (e != cudaSuccess) return static_cast<int>(e);
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    if (after_pass) {  // a programmatic dependent of a shared call's prefix pass
+    if constexpr (SC) {  // a programmatic dependent
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -370,23 +379,23 @@ int launch_small_one(const decode_params_t<SC>& p, cudaStream_t stream, bool aft
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         return static_cast<int>(cudaLaunchKernelEx(&cfg, slotkv_decode_small_kernel<HD, G, SC>, p));
+    } else {
+        slotkv_decode_small_kernel<HD, G, SC><<<p.B * p.n_kv_head, 128, C::SMEM, stream>>>(p);
     }
-    slotkv_decode_small_kernel<HD, G, SC><<<p.B * p.n_kv_head, 128, C::SMEM, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }
 
 template <int HD, bool SC = false>
-int launch_small_hd(int G, const decode_params_t<SC>& p, cudaStream_t stream,
-                    bool after_pass = false) {
+int launch_small_hd(int G, const decode_params_t<SC>& p, cudaStream_t stream) {
     switch (G) {
-        case 1: return launch_small_one<HD, 1, SC>(p, stream, after_pass);
-        case 2: return launch_small_one<HD, 2, SC>(p, stream, after_pass);
-        case 3: return launch_small_one<HD, 3, SC>(p, stream, after_pass);
-        case 4: return launch_small_one<HD, 4, SC>(p, stream, after_pass);
-        case 5: return launch_small_one<HD, 5, SC>(p, stream, after_pass);
-        case 6: return launch_small_one<HD, 6, SC>(p, stream, after_pass);
-        case 7: return launch_small_one<HD, 7, SC>(p, stream, after_pass);
-        case 8: return launch_small_one<HD, 8, SC>(p, stream, after_pass);
+        case 1: return launch_small_one<HD, 1, SC>(p, stream);
+        case 2: return launch_small_one<HD, 2, SC>(p, stream);
+        case 3: return launch_small_one<HD, 3, SC>(p, stream);
+        case 4: return launch_small_one<HD, 4, SC>(p, stream);
+        case 5: return launch_small_one<HD, 5, SC>(p, stream);
+        case 6: return launch_small_one<HD, 6, SC>(p, stream);
+        case 7: return launch_small_one<HD, 7, SC>(p, stream);
+        case 8: return launch_small_one<HD, 8, SC>(p, stream);
         default: return static_cast<int>(cudaErrorInvalidValue);
     }
 }

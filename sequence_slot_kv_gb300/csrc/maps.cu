@@ -139,11 +139,15 @@ __device__ __forceinline__ bool blocks_needed(const ExtendTablesParams& P, uint3
                                               uint32_t& have, uint32_t& need) {
     const uint32_t past = __ldg(P.past + r), fresh = __ldg(P.fresh + r);
     const uint64_t len = static_cast<uint64_t>(past) + fresh;
-    have = past / P.block + (past % P.block ? 1u : 0u);
+    // blocks of n keys, rounded up (the divisions are most of the kernel's
+    // instructions, so a power of two shifts)
+    auto blocks = [&](uint32_t n) {
+        return n ? (P.shift < 32u ? (n - 1u) >> P.shift : (n - 1u) / P.block) + 1u : 0u;
+    };
+    have = blocks(past);
     need = 0;
     if (len > 0xFFFFFFFFull) return false;
-    const uint32_t want = static_cast<uint32_t>(len) / P.block +
-                          (static_cast<uint32_t>(len) % P.block ? 1u : 0u);
+    const uint32_t want = blocks(static_cast<uint32_t>(len));
     if (want > P.bt_stride) return false;
     need = want - have;
     return true;
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kMapThreads)
     my_part(P.R, r0, r1);
     if (threadIdx.x == 0) used = 0;
     uint64_t sum = 0, total;
-#pragma unroll 8
+#pragma unroll 4
     for (uint32_t r = r0; r < r1; ++r) {
         uint32_t have, need;
         blocks_needed(P, r, have, need);
@@ -245,7 +249,8 @@ int launch_extend_tables(const ExtendTablesParams& p, uint32_t sms, cudaStream_t
     const uint64_t room = static_cast<uint64_t>(p.R) * p.bt_stride;
     const uint64_t most = room < p.n_free ? room : p.n_free;
     const uint64_t tiles = most ? (most - 1) / kMapTile + 1 : 1;
-    const uint64_t ctas = tiles < sms ? tiles : sms;
+    // (four CTAs of 512 threads fit on an SM)
+    const uint64_t ctas = tiles < 4ull * sms ? tiles : 4ull * sms;
     slotkv_extend_tables_kernel<<<static_cast<unsigned>(ctas), kMapThreads, 0, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
 }

@@ -28,6 +28,7 @@ struct ExtendTablesParams {
     uint32_t* scratch;            // handle-owned: [0] CTAs done (0 between calls), [1] new head
     uint32_t* status;
     uint32_t R, bt_stride, block, n_free;
+    uint32_t shift;               // log2(block), or 32 where block is no power of two
 };
 
 // Enqueue one kernel each; return a cudaError_t value.

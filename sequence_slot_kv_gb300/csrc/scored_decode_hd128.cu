@@ -12,7 +12,7 @@ int launch_scored_hd128(int G, const ScoredDecodeParams& p, const CUtensorMap& t
                        cudaStream_t stream) {
     if (!small) return launch_hd<128, true>(G, p, tmK, tmV, ctas, stream, part);
     if (part == ScoredPart::plan) return 0;  // one kernel, no plan
-    return launch_small_hd<128, true>(G, p, stream, part == ScoredPart::attention);
+    return launch_small_hd<128, true>(G, p, stream);
 }
 
 }  // namespace slotkv

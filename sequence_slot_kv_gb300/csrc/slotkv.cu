@@ -1389,7 +1389,9 @@ int slot_kv_extend_tables(slotkv_t h, uint32_t n_req, const uint32_t* past,
         return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
     const slotkv::ExtendTablesParams P{past,     fresh,          block_tables, free_blocks, head,
                                        head_out, h->map_scratch, h->status,    n_req,       bt_stride,
-                                       h->slot_ctx, n_free};
+                                       h->slot_ctx, n_free,
+                                       (h->slot_ctx & (h->slot_ctx - 1)) == 0
+                                           ? (uint32_t)__builtin_ctz(h->slot_ctx) : 32u};
     const int rc = slotkv::launch_extend_tables(P, sm_total(h), (cudaStream_t)stream);
     if (rc != 0) return cuda_fail((cudaError_t)rc, "block table kernel launch");
     return SLOTKV_OK;

@@ -440,3 +440,58 @@ def test_captured_calls_replay(hd):
     s.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
     L.kv.free()
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_both_ways_a_call_is_made(compiled, monkeypatch):
+    """The compiled calls and the ctypes ones take the same arguments and give
+    the same results; wrong arguments get the same errors from both."""
+    assert skv._compiled(), "the compiled calls are not built"
+    if not compiled:
+        monkeypatch.setattr(skv, "_call", False)
+    L = Layer(4, 128, 2, 2, 64, 6, seed=31, sinks=True, slopes=True)
+    pos, slots, doc = [5, 90, 127], [3, 0, 1], [0, 80, 3]
+    q = L.step(3)
+    sc = Scores(7.0, 60, L.slopes, i32(doc))
+    s = torch.cuda.Stream()
+    for stream in (None, s, s.cuda_stream):
+        K64, V64, outs, tols = want_rows(L, *q, pos, list(zip(slots, pos)),
+                                         lambda b, t: (slots[b], t), False, 7.0, 60, doc)
+        out = torch.full((3, 4, 64), math.nan, device="cuda")
+        torch.cuda.synchronize()
+        L.kv.decode_batch_attn_scored(*q, i32(pos), i32(slots), *L.params(), sc, out, EPS,
+                                      L.scale, stream)
+        torch.cuda.synchronize()
+        check(out, outs, tols, "decode")
+    bad = [(ValueError, dict(out=out[:2])), (TypeError, dict(out=out.double())),
+           (ValueError, dict(out=out.transpose(1, 2))), (ValueError, dict(out=out.cpu())),
+           (ValueError, dict(scores=Scores(doc_start=i32(doc + [0])))),
+           (ValueError, dict(scores=Scores(slopes=L.slopes[:2]))),
+           (skv.SlotKVError, dict(scores=Scores(cap=-1.0))),
+           (skv.SlotKVError, dict(scores=Scores(cap=math.nan))),
+           (skv.SlotKVError, dict(scores=Scores(cap=1e9))),
+           (skv.SlotKVError, dict(scores=Scores(prefix_end=i32(doc)))),
+           (ValueError, dict(q=None))]
+    good = dict(q=q[0], k_new=q[1], v_new=q[2], positions=i32(pos), slots=i32(slots),
+                q_norm_w=L.qw, k_norm_w=L.kw, inv_freq=L.inv, sinks=L.sinks, scores=sc, out=out,
+                eps=EPS, scale=L.scale)
+    for err, change in bad:
+        with pytest.raises(err):
+            L.kv.decode_batch_attn_scored(**{**good, **change})
+    with pytest.raises(ValueError, match="block_tables"):
+        L.kv.decode_batch_attn_paged_scored(
+            **{k: v for k, v in good.items() if k != "slots"}, block_tables=i32(slots))
+    with pytest.raises(skv.SlotKVError, match="kv heads"):
+        other = SlotKV(1, 128, 1, 64, 1, 2)
+        L.kv.decode_batch_attn_shared(**good, prefix=other, prefix_slots=i32([0] * 3),
+                                      prefix_lens=i32([0] * 3))
+    wide = Layer(1, 64, 1, 1, 256, 1)
+    one = wide.step(1)
+    with pytest.raises(skv.SlotKVError, match="head_dim"):
+        wide.kv.decode_batch_attn_shared(*one, i32([0]), i32([0]), wide.kv, i32([0]), i32([0]),
+                                         *wide.params(), None, torch.empty(1, 1, 256, device="cuda"),
+                                         EPS, 1.0)
+    for h in (L.kv, wide.kv):
+        h.free()
+    with pytest.raises(skv.SlotKVError, match="not allocated"):
+        L.kv.decode_batch_attn_scored(**good)
