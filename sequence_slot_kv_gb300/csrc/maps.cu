@@ -12,7 +12,10 @@
 // to tens of thousands of requests costs less than another kernel or a wait
 // for other CTAs would -- and the threads whose part reaches into the tile
 // mark, in shared memory, the unit at which each request starts.  A running
-// maximum over the marks then tells every unit its request.
+// maximum over the marks then tells every unit its request.  Both
+// kernels are launched as programmatic dependents, wait for what precedes
+// them before anything else, and let their own dependents launch: the set-up
+// of one call overlaps the call before it.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -25,6 +28,11 @@ constexpr uint32_t kRange = 1u;  // SLOTKV_DEV_RANGE
 constexpr int kMapThreads = 512;
 constexpr int kMapWarps = kMapThreads / 32;
 constexpr uint32_t kMapTile = 2 * kMapThreads;  // units per tile
+
+__device__ __forceinline__ void begin_dependent() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Exclusive prefix sum of one value per thread over the CTA; total: its sum.
 __device__ uint64_t block_exclusive(uint64_t v, uint64_t* warp_sums, uint64_t& total) {
@@ -85,6 +93,7 @@ __global__ void __launch_bounds__(kMapThreads) slotkv_token_map_kernel(const Tok
     __shared__ uint64_t sums[kMapWarps];
     __shared__ uint32_t warp_max[kMapWarps];
     __shared__ uint32_t mark[kMapTile], slot_at[kMapTile], pos_at[kMapTile];
+    begin_dependent();
     const uint64_t t0 = static_cast<uint64_t>(blockIdx.x) * kMapTile;
     mark[threadIdx.x] = mark[threadIdx.x + kMapThreads] = 0;
     uint32_t r0, r1;
@@ -163,6 +172,7 @@ __global__ void __launch_bounds__(kMapThreads)
     __shared__ uint32_t mark[kMapTile];
     __shared__ uint64_t entry_at[kMapTile];  // table entry of the marked unit
     __shared__ uint32_t used;
+    begin_dependent();
     const uint32_t head = __ldcg(P.head);
     const uint64_t avail = head < P.n_free ? P.n_free - head : 0u;
     uint32_t r0, r1;
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kMapThreads)
         }
         if (last) atomicMax(&used, last);
         __syncthreads();
-        if (threadIdx.x == 0) P.scratch[1] = head + used;
+        if (threadIdx.x == 0 && gridDim.x > 1) P.scratch[1] = head + used;
     }
     const uint64_t end = total < avail ? total : avail;
     for (uint64_t t0 = static_cast<uint64_t>(blockIdx.x) * kMapTile; t0 < end;
@@ -226,7 +236,9 @@ __global__ void __launch_bounds__(kMapThreads)
         __syncthreads();  // the marks are free again
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && gridDim.x == 1) {
+        *P.head_out = head + used;
+    } else if (threadIdx.x == 0) {
         __threadfence();
         if (atomicAdd(P.scratch, 1u) == gridDim.x - 1) {
             __threadfence();
@@ -238,10 +250,24 @@ __global__ void __launch_bounds__(kMapThreads)
 
 }  // namespace
 
+template <typename P>
+static int launch_dependent(void (*kernel)(const P), unsigned ctas, const P& p,
+                            cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kMapThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
 int launch_token_map(const TokenMapParams& p, cudaStream_t stream) {
     const uint32_t tiles = p.n_tok ? (p.n_tok - 1) / kMapTile + 1 : 1;
-    slotkv_token_map_kernel<<<tiles, kMapThreads, 0, stream>>>(p);
-    return static_cast<int>(cudaGetLastError());
+    return launch_dependent(slotkv_token_map_kernel, tiles, p, stream);
 }
 
 int launch_extend_tables(const ExtendTablesParams& p, uint32_t sms, cudaStream_t stream) {
@@ -251,8 +277,7 @@ int launch_extend_tables(const ExtendTablesParams& p, uint32_t sms, cudaStream_t
     const uint64_t tiles = most ? (most - 1) / kMapTile + 1 : 1;
     // (four CTAs of 512 threads fit on an SM)
     const uint64_t ctas = tiles < 4ull * sms ? tiles : 4ull * sms;
-    slotkv_extend_tables_kernel<<<static_cast<unsigned>(ctas), kMapThreads, 0, stream>>>(p);
-    return static_cast<int>(cudaGetLastError());
+    return launch_dependent(slotkv_extend_tables_kernel, static_cast<unsigned>(ctas), p, stream);
 }
 
 }  // namespace slotkv
