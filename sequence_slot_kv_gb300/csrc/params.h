@@ -129,8 +129,11 @@ struct ScoredPrefillParams : PrefillParams {
     uint32_t own_n_slots = 0, own_ctx = 0;
     Partials part;
     uint32_t* tile_lo = nullptr;  // workspace [n_tok]: each tile's smallest key
-    uint32_t* list = nullptr;     // workspace: (split << 16 | tile) of each (tile, split)
-    uint32_t sms = 0;             // SMs, for the split choice
+    // workspace [n_tok + splits][8], an entry per (tile, split): first token,
+    // tokens, row of the first key in the [rows][kv_dim] view, first key; keys,
+    // split, 0, 0
+    uint32_t* list = nullptr;
+    uint32_t sms = 0;             // SMs (= the attention kernel's CTAs)
     uint32_t after_plan = 0;      // 1: a decode plan kernel precedes on the stream
 };
 

@@ -442,9 +442,10 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
     }
 }
 
-// The scored calls' plan (one CTA of 1024 threads, PER consecutive tokens per
-// thread and round: one for a call of up to 1024 rows, whose time is the
-// latency of code run once, so the least of it; else eight).  Runs and tiles as above, over the rows that
+// The scored calls' plan (one CTA of NT threads, PER consecutive tokens per
+// thread and round: 256 threads and one token for a call of up to 256 rows,
+// 1024 and one up to 1024 -- the time of such a call is the latency of code run
+// once, so the least of it and few warps to wait for -- else 1024 and eight).  Runs and tiles as above, over the rows that
 // have keys for the tensor cores (PrefillRow); a tile's record is the same,
 // with its smallest key in tile_lo.  The first kPlanTiles tiles are kept in
 // shared memory until the end.
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
 constexpr uint32_t kPlanTiles = 512;
 constexpr uint32_t kItemCost = 2, kMinChunk = 2;  // key tiles
 
-// Inclusive scan of one value per thread over 1024 threads.
+// Inclusive scan of one value per thread over the CTA.
 template <typename T, typename Op>
 __device__ T block_inclusive(T v, T* warp_vals, Op op, T zero) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -477,8 +478,8 @@ __device__ T block_inclusive(T v, T* warp_vals, Op op, T zero) {
     return op(v, w);
 }
 
-template <int MT, int BK, uint32_t PER>
-__global__ void __launch_bounds__(1024, 1)
+template <int MT, int BK, uint32_t NT, uint32_t PER>
+__global__ void __launch_bounds__(NT, 1)
     slotkv_scored_plan_kernel(const ScoredPrefillParams P) {
     __shared__ uint32_t t_first[kPlanTiles], t_rows[kPlanTiles], t_slot[kPlanTiles];
     __shared__ uint32_t t_lo[kPlanTiles], t_hi[kPlanTiles], t_ns[kPlanTiles], t_part[kPlanTiles];
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(1024, 1)
     __syncthreads();
     auto max_op = [](int a, int b) { return a > b ? a : b; };
     auto add_op = [](uint32_t a, uint32_t b) { return a + b; };
-    for (uint32_t r0 = 0; r0 < P.n_tok; r0 += 1024 * PER) {
+    for (uint32_t r0 = 0; r0 < P.n_tok; r0 += NT * PER) {
         const uint32_t i0 = r0 + tid * PER;
         uint32_t slot[PER], lo[PER], hi[PER];
         uint32_t keys = 0, starts = 0;  // bit j: token i0 + j
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(1024, 1)
         }
         flush(t - 1);
         __syncthreads();  // every thread has read the carries
-        if (tid == 1023) {
+        if (tid == NT - 1) {
             carry_tiles += incl;
             carry_start = max_op(incl_start, before);
         }
@@ -635,19 +636,27 @@ __global__ void __launch_bounds__(1024, 1)
     uint32_t ktiles = 0, rows = 0;  // of tile tid
     if (tid < kept) {
         rows = t_rows[tid];
-        tiles[tid] = make_uint4(t_first[tid], rows, t_slot[tid], t_hi[tid]);
-        P.tile_lo[tid] = t_lo[tid];
         ktiles = (t_hi[tid] - t_lo[tid]) / BK + 1;
         if (split) t_part[tid] = ktiles;
     }
     uint32_t chunk = 0x7FFFFFFFu;
+    // split s of a tile with keys lo .. hi, as list entry e
+    auto put = [&](uint32_t e, uint32_t first, uint32_t n, uint32_t slot, uint32_t lo, uint32_t hi,
+                   uint32_t s) {
+        const uint32_t begin = lo + (s ? s * chunk * BK : 0u);
+        uint32_t keys = hi - begin + 1;
+        if (keys / BK >= chunk) keys = chunk * BK;
+        uint4* d = reinterpret_cast<uint4*>(P.list) + 2 * static_cast<size_t>(e);
+        d[0] = make_uint4(first, n, slot * P.slot_ctx + begin, begin);
+        d[1] = make_uint4(keys, s, 0u, 0u);
+    };
     if (split) {
         const uint32_t wmax = __reduce_max_sync(0xffffffffu, ktiles);
         if (lane == 0) atomicMax(&longest, wmax);
         __syncthreads();
-        // warp w tries w + 1 and w + 33 splits of the longest tile; of equal
+        // the warps try 1 .. kMaxSplits splits of the longest tile; of equal
         // costs the longest chunk, so the fewest partials
-        for (uint32_t s = warp + 1; s <= kMaxSplits; s += 32) {
+        for (uint32_t s = warp + 1; s <= kMaxSplits; s += NT / 32) {
             const uint32_t c = (longest + s - 1) / s;
             if (s > 1 && c < kMinChunk) continue;
             uint32_t items = 0;
@@ -681,23 +690,27 @@ __global__ void __launch_bounds__(1024, 1)
             at[kMaxSplits] = sum;
         }
         __syncthreads();
-        for (uint32_t s = 0; s < ns; ++s) P.list[atomicAdd(&at[s], 1u)] = s << 16 | tid;
-        for (uint32_t i = tid; i < P.n_tok; i += 1024) {
+        for (uint32_t s = 0; s < ns; ++s)
+            put(atomicAdd(&at[s], 1u), t_first[tid], rows, t_slot[tid], t_lo[tid], t_hi[tid], s);
+        for (uint32_t i = tid; i < P.n_tok; i += NT) {
             const uint32_t t = P.tile_of[i];
             rec[2 * i] = t == 0xFFFFFFFFu || t_ns[t] == 0
                              ? make_uint4(0u, 0u, 0u, 0u)
                              : make_uint4(t_part[t] + (i - t_first[t]), t_rows[t], t_ns[t], 0u);
         }
     } else {
-        for (uint32_t t = tid; t < n_tiles; t += 1024) P.list[t] = n_tiles - 1 - t;
+        for (uint32_t t = tid; t < n_tiles; t += NT) {
+            const bool near = t < kPlanTiles;
+            const uint4 x = near ? make_uint4(t_first[t], t_rows[t], t_slot[t], t_hi[t]) : __ldcg(tiles + t);
+            put(n_tiles - 1 - t, x.x, x.y, x.z, near ? t_lo[t] : __ldcg(P.tile_lo + t), x.w, 0u);
+        }
         // a shared call's unsplit rows have one partial each
-        for (uint32_t i = tid; i < P.n_tok; i += 1024)
+        for (uint32_t i = tid; i < P.n_tok; i += NT)
             rec[2 * i] = make_uint4(i, 0u, P.shared.lens && P.tile_of[i] != 0xFFFFFFFFu ? 1u : 0u, 0u);
     }
     if (tid == 0) {
         P.plan[0] = (split ? at[kMaxSplits] : n_tiles) * P.n_kv_head;
-        P.plan[1] = 0;
-        P.plan[2] = chunk;
+        P.plan[1] = P.sms;  // the CTAs' first items are theirs without asking
     }
     // a shared call's decode plan runs before this kernel, which may have
     // started beside it: this kernel ends after it
@@ -772,8 +785,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
         if (warp == C::WARP_TMA) {
             // ------------------------------------------------------------ producer
             if (lane == 0) {
-                const uint32_t n_items = __ldcg(P.plan);
-                const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
+                uint32_t n_items = 0;
+                [[maybe_unused]] const uint4* tiles = reinterpret_cast<const uint4*>(P.tiles);
                 uint32_t h = 0;  // half-tiles issued
                 // wait until slot h % NSLOT is free again
                 auto slot_free = [&](uint32_t hh) {
@@ -788,7 +801,20 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     }
                     if (misc[0]) break;
                     volatile uint32_t* d = desc + 8 * is;
-                    const uint32_t it = atomicAdd(P.plan + 1, 1u);
+                    // scored calls: a CTA's first item is its own, and an entry
+                    // has all there is to know of an item, so that the first
+                    // copies start one memory latency after the plan
+                    const uint32_t it = SC && k == 0 ? blockIdx.x : atomicAdd(P.plan + 1, 1u);
+                    [[maybe_unused]] uint4 e0 = make_uint4(0, 0, 0, 0), e1 = e0;
+                    if constexpr (SC) {
+                        if (k == 0 || it < n_items) {
+                            const uint4* e = reinterpret_cast<const uint4*>(P.list) +
+                                             2 * static_cast<size_t>(it / P.n_kv_head);
+                            e0 = __ldcg(e);
+                            e1 = __ldcg(e + 1);
+                        }
+                    }
+                    if (k == 0) n_items = __ldcg(P.plan);
                     if (it >= n_items) {
                         // nothing left for this CTA: what follows may be launched
                         if constexpr (SC) grid_launch_dependents();
@@ -812,38 +838,33 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                         }
                         break;
                     }
-                    // in the plan's hand-out order
-                    uint32_t tile, split = 0;
-                    if constexpr (SC) {
-                        const uint32_t entry = __ldcg(P.list + it / P.n_kv_head);
-                        tile = entry & 0xFFFFu;
-                        split = entry >> 16;
-                    } else {
-                        tile = __ldcg(P.tile_of + it / P.n_kv_head);
-                    }
-                    const uint4 rec = __ldcg(tiles + tile);
                     const uint32_t kvh = it % P.n_kv_head;
-                    // keys k_begin .. max_pos: 0 .. the tile's largest position,
-                    // or in a scored call the split's part of the tile's range
-                    uint32_t k_begin = 0, max_pos = rec.w;
+                    uint32_t y_row, keys;  // first row in the [rows][kv_dim] view, keys from it
                     if constexpr (SC) {
-                        const uint32_t chunk = __ldcg(P.plan + 2);
-                        k_begin = __ldcg(P.tile_lo + tile) + split * chunk * BK;
-                        const uint32_t left = (max_pos - k_begin) / BK;  // further key tiles
-                        if (left >= chunk) max_pos = k_begin + chunk * BK - 1;
+                        y_row = e0.z;
+                        keys = e1.x;
+                        d[0] = e0.x;
+                        d[1] = e0.y;
+                        d[2] = e0.w;  // first key
+                        d[3] = e1.y;  // split
+                    } else {
+                        // in the plan's hand-out order; keys 0 .. max_pos
+                        const uint4 rec = __ldcg(tiles + __ldcg(P.tile_of + it / P.n_kv_head));
+                        y_row = rec.z * P.slot_ctx;
+                        keys = rec.w + 1;
+                        d[0] = rec.x;
+                        d[1] = rec.y;
+                        d[2] = rec.z;
+                        d[3] = rec.w;
                     }
-                    const uint32_t ntiles = (max_pos - k_begin + BK) / BK;
-                    d[0] = rec.x;
-                    d[1] = rec.y;
-                    d[2] = SC ? k_begin : rec.z;
-                    d[3] = SC ? split : max_pos;
+                    const uint32_t ntiles = (keys + BK - 1) / BK;
                     d[4] = kvh;
                     d[5] = ntiles;
                     d[6] = 0;
                     mbar_arrive(IFULL + 8 * is);
-                    const int y0 = static_cast<int>(rec.z * P.slot_ctx + k_begin);
+                    const int y0 = static_cast<int>(y_row);
                     for (uint32_t t = 0; t < ntiles && !misc[0]; ++t) {
-                        const uint32_t left = max_pos - k_begin + 1 - t * BK;
+                        const uint32_t left = keys - t * BK;
                         const int y = y0 + static_cast<int>(t * BK);
                         for (int which = 0; which < 2; ++which, ++h) {  // K, then V
                             if (!slot_free(h)) {
@@ -1822,8 +1843,11 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(1024);
         cfg.numAttrs = p.after_plan ? 1 : 0;
-        e = cudaLaunchKernelEx(&cfg, p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1>
-                                                     : slotkv_scored_plan_kernel<C::MT, C::BK, 8>, p);
+        auto plan = p.n_tok <= 256    ? slotkv_scored_plan_kernel<C::MT, C::BK, 256, 1>
+                    : p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 1>
+                                      : slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 8>;
+        if (p.n_tok <= 256) cfg.blockDim = dim3(256);
+        e = cudaLaunchKernelEx(&cfg, plan, p);
         if (e != cudaSuccess) return static_cast<int>(e);
         cfg.numAttrs = 1;
     } else {

@@ -507,7 +507,7 @@ size_t partial_rows(const slotkv_s* h, bool shared) {
 int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
                      cudaStream_t stream) {
     const size_t R = h->max_rows;
-    const size_t list = R + (size_t)slotkv::kSplitMost * sm_total(h);
+    const size_t list = 8 * (R + (size_t)slotkv::kSplitMost * sm_total(h));
     const size_t pr = partial_rows(h, shared);
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, stream, "scored workspace (q)");
     if (rc == SLOTKV_OK)
@@ -519,11 +519,13 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     if (rc != SLOTKV_OK) return rc;
     P.q_rot = h->sc_q;
     P.part.rec = h->sc_idx;
+    // (records and list entries are read 16 bytes at a time: every offset before
+    // the plan's counters is a multiple of four words)
     P.tiles = h->sc_idx + 8 * R;
-    P.tile_of = h->sc_idx + 12 * R;
-    P.tile_lo = h->sc_idx + 13 * R;
-    P.list = h->sc_idx + 14 * R;
+    P.list = h->sc_idx + 12 * R;
     P.plan = P.list + list;
+    P.tile_of = P.plan + 4;
+    P.tile_lo = P.tile_of + R;
     P.sms = sm_total(h);
     // acc first: its rows are read and written 16 bytes at a time
     P.part.acc = h->sc_part[shared ? 1 : 0];

@@ -288,3 +288,40 @@ def test_requests_from_prompt_to_shared_steps():
     assert int(head) == R * math.ceil((sys_len + 50) / bs)
     for x in (L.kv, pool.kv, pre):
         x.free()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_stalled_pipeline_times_out_and_recovers(hd):
+    """The stall option withholds each CTA's first scores: a scored prefill and a
+    shared step end with DEV_TIMEOUT after their bounded waits, and the handle
+    works again."""
+    L = Layer(4, 200, 1, 2, hd, 40, seed=17)
+    PK, PV = L.rnd(1, 300, 1, hd), L.rnd(1, 300, 1, hd)
+    pkv = SlotKV(1, 300, 1, hd, 1, 2, k_buf=PK, v_buf=PV)
+    pos, slots, plen = [310, 305], [1, 2], [300, 300]
+    q, pq = L.step(2), L.step(40)
+    out, pout = torch.empty(2, 2, hd, device="cuda"), torch.empty(40, 2, hd, device="cuda")
+    ppos, pslots = i32(list(range(40))), i32([3] * 40)
+
+    def shared():
+        L.kv.decode_batch_attn_shared(*q, i32(pos), i32(slots), pkv, i32([0, 0]), i32(plen),
+                                      *L.params(), None, out, EPS, L.scale)
+
+    def prefill():
+        L.kv.prefill_batch_attn_scored(*pq, ppos, pslots, *L.params(), Scores(cap=9.0), pout, EPS,
+                                       L.scale)
+
+    for call in (shared, prefill):
+        call()
+        assert L.kv.get_status() == 0
+        L.kv.set_options(skv.OPT_TEST_STALL)
+        call()
+        assert L.kv.get_status() & skv.DEV_TIMEOUT
+        L.kv.set_options(0)
+        call()
+        assert L.kv.get_status() == 0
+    K64, V64, outs, tols, where = shared_want(L, PK, PV, *q, pos, slots, [0, 0], plen)
+    shared()
+    check(out, outs, tols, "shared")
+    L.kv.free()
+    pkv.free()
