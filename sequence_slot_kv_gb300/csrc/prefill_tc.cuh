@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if (tid <= kMaxSplits) hist[tid] = at[tid] = 0;
     __syncthreads();
+    uint32_t own_tile = 0xFFFFFFFFu;  // of the thread's last token
     auto max_op = [](int a, int b) { return a > b ? a : b; };
     auto add_op = [](uint32_t a, uint32_t b) { return a + b; };
     for (uint32_t r0 = 0; r0 < P.n_tok; r0 += NT * PER) {
@@ -611,7 +612,8 @@ __global__ void __launch_bounds__(NT, 1)
                 tlo = tlo < lo[j] ? tlo : lo[j];
                 thi = thi > hi[j] ? thi : hi[j];
             }
-            if (i0 + j < P.n_tok) P.tile_of[i0 + j] = in ? t - 1 : 0xFFFFFFFFu;
+            own_tile = in ? t - 1 : 0xFFFFFFFFu;
+            if (PER > 1 && i0 + j < P.n_tok) P.tile_of[i0 + j] = own_tile;
         }
         const uint32_t t_of_0 = __shfl_sync(0xffffffffu, t, 0);  // (every lane takes part)
         const bool one = __all_sync(0xffffffffu, n != 0 && t == t_of_0);
@@ -654,18 +656,23 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t wmax = __reduce_max_sync(0xffffffffu, ktiles);
         if (lane == 0) atomicMax(&longest, wmax);
         __syncthreads();
-        // the warps try 1 .. kMaxSplits splits of the longest tile; of equal
-        // costs the longest chunk, so the fewest partials
-        for (uint32_t s = warp + 1; s <= kMaxSplits; s += NT / 32) {
-            const uint32_t c = (longest + s - 1) / s;
-            if (s > 1 && c < kMinChunk) continue;
+        // thread s - 1 tries s splits of the longest tile; of equal costs the
+        // longest chunk, so the fewest partials.  (Divisions by the chunk are
+        // most of the work: a multiplication by ceil(2^32 / c) does them, exact
+        // while x c < 2^32, so for tiles of fewer than 32768 key tiles.)
+        if (tid < kMaxSplits) {
+            const uint32_t s = tid + 1, c = (longest + s - 1) / s;
+            const uint32_t magic = c > 1 && longest < 32768u ? 0xFFFFFFFFu / c + 1u : 0u;
             uint32_t items = 0;
-            for (uint32_t t = lane; t < n_tiles; t += 32) items += (t_part[t] + c - 1) / c;
-            items = __reduce_add_sync(0xffffffffu, items) * P.n_kv_head;
-            if (s > 1 && items > kSplitMost * P.sms) continue;
-            const uint64_t waves = (items + P.sms - 1) / P.sms;
-            const uint64_t cost = waves * (c + kItemCost + (s > 1 ? 1u : 0u));
-            if (lane == 0) atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - c));
+            for (uint32_t t = 0; t < n_tiles; ++t) {
+                const uint32_t x = t_part[t] + c - 1;
+                items += c == 1 ? x : (magic ? __umulhi(x, magic) : x / c);
+            }
+            items *= P.n_kv_head;
+            const uint32_t waves = (items + P.sms - 1) / P.sms;
+            uint64_t cost = static_cast<uint64_t>(waves) * (c + kItemCost + (s > 1 ? 1u : 0u));
+            if (s > 1 && (c < kMinChunk || items > kSplitMost * P.sms)) cost = 0x7FFFFFFFull;
+            atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - c));
         }
         __syncthreads();
         chunk = 0xFFFFFFFFu - static_cast<uint32_t>(best & 0xFFFFFFFFu);
@@ -679,21 +686,30 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncthreads();
         // split s begins in the list after the tiles with more than s' splits
-        // of every s' < s
-        if (tid == 0) {
-            uint32_t left = n_tiles, sum = 0;
-            for (uint32_t s = 0; s < kMaxSplits && left; ++s) {
-                left -= hist[s];  // (hist[0] is 0)
-                at[s] = sum;
-                sum += left;
-            }
-            at[kMaxSplits] = sum;
+        // of every s' < s; lane l has splits 2 l and 2 l + 1
+        static_assert(kMaxSplits == 64, "one warp has all splits, two a lane");
+        if (warp == 0) {
+            auto scan = [&](uint32_t v) {
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
+                    if (lane >= static_cast<uint32_t>(off)) v += o;
+                }
+                return v;
+            };
+            const uint32_t h0 = hist[2 * lane], h1 = hist[2 * lane + 1];
+            const uint32_t upto = scan(h0 + h1);              // tiles of <= 2 l + 1 splits
+            const uint32_t m1 = n_tiles - upto, m0 = m1 + h1;  // tiles that have split 2 l + 1, 2 l
+            const uint32_t end = scan(m0 + m1);
+            at[2 * lane] = end - m0 - m1;
+            at[2 * lane + 1] = end - m1;
+            if (lane == 31) at[kMaxSplits] = end;
         }
         __syncthreads();
         for (uint32_t s = 0; s < ns; ++s)
             put(atomicAdd(&at[s], 1u), t_first[tid], rows, t_slot[tid], t_lo[tid], t_hi[tid], s);
         for (uint32_t i = tid; i < P.n_tok; i += NT) {
-            const uint32_t t = P.tile_of[i];
+            const uint32_t t = PER == 1 ? own_tile : P.tile_of[i];  // (one round: its own token)
             rec[2 * i] = t == 0xFFFFFFFFu || t_ns[t] == 0
                              ? make_uint4(0u, 0u, 0u, 0u)
                              : make_uint4(t_part[t] + (i - t_first[t]), t_rows[t], t_ns[t], 0u);
@@ -706,7 +722,8 @@ __global__ void __launch_bounds__(NT, 1)
         }
         // a shared call's unsplit rows have one partial each
         for (uint32_t i = tid; i < P.n_tok; i += NT)
-            rec[2 * i] = make_uint4(i, 0u, P.shared.lens && P.tile_of[i] != 0xFFFFFFFFu ? 1u : 0u, 0u);
+            rec[2 * i] = make_uint4(
+                i, 0u, P.shared.lens && (PER == 1 ? own_tile : P.tile_of[i]) != 0xFFFFFFFFu ? 1u : 0u, 0u);
     }
     if (tid == 0) {
         P.plan[0] = (split ? at[kMaxSplits] : n_tiles) * P.n_kv_head;
