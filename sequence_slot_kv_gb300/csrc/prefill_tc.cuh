@@ -135,9 +135,16 @@ struct PCfg {
     static constexpr int OFF_DESC = NSLOT * SLOT;
     static constexpr int OFF_META = OFF_DESC + 2 * 32;
     static constexpr int OFF_BAR = OFF_META + NSLOT * 16;
-    // full[NSLOT], conv[NSLOT], empty[NSLOT], s_full[2], p_ready[2],
-    // pv_done[2], q_ready, item_full[2], item_free[2], drain
-    static constexpr int NBAR = 3 * NSLOT + 12;
+    // full[NLAND], conv[NLAND], empty[NSLOT], s_full[2], p_ready[2],
+    // pv_done[2], q_ready, item_full[2], item_free[2], drain.  Half-tile h's
+    // full and conv barriers: h % NSLOT in plain calls, whose converters see
+    // every half-tile; h % 6 in scored calls, so that a barrier belongs to K
+    // half-tiles or to V ones alone and the converters of one kind see every
+    // phase of theirs (with three slots a slot is K's and V's by turns, and
+    // copies land in any order)
+    static constexpr int NLAND = 6;
+    static_assert(NSLOT <= NLAND && NLAND % 2 == 0, "barriers of landed half-tiles");
+    static constexpr int NBAR = 2 * NLAND + NSLOT + 12;
     static constexpr int OFF_TSLOT = OFF_BAR + NBAR * 8;
     static constexpr int OFF_MISC = OFF_TSLOT + 16;
     // misc[0]: abort; misc[2 + w]: converter warp w's stop flag; misc[8]: see
@@ -754,8 +761,12 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::OFF_TSLOT);
     const uint32_t ring = smem_addr(smem);
     const uint32_t bar0 = smem_addr(smem + C::OFF_BAR);
-    const uint32_t FULL = bar0, CONV = bar0 + 8 * NSLOT, EMPTY = bar0 + 16 * NSLOT;
-    const uint32_t SFULL = bar0 + 24 * NSLOT, PREADY = SFULL + 16;
+    constexpr uint32_t NL = SC ? C::NLAND : NSLOT;
+    const uint32_t FULL = bar0, CONV = bar0 + 8 * C::NLAND, EMPTY = bar0 + 16 * C::NLAND;
+    auto full_bar = [&](uint32_t h) { return FULL + 8 * (h % NL); };
+    auto conv_bar = [&](uint32_t h) { return CONV + 8 * (h % NL); };
+    auto land_phase = [](uint32_t h) { return (h / NL) & 1u; };
+    const uint32_t SFULL = EMPTY + 8 * NSLOT, PREADY = SFULL + 16;
     const uint32_t PVDONE = PREADY + 16, QREADY = PVDONE + 16, IFULL = QREADY + 8;
     const uint32_t IFREE = IFULL + 16, DRAIN = IFREE + 16;
     // hi and lo operand buffers of a slot
@@ -763,9 +774,11 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
     auto slot_lo = [&](uint32_t sl) { return ring + sl * C::SLOT + C::BUF; };
 
     if (tid == 0) {
-        for (int i = 0; i < NSLOT; ++i) {
+        for (int i = 0; i < C::NLAND; ++i) {
             mbar_init(FULL + 8 * i, 1);
             mbar_init(CONV + 8 * i, C::NCONV);
+        }
+        for (int i = 0; i < NSLOT; ++i) {
             mbar_init(EMPTY + 8 * i, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -843,7 +856,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             break;
                         }
                         meta[4 * (h % NSLOT) + 1] = 1;
-                        mbar_arrive(FULL + 8 * (h % NSLOT));
+                        mbar_arrive(full_bar(h));
                         if constexpr (SC) {  // and one for the V converters
                             ++h;
                             if (!slot_free(h)) {
@@ -851,7 +864,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                                 break;
                             }
                             meta[4 * (h % NSLOT) + 1] = 1;
-                            mbar_arrive(FULL + 8 * (h % NSLOT));
+                            mbar_arrive(full_bar(h));
                         }
                         break;
                     }
@@ -891,11 +904,11 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             const uint32_t sl = h % NSLOT;
                             meta[4 * sl + 0] = left < static_cast<uint32_t>(BK) ? left : BK;
                             meta[4 * sl + 1] = 0;
-                            mbar_expect_tx(FULL + 8 * sl, C::BUF);
+                            mbar_expect_tx(full_bar(h), C::BUF);
     #pragma unroll
                             for (int c = 0; c < NB; ++c)
                                 tma_load_2d(slot_hi(sl) + c * C::BLK, which ? &tmV : &tmK,
-                                            static_cast<int>(kvh * HD) + 32 * c, y, FULL + 8 * sl);
+                                            static_cast<int>(kvh * HD) + 32 * c, y, full_bar(h));
                         }
                     }
                     if (misc[0]) break;
@@ -903,7 +916,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 if (misc[0]) {
                     // drain this CTA's copies that may still be in flight
                     for (uint32_t u = h > static_cast<uint32_t>(NSLOT) ? h - NSLOT : 0; u < h; ++u)
-                        mbar_wait(FULL + 8 * (u % NSLOT), (u / NSLOT) & 1, 1ll << 28);
+                        mbar_wait(full_bar(u), land_phase(u), 1ll << 28);
                 }
             }
         } else if (warp >= C::WARP_CONV + C::NCONV) {
@@ -916,7 +929,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
             const int ct = tid - (C::WARP_CONV + C::NCONV) * 32;
             for (uint32_t h = 0;; h += 2) {
                 const uint32_t sl = h % NSLOT;
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(FULL + 8 * sl, (h / NSLOT) & 1));
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(full_bar(h), land_phase(h)));
                 if (!ok) timeout();
                 if (__any_sync(0xffffffffu, !ok || misc[0] || meta[4 * sl + 1])) break;
                 const uint32_t rows = meta[4 * sl + 0];
@@ -946,7 +959,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane < C::NCONV / C::NKCONV) mbar_arrive(CONV + 8 * sl);
+                if (lane < C::NCONV / C::NKCONV) mbar_arrive(conv_bar(h));
             }
         } else if (warp >= C::WARP_CONV) {
             // ------------------------------------------------------------ converters
@@ -960,7 +973,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 // all stop at the same half-tile: each publishes its own reason
                 // to stop (a wait that expired, an abort, the end marker) and all
                 // decide from the published flags.
-                const bool ok = mbar_wait(FULL + 8 * sl, (h / NSLOT) & 1);
+                const bool ok = mbar_wait(full_bar(h), land_phase(h));
                 if (!ok) timeout();
                 if (lane == 0) misc[2 + w] = (!ok || misc[0] || meta[4 * sl + 1]) ? 1 : 0;
                 named_sync_conv<NT>();
@@ -1057,7 +1070,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(CONV + 8 * sl);
+                if (lane == 0) mbar_arrive(conv_bar(h));
             }
         } else if (warp == C::WARP_MMA) {
             // ------------------------------------------------------------ MMA issuer
@@ -1082,7 +1095,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     return SC ? __any_sync(0xffffffffu, a) != 0 : a;
                 };
                 auto converted = [&](uint32_t hh) {
-                    return wait(CONV + 8 * (hh % NSLOT), (hh / NSLOT) & 1);
+                    return wait(conv_bar(hh), land_phase(hh));
                 };
                 // O += P V for tile t of the item (global tile gp)
                 auto issue_pv = [&](uint32_t t, uint32_t gp) {
