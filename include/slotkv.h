@@ -356,11 +356,13 @@ typedef struct {
  * prefill_batch_attn's, each reading the union of its rows' keys.  A call of
  * few tiles (a chunk of a long prompt) also cuts each tile's keys into splits
  * and joins them with one more kernel, so results depend on the batch in the
- * last bits.  Its workspace is allocated by the handle's first such call
- * (queries, items, and 128 * 4 partial rows per SM), at the size of max_rows
- * and max_n_head: make one before capturing into a graph (a call under
- * capture that would have to allocate returns SLOTKV_ERR_STATE and captures
- * nothing).  Head dim 256 runs the scored decode kernel once per token.
+ * last bits.  A key that a row attends and that is not finite in K makes the
+ * row NaN (in V, it has its usual effect).  The prefill's workspace is
+ * allocated by the handle's first such call (queries, items, and 128 * 8
+ * partial rows per SM), at the size of max_rows and max_n_head: make one
+ * before capturing into a graph (a call under capture that would have to
+ * allocate returns SLOTKV_ERR_STATE and captures nothing).  Head dim 256 runs
+ * the scored decode kernel once per token.
  */
 int decode_batch_attn_scored(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
                              const float* k_new, const float* v_new, const uint32_t* positions,
@@ -391,7 +393,8 @@ int prefill_batch_attn_scored(slotkv_t handle, uint32_t n_tok, uint32_t n_head, 
  *                 prefill_batch_attn or decode steps as any slot is; it has
  *                 the same n_kv_head, head_dim and device as `handle`, its
  *                 own n_slots and slot_ctx, and may be `handle` itself.  It
- *                 is only read.
+ *                 is only read; no row's own slot may be one of the prefix
+ *                 slots in use when it is `handle`.
  *   prefix_slots  device u32[B]: the prefix handle's slot with the row's prefix.
  *   prefix_lens   device u32[B]: how many of the row's keys are there, positions
  *                 0 .. prefix_lens[b] - 1 of that slot.  0: none (a plain row,

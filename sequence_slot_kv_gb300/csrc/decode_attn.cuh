@@ -941,8 +941,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
             }
             r.prow = slot * P.slot_ctx + r.p;
         }
-        uint32_t end = r.p;  // keys [base, end], plus none past key p
-        uint32_t base = 0;
+        uint32_t base = 0, end = r.p;  // keys [base, end]
         if constexpr (SC) {
             if (!paged) end = hi;
             base = row_base(r.lo, end, T);

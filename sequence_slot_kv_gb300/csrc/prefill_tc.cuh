@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) {
         P.plan[0] = (split ? at[kMaxSplits] : n_tiles) * P.n_kv_head;
         P.plan[1] = P.sms;  // the CTAs' first items are theirs without asking
+        P.plan[2] = split ? 1u : 0u;
     }
     // a shared call's decode plan runs before this kernel, which may have
     // started beside it: this kernel ends after it
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             meta[4 * sl + 0] = left < static_cast<uint32_t>(BK) ? left : BK;
                             meta[4 * sl + 1] = 0;
                             mbar_expect_tx(full_bar(h), C::BUF);
-    #pragma unroll
+#pragma unroll
                             for (int c = 0; c < NB; ++c)
                                 tma_load_2d(slot_hi(sl) + c * C::BLK, which ? &tmV : &tmK,
                                             static_cast<int>(kvh * HD) + 32 * c, y, full_bar(h));
@@ -978,7 +979,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 if (lane == 0) misc[2 + w] = (!ok || misc[0] || meta[4 * sl + 1]) ? 1 : 0;
                 named_sync_conv<NT>();
                 int stop = 0;
-    #pragma unroll
+#pragma unroll
                 for (int w2 = 0; w2 < C::NCONV; ++w2) stop |= misc[2 + w2];
                 if (stop) break;
                 const uint32_t rows = meta[4 * sl + 0];
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     // rows past the item's last key are zeroed in both
                     float4* hi = reinterpret_cast<float4*>(hib);
                     float4* lo = reinterpret_cast<float4*>(lob);
-    #pragma unroll
+#pragma unroll
                     for (int i = ct; i < C::BUF / 16; i += NT) {
                         // each 128-byte row of a column block is 8 float4s
                         const uint32_t row = static_cast<uint32_t>(i % (C::BLK / 16)) / 8;
@@ -1017,12 +1018,12 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     // key per load) before any writes, so the in-place
                     // permutation is safe whatever its cycles.
                     float x[C::SB_PER_WARP][32];
-    #pragma unroll
+#pragma unroll
                     for (int j = 0; j < C::SB_PER_WARP; ++j) {
                         const int sb = w + C::NCONV * j;
                         const int kb = sb / NB, db = sb % NB;
                         const uint8_t* src = hib + db * C::BLK + kb * 4096;
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const uint32_t off = (k / 8) * 1024 + (k % 8) * 128 +
                                                  (((lane / 4) ^ (k % 8)) * 16) + (lane % 4) * 4;
@@ -1033,34 +1034,34 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     if constexpr (SC) {
                         // the largest magnitude's bits tell whether every value is finite
                         uint32_t top = 0;
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < C::SB_PER_WARP; ++j)
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 const uint32_t u = __float_as_uint(x[j][k]) & 0x7FFFFFFFu;
                                 top = top > u ? top : u;
                             }
                         if (top >= 0x7F800000u) {
                             misc[8] = 1;  // seen by the epilogue through this tile's barriers
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < C::SB_PER_WARP; ++j)
-    #pragma unroll
+#pragma unroll
                                 for (int k = 0; k < 32; ++k)
                                     if ((__float_as_uint(x[j][k]) & 0x7F800000u) == 0x7F800000u)
                                         x[j][k] = 0.f;
                         }
                     }
                     named_sync_conv<NT>();
-    #pragma unroll
+#pragma unroll
                     for (int j = 0; j < C::SB_PER_WARP; ++j) {
                         const int sb = w + C::NCONV * j;
                         const int kb = sb / NB, db = sb % NB;
                         const uint32_t base = kb * C::VT_BLK + db * 4096 + (lane / 8) * 1024 +
                                               (lane % 8) * 128;
-    #pragma unroll
+#pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             uint32_t hh[4], ll[4];
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 4; ++e) tf32_split(x[j][4 * c + e], hh[e], ll[e]);
                             const uint32_t off = base + ((c ^ (lane % 8)) * 16);
                             *reinterpret_cast<uint4*>(hib + off) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
@@ -1129,7 +1130,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     } else {
                         // O += P_lo V_hi + P_hi V_hi + P_hi V_lo, K-step by K-step
                         // (consecutive products share their B, then their A, slice)
-        #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < BK / 8; ++kk) {
                             const uint32_t off = (kk / 4) * C::VT_BLK + (kk % 4) * 32;
                             const uint64_t bh = tc::smem_desc(slot_hi(sl) + off, 16, 1024, tc::kSwizzle128B);
@@ -1756,19 +1757,28 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
     if (warp == 0) tc::tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
-// Join the splits of a scored prefill: one warp per (token, head), splits in
-// order; rows the attention kernel has finished itself have no partials.
+// Join the splits of one (token, head) of a scored prefill, by one warp,
+// splits in order.
 template <int HD>
-__global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefillParams P) {
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t wg = blockIdx.x * 4 + (threadIdx.x >> 5);
-    grid_dependency_wait();
-    const uint32_t tok = wg / P.n_head, head = wg % P.n_head;
-    if (tok >= P.n_tok) return;
-    const uint4 rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + 2 * tok);
-    if (rec.z == 0u) return;
+__device__ __forceinline__ void combine_row(const ScoredPrefillParams& P, uint4 rec, uint32_t tok,
+                                            uint32_t head, uint32_t lane) {
     const size_t at0 = static_cast<size_t>(rec.x) * P.n_head + head;
     const size_t step = static_cast<size_t>(rec.y) * P.n_head;
+    constexpr int EL = HD / 32;  // elements per lane
+    float v[4][EL];
+    auto load4 = [&](uint32_t s0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float2* src = reinterpret_cast<const float2*>(P.part.acc + (at0 + (s0 + u) * step) * HD);
+#pragma unroll
+            for (int e = 0; e < EL / 2; ++e) {
+                const float2 x = s0 + u < rec.z ? __ldcg(src + lane + 32 * e) : make_float2(0.f, 0.f);
+                v[u][2 * e] = x.x;
+                v[u][2 * e + 1] = x.y;
+            }
+        }
+    };
+    load4(0);  // (in flight with the maxima and sums)
     // lanes take splits lane and lane + 32 (kMaxSplits is 64)
     float2 c[2];
     float M = -CUDART_INF_F;
@@ -1798,20 +1808,9 @@ __global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefill
         const float cm = exp2f(M - M2);
         f = cm / (L * cm + exp2f(sk - M2));
     }
-    constexpr int EL = HD / 32;  // elements per lane
     float a[EL] = {};
     for (uint32_t s0 = 0; s0 < rec.z; s0 += 4) {
-        float v[4][EL];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float2* src = reinterpret_cast<const float2*>(P.part.acc + (at0 + (s0 + u) * step) * HD);
-#pragma unroll
-            for (int e = 0; e < EL / 2; ++e) {
-                const float2 x = s0 + u < rec.z ? __ldcg(src + lane + 32 * e) : make_float2(0.f, 0.f);
-                v[u][2 * e] = x.x;
-                v[u][2 * e + 1] = x.y;
-            }
-        }
+        if (s0) load4(s0);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const uint32_t s = s0 + u;
@@ -1823,6 +1822,37 @@ __global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefill
     float2* o = reinterpret_cast<float2*>(P.out + (static_cast<size_t>(tok) * P.n_head + head) * HD);
 #pragma unroll
     for (int e = 0; e < EL / 2; ++e) o[lane + 32 * e] = make_float2(a[2 * e] * f, a[2 * e + 1] * f);
+}
+
+// Every prefill launches it: whether the plan split the tiles is known on the
+// device alone, since rows out of range belong to no tile (a padded call may
+// have few).  With nothing to join its CTAs end at once, ~1.5 us of a call's
+// end.  517 tokens of 64 heads of 64 in four splits: 13 us after the attention
+// kernel's end (34 MB read, 8 MB written: 3.3 TB/s), one round trip per row
+// for its partials; 24 us at four CTAs per SM.
+constexpr uint32_t kCombineCtas = 16;
+template <int HD>
+__global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefillParams P) {
+    grid_dependency_wait();
+    if (__ldcg(P.plan + 2) == 0u) return;
+    // a warp's rows are one grid apart; its lanes look up which of the next 32
+    // have splits (rows that the attention kernel has finished itself have none)
+    const uint32_t n = P.n_tok * P.n_head, warps = gridDim.x * 4, lane = threadIdx.x & 31;
+    for (uint64_t w0 = blockIdx.x * 4 + (threadIdx.x >> 5); w0 < n; w0 += 32ull * warps) {
+        const uint64_t mine = w0 + static_cast<uint64_t>(lane) * warps;
+        uint4 rec = make_uint4(0, 0, 0, 0);
+        if (mine < n)
+            rec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) +
+                         2 * static_cast<size_t>(static_cast<uint32_t>(mine) / P.n_head));
+        for (uint32_t left = __ballot_sync(0xffffffffu, rec.z != 0u); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            const uint32_t w = static_cast<uint32_t>(w0) + from * warps;
+            const uint4 x = make_uint4(__shfl_sync(0xffffffffu, rec.x, from),
+                                       __shfl_sync(0xffffffffu, rec.y, from),
+                                       __shfl_sync(0xffffffffu, rec.z, from), 0u);
+            combine_row<HD>(P, x, w / P.n_head, w % P.n_head, lane);
+        }
+    }
 }
 
 template <int HD, int G, bool SC = false>
@@ -1894,11 +1924,9 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
         cfg.dynamicSmemBytes = C::SMEM_SC;
         e = cudaLaunchKernelEx(&cfg, slotkv_prefill_tc_kernel<HD, G, SC>, tmK, tmV, p);
         if (e != cudaSuccess) return static_cast<int>(e);
-        // a prefill that the plan may split: join the splits (at least
-        // ceil(n_tok / MT) tiles; the plan splits below kSplitBelow items per SM)
-        if (!p.shared.lens && static_cast<uint64_t>((p.n_tok + C::MT - 1) / C::MT) * p.n_kv_head <
-                                  static_cast<uint64_t>(kSplitBelow) * p.sms) {
-            cfg.gridDim = dim3((p.n_tok * p.n_head + 3) / 4);
+        if (!p.shared.lens) {  // join the splits, if any
+            const uint32_t most = kCombineCtas * p.sms, rows = (p.n_tok * p.n_head + 3) / 4;
+            cfg.gridDim = dim3(rows < most ? rows : most);
             cfg.blockDim = dim3(128);
             cfg.dynamicSmemBytes = 0;
             e = cudaLaunchKernelEx(&cfg, slotkv_combine_kernel<HD>, p);

@@ -256,12 +256,13 @@ def test_decode_rows_out_of_range(hd, block):
 
 
 # ------------------------------------------------------------------ prefill
-def prefill_case(hd, G, n_kv, seqs, ctx, rule, seed, poison=True, order=None, cold=1):
-    """seqs: (past, fresh) per sequence; order: a permutation seed of the tokens."""
+def prefill_case(hd, G, n_kv, seqs, ctx, rule, seed, poison=True, order=None, pad=0):
+    """seqs: (past, fresh) per sequence; order: a permutation seed of the tokens;
+    pad: rows of no slot after the others."""
     sinks, slopes = rule.get("sinks", False), rule.get("slopes", False)
     cap, window = rule.get("cap", 0.0), rule.get("window", 0)
     n = sum(f for _, f in seqs)
-    L = Layer(len(seqs) + 1, ctx, n_kv, G, hd, n + 3, seed, sinks, slopes)
+    L = Layer(len(seqs) + 1, ctx, n_kv, G, hd, n + pad + 3, seed, sinks, slopes)
     r = torch.Generator().manual_seed(seed)
     toks = [(s + 1, p) for s, (past, f) in enumerate(seqs) for p in range(past, past + f)]
     if order is not None:
@@ -288,12 +289,16 @@ def prefill_case(hd, G, n_kv, seqs, ctx, rule, seed, poison=True, order=None, co
             L.K[s, :min(first, past)], L.V[s, :min(first, past)] = math.inf, math.nan
     K64, V64, outs, tols = want_rows(L, q, k_new, v_new, pos, where, lambda b, t: (toks[b][0], t),
                                      True, cap, window, doc, pend)
-    out = torch.full((n, L.n_head, hd), math.nan, device="cuda")
-    sc = Scores(cap, window, L.slopes, i32(doc) if doc else None, i32(pend) if pend else None)
-    L.kv.prefill_batch_attn_scored(q, k_new, v_new, i32(pos), i32([s for s, _ in toks]),
-                                   *L.params(), sc, out, EPS, L.scale)
-    assert L.kv.get_status() == 0
+    more = lambda x: torch.cat([x, x[:1].expand(pad, *x.shape[1:])]).contiguous() if pad else x
+    rows = lambda x: i32(x + [0] * pad) if x else None
+    out = torch.full((n + pad, L.n_head, hd), math.nan, device="cuda")
+    sc = Scores(cap, window, L.slopes, rows(doc), rows(pend))
+    L.kv.prefill_batch_attn_scored(more(q), more(k_new), more(v_new), rows(pos),
+                                   i32([s for s, _ in toks] + [-1] * pad), *L.params(), sc, out,
+                                   EPS, L.scale)
+    assert L.kv.get_status() == (1 if pad else 0)
     check(out, outs, tols, "prefill")
+    assert bool(torch.isnan(out[n:]).all()), "a row of no slot was written"
     check_cache(L, K64, V64, where)
     L.kv.free()
 
@@ -325,6 +330,20 @@ def test_prefill_split_over_a_long_history(hd, rule):
 @pytest.mark.parametrize("hd", [64, 128, 256])
 def test_prefill_tokens_in_any_order(hd):
     prefill_case(hd, 2, 2, [(0, 40), (20, 50), (300, 9)], 400, PREFILL_RULES[-1], seed=hd, order=3)
+
+
+@pytest.mark.parametrize("hd,G", [(64, 8), (128, 8), (64, 1)])
+def test_prefill_of_a_padded_batch(hd, G):
+    """A call padded with rows of no slot, as one of fixed capacity is: enough
+    rows that it would not be split, too few tokens not to be."""
+    prefill_case(hd, G, 8 if G == 8 else 2, [(900, 21), (0, 3)], 1000, dict(cap=12.0, window=600),
+                 seed=hd + G, pad=5000 if G == 1 else 900)
+
+
+def test_prefill_of_many_tokens():
+    """More tokens than one round of the plan takes, most sequences short."""
+    prefill_case(64, 1, 1, [(3, 5)] * 1500 + [(0, 790), (40, 150)], 800, dict(window=50, slopes=True),
+                 seed=5, poison=False)
 
 
 @pytest.mark.parametrize("hd", [64, 128])
