@@ -76,7 +76,12 @@ double number(PyObject* o) {
 
 int64_t integer(PyObject* o) {
     if (!PyLong_Check(o)) throw Unlike{};
-    return PyLong_AsLongLong(o);
+    const int64_t x = PyLong_AsLongLong(o);
+    if (x == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw Unlike{};
+    }
+    return x;
 }
 
 slotkv_stream_t stream_of(PyObject* o, int dev) {
