@@ -226,6 +226,8 @@ constexpr uint32_t kSplitBelow = 2, kSplitMost = 8, kMaxSplits = 64;
 inline size_t partial_head_rows(uint32_t sms) { return (size_t)128 * kSplitMost * sms; }
 
 // Keys per pipeline stage of the tensor-core prefill.
-__host__ __device__ constexpr int prefill_tile_keys(int) { return 64; }
+__host__ __device__ constexpr int prefill_tile_keys(int hd, bool scored = false) {
+    return scored && hd == 128 ? 32 : 64;
+}
 
 }  // namespace slotkv

@@ -88,12 +88,12 @@
 
 namespace slotkv {
 
-template <int HD, int G>
+template <int HD, int G, bool SC = false>
 struct PCfg {
     static constexpr int M = 128;               // query rows per tile (MMA M)
     static constexpr int MT = M / G;            // tokens per tile
     static constexpr int ROWS = MT * G;         // rows in use (<= 128)
-    static constexpr int BK = prefill_tile_keys(HD);  // keys per tile (QK's N)
+    static constexpr int BK = prefill_tile_keys(HD, SC);  // keys per tile (QK's N)
     static constexpr int NB = HD / 32;          // 128-byte column blocks per key row
     static constexpr int BLK = BK * 128;        // one column block: BK rows x 128 B
     static constexpr int BUF = NB * BLK;        // one operand buffer, [BK][HD] f32
@@ -126,7 +126,7 @@ struct PCfg {
     // scored calls: with two score buffers PV(t) may run while O(t - 1) is
     // still to be read, so O has a second buffer after the score buffers
     static constexpr uint32_t C_O2 = 3 * HD + NBUF * 2 * BK;
-    static_assert(NBUF == 1 || C_O2 + HD <= 512, "tensor memory columns");
+    static constexpr bool TWO_O = SC && NBUF == 2 && C_O2 + HD <= 512;
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(3 * HD + NBUF * 2 * BK <= 512, "tensor memory columns");
     static_assert(BK % 32 == 0 && HD % 32 == 0, "32-column tensor memory accesses");
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
 // in L2; unsplit tiles are listed last to first, as above.  The order has no
 // part in any result: a split's partial has a place of its own.
 constexpr uint32_t kPlanTiles = 512;
-constexpr uint32_t kItemCost = 2, kMinChunk = 2;  // key tiles
+constexpr uint32_t kItemCost = 128, kMinChunk = 128;  // in keys
 
 // Inclusive scan of one value per thread over the CTA.
 template <typename T, typename Op>
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(NT, 1)
             }
             items *= P.n_kv_head;
             const uint32_t waves = (items + P.sms - 1) / P.sms;
-            uint64_t cost = static_cast<uint64_t>(waves) * (c + kItemCost + (s > 1 ? 1u : 0u));
-            if (s > 1 && (c < kMinChunk || items > kSplitMost * P.sms)) cost = 0x7FFFFFFFull;
+            uint64_t cost = static_cast<uint64_t>(waves) * (c * BK + kItemCost + (s > 1 ? kItemCost / 2 : 0u));
+            if (s > 1 && (c * BK < kMinChunk || items > kSplitMost * P.sms)) cost = 0x7FFFFFFFull;
             atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - c));
         }
         __syncthreads();
@@ -746,11 +746,11 @@ __global__ void __launch_bounds__(NT, 1)
 // Half-tile h of the CTA's stream of key tiles: h = 2g is tile g's K, h = 2g + 1
 // its V; it lives in slot h % NSLOT.
 template <int HD, int G, bool SC = false>
-__global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::THREADS, 1)
+__global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>::THREADS, 1)
     slotkv_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV,
                              const prefill_params_t<SC> P) {
-    using C = PCfg<HD, G>;
+    using C = PCfg<HD, G, SC>;
     constexpr int BK = C::BK, NB = C::NB, NSLOT = C::NSLOT, NBUF = C::NBUF;
     constexpr float kLog2e = 1.4426950408889634f;
     extern __shared__ uint8_t smem_raw[];
@@ -1110,7 +1110,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     const uint32_t pcol0 = C::C_S + (gp % NBUF) * C::C_BUF;
                     if constexpr (SC) {
                         // the tile's own O: products with a low part first
-                        const uint32_t ocol = tb + (NBUF == 2 && (gp & 1) ? C::C_O2 : C::C_O);
+                        const uint32_t ocol = tb + (C::TWO_O && (gp & 1) ? C::C_O2 : C::C_O);
                         const uint32_t phi = tb + pcol0, plo = phi + BK;
                         const uint64_t bh = tc::smem_desc(slot_hi(sl), 16, 1024, tc::kSwizzle128B);
                         const uint64_t bl = tc::smem_desc(slot_lo(sl), 16, 1024, tc::kSwizzle128B);
@@ -1251,7 +1251,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
         // acted on alone), so neither half can leave its partner waiting at
         // the barrier.
         constexpr int HB = BK / 2, HH = HD / 2;
-        static_assert(HB == 32 && HH % 32 == 0, "one 32-column access per half of a score tile");
+        static_assert((HB == 32 || HB == 16) && HH % 32 == 0, "one access per half of a score tile");
         const int quarter = warp & 3, hf = warp >> 2;
         const uint32_t r = static_cast<uint32_t>(quarter * 32 + lane);  // query row = TMEM lane
         const uint32_t lrow = tbase + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -1429,7 +1429,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 return false;
             }
             tc::fence_after_sync();
-            const uint32_t ocol = NBUF == 2 && (j & 1) ? C::C_O2 : C::C_O;
+            const uint32_t ocol = C::TWO_O && (j & 1) ? C::C_O2 : C::C_O;
 #pragma unroll
             for (int c0 = 0; c0 < HH; c0 += 32) {
                 uint32_t v[32];
@@ -1476,12 +1476,12 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                     const uint32_t scol = C::C_S + (g % NBUF) * C::C_BUF + hf * HB;
                     float s[HB];
                     {
-                        uint32_t v[32];
-                        tc::tmem_ld32(lrow + scol, v);
-                        if constexpr (SC && NBUF == 2) {
+                        uint32_t v[HB];
+                        tc::tmem_ld(lrow + scol, v);
+                        if constexpr (SC && C::TWO_O) {
                             // two: the O of tile t - 2 with S(t), whose commit
                             // covers its PV
-                            static_assert(NBUF == 1 || HH == 32, "one access per half of O");
+                            static_assert(!C::TWO_O || HH == 32, "one access per half of O");
                             if (t >= 2) {
                                 uint32_t o[32];
                                 tc::tmem_ld32(lrow + (g & 1 ? C::C_O2 : C::C_O) + hf * HH, o);
@@ -1578,6 +1578,11 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                             for (int i = 0; i < HH; ++i) acc[i] *= corr;
                         }
                         corr_prev = rescale ? corr : 1.f;
+                        // two score buffers but one O: that of tile t - 1 is read
+                        // before P(t) lets the tensor core write it again
+                        if constexpr (NBUF == 2 && !C::TWO_O) {
+                            if (t >= 1 && !add_tile(g - 1, corr_prev)) failed = true;
+                        }
                     }
                     // O may be rescaled only once the previous tile's O += P V
                     // (global tile g - 1) has completed.  PV(j) completes a phase
@@ -1609,7 +1614,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                         }
                     }
                     {
-                        uint32_t hi[32], lo[32];
+                        uint32_t hi[HB], lo[HB];
 #pragma unroll
                         for (int c = 0; c < HB; c += 2) {
                             if constexpr (SC) {
@@ -1619,8 +1624,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                                 tf32_split(s[c + 1], hi[c + 1], lo[c + 1]);
                             }
                         }
-                        tc::tmem_st32(lrow + scol, hi);
-                        tc::tmem_st32(lrow + scol + BK, lo);
+                        tc::tmem_st(lrow + scol, hi);
+                        tc::tmem_st(lrow + scol + BK, lo);
                     }
                     tc::tmem_st_wait();
                     tc::fence_before_sync();
@@ -1649,7 +1654,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G>::THREADS_SC : PCfg<HD, G>::TH
                 // wait that ran out.
                 bool stop3;
                 if constexpr (SC) {
-                    stop3 = NBUF == 2 && ntiles >= 2 && !add_tile(g - 2, corr_prev);
+                    stop3 = C::TWO_O && ntiles >= 2 && !add_tile(g - 2, corr_prev);
                     stop3 = !add_tile(g - 1, 1.f) || stop3;
                 } else {
                     stop3 = !mbar_wait(PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1);
@@ -1858,7 +1863,7 @@ __global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefill
 template <int HD, int G, bool SC = false>
 int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        unsigned ctas, cudaStream_t stream) {
-    using C = PCfg<HD, G>;
+    using C = PCfg<HD, G, SC>;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;

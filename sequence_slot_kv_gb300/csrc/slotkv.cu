@@ -94,6 +94,7 @@ struct slotkv_s {
     // slot buffers, and a workspace grown on demand by prefill calls
     bool tc_prefill = false;
     CUtensorMap tmKs, tmVs;
+    CUtensorMap tmKc, tmVc;  // the scored calls', with their own tile height
     float* pf_q = nullptr;           // [tokens][n_head][hd] rotated q
     uint32_t* pf_tiles = nullptr;    // [tokens][4] tile records
     uint32_t* pf_tile_of = nullptr;  // [tokens]
@@ -235,10 +236,11 @@ int encode_maps(slotkv_s* h) {
     // the tensor-core prefill reads [keys][32 floats] boxes, 128-byte swizzled
     h->tc_prefill = h->head_dim == 64 || h->head_dim == 128;
     if (h->tc_prefill) {
-        const cuuint32_t sbox[2] = {32, (cuuint32_t)slotkv::prefill_tile_keys((int)h->head_dim)};
-        CUtensorMap* smaps[2] = {&h->tmKs, &h->tmVs};
-        for (int i = 0; i < 2; ++i) {
-            CUresult r = enc(smaps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, bufs[i], dims, strides,
+        CUtensorMap* smaps[4] = {&h->tmKs, &h->tmVs, &h->tmKc, &h->tmVc};
+        for (int i = 0; i < 4; ++i) {
+            const cuuint32_t sbox[2] = {
+                32, (cuuint32_t)slotkv::prefill_tile_keys((int)h->head_dim, i >= 2)};
+            CUresult r = enc(smaps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, bufs[i & 1], dims, strides,
                              sbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1271,7 +1273,7 @@ int prefill_batch_attn_scored(slotkv_t h, uint32_t n_tok, uint32_t n_head, const
     P.scale_log2 = scale * 1.4426950408889634f;
     P.flags = h->options;
     P.rule = score_rule(scores);
-    return launch_scored_prefill(h, P, h->tmKs, h->tmVs, s);
+    return launch_scored_prefill(h, P, h->tmKc, h->tmVc, s);
 }
 
 int decode_batch_attn_shared(slotkv_t h, uint32_t B, uint32_t n_head, const float* q,
@@ -1346,7 +1348,7 @@ int decode_batch_attn_shared(slotkv_t h, uint32_t B, uint32_t n_head, const floa
     P.own_slots = slots;
     P.own_n_slots = h->n_slots;
     P.own_ctx = h->slot_ctx;
-    rc = launch_scored_prefill(h, P, prefix->tmKs, prefix->tmVs, s);
+    rc = launch_scored_prefill(h, P, prefix->tmKc, prefix->tmVc, s);
     if (rc != SLOTKV_OK) return rc;
     return launch_scored(h, D, cs, slotkv::ScoredPart::attention, s);
 }
