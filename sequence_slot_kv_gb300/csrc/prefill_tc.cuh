@@ -1086,10 +1086,18 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                 uint32_t g = 0;  // key tiles whose QK was issued
                 bool ok = true;
                 // a wait's outcome and the abort flag, the same for the whole
-                // warp (the lanes meet again below, so they leave together)
+                // warp (the lanes meet again below, so they leave together).
+                // Scored calls look at the abort flag only where a wait did
+                // not find its phase complete at once: a role that has left
+                // arrives no more.
                 auto wait = [&](uint32_t bar, uint32_t parity) {
-                    const bool done = mbar_wait(bar, parity);
-                    return SC ? __all_sync(0xffffffffu, done) != 0 : done;
+                    if constexpr (SC) {
+                        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+                        const bool done = mbar_wait(bar, parity) && misc[0] == 0;
+                        return __all_sync(0xffffffffu, done) != 0;
+                    } else {
+                        return mbar_wait(bar, parity);
+                    }
                 };
                 auto aborted = [&]() {
                     const bool a = misc[0] != 0;
@@ -1173,7 +1181,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                             ok = false;
                             break;
                         }
-                        if (aborted()) {
+                        if (!SC && aborted()) {
                             ok = false;
                             break;
                         }
