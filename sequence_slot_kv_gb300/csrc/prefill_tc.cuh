@@ -73,14 +73,29 @@
 //     core's accumulation drops bits at every step, always toward zero, so a
 //     long chain drifts (1.2e-4 relative over 16 thousand keys).  Each key
 //     tile's P V therefore starts a new accumulator, which the softmax warps
-//     add to a register copy of O with rounded f32 adds -- O(t) is read while
-//     the tensor core forms the next scores -- and within a chain the products
-//     with a low part come first, while the partial sum is still small.  Q
-//     and P are split with a rounded high part, so the dropped lo x lo terms
-//     have no common sign;
+//     add to a register copy of O with rounded f32 adds, and within a chain
+//     the products with a low part come first, while the partial sum is still
+//     small.  Q and P are split with a rounded high part, so the dropped
+//     lo x lo terms have no common sign;
+//   * two score buffers at head dim 128 too: its key tiles are 32 keys, not 64,
+//     so Q, O and two buffers of (S, P) fill the 512 columns of tensor memory.
+//     O has one buffer there: O(t - 1) is read once the softmax of tile t is
+//     done, just before P(t) allows the tensor core to write O again.  At head
+//     dim 64 O has two, and O(t - 2) is read with S(t);
+//   * 16 warps: converters 10-13 take V and 14-15 K, so K(t + 1) and V(t) are
+//     converted side by side; the MMA warp issues in step, one elected lane;
+//     q and out rows pass through 2 KB of shared memory per softmax warp, in
+//     64-byte pieces; the softmax's halves exchange maxima only when a row's
+//     would rise;
 //   * a V value that is not finite is taken as 0 by the tensor core (0 times
 //     it would poison every masked row of the tile), and rows that do attend
 //     it get it added in the epilogue from the slot itself.
+// What bounds them, measured: head dim 128, 256 rows on a prefix of 32700 keys,
+// 497 us, 2100 cycles per tile of 32 keys of which the tensor core needs 1800
+// (three TF32 products: 85 % of its rate); head dim 64, 517 tokens on 15.8
+// thousand keys, 561 us, 2340 cycles per tile of 64 keys against 1800, the
+// rest the softmax's latencies.  64-key tiles with one score buffer at head
+// dim 128 took 636 us, a single thread issuing 33 % longer.
 #pragma once
 
 #include "decode_attn.cuh"
@@ -123,10 +138,13 @@ struct PCfg {
     static constexpr uint32_t C_QHI = 0, C_QLO = HD, C_O = 2 * HD, C_S = 3 * HD;
     static constexpr uint32_t C_BUF = 2 * BK;   // columns per score buffer
     static constexpr int NBUF = (512 - 3 * HD) / (2 * BK) >= 2 ? 2 : 1;
-    // scored calls: with two score buffers PV(t) may run while O(t - 1) is
-    // still to be read, so O has a second buffer after the score buffers
+    // scored calls: a second O after the score buffers where there is room
+    // (head dim 64): O(t - 2) is then read together with S(t); with one, O(t -
+    // 1) is read before P(t) is handed over (604 instead of 584 us for 517
+    // tokens on 15.8 thousand keys)
     static constexpr uint32_t C_O2 = 3 * HD + NBUF * 2 * BK;
     static constexpr bool TWO_O = SC && NBUF == 2 && C_O2 + HD <= 512;
+    static_assert(!SC || NBUF == 2, "scored calls: two score buffers");
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(3 * HD + NBUF * 2 * BK <= 512, "tensor memory columns");
     static_assert(BK % 32 == 0 && HD % 32 == 0, "32-column tensor memory accesses");
@@ -452,7 +470,8 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
 // The scored calls' plan (one CTA of NT threads, PER consecutive tokens per
 // thread and round: 256 threads and one token for a call of up to 256 rows,
 // 1024 and one up to 1024 -- the time of such a call is the latency of code run
-// once, so the least of it and few warps to wait for -- else 1024 and eight).  Runs and tiles as above, over the rows that
+// once, so the least of it and few warps to wait for: 6.8 us for 51 rows, 9.0
+// for 528 -- else 1024 and eight).  Runs and tiles as above, over the rows that
 // have keys for the tensor cores (PrefillRow); a tile's record is the same,
 // with its smallest key in tile_lo.  The first kPlanTiles tiles are kept in
 // shared memory until the end.
@@ -1471,11 +1490,6 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                     for (int i = 0; i < HH; ++i) acc[i] = 0.f;
                 }
                 for (uint32_t t = 0; t < ntiles; ++t, ++g) {
-                    // one score buffer: the O of tile t - 1, while the tensor
-                    // core forms S(t)
-                    if constexpr (SC && NBUF == 1) {
-                        if (t >= 1 && !add_tile(g - 1, 1.f)) failed = true;
-                    }
                     if (!mbar_wait(SFULL + 8 * (g & 1), (g >> 1) & 1)) {
                         timeout();
                         failed = true;
@@ -1588,7 +1602,7 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                         corr_prev = rescale ? corr : 1.f;
                         // two score buffers but one O: that of tile t - 1 is read
                         // before P(t) lets the tensor core write it again
-                        if constexpr (NBUF == 2 && !C::TWO_O) {
+                        if constexpr (!C::TWO_O) {
                             if (t >= 1 && !add_tile(g - 1, corr_prev)) failed = true;
                         }
                     }
