@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(128) slotkv_decode_small_kernel(const decode_p
         if (P.shared.lens) {
             // everything above ran beside the prefix pass; its partials here
             grid_dependency_wait();
+            grid_launch_dependents();
             const uint4 prec = __ldcg(reinterpret_cast<const uint4*>(P.part.rec) + 2 * b);
             fold_partials<HD, G, EF>(P.part, prec, P.n_head, g * G, warp, W, m, l, acc, dim);
         }

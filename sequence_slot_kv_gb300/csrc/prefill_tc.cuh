@@ -514,6 +514,9 @@ __global__ void __launch_bounds__(NT, 1)
     __shared__ uint32_t carry_tiles, longest;
     __shared__ int carry_start;
     __shared__ unsigned long long best;
+    // This kernel is a programmatic dependent: of the decode plan in a shared
+    // call, which has waited for the work before the call, else of that work.
+    if (!P.after_plan) grid_dependency_wait();
     // Prep, launched next as a programmatic dependent, may start at once: it
     // reads nothing of what this kernel writes, and its last CTA waits for
     // this kernel, so the attention kernel after it waits for both.
@@ -1861,6 +1864,7 @@ constexpr uint32_t kCombineCtas = 16;
 template <int HD>
 __global__ void __launch_bounds__(128) slotkv_combine_kernel(const ScoredPrefillParams P) {
     grid_dependency_wait();
+    grid_launch_dependents();
     if (__ldcg(P.plan + 2) == 0u) return;
     // a warp's rows are one grid apart; its lanes look up which of the next 32
     // have splits (rows that the attention kernel has finished itself have none)
@@ -1926,17 +1930,15 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
         // Scored calls: a chain of programmatic dependents.  In a shared call
         // the decode plan comes first, and this plan runs beside it (it has
         // waited for the work before the call); otherwise this plan starts
-        // the chain in stream order.
+        // the chain, and its launch overlaps the end of the work before.
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(1024);
-        cfg.numAttrs = p.after_plan ? 1 : 0;
         auto plan = p.n_tok <= 256    ? slotkv_scored_plan_kernel<C::MT, C::BK, 256, 1>
                     : p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 1>
                                       : slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 8>;
         if (p.n_tok <= 256) cfg.blockDim = dim3(256);
         e = cudaLaunchKernelEx(&cfg, plan, p);
         if (e != cudaSuccess) return static_cast<int>(e);
-        cfg.numAttrs = 1;
     } else {
         slotkv_prefill_plan_kernel<C::MT><<<1, 1024, 0, stream>>>(p);
     }
