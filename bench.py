@@ -51,11 +51,10 @@ FLUSH_BYTES = 256 * 1024 * 1024  # written between calls of a step that fits in 
 MEASURED_TRAFFIC = {
     # all at full size; large's is its first step's ratio to the algorithmic
     # bytes times the mean algorithmic bytes of its 64 steps
-    # (plan + decode kernel bytes, the mean of two calls; of 18 calls for the
-    # eight-heads-per-kv-head workloads)
-    "26542fcb3b784732": {"mid": 551_830_912, "sinks": 2_336_513_024,
-                         "skewed": 17_227_054_208, "large": 2_238_835_960,
-                         "gqa8_hd128": 509_073_606, "gqa8_hd256": 627_442_587},
+    # (plan + decode kernel bytes, the mean of two calls)
+    "2e7d6b87bdebec18": {"mid": 551_777_920, "sinks": 2_336_571_392,
+                         "skewed": 17_226_651_136, "large": 2_238_753_490,
+                         "gqa8_hd128": 509_397_120, "gqa8_hd256": 627_379_840},
 }
 
 
@@ -85,7 +84,7 @@ def measured_traffic(workload):
 # prefill workload of a geometry (ncu one-pass counters, the mean over the
 # full-size calls' launches), keyed by code_hash of prefill_tc.cuh; reported
 # only while the kernel is the one measured.
-MEASURED_PREFILL_TRAFFIC = {"56858cc248ba86b3": {"mid": 247_501_909, "sinks": 170_577_280}}
+MEASURED_PREFILL_TRAFFIC = {"264e9da811e82a42": {"mid": 247_734_016, "sinks": 170_438_144}}
 
 
 def prefill_source_hash():

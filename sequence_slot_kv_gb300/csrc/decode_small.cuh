@@ -30,7 +30,9 @@
 //      the max and the denominator, and out is written.
 // Scored calls (SC) start at the chunk of the row's first attended key and
 // apply the score rule where the persistent kernel does; in a shared call the
-// prefix partials join in step 6, spread over the four warps.
+// prefix partials join in step 6, spread over the four warps.  Three rows of up
+// to 383 keys (head dim 64, cap, window 256): 7.8 us; three chunks in flight
+// instead of two 9.1 against 9.0 at the time.
 // No spin-waits: only __syncthreads and cp.async groups.
 #pragma once
 

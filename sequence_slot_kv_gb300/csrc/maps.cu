@@ -15,7 +15,10 @@
 // maximum over the marks then tells every unit its request.  Both
 // kernels are launched as programmatic dependents, wait for what precedes
 // them before anything else, and let their own dependents launch: the set-up
-// of one call overlaps the call before it.
+// of one call overlaps the call before it.  Measured back to back: 5 requests
+// 2.7 us, 601 requests with 65 thousand tokens 3.5 us, a step of 67 requests'
+// tables 3.4 us, the tables of 4099 prompts 10.3 us (there every CTA's sum of
+// all the counts is most of the instructions).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
