@@ -1756,7 +1756,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float4 y = stage[stage_at(i * 8 + sub, ch)];
-                            if (dst[i]) *reinterpret_cast<float4*>(dst[i] + c0) = y;
+                            // (streaming: q's rows stay in L2 for the items to come)
+                            if (dst[i]) __stcs(reinterpret_cast<float4*>(dst[i] + c0), y);
                         }
                     }
                 } else {
