@@ -17,8 +17,8 @@
 // them before anything else, and let their own dependents launch: the set-up
 // of one call overlaps the call before it.  Measured back to back: 5 requests
 // 2.7 us, 601 requests with 65 thousand tokens 3.5 us, a step of 67 requests'
-// tables 3.4 us, the tables of 4099 prompts 10.3 us (there every CTA's sum of
-// all the counts is most of the instructions).
+// tables 3.4 us, the tables of 4099 prompts 8.7 us (a chain of passes: counts,
+// scan, marks, owners, free list; one or four CTAs per SM differ by 1 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -165,9 +165,10 @@ __device__ __forceinline__ bool blocks_needed(const ExtendTablesParams& P, uint3
     return true;
 }
 
-// Tiles of new blocks, one after the other over the grid.  CTA 0 checks the
-// requests and finds the new head; the last CTA to finish writes it, since
-// the others may still have to read the old one from the same word.
+// Tiles of new blocks, one after the other over the grid.  The grid's last CTA,
+// which has the fewest of them, checks the requests and finds the new head.
+// It writes it at once, unless that is the word the other CTAs may still have
+// to read the old one from: then the last CTA to finish does (1.5 us more).
 __global__ void __launch_bounds__(kMapThreads)
     slotkv_extend_tables_kernel(const ExtendTablesParams P) {
     __shared__ uint64_t sums[kMapWarps];
@@ -189,9 +190,11 @@ __global__ void __launch_bounds__(kMapThreads)
         sum += need;
     }
     const uint64_t at0 = block_exclusive(sum, sums, total);
-    if (blockIdx.x == 0) {
+    const bool same_word = P.head_out == P.head && gridDim.x > 1;
+    if (blockIdx.x == gridDim.x - 1) {
         uint64_t at = at0;
         uint32_t last = 0;
+#pragma unroll 4
         for (uint32_t r = r0; r < r1; ++r) {
             uint32_t have, need;
             const bool ok = blocks_needed(P, r, have, need);
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kMapThreads)
         }
         if (last) atomicMax(&used, last);
         __syncthreads();
-        if (threadIdx.x == 0 && gridDim.x > 1) P.scratch[1] = head + used;
+        if (threadIdx.x == 0) *(same_word ? P.scratch + 1 : P.head_out) = head + used;
     }
     const uint64_t end = total < avail ? total : avail;
     for (uint64_t t0 = static_cast<uint64_t>(blockIdx.x) * kMapTile; t0 < end;
@@ -238,10 +241,9 @@ __global__ void __launch_bounds__(kMapThreads)
         }
         __syncthreads();  // the marks are free again
     }
+    if (!same_word) return;
     __syncthreads();
-    if (threadIdx.x == 0 && gridDim.x == 1) {
-        *P.head_out = head + used;
-    } else if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
         __threadfence();
         if (atomicAdd(P.scratch, 1u) == gridDim.x - 1) {
             __threadfence();
