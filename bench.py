@@ -52,9 +52,9 @@ MEASURED_TRAFFIC = {
     # all at full size; large's is its first step's ratio to the algorithmic
     # bytes times the mean algorithmic bytes of its 64 steps
     # (plan + decode kernel bytes, the mean of two calls)
-    "2e7d6b87bdebec18": {"mid": 551_777_920, "sinks": 2_336_571_392,
-                         "skewed": 17_226_651_136, "large": 2_238_753_490,
-                         "gqa8_hd128": 509_397_120, "gqa8_hd256": 627_379_840},
+    "2e7d6b87bdebec18": {"mid": 551_848_064, "sinks": 2_336_483_840,
+                         "skewed": 17_226_947_200, "large": 2_238_627_873,
+                         "gqa8_hd128": 509_223_936, "gqa8_hd256": 627_351_680},
 }
 
 
@@ -84,7 +84,7 @@ def measured_traffic(workload):
 # prefill workload of a geometry (ncu one-pass counters, the mean over the
 # full-size calls' launches), keyed by code_hash of prefill_tc.cuh; reported
 # only while the kernel is the one measured.
-MEASURED_PREFILL_TRAFFIC = {"264e9da811e82a42": {"mid": 247_734_016, "sinks": 170_438_144}}
+MEASURED_PREFILL_TRAFFIC = {"8fb9ab5e5936775a": {"mid": 247_635_200, "sinks": 170_428_928}}
 
 
 def prefill_source_hash():
