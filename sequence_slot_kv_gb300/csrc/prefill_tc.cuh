@@ -513,7 +513,10 @@ __global__ void __launch_bounds__(NT, 1)
     __shared__ uint32_t scan_u[32], hist[kMaxSplits + 1], at[kMaxSplits + 1];
     __shared__ uint32_t carry_tiles, longest;
     __shared__ int carry_start;
-    __shared__ unsigned long long best;
+    __shared__ uint64_t best[kMaxSplits / 32];
+    // the last token of the previous round and of each warp: its slot, and
+    // whether it has keys
+    __shared__ uint32_t last_of_slot[NT / 32 + 1], last_of_keys[NT / 32 + 1];
     // This kernel is a programmatic dependent: of the decode plan in a shared
     // call, which has waited for the work before the call, else of that work.
     if (!P.after_plan) grid_dependency_wait();
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(NT, 1)
         carry_tiles = 0;
         carry_start = -1;
         longest = 1;
-        best = ~0ull;
+        last_of_keys[0] = 0;
     }
     if (tid <= kMaxSplits) hist[tid] = at[tid] = 0;
     __syncthreads();
@@ -540,12 +543,6 @@ __global__ void __launch_bounds__(NT, 1)
         uint32_t slot[PER], lo[PER], hi[PER];
         uint32_t keys = 0, starts = 0;  // bit j: token i0 + j
         uint32_t last_slot = 0, last_keys = 0;  // of the thread's last token
-        uint32_t first_prev_slot = 0, first_prev = 0;
-        if (lane == 0 && i0 > 0 && i0 < P.n_tok) {
-            const PrefillRow r = prefill_row(P, i0 - 1);
-            first_prev = r.keys ? 1u : 0u;
-            first_prev_slot = r.slot;
-        }
 #pragma unroll
         for (uint32_t j = 0; j < PER; ++j) {
             slot[j] = lo[j] = hi[j] = 0;
@@ -563,9 +560,14 @@ __global__ void __launch_bounds__(NT, 1)
         }
         uint32_t prev_slot = __shfl_up_sync(0xffffffffu, last_slot, 1);
         uint32_t prev = __shfl_up_sync(0xffffffffu, last_keys, 1);
+        if (lane == 31) {
+            last_of_slot[warp + 1] = last_slot;
+            last_of_keys[warp + 1] = last_keys;
+        }
+        __syncthreads();
         if (lane == 0) {
-            prev_slot = first_prev_slot;
-            prev = first_prev;
+            prev_slot = last_of_slot[warp];
+            prev = last_of_keys[warp];
         }
         int last_start = -1;
 #pragma unroll
@@ -657,6 +659,8 @@ __global__ void __launch_bounds__(NT, 1)
         if (tid == NT - 1) {
             carry_tiles += incl;
             carry_start = max_op(incl_start, before);
+            last_of_slot[0] = last_slot;
+            last_of_keys[0] = last_keys;
         }
         __syncthreads();
     }
@@ -701,10 +705,17 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t waves = (items + P.sms - 1) / P.sms;
             uint64_t cost = static_cast<uint64_t>(waves) * (c * BK + kItemCost + (s > 1 ? kItemCost / 2 : 0u));
             if (s > 1 && (c * BK < kMinChunk || items > kSplitMost * P.sms)) cost = 0x7FFFFFFFull;
-            atomicMin(&best, (cost << 32) | (0xFFFFFFFFu - c));
+            uint64_t key = (cost << 32) | (0xFFFFFFFFu - c);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+                const uint64_t o = __shfl_xor_sync(0xffffffffu, key, off);
+                key = o < key ? o : key;
+            }
+            if (lane == 0) best[warp] = key;
         }
         __syncthreads();
-        chunk = 0xFFFFFFFFu - static_cast<uint32_t>(best & 0xFFFFFFFFu);
+        static_assert(kMaxSplits == 64, "two warps have a candidate a lane");
+        chunk = 0xFFFFFFFFu - static_cast<uint32_t>((best[0] < best[1] ? best[0] : best[1]) & 0xFFFFFFFFu);
         const uint32_t ns = tid < n_tiles ? (ktiles + chunk - 1) / chunk : 0u;
         const uint32_t mine = ns > 1 || P.shared.lens ? ns * rows : 0u;  // partial rows
         const uint32_t base = block_inclusive(mine, scan_u, add_op, 0u) - mine;
