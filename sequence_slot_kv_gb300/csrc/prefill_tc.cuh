@@ -263,8 +263,8 @@ __device__ __forceinline__ PrefillRow prefill_row(const ScoredPrefillParams& P, 
 }
 
 template <int HD>
-__host__ __device__ constexpr int prep_smem_bytes() {
-    return 4 * kPrepHeads * HD * 4;  // four warps x kPrepHeads rows
+__host__ __device__ constexpr int prep_smem_bytes(int warps = 4) {
+    return warps * kPrepHeads * HD * 4;  // kPrepHeads rows per warp
 }
 
 // query-head groups and kv-head groups per token
@@ -275,15 +275,15 @@ __host__ __device__ inline uint32_t prep_groups(uint32_t n_head, uint32_t n_kv_h
     return prep_q_groups(n_head) + (n_kv_head + kPrepKvHeads - 1) / kPrepKvHeads;
 }
 
+// wg: the warp's place in the grid
 template <int HD, bool SC>
-__device__ __forceinline__ void prefill_prep(const prefill_params_t<SC>& P) {
+__device__ __forceinline__ void prefill_prep(const prefill_params_t<SC>& P, const uint32_t wg) {
     extern __shared__ __align__(16) uint8_t prep_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t qg = prep_q_groups(P.n_head);
     uint32_t groups = prep_groups(P.n_head, P.n_kv_head);
     if constexpr (SC)
         if (P.shared.lens) groups = qg;  // the decode kernel forms and writes k' and v
-    const uint32_t wg = blockIdx.x * 4 + warp;
     const uint32_t tok = wg / groups, grp = wg % groups;
     if (tok >= P.n_tok) return;
     const uint32_t p = P.positions[tok], slot = P.slots[tok];
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(128)
     // and the last CTA ends after the plan, this kernel's programmatic
     // predecessor
     if constexpr (SC) grid_launch_dependents();
-    prefill_prep<HD, SC>(P);
+    prefill_prep<HD, SC>(P, blockIdx.x * 4 + (threadIdx.x >> 5));
     if constexpr (SC)
         if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(1024, 1) slotkv_prefill_plan_kernel(const Pref
 // The scored calls' plan (one CTA of NT threads, PER consecutive tokens per
 // thread and round: 256 threads and one token for a call of up to 256 rows,
 // 1024 and one up to 1024 -- the time of such a call is the latency of code run
-// once, so the least of it and few warps to wait for: 6.8 us for 51 rows, 9.0
-// for 528 -- else 1024 and eight).  Runs and tiles as above, over the rows that
+// once, so the least of it and few warps to wait for: 4.3 us for six rows, 7.4
+// for 517 -- else 1024 and eight).  Runs and tiles as above, over the rows that
 // have keys for the tensor cores (PrefillRow); a tile's record is the same,
 // with its smallest key in tile_lo.  The first kPlanTiles tiles are kept in
 // shared memory until the end.
@@ -505,8 +505,7 @@ __device__ T block_inclusive(T v, T* warp_vals, Op op, T zero) {
 }
 
 template <int MT, int BK, uint32_t NT, uint32_t PER>
-__global__ void __launch_bounds__(NT, 1)
-    slotkv_scored_plan_kernel(const ScoredPrefillParams P) {
+__device__ __forceinline__ void scored_plan(const ScoredPrefillParams& P) {
     __shared__ uint32_t t_first[kPlanTiles], t_rows[kPlanTiles], t_slot[kPlanTiles];
     __shared__ uint32_t t_lo[kPlanTiles], t_hi[kPlanTiles], t_ns[kPlanTiles], t_part[kPlanTiles];
     __shared__ int scan_i[32];
@@ -517,13 +516,6 @@ __global__ void __launch_bounds__(NT, 1)
     // the last token of the previous round and of each warp: its slot, and
     // whether it has keys
     __shared__ uint32_t last_of_slot[NT / 32 + 1], last_of_keys[NT / 32 + 1];
-    // This kernel is a programmatic dependent: of the decode plan in a shared
-    // call, which has waited for the work before the call, else of that work.
-    if (!P.after_plan) grid_dependency_wait();
-    // Prep, launched next as a programmatic dependent, may start at once: it
-    // reads nothing of what this kernel writes, and its last CTA waits for
-    // this kernel, so the attention kernel after it waits for both.
-    grid_launch_dependents();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint4* tiles = reinterpret_cast<uint4*>(P.tiles);
     uint4* rec = reinterpret_cast<uint4*>(P.part.rec);
@@ -773,6 +765,36 @@ __global__ void __launch_bounds__(NT, 1)
     // a shared call's decode plan runs before this kernel, which may have
     // started beside it: this kernel ends after it
     grid_dependency_wait();
+}
+
+template <int MT, int BK, uint32_t NT, uint32_t PER>
+__global__ void __launch_bounds__(NT, 1)
+    slotkv_scored_plan_kernel(const ScoredPrefillParams P) {
+    // This kernel is a programmatic dependent: of the decode plan in a shared
+    // call, which has waited for the work before the call, else of that work.
+    if (!P.after_plan) grid_dependency_wait();
+    // Prep, launched next as a programmatic dependent, may start at once: it
+    // reads nothing of what this kernel writes, and its last CTA waits for
+    // this kernel, so the attention kernel after it waits for both.
+    grid_launch_dependents();
+    scored_plan<MT, BK, NT, PER>(P);
+}
+
+// Calls of up to kFrontRows rows have the plan (CTA 0) and prep (the others) in
+// one launch: such a call takes the host, at 2 to 5 us a launch, about as long
+// as the GPU (six rows on a prefix 17.1 -> 16.2 us, 9 tokens on 600 keys 16.5
+// -> 15.6, 51 rows on two prefixes 98.8 -> 97.9).  Larger calls keep the plan's
+// 1024 threads and prep's small CTAs, which fill the SMs better.
+constexpr uint32_t kFrontRows = 256, kFrontThreads = 256;
+template <int HD, int MT, int BK>
+__global__ void __launch_bounds__(kFrontThreads)
+    slotkv_scored_front_kernel(const ScoredPrefillParams P) {
+    if (!P.after_plan) grid_dependency_wait();  // (as the plan kernel)
+    grid_launch_dependents();
+    if (blockIdx.x == 0)
+        scored_plan<MT, BK, kFrontThreads, 1>(P);
+    else
+        prefill_prep<HD, true>(P, (blockIdx.x - 1) * (kFrontThreads / 32) + (threadIdx.x >> 5));
 }
 
 // ------------------------------------------------------------------ attention
@@ -1918,6 +1940,19 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
             e = cudaFuncGetAttributes(&fa, slotkv_prefill_tc_kernel<HD, G, SC>);
             if (e != cudaSuccess) return static_cast<int>(e);
             if (fa.numRegs != 128) return static_cast<int>(cudaErrorInvalidConfiguration);
+            // the attention kernel's shared-memory carve-out for the kernels
+            // around it, so the SMs need no reconfiguration between them
+            const int carve = cudaSharedmemCarveoutMaxShared;
+            const cudaFuncAttribute which = cudaFuncAttributePreferredSharedMemoryCarveout;
+            if ((e = cudaFuncSetAttribute(slotkv_scored_front_kernel<HD, C::MT, C::BK>, which, carve)) !=
+                    cudaSuccess ||
+                (e = cudaFuncSetAttribute(slotkv_prefill_prep_kernel<HD, SC>, which, carve)) != cudaSuccess ||
+                (e = cudaFuncSetAttribute(slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 1>, which, carve)) !=
+                    cudaSuccess ||
+                (e = cudaFuncSetAttribute(slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 8>, which, carve)) !=
+                    cudaSuccess ||
+                (e = cudaFuncSetAttribute(slotkv_combine_kernel<HD>, which, carve)) != cudaSuccess)
+                return static_cast<int>(e);
         }
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
@@ -1943,22 +1978,30 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
         // the decode plan comes first, and this plan runs beside it (it has
         // waited for the work before the call); otherwise this plan starts
         // the chain, and its launch overlaps the end of the work before.
-        cfg.gridDim = dim3(1);
-        cfg.blockDim = dim3(1024);
-        auto plan = p.n_tok <= 256    ? slotkv_scored_plan_kernel<C::MT, C::BK, 256, 1>
-                    : p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 1>
-                                      : slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 8>;
-        if (p.n_tok <= 256) cfg.blockDim = dim3(256);
-        e = cudaLaunchKernelEx(&cfg, plan, p);
+        if (p.n_tok <= kFrontRows) {
+            constexpr uint32_t W = kFrontThreads / 32;
+            cfg.gridDim = dim3(1 + (warps + W - 1) / W);
+            cfg.blockDim = dim3(kFrontThreads);
+            cfg.dynamicSmemBytes = prep_smem_bytes<HD>(W);
+            e = cudaLaunchKernelEx(&cfg, slotkv_scored_front_kernel<HD, C::MT, C::BK>, p);
+        } else {
+            cfg.gridDim = dim3(1);
+            cfg.blockDim = dim3(1024);
+            auto plan = p.n_tok <= 1024 ? slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 1>
+                                        : slotkv_scored_plan_kernel<C::MT, C::BK, 1024, 8>;
+            e = cudaLaunchKernelEx(&cfg, plan, p);
+        }
         if (e != cudaSuccess) return static_cast<int>(e);
     } else {
         slotkv_prefill_plan_kernel<C::MT><<<1, 1024, 0, stream>>>(p);
     }
-    cfg.gridDim = dim3((warps + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = prep_smem_bytes<HD>();
-    e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD, SC>, p);
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (!SC || p.n_tok > kFrontRows) {
+        cfg.gridDim = dim3((warps + 3) / 4);
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = prep_smem_bytes<HD>();
+        e = cudaLaunchKernelEx(&cfg, slotkv_prefill_prep_kernel<HD, SC>, p);
+        if (e != cudaSuccess) return static_cast<int>(e);
+    }
     if constexpr (SC) {
         cfg.gridDim = dim3(ctas);
         cfg.blockDim = dim3(C::THREADS_SC);
