@@ -84,7 +84,7 @@ def measured_traffic(workload):
 # prefill workload of a geometry (ncu one-pass counters, the mean over the
 # full-size calls' launches), keyed by code_hash of prefill_tc.cuh; reported
 # only while the kernel is the one measured.
-MEASURED_PREFILL_TRAFFIC = {"8fb9ab5e5936775a": {"mid": 247_635_200, "sinks": 170_428_928}}
+MEASURED_PREFILL_TRAFFIC = {"f28075a46c9a73c5": {"mid": 247_365_333, "sinks": 170_332_331}}
 
 
 def prefill_source_hash():
