@@ -89,7 +89,13 @@
 //     would rise;
 //   * a V value that is not finite is taken as 0 by the tensor core (0 times
 //     it would poison every masked row of the tile), and rows that do attend
-//     it get it added in the epilogue from the slot itself.
+//     it get it added in the epilogue from the slot itself.  The converters
+//     keep a log of the key tiles that held one, so that only those are read
+//     again, and only for the item they belong to: of 39 tiles of 16 tokens on
+//     12000 keys, one infinity in another sequence of the call leaves the time
+//     as it is (1.01 ms at head dim 64, 1.28 at 128), one in every 997th key
+//     adds 0.1 to 0.2 ms; a history of nothing else takes 0.5 to 0.7 us a key.
+//     The log costs the calls without any 0.6 to 1.3 %.
 // What bounds them, measured: head dim 128, 256 rows on a prefix of 32700 keys,
 // 497 us, 2100 cycles per tile of 32 keys of which the tensor core needs 1800
 // (three TF32 products: 85 % of its rate); head dim 64, 517 tokens on 15.8
@@ -165,8 +171,7 @@ struct PCfg {
     static constexpr int NBAR = 2 * NLAND + NSLOT + 12;
     static constexpr int OFF_TSLOT = OFF_BAR + NBAR * 8;
     static constexpr int OFF_MISC = OFF_TSLOT + 16;
-    // misc[0]: abort; misc[2 + w]: converter warp w's stop flag; misc[8]: see
-    // the kernel
+    // misc[0]: abort; misc[2 + w]: converter warp w's stop flag
     // the softmax halves' exchange: row maxima [2 parities][2 halves][M],
     // row sums [2 halves][M], and a stop flag beside each
     static constexpr int OFF_XCH = OFF_MISC + 64;
@@ -174,7 +179,12 @@ struct PCfg {
     static constexpr int SMEM = SMEM_USED + 1024;   // slack to align the ring to 1 KiB
     // scored calls: 2 KB for each softmax warp to stage rows in
     static constexpr int OFF_STAGE = (SMEM_USED + 15) / 16 * 16;
-    static constexpr int SMEM_SC = OFF_STAGE + NSW * 2048 + 1024;
+    // and each converter warp's log of the key tiles, numbered over the CTA's
+    // items, that held a V value that is not finite: [NCONV][LOG] runs of
+    // tiles (first, last), then the runs so far and the last tile plus 1
+    static constexpr int LOG = 64, LOG_GAP = 8;
+    static constexpr int OFF_LOG = OFF_STAGE + NSW * 2048;
+    static constexpr int SMEM_SC = OFF_LOG + NCONV * (2 * LOG + 2) * 4 + 1024;
     static_assert(SMEM <= 227 * 1024 && SMEM_SC <= 227 * 1024, "shared memory");
     static_assert(BLK % 1024 == 0 && SLOT % 1024 == 0, "128-byte swizzle atoms stay 1 KiB aligned");
     static constexpr uint32_t IDESC_QK = tc::idesc_tf32(M, BK, false);
@@ -815,6 +825,9 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
     volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_META);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::OFF_TSLOT);
+    [[maybe_unused]] auto log_of = [&](int w) {
+        return reinterpret_cast<volatile uint32_t*>(smem + C::OFF_LOG) + w * (2 * C::LOG + 2);
+    };
     const uint32_t ring = smem_addr(smem);
     const uint32_t bar0 = smem_addr(smem + C::OFF_BAR);
     constexpr uint32_t NL = SC ? C::NLAND : NSLOT;
@@ -847,7 +860,8 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
         mbar_init(QREADY, C::NSW);
         mbar_init(DRAIN, 1);
         misc[0] = 0;
-        misc[8] = 0;  // scored calls: a V value of this CTA's tiles was not finite
+        if constexpr (SC)
+            for (int w = 0; w < C::NCONV; ++w) log_of(w)[2 * C::LOG] = log_of(w)[2 * C::LOG + 1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -1096,8 +1110,22 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                                 const uint32_t u = __float_as_uint(x[j][k]) & 0x7FFFFFFFu;
                                 top = top > u ? top : u;
                             }
-                        if (top >= 0x7F800000u) {
-                            misc[8] = 1;  // seen by the epilogue through this tile's barriers
+                        if (__builtin_expect(__any_sync(0xffffffffu, top >= 0x7F800000u), 0)) {
+                            // into the log (seen by the epilogue through this
+                            // tile's barriers): the newest run goes on over a
+                            // few tiles without one
+                            if (lane == 0) {
+                                volatile uint32_t* log = log_of(w);
+                                const uint32_t g = h / 2;
+                                uint32_t n = log[2 * C::LOG];
+                                if (n == 0 || g > log[2 * C::LOG + 1] + C::LOG_GAP) {
+                                    log[2 * (n % C::LOG)] = g;
+                                    ++n;
+                                }
+                                log[2 * ((n - 1) % C::LOG) + 1] = g;
+                                log[2 * C::LOG] = n;
+                                log[2 * C::LOG + 1] = g + 1;
+                            }
 #pragma unroll
                             for (int j = 0; j < C::SB_PER_WARP; ++j)
 #pragma unroll
@@ -1502,6 +1530,47 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
             }
             return true;
         };
+        // Scored calls: 32 columns (from c0 on) of the V values that are not
+        // finite, in the tiles of a converter's log that are the item's, added
+        // to acc where the row attends them.  Adding one twice, or looking at a
+        // tile that has none, changes nothing, so a run may hold more than its
+        // tiles: those of other items, or once runs of this item may have left
+        // the log (the converters are three tiles ahead at most) all before.
+        [[maybe_unused]] auto add_logged = [&](volatile const uint32_t* log, const ItemRow& w, uint32_t g0,
+                                               uint32_t ntiles, uint32_t k_begin, int c0) {
+            const uint32_t slot = __ldg(P.slots + w.tok);
+            const float* v0 = P.V + (static_cast<size_t>(slot) * P.slot_ctx * P.n_kv_head + w.head / G) * HD +
+                              hf * HH + c0;
+            const uint32_t n = log[2 * C::LOG];
+#pragma unroll 1
+            for (uint32_t i = 1; i <= n && i <= C::LOG - 4; ++i) {  // newest first
+                const uint32_t last = log[2 * ((n - i) % C::LOG) + 1];
+                uint32_t first = log[2 * ((n - i) % C::LOG)];
+                if (last < g0) break;
+                if (first < g0 || i == C::LOG - 4) first = g0;
+                uint32_t key = k_begin + (first - g0) * BK;
+                uint32_t end = k_begin + (last - g0 < ntiles ? last - g0 + 1 : ntiles) * BK;  // past its keys
+                key = key > w.lo ? key : w.lo;
+                end = end <= w.hi ? end : w.hi + 1;
+#pragma unroll 1
+                for (; key < end; ++key) {
+                    const float4* vr = reinterpret_cast<const float4*>(
+                        v0 + static_cast<size_t>(key) * P.n_kv_head * HD);
+                    auto add = [&](int at, float x) {
+                        if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) acc[at] += x;
+                    };
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 x = vr[c];
+                        const int at = SC ? c0 + 4 * c : 0;
+                        add(at, x.x);
+                        add(at + 1, x.y);
+                        add(at + 2, x.z);
+                        add(at + 3, x.w);
+                    }
+                }
+            }
+        };
         [[maybe_unused]] CapSeries cap_k{};
         if constexpr (SC) cap_k = cap_series(P.rule.cap_in);
         uint32_t d[ND];
@@ -1753,19 +1822,14 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
                 if constexpr (SC) {
                     // the values the tensor core took as 0, for the keys of
                     // this item that the row attends
-                    if (misc[8] != 0 && cur.valid) {
-                        const uint32_t slot = __ldg(P.slots + cur.tok);
-                        const uint32_t k_end = k_begin + ntiles * BK;  // past the item's keys
-                        for (uint32_t key = cur.lo > k_begin ? cur.lo : k_begin;
-                             key <= cur.hi && key < k_end; ++key) {
-                            const float* vr = P.V + ((static_cast<size_t>(slot) * P.slot_ctx + key) *
-                                                         P.n_kv_head + cur.head / G) * HD + hf * HH;
-#pragma unroll
-                            for (int c = 0; c < HH; ++c) {
-                                const float x = vr[c];
-                                if ((__float_as_uint(x) & 0x7F800000u) == 0x7F800000u) acc[c] += x;
-                            }
-                        }
+                    const uint32_t g0 = g - ntiles;  // the item's first tile
+                    // the two converter warps whose dims are in this half
+                    volatile uint32_t* log0 = log_of(NB == 4 ? 2 * hf : hf);
+                    volatile uint32_t* log1 = log_of(NB == 4 ? 2 * hf + 1 : hf + 2);
+                    const bool met = log0[2 * C::LOG + 1] > g0 || log1[2 * C::LOG + 1] > g0;
+                    if (__builtin_expect(met && cur.valid, 0)) {
+                        add_logged(log0, cur, g0, ntiles, k_begin, 0);
+                        add_logged(log1, cur, g0, ntiles, k_begin, NB == 4 ? 32 : 0);
                     }
                     // rows to memory by way of the stage; each lane has the
                     // destinations of the four rows it writes pieces of
