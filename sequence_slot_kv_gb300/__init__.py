@@ -301,45 +301,51 @@ def _raw_stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _rule_array(i, doc):
+    """An array of a Scores: what is assigned to it is what the next call uses."""
+    def put(self, t):
+        self._args = self._args[:i] + (t,) + self._args[i + 1:]
+    return property(lambda self: self._args[i], put, doc=doc)
+
+
 class Scores:
     """A score rule (slotkv_scores): tanh cap, window, per-head slopes of the
     distance bias (float32 [n_head]), the rows' document starts and, in a
-    prefill, prefix ends (int32 [rows]); CUDA tensors, kept referenced."""
+    prefill, prefix ends (int32 [rows]); CUDA tensors, kept referenced.  The
+    arrays may be replaced between calls, each of which checks them."""
 
     def __init__(self, cap=0.0, window=0, slopes=None, doc_start=None, prefix_end=None):
         import torch
         if not 0 <= int(window) < 2 ** 32:
             raise ValueError("window must be 0 .. 2^32 - 1")
-        self.slopes, self.doc_start, self.prefix_end = slopes, doc_start, prefix_end
-        self._arrays = slopes is not None or doc_start is not None or prefix_end is not None
-        self._c = _CScores(cap, int(window), _ptr(slopes, torch.float32, "slopes"),
-                           _ptr(doc_start, torch.int32, "doc_start"),
-                           _ptr(prefix_end, torch.int32, "prefix_end"))
-        self._ref = ctypes.byref(self._c)
+        _ptr(slopes, torch.float32, "slopes")
+        _ptr(doc_start, torch.int32, "doc_start")
+        _ptr(prefix_end, torch.int32, "prefix_end")
+        # as the compiled calls take it
         self._args = (float(cap), int(window), slopes, doc_start, prefix_end)
 
-    @property
-    def cap(self):
-        return self._c.cap
-
-    @property
-    def window(self):
-        return self._c.window
+    cap = property(lambda self: self._args[0], doc="tanh cap, 0: none")
+    window = property(lambda self: self._args[1], doc="keys t with p - t < window, 0: all")
+    slopes = _rule_array(2, "distance slopes [n_head], or None")
+    doc_start = _rule_array(3, "first key of each row's document [rows], or None")
+    prefix_end = _rule_array(4, "end of each row's prefix [rows], or None (prefill)")
 
 
 def _scores(sc, rows, n_head, dev):
-    """The struct pointer of a Scores for a step of ``rows`` rows on device
-    ``dev``; None stays NULL."""
+    """The struct of a Scores, by reference, for a step of ``rows`` rows on
+    device ``dev``; None stays NULL."""
     if sc is None:
         return None
-    if sc._arrays:
-        for name, t, n in (("slopes", sc.slopes, n_head), ("doc_start", sc.doc_start, rows),
-                           ("prefix_end", sc.prefix_end, rows)):
-            if t is not None:
-                if t.shape != (n,):
-                    raise ValueError(f"{name} has shape {_shape(t)}, expected {(n,)}")
-                _on_device(t, dev, name)
-    return sc._ref
+    import torch
+    ptrs = []
+    for name, t, dtype, n in (("slopes", sc.slopes, torch.float32, n_head),
+                              ("doc_start", sc.doc_start, torch.int32, rows),
+                              ("prefix_end", sc.prefix_end, torch.int32, rows)):
+        ptrs.append(_ptr(t, dtype, name))
+        if t is not None and t.shape != (n,):
+            raise ValueError(f"{name} has shape {_shape(t)}, expected {(n,)}")
+        _on_device(t, dev, name)
+    return ctypes.byref(_CScores(sc.cap, sc.window, *ptrs))
 
 
 class SlotKV:
