@@ -564,9 +564,9 @@ class SlotKV:
                 None if scores is None else scores._args, out, eps, scale, _stream_arg(stream)),
                 name):
             return out
-        for name, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
+        for what, t in (("prefix_slots", prefix_slots), ("prefix_lens", prefix_lens)):
             if t is None or t.dim() != 1 or t.shape != positions.shape:
-                raise ValueError(f"{name} must be [B]")
+                raise ValueError(f"{what} must be [B]")
         (B, n_head, aq, ak, av, ap, ai, aqw, akw, af, asn, ao, dev) = _step_addrs(
             self, q, k_new, v_new, positions, slots, out, q_norm_w, k_norm_w, inv_freq, sinks)
         _check(_lib.decode_batch_attn_shared(
