@@ -223,9 +223,11 @@ class _Unlike(Exception):
 
 def _addr(t, dtype, dev, shape):
     """Address of a contiguous tensor of this type and shape on CUDA device
-    ``dev``.  A step's calls come every few microseconds, so the checks of a
-    good argument are a handful of attribute reads; anything else raises
-    _Unlike and is looked at again by _check_step and _ptr for its message."""
+    ``dev``.  Where the compiled calls are not built these checks are part of
+    every step, so those of a good argument are a handful of attribute reads
+    (a scored decode's call takes the host 8.5 us so, 16 with _check_step and
+    _ptr); anything else raises _Unlike and is looked at again by those for its
+    message."""
     if (t.dtype is dtype and t.get_device() == dev and t.shape == shape and
             t.is_contiguous()):
         return t.data_ptr()
@@ -256,7 +258,8 @@ def _step_addrs(kv, q, k_new, v_new, positions, rows_idx, out, q_norm_w, k_norm_
         pass
     B, n_head = _check_step(q, k_new, v_new, positions, rows_idx, out, q_norm_w, k_norm_w,
                             inv_freq, sinks, kv.n_kv_head, kv.head_dim, idx_name)
-    if idx_name != "slots" and (rows_idx.dim() != 2 or int(rows_idx.shape[0]) != B):
+    if idx_name != "slots" and (rows_idx is None or rows_idx.dim() != 2 or
+                                int(rows_idx.shape[0]) != B):
         raise ValueError("block_tables must be [B][max_blocks]")
     for name, t, dt in (("q", q, f), ("k_new", k_new, f), ("v_new", v_new, f),
                         ("positions", positions, u), (idx_name, rows_idx, u),

@@ -28,3 +28,13 @@ def test_a_failing_call_is_named(compiled, monkeypatch):
                        ("decode_batch_attn_shared", step + [h, i, i] + rest)):
         with pytest.raises(skv.SlotKVError, match=name):
             getattr(h, name)(*args, stream=0)
+
+
+def test_a_step_without_block_tables_is_refused(monkeypatch):
+    monkeypatch.setattr(skv, "_call", False)
+    h, i = _Handle(2, 64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="block_tables"):
+        h.decode_batch_attn_paged_scored(torch.zeros(3, 4, 64), torch.zeros(3, 2, 64),
+                                         torch.zeros(3, 2, 64), i, None, torch.ones(64),
+                                         torch.ones(64), torch.ones(32), None, None,
+                                         torch.zeros(3, 4, 64), 1e-6, 0.1)
