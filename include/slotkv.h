@@ -358,11 +358,12 @@ typedef struct {
  * and joins them with one more kernel, so results depend on the batch in the
  * last bits.  A key that a row attends and that is not finite in K makes the
  * row NaN (in V, it has its usual effect).  The prefill's workspace is
- * allocated by the handle's first such call (queries, items, and 128 * 8
- * partial rows per SM), at the size of max_rows and max_n_head: make one
- * before capturing into a graph (a call under capture that would have to
- * allocate returns SLOTKV_ERR_STATE and captures nothing).  Head dim 256 runs
- * the scored decode kernel once per token.
+ * allocated by the handle's first such call, at the size of max_rows and
+ * max_n_head (queries, items, and the partial results of splits: 64 per row
+ * and head, at most 128 * 8 per SM): make one before capturing into a graph
+ * (a call under capture that would have to allocate returns SLOTKV_ERR_STATE
+ * and captures nothing).  Head dim 256 runs the scored decode kernel once per
+ * token.
  */
 int decode_batch_attn_scored(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
                              const float* k_new, const float* v_new, const uint32_t* positions,
@@ -414,11 +415,12 @@ int prefill_batch_attn_scored(slotkv_t handle, uint32_t n_tok, uint32_t n_head, 
  * >= its n_slots.  Flags are raised on `handle`.
  *
  * Head dims 64 and 128 (SLOTKV_ERR_UNSUPPORTED otherwise).  The prefix pass
- * keeps a workspace in `handle`, allocated by the first call as
- * prefill_batch_attn_scored's is (the same rule for captures), with a partial
- * result per row and head besides.  Other errors as decode_batch_attn, and
- * SLOTKV_ERR_ARG for a prefix handle of another shape, SLOTKV_ERR_STATE for
- * one that is not allocated or on another device.
+ * uses prefill_batch_attn_scored's workspace in `handle`, and a buffer of
+ * partial results of its own where max_rows * max_n_head passes what splits
+ * need; the first shared call allocates what is not there (the same rule for
+ * captures).  Other errors as decode_batch_attn, and SLOTKV_ERR_ARG for a
+ * prefix handle of another shape, SLOTKV_ERR_STATE for one that is not
+ * allocated or on another device.
  */
 int decode_batch_attn_shared(slotkv_t handle, uint32_t B, uint32_t n_head, const float* q,
                              const float* k_new, const float* v_new, const uint32_t* positions,

@@ -221,8 +221,8 @@ int launch_scored_prefill_hd128(int G, const ScoredPrefillParams& p, const CUten
 // make by splitting; a call with more tiles than kSplitBelow items per SM is
 // never split.
 constexpr uint32_t kSplitBelow = 2, kSplitMost = 8, kMaxSplits = 64;
-// rows (tokens) of partials a call can need beyond one per row of a shared
-// call: 128 query rows per split item
+// head rows of partials that splits can need, however many rows a call has: 128
+// query rows per split item
 inline size_t partial_head_rows(uint32_t sms) { return (size_t)128 * kSplitMost * sms; }
 
 // Keys per pipeline stage of the tensor-core prefill.

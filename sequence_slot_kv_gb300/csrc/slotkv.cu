@@ -102,11 +102,12 @@ struct slotkv_s {
     size_t pf_q_elems = 0, pf_tok = 0;
     // scored prefill and shared decode: a workspace of its own, allocated by
     // the first such call at the size of the largest one the handle allows
-    // (so a captured call's pointers stay good until slot_kv_free); the
-    // splits' partials of a prefill and those of a prefix pass apart
+    // (so a captured call's pointers stay good until slot_kv_free).  Calls on a
+    // handle are ordered, so both kinds use the first buffer of partials, unless
+    // a shared call may leave more of them than a prefill: then it has the second
     float* sc_q = nullptr;            // [max_rows][max_n_head][hd] rotated q
     uint32_t* sc_idx = nullptr;       // rec, tiles, tile_of, tile_lo, list, plan
-    float* sc_part[2] = {};           // (m, l) then acc, each partial_rows() head rows
+    float* sc_part[2] = {};           // acc then (m, l), each of partial_rows() head rows
     uint32_t* map_scratch = nullptr;  // slot_kv_extend_tables: CTA counter, new head
     std::vector<slotkv_host_call_s*> calls;  // prepared host calls on this handle
     cudaStream_t copy_stream = nullptr;      // their enqueued input copies (created on demand)
@@ -497,11 +498,13 @@ int first_use(float** p, size_t floats, cudaStream_t stream, const char* what) {
 
 uint32_t sm_total(const slotkv_s* h) { return (uint32_t)(h->sm_count > 0 ? h->sm_count : 1); }
 
-// Head rows of partials: what splits can need, and one per row and head of a
-// shared call that is not split.
+// Head rows of partials a call can leave: what splits can need, or one per row
+// and head of a shared call that is not split.
 size_t partial_rows(const slotkv_s* h, bool shared) {
-    return slotkv::partial_head_rows(sm_total(h)) +
-           (shared ? (size_t)h->max_rows * h->max_n_head : 0);
+    const size_t each = (size_t)h->max_rows * h->max_n_head;
+    const size_t split =
+        std::min(slotkv::partial_head_rows(sm_total(h)), slotkv::kMaxSplits * each);
+    return shared ? std::max(split, each) : split;
 }
 
 // Workspace of the tensor-core kernels of a scored prefill (shared false) or
@@ -511,12 +514,13 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     const size_t R = h->max_rows;
     const size_t list = 8 * (R + (size_t)slotkv::kSplitMost * sm_total(h));
     const size_t pr = partial_rows(h, shared);
+    float** part = &h->sc_part[pr > partial_rows(h, false) ? 1 : 0];
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, stream, "scored workspace (q)");
     if (rc == SLOTKV_OK)
         rc = first_use(reinterpret_cast<float**>(&h->sc_idx), 14 * R + list + 4, stream,
                        "scored workspace (items)");
     if (rc == SLOTKV_OK)
-        rc = first_use(&h->sc_part[shared ? 1 : 0], pr * (2 + h->head_dim), stream,
+        rc = first_use(part, pr * (2 + h->head_dim), stream,
                        "scored workspace (partials)");
     if (rc != SLOTKV_OK) return rc;
     P.q_rot = h->sc_q;
@@ -530,7 +534,7 @@ int scored_workspace(slotkv_s* h, bool shared, slotkv::ScoredPrefillParams& P,
     P.tile_lo = P.tile_of + R;
     P.sms = sm_total(h);
     // acc first: its rows are read and written 16 bytes at a time
-    P.part.acc = h->sc_part[shared ? 1 : 0];
+    P.part.acc = *part;
     P.part.ml = P.part.acc + pr * h->head_dim;
     return SLOTKV_OK;
 }
