@@ -2,7 +2,8 @@
 
 The translation units compile in parallel (one per head dim for the decode
 and the tensor-core prefill kernels and their scored forms, the request-length
-kernels, the host side, the allocation-free entry point), then link into ``sequence_slot_kv_gb300/libslotkv.so``.
+kernels, the host side, the allocation-free entry point), then link into
+``sequence_slot_kv_gb300/libslotkv.so``.
 """
 import importlib.util
 import os
@@ -58,6 +59,21 @@ def _call_flags():
     return cflags, ldflags
 
 
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
+def _call_stamp(flags):
+    """What the compiled calls are made for beside their own sources: the torch
+    and the Python whose headers they were compiled with."""
+    spec = importlib.util.find_spec("torch")
+    torch_version = _read(os.path.join(spec.submodule_search_locations[0], "version.py"))
+    return repr((flags, torch_version, sys.version))
+
+
 def build(force=False, verbose_ptxas=False):
     os.makedirs(OBJDIR, exist_ok=True)
     header = os.path.join(INCLUDE, "slotkv.h")
@@ -75,9 +91,17 @@ def build(force=False, verbose_ptxas=False):
                                                 stderr=subprocess.STDOUT, text=True)))
     flags = _call_flags()
     call_src, call_obj = os.path.join(CSRC, "call.cpp"), os.path.join(OBJDIR, "call.o")
+    stamp_file = os.path.join(OBJDIR, "call.stamp")
+    call_stale = False
     if flags is None:
         print("no headers of Python or torch: the compiled calls are not built")
-    elif force or _stale(call_obj, [call_src, header]):
+        if os.path.exists(CALL):  # made for other headers, maybe other C declarations
+            os.remove(CALL)
+    else:
+        stamp = _call_stamp(flags)
+        call_stale = (force or _stale(call_obj, [call_src, header]) or
+                      _read(stamp_file) != stamp)
+    if call_stale:
         procs.append(("call.cpp", subprocess.Popen(
             ["g++"] + flags[0] + ["-c", call_src, "-o", call_obj], stdout=subprocess.PIPE,
             stderr=subprocess.STDOUT, text=True)))
@@ -95,8 +119,10 @@ def build(force=False, verbose_ptxas=False):
         cmd = ["nvcc", "-shared", "-o", LIB] + objs + ARCH + [
             "-cudart", "shared", "-Xlinker", "-rpath=" + cuda_lib]
         subprocess.run(cmd, check=True)
-    if flags is not None and (force or _stale(CALL, [call_obj, LIB])):
+    if flags is not None and (call_stale or _stale(CALL, [call_obj, LIB])):
         subprocess.run(["g++", "-shared", "-o", CALL, call_obj] + flags[1], check=True)
+        with open(stamp_file, "w") as f:
+            f.write(stamp)
     return LIB
 
 
