@@ -26,7 +26,8 @@
 //       - warp 8 (producer): claims items and streams each key tile's K
 //         and then V (BK = 64 keys x hd, 128-byte swizzled boxes of 32
 //         floats) with TMA into a ring of half-stage slots (one operand's
-//         hi and lo buffers each: 3 slots for hd 128, 6 for hd 64);
+//         hi and lo buffers each: 3 slots for hd 128, 6 for hd 64 and for
+//         scored calls);
 //       - warps 10-13 (converters): write each landed K tile's lo part
 //         beside it (the tensor core reads a TF32 operand's f32 bits with the
 //         low 13 mantissa bits ignored, so the landed tile is its own hi
@@ -96,6 +97,14 @@
 //     as it is (1.01 ms at head dim 64, 1.28 at 128), one in every 997th key
 //     adds 0.1 to 0.2 ms; a history of nothing else takes 0.5 to 0.7 us a key.
 //     The log costs the calls without any 0.6 to 1.3 %.
+// Where they hold fewer bits than f32: the low parts of Q, K, V and P are cut
+// to TF32 by the tensor core and the product of two low parts is left out.  K
+// and V are split by truncation (K's landed tile is then its own high part, and
+// is not written again), so their low parts reach 2^-10 of the value and each
+// of the two losses 2^-20 of a product; the tests' bounds count those.
+// Exponentials are ex2.approx.ftz and the cap divides by __fdividef, both a few
+// ulp.  Against 64 bits the listed cases are off by 4e-7 to 7e-7 of the largest
+// value, plain f32 forms by 2e-7 to 3e-6.
 // What bounds them, measured: head dim 128, 256 rows on a prefix of 32700 keys,
 // 497 us, 2100 cycles per tile of 32 keys of which the tensor core needs 1800
 // (three TF32 products: 85 % of its rate); head dim 64, 517 tokens on 15.8
@@ -119,7 +128,7 @@ struct PCfg {
     static constexpr int BLK = BK * 128;        // one column block: BK rows x 128 B
     static constexpr int BUF = NB * BLK;        // one operand buffer, [BK][HD] f32
     static constexpr int SLOT = 2 * BUF;        // half-stage slot: hi | lo of K or V
-    static constexpr int NSLOT = (192 * 1024) / SLOT;  // 3 (hd 128) or 6 (hd 64)
+    static constexpr int NSLOT = (192 * 1024) / SLOT;  // 6; plain calls at hd 128: 3
     // V transposed: KB column blocks of 32 keys, each [HD rows][128 B]; the
     // 32 x 32 sub-block (key block kb, dim block db) lands at kb * VT_BLK +
     // db * 4096 (TMA put it at db * BLK + kb * 4096)
@@ -159,16 +168,13 @@ struct PCfg {
     static constexpr int OFF_DESC = NSLOT * SLOT;
     static constexpr int OFF_META = OFF_DESC + 2 * 32;
     static constexpr int OFF_BAR = OFF_META + NSLOT * 16;
-    // full[NLAND], conv[NLAND], empty[NSLOT], s_full[2], p_ready[2],
-    // pv_done[2], q_ready, item_full[2], item_free[2], drain.  Half-tile h's
-    // full and conv barriers: h % NSLOT in plain calls, whose converters see
-    // every half-tile; h % 6 in scored calls, so that a barrier belongs to K
-    // half-tiles or to V ones alone and the converters of one kind see every
-    // phase of theirs (with three slots a slot is K's and V's by turns, and
-    // copies land in any order)
-    static constexpr int NLAND = 6;
-    static_assert(NSLOT <= NLAND && NLAND % 2 == 0, "barriers of landed half-tiles");
-    static constexpr int NBAR = 2 * NLAND + NSLOT + 12;
+    // full[NSLOT], conv[NSLOT], empty[NSLOT], s_full[2], p_ready[2],
+    // pv_done[2], q_ready, item_full[2], item_free[2], drain
+    static constexpr int NBAR = 3 * NSLOT + 12;
+    // (scored calls' converters see one kind of half-tile each: with an even
+    // number of slots a slot, and its barriers, is always K's or always V's,
+    // and they see every phase of theirs)
+    static_assert(!SC || NSLOT % 2 == 0, "a slot is of one kind");
     static constexpr int OFF_TSLOT = OFF_BAR + NBAR * 8;
     static constexpr int OFF_MISC = OFF_TSLOT + 16;
     // misc[0]: abort; misc[2 + w]: converter warp w's stop flag
@@ -830,11 +836,10 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
     };
     const uint32_t ring = smem_addr(smem);
     const uint32_t bar0 = smem_addr(smem + C::OFF_BAR);
-    constexpr uint32_t NL = SC ? C::NLAND : NSLOT;
-    const uint32_t FULL = bar0, CONV = bar0 + 8 * C::NLAND, EMPTY = bar0 + 16 * C::NLAND;
-    auto full_bar = [&](uint32_t h) { return FULL + 8 * (h % NL); };
-    auto conv_bar = [&](uint32_t h) { return CONV + 8 * (h % NL); };
-    auto land_phase = [](uint32_t h) { return (h / NL) & 1u; };
+    const uint32_t FULL = bar0, CONV = FULL + 8 * NSLOT, EMPTY = CONV + 8 * NSLOT;
+    auto full_bar = [&](uint32_t h) { return FULL + 8 * (h % NSLOT); };
+    auto conv_bar = [&](uint32_t h) { return CONV + 8 * (h % NSLOT); };
+    auto land_phase = [](uint32_t h) { return (h / NSLOT) & 1u; };
     const uint32_t SFULL = EMPTY + 8 * NSLOT, PREADY = SFULL + 16;
     const uint32_t PVDONE = PREADY + 16, QREADY = PVDONE + 16, IFULL = QREADY + 8;
     const uint32_t IFREE = IFULL + 16, DRAIN = IFREE + 16;
@@ -843,11 +848,9 @@ __global__ void __launch_bounds__(SC ? PCfg<HD, G, SC>::THREADS_SC : PCfg<HD, G>
     auto slot_lo = [&](uint32_t sl) { return ring + sl * C::SLOT + C::BUF; };
 
     if (tid == 0) {
-        for (int i = 0; i < C::NLAND; ++i) {
+        for (int i = 0; i < NSLOT; ++i) {
             mbar_init(FULL + 8 * i, 1);
             mbar_init(CONV + 8 * i, C::NCONV);
-        }
-        for (int i = 0; i < NSLOT; ++i) {
             mbar_init(EMPTY + 8 * i, 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -2025,10 +2028,11 @@ int launch_prefill_one(const prefill_params_t<SC>& p, const CUtensorMap& tmK, co
         if (p.shared.lens) groups = prep_q_groups(p.n_head);
     const uint32_t warps = p.n_tok * groups;
     // the plan (one CTA) first, then prep beside it as its programmatic
-    // dependent; the attention kernel, launched in stream order, waits for
-    // both.  Prep starts only once the plan runs, hence after the previous
-    // call's attention kernel has finished reading the rows and q workspace
-    // that prep overwrites.
+    // dependent; the attention kernel waits for both (a plain call's by stream
+    // order, a scored call's as a programmatic dependent of prep, whose last
+    // CTA ends after the plan).  Prep starts only once the plan runs, hence
+    // after the previous call's attention kernel has finished reading the rows
+    // and q workspace that prep overwrites.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -454,7 +454,9 @@ int launch(slotkv_s* h, uint32_t B, uint32_t n_head, const float* q, const float
 // ------------------------------------------------------------ scored calls
 int check_scores(const slotkv_scores* sc, bool prefill) {
     if (!sc) return SLOTKV_OK;
-    // (the kernels use powers of the cap's reciprocal: they stay normal)
+    // (the kernels use powers of the cap's reciprocal up to the sixth.  At 1e6
+    // the sixth's coefficient, -6.0e-39, is subnormal and has 22 bits, enough for
+    // a term of at most 2^-22 of the score; past 1e6 it would have fewer)
     if (!(sc->cap >= 0.f) || sc->cap > 1e6f || (sc->cap > 0.f && sc->cap < 1e-6f))
         return fail(SLOTKV_ERR_ARG, "scores: cap=%g must be 0 or in 1e-6 .. 1e6",
                     (double)sc->cap);
