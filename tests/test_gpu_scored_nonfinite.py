@@ -80,8 +80,8 @@ def test_one_value_beside_long_sequences(hd, bad):
 
 @pytest.mark.parametrize("hd", [64, 128])
 def test_values_at_both_ends_of_a_long_history(hd):
-    """More key tiles than the kernel has marks for them, values in two tiles
-    that share a mark, and documents that begin after none, one or both."""
+    """Values in the first and the last tiles of a history of 1024 tiles, and
+    documents that begin after none, one or all of them."""
     n_kv, G, n = 8, 1, 39 * 128
     bk = 32 if hd == 128 else 64
     far = 1024 * bk
@@ -102,6 +102,34 @@ def test_values_at_both_ends_of_a_long_history(hd):
     want, tols = wanted(L, q, pos, [0] * n, rows, doc=doc)
     assert bool(torch.isnan(want[0]).any()) and bool(torch.isinf(want[0]).any())
     assert bool(torch.isfinite(want[3]).all())
+    check(out[rows], want, tols, "prefill")
+    L.kv.free()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_values_in_a_hundred_places_of_a_long_history(hd):
+    """More places, ten tiles apart, than the kernel keeps note of for an item:
+    NaN in the first ten, infinities in the others, documents that begin before,
+    between and after them."""
+    n_kv, G, n = 8, 1, 39 * 128
+    apart = 10 * (32 if hd == 128 else 64)
+    ctx = 100 * apart + n + 100
+    L = Layer(1, ctx, n_kv, G, hd, n, seed=hd + 5)
+    keys = [apart * j + j for j in range(100)]
+    for j, key in enumerate(keys):
+        L.V[0, key, :, j % (32 if j < 60 else 16)] = math.nan if j < 10 else math.inf
+    pos = list(range(ctx - n, ctx))
+    starts = [0, keys[9], keys[9] + 1, keys[70], keys[99], keys[99] + 1]
+    doc = [starts[b % 6] for b in range(n)]
+    q, k, v = L.step(n)
+    out = torch.full((n, L.n_head, hd), math.nan, device="cuda")
+    L.kv.prefill_batch_attn_scored(q, k, v, i32(pos), i32([0] * n), *L.params(),
+                                   Scores(doc_start=i32(doc)), out, EPS, L.scale)
+    assert L.kv.get_status() == 0
+    rows = [*range(6), *range(2004, 2010), *range(n - 6, n)]
+    want, tols = wanted(L, q, pos, [0] * n, rows, doc=doc)
+    assert [int((~torch.isfinite(w[0])).sum()) for w in want[:6]] == [32, 32, 32, 16, 1, 0]
+    assert [int(torch.isnan(w[0]).sum()) for w in want[:6]] == [10, 1, 0, 0, 0, 0]
     check(out[rows], want, tols, "prefill")
     L.kv.free()
 
