@@ -84,7 +84,7 @@ def measured_traffic(workload):
 # prefill workload of a geometry (ncu one-pass counters, the mean over the
 # full-size calls' launches), keyed by code_hash of prefill_tc.cuh; reported
 # only while the kernel is the one measured.
-MEASURED_PREFILL_TRAFFIC = {"f28075a46c9a73c5": {"mid": 247_365_333, "sinks": 170_332_331}}
+MEASURED_PREFILL_TRAFFIC = {"38dce91f4de06ad5": {"mid": 247_479_979, "sinks": 170_464_000}}
 
 
 def prefill_source_hash():

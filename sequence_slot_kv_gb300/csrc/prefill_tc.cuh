@@ -106,9 +106,9 @@
 // ulp.  Against 64 bits the listed cases are off by 4e-7 to 7e-7 of the largest
 // value, plain f32 forms by 2e-7 to 3e-6.
 // What bounds them, measured: head dim 128, 256 rows on a prefix of 32700 keys,
-// 497 us, 2100 cycles per tile of 32 keys of which the tensor core needs 1800
+// 502 us, 2120 cycles per tile of 32 keys of which the tensor core needs 1800
 // (three TF32 products: 85 % of its rate); head dim 64, 517 tokens on 15.8
-// thousand keys, 561 us, 2340 cycles per tile of 64 keys against 1800, the
+// thousand keys, 568 us, 2370 cycles per tile of 64 keys against 1800, the
 // rest the softmax's latencies.  64-key tiles with one score buffer at head
 // dim 128 took 636 us, a single thread issuing 33 % longer.
 #pragma once
