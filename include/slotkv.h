@@ -481,6 +481,172 @@ int slot_kv_extend_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
                           uint32_t* head_out, slotkv_stream_t stream);
 
 /*
+ * tree_batch_attn, tree_batch_attn_paged -- attention of trees of drafted
+ * tokens (speculative decoding): every request brings a tree of candidate
+ * tokens, all of which attend its history and their own ancestors in one
+ * call, so that one step verifies several continuations.
+ *
+ * Request r's nodes are the rows starts[r] .. starts[r+1] - 1 of q, k_new,
+ * v_new, parents and out; node i of n (row starts[r] + i) has the parent node
+ * parents[starts[r] + i] < i of the same request, or 0xFFFFFFFF: it follows
+ * the history (several may; the last accepted token, whose K and V are not in
+ * the cache yet, is usually node 0 and the only one).  With depth(i) the
+ * number of its ancestors:
+ *   1. q' and k' as in decode_batch_attn, at position past[r] + depth(i);
+ *   2. node i's k' and v go to place past[r] + i of the request's slot: the
+ *      nodes stand in tree order, not by position (slot_kv_keep_path puts an
+ *      accepted path in order);
+ *   3. out = decode_batch_attn's attention over the keys at places 0 ..
+ *      past[r] - 1 (positions the same), the node's ancestors and itself.
+ *
+ *   n_req         requests, 0 .. max_rows; n_tok: rows of the tensors, 0 ..
+ *                 max_rows.  Rows that belong to no request are left alone.
+ *   slots         device u32[n_req], the requests' slots, pairwise distinct;
+ *                 or block_tables device u32[n_req][bt_stride] as in
+ *                 decode_batch_attn_paged: place t in block
+ *                 block_tables[r*bt_stride + t/block_size], offset
+ *                 t % block_size; blocks that hold a node's place belong to
+ *                 that request alone, the others may be shared.
+ *   past          device u32[n_req]: keys already in the cache.
+ *   starts        device u32[n_req + 1], not decreasing (slot_kv_token_map
+ *                 writes such an array).
+ *   parents       device u32[n_tok].
+ *   scores        a score rule, or NULL.  doc_start is u32[n_req] here, one
+ *                 per request, and positions count as above (a node is masked
+ *                 by its position, not its place); prefix_end is refused.
+ * The other arguments, their alignment, the options of slot_kv_set_options
+ * and the host-side errors are those of decode_batch_attn; for the paged call
+ * the block size has to be a multiple of 4096/head_dim
+ * (SLOTKV_ERR_UNSUPPORTED).
+ *
+ * Skipped with SLOTKV_DEV_RANGE, nothing of them written: a request with
+ * nodes whose slot is >= n_slots, whose past[r] + n passes slot_ctx (bt_stride
+ * * block_size), one of whose used table entries is >= n_blocks, with more than
+ * SLOTKV_MAX_TREE nodes, with starts that decrease or pass n_tok, or with a
+ * parent that is neither below its node nor 0xFFFFFFFF.  Keys that a row does
+ * not attend never affect it, whatever they hold (another branch's or another
+ * sequence's infinities and NaN included); a key that a row attends and that
+ * is not finite in K makes the row NaN.  A row whose mask leaves nothing gets
+ * zeros.  The results agree with one decode step per node in f32 rounding;
+ * they may differ in the last bits between batches.
+ *
+ * The workspace is allocated by the handle's first such call, at the size of
+ * max_rows and max_n_head: make one before capturing into a graph (a call
+ * under capture that would have to allocate returns SLOTKV_ERR_STATE).
+ */
+#define SLOTKV_MAX_TREE 256u
+int tree_batch_attn(slotkv_t handle, uint32_t n_req, uint32_t n_tok, uint32_t n_head,
+                    const float* q, const float* k_new, const float* v_new,
+                    const uint32_t* slots, const uint32_t* past, const uint32_t* starts,
+                    const uint32_t* parents, const float* q_norm_w, const float* k_norm_w,
+                    const float* inv_freq, const float* sinks, const slotkv_scores* scores,
+                    float* out, float eps, float scale, slotkv_stream_t stream);
+int tree_batch_attn_paged(slotkv_t handle, uint32_t n_req, uint32_t n_tok, uint32_t n_head,
+                          const float* q, const float* k_new, const float* v_new,
+                          const uint32_t* block_tables, uint32_t bt_stride,
+                          const uint32_t* past, const uint32_t* starts,
+                          const uint32_t* parents, const float* q_norm_w,
+                          const float* k_norm_w, const float* inv_freq, const float* sinks,
+                          const slotkv_scores* scores, float* out, float eps, float scale,
+                          slotkv_stream_t stream);
+
+/*
+ * slot_kv_keep_path, slot_kv_keep_path_paged -- the rows of an accepted path
+ * put in order after tree_batch_attn: K and V at place past[r] + k of request
+ * r take those of place past[r] + path[starts[r] + k], for k < n_keep[r].  The
+ * caller then advances past[r] by n_keep[r] (slot_kv_advance_positions for a
+ * path of one length); the places of nodes that were not kept are stale.
+ *   path    device u32[n_tok]: the path's nodes from path[starts[r]] on,
+ *           strictly increasing, below the request's number of nodes.
+ *   n_keep  device u32[n_req], 0: the request is left alone.
+ * The others as in tree_batch_attn (any block size).  A request that keeps
+ * nodes and is out of range as there, or whose path is not strictly
+ * increasing or leaves its nodes, is left alone with SLOTKV_DEV_RANGE.  A
+ * row's bits are copied.  Asynchronous, one kernel; errors SLOTKV_ERR_ARG
+ * (NULL or misaligned pointer, n_req > max_rows, bt_stride = 0),
+ * SLOTKV_ERR_STATE, SLOTKV_ERR_CUDA.
+ */
+int slot_kv_keep_path(slotkv_t handle, uint32_t n_req, uint32_t n_tok, const uint32_t* slots,
+                      const uint32_t* past, const uint32_t* starts, const uint32_t* n_keep,
+                      const uint32_t* path, slotkv_stream_t stream);
+int slot_kv_keep_path_paged(slotkv_t handle, uint32_t n_req, uint32_t n_tok,
+                            const uint32_t* block_tables, uint32_t bt_stride,
+                            const uint32_t* past, const uint32_t* starts,
+                            const uint32_t* n_keep, const uint32_t* path,
+                            slotkv_stream_t stream);
+
+/*
+ * Pages of a pool, on the device, beside slot_kv_extend_tables: the handle is
+ * the pool (slot_ctx its block size bs, n_slots its number of blocks).
+ *   free_blocks, head  the free list of slot_kv_extend_tables, a stack: ids
+ *                 are taken from free_blocks[head[0]] on and given back below
+ *                 it, so a list of n_blocks entries always has room.
+ *   shares        device u32[n_blocks]: how many table entries name the block
+ *                 beyond the first (0: one, or none).  Zeroed once by the
+ *                 caller; slot_kv_extend_tables needs no change to it.
+ * A table row of past[r] keys uses its first ceil(past[r] / bs) entries.  The
+ * calls are asynchronous; errors as slot_kv_extend_tables.  Where head_out is
+ * given it may be head.  An id taken from the caller's arrays that is >=
+ * n_blocks is never used as an address: it raises SLOTKV_DEV_RANGE.
+ *
+ * slot_kv_fork_tables -- n_fork new tables (samples, beams), fork i from row
+ * src[i] < n_rows of block_tables with past[src[i]] keys: the full blocks are
+ * shared (out_tables' row i takes the entries, their shares grow by one), and
+ * of a partial last block the keys in use are copied into the next id of the
+ * free list, so that both rows can go on writing.  Entries past them are left
+ * as they are.  out_tables (u32[n_fork][bt_stride]) must not overlap
+ * block_tables.  Skipped with SLOTKV_DEV_RANGE, its row left alone: a fork
+ * with src[i] >= n_rows or more blocks than bt_stride, and one that needs a
+ * block when the free list has run out (later ones that need none go on).
+ * An entry >= n_blocks is copied as it stands.  n_rows <= and n_fork <=
+ * SLOTKV_MAX_REQUESTS.  head_out receives head[0] plus the ids taken.
+ */
+int slot_kv_fork_tables(slotkv_t handle, uint32_t n_fork, const uint32_t* src, uint32_t n_rows,
+                        const uint32_t* past, const uint32_t* block_tables, uint32_t bt_stride,
+                        uint32_t* out_tables, uint32_t* shares, const uint32_t* free_blocks,
+                        uint32_t n_free, const uint32_t* head, uint32_t* head_out,
+                        slotkv_stream_t stream);
+
+/*
+ * slot_kv_free_tables -- rows that end, or go back to their first keep[r]
+ * keys: every entry from ceil(keep[r] / bs) to ceil(past[r] / bs) - 1 gives up
+ * its block.  A block's share count falls by one for each, and one that has
+ * nobody left goes back on the free list.  The k-th of the F blocks that do,
+ * in the order of their first entries given up (request by request), is
+ * written to free_blocks[head[0] - F + k]; head_out receives head[0] - F.
+ * The tables are left as they are.
+ *   keep    device u32[n_req], or NULL: 0.
+ *   shares  or NULL for a pool without shared blocks (every entry then goes
+ *           back on the list).
+ * A request with more blocks than bt_stride gives up nothing, an entry >=
+ * n_blocks nothing either; a block given up more often than it was held goes
+ * back once; of more blocks than the list has room for below head the first
+ * are lost.  Each raises SLOTKV_DEV_RANGE.  n_req * bt_stride <= 2^30.
+ */
+int slot_kv_free_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
+                        const uint32_t* keep, const uint32_t* block_tables, uint32_t bt_stride,
+                        uint32_t* shares, uint32_t* free_blocks, uint32_t n_free,
+                        const uint32_t* head, uint32_t* head_out, slotkv_stream_t stream);
+
+/*
+ * slot_kv_compact_pool -- the L blocks in use (those that a used table entry
+ * names) moved to the ids 0 .. L - 1: of the ids in use, those >= L move, in
+ * order, to the ids below L that are free, in order; K, V, the table entries
+ * and the share counts follow (share counts from L on become 0).  The free
+ * list becomes L .. n_blocks - 1 in order, its last entries, and head[0]
+ * points at its first (a list of fewer entries takes the first ids and raises
+ * SLOTKV_DEV_RANGE).  Every block in use has to be named in block_tables:
+ * others count as free.  shares may be NULL.  A request with more blocks than
+ * bt_stride counts with all its entries, an entry >= n_blocks is left as it
+ * is; each raises SLOTKV_DEV_RANGE.  n_req * bt_stride <= 2^30.  The first
+ * call allocates a workspace: make one before capturing into a graph.
+ */
+int slot_kv_compact_pool(slotkv_t handle, uint32_t n_req, const uint32_t* past,
+                         uint32_t* block_tables, uint32_t bt_stride, uint32_t* shares,
+                         uint32_t* free_blocks, uint32_t n_free, uint32_t* head,
+                         slotkv_stream_t stream);
+
+/*
  * decode_batch_attn_host -- decode_batch_attn for callers whose per-step
  * inputs and output live in host memory.  q, k_new, v_new, positions, slots
  * and out are HOST pointers with the layouts above; q_norm_w, k_norm_w,

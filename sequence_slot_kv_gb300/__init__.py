@@ -17,7 +17,10 @@ host-buffer form ``decode_batch_attn_paged_host``, the allocation-free
 ``decode_batch_attn_scored``, ``decode_batch_attn_paged_scored``,
 ``prefill_batch_attn_scored``) and over shared prefixes
 (``decode_batch_attn_shared``), index arrays from request lengths
-(``slot_kv_token_map``, ``slot_kv_extend_tables``), multi-step support
+(``slot_kv_token_map``, ``slot_kv_extend_tables``), trees of drafted tokens
+(``tree_batch_attn``, ``tree_batch_attn_paged``, ``slot_kv_keep_path``,
+``slot_kv_keep_path_paged``), a pool's pages (``slot_kv_fork_tables``,
+``slot_kv_free_tables``, ``slot_kv_compact_pool``), multi-step support
 (``slot_kv_advance_positions``), and control (``slot_kv_get_status``,
 ``slot_kv_set_split``, ``slot_kv_set_options``, ``slot_kv_call_shape``).
 ``SlotKV`` wraps a handle.
@@ -32,7 +35,9 @@ __all__ = [
     "decode_batch_attn_paged", "decode_batch_attn_paged_host", "decode_batch_attn_noalloc",
     "Scores", "decode_batch_attn_scored", "decode_batch_attn_paged_scored",
     "prefill_batch_attn_scored", "decode_batch_attn_shared", "slot_kv_token_map",
-    "slot_kv_extend_tables", "slot_kv_advance_positions",
+    "slot_kv_extend_tables", "tree_batch_attn", "tree_batch_attn_paged", "slot_kv_keep_path",
+    "slot_kv_keep_path_paged", "slot_kv_fork_tables", "slot_kv_free_tables",
+    "slot_kv_compact_pool", "MAX_TREE", "slot_kv_advance_positions",
     "slot_kv_get_status", "slot_kv_set_split", "HostCall", "LIB_PATH", "EXPORTS", "DEV_RANGE",
     "DEV_TIMEOUT", "OPT_VNORM", "OPT_NORM_PLUS_ONE", "OPT_TEST_STALL",
 ]
@@ -44,6 +49,7 @@ OPT_VNORM = 1
 OPT_NORM_PLUS_ONE = 2
 OPT_TEST_STALL = 0x80000000
 PREFILL_HOST_MAX_PARTS = 8  # SLOTKV_PREFILL_HOST_MAX_PARTS
+MAX_TREE = 256  # SLOTKV_MAX_TREE
 SIZE_MAX = ctypes.c_size_t(-1).value
 
 _u32, _f32, _vp, _int = ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
@@ -87,6 +93,15 @@ EXPORTS = {
                                  [_SCP, _vp, _f32, _f32, _vp], _int),
     "slot_kv_token_map": ([_vp, _u32, _vp, _vp, _vp, _u32, _vp, _vp, _vp, _vp], _int),
     "slot_kv_extend_tables": ([_vp, _u32, _vp, _vp, _vp, _u32, _vp, _u32, _vp, _vp, _vp], _int),
+    "tree_batch_attn": ([_vp, _u32, _u32, _u32] + [_vp] * 11 + [_SCP, _vp, _f32, _f32, _vp], _int),
+    "tree_batch_attn_paged": ([_vp, _u32, _u32, _u32] + [_vp] * 4 + [_u32] + [_vp] * 7 +
+                              [_SCP, _vp, _f32, _f32, _vp], _int),
+    "slot_kv_keep_path": ([_vp, _u32, _u32] + [_vp] * 6, _int),
+    "slot_kv_keep_path_paged": ([_vp, _u32, _u32, _vp, _u32] + [_vp] * 5, _int),
+    "slot_kv_fork_tables": ([_vp, _u32, _vp, _u32, _vp, _vp, _u32, _vp, _vp, _vp, _u32, _vp, _vp,
+                             _vp], _int),
+    "slot_kv_free_tables": ([_vp, _u32, _vp, _vp, _vp, _u32, _vp, _vp, _u32, _vp, _vp, _vp], _int),
+    "slot_kv_compact_pool": ([_vp, _u32, _vp, _vp, _u32, _vp, _vp, _u32, _vp, _vp], _int),
     "slot_kv_get_status": ([_vp, _vp, ctypes.POINTER(_u32)], _int),
     "slot_kv_set_split": ([_vp, _u32, _u32], _int),
     "slot_kv_call_shape": ([_vp, _u32, _u32, _u32, ctypes.POINTER(_u32), ctypes.POINTER(_u32),
@@ -268,6 +283,36 @@ def _step_addrs(kv, q, k_new, v_new, positions, rows_idx, out, q_norm_w, k_norm_
         _ptr(t, dt, name)
         _on_device(t, dev, name)
     raise ValueError("the step's tensors cannot be used")
+
+
+def _ints(dev, **want):
+    """Addresses of int32 tensors on CUDA device ``dev``, each given as name=(tensor,
+    shape); a tensor that is None stays NULL."""
+    import torch
+    for name, (t, shape) in want.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {_shape(t)}, expected {shape}")
+    return [None if t is None else _int_addr(t, dev, name) for name, (t, _) in want.items()]
+
+
+def _need(**tensors):
+    """Refuses a required tensor that is missing, or one of another rank: name=(tensor, rank)."""
+    for name, (t, dims) in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+        if not hasattr(t, "dim"):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+
+
+def _device():
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
 
 
 def _on_device(t, dev, what):
@@ -638,6 +683,157 @@ class SlotKV:
             _raw_stream(stream, dev)), "slot_kv_extend_tables")
         return block_tables, head_out
 
+    def tree_batch_attn(self, q, k_new, v_new, slots, past, starts, parents, q_norm_w, k_norm_w,
+                        inv_freq, sinks, scores, out, eps, scale, stream=None):
+        """Attention of trees of drafted tokens: request r's nodes are the rows
+        starts[r] .. starts[r+1] - 1, their parents[...] earlier nodes of the
+        request (-1: the history); each attends the past[r] keys of slot
+        slots[r], its ancestors and itself, and its K and V go to place
+        past[r] + node.  scores: a Scores (doc_start per request), or None."""
+        return self._tree("tree_batch_attn", q, k_new, v_new, slots, past, starts, parents,
+                          q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps, scale, stream)
+
+    def tree_batch_attn_paged(self, q, k_new, v_new, block_tables, past, starts, parents,
+                              q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                              stream=None):
+        """As tree_batch_attn over a paged pool: block_tables int32 [requests][max_blocks]."""
+        return self._tree("tree_batch_attn_paged", q, k_new, v_new, block_tables, past, starts,
+                          parents, q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                          stream)
+
+    def _tree(self, name, q, k_new, v_new, idx, past, starts, parents, q_norm_w, k_norm_w,
+              inv_freq, sinks, scores, out, eps, scale, stream):
+        c = _compiled()
+        if c and _done(getattr(c, name)(
+                self._h.value, self.n_kv_head, self.head_dim, q, k_new, v_new, idx, past, starts,
+                parents, q_norm_w, k_norm_w, inv_freq, sinks,
+                None if scores is None else scores._args, out, eps, scale, _stream_arg(stream)),
+                name):
+            return out
+        import torch
+        paged = name == "tree_batch_attn_paged"
+        _need(q=(q, 3), past=(past, 1), starts=(starts, 1), parents=(parents, 1),
+              **{"block_tables" if paged else "slots": (idx, 2 if paged else 1)})
+        dev, R, f = _device(), past.shape[0], torch.float32
+        if parents.shape != (q.shape[0],):
+            raise ValueError(f"parents has shape {_shape(parents)}, expected {(q.shape[0],)}")
+        # (parents stands in for the positions of a step: one int32 per row)
+        B, n_head = _check_step(q, k_new, v_new, parents, idx, out, q_norm_w, k_norm_w, inv_freq,
+                                sinks, self.n_kv_head, self.head_dim, "block_tables")
+        tensors = {"q": q, "k_new": k_new, "v_new": v_new, "q_norm_w": q_norm_w,
+                   "k_norm_w": k_norm_w, "inv_freq": inv_freq, "sinks": sinks, "out": out}
+        at = {}
+        for what, t in tensors.items():
+            at[what] = _ptr(t, f, what)
+            _on_device(t, dev, what)
+        shape = (R, idx.shape[1]) if paged else (R,)
+        ai, ap, ast, apar = _ints(dev, **{"block_tables" if paged else "slots": (idx, shape)},
+                                  past=(past, (R,)), starts=(starts, (R + 1,)),
+                                  parents=(parents, (B,)))
+        _check(getattr(_lib, name)(
+            self._h, R, B, n_head, at["q"], at["k_new"], at["v_new"], ai,
+            *((idx.shape[1],) if paged else ()), ap, ast, apar, at["q_norm_w"], at["k_norm_w"],
+            at["inv_freq"], at["sinks"], _scores(scores, R, n_head, dev), at["out"], eps, scale,
+            _raw_stream(stream, dev)), name)
+        return out
+
+    def keep_path(self, slots, past, starts, n_keep, path, stream=None):
+        """slot_kv_keep_path: the K and V of place past[r] + k become those of
+        place past[r] + path[starts[r] + k], k < n_keep[r].  int32 CUDA tensors."""
+        self._keep_path("slot_kv_keep_path", slots, past, starts, n_keep, path, stream)
+
+    def keep_path_paged(self, block_tables, past, starts, n_keep, path, stream=None):
+        """As keep_path over a paged pool: block_tables int32 [requests][max_blocks]."""
+        self._keep_path("slot_kv_keep_path_paged", block_tables, past, starts, n_keep, path,
+                        stream)
+
+    def _keep_path(self, name, idx, past, starts, n_keep, path, stream):
+        c = _compiled()
+        if c and _done(getattr(c, name)(self._h.value, idx, past, starts, n_keep, path,
+                                        _stream_arg(stream)), name):
+            return
+        paged = name == "slot_kv_keep_path_paged"
+        what = "block_tables" if paged else "slots"
+        _need(past=(past, 1), starts=(starts, 1), n_keep=(n_keep, 1), path=(path, 1),
+              **{what: (idx, 2 if paged else 1)})
+        dev, R = _device(), past.shape[0]
+        shape = (R, idx.shape[1]) if paged else (R,)
+        ai, ap, ast, an, apath = _ints(dev, **{what: (idx, shape)}, past=(past, (R,)),
+                                       starts=(starts, (R + 1,)), n_keep=(n_keep, (R,)),
+                                       path=(path, (path.shape[0],)))
+        _check(getattr(_lib, name)(self._h, R, path.shape[0], ai,
+                                   *((idx.shape[1],) if paged else ()), ap, ast, an, apath,
+                                   _raw_stream(stream, dev)), name)
+
+    def fork_tables(self, src, past, block_tables, out_tables, shares, free_blocks, head,
+                    head_out=None, stream=None):
+        """slot_kv_fork_tables: row i of out_tables (int32 [forks][max_blocks])
+        becomes a fork of row src[i] of block_tables, which holds past[src[i]]
+        keys: full blocks shared, the partial one copied into a block of the
+        free list.  head_out None advances ``head`` itself.  int32 CUDA tensors."""
+        if head_out is None:
+            head_out = head
+        c, name = _compiled(), "slot_kv_fork_tables"
+        if c and _done(c.slot_kv_fork_tables(self._h.value, self.n_slots, src, past, block_tables,
+                                             out_tables, shares, free_blocks, head, head_out,
+                                             _stream_arg(stream)), name):
+            return out_tables, head_out
+        _need(src=(src, 1), past=(past, 1), block_tables=(block_tables, 2),
+              out_tables=(out_tables, 2), shares=(shares, 1), free_blocks=(free_blocks, 1),
+              head=(head, 1), head_out=(head_out, 1))
+        dev, n, (R, stride), n_free = (_device(), src.shape[0], block_tables.shape,
+                                       free_blocks.shape[0])
+        asrc, ap, at, ao, ash, af, ah, aho = _ints(
+            dev, src=(src, (n,)), past=(past, (R,)), block_tables=(block_tables, (R, stride)),
+            out_tables=(out_tables, (n, stride)), shares=(shares, (self.n_slots,)),
+            free_blocks=(free_blocks, (n_free,)), head=(head, (1,)), head_out=(head_out, (1,)))
+        _check(_lib.slot_kv_fork_tables(self._h, n, asrc, R, ap, at, stride, ao, ash, af, n_free,
+                                        ah, aho, _raw_stream(stream, dev)), name)
+        return out_tables, head_out
+
+    def free_tables(self, past, block_tables, shares, free_blocks, head, head_out=None, keep=None,
+                    stream=None):
+        """slot_kv_free_tables: the blocks of block_tables' rows past their first
+        keep[r] keys (None: all) given up; those that nobody shares go back to
+        free_blocks, below head.  shares None: no block is shared.  head_out
+        None moves ``head`` itself.  int32 CUDA tensors."""
+        if head_out is None:
+            head_out = head
+        c, name = _compiled(), "slot_kv_free_tables"
+        if c and _done(c.slot_kv_free_tables(self._h.value, self.n_slots, past, keep, block_tables,
+                                             shares, free_blocks, head, head_out,
+                                             _stream_arg(stream)), name):
+            return free_blocks, head_out
+        _need(past=(past, 1), block_tables=(block_tables, 2), free_blocks=(free_blocks, 1),
+              head=(head, 1), head_out=(head_out, 1))
+        dev, (R, stride), n_free = _device(), block_tables.shape, free_blocks.shape[0]
+        ap, ak, at, ash, af, ah, aho = _ints(
+            dev, past=(past, (R,)), keep=(keep, (R,)), block_tables=(block_tables, (R, stride)),
+            shares=(shares, (self.n_slots,)), free_blocks=(free_blocks, (n_free,)),
+            head=(head, (1,)), head_out=(head_out, (1,)))
+        _check(_lib.slot_kv_free_tables(self._h, R, ap, ak, at, stride, ash, af, n_free, ah, aho,
+                                        _raw_stream(stream, dev)), name)
+        return free_blocks, head_out
+
+    def compact_pool(self, past, block_tables, shares, free_blocks, head, stream=None):
+        """slot_kv_compact_pool: the blocks that block_tables' rows use moved to
+        the ids 0 .. L - 1; K, V, tables, shares (or None), the free list and
+        head follow, all in place.  int32 CUDA tensors."""
+        c, name = _compiled(), "slot_kv_compact_pool"
+        if c and _done(c.slot_kv_compact_pool(self._h.value, self.n_slots, past, block_tables,
+                                              shares, free_blocks, head, _stream_arg(stream)),
+                       name):
+            return
+        _need(past=(past, 1), block_tables=(block_tables, 2), free_blocks=(free_blocks, 1),
+              head=(head, 1))
+        dev, (R, stride), n_free = _device(), block_tables.shape, free_blocks.shape[0]
+        ap, at, ash, af, ah = _ints(
+            dev, past=(past, (R,)), block_tables=(block_tables, (R, stride)),
+            shares=(shares, (self.n_slots,)), free_blocks=(free_blocks, (n_free,)),
+            head=(head, (1,)))
+        _check(_lib.slot_kv_compact_pool(self._h, R, ap, at, stride, ash, af, n_free, ah,
+                                         _raw_stream(stream, dev)), name)
+
     def prepare_host_call(self, q, k_new, v_new, positions, slots, q_norm_w, k_norm_w,
                           inv_freq, sinks, out, eps, scale, block_tables=None):
         """A prepared host step (slot_kv_host_call_create): the arguments of
@@ -794,6 +990,41 @@ def slot_kv_token_map(h, slots, past, fresh, starts, tok_slots, tok_positions, s
 def slot_kv_extend_tables(h, past, fresh, block_tables, free_blocks, head, head_out=None,
                           stream=None):
     return h.extend_tables(past, fresh, block_tables, free_blocks, head, head_out, stream)
+
+
+def tree_batch_attn(h, q, k_new, v_new, slots, past, starts, parents, q_norm_w, k_norm_w,
+                    inv_freq, sinks, scores, out, eps, scale, stream=None):
+    return h.tree_batch_attn(q, k_new, v_new, slots, past, starts, parents, q_norm_w, k_norm_w,
+                             inv_freq, sinks, scores, out, eps, scale, stream)
+
+
+def tree_batch_attn_paged(h, q, k_new, v_new, block_tables, past, starts, parents, q_norm_w,
+                          k_norm_w, inv_freq, sinks, scores, out, eps, scale, stream=None):
+    return h.tree_batch_attn_paged(q, k_new, v_new, block_tables, past, starts, parents, q_norm_w,
+                                   k_norm_w, inv_freq, sinks, scores, out, eps, scale, stream)
+
+
+def slot_kv_keep_path(h, slots, past, starts, n_keep, path, stream=None):
+    h.keep_path(slots, past, starts, n_keep, path, stream)
+
+
+def slot_kv_keep_path_paged(h, block_tables, past, starts, n_keep, path, stream=None):
+    h.keep_path_paged(block_tables, past, starts, n_keep, path, stream)
+
+
+def slot_kv_fork_tables(h, src, past, block_tables, out_tables, shares, free_blocks, head,
+                        head_out=None, stream=None):
+    return h.fork_tables(src, past, block_tables, out_tables, shares, free_blocks, head, head_out,
+                         stream)
+
+
+def slot_kv_free_tables(h, past, block_tables, shares, free_blocks, head, head_out=None,
+                        keep=None, stream=None):
+    return h.free_tables(past, block_tables, shares, free_blocks, head, head_out, keep, stream)
+
+
+def slot_kv_compact_pool(h, past, block_tables, shares, free_blocks, head, stream=None):
+    h.compact_pool(past, block_tables, shares, free_blocks, head, stream)
 
 
 class HostCall:

@@ -2,7 +2,8 @@
 
 The translation units compile in parallel (one per head dim for the decode
 and the tensor-core prefill kernels and their scored forms, the request-length
-kernels, the host side, the allocation-free entry point), then link into
+kernels, the tree attention, the pool's pages, the host side, the
+allocation-free entry point), then link into
 ``sequence_slot_kv_gb300/libslotkv.so``.
 """
 import importlib.util
@@ -20,9 +21,9 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["slotkv.cu", "decode_attn_hd64.cu", "decode_attn_hd128.cu", "decode_attn_hd256.cu",
            "noalloc.cu", "prefill_tc_hd64.cu", "prefill_tc_hd128.cu", "scored_decode_hd64.cu",
            "scored_decode_hd128.cu", "scored_decode_hd256.cu", "scored_prefill_hd64.cu",
-           "scored_prefill_hd128.cu", "maps.cu"]
-DEPS = ["params.h", "maps.h", "score_rule.cuh", "decode_attn.cuh", "decode_small.cuh",
-        "prefill_tc.cuh", "tc_ops.cuh"]
+           "scored_prefill_hd128.cu", "maps.cu", "tree_attn.cu", "pages.cu"]
+DEPS = ["params.h", "maps.h", "pages.h", "tree_attn.h", "tree_attn.cuh", "score_rule.cuh",
+        "decode_attn.cuh", "decode_small.cuh", "prefill_tc.cuh", "tc_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE] + ARCH
 

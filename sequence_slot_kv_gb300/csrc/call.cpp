@@ -1,5 +1,6 @@
-// call.cpp -- the Python module _slotkv_call: the scored, shared and
-// request-length calls of include/slotkv.h made straight from torch tensors.
+// call.cpp -- the Python module _slotkv_call: the scored, shared, tree and
+// request-length calls and those on pages of include/slotkv.h made straight
+// from torch tensors.
 //
 // A small step's kernels take a few microseconds, and checking a dozen tensors
 // and marshalling them attribute by attribute in Python takes as long (3.5 us
@@ -89,7 +90,8 @@ slotkv_stream_t stream_of(PyObject* o, int dev) {
     return pointer(o);
 }
 
-// (cap, window, slopes, doc_start, prefix_end) or None
+// (cap, window, slopes, doc_start, prefix_end) or None; rows: what doc_start and
+// prefix_end have an entry for
 const slotkv_scores* scores_of(PyObject* o, slotkv_scores& s, int dev, int64_t rows,
                                int64_t n_head) {
     if (o == Py_None) return nullptr;
@@ -139,12 +141,14 @@ struct Rest {
     float* out;
     float eps, scale;
     slotkv_stream_t stream;
-    Rest(PyObject* const* a, const Step& s) {
+    Rest(PyObject* const* a, const Step& s) : Rest(a, s, s.B) {}
+    template <typename S>
+    Rest(PyObject* const* a, const S& s, int64_t rule_rows) {
         qw = floats(a[0], s.dev, {s.hd});
         kw = floats(a[1], s.dev, {s.hd});
         inv = floats(a[2], s.dev, {s.hd / 2});
         sinks = floats_or_null(a[3], s.dev, {s.n_head});
-        scores = scores_of(a[4], store, s.dev, s.B, s.n_head);
+        scores = scores_of(a[4], store, s.dev, rule_rows, s.n_head);
         out = address<float>(a[5], F32, s.dev, {s.B, s.n_head, s.hd});
         eps = static_cast<float>(number(a[6]));
         scale = static_cast<float>(number(a[7]));
@@ -274,6 +278,180 @@ PyObject* py_extend_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A tree call's; a[0..] = handle, n_kv_head, head_dim, q, k_new, v_new, slots or
+// block tables, past, starts, parents.
+struct TreeStep {
+    slotkv_t h;
+    int64_t B, n_head, hd, R, stride = 0;
+    const float *q, *k_new, *v_new;
+    const uint32_t *idx, *past, *starts, *parents;
+    int dev;
+    TreeStep(PyObject* const* a, bool paged) {
+        dev = static_cast<int>(c10::cuda::current_device());
+        h = static_cast<slotkv_t>(pointer(a[0]));
+        const int64_t n_kv = integer(a[1]);
+        const at::Tensor& tq = tensor(a[3], F32, dev);
+        if (tq.dim() != 3) throw Unlike{};
+        B = tq.size(0);
+        n_head = tq.size(1);
+        hd = tq.size(2);
+        if (hd != integer(a[2]) || B > UINT32_MAX || n_head > UINT32_MAX) throw Unlike{};
+        q = static_cast<const float*>(tq.data_ptr());
+        k_new = floats(a[4], dev, {B, n_kv, hd});
+        v_new = floats(a[5], dev, {B, n_kv, hd});
+        const at::Tensor& tp = tensor(a[7], I32, dev);
+        if (tp.dim() != 1 || tp.size(0) >= UINT32_MAX) throw Unlike{};
+        R = tp.size(0);
+        past = static_cast<const uint32_t*>(tp.data_ptr());
+        if (paged) {
+            const at::Tensor& tab = tensor(a[6], I32, dev);
+            if (tab.dim() != 2 || tab.size(0) != R || tab.size(1) > UINT32_MAX) throw Unlike{};
+            stride = tab.size(1);
+            idx = static_cast<const uint32_t*>(tab.data_ptr());
+        } else {
+            idx = ints(a[6], dev, {R});
+        }
+        starts = ints(a[8], dev, {R + 1});
+        parents = ints(a[9], dev, {B});
+    }
+};
+
+PyObject* py_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return run(n, 19, [&] {
+        const TreeStep s(a, false);
+        const Rest r(a + 10, s, s.R);
+        return without_gil([&] {
+            return tree_batch_attn(s.h, static_cast<uint32_t>(s.R), static_cast<uint32_t>(s.B),
+                                   static_cast<uint32_t>(s.n_head), s.q, s.k_new, s.v_new, s.idx,
+                                   s.past, s.starts, s.parents, r.qw, r.kw, r.inv, r.sinks,
+                                   r.scores, r.out, r.eps, r.scale, r.stream);
+        });
+    });
+}
+
+PyObject* py_tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return run(n, 19, [&] {
+        const TreeStep s(a, true);
+        const Rest r(a + 10, s, s.R);
+        return without_gil([&] {
+            return tree_batch_attn_paged(
+                s.h, static_cast<uint32_t>(s.R), static_cast<uint32_t>(s.B),
+                static_cast<uint32_t>(s.n_head), s.q, s.k_new, s.v_new, s.idx,
+                static_cast<uint32_t>(s.stride), s.past, s.starts, s.parents, r.qw, r.kw, r.inv,
+                r.sinks, r.scores, r.out, r.eps, r.scale, r.stream);
+        });
+    });
+}
+
+// handle, slots or block tables, past, starts, n_keep, path, stream
+PyObject* keep_path(PyObject* const* a, Py_ssize_t n, bool paged) {
+    return run(n, 7, [&] {
+        const int dev = static_cast<int>(c10::cuda::current_device());
+        slotkv_t h = static_cast<slotkv_t>(pointer(a[0]));
+        const at::Tensor& tp = tensor(a[2], I32, dev);
+        const at::Tensor& path = tensor(a[5], I32, dev);
+        if (tp.dim() != 1 || path.dim() != 1 || tp.size(0) >= UINT32_MAX ||
+            path.size(0) > UINT32_MAX)
+            throw Unlike{};
+        const int64_t R = tp.size(0);
+        const at::Tensor& idx = tensor(a[1], I32, dev);
+        if (idx.dim() != (paged ? 2 : 1) || idx.size(0) != R ||
+            (paged && idx.size(1) > UINT32_MAX))
+            throw Unlike{};
+        const uint32_t* past = static_cast<const uint32_t*>(tp.data_ptr());
+        const uint32_t* where = static_cast<const uint32_t*>(idx.data_ptr());
+        const uint32_t* starts = ints(a[3], dev, {R + 1});
+        const uint32_t* n_keep = ints(a[4], dev, {R});
+        const uint32_t* p = static_cast<const uint32_t*>(path.data_ptr());
+        const uint32_t r = static_cast<uint32_t>(R), t = static_cast<uint32_t>(path.size(0));
+        slotkv_stream_t stream = stream_of(a[6], dev);
+        return without_gil([&] {
+            return paged ? slot_kv_keep_path_paged(h, r, t, where,
+                                                   static_cast<uint32_t>(idx.size(1)), past,
+                                                   starts, n_keep, p, stream)
+                         : slot_kv_keep_path(h, r, t, where, past, starts, n_keep, p, stream);
+        });
+    });
+}
+PyObject* py_keep(PyObject*, PyObject* const* a, Py_ssize_t n) { return keep_path(a, n, false); }
+PyObject* py_keep_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return keep_path(a, n, true);
+}
+
+// The arguments that the calls on pages share: past [rows], block tables
+// [rows][stride], shares (or None), free list, head.
+struct Pages {
+    slotkv_t h;
+    int dev;
+    uint32_t rows, stride, n_free;
+    uint32_t *past, *tables, *shares, *free_ids, *head;
+    int64_t shape1;
+    Pages(PyObject* handle, PyObject* n_blocks, PyObject* o_past, PyObject* o_tables,
+          PyObject* o_shares, PyObject* o_free, PyObject* o_head) {
+        dev = static_cast<int>(c10::cuda::current_device());
+        h = static_cast<slotkv_t>(pointer(handle));
+        const at::Tensor& tab = tensor(o_tables, I32, dev);
+        const at::Tensor& f = tensor(o_free, I32, dev);
+        if (tab.dim() != 2 || f.dim() != 1 || tab.size(0) > UINT32_MAX ||
+            tab.size(1) > UINT32_MAX || f.size(0) > UINT32_MAX)
+            throw Unlike{};
+        shape1 = tab.size(1);
+        rows = static_cast<uint32_t>(tab.size(0));
+        stride = static_cast<uint32_t>(shape1);
+        n_free = static_cast<uint32_t>(f.size(0));
+        past = ints(o_past, dev, {tab.size(0)});
+        tables = static_cast<uint32_t*>(tab.data_ptr());
+        shares = o_shares == Py_None ? nullptr : ints(o_shares, dev, {integer(n_blocks)});
+        free_ids = static_cast<uint32_t*>(f.data_ptr());
+        head = ints(o_head, dev, {1});
+    }
+};
+
+// handle, n_blocks, src, past, block tables, out tables, shares, free list, head,
+// head out, stream
+PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return run(n, 11, [&] {
+        const Pages p(a[0], a[1], a[3], a[4], a[6], a[7], a[8]);
+        const at::Tensor& src = tensor(a[2], I32, p.dev);
+        if (src.dim() != 1 || src.size(0) > UINT32_MAX || !p.shares) throw Unlike{};
+        uint32_t* out = ints(a[5], p.dev, {src.size(0), p.shape1});
+        uint32_t* head_out = ints(a[9], p.dev, {1});
+        slotkv_stream_t stream = stream_of(a[10], p.dev);
+        return without_gil([&] {
+            return slot_kv_fork_tables(p.h, static_cast<uint32_t>(src.size(0)),
+                                       static_cast<const uint32_t*>(src.data_ptr()), p.rows,
+                                       p.past, p.tables, p.stride, out, p.shares, p.free_ids,
+                                       p.n_free, p.head, head_out, stream);
+        });
+    });
+}
+
+// handle, n_blocks, past, keep, block tables, shares, free list, head, head out, stream
+PyObject* py_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return run(n, 10, [&] {
+        const Pages p(a[0], a[1], a[2], a[4], a[5], a[6], a[7]);
+        const uint32_t* keep = ints_or_null(a[3], p.dev, {static_cast<int64_t>(p.rows)});
+        uint32_t* head_out = ints(a[8], p.dev, {1});
+        slotkv_stream_t stream = stream_of(a[9], p.dev);
+        return without_gil([&] {
+            return slot_kv_free_tables(p.h, p.rows, p.past, keep, p.tables, p.stride, p.shares,
+                                       p.free_ids, p.n_free, p.head, head_out, stream);
+        });
+    });
+}
+
+// handle, n_blocks, past, block tables, shares, free list, head, stream
+PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return run(n, 8, [&] {
+        const Pages p(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+        slotkv_stream_t stream = stream_of(a[7], p.dev);
+        return without_gil([&] {
+            return slot_kv_compact_pool(p.h, p.rows, p.past, p.tables, p.stride, p.shares,
+                                        p.free_ids, p.n_free, p.head, stream);
+        });
+    });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F)), METH_FASTCALL, nullptr};
@@ -285,6 +463,13 @@ PyMethodDef methods[] = {method<py_decode>("decode_batch_attn_scored"),
                          method<py_shared>("decode_batch_attn_shared"),
                          method<py_token_map>("slot_kv_token_map"),
                          method<py_extend_tables>("slot_kv_extend_tables"),
+                         method<py_tree>("tree_batch_attn"),
+                         method<py_tree_paged>("tree_batch_attn_paged"),
+                         method<py_keep>("slot_kv_keep_path"),
+                         method<py_keep_paged>("slot_kv_keep_path_paged"),
+                         method<py_fork>("slot_kv_fork_tables"),
+                         method<py_free>("slot_kv_free_tables"),
+                         method<py_compact>("slot_kv_compact_pool"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_slotkv_call", nullptr, -1, methods,

@@ -1,0 +1,537 @@
+// pages.cu -- cache rows and pool blocks moved, shared and given back, on the
+// device: slot_kv_keep_path (the rows of a verified tree's accepted path),
+// slot_kv_fork_tables (tables that share full blocks and copy the partial
+// one), slot_kv_free_tables (blocks back on the free list) and
+// slot_kv_compact_pool (the blocks in use moved to the pool's front).
+//
+// All of them move bytes and count; there is no arithmetic to speak of.  Small
+// calls are bound by their dependent loads (a few round trips to L2), large
+// ones by the rows they copy.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pages.h"
+
+namespace slotkv {
+namespace {
+
+constexpr uint32_t kRange = 1u;  // SLOTKV_DEV_RANGE
+constexpr int kCopyThreads = 256;
+constexpr uint32_t kBatch = 8;   // 16-byte pieces a thread has in flight
+
+__device__ __forceinline__ void begin_dependent() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t blocks_of(uint32_t keys, uint32_t block) {
+    return keys ? (keys - 1u) / block + 1u : 0u;
+}
+
+// n float4s from src to dst, by the threads i0, i0 + step, ...; the ranges do
+// not overlap.
+__device__ __forceinline__ void copy_float4(const float4* __restrict__ src,
+                                            float4* __restrict__ dst, uint32_t n, uint32_t i0,
+                                            uint32_t step) {
+    for (uint64_t i = i0; i < n; i += static_cast<uint64_t>(kBatch) * step) {
+        float4 x[kBatch];
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint64_t j = i + static_cast<uint64_t>(k) * step;
+            if (j < n) x[k] = __ldcs(src + j);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint64_t j = i + static_cast<uint64_t>(k) * step;
+            if (j < n) dst[j] = x[k];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ keep path
+// Row past + k of the request takes row past + path[k], k in order.  path is
+// strictly increasing, so path[k] >= k: row k is written after every row that
+// it was the source of has been read.  A thread owns one 16-byte column of the
+// request's rows and goes through the path in order, eight loads before their
+// eight stores, so no thread waits for another and the moves may overlap.
+__global__ void __launch_bounds__(kCopyThreads) slotkv_keep_path_kernel(const KeepPathParams P) {
+    __shared__ uint32_t from[kMaxTree], to[kMaxTree];
+    begin_dependent();
+    const uint32_t r = blockIdx.x;
+    const uint32_t s0 = __ldg(P.starts + r), s1 = __ldg(P.starts + r + 1);
+    const uint32_t n = __ldg(P.n_keep + r), past = __ldg(P.past + r);
+    if (n == 0) return;
+    const uint64_t limit = P.slots ? P.pool.block : static_cast<uint64_t>(P.bt_stride) * P.pool.block;
+    bool ok = s0 <= s1 && s1 <= P.n_tok && s1 - s0 <= kMaxTree && n <= s1 - s0 &&
+              static_cast<uint64_t>(past) + (s1 - s0) <= limit;
+    const uint32_t slot = P.slots ? __ldg(P.slots + r) : 0u;
+    if (P.slots) ok = ok && slot < P.pool.n_blocks;
+    // row of the request's position p in the [rows][kv_dim] view
+    auto row_of = [&](uint32_t p, bool& good) {
+        if (P.slots) return slot * P.pool.block + p;
+        const uint32_t id =
+            __ldg(P.block_tables + static_cast<size_t>(r) * P.bt_stride + p / P.pool.block);
+        good = good && id < P.pool.n_blocks;
+        return id * P.pool.block + p % P.pool.block;
+    };
+    if (ok) {
+        for (uint32_t k = threadIdx.x; k < n; k += kCopyThreads) {
+            const uint32_t i = __ldg(P.path + s0 + k);
+            const uint32_t before = k ? __ldg(P.path + s0 + k - 1) : 0u;
+            if (i >= s1 - s0 || (k && i <= before)) {
+                ok = false;
+            } else {
+                from[k] = row_of(past + i, ok);
+                to[k] = row_of(past + k, ok);
+            }
+        }
+    }
+    if (!__syncthreads_and(ok)) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(P.pool.status, kRange);
+        return;
+    }
+    const uint32_t cols = P.pool.kv_dim / 4;
+    for (uint32_t c = blockIdx.y * kCopyThreads + threadIdx.x; c < 2 * cols;
+         c += gridDim.y * kCopyThreads) {
+        float4* X = reinterpret_cast<float4*>(c < cols ? P.pool.K : P.pool.V) +
+                    (c < cols ? c : c - cols);
+        for (uint32_t k0 = 0; k0 < n; k0 += kBatch) {
+            float4 x[kBatch];
+#pragma unroll
+            for (uint32_t k = 0; k < kBatch; ++k)
+                if (k0 + k < n && from[k0 + k] != to[k0 + k])
+                    x[k] = X[static_cast<size_t>(from[k0 + k]) * cols];
+#pragma unroll
+            for (uint32_t k = 0; k < kBatch; ++k)
+                if (k0 + k < n && from[k0 + k] != to[k0 + k])
+                    X[static_cast<size_t>(to[k0 + k]) * cols] = x[k];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ fork
+// Whether fork j takes a block of the free list; false in ok: out of range.
+__device__ __forceinline__ bool fork_needs(const ForkTablesParams& P, uint32_t j, bool& ok,
+                                           uint32_t& s, uint32_t& past) {
+    s = __ldg(P.src + j);
+    ok = s < P.n_rows;
+    past = ok ? __ldg(P.past + s) : 0u;
+    ok = ok && blocks_of(past, P.pool.block) <= P.bt_stride;
+    return ok && past % P.pool.block != 0u;
+}
+
+// CTA (fork, part): counts the forks before its own that take a block, which
+// names its own; part 0 writes the fork's table, and every part copies its
+// share of the partial block.
+__global__ void __launch_bounds__(kCopyThreads) slotkv_fork_tables_kernel(const ForkTablesParams P) {
+    __shared__ uint32_t count;
+    begin_dependent();
+    const uint32_t i = blockIdx.x;
+    const uint32_t head = __ldcg(P.head);
+    const uint32_t avail = head < P.n_free ? P.n_free - head : 0u;
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t j = threadIdx.x; j < i; j += kCopyThreads) {
+        bool ok;
+        uint32_t s, past;
+        before += fork_needs(P, j, ok, s, past);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if ((threadIdx.x & 31) == 0 && before) atomicAdd(&count, before);
+    __syncthreads();
+    const uint32_t at = count;  // blocks that the forks before this one take
+    bool ok = false;
+    uint32_t s = 0, past = 0;
+    const bool need = i < P.n_fork && fork_needs(P, i, ok, s, past);
+    const bool served = !need || at < avail;
+    if (blockIdx.y == 0 && threadIdx.x == 0 && i < P.n_fork && !(ok && served))
+        atomicOr(P.pool.status, kRange);
+    if (ok && served) {
+        const uint32_t full = past / P.pool.block, rest = past % P.pool.block;
+        const uint32_t* row = P.block_tables + static_cast<size_t>(s) * P.bt_stride;
+        uint32_t* out = P.out_tables + static_cast<size_t>(i) * P.bt_stride;
+        if (blockIdx.y == 0) {
+            for (uint32_t e = threadIdx.x; e < full; e += kCopyThreads) {
+                const uint32_t id = __ldg(row + e);
+                out[e] = id;
+                if (id < P.pool.n_blocks)
+                    atomicAdd(P.shares + id, 1u);
+                else
+                    atomicOr(P.pool.status, kRange);
+            }
+        }
+        if (need) {
+            const uint32_t id = __ldg(P.free_blocks + head + at), old = __ldg(row + full);
+            const bool good = id < P.pool.n_blocks && old < P.pool.n_blocks;
+            if (blockIdx.y == 0 && threadIdx.x == 0) {
+                out[full] = id;
+                if (!good) atomicOr(P.pool.status, kRange);
+            }
+            if (good && id != old) {
+                const size_t block4 = static_cast<size_t>(P.pool.block) * (P.pool.kv_dim / 4);
+                const uint32_t n = rest * (P.pool.kv_dim / 4);
+                const uint32_t t = blockIdx.y * kCopyThreads + threadIdx.x;
+                const uint32_t step = gridDim.y * kCopyThreads;
+                copy_float4(reinterpret_cast<const float4*>(P.pool.K) + old * block4,
+                            reinterpret_cast<float4*>(P.pool.K) + id * block4, n, t, step);
+                copy_float4(reinterpret_cast<const float4*>(P.pool.V) + old * block4,
+                            reinterpret_cast<float4*>(P.pool.V) + id * block4, n, t, step);
+            }
+        }
+    }
+    // the last fork's CTA knows the new head; where that is the word the others
+    // read the old one from, the last CTA to finish writes it
+    const bool last = i + 1 >= P.n_fork && blockIdx.y == 0;
+    const uint32_t used = at + (need ? 1u : 0u);
+    const uint32_t new_head = head + (used < avail ? used : avail);
+    if (P.head_out != P.head) {
+        if (last && threadIdx.x == 0) *P.head_out = new_head;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        if (last) atomicExch(P.scratch + 1, new_head);
+        __threadfence();
+        if (atomicAdd(P.scratch, 1u) == gridDim.x * gridDim.y - 1) {
+            __threadfence();
+            *P.head_out = __ldcg(P.scratch + 1);
+            P.scratch[0] = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ cluster phases
+// The list kernels below go through phases that all CTAs finish before the
+// next: one cluster of CTAs, whose barrier orders their global accesses too.
+constexpr int kListThreads = 1024, kListWarps = kListThreads / 32;
+constexpr uint32_t kListCtas = 8;
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A word of another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t cta) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(cta));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Exclusive prefix sum, over the cluster's warps in order, of one value per
+// warp (the same in all its lanes); total: the sum.
+struct ListScan {
+    uint32_t warp_sum[kListWarps];
+    uint32_t cta_sum;
+};
+__device__ uint32_t cluster_exclusive(uint32_t v, ListScan& sh, uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) sh.warp_sum[warp] = v;
+    __syncthreads();
+    const uint32_t x = sh.warp_sum[lane];  // (kListWarps = 32)
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0u);
+    if (threadIdx.x == 0) sh.cta_sum = 0;
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, x);
+    __syncthreads();
+    if (threadIdx.x == 0) sh.cta_sum = sum;
+    cluster_barrier();
+    uint32_t at = before;
+    total = 0;
+    for (uint32_t c = 0; c < gridDim.x; ++c) {
+        const uint32_t y = cluster_load(&sh.cta_sum, c);
+        if (c < blockIdx.x) at += y;
+        total += y;
+    }
+    cluster_barrier();  // (no CTA leaves, or reuses the word, while others read it)
+    return at;
+}
+static_assert(kListWarps == 32, "one lane per warp");
+
+// A warp's items: 32 table entries of one request each, in entry order.
+struct EntryItems {
+    uint32_t per_row, begin, end;  // items per request; this warp's [begin, end)
+};
+__device__ __forceinline__ EntryItems my_items(uint32_t R, uint32_t bt_stride) {
+    EntryItems it;
+    it.per_row = (bt_stride + 31) / 32;
+    const uint64_t n = static_cast<uint64_t>(R) * it.per_row;
+    const uint32_t warps = gridDim.x * kListWarps;
+    const uint64_t per = (n + warps - 1) / warps;
+    const uint64_t b = (blockIdx.x * kListWarps + (threadIdx.x >> 5)) * per;
+    it.begin = static_cast<uint32_t>(b < n ? b : n);
+    it.end = static_cast<uint32_t>(b + per < n ? b + per : n);
+    return it;
+}
+
+// ------------------------------------------------------------------ free
+// The entry of this lane in an item, if it gives up a block.
+struct FreeEntry {
+    uint32_t id, code;
+    bool live;
+};
+__device__ __forceinline__ FreeEntry free_entry(const FreeTablesParams& P, uint32_t item,
+                                                uint32_t per_row, bool flag) {
+    const uint32_t r = item / per_row, e = (item % per_row) * 32 + (threadIdx.x & 31);
+    const uint32_t n = blocks_of(__ldg(P.past + r), P.pool.block);
+    const uint32_t k = P.keep ? blocks_of(__ldg(P.keep + r), P.pool.block) : 0u;
+    FreeEntry x;
+    x.live = n <= P.bt_stride && e >= k && e < n;
+    const uint32_t at = r * P.bt_stride + e;
+    x.id = x.live ? __ldg(P.block_tables + at) : 0u;
+    x.code = 0x80000000u + at;
+    const bool bad = n > P.bt_stride || (x.live && x.id >= P.pool.n_blocks);
+    if (flag && __any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)
+        atomicOr(P.pool.status, kRange);
+    x.live = x.live && x.id < P.pool.n_blocks;
+    return x;
+}
+
+// Which blocks go, and in which order, without an order among the threads: (1)
+// every entry takes one from its block's share count, which goes below zero
+// where nobody is left; (2) the entries of those blocks leave their place in
+// the tables there, as the most negative numbers, and the first one stays
+// (atomic minimum); (3) the entry that finds its own place is the one that
+// gives the block back; a prefix sum over them gives their places in the list.
+__global__ void __launch_bounds__(kListThreads) slotkv_free_tables_kernel(const FreeTablesParams P) {
+    __shared__ ListScan scan;
+    begin_dependent();
+    const int lane = threadIdx.x & 31;
+    const EntryItems it = my_items(P.R, P.bt_stride);
+    const uint32_t head0 = __ldcg(P.head), head = head0 < P.n_free ? head0 : P.n_free;
+    int* shares = reinterpret_cast<int*>(P.shares);
+    if (shares) {
+        for (uint32_t i = it.begin; i < it.end; ++i) {
+            const FreeEntry x = free_entry(P, i, it.per_row, false);
+            if (x.live) atomicSub(shares + x.id, 1);
+        }
+        cluster_barrier();
+        for (uint32_t i = it.begin; i < it.end; ++i) {
+            const FreeEntry x = free_entry(P, i, it.per_row, false);
+            if (x.live && __ldcg(shares + x.id) < 0) {
+                const int old = atomicMin(shares + x.id, static_cast<int>(x.code));
+                if (old < -1 && old >= -(1 << 30)) atomicOr(P.pool.status, kRange);  // given up twice
+            }
+        }
+        cluster_barrier();
+    }
+    auto gone = [&](const FreeEntry& x) {
+        return x.live && (!shares || __ldcg(shares + x.id) == static_cast<int>(x.code));
+    };
+    uint32_t mine = 0;
+    for (uint32_t i = it.begin; i < it.end; ++i)
+        mine += __popc(__ballot_sync(0xffffffffu, gone(free_entry(P, i, it.per_row, true))));
+    uint32_t total;
+    uint32_t at = cluster_exclusive(mine, scan, total);
+    // the list is a stack below head: total ids end where the taken ones began
+    for (uint32_t i = it.begin; i < it.end; ++i) {
+        const FreeEntry x = free_entry(P, i, it.per_row, false);
+        const bool go = gone(x);
+        const uint32_t m = __ballot_sync(0xffffffffu, go);
+        const uint32_t k = at + __popc(m & ((1u << lane) - 1u));
+        if (go) {
+            if (head + k >= total) P.free_blocks[head + k - total] = x.id;
+            if (shares) shares[x.id] = 0;
+        }
+        at += __popc(m);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *P.head_out = head > total ? head - total : 0u;
+        if (head != head0 || total > head) atomicOr(P.pool.status, kRange);
+    }
+}
+
+// ------------------------------------------------------------------ compact
+// scratch: map[n] (1 where in use, then the new id), movers[n], holes[n], [L, moves]
+struct CompactScratch {
+    uint32_t *map, *movers, *holes, *counts;
+};
+__host__ __device__ inline CompactScratch compact_scratch(uint32_t* s, uint32_t n) {
+    return {s, s + n, s + 2 * static_cast<size_t>(n), s + 3 * static_cast<size_t>(n)};
+}
+
+__device__ __forceinline__ uint32_t used_entries(const CompactPoolParams& P, uint32_t r, bool& ok) {
+    const uint32_t n = blocks_of(__ldg(P.past + r), P.pool.block);
+    ok = n <= P.bt_stride;
+    return ok ? n : P.bt_stride;
+}
+
+// Which blocks are in use, how many (L), and the moves: the blocks in use from
+// L on, in order, go to the free ids below L, in order.
+__global__ void __launch_bounds__(kListThreads) slotkv_compact_plan_kernel(const CompactPoolParams P) {
+    __shared__ ListScan scan;
+    begin_dependent();
+    const int lane = threadIdx.x & 31;
+    const uint32_t n = P.pool.n_blocks;
+    const CompactScratch S = compact_scratch(P.scratch, n);
+    const uint32_t gt = blockIdx.x * kListThreads + threadIdx.x, nt = gridDim.x * kListThreads;
+    for (uint32_t i = gt; i < n; i += nt) S.map[i] = 0;
+    cluster_barrier();
+    const EntryItems it = my_items(P.R, P.bt_stride);
+    for (uint32_t i = it.begin; i < it.end; ++i) {
+        const uint32_t r = i / it.per_row, e = (i % it.per_row) * 32 + lane;
+        bool ok;
+        const bool live = e < used_entries(P, r, ok);
+        const uint32_t id = live ? __ldg(P.block_tables + static_cast<size_t>(r) * P.bt_stride + e) : 0u;
+        const bool bad = !ok || (live && id >= n);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.pool.status, kRange);
+        if (live && id < n) S.map[id] = 1;
+    }
+    cluster_barrier();
+    // ids in order over the warps, 32 at a time
+    const uint32_t warps = gridDim.x * kListWarps, groups = (n + 31) / 32;
+    const uint32_t per = (groups + warps - 1) / warps;
+    const uint32_t w = blockIdx.x * kListWarps + (threadIdx.x >> 5);
+    const uint64_t g0 = static_cast<uint64_t>(w) * per;
+    const uint32_t b = static_cast<uint32_t>(g0 < groups ? g0 : groups);
+    const uint32_t e = static_cast<uint32_t>(g0 + per < groups ? g0 + per : groups);
+    uint32_t mine = 0;
+    for (uint32_t g = b; g < e; ++g) {
+        const uint32_t id = g * 32 + lane;
+        mine += __popc(__ballot_sync(0xffffffffu, id < n && __ldcg(S.map + id) != 0u));
+    }
+    uint32_t L;
+    const uint32_t first = cluster_exclusive(mine, scan, L);
+    // blocks in use below L: found by the warp that holds id L
+    uint32_t at = first;
+    for (uint32_t g = b; g < e; ++g) {
+        const uint32_t id = g * 32 + lane;
+        const bool live = id < n && __ldcg(S.map + id) != 0u;
+        const uint32_t m = __ballot_sync(0xffffffffu, live);
+        const uint32_t before = at + __popc(m & ((1u << lane) - 1u));  // in use below id
+        if (id == L) S.counts[1] = L - before;
+        if (id < L && !live) S.holes[id - before] = id;
+        at += __popc(m);
+    }
+    if (gt == 0) {
+        S.counts[0] = L;
+        if (L == n) S.counts[1] = 0;
+    }
+    cluster_barrier();
+    const uint32_t below = L - __ldcg(S.counts + 1);
+    at = first;
+    for (uint32_t g = b; g < e; ++g) {
+        const uint32_t id = g * 32 + lane;
+        const bool live = id < n && __ldcg(S.map + id) != 0u;
+        const uint32_t m = __ballot_sync(0xffffffffu, live);
+        const uint32_t before = at + __popc(m & ((1u << lane) - 1u));
+        if (id < n) {
+            uint32_t to = id;
+            if (live && id >= L) {
+                to = __ldcg(S.holes + before - below);
+                S.movers[before - below] = id;
+            }
+            S.map[id] = to;
+        }
+        at += __popc(m);
+    }
+    // the ids from L on are the free list now
+    const uint32_t left = n - L, F = left < P.n_free ? left : P.n_free;
+    for (uint32_t i = gt; i < F; i += nt) P.free_blocks[P.n_free - F + i] = L + i;
+    if (gt == 0) {
+        *P.head = P.n_free - F;
+        if (F < left) atomicOr(P.pool.status, kRange);
+    }
+}
+
+// The moves, share counts and tables, over the whole GPU: CTAs take (block,
+// part) pairs in turn, then table entries.
+__global__ void __launch_bounds__(kCopyThreads) slotkv_compact_move_kernel(const CompactPoolParams P,
+                                                                           uint32_t parts) {
+    begin_dependent();
+    const CompactScratch S = compact_scratch(P.scratch, P.pool.n_blocks);
+    const uint32_t moves = __ldcg(S.counts + 1), L = __ldcg(S.counts);
+    const uint32_t n4 = P.pool.block * (P.pool.kv_dim / 4);
+    const uint64_t work = static_cast<uint64_t>(moves) * parts;
+    for (uint64_t i = blockIdx.x; i < work; i += gridDim.x) {
+        const uint32_t k = static_cast<uint32_t>(i / parts), part = static_cast<uint32_t>(i % parts);
+        const uint32_t src = __ldcg(S.movers + k), dst = __ldcg(S.holes + k);
+        const uint32_t t = part * kCopyThreads + threadIdx.x, step = parts * kCopyThreads;
+        copy_float4(reinterpret_cast<const float4*>(P.pool.K) + static_cast<size_t>(src) * n4,
+                    reinterpret_cast<float4*>(P.pool.K) + static_cast<size_t>(dst) * n4, n4, t, step);
+        copy_float4(reinterpret_cast<const float4*>(P.pool.V) + static_cast<size_t>(src) * n4,
+                    reinterpret_cast<float4*>(P.pool.V) + static_cast<size_t>(dst) * n4, n4, t, step);
+        if (P.shares && part == 0 && threadIdx.x == 0) P.shares[dst] = P.shares[src];
+    }
+    const uint64_t gt = static_cast<uint64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+    const uint64_t nt = static_cast<uint64_t>(gridDim.x) * kCopyThreads;
+    const uint64_t entries = static_cast<uint64_t>(P.R) * P.bt_stride;
+    for (uint64_t i = gt; i < entries; i += nt) {
+        bool ok;
+        const uint32_t r = static_cast<uint32_t>(i / P.bt_stride);
+        if (i % P.bt_stride >= used_entries(P, r, ok)) continue;
+        const uint32_t id = P.block_tables[i];
+        if (id >= L && id < P.pool.n_blocks) P.block_tables[i] = __ldcg(S.map + id);
+    }
+}
+
+// Share counts of the ids that are free now: after the moves have read them.
+__global__ void __launch_bounds__(kCopyThreads) slotkv_compact_shares_kernel(const CompactPoolParams P) {
+    begin_dependent();
+    const uint32_t L = __ldcg(compact_scratch(P.scratch, P.pool.n_blocks).counts);
+    const uint64_t i = static_cast<uint64_t>(L) + blockIdx.x * kCopyThreads + threadIdx.x;
+    if (i < P.pool.n_blocks) P.shares[i] = 0;
+}
+
+template <typename... A>
+int launch_dependent(void (*kernel)(A...), dim3 grid, int threads, uint32_t cluster,
+                     cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// CTAs of a list kernel over n items of 32: one where its warps have one each.
+uint32_t list_ctas(uint64_t n) { return n <= kListWarps ? 1u : kListCtas; }
+
+}  // namespace
+
+int launch_keep_path(const KeepPathParams& p, cudaStream_t stream) {
+    const uint32_t cols = 2 * (p.pool.kv_dim / 4);
+    const dim3 grid(p.R, (cols + kCopyThreads - 1) / kCopyThreads);
+    return launch_dependent(slotkv_keep_path_kernel, grid, kCopyThreads, 0, stream, p);
+}
+
+int launch_fork_tables(const ForkTablesParams& p, uint32_t sms, cudaStream_t stream) {
+    // enough parts for few forks to fill the GPU, none smaller than one batch of every thread
+    const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
+                          (kBatch * kCopyThreads);
+    const uint32_t forks = p.n_fork ? p.n_fork : 1u;
+    uint32_t parts = (4 * sms + forks - 1) / forks;
+    parts = parts < most ? parts : most;
+    parts = parts < 64u ? parts : 64u;
+    return launch_dependent(slotkv_fork_tables_kernel, dim3(forks, parts ? parts : 1u), kCopyThreads,
+                            0, stream, p);
+}
+
+int launch_free_tables(const FreeTablesParams& p, cudaStream_t stream) {
+    const uint32_t ctas = list_ctas(static_cast<uint64_t>(p.R) * ((p.bt_stride + 31) / 32));
+    return launch_dependent(slotkv_free_tables_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+}
+
+int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t stream) {
+    const uint64_t items = static_cast<uint64_t>(p.R) * ((p.bt_stride + 31) / 32);
+    const uint64_t groups = (static_cast<uint64_t>(p.pool.n_blocks) + 31) / 32;
+    const uint32_t ctas = list_ctas(items > groups ? items : groups);
+    int rc = launch_dependent(slotkv_compact_plan_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+    if (rc != 0) return rc;
+    const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
+                          (kBatch * kCopyThreads);
+    const uint32_t parts = most < 8u ? most : 8u;
+    rc = launch_dependent(slotkv_compact_move_kernel, dim3(4 * sms), kCopyThreads, 0, stream, p, parts);
+    if (rc != 0 || !p.shares) return rc;
+    const uint32_t grid = (p.pool.n_blocks + kCopyThreads - 1) / kCopyThreads;
+    return launch_dependent(slotkv_compact_shares_kernel, dim3(grid), kCopyThreads, 0, stream, p);
+}
+
+}  // namespace slotkv

@@ -17,7 +17,9 @@
 
 #include "../../include/slotkv.h"
 #include "maps.h"
+#include "pages.h"
 #include "params.h"
+#include "tree_attn.h"
 
 using slotkv::DecodeParams;
 
@@ -108,7 +110,11 @@ struct slotkv_s {
     float* sc_q = nullptr;            // [max_rows][max_n_head][hd] rotated q
     uint32_t* sc_idx = nullptr;       // rec, tiles, tile_of, tile_lo, list, plan
     float* sc_part[2] = {};           // acc then (m, l), each of partial_rows() head rows
-    uint32_t* map_scratch = nullptr;  // slot_kv_extend_tables: CTA counter, new head
+    uint32_t* map_scratch = nullptr;  // table calls: CTA counter, new head
+    // tree calls: per-node words (request, depth, ancestors), allocated by the
+    // first one (their rotated q is sc_q); slot_kv_compact_pool's map of ids
+    uint32_t* tree_idx = nullptr;
+    uint32_t* compact_map = nullptr;
     std::vector<slotkv_host_call_s*> calls;  // prepared host calls on this handle
     cudaStream_t copy_stream = nullptr;      // their enqueued input copies (created on demand)
     // prefill_batch_attn_host in parts: its outputs' copies, the second
@@ -186,6 +192,8 @@ void release(slotkv_s* h) {
     cudaFree(h->sc_part[0]);
     cudaFree(h->sc_part[1]);
     cudaFree(h->map_scratch);
+    cudaFree(h->tree_idx);
+    cudaFree(h->compact_map);
     if (h->owns_kv) {
         cudaFree(h->K);
         cudaFree(h->V);
@@ -1404,6 +1412,230 @@ int slot_kv_extend_tables(slotkv_t h, uint32_t n_req, const uint32_t* past,
                                            ? (uint32_t)__builtin_ctz(h->slot_ctx) : 32u};
     const int rc = slotkv::launch_extend_tables(P, sm_total(h), (cudaStream_t)stream);
     if (rc != 0) return cuda_fail((cudaError_t)rc, "block table kernel launch");
+    return SLOTKV_OK;
+}
+
+// A tree call; slots or block_tables is null.
+static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head, const float* q,
+                     const float* k_new, const float* v_new, const uint32_t* slots,
+                     const uint32_t* block_tables, uint32_t bt_stride, const uint32_t* past,
+                     const uint32_t* starts, const uint32_t* parents, const float* q_norm_w,
+                     const float* k_norm_w, const float* inv_freq, const float* sinks,
+                     const slotkv_scores* scores, float* out, float eps, float scale,
+                     cudaStream_t s) {
+    if (n_req > h->max_rows)
+        return fail(SLOTKV_ERR_ARG, "n_req=%u exceeds max_rows=%u", n_req, h->max_rows);
+    if (n_req == 0 || n_tok == 0) return SLOTKV_OK;
+    if (!starts || !parents) return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (((uintptr_t)starts | (uintptr_t)parents | (uintptr_t)sinks) & 3)
+        return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    slotkv::TreeParams P;
+    const size_t R = h->max_rows;
+    int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, s, "tree workspace (q)");
+    if (rc == SLOTKV_OK)
+        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), R * (2 + slotkv::kTreeWords), s,
+                       "tree workspace (nodes)");
+    if (rc != SLOTKV_OK) return rc;
+    P.q = q;
+    P.k_new = k_new;
+    P.v_new = v_new;
+    P.slots = slots;
+    P.block_tables = block_tables;
+    P.bt_stride = bt_stride;
+    P.past = past;
+    P.starts = starts;
+    P.parents = parents;
+    P.q_norm_w = q_norm_w;
+    P.k_norm_w = k_norm_w;
+    P.inv_freq = inv_freq;
+    P.sinks = sinks;
+    P.out = out;
+    P.K = h->K;
+    P.V = h->V;
+    P.q_rot = h->sc_q;
+    P.anc = h->tree_idx;
+    P.req_of = P.anc + R * slotkv::kTreeWords;
+    P.depth = P.req_of + R;
+    P.status = h->status;
+    P.n_slots = h->n_slots;
+    P.slot_ctx = h->slot_ctx;
+    P.n_head = n_head;
+    P.n_kv_head = h->n_kv_head;
+    P.n_req = n_req;
+    P.n_tok = n_tok;
+    P.eps = eps;
+    P.scale_log2 = scale * 1.4426950408889634f;
+    P.flags = h->options;
+    P.rule = score_rule(scores);
+    rc = slotkv::launch_tree_attn((int)h->head_dim, P, s);
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "tree kernel launch");
+    return SLOTKV_OK;
+}
+
+int tree_batch_attn(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head, const float* q,
+                    const float* k_new, const float* v_new, const uint32_t* slots,
+                    const uint32_t* past, const uint32_t* starts, const uint32_t* parents,
+                    const float* q_norm_w, const float* k_norm_w, const float* inv_freq,
+                    const float* sinks, const slotkv_scores* scores, float* out, float eps,
+                    float scale, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, n_req ? n_tok : 0, n_head, q, k_new, v_new, past, slots,
+                               q_norm_w, k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, false);
+    if (rc != SLOTKV_OK) return rc;
+    return tree_call(h, n_req, n_tok, n_head, q, k_new, v_new, slots, nullptr, 0, past, starts,
+                     parents, q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps, scale,
+                     (cudaStream_t)stream);
+}
+
+int tree_batch_attn_paged(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head,
+                          const float* q, const float* k_new, const float* v_new,
+                          const uint32_t* block_tables, uint32_t bt_stride,
+                          const uint32_t* past, const uint32_t* starts, const uint32_t* parents,
+                          const float* q_norm_w, const float* k_norm_w, const float* inv_freq,
+                          const float* sinks, const slotkv_scores* scores, float* out, float eps,
+                          float scale, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    int rc = check_decode_args(h, n_req ? n_tok : 0, n_head, q, k_new, v_new, past, block_tables,
+                               q_norm_w, k_norm_w, inv_freq, out);
+    if (rc == SLOTKV_OK) rc = check_scores(scores, false);
+    if (rc != SLOTKV_OK) return rc;
+    const uint32_t T = (uint32_t)slotkv::tile_keys((int)h->head_dim);
+    if (h->slot_ctx % T != 0)
+        return fail(SLOTKV_ERR_UNSUPPORTED, "block size %u is not a multiple of %u keys",
+                    h->slot_ctx, T);
+    if (bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
+    return tree_call(h, n_req, n_tok, n_head, q, k_new, v_new, nullptr, block_tables, bt_stride,
+                     past, starts, parents, q_norm_w, k_norm_w, inv_freq, sinks, scores, out, eps,
+                     scale, (cudaStream_t)stream);
+}
+
+static slotkv::PoolView pool_view(const slotkv_s* h) {
+    return {h->K, h->V, h->n_slots, h->slot_ctx, h->kv_dim, h->status};
+}
+
+// slots or block_tables is null
+static int keep_path(slotkv_t h, uint32_t n_req, uint32_t n_tok, const uint32_t* slots,
+                     const uint32_t* block_tables, uint32_t bt_stride, const uint32_t* past,
+                     const uint32_t* starts, const uint32_t* n_keep, const uint32_t* path,
+                     cudaStream_t stream) {
+    if (!valid_handle(h)) return fail(SLOTKV_ERR_STATE, "handle is not allocated");
+    if (check_device(h) != SLOTKV_OK) return SLOTKV_ERR_STATE;
+    if (n_req > h->max_rows || n_tok > h->max_rows)
+        return fail(SLOTKV_ERR_ARG, "n_req=%u or n_tok=%u exceeds max_rows=%u", n_req, n_tok,
+                    h->max_rows);
+    if (n_req == 0 || n_tok == 0) return SLOTKV_OK;
+    if ((!slots && !block_tables) || !past || !starts || !n_keep || !path)
+        return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (((uintptr_t)slots | (uintptr_t)block_tables | (uintptr_t)past | (uintptr_t)starts |
+         (uintptr_t)n_keep | (uintptr_t)path) & 3)
+        return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    const slotkv::KeepPathParams P{pool_view(h), slots,  block_tables, past,  starts,
+                                   n_keep,       path,   n_req,        n_tok, bt_stride};
+    const int rc = slotkv::launch_keep_path(P, stream);
+    if (rc != 0) return cuda_fail((cudaError_t)rc, "keep path kernel launch");
+    return SLOTKV_OK;
+}
+
+int slot_kv_keep_path(slotkv_t h, uint32_t n_req, uint32_t n_tok, const uint32_t* slots,
+                      const uint32_t* past, const uint32_t* starts, const uint32_t* n_keep,
+                      const uint32_t* path, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    return keep_path(h, n_req, n_tok, slots, nullptr, 0, past, starts, n_keep, path,
+                     (cudaStream_t)stream);
+}
+
+int slot_kv_keep_path_paged(slotkv_t h, uint32_t n_req, uint32_t n_tok,
+                            const uint32_t* block_tables, uint32_t bt_stride,
+                            const uint32_t* past, const uint32_t* starts, const uint32_t* n_keep,
+                            const uint32_t* path, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    if (valid_handle(h) && bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
+    return keep_path(h, n_req, n_tok, nullptr, block_tables, bt_stride, past, starts, n_keep,
+                     path, (cudaStream_t)stream);
+}
+
+// What the calls on tables check alike; n: their rows.
+static int check_tables(slotkv_t h, uint32_t n, uint32_t bt_stride, bool pointers,
+                        uintptr_t all) {
+    if (!valid_handle(h)) return fail(SLOTKV_ERR_STATE, "handle is not allocated");
+    if (check_device(h) != SLOTKV_OK) return SLOTKV_ERR_STATE;
+    if (n > SLOTKV_MAX_REQUESTS)
+        return fail(SLOTKV_ERR_ARG, "%u requests exceed %u", n, SLOTKV_MAX_REQUESTS);
+    if (bt_stride == 0) return fail(SLOTKV_ERR_ARG, "bt_stride must be >= 1");
+    if (!pointers) return fail(SLOTKV_ERR_ARG, "null tensor pointer");
+    if (all & 3) return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
+    return SLOTKV_OK;
+}
+
+int slot_kv_fork_tables(slotkv_t h, uint32_t n_fork, const uint32_t* src, uint32_t n_rows,
+                        const uint32_t* past, const uint32_t* block_tables, uint32_t bt_stride,
+                        uint32_t* out_tables, uint32_t* shares, const uint32_t* free_blocks,
+                        uint32_t n_free, const uint32_t* head, uint32_t* head_out,
+                        slotkv_stream_t stream) {
+    g_err[0] = 0;
+    const bool all = head && head_out && shares && (!n_fork || (src && out_tables)) &&
+                     (!n_rows || (past && block_tables)) && (!n_free || free_blocks);
+    const int rc = check_tables(h, std::max(n_fork, n_rows), bt_stride, all,
+                                (uintptr_t)src | (uintptr_t)past | (uintptr_t)block_tables |
+                                    (uintptr_t)out_tables | (uintptr_t)shares |
+                                    (uintptr_t)free_blocks | (uintptr_t)head | (uintptr_t)head_out);
+    if (rc != SLOTKV_OK) return rc;
+    if (n_fork && n_rows) {
+        const uint32_t *a = block_tables, *b = out_tables;
+        if (b < a + (size_t)n_rows * bt_stride && a < b + (size_t)n_fork * bt_stride)
+            return fail(SLOTKV_ERR_ARG, "out_tables overlaps block_tables");
+    }
+    const slotkv::ForkTablesParams P{pool_view(h), src,         past, block_tables,
+                                     out_tables,   shares,      free_blocks, head,
+                                     head_out,     h->map_scratch, n_fork, n_rows,
+                                     bt_stride,    n_free};
+    const int e = slotkv::launch_fork_tables(P, sm_total(h), (cudaStream_t)stream);
+    if (e != 0) return cuda_fail((cudaError_t)e, "fork tables kernel launch");
+    return SLOTKV_OK;
+}
+
+int slot_kv_free_tables(slotkv_t h, uint32_t n_req, const uint32_t* past, const uint32_t* keep,
+                        const uint32_t* block_tables, uint32_t bt_stride, uint32_t* shares,
+                        uint32_t* free_blocks, uint32_t n_free, const uint32_t* head,
+                        uint32_t* head_out, slotkv_stream_t stream) {
+    g_err[0] = 0;
+    const bool all = head && head_out && (!n_req || (past && block_tables)) &&
+                     (!n_free || free_blocks);
+    const int rc = check_tables(h, n_req, bt_stride, all,
+                                (uintptr_t)past | (uintptr_t)keep | (uintptr_t)block_tables |
+                                    (uintptr_t)shares | (uintptr_t)free_blocks | (uintptr_t)head |
+                                    (uintptr_t)head_out);
+    if (rc != SLOTKV_OK) return rc;
+    if ((uint64_t)n_req * bt_stride > (1ull << 30))
+        return fail(SLOTKV_ERR_ARG, "n_req * bt_stride exceeds 2^30");
+    const slotkv::FreeTablesParams P{pool_view(h), past,   keep,  block_tables, shares, free_blocks,
+                                     head,         head_out, n_req, bt_stride,  n_free};
+    const int e = slotkv::launch_free_tables(P, (cudaStream_t)stream);
+    if (e != 0) return cuda_fail((cudaError_t)e, "free tables kernel launch");
+    return SLOTKV_OK;
+}
+
+int slot_kv_compact_pool(slotkv_t h, uint32_t n_req, const uint32_t* past,
+                         uint32_t* block_tables, uint32_t bt_stride, uint32_t* shares,
+                         uint32_t* free_blocks, uint32_t n_free, uint32_t* head,
+                         slotkv_stream_t stream) {
+    g_err[0] = 0;
+    const bool all = head && (!n_req || (past && block_tables)) && (!n_free || free_blocks);
+    int rc = check_tables(h, n_req, bt_stride, all,
+                          (uintptr_t)past | (uintptr_t)block_tables | (uintptr_t)shares |
+                              (uintptr_t)free_blocks | (uintptr_t)head);
+    if (rc != SLOTKV_OK) return rc;
+    if ((uint64_t)n_req * bt_stride > (1ull << 30))
+        return fail(SLOTKV_ERR_ARG, "n_req * bt_stride exceeds 2^30");
+    rc = first_use(reinterpret_cast<float**>(&h->compact_map),
+                   slotkv::compact_scratch_words(h->n_slots), (cudaStream_t)stream,
+                   "compaction workspace");
+    if (rc != SLOTKV_OK) return rc;
+    const slotkv::CompactPoolParams P{pool_view(h), past, block_tables,   shares, free_blocks,
+                                      head,         h->compact_map, n_req, bt_stride, n_free};
+    const int e = slotkv::launch_compact_pool(P, sm_total(h), (cudaStream_t)stream);
+    if (e != 0) return cuda_fail((cudaError_t)e, "compact pool kernel launch");
     return SLOTKV_OK;
 }
 

@@ -1,0 +1,47 @@
+// tree_attn.h -- launch parameters of the attention of drafted trees
+// (tree_attn.cuh).  Plain data only.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "params.h"
+
+namespace slotkv {
+
+// Nodes a request's tree may have, and the words of a set of them.
+constexpr uint32_t kTreeNodes = 256, kTreeWords = kTreeNodes / 32;
+
+struct TreeParams {
+    const float* q;          // [n_tok][n_head][hd]
+    const float* k_new;      // [n_tok][n_kv_head][hd]
+    const float* v_new;
+    const uint32_t* slots;   // [n_req], or null: paged
+    const uint32_t* block_tables;  // [n_req][bt_stride]
+    const uint32_t* past;    // [n_req]
+    const uint32_t* starts;  // [n_req + 1]
+    const uint32_t* parents; // [n_tok]
+    const float* q_norm_w;   // [hd]
+    const float* k_norm_w;
+    const float* inv_freq;   // [hd/2]
+    const float* sinks;      // [n_head] or null
+    float* out;              // [n_tok][n_head][hd]
+    float* K;                // [n_slots][slot_ctx][n_kv_head][hd]
+    float* V;
+    float* q_rot;            // workspace [n_tok][n_head][hd]: normed, rotated, scaled q
+    uint32_t* req_of;        // workspace [n_tok]: the node's request, kTreeSkip: skipped
+    uint32_t* depth;         // workspace [n_tok]
+    uint32_t* anc;           // workspace [n_tok][kTreeWords]: the node's ancestors and itself
+    uint32_t* status;        // sticky SLOTKV_DEV_* flags
+    uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
+    float eps;
+    float scale_log2;        // softmax scale * log2(e)
+    uint32_t flags;          // SLOTKV_OPT_* norm options
+    ScoreRule rule;          // doc_start: [n_req]
+};
+constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
+
+// Enqueues the kernels of a call; returns a cudaError_t value.
+int launch_tree_attn(int hd, const TreeParams& p, cudaStream_t stream);
+
+}  // namespace slotkv
