@@ -559,11 +559,12 @@ int tree_batch_attn_paged(slotkv_t handle, uint32_t n_req, uint32_t n_tok, uint3
  *   path    device u32[n_tok]: the path's nodes from path[starts[r]] on,
  *           strictly increasing, below the request's number of nodes.
  *   n_keep  device u32[n_req], 0: the request is left alone.
- * The others as in tree_batch_attn (any block size).  A request that keeps
+ * The others as in tree_batch_attn (any block size; n_req and n_tok are not
+ * bound by max_rows).  A request that keeps
  * nodes and is out of range as there, or whose path is not strictly
  * increasing or leaves its nodes, is left alone with SLOTKV_DEV_RANGE.  A
  * row's bits are copied.  Asynchronous, one kernel; errors SLOTKV_ERR_ARG
- * (NULL or misaligned pointer, n_req > max_rows, bt_stride = 0),
+ * (NULL or misaligned pointer, n_req too large, bt_stride = 0),
  * SLOTKV_ERR_STATE, SLOTKV_ERR_CUDA.
  */
 int slot_kv_keep_path(slotkv_t handle, uint32_t n_req, uint32_t n_tok, const uint32_t* slots,

@@ -21,7 +21,8 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["slotkv.cu", "decode_attn_hd64.cu", "decode_attn_hd128.cu", "decode_attn_hd256.cu",
            "noalloc.cu", "prefill_tc_hd64.cu", "prefill_tc_hd128.cu", "scored_decode_hd64.cu",
            "scored_decode_hd128.cu", "scored_decode_hd256.cu", "scored_prefill_hd64.cu",
-           "scored_prefill_hd128.cu", "maps.cu", "tree_attn.cu", "pages.cu"]
+           "scored_prefill_hd128.cu", "maps.cu", "tree_attn_hd64.cu",
+           "tree_attn_hd128.cu", "tree_attn_hd256.cu", "pages.cu"]
 DEPS = ["params.h", "maps.h", "pages.h", "tree_attn.h", "tree_attn.cuh", "score_rule.cuh",
         "decode_attn.cuh", "decode_small.cuh", "prefill_tc.cuh", "tc_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

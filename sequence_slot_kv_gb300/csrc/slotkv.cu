@@ -111,9 +111,14 @@ struct slotkv_s {
     uint32_t* sc_idx = nullptr;       // rec, tiles, tile_of, tile_lo, list, plan
     float* sc_part[2] = {};           // acc then (m, l), each of partial_rows() head rows
     uint32_t* map_scratch = nullptr;  // table calls: CTA counter, new head
-    // tree calls: per-node words (request, depth, ancestors), allocated by the
-    // first one (their rotated q is sc_q); slot_kv_compact_pool's map of ids
+    // tree calls: views of the buffers for slots [0] and pages [1], keys of a
+    // box of K in each (0: no pages); per-node words (request, depth,
+    // ancestors) and the requests' first tiles, and partial results, allocated by
+    // the first one (their rotated q is sc_q); slot_kv_compact_pool's map of ids
+    CUtensorMap tmKt[2], tmVt[2];
+    uint32_t tree_box[2] = {};
     uint32_t* tree_idx = nullptr;
+    float* tree_part = nullptr;
     uint32_t* compact_map = nullptr;
     std::vector<slotkv_host_call_s*> calls;  // prepared host calls on this handle
     cudaStream_t copy_stream = nullptr;      // their enqueued input copies (created on demand)
@@ -193,6 +198,7 @@ void release(slotkv_s* h) {
     cudaFree(h->sc_part[1]);
     cudaFree(h->map_scratch);
     cudaFree(h->tree_idx);
+    cudaFree(h->tree_part);
     cudaFree(h->compact_map);
     if (h->owns_kv) {
         cudaFree(h->K);
@@ -257,6 +263,25 @@ int encode_maps(slotkv_s* h) {
                 return fail(SLOTKV_ERR_CUDA, "cuTensorMapEncodeTiled (swizzled) failed (%d)",
                             (int)r);
         }
+    }
+    // tree calls: a slot's keys 128 at a time, a pool's by the largest power of
+    // two up to that which divides the block
+    const uint32_t low = h->slot_ctx & (0u - h->slot_ctx);
+    h->tree_box[0] = 128;
+    h->tree_box[1] = h->slot_ctx % (uint32_t)slotkv::tile_keys((int)h->head_dim) ? 0 : std::min(low, 128u);
+    for (int i = 0; i < 2 && h->tree_box[i]; ++i) {
+        const cuuint32_t kbox[2] = {32, h->tree_box[i]};
+        const cuuint32_t vbox[2] = {slotkv::tree_v_dims((int)h->head_dim),
+                                    std::min(h->tree_box[i], slotkv::tree_v_keys((int)h->head_dim))};
+        CUresult r = enc(&h->tmKt[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, h->K, dims, strides, kbox, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r == CUDA_SUCCESS)
+            r = enc(&h->tmVt[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, h->V, dims, strides, vbox, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS)
+            return fail(SLOTKV_ERR_CUDA, "cuTensorMapEncodeTiled (trees) failed (%d)", (int)r);
     }
     return SLOTKV_OK;
 }
@@ -1433,8 +1458,11 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     const size_t R = h->max_rows;
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, s, "tree workspace (q)");
     if (rc == SLOTKV_OK)
-        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), R * (2 + slotkv::kTreeWords), s,
-                       "tree workspace (nodes)");
+        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), 2 * (R + 1) + R * (2 + slotkv::kTreeWords),
+                       s, "tree workspace (nodes)");
+    const size_t pr = slotkv::tree_partial_rows((int)h->head_dim, sm_total(h));
+    if (rc == SLOTKV_OK)
+        rc = first_use(&h->tree_part, pr * (2 + h->head_dim), s, "tree workspace (partials)");
     if (rc != SLOTKV_OK) return rc;
     P.q = q;
     P.k_new = k_new;
@@ -1453,8 +1481,13 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     P.K = h->K;
     P.V = h->V;
     P.q_rot = h->sc_q;
-    P.anc = h->tree_idx;
+    P.base = reinterpret_cast<uint64_t*>(h->tree_idx);
+    P.anc = h->tree_idx + 2 * (R + 1);
     P.req_of = P.anc + R * slotkv::kTreeWords;
+    P.part = h->tree_part;
+    P.part_ml = P.part + pr * h->head_dim;
+    const int paged = block_tables ? 1 : 0;
+    P.box_keys = h->tree_box[paged];
     P.depth = P.req_of + R;
     P.status = h->status;
     P.n_slots = h->n_slots;
@@ -1467,7 +1500,10 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     P.scale_log2 = scale * 1.4426950408889634f;
     P.flags = h->options;
     P.rule = score_rule(scores);
-    rc = slotkv::launch_tree_attn((int)h->head_dim, P, s);
+    auto run = h->head_dim == 64    ? slotkv::launch_tree_hd64
+               : h->head_dim == 128 ? slotkv::launch_tree_hd128
+                                    : slotkv::launch_tree_hd256;
+    rc = run(P, h->tmKt[paged], h->tmVt[paged], sm_total(h), s);
     if (rc != 0) return cuda_fail((cudaError_t)rc, "tree kernel launch");
     return SLOTKV_OK;
 }
@@ -1521,9 +1557,8 @@ static int keep_path(slotkv_t h, uint32_t n_req, uint32_t n_tok, const uint32_t*
                      cudaStream_t stream) {
     if (!valid_handle(h)) return fail(SLOTKV_ERR_STATE, "handle is not allocated");
     if (check_device(h) != SLOTKV_OK) return SLOTKV_ERR_STATE;
-    if (n_req > h->max_rows || n_tok > h->max_rows)
-        return fail(SLOTKV_ERR_ARG, "n_req=%u or n_tok=%u exceeds max_rows=%u", n_req, n_tok,
-                    h->max_rows);
+    if (n_req > SLOTKV_MAX_REQUESTS)
+        return fail(SLOTKV_ERR_ARG, "n_req=%u exceeds %u", n_req, SLOTKV_MAX_REQUESTS);
     if (n_req == 0 || n_tok == 0) return SLOTKV_OK;
     if ((!slots && !block_tables) || !past || !starts || !n_keep || !path)
         return fail(SLOTKV_ERR_ARG, "null tensor pointer");

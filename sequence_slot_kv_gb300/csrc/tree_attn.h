@@ -32,8 +32,12 @@ struct TreeParams {
     uint32_t* req_of;        // workspace [n_tok]: the node's request, kTreeSkip: skipped
     uint32_t* depth;         // workspace [n_tok]
     uint32_t* anc;           // workspace [n_tok][kTreeWords]: the node's ancestors and itself
+    float* part;             // workspace: partial results, two of a unit's rows per CTA [rows][hd]
+    float* part_ml;          // and their (m, l)
+    uint64_t* base;          // workspace [n_req + 1]: the requests' first tiles
     uint32_t* status;        // sticky SLOTKV_DEV_* flags
     uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
+    uint32_t box_keys;       // keys of one TMA box of K: a power of two, at most 128
     float eps;
     float scale_log2;        // softmax scale * log2(e)
     uint32_t flags;          // SLOTKV_OPT_* norm options
@@ -41,7 +45,22 @@ struct TreeParams {
 };
 constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
 
-// Enqueues the kernels of a call; returns a cudaError_t value.
-int launch_tree_attn(int hd, const TreeParams& p, cudaStream_t stream);
+// Rows of a block (a unit of work), and the keys and dims of a piece of V.
+__host__ __device__ constexpr uint32_t tree_rows(int hd) { return hd == 256 ? 32u : 64u; }
+__host__ __device__ constexpr uint32_t tree_v_dims(int hd) { return hd < 128 ? hd : 128u; }
+__host__ __device__ constexpr uint32_t tree_v_keys(int hd) { return 4096u / tree_v_dims(hd); }
+// Head rows of partial results that a call can leave on `sms` CTAs.
+inline size_t tree_partial_rows(int hd, uint32_t sms) { return (size_t)2 * sms * tree_rows(hd); }
+
+// Enqueue the kernels of a call (prep, attention on `sms` CTAs, combine); tmK:
+// the 128-byte-swizzled view of K with boxes of 32 floats x box_keys rows, tmV:
+// V's with boxes of tree_v_dims(hd) floats x min(box_keys, tree_v_keys(hd))
+// rows, not swizzled.  Return a cudaError_t value.
+int launch_tree_hd64(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, uint32_t sms,
+                     cudaStream_t stream);
+int launch_tree_hd128(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, uint32_t sms,
+                      cudaStream_t stream);
+int launch_tree_hd256(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, uint32_t sms,
+                      cudaStream_t stream);
 
 }  // namespace slotkv

@@ -343,3 +343,22 @@ def test_cache_past_32_bits():
     c.run(kv)
     c.check(K0, V0)
     kv.free()
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("past", [300, 30000])
+def test_a_wait_that_runs_out_ends_the_call(hd, past):
+    """The stalled pipeline (a signal withheld): the call ends by itself with the
+    flag raised, and the handle works afterwards."""
+    c = Case(requests(2, [(past, 16), (64, 7)]), 1, 4, hd)
+    kv = c.handle()
+    kv.set_options(skv.OPT_TEST_STALL)
+    c.run(kv)
+    assert kv.get_status() & skv.DEV_TIMEOUT
+    kv.set_options(0)
+    c.out.fill_(7.5)
+    K0, V0 = c.K.clone(), c.V.clone()
+    c.run(kv)
+    c.check(K0, V0)
+    assert kv.get_status() == 0
+    kv.free()
