@@ -212,20 +212,28 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // transposition free.  At head dim 64 one A holds V^T's high part in lanes 0-63
 // and its low part in lanes 64-127, and one MMA forms all four products.
 //
-// Roles (14 warps):
-//   0-3   softmax: a thread per key of the tile.  Q rows into shared memory at a
-//         unit's start; then per tile S from tensor memory, the rule and the
-//         masks, P^T (hi, lo) into shared memory.  The running maxima are raised
-//         lazily (by 2^8), all 128 threads agreeing at a named barrier.
-//   4-7   converters: K's low part and V^T (hi, lo) into tensor memory.
-//   8-11  accumulators: a thread per dim.  Every tile's O^T starts anew in
+// Roles (eight warpgroups; the converters' and the last one's registers go to
+// the accumulators):
+//   0-3   softmax: a thread per key of the tile, each warpgroup every fourth group
+//         of 8 rows.  Q rows into shared memory at a unit's start; then per tile S
+//         from tensor memory, the rule and the masks, P^T (hi, lo) into shared
+//         memory, the rows' sums in registers.  The running maxima are raised
+//         lazily (by 2^8), the 128 threads agreeing at a named barrier.  (The MMAs
+//         take most of what shared memory gives, so these loads and stores have
+//         long latencies, which more warps hide.)
+//   4     accumulators: a thread per dim.  Every tile's O^T starts anew in
 //         tensor memory (its chain of sums is cut toward zero at each step) and
-//         is added to registers with rounded adds; also the rows' sums, from P.
-//         At the end out, or the unit's partial result.
-//   12    producer: 16 KB pieces of K (128 keys x 32 dims, swizzled) and V by TMA
-//         into a ring.  13: MMA issuer.
+//         is added to registers with rounded adds.  At the end out, or the
+//         unit's partial result.
+//   5, 6  converters: K's low part, and V^T (hi, lo), into tensor memory.
+//   7     producer (16 KB pieces of K, 128 keys x 32 dims, swizzled, and of V by TMA
+//         into a ring), two MMA issuers, and a warp that finds the CTA's units and
+//         tells the others.
 // The pieces go K(0), K(1), V(0), K(2), V(1), ...: S(t + 1) is formed while the
-// softmax of tile t runs.
+// softmax of tile t runs.  P is handed over by blocks of 32 keys (a warp of each
+// softmax warpgroup writes one), so tile t + 1's first blocks are written while
+// the MMAs read tile t's last ones.  A unit's tiles go from its last keys to its first, so
+// that a distance bias raises no maximum tile after tile.
 //
 // The tiles of all units, in order, are cut into one equal range per CTA (every
 // CTA finds its own from the lengths), so a unit may lie in several CTAs; each
@@ -253,36 +261,41 @@ struct TreeCfg {
     static constexpr int QBYTES = 2 * RB * HD * 4, PBYTES = 2 * RB * KT * 4;
     static constexpr int OFF_P = QBYTES, OFF_RING = QBYTES + PBYTES;
     static constexpr int NSLOT = (224 * 1024 - OFF_RING) / PIECE;  // 8, 6, 8
-    static constexpr int NKL = 4, NV = 2;               // buffers of K lo and of V^T
+    static constexpr int NKL = HD == 256 ? 4 : 2, NV = HD == 64 ? 2 : 3;  // buffers of K lo and of V^T
     // tensor memory columns
     static constexpr int C_S = 0, C_O = 2 * RB, C_KL = C_O + DH * 2 * RB, C_V = C_KL + NKL * 32;
     static constexpr int VCOLS = 64;                    // a V^T buffer: hi | lo, 32 keys each (FOLD: 64 keys)
     static_assert(C_V + NV * VCOLS <= 512, "tensor memory");
     static constexpr int TMEM_COLS = 512;
     // shared memory behind the ring: row data, scratch of the maxima, barriers, flags
-    static constexpr int OFF_M = OFF_RING + NSLOT * PIECE;      // running maxima [RB]
-    static constexpr int OFF_F = OFF_M + RB * 4;                // factors of a raise [RB]
-    static constexpr int OFF_L = OFF_F + RB * 4;                // sums [RB]
-    static constexpr int OFF_POS = OFF_L + RB * 4;              // rows' positions [RB]
-    static constexpr int OFF_LO = OFF_POS + RB * 4;             // rows' first position attended [RB]
-    static constexpr int OFF_SLOPE = OFF_LO + RB * 4;           // rows' slopes [RB]
-    static constexpr int OFF_MAX = OFF_SLOPE + RB * 4;          // tile maxima [4][RB]
-    static constexpr int OFF_BAR = OFF_MAX + 4 * RB * 4;
-    // full, K empty, V empty [NSLOT]; K lo full, empty [NKL]; V full, empty [NV]; S full, empty;
-    // P full, empty; O full, empty; Q full; unit's end; drain
-    static constexpr int NBAR = 3 * NSLOT + 2 * NKL + 2 * NV + 9;
+    static constexpr int OFF_M = OFF_RING + NSLOT * PIECE;      // running maxima [2 units][RB]
+    static constexpr int OFF_F = OFF_M + 2 * RB * 4;            // factors of a raise, of the end [RB]
+    static constexpr int OFF_POS = OFF_F + RB * 4;              // rows' positions [RB]
+    static constexpr int OFF_SLOPE = OFF_POS + RB * 4;          // rows' slopes [RB]
+    static constexpr int OFF_MAX = OFF_SLOPE + RB * 4;          // a warp's maxima, its sums [4][RB]
+    static constexpr int OFF_DESC = OFF_MAX + 4 * RB * 4;       // what the roles need to know of a unit [2]
+    static constexpr int OFF_BAR = OFF_DESC + 2 * 12 * 4;
+    // K landed, V landed, K empty, V empty [NSLOT]; K lo full, empty [NKL]; V full, empty [NV];
+    // S full, empty; P full, empty [4]; tile done with; O full, empty; Q full; unit's end; drain [2];
+    // unit known, done with [2].
+    // (A slot takes K and V in turn; barriers of their own let each kind's readers see every phase.)
+    static constexpr int NBAR = 4 * NSLOT + 2 * NKL + 2 * NV + 21;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + 64;
+    static constexpr int SMEM = OFF_MISC + 56;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static constexpr int CW = RB / 4;                   // rows of a softmax warpgroup
     static_assert(OFF_BAR % 8 == 0 && NSLOT >= 6, "layout");
 };
-constexpr int kTreeWarps = 14, kTreeThreads = 32 * kTreeWarps;
+constexpr int kTreeWarps = 32, kTreeThreads = 32 * kTreeWarps;
+// registers of a thread: at launch (and of the softmax), and of the others from there on
+constexpr int kTreeRegs = 64, kRegAcc = 112, kRegConv = 48, kRegAux = 48;
+static_assert(4 * kTreeRegs + kRegAcc + 2 * kRegConv + kRegAux == kTreeWarps / 4 * kTreeRegs,
+              "register hand-over must add up to the launch's registers");
 
-// A part of a unit: its rows, and its tiles [t0, t1) of tl, from absolute tile
-// tile0 on.
-struct TreeSeg {
-    uint32_t r, s0, n, past, g, row0, rows, tile0, t0, t1, tl;
-};
+// What a role reads of a unit (or the part of it that the CTA has), in words of
+// shared memory.  Tiles go from the last keys to the first: tile t of the part
+// begins at place d[kPlace] - 128 t.
+enum TreeWord { kReq, kRow, kNodes, kPast, kKvHead, kRow0, kRows, kPlace, kTiles, kStart, kWhole, kMore };
 
 // A request's shape: row blocks, first tile, tiles; 0 blocks: nothing to do.
 struct TreeShape {
@@ -317,14 +330,14 @@ __device__ __forceinline__ uint32_t tree_owner(uint64_t total, uint32_t ctas, ui
     return static_cast<uint32_t>(((x + 1) * ctas - 1) / total);
 }
 
-// A CTA's segments in order; every role walks them by itself.
+// A CTA's parts of units, in order.
 template <int RB>
 struct TreeWalk {
     uint32_t r;
     uint64_t off, left;  // tiles into request r, tiles left
     TreeShape x;
     bool known;
-    __device__ bool next(const TreeParams& P, TreeSeg& s) {
+    __device__ bool next(const TreeParams& P, uint32_t (&d)[12]) {
         if (left == 0) return false;
         for (;;) {
             if (!known) {
@@ -338,21 +351,23 @@ struct TreeWalk {
             known = false;
         }
         const uint32_t unit = static_cast<uint32_t>(off / x.tl);
-        s.r = r;
-        s.s0 = x.q.s0;
-        s.n = x.q.n;
-        s.past = x.q.past;
-        s.g = unit / x.nb;
-        s.row0 = unit % x.nb * RB;
-        const uint32_t all = x.q.n * (P.n_head / P.n_kv_head) - s.row0;
-        s.rows = all < RB ? all : RB;
-        s.tile0 = x.tile0;
-        s.tl = x.tl;
-        s.t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
-        const uint64_t end = s.t0 + left;
-        s.t1 = end < x.tl ? static_cast<uint32_t>(end) : x.tl;
-        off += s.t1 - s.t0;
-        left -= s.t1 - s.t0;
+        const uint32_t t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
+        const uint32_t n = left < x.tl - t0 ? static_cast<uint32_t>(left) : x.tl - t0;
+        const uint32_t row0 = unit % x.nb * RB, all = x.q.n * (P.n_head / P.n_kv_head) - row0;
+        d[kReq] = r;
+        d[kRow] = x.q.s0;
+        d[kNodes] = x.q.n;
+        d[kPast] = x.q.past;
+        d[kKvHead] = unit / x.nb;
+        d[kRow0] = row0;
+        d[kRows] = all < RB ? all : RB;
+        d[kPlace] = (x.tile0 + x.tl - 1 - t0) * 128;
+        d[kTiles] = n;
+        d[kStart] = t0 == 0 ? 1u : 0u;
+        d[kWhole] = n == x.tl ? 1u : 0u;
+        d[kMore] = 1u;
+        off += n;
+        left -= n;
         return true;
     }
 };
@@ -389,15 +404,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t sbase = smem_addr(smem);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
-    // misc: [0] abort, [1] a raise comes with P, [2], [3] the last tile (even, odd; plus 1) with
-    // a V value that is not finite, [4] tensor memory
+    // misc: [0] abort, [1] tensor memory; tiles (plus 1): [2 + 4 (tile & 1) + block] the last with a
+    // V value that is not finite in that block of 32 keys, [10 + softmax warpgroup] the last
+    // with a raise
     const uint32_t bar0 = sbase + C::OFF_BAR;
-    const uint32_t FULL = bar0, KE = FULL + 8 * NSLOT, VE = KE + 8 * NSLOT, KLF = VE + 8 * NSLOT,
+    const uint32_t KF = bar0, VL = KF + 8 * NSLOT, KE = VL + 8 * NSLOT, VE = KE + 8 * NSLOT, KLF = VE + 8 * NSLOT,
                    KLE = KLF + 8 * C::NKL, VF = KLE + 8 * C::NKL, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
-                   SE = SF + 8, PF = SE + 8, PE = PF + 8, OF = PE + 8, OE = OF + 8, QF = OE + 8, UE = QF + 8, DRAIN = UE + 8;
+                   SE = SF + 8, PF = SE + 8, PE = PF + 32, FX = PE + 32, OF = FX + 8, OE = OF + 8, QF = OE + 8,
+                   UE = QF + 8, DRAIN = UE + 8, GF = DRAIN + 16, GE = GF + 16;
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) {
-            mbar_init(FULL + 8 * i, 1);
+            mbar_init(KF + 8 * i, 1);
+            mbar_init(VL + 8 * i, 1);
             mbar_init(KE + 8 * i, 1);
             mbar_init(VE + 8 * i, 4);
         }
@@ -410,19 +428,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(VFE + 8 * i, 1);
         }
         mbar_init(SF, 1);
-        mbar_init(SE, 4);
-        mbar_init(PF, 4);
-        mbar_init(PE, 5);
+        mbar_init(SE, 16);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(PF + 8 * i, 4);
+            mbar_init(PE + 8 * i, 1);
+        }
+        mbar_init(FX, 4);
         mbar_init(OF, 1);
         mbar_init(OE, 4);
-        mbar_init(QF, 4);
+        mbar_init(QF, 16);
         mbar_init(UE, 4);
         mbar_init(DRAIN, 1);
+        mbar_init(DRAIN + 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(GF + 8 * i, 1);
+            mbar_init(GE + 8 * i, 31);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        for (int i = 0; i < 4; ++i) misc[i] = 0;
+        for (int i = 0; i < 14; ++i) misc[i] = 0;
     }
-    if (warp == 13) {
-        tc::tmem_alloc(sbase + C::OFF_MISC + 16, C::TMEM_COLS);
+    if (warp == 29) {
+        tc::tmem_alloc(sbase + C::OFF_MISC + 4, C::TMEM_COLS);
         tc::tmem_relinquish();
     }
     // this CTA's range: every thread sums a part of the requests, a scan finds the
@@ -476,12 +502,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (tid == 0) P.base[P.n_req] = total;
     }
     __syncthreads();
-    TreeWalk<RB> walk;
-    walk.known = false;
-    walk.r = work ? static_cast<uint32_t>(found[0]) : 0u;
-    walk.off = work ? found[1] : 0u;
-    walk.left = work ? u1 - u0 : 0u;
-    const uint32_t tb = __shfl_sync(0xffffffffu, misc[4], 0);
+    const uint32_t tb = __shfl_sync(0xffffffffu, misc[1], 0);
+    const uint32_t r_first = work ? static_cast<uint32_t>(found[0]) : 0u;
+    const uint64_t off_first = work ? found[1] : 0u;
     __syncthreads();  // (the scan's words are Q's from here on)
 
     // A bounded wait; once the CTA has given up every wait ends at once.
@@ -500,576 +523,649 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
+    // unit k of the CTA: its words, once they are there; done with them
+    auto words = [&](uint32_t k) {
+        return reinterpret_cast<const volatile uint32_t*>(smem + C::OFF_DESC) + 12 * (k & 1);
+    };
+    auto known = [&](uint32_t k) { return warp_wait(GF + 8 * (k & 1), (k >> 1) & 1); };
+    auto done = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(GE + 8 * (k & 1));
+    };
     const uint32_t G = P.n_head / P.n_kv_head;
-    TreeSeg s;
 
-    if (warp < 4) {
+    if (warp < 16) {
         // ------------------------------------------------------------ softmax
         grid_dependency_wait();
-        float* ms = reinterpret_cast<float*>(smem + C::OFF_M);
-        float* fs = reinterpret_cast<float*>(smem + C::OFF_F);
+        constexpr int CW = C::CW;
+        const int sg = warp >> 2, key = tid & 127, wq = warp & 3;  // warpgroup, key of the tile, lane quarter
+        const int bar_id = 1 + sg;
+        // row of the block of this warpgroup's row c
+        auto row_of = [&](int c) { return 32 * (c / 8) + 8 * sg + c % 8; };
+        float* fs = reinterpret_cast<float*>(smem + C::OFF_F) + 8 * sg;
         float* tmax = reinterpret_cast<float*>(smem + C::OFF_MAX);
-        uint32_t* posr = reinterpret_cast<uint32_t*>(smem + C::OFF_POS);
-        uint32_t* lor = reinterpret_cast<uint32_t*>(smem + C::OFF_LO);
-        float* sloper = reinterpret_cast<float*>(smem + C::OFF_SLOPE);
-        const CapSeries series = cap_series(P.rule.cap_in);
-        const uint32_t tlane = tb + (static_cast<uint32_t>(warp) << 21);
-        const int key = tid;  // of the tile
+        uint32_t* posr = reinterpret_cast<uint32_t*>(smem + C::OFF_POS) + 8 * sg;
+        float* sloper = reinterpret_cast<float*>(smem + C::OFF_SLOPE) + 8 * sg;
+        const uint32_t tlane = tb + (static_cast<uint32_t>(wq) << 21);
         bool ok = true;
         uint32_t gt = 0;  // tiles so far
-        for (uint32_t units = 0; walk.next(P, s); ++units) {
-            const uint32_t Rp = (s.rows + 15) / 16 * 16;
-            // the accumulators are done with the unit before: its maxima, and P's buffer
-            if (units) ok = warp_wait(UE, (units - 1) & 1) && warp_wait(PE, (gt - 1) & 1) && ok;
-            if (tid < RB) {
-                ms[tid] = -1e30f;
-                const uint32_t row = tid < static_cast<int>(s.rows) ? tid : s.rows - 1;
-                const uint32_t node = (s.row0 + row) / G, h = s.g * G + (s.row0 + row) % G;
-                const uint32_t pos = s.past + P.depth[s.s0 + node];
-                posr[tid] = pos;
-                lor[tid] = SC ? rule_first(P.rule, s.r, pos) : 0u;
-                sloper[tid] = SC && P.rule.slopes ? __ldg(P.rule.slopes + h) * kRuleLog2e : 0.f;
+        for (uint32_t u = 0;; ++u) {
+            ok = known(u) && ok;
+            const volatile uint32_t* d = words(u);
+            // (the four warps go on, or leave, together)
+            if (bar_or(bar_id, !ok || !d[kMore])) break;
+            const uint32_t rows = d[kRows], Rp = (rows + 15) / 16 * 16;
+            float* ms = reinterpret_cast<float*>(smem + C::OFF_M) + (u & 1) * RB + 8 * sg;
+            if (key < CW) {
+                const uint32_t row = d[kRow0] + min(static_cast<uint32_t>(row_of(key)), rows - 1);
+                const uint32_t pos = d[kPast] + P.depth[d[kRow] + row / G];
+                const int at = row_of(key) - 8 * sg;
+                ms[at] = -1e30f;
+                posr[at] = pos;
+                if (SC) sloper[at] = P.rule.slopes ? __ldg(P.rule.slopes + d[kKvHead] * G + row % G) * kRuleLog2e : 0.f;
             }
-            // Q rows, split with rounded high parts: [32-dim blocks][hi rows | lo rows][128 B]
+            // Q rows, split with rounded high parts: [32-dim blocks][hi rows | lo rows][128 B].
+            // (The last S has been read, so no MMA reads the last unit's Q.)
             constexpr int F4 = HD / 4;  // float4s of a row
-            for (uint32_t i0 = 0; i0 < Rp * F4; i0 += 8 * 128) {
-                float4 x[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t i = i0 + k * 128 + tid, row = i / F4, c = i % F4;
-                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (row < s.rows) {
-                        const uint32_t node = (s.row0 + row) / G, h = s.g * G + (s.row0 + row) % G;
-                        x[k] = *reinterpret_cast<const float4*>(
-                            P.q_rot + (static_cast<size_t>(s.s0 + node) * P.n_head + h) * HD + 4 * c);
-                    }
+            for (uint32_t i = tid; i < Rp * F4; i += 512) {
+                const uint32_t row = i / F4, c = i % F4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row < rows) {
+                    const uint32_t at = d[kRow0] + row;
+                    x = *reinterpret_cast<const float4*>(
+                        P.q_rot + (static_cast<size_t>(d[kRow] + at / G) * P.n_head + d[kKvHead] * G + at % G) * HD +
+                        4 * c);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t i = i0 + k * 128 + tid, row = i / F4, c = i % F4;
-                    if (row >= Rp) continue;
-                    uint4 hi, lo;
-                    auto split = [](float v, uint32_t& a, uint32_t& b) {
-                        a = (__float_as_uint(v) + 0x1000u) & 0xFFFFE000u;
-                        b = __float_as_uint(v - __uint_as_float(a));
-                    };
-                    split(x[k].x, hi.x, lo.x);
-                    split(x[k].y, hi.y, lo.y);
-                    split(x[k].z, hi.z, lo.z);
-                    split(x[k].w, hi.w, lo.w);
-                    uint8_t* dst = smem + (c / 8) * (2 * Rp * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = hi;
-                    *reinterpret_cast<uint4*>(dst + Rp * 128) = lo;
-                }
+                uint4 hi, lo;
+                auto split = [](float v, uint32_t& a, uint32_t& b) {
+                    a = (__float_as_uint(v) + 0x1000u) & 0xFFFFE000u;
+                    b = __float_as_uint(v - __uint_as_float(a));
+                };
+                split(x.x, hi.x, lo.x);
+                split(x.y, hi.y, lo.y);
+                split(x.z, hi.z, lo.z);
+                split(x.w, hi.w, lo.w);
+                uint8_t* dst = smem + (c / 8) * (2 * Rp * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                *reinterpret_cast<uint4*>(dst) = hi;
+                *reinterpret_cast<uint4*>(dst + Rp * 128) = lo;
             }
             tc::fence_proxy_async_smem();
-            bar_128(1);  // (the rows' data too)
+            __syncwarp();
             if (lane == 0) mbar_arrive(QF);
-            for (uint32_t t = s.t0; t < s.t1; ++t, ++gt) {
+            bar_128(bar_id);  // the row data
+            float l[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c) l[c] = 0.f;
+            const uint32_t past = d[kPast];
+            uint32_t place = d[kPlace];
+            for (uint32_t left = d[kTiles]; left; --left, ++gt, place -= C::KT) {
                 ok = warp_wait(SF, gt & 1) && ok;
                 tc::fence_after_sync();
-                float x[RB];
+                float x[CW];
 #pragma unroll
-                for (int c = 0; c < RB / 16; ++c) {
-                    if (c * 16 >= static_cast<int>(Rp)) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[16 * c + k] = 0.f;
-                        continue;
+                for (int c = 0; c < CW; c += 8) {
+                    uint32_t a[8] = {}, b[8] = {};
+                    const uint32_t col = 4 * c + 8 * sg;
+                    if (col < Rp) {
+                        tc::tmem_ld8(tlane + C::C_S + col, a);
+                        tc::tmem_ld8(tlane + C::C_S + Rp + col, b);
+                        tc::tmem_ld_wait();
                     }
-                    uint32_t a[16], b[16];
-                    tc::tmem_ld16(tlane + C::C_S + 16 * c, a);
-                    tc::tmem_ld16(tlane + C::C_S + Rp + 16 * c, b);
-                    tc::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[16 * c + k] = __uint_as_float(a[k]) + __uint_as_float(b[k]);
+                    for (int k = 0; k < 8; ++k) x[c + k] = __uint_as_float(a[k]) + __uint_as_float(b[k]);
                 }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(SE);
-                const uint32_t kt = (s.tile0 + t) * C::KT + key;  // this thread's key, its place
-                const bool tail = (s.tile0 + t + 1) * C::KT > s.past;
-                // bit per row: attended
-                uint32_t on[RB / 32];
+                // whether the tile has keys that some row does not attend: nodes, or what
+                // the rule leaves out
+                bool masked = place + C::KT > past;
+                uint32_t on = 0xffffffffu;   // a bit per row: this key is attended
+                uint32_t kp = place + key;   // the key's place, then its position
+                if (masked && kp >= past) {
+                    const uint32_t j = kp - past;
+                    on = 0u;
+                    if (j < d[kNodes]) {
+                        kp = past + P.depth[d[kRow] + j];
+                        // node after node, each with its rows of the block
+                        const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
+                        const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
+                        uint64_t all = 0;
+                        for (uint32_t i = row0 / G; i <= n1; ++i) {
+                            const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
+                            const uint32_t e = min((i + 1) * G - row0, rows);
+                            const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
+                            if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
+                        }
+                        on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
+                        if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
+                    }
+                }
+                if constexpr (SC) {
+                    if (P.rule.cap_out != 0.f) cap_scores<CW>(x, P.rule, cap_series(P.rule.cap_in));
+                    const uint32_t window = P.rule.window;
+                    const bool early = P.rule.doc_start && kp < __ldg(P.rule.doc_start + d[kReq]);
+                    if (window || P.rule.doc_start) masked = true;
 #pragma unroll
-                for (int w = 0; w < RB / 32; ++w) on[w] = 0xffffffffu;
-                uint32_t kp = kt;
-                if (SC || tail) {
-                    const bool in_tree = kt >= s.past;
-                    const uint32_t j = kt - s.past;
-                    const bool real = kt < s.past + s.n;
-                    if (in_tree && real) kp = s.past + P.depth[s.s0 + j];
-                    if (SC) {
-                        if (P.rule.cap_out != 0.f) cap_scores<RB>(x, P.rule, series);
-                        if (P.rule.slopes) {
+                    for (int c = 0; c < CW; c += 4) {
+                        const int at = 32 * (c / 8) + c % 8;
+                        const float4 sl = *reinterpret_cast<const float4*>(sloper + at);
+                        const uint4 ps = *reinterpret_cast<const uint4*>(posr + at);
+                        const uint32_t far[4] = {ps.x - kp, ps.y - kp, ps.z - kp, ps.w - kp};
+                        const float by[4] = {sl.x, sl.y, sl.z, sl.w};
 #pragma unroll
-                            for (int c = 0; c < RB; ++c)
-                                x[c] = fmaf(-sloper[c], static_cast<float>(static_cast<int>(posr[c] - kp)), x[c]);
+                        for (int k = 0; k < 4; ++k) {
+                            x[c + k] = fmaf(-by[k], static_cast<float>(static_cast<int>(far[k])), x[c + k]);
+                            if (early || (window && far[k] >= window))
+                                on &= ~(1u << (c + k));
                         }
                     }
+                }
+                if (masked) {
 #pragma unroll
-                    for (int w = 0; w < RB / 32; ++w) {
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!SC || kp >= lor[32 * w + c]) m |= 1u << c;
-                        if (in_tree) {
-                            uint32_t in = 0;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const uint32_t row = 32 * w + c;
-                                if (real && row < s.rows) {
-                                    const uint32_t node = (s.row0 + row) / G;
-                                    in |= (P.anc[static_cast<size_t>(s.s0 + node) * kTreeWords + j / 32] >>
-                                           (j % 32) & 1u) << c;
-                                }
-                            }
-                            m &= in;
-                        }
-                        on[w] = m;
-                    }
+                    for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -CUDART_INF_F;
                 }
                 // by how much the scores pass the maxima
-                float over = -1e30f;
+                float over[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
 #pragma unroll
-                for (int c = 0; c < RB; ++c)
-                    if (on[c / 32] >> (c % 32) & 1u && c < static_cast<int>(Rp)) over = fmaxf(over, x[c] - ms[c]);
-                const bool raise = bar_or(1, over > 8.f || !ok);
-                bool wrote = false;
-                if (raise) {
-                    ok = !bar_or(1, !ok);
-                    if (ok) {
-                        // every row's maximum over the tile (as integers in the same order)
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
+                    over[0] = fmaxf(over[0], x[c] - m.x);
+                    over[1] = fmaxf(over[1], x[c + 1] - m.y);
+                    over[2] = fmaxf(over[2], x[c + 2] - m.z);
+                    over[3] = fmaxf(over[3], x[c + 3] - m.w);
+                }
+                const bool raise = bar_or(bar_id, fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > 8.f || !ok);
+                // this warp's block of P is free once the MMAs have read the last tile's (and, where V
+                // was not finite there, the accumulators have); at a unit's start, once the
+                // accumulators are done with the last unit
+                if (gt) {
+                    ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && ok;
+                    if (raise || misc[2 + 4 * ((gt - 1) & 1) + wq] == gt) ok = warp_wait(FX, (gt - 1) & 1) && ok;
+                    if (left == d[kTiles] && u) ok = warp_wait(UE, (u - 1) & 1) && ok;
+                }
+                if (raise) {  // (the accumulators have read the last factors)
+                    // every row's maximum over the tile (as integers in the same order)
 #pragma unroll
-                        for (int c = 0; c < RB; ++c) {
-                            const bool use = on[c / 32] >> (c % 32) & 1u && x[c] == x[c];
-                            const int b = __float_as_int(use ? x[c] : -1e30f);
-                            const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-                            if (lane == 0) tmax[warp * RB + c] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-                        }
-                        // P's buffer is free, so the accumulators have read the last factors
-                        if (t != s.t0) ok = warp_wait(PE, (gt - 1) & 1);
-                        wrote = true;
-                        bar_128(1);
-                        if (tid < RB) {
-                            const float top = fmaxf(fmaxf(tmax[tid], tmax[RB + tid]),
-                                                    fmaxf(tmax[2 * RB + tid], tmax[3 * RB + tid]));
-                            const float old = ms[tid], m = fmaxf(old, top);
-                            // (not 0: an infinity that the row holds has to stay one)
-                            fs[tid] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
-                            ms[tid] = m;
-                        }
-                        bar_128(1);
+                    for (int c = 0; c < CW; ++c) {
+                        const int b = __float_as_int(x[c] == x[c] ? x[c] : -1e30f);
+                        const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+                        if (lane == 0) tmax[wq * RB + row_of(c)] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
                     }
+                    bar_128(bar_id);
+                    if (key < CW) {
+                        const int row = row_of(key), at = row - 8 * sg;
+                        const float top = fmaxf(fmaxf(tmax[row], tmax[RB + row]),
+                                                fmaxf(tmax[2 * RB + row], tmax[3 * RB + row]));
+                        const float old = ms[at], m = fmaxf(old, top);
+                        // (not 0: an infinity that the row holds has to stay one)
+                        fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
+                        ms[at] = m;
+                        if (key == 0) misc[10 + sg] = gt + 1;
+                    }
+                    bar_128(bar_id);
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) l[c] *= fs[32 * (c / 8) + c % 8];
                 }
 #pragma unroll
-                for (int c = 0; c < RB; ++c)
-                    x[c] = on[c / 32] >> (c % 32) & 1u ? tree_exp2(x[c] - ms[c]) : -0.f;
-                if (!wrote && t != s.t0) ok = warp_wait(PE, (gt - 1) & 1) && ok;
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
+                    x[c] = tree_exp2(x[c] - m.x);
+                    x[c + 1] = tree_exp2(x[c + 1] - m.y);
+                    x[c + 2] = tree_exp2(x[c + 2] - m.z);
+                    x[c + 3] = tree_exp2(x[c + 3] - m.w);
+                }
+                if (masked) {  // the accumulators tell a masked key by its sign
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < CW; ++c) l[c] += x[c];
                 // P^T: [32-key blocks][hi rows | lo rows][128 B]
-                uint8_t* dst = smem + C::OFF_P + warp * (2 * Rp * 128) + (lane & 3) * 4;
+                uint8_t* dst = smem + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane & 3) * 4;
 #pragma unroll
-                for (int c = 0; c < RB; ++c) {
-                    if (c < static_cast<int>(Rp)) {
-                        uint8_t* d = dst + c * 128 + (((lane >> 2) ^ (c & 7)) << 4);
-                        *reinterpret_cast<float*>(d) = x[c];
-                        *reinterpret_cast<float*>(d + Rp * 128) = x[c] - __uint_as_float(tf32_part(x[c]));
+                for (int c0 = 0; c0 < CW; c0 += 8) {
+                    if (4 * c0 + 8 * sg < static_cast<int>(Rp)) {
+#pragma unroll
+                        for (int c = c0; c < c0 + 8; ++c) {
+                            uint8_t* q = dst + (4 * c0 + c % 8) * 128 + (((lane >> 2) ^ (c & 7)) << 4);
+                            *reinterpret_cast<float*>(q) = x[c];
+                            *reinterpret_cast<float*>(q + Rp * 128) = x[c] - __uint_as_float(tf32_part(x[c]));
+                        }
                     }
                 }
-                if (tid == 0) misc[1] = raise ? 1u : 0u;
+                if (left == 1) {  // the rows' sums over the warp's keys, a lane per row
+#pragma unroll
+                    for (int off = 16; off >= CW; off >>= 1)
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], off);
+#pragma unroll
+                    for (int h = CW / 2; h > 0; h >>= 1) {
+                        const bool up = lane & h;
+#pragma unroll
+                        for (int c = 0; c < h; ++c) {
+                            const float give = up ? l[c] : l[c + h], mine = up ? l[c + h] : l[c];
+                            l[c] = mine + __shfl_xor_sync(0xffffffffu, give, h);
+                        }
+                    }
+                    if (lane < CW) tmax[wq * RB + row_of(lane)] = l[0];
+                }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(PF);
+                if (lane == 0) mbar_arrive(PF + 8 * wq);
             }
+            done(u);
         }
-    } else if (warp < 8) {
-        // ------------------------------------------------------------ converters
-        const int w = warp - 4, me = w * 32 + lane;
-        const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
-        uint32_t pc = 0, kc = 0, vc = 0, gt = 0;  // pieces, K and V ones, tiles whose V is done
-        auto k_tile = [&]() {
-            for (int j = 0; j < C::KP; ++j, ++pc, ++kc) {
-                const uint32_t sl = pc % NSLOT, b = kc % C::NKL;
-                bool ok = warp_wait(FULL + 8 * sl, (pc / NSLOT) & 1);
-                if (kc >= C::NKL) ok = warp_wait(KLE + 8 * b, (kc / C::NKL - 1) & 1) && ok;
-                tc::fence_after_sync();
-                const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
-                uint32_t lo[32];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 x = *reinterpret_cast<const float4*>(src + ((c ^ (me & 7)) << 4));
-                    lo[4 * c] = __float_as_uint(x.x - __uint_as_float(tf32_part(x.x)));
-                    lo[4 * c + 1] = __float_as_uint(x.y - __uint_as_float(tf32_part(x.y)));
-                    lo[4 * c + 2] = __float_as_uint(x.z - __uint_as_float(tf32_part(x.z)));
-                    lo[4 * c + 3] = __float_as_uint(x.w - __uint_as_float(tf32_part(x.w)));
-                }
-                tc::tmem_st32(tlane + C::C_KL + 32 * b, lo);
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(KLF + 8 * b);
-            }
-        };
-        auto v_tile = [&](uint32_t t) {
-            // keys of the tile that the request has
-            const uint32_t end = s.past + s.n - (s.tile0 + t) * C::KT;
-            for (int j = 0; j < C::VP; ++j, ++pc, ++vc) {
-                const uint32_t sl = pc % NSLOT, b = vc % C::NV;
-                const uint32_t k0 = j / C::DH * C::VK;
-                bool ok = warp_wait(FULL + 8 * sl, (pc / NSLOT) & 1);
-                const int dim = me % C::VD;
-                const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + dim;
-                uint32_t x[C::VK];
-                uint32_t top = 0;
-#pragma unroll
-                for (int k = 0; k < C::VK; ++k) {
-                    x[k] = k0 + k < end ? __float_as_uint(src[k * C::VD]) : 0u;
-                    top = max(top, x[k] & 0x7FFFFFFFu);
-                }
-                if (__any_sync(0xffffffffu, top >= 0x7F800000u)) {
-#pragma unroll
-                    for (int k = 0; k < C::VK; ++k)
-                        if ((x[k] & 0x7F800000u) == 0x7F800000u) x[k] = 0u;
-                    if (lane == 0) misc[2 + (gt & 1)] = gt + 1;
-                }
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(VE + 8 * sl);
-                if (vc >= C::NV) ok = warp_wait(VFE + 8 * b, (vc / C::NV - 1) & 1) && ok;
-                tc::fence_after_sync();
-                const uint32_t dst = tlane + C::C_V + C::VCOLS * b;
-#pragma unroll
-                for (int c = 0; c < C::VK / 32; ++c) {
-                    uint32_t y[32];
-                    if (C::FOLD) {
-                        const bool low = w >= 2;
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const uint32_t h = x[32 * c + k] & 0xFFFFE000u;
-                            y[k] = low ? __float_as_uint(__uint_as_float(x[32 * c + k]) - __uint_as_float(h)) : h;
-                        }
-                        tc::tmem_st32(dst + 32 * c, y);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] = x[32 * c + k];
-                        tc::tmem_st32(dst, y);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            y[k] = __float_as_uint(__uint_as_float(y[k]) - __uint_as_float(y[k] & 0xFFFFE000u));
-                        tc::tmem_st32(dst + 32, y);
-                    }
-                }
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(VF + 8 * b);
-            }
-            ++gt;
-        };
-        while (walk.next(P, s)) {
-            k_tile();
-            for (uint32_t t = s.t0; t < s.t1; ++t) {
-                if (t + 1 < s.t1) k_tile();
-                v_tile(t);
-            }
-        }
-    } else if (warp < 12) {
+    } else if (warp < 20) {
         // ------------------------------------------------------------ accumulators
+        regs_increase<kRegAcc>();
         grid_dependency_wait();
-        const int w = warp - 8, me = w * 32 + lane;
+        const int w = warp & 3, me = w * 32 + lane;
         const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
-        const float* ms = reinterpret_cast<const float*>(smem + C::OFF_M);
-        const float* fs = reinterpret_cast<const float*>(smem + C::OFF_F);
-        float* ls = reinterpret_cast<float*>(smem + C::OFF_L);
-        constexpr int TPR = 128 / RB, KPT = C::KT / TPR;  // threads per row of P, keys of each
-        const int lrow = me / TPR, lpart = me % TPR;
+        float* fs = reinterpret_cast<float*>(smem + C::OFF_F);
+        const float* sums = reinterpret_cast<const float*>(smem + C::OFF_MAX);
         bool ok = true;
         uint32_t gt = 0;
-        while (walk.next(P, s)) {
-            const uint32_t Rp = (s.rows + 15) / 16 * 16;
+        for (uint32_t u = 0;; ++u) {
+            ok = known(u) && ok;
+            const volatile uint32_t* d = words(u);
+            if (bar_or(5, !ok || !d[kMore])) break;
+            const uint32_t rows = d[kRows], Rp = (rows + 15) / 16 * 16;
             float o[C::DH][RB];
 #pragma unroll
-            for (int d = 0; d < C::DH; ++d)
+            for (int h = 0; h < C::DH; ++h)
 #pragma unroll
-                for (int c = 0; c < RB; ++c) o[d][c] = 0.f;
-            float l = 0.f;
-            for (uint32_t t = s.t0; t < s.t1; ++t, ++gt) {
-                ok = warp_wait(PF, gt & 1) && ok;
-                if (misc[1]) {  // the maxima were raised: what there is shrinks
-                    l *= fs[lrow];
-#pragma unroll
-                    for (int c = 0; c < RB; ++c) {
-                        const float f = fs[c];
-#pragma unroll
-                        for (int d = 0; d < C::DH; ++d) o[d][c] *= f;
-                    }
-                }
-                if (lrow < static_cast<int>(Rp)) {
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < KPT / 4; ++c) {
-                        const int k = lpart * KPT + 4 * c;  // keys k .. k + 3
-                        // (the two threads of a row read different banks)
-                        const int q = (k / 4 & 7) ^ (lpart & 1) * 4;
-                        const float4 p = *reinterpret_cast<const float4*>(
-                            smem + C::OFF_P + k / 32 * (2 * Rp * 128) + lrow * 128 + ((q ^ (lrow & 7)) << 4));
-                        sum[0] += p.x;
-                        sum[1] += p.y;
-                        sum[2] += p.z;
-                        sum[3] += p.w;
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                }
+                for (int c = 0; c < RB; ++c) o[h][c] = 0.f;
+            uint32_t place = d[kPlace];
+            for (uint32_t left = d[kTiles]; left; --left, ++gt, place -= C::KT) {
                 ok = warp_wait(OF, gt & 1) && ok;
                 tc::fence_after_sync();
-                const bool odd = misc[2 + (gt & 1)] == gt + 1;  // V values that are not finite
-                if (!odd) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(PE);
-                }
 #pragma unroll
-                for (int d = 0; d < C::DH; ++d) {
+                for (int sg = 0; sg < 4; ++sg) {
+                    if (misc[10 + sg] != gt + 1) continue;  // the maxima were raised: what there is shrinks
+#pragma unroll
+                    for (int c = 0; c < RB; ++c) {
+                        if ((c / 8) % 4 != sg) continue;
+                        const float f = fs[c];
+#pragma unroll
+                        for (int h = 0; h < C::DH; ++h) o[h][c] *= f;
+                    }
+                }
+                for (uint32_t kb = 0; kb < 4; ++kb) {  // V values that are not finite
+                    if (misc[2 + 4 * (gt & 1) + kb] != gt + 1 || (C::FOLD && me >= C::VD)) continue;
+                    const uint32_t k0 = place + 32 * kb, end = d[kPast] + d[kNodes];
+                    for (uint32_t k = 0; k < 32 && k0 + k < end; ++k) {
+                        const size_t at = (static_cast<size_t>(tree_place(P, d[kReq], k0 + k)) * P.n_kv_head + d[kKvHead]) * HD;
+#pragma unroll
+                        for (int h = 0; h < C::DH; ++h) {
+                            const float v = P.V[at + h * C::VD + me];
+                            if ((__float_as_uint(v) & 0x7F800000u) != 0x7F800000u) continue;
+#pragma unroll
+                            for (int c = 0; c < RB; ++c) {
+                                if (c >= static_cast<int>(rows)) break;
+                                const uint32_t p = *reinterpret_cast<const uint32_t*>(
+                                    smem + C::OFF_P + kb * (2 * Rp * 128) + c * 128 +
+                                    (((k / 4) ^ (c & 7)) << 4) + (k & 3) * 4);
+                                if (p != 0x80000000u) o[h][c] += v;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(FX);
+#pragma unroll
+                for (int h = 0; h < C::DH; ++h) {
 #pragma unroll
                     for (int c = 0; c < RB / 16; ++c) {
                         if (c * 16 >= static_cast<int>(Rp)) break;
                         uint32_t a[16], b[16];
-                        tc::tmem_ld16(tlane + C::C_O + d * 2 * RB + 16 * c, a);
-                        tc::tmem_ld16(tlane + C::C_O + d * 2 * RB + Rp + 16 * c, b);
+                        tc::tmem_ld16(tlane + C::C_O + h * 2 * RB + 16 * c, a);
+                        tc::tmem_ld16(tlane + C::C_O + h * 2 * RB + Rp + 16 * c, b);
                         tc::tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
-                            o[d][16 * c + k] += __uint_as_float(a[k]) + __uint_as_float(b[k]);
+                            o[h][16 * c + k] += __uint_as_float(a[k]) + __uint_as_float(b[k]);
                     }
                 }
                 tc::fence_before_sync();
-                if (odd) {
-                    const uint32_t k0 = (s.tile0 + t) * C::KT;
-                    const uint32_t end = min(s.past + s.n - k0, static_cast<uint32_t>(C::KT));
-                    if (!C::FOLD || me < C::VD) {
-                        for (uint32_t k = 0; k < end; ++k) {
-                            const size_t place = tree_place(P, s.r, k0 + k);
-#pragma unroll
-                            for (int d = 0; d < C::DH; ++d) {
-                                const float v = P.V[(place * P.n_kv_head + s.g) * HD + d * C::VD + me];
-                                if ((__float_as_uint(v) & 0x7F800000u) != 0x7F800000u) continue;
-#pragma unroll
-                                for (int c = 0; c < RB; ++c) {
-                                    if (c >= static_cast<int>(s.rows)) break;
-                                    const uint32_t p = *reinterpret_cast<const uint32_t*>(
-                                        smem + C::OFF_P + k / 32 * (2 * Rp * 128) + c * 128 +
-                                        (((k / 4 & 7) ^ (c & 7)) << 4) + (k & 3) * 4);
-                                    if (p != 0x80000000u) o[d][c] += v;
-                                }
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(PE);
-                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(OE);
             }
-            // the unit's end: the rows' sums to everyone, then out or the partial
+            // the unit's end: O through P's buffer (at head dim 64 with the products of V's low
+            // parts beside it), then a factor for every row, and out or the partial result
+            float* stage = reinterpret_cast<float*>(smem + C::OFF_P);
+            const bool write = !bar_or(5, !ok) && P.req_of[d[kRow]] == d[kReq];
 #pragma unroll
-            for (int off = 1; off < TPR; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-            if (lpart == 0) ls[lrow] = l;
-            const bool write = !bar_or(2, !ok);
-            if (C::FOLD) {  // the products with V's low parts, through P's buffer
-                float* fold = reinterpret_cast<float*>(smem + C::OFF_P);
-                if (me >= 64) {
+            for (int h = 0; h < C::DH; ++h)
 #pragma unroll
-                    for (int c = 0; c < RB; ++c) fold[c * 64 + me - 64] = o[0][c];
+                for (int c = 0; c < RB; ++c)
+                    stage[(C::FOLD && me >= 64 ? RB * 64 : 0) + c * HD + (C::FOLD ? me & 63 : h * C::VD + me)] = o[h][c];
+            const bool whole = d[kWhole] != 0;
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + d[kStart];
+            if (me < static_cast<int>(rows)) {
+                float den = (sums[me] + sums[RB + me]) + (sums[2 * RB + me] + sums[3 * RB + me]), f = 1.f;
+                const float m = reinterpret_cast<const float*>(smem + C::OFF_M)[(u & 1) * RB + me];
+                if (whole) {
+                    if (P.sinks)
+                        den += tree_exp2(__ldg(P.sinks + d[kKvHead] * G + (d[kRow0] + me) % G) * kRuleLog2e - m);
+                    f = den == 0.f ? 0.f : 1.f / den;
+                } else if (write) {
+                    *reinterpret_cast<float2*>(P.part_ml + 2 * (slot * RB + me)) = make_float2(m, den);
                 }
-                bar_128(2);
-                if (me < 64) {
-#pragma unroll
-                    for (int c = 0; c < RB; ++c) o[0][c] += fold[c * 64 + me];
+                fs[me] = f;
+            }
+            bar_128(5);
+            if (write) {
+                constexpr int F4 = HD / 4;
+                for (uint32_t i = me; i < rows * F4; i += 128) {
+                    const uint32_t c = i / F4, at = d[kRow0] + c;
+                    float4 x = reinterpret_cast<const float4*>(stage)[i];
+                    if (C::FOLD) {
+                        const float4 y = reinterpret_cast<const float4*>(stage + RB * 64)[i];
+                        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                    }
+                    const float f = fs[c];
+                    x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+                    const size_t row = (static_cast<size_t>(d[kRow] + at / G)) * P.n_head + d[kKvHead] * G + at % G;
+                    *reinterpret_cast<float4*>((whole ? P.out + row * HD : P.part + (slot * RB + c) * HD) + i % F4 * 4) = x;
                 }
             }
-            const bool whole = s.t0 == 0 && s.t1 == s.tl;
-            if (write && P.req_of[s.s0] == s.r && (!C::FOLD || me < 64)) {
-                const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
-                uint32_t node = s.row0 / G, h = s.row0 % G;
-#pragma unroll
-                for (int c = 0; c < RB; ++c) {
-                    if (c >= static_cast<int>(s.rows)) break;
-                    const float sum = ls[c], m = ms[c];
-                    if (whole) {
-                        float den = sum;
-                        if (P.sinks) den += tree_exp2(__ldg(P.sinks + s.g * G + h) * kRuleLog2e - m);
-                        const float inv = den == 0.f ? 0.f : 1.f / den;
-                        float* dst = P.out + (static_cast<size_t>(s.s0 + node) * P.n_head + s.g * G + h) * HD + me;
-#pragma unroll
-                        for (int d = 0; d < C::DH; ++d) dst[d * C::VD] = o[d][c] * inv;
-                    } else {
-                        float* dst = P.part + (slot * RB + c) * HD + me;
-#pragma unroll
-                        for (int d = 0; d < C::DH; ++d) dst[d * C::VD] = o[d][c];
-                        if (me == 0)
-                            *reinterpret_cast<float2*>(P.part_ml + 2 * (slot * RB + c)) = make_float2(m, sum);
-                    }
-                    if (++h == G) {
-                        h = 0;
-                        ++node;
-                    }
-                }
-            }
-            bar_128(2);  // everyone has read the sums, the maxima and the fold's rows ...
+            bar_128(5);  // everyone has read the sums, the maxima, the factors and the rows ...
             if (lane == 0) mbar_arrive(UE);  // ... which are the next unit's from here on
+            done(u);
         }
-    } else if (warp == 12) {
+    } else if (warp < 28) {
+        // ------------------------------------------------------------ converters
+        regs_decrease<kRegConv>();
+        const bool is_k = warp < 24;
+        const int w = warp & 3, me = w * 32 + lane;
+        const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
+        uint32_t pc = 0, n = 0, gt = 0, phase = 0;  // pieces, this kind's, tiles; per slot: its parity
+        bool ok = true;
+        for (uint32_t u = 0;; ++u) {
+            ok = known(u) && ok;
+            const volatile uint32_t* d = words(u);
+            if (!ok || !d[kMore]) break;
+            const uint32_t tiles = d[kTiles];
+            // K(0), then K(t + 1) and V(t) by turns
+            if (is_k) {
+                for (uint32_t t = 0; t < tiles; ++t) {
+                    for (int j = 0; j < C::KP; ++j, ++pc, ++n) {
+                        const uint32_t sl = pc % NSLOT, b = n % C::NKL;
+                        ok = warp_wait(KF + 8 * sl, phase >> sl & 1) && ok;
+                        phase ^= 1u << sl;
+                        const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
+                        uint32_t lo[32];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 x = *reinterpret_cast<const float4*>(src + ((c ^ (me & 7)) << 4));
+                            lo[4 * c] = __float_as_uint(x.x - __uint_as_float(tf32_part(x.x)));
+                            lo[4 * c + 1] = __float_as_uint(x.y - __uint_as_float(tf32_part(x.y)));
+                            lo[4 * c + 2] = __float_as_uint(x.z - __uint_as_float(tf32_part(x.z)));
+                            lo[4 * c + 3] = __float_as_uint(x.w - __uint_as_float(tf32_part(x.w)));
+                        }
+                        if (n >= C::NKL) ok = warp_wait(KLE + 8 * b, (n / C::NKL - 1) & 1) && ok;
+                        tc::fence_after_sync();
+                        tc::tmem_st32(tlane + C::C_KL + 32 * b, lo);
+                        tc::tmem_st_wait();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(KLF + 8 * b);
+                    }
+                    if (t) pc += C::VP;
+                }
+                pc += C::VP;
+            } else {
+                uint32_t end = d[kPast] + d[kNodes] - d[kPlace];  // keys that the request has from the tile on
+                pc += C::KP;
+                for (uint32_t t = 0; t < tiles; ++t, ++gt, end += C::KT) {
+                    if (t + 1 < tiles) pc += C::KP;
+                    for (int j = 0; j < C::VP; ++j, ++pc, ++n) {
+                        const uint32_t sl = pc % NSLOT, b = n % C::NV;
+                        ok = warp_wait(VL + 8 * sl, phase >> sl & 1) && ok;
+                        phase ^= 1u << sl;
+                        const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
+                        const uint32_t dst = tlane + C::C_V + C::VCOLS * b;
+#pragma unroll
+                        for (int h = 0; h < C::VK / 32; ++h) {  // 32 keys at a time
+                            const uint32_t k0 = j / C::DH * C::VK + 32 * h;
+                            uint32_t x[32];
+                            float sum[2] = {0.f, 0.f};  // of the low parts: NaN where a value is not finite
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(src[(32 * h + k) * C::VD]);
+                            if (k0 + 32 > end) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (k0 + k >= end) x[k] = 0u;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                sum[k & 1] += __uint_as_float(x[k]) - __uint_as_float(x[k] & 0xFFFFE000u);
+                            if (__any_sync(0xffffffffu, !(sum[0] + sum[1] == sum[0] + sum[1]))) {
+                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if ((x[k] & 0x7F800000u) == 0x7F800000u) x[k] = 0u;
+                            }
+                            if (h == 0) {
+                                if (n >= C::NV) ok = warp_wait(VFE + 8 * b, (n / C::NV - 1) & 1) && ok;
+                                tc::fence_after_sync();
+                            }
+                            if (!C::FOLD) tc::tmem_st32(dst, x);
+                            if (!C::FOLD || w >= 2) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    x[k] = __float_as_uint(__uint_as_float(x[k]) - __uint_as_float(x[k] & 0xFFFFE000u));
+                            }
+                            tc::tmem_st32(C::FOLD ? dst + 32 * h : dst + 32, x);
+                        }
+                        tc::tmem_st_wait();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0 && ok) {
+                            mbar_arrive(VE + 8 * sl);
+                            mbar_arrive(VF + 8 * b);
+                        }
+                    }
+                }
+            }
+            done(u);
+        }
+    } else if (warp == 28) {
         // ------------------------------------------------------------ producer
+        regs_decrease<kRegAux>();
         bool ok = true, waited = false;
         uint32_t pc = 0;
-        uint32_t was_v = 0, ke = 0, ve = 0;  // per slot: its last piece was V; phases of its waits
+        // per slot: its last piece was V, the parities of the waits for its being empty, and of
+        // what was last sent into it (filled: K's bits, V's 16 up)
+        uint32_t was_v = 0, ke = 0, ve = 0, kf = 0, vl = 0, filled = 0;
         const uint32_t box = P.box_keys, boxes = C::KT / box;
-        // the row of this lane's box in a tile
-        auto rows_of = [&](uint32_t t) {
-            const uint32_t k = (s.tile0 + t) * C::KT + lane * box;
-            if (static_cast<uint32_t>(lane) >= boxes || k >= s.past + s.n) return 0u;
-            return tree_place(P, s.r, k);
-        };
-        auto slot_free = [&](uint32_t sl) {
-            if (pc < NSLOT) return;
-            const uint32_t bit = 1u << sl;
-            const bool v = was_v & bit;
-            ok = warp_wait((v ? VE : KE) + 8 * sl, (v ? ve : ke) & bit ? 1 : 0) && ok;
-            (v ? ve : ke) ^= bit;
-        };
-        auto k_tile = [&](uint32_t y) {
-            for (int j = 0; j < C::KP; ++j, ++pc) {
-                const uint32_t sl = pc % NSLOT;
-                slot_free(sl);
-                if (!ok) continue;
-                was_v &= ~(1u << sl);
-                if (lane == 0) mbar_expect_tx(FULL + 8 * sl, C::PIECE);
-                __syncwarp();
-                if (static_cast<uint32_t>(lane) < boxes)
-                    tma_load_2d(sbase + C::OFF_RING + sl * C::PIECE + lane * box * 128, &tmK,
-                                static_cast<int>(s.g * HD + 32 * j), static_cast<int>(y), FULL + 8 * sl);
-            }
-        };
         const uint32_t vbox = min(box, static_cast<uint32_t>(C::VK)), vboxes = C::VK / vbox;
-        auto v_tile = [&](uint32_t y) {
-            for (int j = 0; j < C::VP; ++j, ++pc) {
-                const uint32_t sl = pc % NSLOT;
-                slot_free(sl);
-                const uint32_t k = j / C::DH * C::VK + lane * vbox;  // key of this lane's box
-                const uint32_t row = __shfl_sync(0xffffffffu, y, (k / box) & 31) + k % box;
-                if (!ok) continue;
-                was_v |= 1u << sl;
-                if (lane == 0) mbar_expect_tx(FULL + 8 * sl, C::PIECE);
-                __syncwarp();
-                if (static_cast<uint32_t>(lane) < vboxes)
-                    tma_load_2d(sbase + C::OFF_RING + sl * C::PIECE + lane * vbox * C::VD * 4, &tmV,
-                                static_cast<int>(s.g * HD + j % C::DH * C::VD), static_cast<int>(row),
-                                FULL + 8 * sl);
-            }
-        };
-        while (walk.next(P, s)) {
-            // tiles of history may be read while the prep kernel still runs
-            auto ready = [&](uint32_t t) {
-                if (!waited && (s.tile0 + t + 1) * C::KT > s.past) {
-                    grid_dependency_wait();
-                    waited = true;
+        for (uint32_t u = 0;; ++u) {
+            ok = known(u) && ok;
+            const volatile uint32_t* d = words(u);
+            if (!ok || !d[kMore]) break;
+            const uint32_t tiles = d[kTiles], x0 = d[kKvHead] * HD, end = d[kPast] + d[kNodes];
+            uint32_t y[2] = {0, 0};  // this lane's box of a tile, by the tile's parity: its row
+            // K(0), then K(t + 1) and V(t) by turns
+            for (uint32_t i = 0; i < 2 * tiles; ++i) {
+                const bool v = i == 2 * tiles - 1 || (i && !(i & 1));
+                const uint32_t t = v ? (i - 1) / 2 : (i + 1) / 2;
+                if (!v) {
+                    const uint32_t place = d[kPlace] - t * C::KT, k = place + lane * box;
+                    // (tiles of history may be read while the prep kernel still runs)
+                    if (!waited && place + C::KT > d[kPast]) {
+                        grid_dependency_wait();
+                        waited = true;
+                    }
+                    const uint32_t row = static_cast<uint32_t>(lane) < boxes && k < end ? tree_place(P, d[kReq], k) : 0u;
+                    y[0] = t & 1 ? y[0] : row;
+                    y[1] = t & 1 ? row : y[1];
                 }
-            };
-            ready(s.t0);
-            uint32_t y = rows_of(s.t0);
-            k_tile(y);
-            for (uint32_t t = s.t0; t < s.t1; ++t) {
-                uint32_t y1 = 0;
-                if (t + 1 < s.t1) {
-                    ready(t + 1);
-                    y1 = rows_of(t + 1);
-                    k_tile(y1);
+                const uint32_t yt = t & 1 ? y[1] : y[0];
+                const int pieces = v ? C::VP : C::KP;
+#pragma unroll 1
+                for (int j = 0; j < pieces; ++j, ++pc) {
+                    const uint32_t sl = pc % NSLOT, bit = 1u << sl;
+                    if (pc >= NSLOT) {
+                        const bool w = was_v & bit;
+                        ok = warp_wait((w ? VE : KE) + 8 * sl, (w ? ve : ke) & bit ? 1 : 0) && ok;
+                        (w ? ve : ke) ^= bit;
+                    }
+                    // the row of this lane's box of the piece
+                    const uint32_t k = v ? j / C::DH * C::VK + lane * vbox : lane * box;
+                    const uint32_t row = __shfl_sync(0xffffffffu, yt, (k / box) & 31) + k % box;
+                    if (!ok) continue;
+                    const uint32_t bar = (v ? VL : KF) + 8 * sl;
+                    was_v = v ? was_v | bit : was_v & ~bit;
+                    const uint32_t sent = v ? bit << 16 : bit;
+                    if (filled & sent) (v ? vl : kf) ^= bit;
+                    filled |= sent;
+                    if (lane == 0) mbar_expect_tx(bar, C::PIECE);
+                    __syncwarp();
+                    const uint32_t dst = sbase + C::OFF_RING + sl * C::PIECE + lane * (v ? vbox * C::VD * 4 : box * 128);
+                    if (static_cast<uint32_t>(lane) < (v ? vboxes : boxes))
+                        tma_load_2d(dst, v ? &tmV : &tmK, static_cast<int>(x0 + (v ? j % C::DH * C::VD : 32 * j)),
+                                    static_cast<int>(row), bar);
                 }
-                v_tile(y);
-                y = y1;
             }
+            done(u);
         }
         grid_launch_dependents();
         if (misc[0])  // copies that may still be in flight
-            for (uint32_t u = pc > NSLOT ? pc - NSLOT : 0; u < pc; ++u)
-                mbar_wait(FULL + 8 * (u % NSLOT), (u / NSLOT) & 1, 1ll << 28);
+            for (uint32_t sl = 0; sl < NSLOT; ++sl) {
+                if (filled >> sl & 1) mbar_wait(KF + 8 * sl, kf >> sl & 1, 1ll << 28);
+                if (filled >> (16 + sl) & 1) mbar_wait(VL + 8 * sl, vl >> sl & 1, 1ll << 28);
+            }
+    } else if (warp == 31) {
+        // ------------------------------------------------------------ units
+        regs_decrease<kRegAux>();
+        TreeWalk<RB> walk;
+        walk.known = false;
+        walk.r = r_first;
+        walk.off = off_first;
+        walk.left = work ? u1 - u0 : 0u;
+        for (uint32_t u = 0;; ++u) {
+            uint32_t d[12];
+            const bool more = walk.next(P, d);
+            if (!more) d[kMore] = 0u;
+            if (u >= 2 && !warp_wait(GE + 8 * (u & 1), ((u >> 1) - 1) & 1)) break;
+            if (lane == 0) {
+                volatile uint32_t* to = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_DESC) + 12 * (u & 1);
+                if (more)
+#pragma unroll
+                    for (int i = 0; i < 11; ++i) to[i] = d[i];
+                to[kMore] = d[kMore];
+                mbar_arrive(GF + 8 * (u & 1));
+            }
+            __syncwarp();
+            if (!more) break;
+        }
     } else {
-        // ------------------------------------------------------------ MMA issuer
+        // ------------------------------------------------------------ MMA issuers
+        // Warp 29 issues the products of S, warp 30 those of P V: while one waits
+        // at a barrier (a couple of hundred cycles beside MMAs that read shared
+        // memory) the other's MMAs run.
+        regs_decrease<kRegAux>();
         const bool lead = tc::elect_one();
         bool ok = true;
-        uint32_t pc = 0, kc = 0, vc = 0, gs = 0, gp = 0, units = 0;  // pieces, tiles of S and of PV
-        const uint64_t kdesc0 = tc::smem_desc(sbase + C::OFF_RING, 16, 1024, tc::kSwizzle128B);
-        const uint64_t qdesc0 = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
-        const uint64_t pdesc0 = tc::smem_desc(sbase + C::OFF_P, 16, 1024, tc::kSwizzle128B);
-        while (walk.next(P, s)) {
-            const uint32_t Rp = (s.rows + 15) / 16 * 16;
+        uint32_t pc = 0, n_piece = 0, tiles = 0;  // pieces, this warp's, its tiles
+        for (uint32_t u = 0;; ++u) {
+            ok = known(u) && ok;
+            const volatile uint32_t* d = words(u);
+            // (the same in all lanes, so that an MMA's operands are in uniform registers)
+            if (!ok || !__shfl_sync(0xffffffffu, d[kMore], 0)) break;
+            const uint32_t Rp = __shfl_sync(0xffffffffu, (d[kRows] + 15) / 16 * 16, 0);
+            const uint32_t n = __shfl_sync(0xffffffffu, d[kTiles], 0);
+            done(u);
             const uint32_t i2 = tc::idesc_tf32(128, 0, false) | (2 * Rp >> 3) << 17;
             const uint32_t i1 = tc::idesc_tf32(128, 0, false) | (Rp >> 3) << 17;
             const uint32_t block = 2 * Rp * 128 >> 4;  // a 32-wide block of Q or P
-            ok = warp_wait(QF, units & 1) && ok;
-            ++units;
-            auto s_tile = [&]() {
-                if (gs) ok = warp_wait(SE, (gs - 1) & 1) && ok;
-                for (int j = 0; j < C::KP; ++j, ++pc, ++kc) {
-                    const uint32_t sl = pc % NSLOT, b = kc % C::NKL;
-                    ok = warp_wait(FULL + 8 * sl, (pc / NSLOT) & 1) && ok;
-                    ok = warp_wait(KLF + 8 * b, (kc / C::NKL) & 1) && ok;
-                    if (!ok) continue;
-                    tc::fence_after_sync();
-                    if (lead) {
+            if (warp == 29) {
+                const uint64_t kdesc0 = tc::smem_desc(sbase + C::OFF_RING, 16, 1024, tc::kSwizzle128B);
+                const uint64_t qdesc0 = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
+                const uint32_t sc = tb + C::C_S, sl2 = sc + Rp;
+                ok = warp_wait(QF, u & 1) && ok;
+                for (uint32_t t = 0; t < n; ++t, ++tiles) {
+                    if (tiles) ok = warp_wait(SE, (tiles - 1) & 1) && ok;
+#pragma unroll 1
+                    for (int j = 0; j < C::KP; ++j, ++pc, ++n_piece) {
+                        const uint32_t sl = pc % NSLOT, b = n_piece % C::NKL;
+                        // (the converters have waited for the piece to land)
+                        ok = warp_wait(KLF + 8 * b, (n_piece / C::NKL) & 1) && ok;
+                        if (!ok) continue;
+                        tc::fence_after_sync();
                         const uint64_t kd = kdesc0 + (sl * C::PIECE >> 4), qd = qdesc0 + j * block;
+                        const uint32_t kl = tb + C::C_KL + 32 * b, ke = KE + 8 * sl, kle = KLE + 8 * b;
+                        const uint32_t more = j ? 1u : 0u;
+                        if (lead) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            tc::mma_tf32_ss(tb + C::C_S, kd + 2 * kk, qd + 2 * kk, i2, j | kk ? 1u : 0u);
-                            tc::mma_tf32_ts(tb + C::C_S + Rp, tb + C::C_KL + 32 * b + 8 * kk, qd + 2 * kk, i1, 1u);
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_tf32_ss(sc, kd + 2 * kk, qd + 2 * kk, i2, kk ? 1u : more);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_tf32_ts(sl2, kl + 8 * kk, qd + 2 * kk, i1, 1u);
+                            tc::mma_commit(ke);
+                            tc::mma_commit(kle);
                         }
-                        tc::mma_commit(KE + 8 * sl);
-                        tc::mma_commit(KLE + 8 * b);
+                        __syncwarp();
                     }
+                    // (the failure-path test option withholds the CTA's first score-ready signal)
+                    if (lead && ok && !(tiles == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SF);
+                    __syncwarp();
+                    if (t) pc += C::VP;  // V(t - 1) stands behind K(t) in the ring, ...
+                }
+                pc += C::VP;  // ... and the unit's last V behind that
+            } else {
+                const uint64_t pdesc0 = tc::smem_desc(sbase + C::OFF_P, 16, 1024, tc::kSwizzle128B);
+                for (uint32_t t = 0; t < n; ++t, ++tiles) {
+                    if (tiles) ok = warp_wait(OE, (tiles - 1) & 1) && ok;
+#pragma unroll 1
+                    for (int j = 0; j < C::VP; ++j, ++n_piece) {
+                        const uint32_t b = n_piece % C::NV;
+                        if (j % C::DH == 0)
+#pragma unroll
+                            for (int h = 0; h < C::VK / 32; ++h)
+                                ok = warp_wait(PF + 8 * (j / C::DH * (C::VK / 32) + h), tiles & 1) && ok;
+                        ok = warp_wait(VF + 8 * b, (n_piece / C::NV) & 1) && ok;
+                        if (!ok) continue;
+                        tc::fence_after_sync();
+                        const uint32_t a = tb + C::C_V + C::VCOLS * b, o = tb + C::C_O + j % C::DH * 2 * RB;
+                        const uint32_t ol = o + Rp;
+                        const uint64_t pd = pdesc0 + j / C::DH * (C::VK / 32) * block, pd2 = pd + block;
+                        const uint32_t more = j >= C::DH ? 1u : 0u;
+                        const uint32_t vfe = VFE + 8 * b, pe = PE + 8 * (j / C::DH * (C::VK / 32));
+                        const bool last = j % C::DH == C::DH - 1;
+                        if (lead) {
+#pragma unroll
+                            for (int kk = 0; kk < C::VK / 8; ++kk)
+                                tc::mma_tf32_ts(o, a + 8 * kk, (kk < 4 ? pd : pd2) + 2 * (kk % 4), i2,
+                                                kk ? 1u : more);
+#pragma unroll
+                            for (int kk = 0; kk < (C::FOLD ? 0 : 4); ++kk)
+                                tc::mma_tf32_ts(ol, a + 32 + 8 * kk, pd + 2 * kk, i1, 1u);
+                            tc::mma_commit(vfe);
+                            if (last)
+#pragma unroll
+                                for (int h = 0; h < C::VK / 32; ++h) tc::mma_commit(pe + 8 * h);
+                        }
+                        __syncwarp();
+                    }
+                    if (lead && ok) tc::mma_commit(OF);
                     __syncwarp();
                 }
-                // (the failure-path test option withholds the CTA's first score-ready signal)
-                if (lead && ok && !(gs == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SF);
-                __syncwarp();
-                ++gs;
-            };
-            s_tile();
-            for (uint32_t t = s.t0; t < s.t1; ++t, ++gp) {
-                if (t + 1 < s.t1) s_tile();
-                ok = warp_wait(PF, gp & 1) && ok;
-                if (gp) ok = warp_wait(OE, (gp - 1) & 1) && ok;
-                for (int j = 0; j < C::VP; ++j, ++pc, ++vc) {
-                    const uint32_t b = vc % C::NV;
-                    ok = warp_wait(VF + 8 * b, (vc / C::NV) & 1) && ok;
-                    if (!ok) continue;
-                    tc::fence_after_sync();
-                    if (lead) {
-                        const uint32_t a = tb + C::C_V + C::VCOLS * b, d = tb + C::C_O + j % C::DH * 2 * RB;
-                        const uint32_t k0 = j / C::DH * C::VK;
-#pragma unroll
-                        for (int kk = 0; kk < C::VK / 8; ++kk) {
-                            const uint64_t pd = pdesc0 + (k0 + 8 * kk) / 32 * block + 2 * (kk % 4);
-                            const uint32_t acc = j >= C::DH || kk ? 1u : 0u;
-                            tc::mma_tf32_ts(d, a + 8 * kk, pd, i2, acc);
-                            if (!C::FOLD) tc::mma_tf32_ts(d + Rp, a + 32 + 8 * kk, pd, i1, 1u);
-                        }
-                        tc::mma_commit(VFE + 8 * b);
-                    }
-                    __syncwarp();
-                }
-                if (lead && ok) {
-                    tc::mma_commit(PE);
-                    tc::mma_commit(OF);
-                }
-                __syncwarp();
             }
         }
         // every MMA has ended before tensor memory is freed
-        if (lead) tc::mma_commit(DRAIN);
+        const uint32_t drain = DRAIN + 8 * (warp - 29);
+        if (lead) tc::mma_commit(drain);
         __syncwarp();
-        mbar_wait(DRAIN, 0);
+        mbar_wait(drain, 0);
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 13) tc::tmem_dealloc(tb, C::TMEM_COLS);
+    if (warp == 29) tc::tmem_dealloc(tb, C::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------ combine
@@ -1129,6 +1225,14 @@ int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMa
         if ((e = cudaFuncSetAttribute(slotkv_tree_attn_kernel<HD, false>, which, C::SMEM)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(slotkv_tree_attn_kernel<HD, true>, which, C::SMEM)) != cudaSuccess)
             return static_cast<int>(e);
+        // the register hand-over assumes what the kernels are launched with: with fewer the
+        // softmax warps' request could never be met
+        cudaFuncAttributes fa[2];
+        if ((e = cudaFuncGetAttributes(&fa[0], slotkv_tree_attn_kernel<HD, false>)) != cudaSuccess ||
+            (e = cudaFuncGetAttributes(&fa[1], slotkv_tree_attn_kernel<HD, true>)) != cudaSuccess)
+            return static_cast<int>(e);
+        if (fa[0].numRegs != kTreeRegs || fa[1].numRegs != kTreeRegs)
+            return static_cast<int>(cudaErrorInvalidConfiguration);
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
     cudaLaunchAttribute attr[1];
