@@ -390,8 +390,17 @@ __device__ __forceinline__ float tree_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Packed f32x2 forms (each element rounded as the scalar operation would be).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+    return __ffma2_rn(b, make_float2(-1.f, -1.f), a);
+}
 // x without its low 13 mantissa bits: what the tensor core reads of it.
 __device__ __forceinline__ uint32_t tf32_part(float x) { return __float_as_uint(x) & 0xFFFFE000u; }
+// The low parts of two values.
+__device__ __forceinline__ float2 low2(float x, float y) {
+    return sub2(make_float2(x, y), make_float2(__uint_as_float(tf32_part(x)), __uint_as_float(tf32_part(y))));
+}
 
 template <int HD, bool SC>
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -600,6 +609,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             uint32_t place = d[kPlace];
             for (uint32_t left = d[kTiles]; left; --left, ++gt, place -= C::KT) {
                 ok = warp_wait(SF, gt & 1) && ok;
+                if (8u * sg >= Rp) {  // no rows for this warpgroup (which has to stay in step all the same)
+                    if (lane == 0) mbar_arrive(SE);
+                    if (gt) ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && ok;
+                    if (lane == 0) mbar_arrive(PF + 8 * wq);
+                    continue;
+                }
                 tc::fence_after_sync();
                 float x[CW];
 #pragma unroll
@@ -612,7 +627,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         tc::tmem_ld_wait();
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[c + k] = __uint_as_float(a[k]) + __uint_as_float(b[k]);
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 y = add2(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])),
+                                              make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1])));
+                        x[c + k] = y.x;
+                        x[c + k + 1] = y.y;
+                    }
                 }
                 tc::fence_before_sync();
                 __syncwarp();
@@ -670,10 +690,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
-                    over[0] = fmaxf(over[0], x[c] - m.x);
-                    over[1] = fmaxf(over[1], x[c + 1] - m.y);
-                    over[2] = fmaxf(over[2], x[c + 2] - m.z);
-                    over[3] = fmaxf(over[3], x[c + 3] - m.w);
+                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+                    over[0] = fmaxf(over[0], y.x);
+                    over[1] = fmaxf(over[1], y.y);
+                    over[2] = fmaxf(over[2], z.x);
+                    over[3] = fmaxf(over[3], z.y);
                 }
                 const bool raise = bar_or(bar_id, fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > 8.f || !ok);
                 // this warp's block of P is free once the MMAs have read the last tile's (and, where V
@@ -710,27 +732,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
-                    x[c] = tree_exp2(x[c] - m.x);
-                    x[c + 1] = tree_exp2(x[c + 1] - m.y);
-                    x[c + 2] = tree_exp2(x[c + 2] - m.z);
-                    x[c + 3] = tree_exp2(x[c + 3] - m.w);
+                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+                    x[c] = tree_exp2(y.x);
+                    x[c + 1] = tree_exp2(y.y);
+                    x[c + 2] = tree_exp2(z.x);
+                    x[c + 3] = tree_exp2(z.y);
                 }
                 if (masked) {  // the accumulators tell a masked key by its sign
 #pragma unroll
                     for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -0.f;
                 }
 #pragma unroll
-                for (int c = 0; c < CW; ++c) l[c] += x[c];
+                for (int c = 0; c < CW; c += 2) {
+                    const float2 y = add2(make_float2(l[c], l[c + 1]), make_float2(x[c], x[c + 1]));
+                    l[c] = y.x;
+                    l[c + 1] = y.y;
+                }
                 // P^T: [32-key blocks][hi rows | lo rows][128 B]
                 uint8_t* dst = smem + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane & 3) * 4;
 #pragma unroll
                 for (int c0 = 0; c0 < CW; c0 += 8) {
                     if (4 * c0 + 8 * sg < static_cast<int>(Rp)) {
 #pragma unroll
-                        for (int c = c0; c < c0 + 8; ++c) {
+                        for (int c = c0; c < c0 + 8; c += 2) {
+                            const float2 lo = low2(x[c], x[c + 1]);
                             uint8_t* q = dst + (4 * c0 + c % 8) * 128 + (((lane >> 2) ^ (c & 7)) << 4);
                             *reinterpret_cast<float*>(q) = x[c];
-                            *reinterpret_cast<float*>(q + Rp * 128) = x[c] - __uint_as_float(tf32_part(x[c]));
+                            *reinterpret_cast<float*>(q + Rp * 128) = lo.x;
+                            q = dst + (4 * c0 + c % 8 + 1) * 128 + (((lane >> 2) ^ ((c + 1) & 7)) << 4);
+                            *reinterpret_cast<float*>(q) = x[c + 1];
+                            *reinterpret_cast<float*>(q + Rp * 128) = lo.y;
                         }
                     }
                 }
@@ -823,8 +855,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         tc::tmem_ld16(tlane + C::C_O + h * 2 * RB + Rp + 16 * c, b);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            o[h][16 * c + k] += __uint_as_float(a[k]) + __uint_as_float(b[k]);
+                        for (int k = 0; k < 16; k += 2) {
+                            const float2 hi = make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1]));
+                            const float2 lo = make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1]));
+                            const float2 y = add2(make_float2(o[h][16 * c + k], o[h][16 * c + k + 1]), add2(hi, lo));
+                            o[h][16 * c + k] = y.x;
+                            o[h][16 * c + k + 1] = y.y;
+                        }
                     }
                 }
                 tc::fence_before_sync();
@@ -887,30 +924,49 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const volatile uint32_t* d = words(u);
             if (!ok || !d[kMore]) break;
             const uint32_t tiles = d[kTiles];
+            // A piece's stores to tensor memory are waited for, and the piece handed over, only
+            // after the next piece's loads, if that has landed already.
+            uint32_t handed = 0;  // the barrier of the piece that is still to be handed over
+            auto hand_over = [&]() {
+                if (!handed) return;
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(handed);
+                handed = 0;
+            };
+            auto landed = [&](uint32_t bar) {
+                const uint32_t parity = phase >> (pc % NSLOT) & 1;
+                phase ^= 1u << (pc % NSLOT);
+                if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
+                hand_over();
+                ok = warp_wait(bar, parity) && ok;
+            };
             // K(0), then K(t + 1) and V(t) by turns
             if (is_k) {
                 for (uint32_t t = 0; t < tiles; ++t) {
+#pragma unroll 1
                     for (int j = 0; j < C::KP; ++j, ++pc, ++n) {
                         const uint32_t sl = pc % NSLOT, b = n % C::NKL;
-                        ok = warp_wait(KF + 8 * sl, phase >> sl & 1) && ok;
-                        phase ^= 1u << sl;
+                        landed(KF + 8 * sl);
                         const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
+                        float4 x[8];
                         uint32_t lo[32];
 #pragma unroll
+                        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const float4*>(src + ((c ^ (me & 7)) << 4));
+                        hand_over();
+#pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const float4 x = *reinterpret_cast<const float4*>(src + ((c ^ (me & 7)) << 4));
-                            lo[4 * c] = __float_as_uint(x.x - __uint_as_float(tf32_part(x.x)));
-                            lo[4 * c + 1] = __float_as_uint(x.y - __uint_as_float(tf32_part(x.y)));
-                            lo[4 * c + 2] = __float_as_uint(x.z - __uint_as_float(tf32_part(x.z)));
-                            lo[4 * c + 3] = __float_as_uint(x.w - __uint_as_float(tf32_part(x.w)));
+                            const float2 a = low2(x[c].x, x[c].y), e = low2(x[c].z, x[c].w);
+                            lo[4 * c] = __float_as_uint(a.x);
+                            lo[4 * c + 1] = __float_as_uint(a.y);
+                            lo[4 * c + 2] = __float_as_uint(e.x);
+                            lo[4 * c + 3] = __float_as_uint(e.y);
                         }
                         if (n >= C::NKL) ok = warp_wait(KLE + 8 * b, (n / C::NKL - 1) & 1) && ok;
                         tc::fence_after_sync();
                         tc::tmem_st32(tlane + C::C_KL + 32 * b, lo);
-                        tc::tmem_st_wait();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0 && ok) mbar_arrive(KLF + 8 * b);
+                        handed = KLF + 8 * b;
                     }
                     if (t) pc += C::VP;
                 }
@@ -920,17 +976,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 pc += C::KP;
                 for (uint32_t t = 0; t < tiles; ++t, ++gt, end += C::KT) {
                     if (t + 1 < tiles) pc += C::KP;
+#pragma unroll 1
                     for (int j = 0; j < C::VP; ++j, ++pc, ++n) {
                         const uint32_t sl = pc % NSLOT, b = n % C::NV;
-                        ok = warp_wait(VL + 8 * sl, phase >> sl & 1) && ok;
-                        phase ^= 1u << sl;
+                        landed(VL + 8 * sl);
                         const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
                         const uint32_t dst = tlane + C::C_V + C::VCOLS * b;
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < C::VK / 32; ++h) {  // 32 keys at a time
                             const uint32_t k0 = j / C::DH * C::VK + 32 * h;
                             uint32_t x[32];
-                            float sum[2] = {0.f, 0.f};  // of the low parts: NaN where a value is not finite
 #pragma unroll
                             for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(src[(32 * h + k) * C::VD]);
                             if (k0 + 32 > end) {
@@ -938,37 +993,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 for (int k = 0; k < 32; ++k)
                                     if (k0 + k >= end) x[k] = 0u;
                             }
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                sum[k & 1] += __uint_as_float(x[k]) - __uint_as_float(x[k] & 0xFFFFE000u);
-                            if (__any_sync(0xffffffffu, !(sum[0] + sum[1] == sum[0] + sum[1]))) {
-                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if ((x[k] & 0x7F800000u) == 0x7F800000u) x[k] = 0u;
-                            }
                             if (h == 0) {
+                                hand_over();
                                 if (n >= C::NV) ok = warp_wait(VFE + 8 * b, (n / C::NV - 1) & 1) && ok;
                                 tc::fence_after_sync();
                             }
-                            if (!C::FOLD) tc::tmem_st32(dst, x);
-                            if (!C::FOLD || w >= 2) {
+                            // the landed values are their own high parts
+                            if (!C::FOLD || w < 2) tc::tmem_st32(C::FOLD ? dst + 32 * h : dst, x);
+                            float2 sum = make_float2(0.f, 0.f);  // of the low parts: NaN where a value is not finite
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    x[k] = __float_as_uint(__uint_as_float(x[k]) - __uint_as_float(x[k] & 0xFFFFE000u));
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 lo = low2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                                sum = add2(sum, lo);
+                                x[k] = __float_as_uint(lo.x);
+                                x[k + 1] = __float_as_uint(lo.y);
                             }
-                            tc::tmem_st32(C::FOLD ? dst + 32 * h : dst + 32, x);
+                            if (!C::FOLD || w >= 2) tc::tmem_st32(C::FOLD ? dst + 32 * h : dst + 32, x);
+                            if (__any_sync(0xffffffffu, !(sum.x + sum.y == sum.x + sum.y))) {
+                                // such values are zeros to the tensor core; once more
+                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
+                                tc::tmem_st_wait();
+#pragma unroll 1
+                                for (int low = 0; low < 2; ++low) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) {
+                                        const float v = src[(32 * h + k) * C::VD];
+                                        x[k] = k0 + k >= end || (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u
+                                                   ? 0u
+                                                   : low ? __float_as_uint(v - __uint_as_float(tf32_part(v)))
+                                                         : __float_as_uint(v);
+                                    }
+                                    if (!C::FOLD)
+                                        tc::tmem_st32(dst + 32 * low, x);
+                                    else if ((w >= 2) == (low != 0))
+                                        tc::tmem_st32(dst + 32 * h, x);
+                                }
+                            }
                         }
-                        tc::tmem_st_wait();
-                        tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0 && ok) {
-                            mbar_arrive(VE + 8 * sl);
-                            mbar_arrive(VF + 8 * b);
-                        }
+                        if (lane == 0 && ok) mbar_arrive(VE + 8 * sl);
+                        handed = VF + 8 * b;
                     }
                 }
             }
+            hand_over();
             done(u);
         }
     } else if (warp == 28) {
