@@ -205,11 +205,13 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // memory, so that one MMA with twice the N makes a_hi.b_hi and a_hi.b_lo; the
 // sums of the products with a low part have columns of their own, where nothing
 // large cuts their bits off, and join the others in registers.  A TF32 operand's
-// f32 bits are read with the low 13 mantissa bits ignored, so a landed K tile is
-// its own high part.  The other A operands come from tensor memory, where a
-// warp's lanes are the operand's rows: K's low part is written there by the
-// thread that owns the key, V^T by the thread that owns the dim, which makes the
-// transposition free.  At head dim 64 one A holds V^T's high part in lanes 0-63
+// f32 bits are read with the low 13 mantissa bits ignored, so a value is its own
+// high part.  The A operands come from tensor memory, where a warp's lanes are
+// the operand's rows: K is written there by the thread that owns the key, V^T by
+// the thread that owns the dim, which makes the transposition free (and K's
+// piece of the ring free again as soon as it has been read; MMAs that take A
+// from shared memory too leave everyone else little of its bandwidth).  At head
+// dim 64 one A holds V^T's high part in lanes 0-63
 // and its low part in lanes 64-127, and one MMA forms all four products.
 //
 // Roles (eight warpgroups; the converters' and the last one's registers go to
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 //         tensor memory (its chain of sums is cut toward zero at each step) and
 //         is added to registers with rounded adds.  At the end out, or the
 //         unit's partial result.
-//   5, 6  converters: K's low part, and V^T (hi, lo), into tensor memory.
+//   5, 6  converters: K and V^T (hi, lo) into tensor memory.
 //   7     producer (16 KB pieces of K, 128 keys x 32 dims, swizzled, and of V by TMA
 //         into a ring), two MMA issuers, and a warp that finds the CTA's units and
 //         tells the others.
@@ -261,10 +263,11 @@ struct TreeCfg {
     static constexpr int QBYTES = 2 * RB * HD * 4, PBYTES = 2 * RB * KT * 4;
     static constexpr int OFF_P = QBYTES, OFF_RING = QBYTES + PBYTES;
     static constexpr int NSLOT = (224 * 1024 - OFF_RING) / PIECE;  // 8, 6, 8
-    static constexpr int NKL = HD == 256 ? 4 : 2, NV = HD == 64 ? 2 : 3;  // buffers of K lo and of V^T
+    static constexpr int NK = 2, NV = HD == 256 ? 3 : 2;  // buffers of K and of V^T
     // tensor memory columns
-    static constexpr int C_S = 0, C_O = 2 * RB, C_KL = C_O + DH * 2 * RB, C_V = C_KL + NKL * 32;
-    static constexpr int VCOLS = 64;                    // a V^T buffer: hi | lo, 32 keys each (FOLD: 64 keys)
+    static constexpr int C_S = 0, C_O = 2 * RB, C_K = C_O + DH * 2 * RB, C_V = C_K + NK * 64;
+    // a K buffer: hi | lo, 32 dims each; a V^T buffer: hi | lo, 32 keys each (FOLD: 64 keys)
+    static constexpr int VCOLS = 64;
     static_assert(C_V + NV * VCOLS <= 512, "tensor memory");
     static constexpr int TMEM_COLS = 512;
     // shared memory behind the ring: row data, scratch of the maxima, barriers, flags
@@ -279,7 +282,7 @@ struct TreeCfg {
     // S full, empty; P full, empty [4]; tile done with; O full, empty; Q full; unit's end; drain [2];
     // unit known, done with [2].
     // (A slot takes K and V in turn; barriers of their own let each kind's readers see every phase.)
-    static constexpr int NBAR = 4 * NSLOT + 2 * NKL + 2 * NV + 21;
+    static constexpr int NBAR = 4 * NSLOT + 2 * NK + 2 * NV + 21;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 56;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -390,6 +393,10 @@ __device__ __forceinline__ float tree_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A word of shared memory at addr + at.
+__device__ __forceinline__ void sts(uint32_t addr, int at, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr + at), "f"(v) : "memory");
+}
 // Packed f32x2 forms (each element rounded as the scalar operation would be).
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
@@ -418,17 +425,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // with a raise
     const uint32_t bar0 = sbase + C::OFF_BAR;
     const uint32_t KF = bar0, VL = KF + 8 * NSLOT, KE = VL + 8 * NSLOT, VE = KE + 8 * NSLOT, KLF = VE + 8 * NSLOT,
-                   KLE = KLF + 8 * C::NKL, VF = KLE + 8 * C::NKL, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
+                   KLE = KLF + 8 * C::NK, VF = KLE + 8 * C::NK, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
                    SE = SF + 8, PF = SE + 8, PE = PF + 32, FX = PE + 32, OF = FX + 8, OE = OF + 8, QF = OE + 8,
                    UE = QF + 8, DRAIN = UE + 8, GF = DRAIN + 16, GE = GF + 16;
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(KF + 8 * i, 1);
             mbar_init(VL + 8 * i, 1);
-            mbar_init(KE + 8 * i, 1);
+            mbar_init(KE + 8 * i, 4);
             mbar_init(VE + 8 * i, 4);
         }
-        for (int i = 0; i < C::NKL; ++i) {
+        for (int i = 0; i < C::NK; ++i) {
             mbar_init(KLF + 8 * i, 4);
             mbar_init(KLE + 8 * i, 1);
         }
@@ -617,128 +624,120 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
                 tc::fence_after_sync();
                 float x[CW];
+                bool masked;
+                uint32_t on;  // a bit per row: this thread's key is attended
+                // once, or where a maximum has to be raised once more
+                for (bool raise = false;; raise = true) {
 #pragma unroll
-                for (int c = 0; c < CW; c += 8) {
-                    uint32_t a[8] = {}, b[8] = {};
-                    const uint32_t col = 4 * c + 8 * sg;
-                    if (col < Rp) {
-                        tc::tmem_ld8(tlane + C::C_S + col, a);
-                        tc::tmem_ld8(tlane + C::C_S + Rp + col, b);
-                        tc::tmem_ld_wait();
-                    }
+                    for (int c = 0; c < CW; c += 8) {
+                        uint32_t a[8] = {}, b[8] = {};
+                        const uint32_t col = 4 * c + 8 * sg;
+                        if (col < Rp) {
+                            tc::tmem_ld8(tlane + C::C_S + col, a);
+                            tc::tmem_ld8(tlane + C::C_S + Rp + col, b);
+                            tc::tmem_ld_wait();
+                        }
 #pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const float2 y = add2(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])),
-                                              make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1])));
-                        x[c + k] = y.x;
-                        x[c + k + 1] = y.y;
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 y = add2(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])),
+                                                  make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1])));
+                            x[c + k] = y.x;
+                            x[c + k + 1] = y.y;
+                        }
                     }
+                    // whether the tile has keys that some row does not attend: nodes, or what
+                    // the rule leaves out
+                    masked = place + C::KT > past;
+                    on = 0xffffffffu;
+                    uint32_t kp = place + key;   // the key's place, then its position
+                    if (masked && kp >= past) {
+                        const uint32_t j = kp - past;
+                        on = 0u;
+                        if (j < d[kNodes]) {
+                            kp = past + P.depth[d[kRow] + j];
+                            // node after node, each with its rows of the block
+                            const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
+                            const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
+                            uint64_t all = 0;
+                            for (uint32_t i = row0 / G; i <= n1; ++i) {
+                                const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
+                                const uint32_t e = min((i + 1) * G - row0, rows);
+                                const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
+                                if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
+                            }
+                            on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
+                            if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
+                        }
+                    }
+                    if constexpr (SC) {
+                        if (P.rule.cap_out != 0.f) cap_scores<CW>(x, P.rule, cap_series(P.rule.cap_in));
+                        const uint32_t window = P.rule.window;
+                        const bool early = P.rule.doc_start && kp < __ldg(P.rule.doc_start + d[kReq]);
+                        if (window || P.rule.doc_start) masked = true;
+#pragma unroll
+                        for (int c = 0; c < CW; c += 4) {
+                            const int at = 32 * (c / 8) + c % 8;
+                            const float4 sl = *reinterpret_cast<const float4*>(sloper + at);
+                            const uint4 ps = *reinterpret_cast<const uint4*>(posr + at);
+                            const uint32_t far[4] = {ps.x - kp, ps.y - kp, ps.z - kp, ps.w - kp};
+                            const float by[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                x[c + k] = fmaf(-by[k], static_cast<float>(static_cast<int>(far[k])), x[c + k]);
+                                if (early || (window && far[k] >= window)) on &= ~(1u << (c + k));
+                            }
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -CUDART_INF_F;
+                    }
+                    if (raise) {
+                        // every row's maximum over the tile (as integers in the same order); the
+                        // accumulators have read the last factors, and are done with the last unit.
+                        // (P V of a tile starts when the one before it has been added, so behind PE's
+                        // phase FX is at its last one)
+                        if (gt) ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && warp_wait(FX, (gt - 1) & 1) && ok;
+                        if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) {
+                            const int b = __float_as_int(x[c] == x[c] ? x[c] : -1e30f);
+                            const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+                            if (lane == 0) tmax[wq * RB + row_of(c)] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+                        }
+                        bar_128(bar_id);
+                        if (key < CW) {
+                            const int row = row_of(key), at = row - 8 * sg;
+                            const float top = fmaxf(fmaxf(tmax[row], tmax[RB + row]),
+                                                    fmaxf(tmax[2 * RB + row], tmax[3 * RB + row]));
+                            const float old = ms[at], m = fmaxf(old, top);
+                            // (not 0: an infinity that the row holds has to stay one)
+                            fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
+                            ms[at] = m;
+                            if (key == 0) misc[10 + sg] = gt + 1;
+                        }
+                        bar_128(bar_id);
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) l[c] *= fs[32 * (c / 8) + c % 8];
+                    }
+                    float over[2] = {-1e30f, -1e30f};  // by how much the scores pass the maxima
+#pragma unroll
+                    for (int c = 0; c < CW; c += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
+                        const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+                        const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+                        over[0] = fmaxf(over[0], fmaxf(y.x, y.y));
+                        over[1] = fmaxf(over[1], fmaxf(z.x, z.y));
+                        x[c] = tree_exp2(y.x);
+                        x[c + 1] = tree_exp2(y.y);
+                        x[c + 2] = tree_exp2(z.x);
+                        x[c + 3] = tree_exp2(z.y);
+                    }
+                    if (raise || !bar_or(bar_id, fmaxf(over[0], over[1]) > 8.f)) break;
                 }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(SE);
-                // whether the tile has keys that some row does not attend: nodes, or what
-                // the rule leaves out
-                bool masked = place + C::KT > past;
-                uint32_t on = 0xffffffffu;   // a bit per row: this key is attended
-                uint32_t kp = place + key;   // the key's place, then its position
-                if (masked && kp >= past) {
-                    const uint32_t j = kp - past;
-                    on = 0u;
-                    if (j < d[kNodes]) {
-                        kp = past + P.depth[d[kRow] + j];
-                        // node after node, each with its rows of the block
-                        const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
-                        const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
-                        uint64_t all = 0;
-                        for (uint32_t i = row0 / G; i <= n1; ++i) {
-                            const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
-                            const uint32_t e = min((i + 1) * G - row0, rows);
-                            const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
-                            if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
-                        }
-                        on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
-                        if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
-                    }
-                }
-                if constexpr (SC) {
-                    if (P.rule.cap_out != 0.f) cap_scores<CW>(x, P.rule, cap_series(P.rule.cap_in));
-                    const uint32_t window = P.rule.window;
-                    const bool early = P.rule.doc_start && kp < __ldg(P.rule.doc_start + d[kReq]);
-                    if (window || P.rule.doc_start) masked = true;
-#pragma unroll
-                    for (int c = 0; c < CW; c += 4) {
-                        const int at = 32 * (c / 8) + c % 8;
-                        const float4 sl = *reinterpret_cast<const float4*>(sloper + at);
-                        const uint4 ps = *reinterpret_cast<const uint4*>(posr + at);
-                        const uint32_t far[4] = {ps.x - kp, ps.y - kp, ps.z - kp, ps.w - kp};
-                        const float by[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            x[c + k] = fmaf(-by[k], static_cast<float>(static_cast<int>(far[k])), x[c + k]);
-                            if (early || (window && far[k] >= window))
-                                on &= ~(1u << (c + k));
-                        }
-                    }
-                }
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -CUDART_INF_F;
-                }
-                // by how much the scores pass the maxima
-                float over[4] = {-1e30f, -1e30f, -1e30f, -1e30f};
-#pragma unroll
-                for (int c = 0; c < CW; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
-                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
-                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
-                    over[0] = fmaxf(over[0], y.x);
-                    over[1] = fmaxf(over[1], y.y);
-                    over[2] = fmaxf(over[2], z.x);
-                    over[3] = fmaxf(over[3], z.y);
-                }
-                const bool raise = bar_or(bar_id, fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > 8.f || !ok);
-                // this warp's block of P is free once the MMAs have read the last tile's (and, where V
-                // was not finite there, the accumulators have); at a unit's start, once the
-                // accumulators are done with the last unit
-                if (gt) {
-                    ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && ok;
-                    if (raise || misc[2 + 4 * ((gt - 1) & 1) + wq] == gt) ok = warp_wait(FX, (gt - 1) & 1) && ok;
-                    if (left == d[kTiles] && u) ok = warp_wait(UE, (u - 1) & 1) && ok;
-                }
-                if (raise) {  // (the accumulators have read the last factors)
-                    // every row's maximum over the tile (as integers in the same order)
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        const int b = __float_as_int(x[c] == x[c] ? x[c] : -1e30f);
-                        const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-                        if (lane == 0) tmax[wq * RB + row_of(c)] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-                    }
-                    bar_128(bar_id);
-                    if (key < CW) {
-                        const int row = row_of(key), at = row - 8 * sg;
-                        const float top = fmaxf(fmaxf(tmax[row], tmax[RB + row]),
-                                                fmaxf(tmax[2 * RB + row], tmax[3 * RB + row]));
-                        const float old = ms[at], m = fmaxf(old, top);
-                        // (not 0: an infinity that the row holds has to stay one)
-                        fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
-                        ms[at] = m;
-                        if (key == 0) misc[10 + sg] = gt + 1;
-                    }
-                    bar_128(bar_id);
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) l[c] *= fs[32 * (c / 8) + c % 8];
-                }
-#pragma unroll
-                for (int c = 0; c < CW; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
-                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
-                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
-                    x[c] = tree_exp2(y.x);
-                    x[c + 1] = tree_exp2(y.y);
-                    x[c + 2] = tree_exp2(z.x);
-                    x[c + 3] = tree_exp2(z.y);
-                }
                 if (masked) {  // the accumulators tell a masked key by its sign
 #pragma unroll
                     for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -0.f;
@@ -749,21 +748,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     l[c] = y.x;
                     l[c + 1] = y.y;
                 }
-                // P^T: [32-key blocks][hi rows | lo rows][128 B]
-                uint8_t* dst = smem + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane & 3) * 4;
+                // this warp's block of P is free once the MMAs have read the last tile's (and, where V
+                // was not finite there, the accumulators have); at a unit's start, once the
+                // accumulators are done with the last unit
+                if (gt) {
+                    ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && ok;
+                    if (misc[2 + 4 * ((gt - 1) & 1) + wq] == gt) ok = warp_wait(FX, (gt - 1) & 1) && ok;
+                    if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
+                }
+                // P^T: [32-key blocks][hi rows | lo rows][128 B], 16-byte pieces swizzled by the row
+                const uint32_t dst = sbase + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
+                const uint32_t dst2 = dst + Rp * 128;
 #pragma unroll
-                for (int c0 = 0; c0 < CW; c0 += 8) {
-                    if (4 * c0 + 8 * sg < static_cast<int>(Rp)) {
-#pragma unroll
-                        for (int c = c0; c < c0 + 8; c += 2) {
-                            const float2 lo = low2(x[c], x[c + 1]);
-                            uint8_t* q = dst + (4 * c0 + c % 8) * 128 + (((lane >> 2) ^ (c & 7)) << 4);
-                            *reinterpret_cast<float*>(q) = x[c];
-                            *reinterpret_cast<float*>(q + Rp * 128) = lo.x;
-                            q = dst + (4 * c0 + c % 8 + 1) * 128 + (((lane >> 2) ^ ((c + 1) & 7)) << 4);
-                            *reinterpret_cast<float*>(q) = x[c + 1];
-                            *reinterpret_cast<float*>(q + Rp * 128) = lo.y;
-                        }
+                for (int c = 0; c < CW; c += 2) {
+                    if (4 * (c / 8 * 8) + 8 * sg < static_cast<int>(Rp)) {
+                        const float2 lo = low2(x[c], x[c + 1]);
+                        const int at = (32 * (c / 8) + c % 8) * 128;
+                        sts(dst ^ (c % 8) << 4, at, x[c]);
+                        sts(dst2 ^ (c % 8) << 4, at, lo.x);
+                        sts(dst ^ (c % 8 + 1) << 4, at + 128, x[c + 1]);
+                        sts(dst2 ^ (c % 8 + 1) << 4, at + 128, lo.y);
                     }
                 }
                 if (left == 1) {  // the rows' sums over the warp's keys, a lane per row
@@ -947,25 +951,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (uint32_t t = 0; t < tiles; ++t) {
 #pragma unroll 1
                     for (int j = 0; j < C::KP; ++j, ++pc, ++n) {
-                        const uint32_t sl = pc % NSLOT, b = n % C::NKL;
+                        const uint32_t sl = pc % NSLOT, b = n % C::NK;
                         landed(KF + 8 * sl);
                         const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
-                        float4 x[8];
-                        uint32_t lo[32];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) x[c] = *reinterpret_cast<const float4*>(src + ((c ^ (me & 7)) << 4));
-                        hand_over();
+                        uint32_t x[32];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const float2 a = low2(x[c].x, x[c].y), e = low2(x[c].z, x[c].w);
-                            lo[4 * c] = __float_as_uint(a.x);
-                            lo[4 * c + 1] = __float_as_uint(a.y);
-                            lo[4 * c + 2] = __float_as_uint(e.x);
-                            lo[4 * c + 3] = __float_as_uint(e.y);
+                            const uint4 y = *reinterpret_cast<const uint4*>(src + ((c ^ (me & 7)) << 4));
+                            x[4 * c] = y.x;
+                            x[4 * c + 1] = y.y;
+                            x[4 * c + 2] = y.z;
+                            x[4 * c + 3] = y.w;
                         }
-                        if (n >= C::NKL) ok = warp_wait(KLE + 8 * b, (n / C::NKL - 1) & 1) && ok;
+                        hand_over();
+                        if (n >= C::NK) ok = warp_wait(KLE + 8 * b, (n / C::NK - 1) & 1) && ok;
                         tc::fence_after_sync();
-                        tc::tmem_st32(tlane + C::C_KL + 32 * b, lo);
+                        const uint32_t dst = tlane + C::C_K + 64 * b;
+                        tc::tmem_st32(dst, x);  // (the landed values are their own high parts)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 lo = low2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                            x[k] = __float_as_uint(lo.x);
+                            x[k + 1] = __float_as_uint(lo.y);
+                        }
+                        tc::tmem_st32(dst + 32, x);
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(KE + 8 * sl);
                         handed = KLF + 8 * b;
                     }
                     if (t) pc += C::VP;
@@ -983,14 +994,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
                         const uint32_t dst = tlane + C::C_V + C::VCOLS * b;
 #pragma unroll 1
-                        for (int h = 0; h < C::VK / 32; ++h) {  // 32 keys at a time
-                            const uint32_t k0 = j / C::DH * C::VK + 32 * h;
-                            uint32_t x[32];
+                        for (int h = 0; h < C::VK / 16; ++h) {  // 16 keys at a time
+                            const uint32_t k0 = j / C::DH * C::VK + 16 * h;
+                            uint32_t x[16];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(src[(32 * h + k) * C::VD]);
-                            if (k0 + 32 > end) {
+                            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(src[(16 * h + k) * C::VD]);
+                            if (k0 + 16 > end) {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
+                                for (int k = 0; k < 16; ++k)
                                     if (k0 + k >= end) x[k] = 0u;
                             }
                             if (h == 0) {
@@ -999,16 +1010,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 tc::fence_after_sync();
                             }
                             // the landed values are their own high parts
-                            if (!C::FOLD || w < 2) tc::tmem_st32(C::FOLD ? dst + 32 * h : dst, x);
+                            if (!C::FOLD || w < 2) tc::tmem_st16(dst + 16 * h, x);
                             float2 sum = make_float2(0.f, 0.f);  // of the low parts: NaN where a value is not finite
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
+                            for (int k = 0; k < 16; k += 2) {
                                 const float2 lo = low2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
                                 sum = add2(sum, lo);
                                 x[k] = __float_as_uint(lo.x);
                                 x[k + 1] = __float_as_uint(lo.y);
                             }
-                            if (!C::FOLD || w >= 2) tc::tmem_st32(C::FOLD ? dst + 32 * h : dst + 32, x);
+                            if (!C::FOLD || w >= 2) tc::tmem_st16((C::FOLD ? dst : dst + 32) + 16 * h, x);
                             if (__any_sync(0xffffffffu, !(sum.x + sum.y == sum.x + sum.y))) {
                                 // such values are zeros to the tensor core; once more
                                 if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
@@ -1016,17 +1027,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
                                 for (int low = 0; low < 2; ++low) {
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k) {
-                                        const float v = src[(32 * h + k) * C::VD];
+                                    for (int k = 0; k < 16; ++k) {
+                                        const float v = src[(16 * h + k) * C::VD];
                                         x[k] = k0 + k >= end || (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u
                                                    ? 0u
                                                    : low ? __float_as_uint(v - __uint_as_float(tf32_part(v)))
                                                          : __float_as_uint(v);
                                     }
                                     if (!C::FOLD)
-                                        tc::tmem_st32(dst + 32 * low, x);
+                                        tc::tmem_st16(dst + 32 * low + 16 * h, x);
                                     else if ((w >= 2) == (low != 0))
-                                        tc::tmem_st32(dst + 32 * h, x);
+                                        tc::tmem_st16(dst + 16 * h, x);
                                 }
                             }
                         }
@@ -1137,7 +1148,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         regs_decrease<kRegAux>();
         const bool lead = tc::elect_one();
         bool ok = true;
-        uint32_t pc = 0, n_piece = 0, tiles = 0;  // pieces, this warp's, its tiles
+        uint32_t n_piece = 0, tiles = 0;  // this warp's pieces, its tiles
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
             const volatile uint32_t* d = words(u);
@@ -1150,30 +1161,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const uint32_t i1 = tc::idesc_tf32(128, 0, false) | (Rp >> 3) << 17;
             const uint32_t block = 2 * Rp * 128 >> 4;  // a 32-wide block of Q or P
             if (warp == 29) {
-                const uint64_t kdesc0 = tc::smem_desc(sbase + C::OFF_RING, 16, 1024, tc::kSwizzle128B);
                 const uint64_t qdesc0 = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
                 const uint32_t sc = tb + C::C_S, sl2 = sc + Rp;
                 ok = warp_wait(QF, u & 1) && ok;
                 for (uint32_t t = 0; t < n; ++t, ++tiles) {
                     if (tiles) ok = warp_wait(SE, (tiles - 1) & 1) && ok;
 #pragma unroll 1
-                    for (int j = 0; j < C::KP; ++j, ++pc, ++n_piece) {
-                        const uint32_t sl = pc % NSLOT, b = n_piece % C::NKL;
-                        // (the converters have waited for the piece to land)
-                        ok = warp_wait(KLF + 8 * b, (n_piece / C::NKL) & 1) && ok;
+                    for (int j = 0; j < C::KP; ++j, ++n_piece) {
+                        const uint32_t b = n_piece % C::NK;
+                        ok = warp_wait(KLF + 8 * b, (n_piece / C::NK) & 1) && ok;
                         if (!ok) continue;
                         tc::fence_after_sync();
-                        const uint64_t kd = kdesc0 + (sl * C::PIECE >> 4), qd = qdesc0 + j * block;
-                        const uint32_t kl = tb + C::C_KL + 32 * b, ke = KE + 8 * sl, kle = KLE + 8 * b;
+                        const uint64_t qd = qdesc0 + j * block;
+                        const uint32_t k = tb + C::C_K + 64 * b, kle = KLE + 8 * b;
                         const uint32_t more = j ? 1u : 0u;
                         if (lead) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_tf32_ss(sc, kd + 2 * kk, qd + 2 * kk, i2, kk ? 1u : more);
+                                tc::mma_tf32_ts(sc, k + 8 * kk, qd + 2 * kk, i2, kk ? 1u : more);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_tf32_ts(sl2, kl + 8 * kk, qd + 2 * kk, i1, 1u);
-                            tc::mma_commit(ke);
+                                tc::mma_tf32_ts(sl2, k + 32 + 8 * kk, qd + 2 * kk, i1, 1u);
                             tc::mma_commit(kle);
                         }
                         __syncwarp();
@@ -1181,9 +1189,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     // (the failure-path test option withholds the CTA's first score-ready signal)
                     if (lead && ok && !(tiles == 0 && (P.flags & kOptTestStall))) tc::mma_commit(SF);
                     __syncwarp();
-                    if (t) pc += C::VP;  // V(t - 1) stands behind K(t) in the ring, ...
                 }
-                pc += C::VP;  // ... and the unit's last V behind that
             } else {
                 const uint64_t pdesc0 = tc::smem_desc(sbase + C::OFF_P, 16, 1024, tc::kSwizzle128B);
                 for (uint32_t t = 0; t < n; ++t, ++tiles) {
