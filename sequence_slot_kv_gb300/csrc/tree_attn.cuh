@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 //         tensor memory (its chain of sums is cut toward zero at each step) and
 //         is added to registers with rounded adds.  At the end out, or the
 //         unit's partial result.
-//   5, 6  converters: K and V^T (hi, lo) into tensor memory.
+//   5, 6  converters, a piece each by turns: K and V^T (hi, lo) into tensor memory.
 //   7     producer (16 KB pieces of K, 128 keys x 32 dims, swizzled, and of V by TMA
 //         into a ring), two MMA issuers, and a warp that finds the CTA's units and
 //         tells the others.
@@ -263,7 +263,7 @@ struct TreeCfg {
     static constexpr int QBYTES = 2 * RB * HD * 4, PBYTES = 2 * RB * KT * 4;
     static constexpr int OFF_P = QBYTES, OFF_RING = QBYTES + PBYTES;
     static constexpr int NSLOT = (224 * 1024 - OFF_RING) / PIECE;  // 8, 6, 8
-    static constexpr int NK = 2, NV = HD == 256 ? 3 : 2;  // buffers of K and of V^T
+    static constexpr int NK = 2, NV = 2;                // buffers of K and of V^T
     // tensor memory columns
     static constexpr int C_S = 0, C_O = 2 * RB, C_K = C_O + DH * 2 * RB, C_V = C_K + NK * 64;
     // a K buffer: hi | lo, 32 dims each; a V^T buffer: hi | lo, 32 keys each (FOLD: 64 keys)
@@ -917,17 +917,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
     } else if (warp < 28) {
         // ------------------------------------------------------------ converters
+        // The two warpgroups take the pieces by turns; with an even number of
+        // slots, of a tile's pieces and of buffers, each sees every phase of its
+        // own barriers.
+        static_assert(NSLOT % 2 == 0 && C::KP % 2 == 0 && C::VP % 2 == 0 && C::NK == 2 && C::NV == 2, "turns");
         regs_decrease<kRegConv>();
-        const bool is_k = warp < 24;
+        const uint32_t turn = warp < 24 ? 0u : 1u;
         const int w = warp & 3, me = w * 32 + lane;
         const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
-        uint32_t pc = 0, n = 0, gt = 0, phase = 0;  // pieces, this kind's, tiles; per slot: its parity
+        // pieces, this warpgroup's of K and of V, tiles; per slot: the parity of its K, 16 up of its V
+        uint32_t pc = 0, nk = 0, nv = 0, gt = 0, phase = 0;
         bool ok = true;
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
             const volatile uint32_t* d = words(u);
             if (!ok || !d[kMore]) break;
-            const uint32_t tiles = d[kTiles];
+            const uint32_t last = 2 * d[kTiles] - 1;
+            uint32_t end = d[kPast] + d[kNodes] - d[kPlace];  // keys that the request has from the tile on
             // A piece's stores to tensor memory are waited for, and the piece handed over, only
             // after the next piece's loads, if that has landed already.
             uint32_t handed = 0;  // the barrier of the piece that is still to be handed over
@@ -939,20 +945,84 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (lane == 0 && ok) mbar_arrive(handed);
                 handed = 0;
             };
-            auto landed = [&](uint32_t bar) {
-                const uint32_t parity = phase >> (pc % NSLOT) & 1;
-                phase ^= 1u << (pc % NSLOT);
+            auto landed = [&](uint32_t bar, uint32_t bit) {
+                const uint32_t parity = phase >> bit & 1;
+                phase ^= 1u << bit;
                 if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
                 hand_over();
                 ok = warp_wait(bar, parity) && ok;
             };
             // K(0), then K(t + 1) and V(t) by turns
-            if (is_k) {
-                for (uint32_t t = 0; t < tiles; ++t) {
+            for (uint32_t i = 0; i <= last; ++i) {
+                if (i == last || (i && !(i & 1))) {
+                    pc += turn;
 #pragma unroll 1
-                    for (int j = 0; j < C::KP; ++j, ++pc, ++n) {
-                        const uint32_t sl = pc % NSLOT, b = n % C::NK;
-                        landed(KF + 8 * sl);
+                    for (int j = static_cast<int>(turn); j < C::VP; j += 2, pc += 2, ++nv) {
+                        const uint32_t sl = pc % NSLOT;
+                        landed(VL + 8 * sl, 16 + sl);
+                        const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
+                        const uint32_t dst = tlane + C::C_V + C::VCOLS * turn;
+#pragma unroll 1
+                        for (int h = 0; h < C::VK / 32; ++h) {  // 32 keys at a time
+                            const uint32_t k0 = j / C::DH * C::VK + 32 * h;
+                            uint32_t x[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(src[(32 * h + k) * C::VD]);
+                            if (k0 + 32 > end) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (k0 + k >= end) x[k] = 0u;
+                            }
+                            if (h == 0) {
+                                hand_over();
+                                if (nv) ok = warp_wait(VFE + 8 * turn, (nv - 1) & 1) && ok;
+                                tc::fence_after_sync();
+                            }
+                            // the landed values are their own high parts
+                            if (!C::FOLD || w < 2) tc::tmem_st32(dst + 32 * h, x);
+                            float2 sum = make_float2(0.f, 0.f);  // of the low parts: NaN where a value is not finite
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 lo = low2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                                sum = add2(sum, lo);
+                                x[k] = __float_as_uint(lo.x);
+                                x[k + 1] = __float_as_uint(lo.y);
+                            }
+                            if (!C::FOLD || w >= 2) tc::tmem_st32((C::FOLD ? dst : dst + 32) + 32 * h, x);
+                            if (__any_sync(0xffffffffu, !(sum.x + sum.y == sum.x + sum.y))) {
+                                // such values are zeros to the tensor core; once more
+                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
+                                tc::tmem_st_wait();
+#pragma unroll 1
+                                for (int low = 0; low < 2; ++low) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) {
+                                        const float v = src[(32 * h + k) * C::VD];
+                                        x[k] = k0 + k >= end || (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u
+                                                   ? 0u
+                                                   : low ? __float_as_uint(v - __uint_as_float(tf32_part(v)))
+                                                         : __float_as_uint(v);
+                                    }
+                                    if (!C::FOLD)
+                                        tc::tmem_st32(dst + 32 * low, x);
+                                    else if ((w >= 2) == (low != 0))
+                                        tc::tmem_st32(dst + 32 * h, x);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(VE + 8 * sl);
+                        handed = VF + 8 * turn;
+                    }
+                    pc -= turn;
+                    ++gt;
+                    end += C::KT;
+                } else {
+                    pc += turn;
+#pragma unroll 1
+                    for (int j = static_cast<int>(turn); j < C::KP; j += 2, pc += 2, ++nk) {
+                        const uint32_t sl = pc % NSLOT;
+                        landed(KF + 8 * sl, sl);
                         const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
                         uint32_t x[32];
 #pragma unroll
@@ -964,9 +1034,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             x[4 * c + 3] = y.w;
                         }
                         hand_over();
-                        if (n >= C::NK) ok = warp_wait(KLE + 8 * b, (n / C::NK - 1) & 1) && ok;
+                        if (nk) ok = warp_wait(KLE + 8 * turn, (nk - 1) & 1) && ok;
                         tc::fence_after_sync();
-                        const uint32_t dst = tlane + C::C_K + 64 * b;
+                        const uint32_t dst = tlane + C::C_K + 64 * turn;
                         tc::tmem_st32(dst, x);  // (the landed values are their own high parts)
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
@@ -977,74 +1047,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         tc::tmem_st32(dst + 32, x);
                         __syncwarp();
                         if (lane == 0 && ok) mbar_arrive(KE + 8 * sl);
-                        handed = KLF + 8 * b;
+                        handed = KLF + 8 * turn;
                     }
-                    if (t) pc += C::VP;
-                }
-                pc += C::VP;
-            } else {
-                uint32_t end = d[kPast] + d[kNodes] - d[kPlace];  // keys that the request has from the tile on
-                pc += C::KP;
-                for (uint32_t t = 0; t < tiles; ++t, ++gt, end += C::KT) {
-                    if (t + 1 < tiles) pc += C::KP;
-#pragma unroll 1
-                    for (int j = 0; j < C::VP; ++j, ++pc, ++n) {
-                        const uint32_t sl = pc % NSLOT, b = n % C::NV;
-                        landed(VL + 8 * sl);
-                        const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
-                        const uint32_t dst = tlane + C::C_V + C::VCOLS * b;
-#pragma unroll 1
-                        for (int h = 0; h < C::VK / 16; ++h) {  // 16 keys at a time
-                            const uint32_t k0 = j / C::DH * C::VK + 16 * h;
-                            uint32_t x[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(src[(16 * h + k) * C::VD]);
-                            if (k0 + 16 > end) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (k0 + k >= end) x[k] = 0u;
-                            }
-                            if (h == 0) {
-                                hand_over();
-                                if (n >= C::NV) ok = warp_wait(VFE + 8 * b, (n / C::NV - 1) & 1) && ok;
-                                tc::fence_after_sync();
-                            }
-                            // the landed values are their own high parts
-                            if (!C::FOLD || w < 2) tc::tmem_st16(dst + 16 * h, x);
-                            float2 sum = make_float2(0.f, 0.f);  // of the low parts: NaN where a value is not finite
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float2 lo = low2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                                sum = add2(sum, lo);
-                                x[k] = __float_as_uint(lo.x);
-                                x[k + 1] = __float_as_uint(lo.y);
-                            }
-                            if (!C::FOLD || w >= 2) tc::tmem_st16((C::FOLD ? dst : dst + 32) + 16 * h, x);
-                            if (__any_sync(0xffffffffu, !(sum.x + sum.y == sum.x + sum.y))) {
-                                // such values are zeros to the tensor core; once more
-                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
-                                tc::tmem_st_wait();
-#pragma unroll 1
-                                for (int low = 0; low < 2; ++low) {
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const float v = src[(16 * h + k) * C::VD];
-                                        x[k] = k0 + k >= end || (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u
-                                                   ? 0u
-                                                   : low ? __float_as_uint(v - __uint_as_float(tf32_part(v)))
-                                                         : __float_as_uint(v);
-                                    }
-                                    if (!C::FOLD)
-                                        tc::tmem_st16(dst + 32 * low + 16 * h, x);
-                                    else if ((w >= 2) == (low != 0))
-                                        tc::tmem_st16(dst + 16 * h, x);
-                                }
-                            }
-                        }
-                        __syncwarp();
-                        if (lane == 0 && ok) mbar_arrive(VE + 8 * sl);
-                        handed = VF + 8 * b;
-                    }
+                    pc -= turn;
                 }
             }
             hand_over();
