@@ -624,120 +624,121 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 }
                 tc::fence_after_sync();
                 float x[CW];
-                bool masked;
-                uint32_t on;  // a bit per row: this thread's key is attended
-                // once, or where a maximum has to be raised once more
-                for (bool raise = false;; raise = true) {
 #pragma unroll
-                    for (int c = 0; c < CW; c += 8) {
-                        uint32_t a[8] = {}, b[8] = {};
-                        const uint32_t col = 4 * c + 8 * sg;
-                        if (col < Rp) {
-                            tc::tmem_ld8(tlane + C::C_S + col, a);
-                            tc::tmem_ld8(tlane + C::C_S + Rp + col, b);
-                            tc::tmem_ld_wait();
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const float2 y = add2(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])),
-                                                  make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1])));
-                            x[c + k] = y.x;
-                            x[c + k + 1] = y.y;
-                        }
+                for (int c = 0; c < CW; c += 8) {
+                    uint32_t a[8] = {}, b[8] = {};
+                    const uint32_t col = 4 * c + 8 * sg;
+                    if (col < Rp) {
+                        tc::tmem_ld8(tlane + C::C_S + col, a);
+                        tc::tmem_ld8(tlane + C::C_S + Rp + col, b);
+                        tc::tmem_ld_wait();
                     }
-                    // whether the tile has keys that some row does not attend: nodes, or what
-                    // the rule leaves out
-                    masked = place + C::KT > past;
-                    on = 0xffffffffu;
-                    uint32_t kp = place + key;   // the key's place, then its position
-                    if (masked && kp >= past) {
-                        const uint32_t j = kp - past;
-                        on = 0u;
-                        if (j < d[kNodes]) {
-                            kp = past + P.depth[d[kRow] + j];
-                            // node after node, each with its rows of the block
-                            const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
-                            const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
-                            uint64_t all = 0;
-                            for (uint32_t i = row0 / G; i <= n1; ++i) {
-                                const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
-                                const uint32_t e = min((i + 1) * G - row0, rows);
-                                const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
-                                if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
-                            }
-                            on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
-                            if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
-                        }
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 y = add2(make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1])),
+                                              make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1])));
+                        x[c + k] = y.x;
+                        x[c + k + 1] = y.y;
                     }
-                    if constexpr (SC) {
-                        if (P.rule.cap_out != 0.f) cap_scores<CW>(x, P.rule, cap_series(P.rule.cap_in));
-                        const uint32_t window = P.rule.window;
-                        const bool early = P.rule.doc_start && kp < __ldg(P.rule.doc_start + d[kReq]);
-                        if (window || P.rule.doc_start) masked = true;
-#pragma unroll
-                        for (int c = 0; c < CW; c += 4) {
-                            const int at = 32 * (c / 8) + c % 8;
-                            const float4 sl = *reinterpret_cast<const float4*>(sloper + at);
-                            const uint4 ps = *reinterpret_cast<const uint4*>(posr + at);
-                            const uint32_t far[4] = {ps.x - kp, ps.y - kp, ps.z - kp, ps.w - kp};
-                            const float by[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                x[c + k] = fmaf(-by[k], static_cast<float>(static_cast<int>(far[k])), x[c + k]);
-                                if (early || (window && far[k] >= window)) on &= ~(1u << (c + k));
-                            }
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -CUDART_INF_F;
-                    }
-                    if (raise) {
-                        // every row's maximum over the tile (as integers in the same order); the
-                        // accumulators have read the last factors, and are done with the last unit.
-                        // (P V of a tile starts when the one before it has been added, so behind PE's
-                        // phase FX is at its last one)
-                        if (gt) ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && warp_wait(FX, (gt - 1) & 1) && ok;
-                        if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) {
-                            const int b = __float_as_int(x[c] == x[c] ? x[c] : -1e30f);
-                            const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-                            if (lane == 0) tmax[wq * RB + row_of(c)] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-                        }
-                        bar_128(bar_id);
-                        if (key < CW) {
-                            const int row = row_of(key), at = row - 8 * sg;
-                            const float top = fmaxf(fmaxf(tmax[row], tmax[RB + row]),
-                                                    fmaxf(tmax[2 * RB + row], tmax[3 * RB + row]));
-                            const float old = ms[at], m = fmaxf(old, top);
-                            // (not 0: an infinity that the row holds has to stay one)
-                            fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
-                            ms[at] = m;
-                            if (key == 0) misc[10 + sg] = gt + 1;
-                        }
-                        bar_128(bar_id);
-#pragma unroll
-                        for (int c = 0; c < CW; ++c) l[c] *= fs[32 * (c / 8) + c % 8];
-                    }
-                    float over[2] = {-1e30f, -1e30f};  // by how much the scores pass the maxima
-#pragma unroll
-                    for (int c = 0; c < CW; c += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
-                        const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
-                        const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
-                        over[0] = fmaxf(over[0], fmaxf(y.x, y.y));
-                        over[1] = fmaxf(over[1], fmaxf(z.x, z.y));
-                        x[c] = tree_exp2(y.x);
-                        x[c + 1] = tree_exp2(y.y);
-                        x[c + 2] = tree_exp2(z.x);
-                        x[c + 3] = tree_exp2(z.y);
-                    }
-                    if (raise || !bar_or(bar_id, fmaxf(over[0], over[1]) > 8.f)) break;
                 }
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(SE);
+                // whether the tile has keys that some row does not attend: nodes, or what
+                // the rule leaves out
+                bool masked = place + C::KT > past;
+                uint32_t on = 0xffffffffu;  // a bit per row: this thread's key is attended
+                uint32_t kp = place + key;   // the key's place, then its position
+                if (masked && kp >= past) {
+                    const uint32_t j = kp - past;
+                    on = 0u;
+                    if (j < d[kNodes]) {
+                        kp = past + P.depth[d[kRow] + j];
+                        // node after node, each with its rows of the block
+                        const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
+                        const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
+                        uint64_t all = 0;
+#pragma unroll 4
+                        for (uint32_t i = row0 / G; i <= n1; ++i) {
+                            const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
+                            const uint32_t e = min((i + 1) * G - row0, rows);
+                            const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
+                            if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
+                        }
+                        on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
+                        if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
+                    }
+                }
+                if constexpr (SC) {
+                    if (P.rule.cap_out != 0.f) cap_scores<CW>(x, P.rule, cap_series(P.rule.cap_in));
+                    const uint32_t window = P.rule.window;
+                    const bool early = P.rule.doc_start && kp < __ldg(P.rule.doc_start + d[kReq]);
+                    if (window || P.rule.doc_start) masked = true;
+#pragma unroll
+                    for (int c = 0; c < CW; c += 4) {
+                        const int at = 32 * (c / 8) + c % 8;
+                        const float4 sl = *reinterpret_cast<const float4*>(sloper + at);
+                        const uint4 ps = *reinterpret_cast<const uint4*>(posr + at);
+                        const uint32_t far[4] = {ps.x - kp, ps.y - kp, ps.z - kp, ps.w - kp};
+                        const float by[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            x[c + k] = fmaf(-by[k], static_cast<float>(static_cast<int>(far[k])), x[c + k]);
+                            if (early || (window && far[k] >= window)) on &= ~(1u << (c + k));
+                        }
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -CUDART_INF_F;
+                }
+                float over[2] = {-1e30f, -1e30f};  // by how much the scores pass the maxima
+#pragma unroll
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
+                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+                    over[0] = fmaxf(over[0], fmaxf(y.x, y.y));
+                    over[1] = fmaxf(over[1], fmaxf(z.x, z.y));
+                }
+                if (bar_or(bar_id, fmaxf(over[0], over[1]) > 8.f)) {
+                    // every row's maximum over the tile (as integers in the same order); the
+                    // accumulators have read the last factors, and are done with the last unit.
+                    // (P V of a tile starts when the one before it has been added, so behind PE's
+                    // phase FX is at its last one)
+                    if (gt) ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && warp_wait(FX, (gt - 1) & 1) && ok;
+                    if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) {
+                        const int b = __float_as_int(x[c] == x[c] ? x[c] : -1e30f);
+                        const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+                        if (lane == 0) tmax[wq * RB + row_of(c)] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+                    }
+                    bar_128(bar_id);
+                    if (key < CW) {
+                        const int row = row_of(key), at = row - 8 * sg;
+                        const float top = fmaxf(fmaxf(tmax[row], tmax[RB + row]),
+                                                fmaxf(tmax[2 * RB + row], tmax[3 * RB + row]));
+                        const float old = ms[at], m = fmaxf(old, top);
+                        // (not 0: an infinity that the row holds has to stay one)
+                        fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
+                        ms[at] = m;
+                        if (key == 0) misc[10 + sg] = gt + 1;
+                    }
+                    bar_128(bar_id);
+#pragma unroll
+                    for (int c = 0; c < CW; ++c) l[c] *= fs[32 * (c / 8) + c % 8];
+                }
+#pragma unroll
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(ms + 32 * (c / 8) + c % 8);
+                    const float2 y = sub2(make_float2(x[c], x[c + 1]), make_float2(m.x, m.y));
+                    const float2 z = sub2(make_float2(x[c + 2], x[c + 3]), make_float2(m.z, m.w));
+                    x[c] = tree_exp2(y.x);
+                    x[c + 1] = tree_exp2(y.y);
+                    x[c + 2] = tree_exp2(z.x);
+                    x[c + 3] = tree_exp2(z.y);
+                }
                 if (masked) {  // the accumulators tell a masked key by its sign
 #pragma unroll
                     for (int c = 0; c < CW; ++c) x[c] = on >> c & 1u ? x[c] : -0.f;
