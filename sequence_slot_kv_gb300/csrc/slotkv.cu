@@ -1482,8 +1482,8 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     P.V = h->V;
     P.q_rot = h->sc_q;
     P.base = reinterpret_cast<uint64_t*>(h->tree_idx);
-    P.anc = h->tree_idx + 2 * (R + 1);
-    P.req_of = P.anc + R * slotkv::kTreeWords;
+    P.below = h->tree_idx + 2 * (R + 1);
+    P.req_of = P.below + R * slotkv::kTreeWords;
     P.part = h->tree_part;
     P.part_ml = P.part + pr * h->head_dim;
     const int paged = block_tables ? 1 : 0;

@@ -33,14 +33,17 @@ __device__ __forceinline__ uint32_t tree_place(const TreeParams& P, uint32_t r, 
 }
 
 // ------------------------------------------------------------------ prep
-// CTA (request, part): checks the request, finds every node's ancestors and
-// depth (pointer doubling over the tree in shared memory: each round joins a
-// node's set with that of the node it points at and doubles the distance, so
-// a chain of 256 takes 8 rounds), then forms its part of the request's
-// vectors, one warp per (node, kTreeQHeads query heads or kTreeKvHeads kv
-// heads): q' = RoPE(RMSnorm(q) w) scale log2(e) into the workspace, k' and v
-// into the node's cache row, with the decode kernel's vector routines (so
-// the same bits as a decode step's at that position).
+// CTA (request, part).  Every part checks the request and finds its nodes' depths
+// by pointer doubling over the tree in shared memory (a round adds to a node's
+// depth that of the node it points at and doubles the distance, so a chain of
+// 256 takes 8 rounds).  Part 0 does the same with the sets of ancestors and
+// writes, for every node, the set of the nodes that attend it.  The other parts
+// form the request's vectors, one warp per (node, kTreeQHeads query heads or
+// kTreeKvHeads kv heads): q' = RoPE(RMSnorm(q) w) scale log2(e) into the
+// workspace, k' and v into the node's cache row, with the decode kernel's
+// vector routines (so the same bits as a decode step's at that position).  A
+// call is bound by its dependent loads here; a warp's first rows are on their
+// way while the tree is looked at.
 constexpr int kTreeQHeads = 8, kTreeKvHeads = 4, kPrepThreads = 128, kPrepWarps = kPrepThreads / 32;
 
 __device__ __forceinline__ void tree_cp_async16(void* smem_dst, const void* gmem_src) {
@@ -79,8 +82,43 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
     grid_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t r = blockIdx.x;
-    TreeReq q = tree_request(P, r);
+    const bool sets = blockIdx.y == 0;
+    const TreeReq q = tree_request(P, r);
     if (q.n == 0) return;
+    // this warp's rows of item it, on their way
+    const uint32_t qg = (P.n_head + kTreeQHeads - 1) / kTreeQHeads;
+    const uint32_t groups = qg + (P.n_kv_head + kTreeKvHeads - 1) / kTreeKvHeads;
+    float* rows = reinterpret_cast<float*>(prep_smem) + warp * kTreeQHeads * HD;
+    float* vrows = rows + kTreeKvHeads * HD;
+    struct Item {
+        uint32_t node, x0, nx;
+        bool is_q;
+    };
+    auto item = [&](uint32_t it) {
+        Item m;
+        const uint32_t grp = it % groups;
+        m.node = it / groups;
+        m.is_q = grp < qg;
+        m.x0 = m.is_q ? grp * kTreeQHeads : (grp - qg) * kTreeKvHeads;
+        const uint32_t left = (m.is_q ? P.n_head : P.n_kv_head) - m.x0, most = m.is_q ? kTreeQHeads : kTreeKvHeads;
+        m.nx = left < most ? left : most;
+        return m;
+    };
+    auto load = [&](const Item& m) {
+        const size_t tok = q.s0 + m.node;
+        const float* src = m.is_q ? P.q + (tok * P.n_head + m.x0) * HD : P.k_new + (tok * P.n_kv_head + m.x0) * HD;
+        const float* vsrc = P.v_new + (tok * P.n_kv_head + m.x0) * HD;
+        for (uint32_t c = lane; c < m.nx * (HD / 4); c += 32) {
+            tree_cp_async16(rows + 4 * c, src + 4 * c);
+            if (!m.is_q) tree_cp_async16(vrows + 4 * c, vsrc + 4 * c);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const uint32_t step = (gridDim.y - 1) * kPrepWarps;
+    uint32_t it = sets || !q.ok ? 0xFFFFFFFFu : (blockIdx.y - 1) * kPrepWarps + warp;
+    const uint32_t items = q.ok ? q.n * groups : 0u;
+    if (it < items) load(item(it));
+    // the request's table and tree
     bool ok = q.ok;
     if (ok && P.block_tables) {
         const uint32_t used = (q.past + q.n - 1) / P.slot_ctx + 1;
@@ -94,21 +132,23 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
             ok = ok && (root || p < i);
             jump[i] = root || p >= i ? kTreeSkip : p;
             depth[i] = root ? 0u : 1u;
+            if (sets)
 #pragma unroll
-            for (uint32_t w = 0; w < kTreeWords; ++w) set[i][w] = i / 32 == w ? 1u << (i % 32) : 0u;
+                for (uint32_t w = 0; w < kTreeWords; ++w) set[i][w] = i / 32 == w ? 1u << (i % 32) : 0u;
         }
     }
     ok = __syncthreads_and(ok) != 0;
     if (!ok) {
-        if (blockIdx.y == 0) {
+        if (sets) {
             if (tid == 0) atomicOr(P.status, kDevRange);
             if (q.s0 + q.n <= P.n_tok && q.n <= P.n_tok)  // (no more than the rows there are)
                 for (uint32_t i = tid; i < q.n; i += kPrepThreads) P.req_of[q.s0 + i] = kTreeSkip;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         return;
     }
     constexpr int PER = kTreeNodes / kPrepThreads;
-    const uint32_t words = (q.n + 31) / 32;
+    const uint32_t words = sets ? (q.n + 31) / 32 : 0u;
     for (uint32_t far = 1; far < q.n; far *= 2) {
         uint32_t j[PER], d[PER] = {}, to[PER] = {}, s[PER][kTreeWords] = {};
         bool any = false;
@@ -137,46 +177,39 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
         }
         __syncthreads();
     }
-    if (blockIdx.y == 0) {
+    if (sets) {
         for (uint32_t i = tid; i < q.n; i += kPrepThreads) {
             P.req_of[q.s0 + i] = r;
             P.depth[q.s0 + i] = depth[i];
+        }
+        // transposed, 32 x 32 nodes at a time: a lane has a node's ancestors, a vote each
+        // ancestor's lane
+        for (uint32_t b = warp; b < words * words; b += kPrepWarps) {
+            const uint32_t wi = b / words, wj = b % words, i = 32 * wi + lane;
+            const uint32_t v = i < q.n ? set[i][wj] : 0u;
+            uint32_t mine = 0;
 #pragma unroll
-            for (uint32_t w = 0; w < kTreeWords; ++w)
-                P.anc[static_cast<size_t>(q.s0 + i) * kTreeWords + w] = set[i][w];
-        }
-    }
-    const uint32_t qg = (P.n_head + kTreeQHeads - 1) / kTreeQHeads;
-    const uint32_t groups = qg + (P.n_kv_head + kTreeKvHeads - 1) / kTreeKvHeads;
-    const float w1 = (P.flags & kOptNormPlusOne) ? 1.0f : 0.0f;
-    float* rows = reinterpret_cast<float*>(prep_smem) + warp * kTreeQHeads * HD;
-    float* vrows = rows + kTreeKvHeads * HD;
-    for (uint32_t it = blockIdx.y * kPrepWarps + warp; it < q.n * groups; it += gridDim.y * kPrepWarps) {
-        const uint32_t i = it / groups, grp = it % groups, tok = q.s0 + i;
-        const bool is_q = grp < qg;
-        const uint32_t x0 = is_q ? grp * kTreeQHeads : (grp - qg) * kTreeKvHeads;
-        const uint32_t left = (is_q ? P.n_head : P.n_kv_head) - x0, most = is_q ? kTreeQHeads : kTreeKvHeads;
-        const uint32_t nx = left < most ? left : most;
-        for (uint32_t x = 0; x < nx; ++x) {
-            const float* src = is_q ? P.q + (static_cast<size_t>(tok) * P.n_head + x0 + x) * HD
-                                    : P.k_new + (static_cast<size_t>(tok) * P.n_kv_head + x0 + x) * HD;
-            const float* vsrc = P.v_new + (static_cast<size_t>(tok) * P.n_kv_head + x0 + x) * HD;
-            for (int c = lane; c < HD / 4; c += 32) {
-                tree_cp_async16(rows + x * HD + 4 * c, src + 4 * c);
-                if (!is_q) tree_cp_async16(vrows + x * HD + 4 * c, vsrc + 4 * c);
+            for (uint32_t k = 0; k < 32; ++k) {
+                const uint32_t y = __ballot_sync(0xffffffffu, v >> k & 1u);
+                mine = lane == k ? y : mine;
             }
+            if (32 * wj + lane < q.n) P.below[static_cast<size_t>(q.s0 + 32 * wj + lane) * kTreeWords + wi] = mine;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        return;
+    }
+    const float w1 = (P.flags & kOptNormPlusOne) ? 1.0f : 0.0f;
+    for (; it < items; it += step) {
+        const Item m = item(it);
         float cs[HD / 64], sn[HD / 64];
-        warp_rope_angles<HD>(q.past + depth[i], P.inv_freq, cs, sn, lane);
-        const size_t at = is_q ? 0 : (static_cast<size_t>(tree_row(P, r, q.past + i)) * P.n_kv_head + x0) * HD;
+        warp_rope_angles<HD>(q.past + depth[m.node], P.inv_freq, cs, sn, lane);
+        const size_t at = m.is_q ? (static_cast<size_t>(q.s0 + m.node) * P.n_head + m.x0) * HD
+                                 : (static_cast<size_t>(tree_row(P, r, q.past + m.node)) * P.n_kv_head + m.x0) * HD;
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
-        for (uint32_t x = 0; x < nx; ++x) {
-            if (is_q) {
-                warp_norm_rope<HD>(rows + x * HD,
-                                   P.q_rot + (static_cast<size_t>(tok) * P.n_head + x0 + x) * HD, P.q_norm_w,
-                                   w1, P.scale_log2, P.eps, cs, sn, lane);
+        for (uint32_t x = 0; x < m.nx; ++x) {
+            if (m.is_q) {
+                warp_norm_rope<HD>(rows + x * HD, P.q_rot + at + x * HD, P.q_norm_w, w1, P.scale_log2, P.eps, cs, sn,
+                                   lane);
                 continue;
             }
             warp_norm_rope<HD>(rows + x * HD, P.K + at + x * HD, P.k_norm_w, w1, 1.0f, P.eps, cs, sn, lane);
@@ -188,6 +221,7 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
             }
         }
         __syncwarp();
+        if (it + step < items) load(item(it + step));
     }
 }
 
@@ -275,7 +309,8 @@ struct TreeCfg {
     static constexpr int OFF_F = OFF_M + 2 * RB * 4;            // factors of a raise, of the end [RB]
     static constexpr int OFF_POS = OFF_F + RB * 4;              // rows' positions [RB]
     static constexpr int OFF_SLOPE = OFF_POS + RB * 4;          // rows' slopes [RB]
-    static constexpr int OFF_MAX = OFF_SLOPE + RB * 4;          // a warp's maxima, its sums [4][RB]
+    static constexpr int OFF_NODE = OFF_SLOPE + RB * 4;         // rows' nodes, from the block's first (bytes) [RB]
+    static constexpr int OFF_MAX = OFF_NODE + RB;          // a warp's maxima, its sums [4][RB]
     static constexpr int OFF_DESC = OFF_MAX + 4 * RB * 4;       // what the roles need to know of a unit [2]
     static constexpr int OFF_BAR = OFF_DESC + 2 * 12 * 4;
     // K landed, V landed, K empty, V empty [NSLOT]; K lo full, empty [NKL]; V full, empty [NV];
@@ -326,11 +361,13 @@ __device__ __forceinline__ uint32_t tree_ctas(uint64_t total, uint32_t grid) {
     return total < grid ? static_cast<uint32_t>(total) : grid;
 }
 __device__ __forceinline__ uint64_t tree_first(uint64_t total, uint32_t ctas, uint32_t c) {
-    return total * c / ctas;
+    const uint64_t x = total * c;
+    return x >> 32 ? x / ctas : static_cast<uint32_t>(x) / ctas;  // (a division of 32 bits where they do)
 }
 // The CTA of tile x.
 __device__ __forceinline__ uint32_t tree_owner(uint64_t total, uint32_t ctas, uint64_t x) {
-    return static_cast<uint32_t>(((x + 1) * ctas - 1) / total);
+    const uint64_t y = (x + 1) * ctas - 1;
+    return (y | total) >> 32 ? static_cast<uint32_t>(y / total) : static_cast<uint32_t>(y) / static_cast<uint32_t>(total);
 }
 
 // A CTA's parts of units, in order.
@@ -467,61 +504,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc::tmem_alloc(sbase + C::OFF_MISC + 4, C::TMEM_COLS);
         tc::tmem_relinquish();
     }
-    // this CTA's range: every thread sums a part of the requests, a scan finds the
-    // request that the range begins in.  The ring is not in use yet.
-    uint64_t* sums = reinterpret_cast<uint64_t*>(smem);
-    uint64_t* found = sums + kTreeWarps;  // request, tiles into it
-    const uint32_t per = (P.n_req + kTreeThreads - 1) / kTreeThreads;
-    const uint32_t ra = tid * per < P.n_req ? tid * per : P.n_req;
-    const uint32_t rb = ra + per < P.n_req ? ra + per : P.n_req;
-    uint64_t mine = 0;
-    for (uint32_t r = ra; r < rb; ++r) mine += tree_shape<RB>(P, r).tiles(P.n_kv_head);
-    uint64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sums[warp] = incl;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    uint64_t at = incl - mine, total = 0;
-    for (int w = 0; w < kTreeWarps; ++w) {
-        if (w < warp) at += sums[w];
-        total += sums[w];
-    }
-    const uint32_t ctas = tree_ctas(total, gridDim.x);
-    const uint64_t u0 = ctas ? tree_first(total, ctas, blockIdx.x) : 0;
-    const uint64_t u1 = ctas ? tree_first(total, ctas, blockIdx.x + 1) : 0;
-    // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
-    const bool work = blockIdx.x < ctas && (sbase & 1023u) == 0;
-    if ((sbase & 1023u) && tid == 0) atomicOr(P.status, kDevTimeout);
-    if (work && at <= u0 && u0 < at + mine) {
-        uint64_t off = u0 - at;
-        for (uint32_t r = ra; r < rb; ++r) {
-            const uint64_t n = tree_shape<RB>(P, r).tiles(P.n_kv_head);
-            if (off < n) {
-                found[0] = r;
-                found[1] = off;
-                break;
-            }
-            off -= n;
-        }
-    }
-    if (blockIdx.x == 0) {  // for the combine kernel: every request's first tile, and the sum
-        uint64_t b = at;
-        for (uint32_t r = ra; r < rb; ++r) {
-            P.base[r] = b;
-            b += tree_shape<RB>(P, r).tiles(P.n_kv_head);
-        }
-        if (tid == 0) P.base[P.n_req] = total;
-    }
-    __syncthreads();
     const uint32_t tb = __shfl_sync(0xffffffffu, misc[1], 0);
-    const uint32_t r_first = work ? static_cast<uint32_t>(found[0]) : 0u;
-    const uint64_t off_first = work ? found[1] : 0u;
-    __syncthreads();  // (the scan's words are Q's from here on)
 
     // A bounded wait; once the CTA has given up every wait ends at once.
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -562,6 +548,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         float* tmax = reinterpret_cast<float*>(smem + C::OFF_MAX);
         uint32_t* posr = reinterpret_cast<uint32_t*>(smem + C::OFF_POS) + 8 * sg;
         float* sloper = reinterpret_cast<float*>(smem + C::OFF_SLOPE) + 8 * sg;
+        uint8_t* noder = smem + C::OFF_NODE + 8 * sg;
         const uint32_t tlane = tb + (static_cast<uint32_t>(wq) << 21);
         bool ok = true;
         uint32_t gt = 0;  // tiles so far
@@ -578,29 +565,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const int at = row_of(key) - 8 * sg;
                 ms[at] = -1e30f;
                 posr[at] = pos;
+                noder[at] = static_cast<uint8_t>(row / G - d[kRow0] / G);
                 if (SC) sloper[at] = P.rule.slopes ? __ldg(P.rule.slopes + d[kKvHead] * G + row % G) * kRuleLog2e : 0.f;
             }
             // Q rows, split with rounded high parts: [32-dim blocks][hi rows | lo rows][128 B].
             // (The last S has been read, so no MMA reads the last unit's Q.)
-            constexpr int F4 = HD / 4;  // float4s of a row
-            for (uint32_t i = tid; i < Rp * F4; i += 512) {
-                const uint32_t row = i / F4, c = i % F4;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row < rows) {
-                    const uint32_t at = d[kRow0] + row;
-                    x = *reinterpret_cast<const float4*>(
+            constexpr int F4 = HD / 4, QN = RB * F4 / 512;  // float4s of a row, of a thread
+            float4 qv[QN];
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const uint32_t row = (tid + 512 * k) / F4, at = d[kRow0] + row;
+                qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row < rows)
+                    qv[k] = *reinterpret_cast<const float4*>(
                         P.q_rot + (static_cast<size_t>(d[kRow] + at / G) * P.n_head + d[kKvHead] * G + at % G) * HD +
-                        4 * c);
-                }
+                        4 * (tid % F4));
+            }
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const uint32_t row = (tid + 512 * k) / F4, c = tid % F4;
+                if (row >= Rp) continue;
                 uint4 hi, lo;
                 auto split = [](float v, uint32_t& a, uint32_t& b) {
                     a = (__float_as_uint(v) + 0x1000u) & 0xFFFFE000u;
                     b = __float_as_uint(v - __uint_as_float(a));
                 };
-                split(x.x, hi.x, lo.x);
-                split(x.y, hi.y, lo.y);
-                split(x.z, hi.z, lo.z);
-                split(x.w, hi.w, lo.w);
+                split(qv[k].x, hi.x, lo.x);
+                split(qv[k].y, hi.y, lo.y);
+                split(qv[k].z, hi.z, lo.z);
+                split(qv[k].w, hi.w, lo.w);
                 uint8_t* dst = smem + (c / 8) * (2 * Rp * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
                 *reinterpret_cast<uint4*>(dst) = hi;
                 *reinterpret_cast<uint4*>(dst + Rp * 128) = lo;
@@ -653,20 +646,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     const uint32_t j = kp - past;
                     on = 0u;
                     if (j < d[kNodes]) {
-                        kp = past + P.depth[d[kRow] + j];
-                        // node after node, each with its rows of the block
-                        const uint32_t* anc = P.anc + static_cast<size_t>(d[kRow]) * kTreeWords + j / 32;
-                        const uint32_t row0 = d[kRow0], n1 = (row0 + rows - 1) / G;
-                        uint64_t all = 0;
-#pragma unroll 4
-                        for (uint32_t i = row0 / G; i <= n1; ++i) {
-                            const uint32_t a = i * G > row0 ? i * G - row0 : 0u;
-                            const uint32_t e = min((i + 1) * G - row0, rows);
-                            const uint64_t bits = ((e < 64 ? 1ull << e : 0ull) - 1ull) & ~((1ull << a) - 1ull);
-                            if (anc[static_cast<size_t>(i) * kTreeWords] >> (j % 32) & 1u) all |= bits;
+                        if (SC) kp = past + P.depth[d[kRow] + j];
+                        // the nodes that attend this one, from the block's first (at most 64 of them)
+                        const uint32_t n0 = d[kRow0] / G, w0 = n0 / 32;
+                        const uint32_t* below = P.below + static_cast<size_t>(d[kRow] + j) * kTreeWords;
+                        const uint32_t a = below[w0], b = w0 + 1 < kTreeWords ? below[w0 + 1] : 0u;
+                        const uint32_t c2 = w0 + 2 < kTreeWords ? below[w0 + 2] : 0u;
+                        const uint32_t lo = __funnelshift_r(a, b, n0 % 32), hi = __funnelshift_r(b, c2, n0 % 32);
+#pragma unroll
+                        for (int c = 0; c < CW; ++c) {
+                            const uint32_t i = noder[32 * (c / 8) + c % 8];
+                            on |= ((i < 32 ? lo : hi) >> (i % 32) & 1u) << c;
                         }
-                        on = static_cast<uint32_t>(all >> (8 * sg)) & 0xffu;
-                        if constexpr (CW > 8) on |= (static_cast<uint32_t>(all >> (32 + 8 * sg)) & 0xffu) << 8;
                     }
                 }
                 if constexpr (SC) {
@@ -1125,11 +1116,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == 31) {
         // ------------------------------------------------------------ units
         regs_decrease<kRegAux>();
+        // the CTA's range of all the tiles: their number, then the request that it begins in
+        auto tiles_of = [&](uint32_t r) {
+            return r < P.n_req ? tree_shape<RB>(P, r).tiles(P.n_kv_head) : 0ull;
+        };
+        uint64_t mine = 0;
+        const uint64_t first = tiles_of(lane);
+#pragma unroll 4
+        for (uint32_t r = lane + 32; r < P.n_req; r += 32) mine += tiles_of(r);
+        uint64_t total = mine + first;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const uint32_t ctas = tree_ctas(total, gridDim.x);
+        // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
+        const bool work = blockIdx.x < ctas && (sbase & 1023u) == 0;
+        if ((sbase & 1023u) && lane == 0) atomicOr(P.status, kDevTimeout);
         TreeWalk<RB> walk;
         walk.known = false;
-        walk.r = r_first;
-        walk.off = off_first;
-        walk.left = work ? u1 - u0 : 0u;
+        walk.r = 0;
+        walk.off = 0;
+        walk.left = 0;
+        const uint64_t u0 = work ? tree_first(total, ctas, blockIdx.x) : 0;
+        if (work) walk.left = tree_first(total, ctas, blockIdx.x + 1) - u0;
+        const bool tell = blockIdx.x == 0;  // the requests' first tiles, and the sum, for the combine kernel
+        uint64_t at = 0;
+        for (uint32_t r0 = 0; r0 < P.n_req; r0 += 32) {
+            const uint64_t n = r0 ? tiles_of(r0 + lane) : first;
+            uint64_t incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const uint64_t begin = at + incl - n;
+            if (tell && r0 + lane < P.n_req) P.base[r0 + lane] = begin;
+            const uint32_t here = __ballot_sync(0xffffffffu, work && begin <= u0 && u0 < begin + n);
+            if (here) {
+                const int from = __ffs(here) - 1;
+                walk.r = r0 + from;
+                walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
+                if (!tell) break;
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (tell && lane == 0) P.base[P.n_req] = total;
         for (uint32_t u = 0;; ++u) {
             uint32_t d[12];
             const bool more = walk.next(P, d);
@@ -1327,7 +1357,7 @@ int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMa
                             (p.n_kv_head + kTreeKvHeads - 1) / kTreeKvHeads;
     const uint64_t mean = (p.n_tok + p.n_req - 1) / p.n_req;
     const uint64_t parts = (mean * groups + kPrepWarps - 1) / kPrepWarps;
-    cfg.gridDim = dim3(p.n_req, static_cast<unsigned>(parts < 256 ? parts : 256));
+    cfg.gridDim = dim3(p.n_req, 1 + static_cast<unsigned>(parts < 256 ? parts : 256));
     cfg.blockDim = dim3(kPrepThreads);
     cfg.dynamicSmemBytes = tree_prep_smem<HD>();
     if ((e = cudaLaunchKernelEx(&cfg, slotkv_tree_prep_kernel<HD>, p)) != cudaSuccess) return static_cast<int>(e);

@@ -31,7 +31,8 @@ struct TreeParams {
     float* q_rot;            // workspace [n_tok][n_head][hd]: normed, rotated, scaled q
     uint32_t* req_of;        // workspace [n_tok]: the node's request, kTreeSkip: skipped
     uint32_t* depth;         // workspace [n_tok]
-    uint32_t* anc;           // workspace [n_tok][kTreeWords]: the node's ancestors and itself
+    uint32_t* below;         // workspace [n_tok][kTreeWords]: the nodes that attend it (words past the
+                             // request's nodes are not written)
     float* part;             // workspace: partial results, two of a unit's rows per CTA [rows][hd]
     float* part_ml;          // and their (m, l)
     uint64_t* base;          // workspace [n_req + 1]: the requests' first tiles
