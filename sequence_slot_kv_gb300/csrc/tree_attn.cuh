@@ -271,9 +271,14 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // the MMAs read tile t's last ones.  A unit's tiles go from its last keys to its first, so
 // that a distance bias raises no maximum tile after tile.
 //
-// The tiles of all units, in order, are cut into one equal range per CTA (every
-// CTA finds its own from the lengths), so a unit may lie in several CTAs; each
-// leaves (m, l, O) then, and slotkv_tree_combine_kernel joins them in CTA order.
+// A request's row blocks all read the same keys, so they are given out in sets of
+// 8, 4, 2 and 1 (the binary digits of their number): the CTAs of a group take
+// the blocks of a set side by side, tile for tile, and the keys come from memory
+// once for all of them.  The tiles of all sets of one size, in order, are cut into
+// one equal range per group, the CTAs divided among the sizes by their work
+// (tree_plan; every CTA finds its own range from the lengths).  So a unit may lie
+// in several CTAs; each leaves (m, l, O) then, and slotkv_tree_combine_kernel
+// joins them in the groups' order.
 //
 // Keys past the request's last are zeros in V; a masked key's P is -0.  A V value
 // that is not finite is a 0 to the tensor core, and the accumulators add it to
@@ -335,12 +340,21 @@ static_assert(4 * kTreeRegs + kRegAcc + 2 * kRegConv + kRegAux == kTreeWarps / 4
 // begins at place d[kPlace] - 128 t.
 enum TreeWord { kReq, kRow, kNodes, kPast, kKvHead, kRow0, kRows, kPlace, kTiles, kStart, kWhole, kMore };
 
+// The sets of 1 << k blocks of a request of nb, and the first block of the first.
+constexpr int kSetSizes = 4;
+__device__ __forceinline__ uint32_t tree_sets(uint32_t nb, int k) {
+    return k == kSetSizes - 1 ? nb >> k : nb >> k & 1u;
+}
+__device__ __forceinline__ uint32_t tree_set_block(uint32_t nb, int k) {
+    return k == kSetSizes - 1 ? 0u : nb & ~((2u << k) - 1u);
+}
 // A request's shape: row blocks, first tile, tiles; 0 blocks: nothing to do.
 struct TreeShape {
     TreeReq q;
     uint32_t nb, tile0, tl;
-    __device__ uint64_t tiles(uint32_t n_kv_head) const {
-        return static_cast<uint64_t>(nb) * tl * n_kv_head;
+    // tiles of its sets of 1 << k blocks
+    __device__ uint64_t tiles(uint32_t n_kv_head, int k) const {
+        return static_cast<uint64_t>(tree_sets(nb, k)) * tl * n_kv_head;
     }
 };
 template <int RB>
@@ -356,23 +370,71 @@ __device__ __forceinline__ TreeShape tree_shape(const TreeParams& P, uint32_t r)
     return x;
 }
 
-// The CTAs that share `total` tiles, and the first tile of CTA c.
-__device__ __forceinline__ uint32_t tree_ctas(uint64_t total, uint32_t grid) {
-    return total < grid ? static_cast<uint32_t>(total) : grid;
+// The tiles of the sets of each size (one row block's), the groups of CTAs that
+// share them, and the first CTA of the groups.
+struct TreePlan {
+    uint64_t total[kSetSizes];
+    uint32_t groups[kSetSizes], first[kSetSizes];
+};
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {  // (of 32 bits where they do)
+    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
-__device__ __forceinline__ uint64_t tree_first(uint64_t total, uint32_t ctas, uint32_t c) {
-    const uint64_t x = total * c;
-    return x >> 32 ? x / ctas : static_cast<uint32_t>(x) / ctas;  // (a division of 32 bits where they do)
+// As many groups as fit, so that the longest range is as short as may be.
+__device__ __forceinline__ void tree_plan(TreePlan& p, uint32_t ctas) {
+    uint64_t work = 0;
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) work += p.total[k] << k;
+    int left = static_cast<int>(ctas);
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) {
+        uint64_t g = p.total[k] ? divide(p.total[k] * ctas, work) : 0u;
+        g = g < p.total[k] ? g : p.total[k];
+        p.groups[k] = p.total[k] ? (g ? static_cast<uint32_t>(g) : 1u) : 0u;
+        left -= static_cast<int>(p.groups[k] << k);
+    }
+    for (;;) {
+        // the size with the longest ranges gets another group, or, where the groups of at
+        // least one are too many, the one with the shortest loses one
+        int best = -1;
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k) {
+            const bool can = left >= 0 ? (1 << k) <= left && p.groups[k] && p.groups[k] < p.total[k] : p.groups[k] > 1;
+            if (!can) continue;
+            if (best >= 0) {
+                uint64_t a = 0, b = 0;  // total[k] / groups[k] against the best one's
+#pragma unroll
+                for (int x = 0; x < kSetSizes; ++x)
+                    if (x == best) a = p.total[k] * p.groups[x], b = p.total[x] * p.groups[k];
+                if (left >= 0 ? a <= b : a >= b) continue;
+            }
+            best = k;
+        }
+        if (best < 0) break;
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k)
+            if (k == best) p.groups[k] += left >= 0 ? 1u : -1u;
+        left -= left >= 0 ? 1 << best : -(1 << best);
+    }
+    uint32_t at = 0;
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) {
+        p.first[k] = at;
+        at += p.groups[k] << k;
+    }
 }
-// The CTA of tile x.
-__device__ __forceinline__ uint32_t tree_owner(uint64_t total, uint32_t ctas, uint64_t x) {
-    const uint64_t y = (x + 1) * ctas - 1;
-    return (y | total) >> 32 ? static_cast<uint32_t>(y / total) : static_cast<uint32_t>(y) / static_cast<uint32_t>(total);
+// The first tile of group c of n, and the group of tile x.
+__device__ __forceinline__ uint64_t tree_first(uint64_t total, uint32_t n, uint32_t c) {
+    return divide(total * c, n);
+}
+__device__ __forceinline__ uint32_t tree_owner(uint64_t total, uint32_t n, uint64_t x) {
+    return static_cast<uint32_t>(divide((x + 1) * n - 1, total));
 }
 
 // A CTA's parts of units, in order.
 template <int RB>
 struct TreeWalk {
+    int k;               // the sets' size, 1 << k, and the block of a set that is this CTA's
+    uint32_t member;
     uint32_t r;
     uint64_t off, left;  // tiles into request r, tiles left
     TreeShape x;
@@ -385,20 +447,21 @@ struct TreeWalk {
                 x = tree_shape<RB>(P, r);
                 known = true;
             }
-            if (off < x.tiles(P.n_kv_head)) break;
-            off -= x.tiles(P.n_kv_head);
+            const uint64_t n = x.tiles(P.n_kv_head, k);
+            if (off < n) break;
+            off -= n;
             ++r;
             known = false;
         }
-        const uint32_t unit = static_cast<uint32_t>(off / x.tl);
+        const uint32_t unit = static_cast<uint32_t>(divide(off, x.tl)), sets = tree_sets(x.nb, k);
         const uint32_t t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
         const uint32_t n = left < x.tl - t0 ? static_cast<uint32_t>(left) : x.tl - t0;
-        const uint32_t row0 = unit % x.nb * RB, all = x.q.n * (P.n_head / P.n_kv_head) - row0;
+        const uint32_t row0 = (tree_set_block(x.nb, k) + (unit % sets << k) + member) * RB, all = x.q.n * (P.n_head / P.n_kv_head) - row0;
         d[kReq] = r;
         d[kRow] = x.q.s0;
         d[kNodes] = x.q.n;
         d[kPast] = x.q.past;
-        d[kKvHead] = unit / x.nb;
+        d[kKvHead] = unit / sets;
         d[kRow0] = row0;
         d[kRows] = all < RB ? all : RB;
         d[kPlace] = (x.tile0 + x.tl - 1 - t0) * 128;
@@ -559,15 +622,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (bar_or(bar_id, !ok || !d[kMore])) break;
             const uint32_t rows = d[kRows], Rp = (rows + 15) / 16 * 16;
             float* ms = reinterpret_cast<float*>(smem + C::OFF_M) + (u & 1) * RB + 8 * sg;
-            if (key < CW) {
-                const uint32_t row = d[kRow0] + min(static_cast<uint32_t>(row_of(key)), rows - 1);
-                const uint32_t pos = d[kPast] + P.depth[d[kRow] + row / G];
-                const int at = row_of(key) - 8 * sg;
-                ms[at] = -1e30f;
-                posr[at] = pos;
-                noder[at] = static_cast<uint8_t>(row / G - d[kRow0] / G);
-                if (SC) sloper[at] = P.rule.slopes ? __ldg(P.rule.slopes + d[kKvHead] * G + row % G) * kRuleLog2e : 0.f;
-            }
             // Q rows, split with rounded high parts: [32-dim blocks][hi rows | lo rows][128 B].
             // (The last S has been read, so no MMA reads the last unit's Q.)
             constexpr int F4 = HD / 4, QN = RB * F4 / 512;  // float4s of a row, of a thread
@@ -580,6 +634,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     qv[k] = *reinterpret_cast<const float4*>(
                         P.q_rot + (static_cast<size_t>(d[kRow] + at / G) * P.n_head + d[kKvHead] * G + at % G) * HD +
                         4 * (tid % F4));
+            }
+            if (key < CW) {
+                const uint32_t row = d[kRow0] + min(static_cast<uint32_t>(row_of(key)), rows - 1);
+                const uint32_t pos = d[kPast] + P.depth[d[kRow] + row / G];
+                const int at = row_of(key) - 8 * sg;
+                ms[at] = -1e30f;
+                posr[at] = pos;
+                noder[at] = static_cast<uint8_t>(row / G - d[kRow0] / G);
+                if (SC) sloper[at] = P.rule.slopes ? __ldg(P.rule.slopes + d[kKvHead] * G + row % G) * kRuleLog2e : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < QN; ++k) {
@@ -1116,50 +1179,81 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == 31) {
         // ------------------------------------------------------------ units
         regs_decrease<kRegAux>();
-        // the CTA's range of all the tiles: their number, then the request that it begins in
-        auto tiles_of = [&](uint32_t r) {
-            return r < P.n_req ? tree_shape<RB>(P, r).tiles(P.n_kv_head) : 0ull;
-        };
-        uint64_t mine = 0;
-        const uint64_t first = tiles_of(lane);
-#pragma unroll 4
-        for (uint32_t r = lane + 32; r < P.n_req; r += 32) mine += tiles_of(r);
-        uint64_t total = mine + first;
+        // what there is to do, by the size of the sets, and this CTA's part of it
+        TreePlan plan;
+        const TreeShape first = lane < P.n_req ? tree_shape<RB>(P, lane) : TreeShape{};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        const uint32_t ctas = tree_ctas(total, gridDim.x);
-        // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
-        const bool work = blockIdx.x < ctas && (sbase & 1023u) == 0;
-        if ((sbase & 1023u) && lane == 0) atomicOr(P.status, kDevTimeout);
+        for (int k = 0; k < kSetSizes; ++k) plan.total[k] = first.tiles(P.n_kv_head, k);
+#pragma unroll 2
+        for (uint32_t r = lane + 32; r < P.n_req; r += 32) {
+            const TreeShape x = tree_shape<RB>(P, r);
+#pragma unroll
+            for (int k = 0; k < kSetSizes; ++k) plan.total[k] += x.tiles(P.n_kv_head, k);
+        }
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k)
+            if (__any_sync(0xffffffffu, plan.total[k] != 0))
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) plan.total[k] += __shfl_xor_sync(0xffffffffu, plan.total[k], o);
+        tree_plan(plan, gridDim.x);
         TreeWalk<RB> walk;
         walk.known = false;
-        walk.r = 0;
-        walk.off = 0;
-        walk.left = 0;
-        const uint64_t u0 = work ? tree_first(total, ctas, blockIdx.x) : 0;
-        if (work) walk.left = tree_first(total, ctas, blockIdx.x + 1) - u0;
-        const bool tell = blockIdx.x == 0;  // the requests' first tiles, and the sum, for the combine kernel
-        uint64_t at = 0;
-        for (uint32_t r0 = 0; r0 < P.n_req; r0 += 32) {
-            const uint64_t n = r0 ? tiles_of(r0 + lane) : first;
-            uint64_t incl = n;
+        walk.k = 0;
+        walk.r = walk.member = 0;
+        walk.off = walk.left = 0;
+        uint64_t u0 = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const uint64_t begin = at + incl - n;
-            if (tell && r0 + lane < P.n_req) P.base[r0 + lane] = begin;
-            const uint32_t here = __ballot_sync(0xffffffffu, work && begin <= u0 && u0 < begin + n);
-            if (here) {
-                const int from = __ffs(here) - 1;
-                walk.r = r0 + from;
-                walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
-                if (!tell) break;
-            }
-            at += __shfl_sync(0xffffffffu, incl, 31);
+        for (int k = 0; k < kSetSizes; ++k) {
+            const uint32_t c = blockIdx.x - plan.first[k];
+            if (blockIdx.x < plan.first[k] || c >> k >= plan.groups[k]) continue;
+            walk.k = k;
+            walk.member = c & ((1u << k) - 1u);
+            u0 = tree_first(plan.total[k], plan.groups[k], c >> k);
+            walk.left = tree_first(plan.total[k], plan.groups[k], (c >> k) + 1) - u0;
         }
-        if (tell && lane == 0) P.base[P.n_req] = total;
+        // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
+        if (sbase & 1023u) {
+            walk.left = 0;
+            if (lane == 0) atomicOr(P.status, kDevTimeout);
+        }
+        // the request that the part begins in; CTA 0 writes all requests' first tiles, for the
+        // combine kernel
+        const bool tell = blockIdx.x == 0;
+        for (int k = 0; k < kSetSizes; ++k) {
+            if (!tell && k != walk.k) continue;
+            uint64_t at = 0;
+            for (uint32_t r0 = 0; r0 < P.n_req; r0 += 32) {
+                const TreeShape x = !r0 ? first : r0 + lane < P.n_req ? tree_shape<RB>(P, r0 + lane) : TreeShape{};
+                const uint64_t n = x.tiles(P.n_kv_head, k);
+                uint64_t incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                const uint64_t begin = at + incl - n;
+                if (tell && r0 + lane < P.n_req) P.base[static_cast<size_t>(k) * P.n_req + r0 + lane] = begin;
+                const uint32_t here =
+                    __ballot_sync(0xffffffffu, k == walk.k && walk.left && begin <= u0 && u0 < begin + n);
+                if (here) {
+                    const int from = __ffs(here) - 1;
+                    walk.r = r0 + from;
+                    walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
+                    if (!tell) break;
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        if (tell && lane < kSetSizes) {
+#pragma unroll
+            for (int k = 0; k < kSetSizes; ++k)
+                if (lane == k) {
+                    P.plan[4 * k] = static_cast<uint32_t>(plan.total[k]);
+                    P.plan[4 * k + 1] = static_cast<uint32_t>(plan.total[k] >> 32);
+                    P.plan[4 * k + 2] = plan.groups[k];
+                    P.plan[4 * k + 3] = plan.first[k];
+                }
+        }
         for (uint32_t u = 0;; ++u) {
             uint32_t d[12];
             const bool more = walk.next(P, d);
@@ -1283,7 +1377,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // several CTAs, in CTA order; the others are done already.
 constexpr int kJoinThreads = 256;
 template <int HD>
-__global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const TreeParams P, uint32_t grid) {
+__global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const TreeParams P) {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int RB = TreeCfg<HD>::RB, E = HD / 32;
@@ -1296,12 +1390,26 @@ __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const
     const TreeShape x = tree_shape<RB>(P, r);
     if (x.nb == 0 || tok < x.q.s0 || tok - x.q.s0 >= x.q.n) return;  // (left from an earlier call)
     const uint32_t G = P.n_head / P.n_kv_head, g = h / G;
-    const uint32_t row = (tok - x.q.s0) * G + h % G;
-    const uint64_t total = P.base[P.n_req], a = P.base[r] + (static_cast<uint64_t>(g) * x.nb + row / RB) * x.tl;
-    const uint32_t ctas = tree_ctas(total, grid);
-    const uint32_t c0 = tree_owner(total, ctas, a), c1 = tree_owner(total, ctas, a + x.tl - 1);
+    const uint32_t row = (tok - x.q.s0) * G + h % G, b = row / RB;
+    // the row block's set, and where its tiles are
+    int k = 0;
+#pragma unroll
+    for (int i = kSetSizes - 1; i > 0; --i)
+        if (b < (x.nb & ~((1u << i) - 1u))) {
+            k = i;
+            break;
+        }
+    const uint32_t in = b - tree_set_block(x.nb, k), sets = tree_sets(x.nb, k);
+    const uint4 plan = __ldcg(reinterpret_cast<const uint4*>(P.plan) + k);  // tiles, groups, first CTA
+    const uint64_t total = static_cast<uint64_t>(plan.y) << 32 | plan.x;
+    const uint64_t a = __ldcg(P.base + static_cast<size_t>(k) * P.n_req + r) +
+                       (static_cast<uint64_t>(g) * sets + (in >> k)) * x.tl;
+    const uint32_t c0 = tree_owner(total, plan.z, a), c1 = tree_owner(total, plan.z, a + x.tl - 1);
     if (c0 == c1) return;
-    auto slot = [&](uint32_t c) { return (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * RB + row % RB; };
+    auto slot = [&](uint32_t c) {
+        const uint32_t cta = plan.w + (c << k) + (in & ((1u << k) - 1u));
+        return (2 * static_cast<size_t>(cta) + (c == c0 ? 1 : 0)) * RB + row % RB;
+    };
     float m = -1e30f;
     for (uint32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(P.part_ml + 2 * slot(c)));
 #pragma unroll
@@ -1361,7 +1469,7 @@ int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMa
     cfg.blockDim = dim3(kPrepThreads);
     cfg.dynamicSmemBytes = tree_prep_smem<HD>();
     if ((e = cudaLaunchKernelEx(&cfg, slotkv_tree_prep_kernel<HD>, p)) != cudaSuccess) return static_cast<int>(e);
-    cfg.gridDim = dim3(sms);
+    cfg.gridDim = dim3(tree_grid(sms));
     cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     const bool rule = p.rule.cap_out != 0.f || p.rule.window || p.rule.slopes || p.rule.doc_start;
@@ -1372,7 +1480,7 @@ int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMa
     cfg.gridDim = dim3(static_cast<unsigned>((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return static_cast<int>(cudaLaunchKernelEx(&cfg, slotkv_tree_combine_kernel<HD>, p, sms));
+    return static_cast<int>(cudaLaunchKernelEx(&cfg, slotkv_tree_combine_kernel<HD>, p));
 }
 
 }  // namespace slotkv

@@ -35,7 +35,8 @@ struct TreeParams {
                              // request's nodes are not written)
     float* part;             // workspace: partial results, two of a unit's rows per CTA [rows][hd]
     float* part_ml;          // and their (m, l)
-    uint64_t* base;          // workspace [n_req + 1]: the requests' first tiles
+    uint64_t* base;          // workspace [4][n_req]: the requests' first tiles, by the size of the sets
+    uint32_t* plan;          // workspace [4][4]: of each size the tiles (64 bits), groups, first CTA
     uint32_t* status;        // sticky SLOTKV_DEV_* flags
     uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
     uint32_t box_keys;       // keys of one TMA box of K: a power of two, at most 128
@@ -50,10 +51,12 @@ constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
 __host__ __device__ constexpr uint32_t tree_rows(int hd) { return hd == 256 ? 32u : 64u; }
 __host__ __device__ constexpr uint32_t tree_v_dims(int hd) { return hd < 128 ? hd : 128u; }
 __host__ __device__ constexpr uint32_t tree_v_keys(int hd) { return 4096u / tree_v_dims(hd); }
-// Head rows of partial results that a call can leave on `sms` CTAs.
-inline size_t tree_partial_rows(int hd, uint32_t sms) { return (size_t)2 * sms * tree_rows(hd); }
+// CTAs of the attention kernel: one per SM, and enough for a group of each size.
+inline uint32_t tree_grid(uint32_t sms) { return sms < 15u ? 15u : sms; }
+// Head rows of partial results that a call can leave.
+inline size_t tree_partial_rows(int hd, uint32_t sms) { return (size_t)2 * tree_grid(sms) * tree_rows(hd); }
 
-// Enqueue the kernels of a call (prep, attention on `sms` CTAs, combine); tmK:
+// Enqueue the kernels of a call (prep, attention, combine); tmK:
 // the 128-byte-swizzled view of K with boxes of 32 floats x box_keys rows, tmV:
 // V's with boxes of tree_v_dims(hd) floats x min(box_keys, tree_v_keys(hd))
 // rows, not swizzled.  Return a cudaError_t value.
