@@ -293,52 +293,138 @@ __device__ __forceinline__ FreeEntry free_entry(const FreeTablesParams& P, uint3
 // the tables there, as the most negative numbers, and the first one stays
 // (atomic minimum); (3) the entry that finds its own place is the one that
 // gives the block back; a prefix sum over them gives their places in the list.
-__global__ void __launch_bounds__(kListThreads) slotkv_free_tables_kernel(const FreeTablesParams P) {
-    __shared__ ListScan scan;
-    begin_dependent();
-    const int lane = threadIdx.x & 31;
-    const EntryItems it = my_items(P.R, P.bt_stride);
-    const uint32_t head0 = __ldcg(P.head), head = head0 < P.n_free ? head0 : P.n_free;
-    int* shares = reinterpret_cast<int*>(P.shares);
-    if (shares) {
-        for (uint32_t i = it.begin; i < it.end; ++i) {
-            const FreeEntry x = free_entry(P, i, it.per_row, false);
-            if (x.live) atomicSub(shares + x.id, 1);
-        }
-        cluster_barrier();
-        for (uint32_t i = it.begin; i < it.end; ++i) {
-            const FreeEntry x = free_entry(P, i, it.per_row, false);
-            if (x.live && __ldcg(shares + x.id) < 0) {
-                const int old = atomicMin(shares + x.id, static_cast<int>(x.code));
-                if (old < -1 && old >= -(1 << 30)) atomicOr(P.pool.status, kRange);  // given up twice
-            }
-        }
-        cluster_barrier();
-    }
-    auto gone = [&](const FreeEntry& x) {
-        return x.live && (!shares || __ldcg(shares + x.id) == static_cast<int>(x.code));
-    };
-    uint32_t mine = 0;
-    for (uint32_t i = it.begin; i < it.end; ++i)
-        mine += __popc(__ballot_sync(0xffffffffu, gone(free_entry(P, i, it.per_row, true))));
-    uint32_t total;
-    uint32_t at = cluster_exclusive(mine, scan, total);
-    // the list is a stack below head: total ids end where the taken ones began
+__device__ __forceinline__ void free_take(const FreeTablesParams& P, const EntryItems& it) {
+#pragma unroll 4
     for (uint32_t i = it.begin; i < it.end; ++i) {
         const FreeEntry x = free_entry(P, i, it.per_row, false);
-        const bool go = gone(x);
-        const uint32_t m = __ballot_sync(0xffffffffu, go);
-        const uint32_t k = at + __popc(m & ((1u << lane) - 1u));
+        if (x.live) atomicSub(P.shares + x.id, 1u);
+    }
+}
+__device__ __forceinline__ void free_sign(const FreeTablesParams& P, const EntryItems& it) {
+    int* shares = reinterpret_cast<int*>(P.shares);
+#pragma unroll 4
+    for (uint32_t i = it.begin; i < it.end; ++i) {
+        const FreeEntry x = free_entry(P, i, it.per_row, false);
+        if (x.live && __ldcg(shares + x.id) < 0) {
+            const int old = atomicMin(shares + x.id, static_cast<int>(x.code));
+            if (old < -1 && old >= -(1 << 30)) atomicOr(P.pool.status, kRange);  // given up twice
+        }
+    }
+}
+__device__ __forceinline__ bool free_goes(const FreeTablesParams& P, const FreeEntry& x) {
+    return x.live && (!P.shares || __ldcg(P.shares + x.id) == x.code);
+}
+__device__ __forceinline__ uint32_t free_count(const FreeTablesParams& P, const EntryItems& it) {
+    uint32_t n = 0;
+#pragma unroll 4
+    for (uint32_t i = it.begin; i < it.end; ++i)
+        n += __popc(__ballot_sync(0xffffffffu, free_goes(P, free_entry(P, i, it.per_row, true))));
+    return n;
+}
+// The list is a stack below head: total ids end where the taken ones began.
+__device__ __forceinline__ void free_give(const FreeTablesParams& P, const EntryItems& it, uint32_t head,
+                                          uint32_t at, uint32_t total) {
+    const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+#pragma unroll 2
+    for (uint32_t i = it.begin; i < it.end; ++i) {
+        const FreeEntry x = free_entry(P, i, it.per_row, false);
+        const bool go = free_goes(P, x);
+        const uint32_t m = __ballot_sync(0xffffffffu, go), k = at + __popc(m & below);
         if (go) {
             if (head + k >= total) P.free_blocks[head + k - total] = x.id;
-            if (shares) shares[x.id] = 0;
+            if (P.shares) P.shares[x.id] = 0;
         }
         at += __popc(m);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *P.head_out = head > total ? head - total : 0u;
-        if (head != head0 || total > head) atomicOr(P.pool.status, kRange);
+}
+__device__ __forceinline__ void free_head(const FreeTablesParams& P, uint32_t head0, uint32_t head,
+                                          uint32_t total) {
+    *P.head_out = head > total ? head - total : 0u;
+    if (head != head0 || total > head) atomicOr(P.pool.status, kRange);
+}
+
+// One CTA, or one cluster of them: the steps one after the other.
+__global__ void __launch_bounds__(kListThreads) slotkv_free_tables_kernel(const FreeTablesParams P) {
+    __shared__ ListScan scan;
+    begin_dependent();
+    const EntryItems it = my_items(P.R, P.bt_stride);
+    const uint32_t head0 = __ldcg(P.head), head = head0 < P.n_free ? head0 : P.n_free;
+    if (P.shares) {
+        free_take(P, it);
+        cluster_barrier();
+        free_sign(P, it);
+        cluster_barrier();
     }
+    uint32_t total;
+    const uint32_t at = cluster_exclusive(free_count(P, it), scan, total);
+    free_give(P, it, head, at, total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) free_head(P, head0, head, total);
+}
+
+// Many entries: the steps are kernels over the whole GPU, each a programmatic
+// dependent of the one before.  A CTA counts the blocks that its entries give
+// back, the last step sums what the CTAs before it counted.
+constexpr int kFreeThreads = 256, kFreeWarps = kFreeThreads / 32;
+__device__ __forceinline__ EntryItems grid_items(const FreeTablesParams& P) {
+    EntryItems it;
+    it.per_row = (P.bt_stride + 31) / 32;
+    const uint64_t n = static_cast<uint64_t>(P.R) * it.per_row;
+    const uint64_t warps = static_cast<uint64_t>(gridDim.x) * kFreeWarps, per = (n + warps - 1) / warps;
+    const uint64_t b = (static_cast<uint64_t>(blockIdx.x) * kFreeWarps + (threadIdx.x >> 5)) * per;
+    it.begin = static_cast<uint32_t>(b < n ? b : n);
+    it.end = static_cast<uint32_t>(b + per < n ? b + per : n);
+    return it;
+}
+__global__ void __launch_bounds__(kFreeThreads) slotkv_free_take_kernel(const FreeTablesParams P) {
+    begin_dependent();
+    free_take(P, grid_items(P));
+}
+__global__ void __launch_bounds__(kFreeThreads) slotkv_free_sign_kernel(const FreeTablesParams P) {
+    begin_dependent();
+    free_sign(P, grid_items(P));
+}
+__global__ void __launch_bounds__(kFreeThreads) slotkv_free_count_kernel(const FreeTablesParams P) {
+    __shared__ uint32_t sums[kFreeWarps];
+    begin_dependent();
+    const uint32_t n = free_count(P, grid_items(P));
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t all = 0;
+        for (int w = 0; w < kFreeWarps; ++w) all += sums[w];
+        P.counts[blockIdx.x] = all;
+        // (head_out may be head: the next step reads it here)
+        if (blockIdx.x == 0) P.counts[kFreeCtas] = __ldcg(P.head);
+    }
+}
+__global__ void __launch_bounds__(kFreeThreads) slotkv_free_give_kernel(const FreeTablesParams P) {
+    __shared__ uint32_t sums[kFreeWarps], before_sum[kFreeWarps], all_sum[kFreeWarps];
+    begin_dependent();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const EntryItems it = grid_items(P);
+    const uint32_t head0 = __ldcg(P.counts + kFreeCtas), head = head0 < P.n_free ? head0 : P.n_free;
+    const uint32_t mine = free_count(P, it);
+    uint32_t before = 0, all = 0;
+    for (uint32_t c = threadIdx.x; c < gridDim.x; c += kFreeThreads) {
+        const uint32_t x = __ldcg(P.counts + c);
+        all += x;
+        before += c < blockIdx.x ? x : 0u;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) {
+        sums[warp] = mine;
+        before_sum[warp] = before;
+        all_sum[warp] = all;
+    }
+    __syncthreads();
+    uint32_t at = 0, total = 0;
+    for (int w = 0; w < kFreeWarps; ++w) {
+        at += before_sum[w] + (w < warp ? sums[w] : 0u);
+        total += all_sum[w];
+    }
+    free_give(P, it, head, at, total);
+    if (blockIdx.x == 0 && threadIdx.x == 0) free_head(P, head0, head, total);
 }
 
 // ------------------------------------------------------------------ compact
@@ -422,6 +508,7 @@ __global__ void __launch_bounds__(kListThreads) slotkv_compact_plan_kernel(const
                 S.movers[before - below] = id;
             }
             S.map[id] = to;
+            if (P.shares && id >= L && !live) P.shares[id] = 0;  // (the moves clear the others')
         }
         at += __popc(m);
     }
@@ -451,7 +538,10 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_compact_move_kernel(const
                     reinterpret_cast<float4*>(P.pool.K) + static_cast<size_t>(dst) * n4, n4, t, step);
         copy_float4(reinterpret_cast<const float4*>(P.pool.V) + static_cast<size_t>(src) * n4,
                     reinterpret_cast<float4*>(P.pool.V) + static_cast<size_t>(dst) * n4, n4, t, step);
-        if (P.shares && part == 0 && threadIdx.x == 0) P.shares[dst] = P.shares[src];
+        if (P.shares && part == 0 && threadIdx.x == 0) {
+            P.shares[dst] = P.shares[src];
+            P.shares[src] = 0;
+        }
     }
     const uint64_t gt = static_cast<uint64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
     const uint64_t nt = static_cast<uint64_t>(gridDim.x) * kCopyThreads;
@@ -463,14 +553,6 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_compact_move_kernel(const
         const uint32_t id = P.block_tables[i];
         if (id >= L && id < P.pool.n_blocks) P.block_tables[i] = __ldcg(S.map + id);
     }
-}
-
-// Share counts of the ids that are free now: after the moves have read them.
-__global__ void __launch_bounds__(kCopyThreads) slotkv_compact_shares_kernel(const CompactPoolParams P) {
-    begin_dependent();
-    const uint32_t L = __ldcg(compact_scratch(P.scratch, P.pool.n_blocks).counts);
-    const uint64_t i = static_cast<uint64_t>(L) + blockIdx.x * kCopyThreads + threadIdx.x;
-    if (i < P.pool.n_blocks) P.shares[i] = 0;
 }
 
 template <typename... A>
@@ -493,6 +575,8 @@ int launch_dependent(void (*kernel)(A...), dim3 grid, int threads, uint32_t clus
 
 // CTAs of a list kernel over n items of 32: one where its warps have one each.
 uint32_t list_ctas(uint64_t n) { return n <= kListWarps ? 1u : kListCtas; }
+// Items up to which freeing is one cluster's work (two for each of its warps).
+constexpr uint64_t kListItems = 2 * kListWarps * kListCtas;
 
 }  // namespace
 
@@ -514,9 +598,22 @@ int launch_fork_tables(const ForkTablesParams& p, uint32_t sms, cudaStream_t str
                             0, stream, p);
 }
 
-int launch_free_tables(const FreeTablesParams& p, cudaStream_t stream) {
-    const uint32_t ctas = list_ctas(static_cast<uint64_t>(p.R) * ((p.bt_stride + 31) / 32));
-    return launch_dependent(slotkv_free_tables_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+int launch_free_tables(const FreeTablesParams& p, uint32_t sms, cudaStream_t stream) {
+    const uint64_t items = static_cast<uint64_t>(p.R) * ((p.bt_stride + 31) / 32);
+    if (items <= kListItems) {
+        const uint32_t ctas = list_ctas(items);
+        return launch_dependent(slotkv_free_tables_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+    }
+    const uint64_t want = (items + kFreeWarps - 1) / kFreeWarps, most = sms < kFreeCtas / 4 ? 4 * sms : kFreeCtas;
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+    int rc = 0;
+    if (p.shares) {
+        rc = launch_dependent(slotkv_free_take_kernel, grid, kFreeThreads, 0, stream, p);
+        if (rc == 0) rc = launch_dependent(slotkv_free_sign_kernel, grid, kFreeThreads, 0, stream, p);
+    }
+    if (rc == 0) rc = launch_dependent(slotkv_free_count_kernel, grid, kFreeThreads, 0, stream, p);
+    if (rc == 0) rc = launch_dependent(slotkv_free_give_kernel, grid, kFreeThreads, 0, stream, p);
+    return rc;
 }
 
 int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t stream) {
@@ -528,10 +625,7 @@ int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t s
     const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
                           (kBatch * kCopyThreads);
     const uint32_t parts = most < 8u ? most : 8u;
-    rc = launch_dependent(slotkv_compact_move_kernel, dim3(4 * sms), kCopyThreads, 0, stream, p, parts);
-    if (rc != 0 || !p.shares) return rc;
-    const uint32_t grid = (p.pool.n_blocks + kCopyThreads - 1) / kCopyThreads;
-    return launch_dependent(slotkv_compact_shares_kernel, dim3(grid), kCopyThreads, 0, stream, p);
+    return launch_dependent(slotkv_compact_move_kernel, dim3(4 * sms), kCopyThreads, 0, stream, p, parts);
 }
 
 }  // namespace slotkv

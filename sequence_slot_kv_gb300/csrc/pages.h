@@ -49,8 +49,10 @@ struct FreeTablesParams {
     uint32_t* free_blocks;         // [n_free]
     const uint32_t* head;          // [1]
     uint32_t* head_out;            // [1], may be head
+    uint32_t* counts;              // handle-owned: [kFreeCtas + 1]
     uint32_t R, bt_stride, n_free;
 };
+constexpr uint32_t kFreeCtas = 1024;  // at most, of the kernels that free many entries
 
 struct CompactPoolParams {
     PoolView pool;
@@ -72,7 +74,7 @@ constexpr uint32_t kMaxTree = 256;
 // Enqueue the kernels of a call; return a cudaError_t value.
 int launch_keep_path(const KeepPathParams& p, cudaStream_t stream);
 int launch_fork_tables(const ForkTablesParams& p, uint32_t sms, cudaStream_t stream);
-int launch_free_tables(const FreeTablesParams& p, cudaStream_t stream);
+int launch_free_tables(const FreeTablesParams& p, uint32_t sms, cudaStream_t stream);
 int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t stream);
 
 }  // namespace slotkv

@@ -110,7 +110,7 @@ struct slotkv_s {
     float* sc_q = nullptr;            // [max_rows][max_n_head][hd] rotated q
     uint32_t* sc_idx = nullptr;       // rec, tiles, tile_of, tile_lo, list, plan
     float* sc_part[2] = {};           // acc then (m, l), each of partial_rows() head rows
-    uint32_t* map_scratch = nullptr;  // table calls: CTA counter, new head
+    uint32_t* map_scratch = nullptr;  // table calls: CTA counter, new head, counts
     // tree calls: views of the buffers for slots [0] and pages [1], keys of a
     // box of K in each (0: no pages); per-node words (request, depth,
     // ancestors) and the requests' first tiles, and partial results, allocated by
@@ -863,7 +863,7 @@ int slot_kv_alloc(slotkv_t* handle, uint32_t n_slots, uint32_t slot_ctx, uint32_
             rc = cuda_fail(e, "status word");
     }
     if (rc == SLOTKV_OK) {
-        if ((e = cudaMalloc(&h->map_scratch, 2 * sizeof(uint32_t))) != cudaSuccess ||
+        if ((e = cudaMalloc(&h->map_scratch, (3 + slotkv::kFreeCtas) * sizeof(uint32_t))) != cudaSuccess ||
             (e = cudaMemset(h->map_scratch, 0, 2 * sizeof(uint32_t))) != cudaSuccess)
             rc = cuda_fail(e, "table scratch");
     }
@@ -1645,9 +1645,9 @@ int slot_kv_free_tables(slotkv_t h, uint32_t n_req, const uint32_t* past, const 
     if (rc != SLOTKV_OK) return rc;
     if ((uint64_t)n_req * bt_stride > (1ull << 30))
         return fail(SLOTKV_ERR_ARG, "n_req * bt_stride exceeds 2^30");
-    const slotkv::FreeTablesParams P{pool_view(h), past,   keep,  block_tables, shares, free_blocks,
-                                     head,         head_out, n_req, bt_stride,  n_free};
-    const int e = slotkv::launch_free_tables(P, (cudaStream_t)stream);
+    const slotkv::FreeTablesParams P{pool_view(h), past,     keep,  block_tables, shares, free_blocks,
+                                     head, head_out, h->map_scratch + 2, n_req, bt_stride, n_free};
+    const int e = slotkv::launch_free_tables(P, sm_total(h), (cudaStream_t)stream);
     if (e != 0) return cuda_fail((cudaError_t)e, "free tables kernel launch");
     return SLOTKV_OK;
 }

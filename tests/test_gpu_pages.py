@@ -298,7 +298,7 @@ def held_pool(r, R, bs, stride, shared):
 
 
 @pytest.mark.parametrize("R,stride", [(0, 1), (1, 1), (1, 200), (5, 33), (31, 32), (33, 31), (130, 65),
-                                      (700, 40)])
+                                      (700, 40), (256, 33), (513, 32), (3000, 20), (40, 900)])
 @pytest.mark.parametrize("shared", [None, False, True])
 @pytest.mark.parametrize("same", [False, True])
 def test_free_tables(R, stride, shared, same):
