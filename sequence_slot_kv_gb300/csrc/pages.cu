@@ -314,27 +314,47 @@ __device__ __forceinline__ void free_sign(const FreeTablesParams& P, const Entry
 __device__ __forceinline__ bool free_goes(const FreeTablesParams& P, const FreeEntry& x) {
     return x.live && (!P.shares || __ldcg(P.shares + x.id) == x.code);
 }
-__device__ __forceinline__ uint32_t free_count(const FreeTablesParams& P, const EntryItems& it) {
+// A lane's entries that give a block back, of a warp's first items (most warps have
+// no more): whether, and which.
+constexpr uint32_t kKeptItems = 4;
+struct FreeKept {
+    uint32_t id[kKeptItems];
+    bool go[kKeptItems];
+};
+__device__ __forceinline__ uint32_t free_count(const FreeTablesParams& P, const EntryItems& it, FreeKept& kept) {
     uint32_t n = 0;
+    FreeEntry x[kKeptItems];
+#pragma unroll
+    for (uint32_t k = 0; k < kKeptItems; ++k)  // (the loads of all first)
+        x[k] = it.begin + k < it.end ? free_entry(P, it.begin + k, it.per_row, true) : FreeEntry{0u, 0u, false};
+#pragma unroll
+    for (uint32_t k = 0; k < kKeptItems; ++k) {
+        kept.id[k] = x[k].id;
+        kept.go[k] = free_goes(P, x[k]);
+        n += __popc(__ballot_sync(0xffffffffu, kept.go[k]));
+    }
 #pragma unroll 4
-    for (uint32_t i = it.begin; i < it.end; ++i)
+    for (uint32_t i = it.begin + kKeptItems; i < it.end; ++i)
         n += __popc(__ballot_sync(0xffffffffu, free_goes(P, free_entry(P, i, it.per_row, true))));
     return n;
 }
 // The list is a stack below head: total ids end where the taken ones began.
-__device__ __forceinline__ void free_give(const FreeTablesParams& P, const EntryItems& it, uint32_t head,
-                                          uint32_t at, uint32_t total) {
+__device__ __forceinline__ void free_give(const FreeTablesParams& P, const EntryItems& it, const FreeKept& kept,
+                                          uint32_t head, uint32_t at, uint32_t total) {
     const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
-#pragma unroll 2
-    for (uint32_t i = it.begin; i < it.end; ++i) {
-        const FreeEntry x = free_entry(P, i, it.per_row, false);
-        const bool go = free_goes(P, x);
+    auto give = [&](uint32_t id, bool go) {
         const uint32_t m = __ballot_sync(0xffffffffu, go), k = at + __popc(m & below);
         if (go) {
-            if (head + k >= total) P.free_blocks[head + k - total] = x.id;
-            if (P.shares) P.shares[x.id] = 0;
+            if (head + k >= total) P.free_blocks[head + k - total] = id;
+            if (P.shares) P.shares[id] = 0;
         }
         at += __popc(m);
+    };
+#pragma unroll
+    for (uint32_t k = 0; k < kKeptItems; ++k) give(kept.id[k], kept.go[k]);
+    for (uint32_t i = it.begin + kKeptItems; i < it.end; ++i) {
+        const FreeEntry x = free_entry(P, i, it.per_row, false);
+        give(x.id, free_goes(P, x));
     }
 }
 __device__ __forceinline__ void free_head(const FreeTablesParams& P, uint32_t head0, uint32_t head,
@@ -355,9 +375,10 @@ __global__ void __launch_bounds__(kListThreads) slotkv_free_tables_kernel(const 
         free_sign(P, it);
         cluster_barrier();
     }
+    FreeKept kept;
     uint32_t total;
-    const uint32_t at = cluster_exclusive(free_count(P, it), scan, total);
-    free_give(P, it, head, at, total);
+    const uint32_t at = cluster_exclusive(free_count(P, it, kept), scan, total);
+    free_give(P, it, kept, head, at, total);
     if (blockIdx.x == 0 && threadIdx.x == 0) free_head(P, head0, head, total);
 }
 
@@ -386,7 +407,8 @@ __global__ void __launch_bounds__(kFreeThreads) slotkv_free_sign_kernel(const Fr
 __global__ void __launch_bounds__(kFreeThreads) slotkv_free_count_kernel(const FreeTablesParams P) {
     __shared__ uint32_t sums[kFreeWarps];
     begin_dependent();
-    const uint32_t n = free_count(P, grid_items(P));
+    FreeKept kept;
+    const uint32_t n = free_count(P, grid_items(P), kept);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = n;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -403,7 +425,8 @@ __global__ void __launch_bounds__(kFreeThreads) slotkv_free_give_kernel(const Fr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const EntryItems it = grid_items(P);
     const uint32_t head0 = __ldcg(P.counts + kFreeCtas), head = head0 < P.n_free ? head0 : P.n_free;
-    const uint32_t mine = free_count(P, it);
+    FreeKept kept;
+    const uint32_t mine = free_count(P, it, kept);
     uint32_t before = 0, all = 0;
     for (uint32_t c = threadIdx.x; c < gridDim.x; c += kFreeThreads) {
         const uint32_t x = __ldcg(P.counts + c);
@@ -423,7 +446,7 @@ __global__ void __launch_bounds__(kFreeThreads) slotkv_free_give_kernel(const Fr
         at += before_sum[w] + (w < warp ? sums[w] : 0u);
         total += all_sum[w];
     }
-    free_give(P, it, head, at, total);
+    free_give(P, it, kept, head, at, total);
     if (blockIdx.x == 0 && threadIdx.x == 0) free_head(P, head0, head, total);
 }
 
@@ -516,6 +539,70 @@ __global__ void __launch_bounds__(kListThreads) slotkv_compact_plan_kernel(const
     const uint32_t left = n - L, F = left < P.n_free ? left : P.n_free;
     for (uint32_t i = gt; i < F; i += nt) P.free_blocks[P.n_free - F + i] = L + i;
     if (gt == 0) {
+        *P.head = P.n_free - F;
+        if (F < left) atomicOr(P.pool.status, kRange);
+    }
+}
+
+// The same for a pool of up to 32 blocks per thread of one CTA: the blocks in use
+// as bits in shared memory, a word per thread (the phases above are round trips
+// to L2, these barriers).
+constexpr uint32_t kSmallPool = 32 * kListThreads, kSmallEntries = 64 * kListThreads;
+__global__ void __launch_bounds__(kListThreads) slotkv_compact_small_kernel(const CompactPoolParams P) {
+    __shared__ uint32_t bits[kListThreads], warp_sum[kListWarps], moves_sum;
+    begin_dependent();
+    const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5, n = P.pool.n_blocks;
+    const CompactScratch S = compact_scratch(P.scratch, n);
+    bits[t] = 0;
+    if (t == 0) moves_sum = 0;
+    __syncthreads();
+    for (uint32_t i = t; i < P.R * P.bt_stride; i += kListThreads) {
+        const uint32_t r = i / P.bt_stride;
+        bool ok;
+        if (i - r * P.bt_stride >= used_entries(P, r, ok)) continue;
+        const uint32_t id = __ldg(P.block_tables + i);
+        if (id < n) atomicOr(&bits[id / 32], 1u << (id % 32));
+        if (!ok || id >= n) atomicOr(P.pool.status, kRange);
+    }
+    __syncthreads();
+    const uint32_t live = bits[t], mine = __popc(live);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= static_cast<uint32_t>(o)) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    const uint32_t w = warp_sum[lane];  // (kListWarps = 32)
+    const uint32_t first = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + incl - mine;
+    const uint32_t L = __reduce_add_sync(0xffffffffu, w);  // blocks in use
+    // this word's ids below L, from L on, and below n
+    auto under = [&](uint32_t end) {
+        return end <= 32 * t ? 0u : end - 32 * t >= 32 ? 0xffffffffu : (1u << (end - 32 * t)) - 1u;
+    };
+    const uint32_t low = under(L), all = under(n), holes = ~live & low, movers = live & ~low;
+    // a hole's place is the number of holes before it, a mover's that of the movers: of the
+    // ids below its word, 32 t - first are free and first in use
+    for (uint32_t m = holes; m; m &= m - 1) {
+        const uint32_t b = __ffs(m) - 1;
+        S.holes[32 * t - first + __popc(~live & ((1u << b) - 1u))] = 32 * t + b;
+    }
+    if (movers) atomicAdd(&moves_sum, __popc(movers));
+    __syncthreads();  // (the holes too)
+    const uint32_t moves = moves_sum, below = L - moves;
+    for (uint32_t m = movers; m; m &= m - 1) {
+        const uint32_t b = __ffs(m) - 1, k = first + __popc(live & ((1u << b) - 1u)) - below, id = 32 * t + b;
+        S.movers[k] = id;
+        S.map[id] = __ldcg(S.holes + k);
+    }
+    if (P.shares)
+        for (uint32_t m = ~live & ~low & all; m; m &= m - 1) P.shares[32 * t + __ffs(m) - 1] = 0;
+    const uint32_t left = n - L, F = left < P.n_free ? left : P.n_free;
+    for (uint32_t i = t; i < F; i += kListThreads) P.free_blocks[P.n_free - F + i] = L + i;
+    if (t == 0) {
+        S.counts[0] = L;
+        S.counts[1] = moves;
         *P.head = P.n_free - F;
         if (F < left) atomicOr(P.pool.status, kRange);
     }
@@ -619,8 +706,13 @@ int launch_free_tables(const FreeTablesParams& p, uint32_t sms, cudaStream_t str
 int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t stream) {
     const uint64_t items = static_cast<uint64_t>(p.R) * ((p.bt_stride + 31) / 32);
     const uint64_t groups = (static_cast<uint64_t>(p.pool.n_blocks) + 31) / 32;
-    const uint32_t ctas = list_ctas(items > groups ? items : groups);
-    int rc = launch_dependent(slotkv_compact_plan_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+    int rc;
+    if (p.pool.n_blocks <= kSmallPool && static_cast<uint64_t>(p.R) * p.bt_stride <= kSmallEntries) {
+        rc = launch_dependent(slotkv_compact_small_kernel, dim3(1), kListThreads, 0, stream, p);
+    } else {
+        const uint32_t ctas = list_ctas(items > groups ? items : groups);
+        rc = launch_dependent(slotkv_compact_plan_kernel, dim3(ctas), kListThreads, ctas, stream, p);
+    }
     if (rc != 0) return rc;
     const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
                           (kBatch * kCopyThreads);

@@ -378,7 +378,7 @@ def compact_case(past, tables, shares, free, bs, n, stride, n_kv=1, hd=64):
 
 
 @pytest.mark.parametrize("R,stride,bs", [(0, 1, 4), (1, 1, 1), (1, 70, 8), (3, 11, 33), (33, 32, 2),
-                                         (200, 40, 4)])
+                                         (200, 40, 4), (820, 40, 1), (700, 95, 1)])
 @pytest.mark.parametrize("shared", [None, False, True])
 def test_compact_pool(R, stride, bs, shared):
     r = random.Random(R + stride)
