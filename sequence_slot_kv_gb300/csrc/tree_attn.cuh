@@ -318,13 +318,12 @@ struct TreeCfg {
     static constexpr int OFF_MAX = OFF_NODE + RB;          // a warp's maxima, its sums [4][RB]
     static constexpr int OFF_DESC = OFF_MAX + 4 * RB * 4;       // what the roles need to know of a unit [2]
     static constexpr int OFF_BAR = OFF_DESC + 2 * 12 * 4;
-    // K landed, V landed, K empty, V empty [NSLOT]; K lo full, empty [NKL]; V full, empty [NV];
-    // S full, empty; P full, empty [4]; tile done with; O full, empty; Q full; unit's end; drain [2];
-    // unit known, done with [2].
-    // (A slot takes K and V in turn; barriers of their own let each kind's readers see every phase.)
-    static constexpr int NBAR = 4 * NSLOT + 2 * NK + 2 * NV + 21;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + 56;
+    // piece landed, slot empty [NSLOT]; K converted, its buffer empty [NK]; V^T converted, its buffer
+    // empty [NV]; S full, empty; P full, empty [4]; tile done with; O full, empty; Q full; unit's end;
+    // drain [2]; unit known, done with [2]
+    static constexpr int NBAR = 2 * NSLOT + 2 * NK + 2 * NV + 21;
+    static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
+    static constexpr int SMEM = OFF_MISC + 64;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int CW = RB / 4;                   // rows of a softmax warpgroup
     static_assert(OFF_BAR % 8 == 0 && NSLOT >= 6, "layout");
@@ -493,6 +492,11 @@ __device__ __forceinline__ float tree_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 // A word of shared memory at addr + at.
 __device__ __forceinline__ void sts(uint32_t addr, int at, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr + at), "f"(v) : "memory");
@@ -520,20 +524,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t sbase = smem_addr(smem);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
-    // misc: [0] abort, [1] tensor memory; tiles (plus 1): [2 + 4 (tile & 1) + block] the last with a
-    // V value that is not finite in that block of 32 keys, [10 + softmax warpgroup] the last
+    // misc: [0] abort, [1] tensor memory; tiles (plus 1): [4 + 4 (tile & 1) + block] the last with a
+    // V value that is not finite in that block of 32 keys, [12 + softmax warpgroup] the last
     // with a raise
     const uint32_t bar0 = sbase + C::OFF_BAR;
-    const uint32_t KF = bar0, VL = KF + 8 * NSLOT, KE = VL + 8 * NSLOT, VE = KE + 8 * NSLOT, KLF = VE + 8 * NSLOT,
-                   KLE = KLF + 8 * C::NK, VF = KLE + 8 * C::NK, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
+    const uint32_t RF = bar0, RE = RF + 8 * NSLOT, KLF = RE + 8 * NSLOT, KLE = KLF + 8 * C::NK, VF = KLE + 8 * C::NK, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
                    SE = SF + 8, PF = SE + 8, PE = PF + 32, FX = PE + 32, OF = FX + 8, OE = OF + 8, QF = OE + 8,
                    UE = QF + 8, DRAIN = UE + 8, GF = DRAIN + 16, GE = GF + 16;
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) {
-            mbar_init(KF + 8 * i, 1);
-            mbar_init(VL + 8 * i, 1);
-            mbar_init(KE + 8 * i, 4);
-            mbar_init(VE + 8 * i, 4);
+            mbar_init(RF + 8 * i, 1);
+            mbar_init(RE + 8 * i, 4);
         }
         for (int i = 0; i < C::NK; ++i) {
             mbar_init(KLF + 8 * i, 4);
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_init(GE + 8 * i, 31);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        for (int i = 0; i < 14; ++i) misc[i] = 0;
+        for (int i = 0; i < 16; ++i) misc[i] = 0;
     }
     if (warp == 29) {
         tc::tmem_alloc(sbase + C::OFF_MISC + 4, C::TMEM_COLS);
@@ -572,17 +573,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tc::fence_after_sync();
     const uint32_t tb = __shfl_sync(0xffffffffu, misc[1], 0);
 
-    // A bounded wait; once the CTA has given up every wait ends at once.
+    // A bounded wait; once the CTA has given up every wait ends at once.  (As little
+    // code as may be: it stands in many places.)
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long start = clock64();
+        uint32_t start = 0;
+#pragma unroll 1
         for (uint32_t it = 0; it < (1u << 26); ++it) {
             if (mbar_try_wait(bar, parity)) return true;
             if (misc[0]) return false;
-            if (clock64() - start > (1ll << 31)) break;
+            const uint32_t now = static_cast<uint32_t>(clock());
+            start = it ? start : now;
+            if (now - start > 1u << 31) break;
         }
         misc[0] = 1;
-        atomicOr(P.status, kDevTimeout);
         return false;
     };
     auto warp_wait = [&](uint32_t bar, uint32_t parity) {
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         // (not 0: an infinity that the row holds has to stay one)
                         fs[at] = fmaxf(tree_exp2(old - m), 1.17549435e-38f);
                         ms[at] = m;
-                        if (key == 0) misc[10 + sg] = gt + 1;
+                        if (key == 0) misc[12 + sg] = gt + 1;
                     }
                     bar_128(bar_id);
 #pragma unroll
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 // accumulators are done with the last unit
                 if (gt) {
                     ok = warp_wait(PE + 8 * wq, (gt - 1) & 1) && ok;
-                    if (misc[2 + 4 * ((gt - 1) & 1) + wq] == gt) ok = warp_wait(FX, (gt - 1) & 1) && ok;
+                    if (misc[4 + 4 * ((gt - 1) & 1) + wq] == gt) ok = warp_wait(FX, (gt - 1) & 1) && ok;
                     if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
                 }
                 // P^T: [32-key blocks][hi rows | lo rows][128 B], 16-byte pieces swizzled by the row
@@ -871,19 +874,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (uint32_t left = d[kTiles]; left; --left, ++gt, place -= C::KT) {
                 ok = warp_wait(OF, gt & 1) && ok;
                 tc::fence_after_sync();
+                // (all tags at once: beside the MMAs each load takes 200 cycles)
+                const uint4 raised = lds4(sbase + C::OFF_MISC + 48), odd = lds4(sbase + C::OFF_MISC + 16 + 16 * (gt & 1));
+                if (raised.x == gt + 1 || raised.y == gt + 1 || raised.z == gt + 1 || raised.w == gt + 1) {
 #pragma unroll
-                for (int sg = 0; sg < 4; ++sg) {
-                    if (misc[10 + sg] != gt + 1) continue;  // the maxima were raised: what there is shrinks
+                    for (int sg = 0; sg < 4; ++sg) {
+                        // the maxima were raised: what there is shrinks
+                        if ((sg == 0 ? raised.x : sg == 1 ? raised.y : sg == 2 ? raised.z : raised.w) != gt + 1) continue;
 #pragma unroll
-                    for (int c = 0; c < RB; ++c) {
-                        if ((c / 8) % 4 != sg) continue;
-                        const float f = fs[c];
+                        for (int c = 0; c < RB; ++c) {
+                            if ((c / 8) % 4 != sg) continue;
+                            const float f = fs[c];
 #pragma unroll
-                        for (int h = 0; h < C::DH; ++h) o[h][c] *= f;
+                            for (int h = 0; h < C::DH; ++h) o[h][c] *= f;
+                        }
                     }
                 }
-                for (uint32_t kb = 0; kb < 4; ++kb) {  // V values that are not finite
-                    if (misc[2 + 4 * (gt & 1) + kb] != gt + 1 || (C::FOLD && me >= C::VD)) continue;
+                // V values that are not finite
+                const bool any = odd.x == gt + 1 || odd.y == gt + 1 || odd.z == gt + 1 || odd.w == gt + 1;
+                for (uint32_t kb = any && !(C::FOLD && me >= C::VD) ? 0 : 4; kb < 4; ++kb) {
+                    if (misc[4 + 4 * (gt & 1) + kb] != gt + 1) continue;
                     const uint32_t k0 = place + 32 * kb, end = d[kPast] + d[kNodes];
                     for (uint32_t k = 0; k < 32 && k0 + k < end; ++k) {
                         const size_t at = (static_cast<size_t>(tree_place(P, d[kReq], k0 + k)) * P.n_kv_head + d[kKvHead]) * HD;
@@ -980,8 +990,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t turn = warp < 24 ? 0u : 1u;
         const int w = warp & 3, me = w * 32 + lane;
         const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
-        // pieces, this warpgroup's of K and of V, tiles; per slot: the parity of its K, 16 up of its V
-        uint32_t pc = 0, nk = 0, nv = 0, gt = 0, phase = 0;
+        // this warpgroup's slot and the parity of its piece, pieces of K and of V so far, tiles
+        uint32_t sl = turn, phase = 0, nk = 0, nv = 0, gt = 0;
         bool ok = true;
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
@@ -1000,21 +1010,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (lane == 0 && ok) mbar_arrive(handed);
                 handed = 0;
             };
-            auto landed = [&](uint32_t bar, uint32_t bit) {
-                const uint32_t parity = phase >> bit & 1;
-                phase ^= 1u << bit;
-                if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
+            auto landed = [&]() {
+                if (__all_sync(0xffffffffu, mbar_test(RF + 8 * sl, phase))) return;
                 hand_over();
-                ok = warp_wait(bar, parity) && ok;
+                ok = warp_wait(RF + 8 * sl, phase) && ok;
+            };
+            auto read = [&]() {  // the slot is free; to the next one
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(RE + 8 * sl);
+                sl += 2;
+                if (sl >= NSLOT) sl = turn, phase ^= 1;
             };
             // K(0), then K(t + 1) and V(t) by turns
             for (uint32_t i = 0; i <= last; ++i) {
                 if (i == last || (i && !(i & 1))) {
-                    pc += turn;
 #pragma unroll 1
-                    for (int j = static_cast<int>(turn); j < C::VP; j += 2, pc += 2, ++nv) {
-                        const uint32_t sl = pc % NSLOT;
-                        landed(VL + 8 * sl, 16 + sl);
+                    for (int j = static_cast<int>(turn); j < C::VP; j += 2, ++nv) {
+                        landed();
                         const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
                         const uint32_t dst = tlane + C::C_V + C::VCOLS * turn;
 #pragma unroll 1
@@ -1046,7 +1058,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             if (!C::FOLD || w >= 2) tc::tmem_st32((C::FOLD ? dst : dst + 32) + 32 * h, x);
                             if (__any_sync(0xffffffffu, !(sum.x + sum.y == sum.x + sum.y))) {
                                 // such values are zeros to the tensor core; once more
-                                if (lane == 0) misc[2 + 4 * (gt & 1) + k0 / 32] = gt + 1;
+                                if (lane == 0) misc[4 + 4 * (gt & 1) + k0 / 32] = gt + 1;
                                 tc::tmem_st_wait();
 #pragma unroll 1
                                 for (int low = 0; low < 2; ++low) {
@@ -1065,19 +1077,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 }
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0 && ok) mbar_arrive(VE + 8 * sl);
+                        read();
                         handed = VF + 8 * turn;
                     }
-                    pc -= turn;
                     ++gt;
                     end += C::KT;
                 } else {
-                    pc += turn;
 #pragma unroll 1
-                    for (int j = static_cast<int>(turn); j < C::KP; j += 2, pc += 2, ++nk) {
-                        const uint32_t sl = pc % NSLOT;
-                        landed(KF + 8 * sl, sl);
+                    for (int j = static_cast<int>(turn); j < C::KP; j += 2, ++nk) {
+                        landed();
                         const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
                         uint32_t x[32];
 #pragma unroll
@@ -1100,11 +1108,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             x[k + 1] = __float_as_uint(lo.y);
                         }
                         tc::tmem_st32(dst + 32, x);
-                        __syncwarp();
-                        if (lane == 0 && ok) mbar_arrive(KE + 8 * sl);
+                        read();
                         handed = KLF + 8 * turn;
                     }
-                    pc -= turn;
                 }
             }
             hand_over();
@@ -1114,68 +1120,70 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // ------------------------------------------------------------ producer
         regs_decrease<kRegAux>();
         bool ok = true, waited = false;
-        uint32_t pc = 0;
-        // per slot: its last piece was V, the parities of the waits for its being empty, and of
-        // what was last sent into it (filled: K's bits, V's 16 up)
-        uint32_t was_v = 0, ke = 0, ve = 0, kf = 0, vl = 0, filled = 0;
-        const uint32_t box = P.box_keys, boxes = C::KT / box;
-        const uint32_t vbox = min(box, static_cast<uint32_t>(C::VK)), vboxes = C::VK / vbox;
+        uint32_t sl = 0, phase = 1, sent = 0;  // the slot, the parity of its being empty, pieces sent
+        const uint32_t box = P.box_keys, lb = 31 - __clz(box), boxes = C::KT >> lb;
+        const uint32_t vbox = min(box, static_cast<uint32_t>(C::VK)), vboxes = max(C::VK >> lb, 1);
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
             const volatile uint32_t* d = words(u);
             if (!ok || !d[kMore]) break;
-            const uint32_t tiles = d[kTiles], x0 = d[kKvHead] * HD, end = d[kPast] + d[kNodes];
-            uint32_t y[2] = {0, 0};  // this lane's box of a tile, by the tile's parity: its row
+            const uint32_t last = 2 * d[kTiles] - 1, x0 = d[kKvHead] * HD, end = d[kPast] + d[kNodes], past = d[kPast];
+            const uint32_t r = d[kReq];
+            uint32_t place = d[kPlace];
+            // the row of this lane's box of the tile at p
+            auto row_at = [&](uint32_t p) {
+                const uint32_t k = p + lane * box;
+                return static_cast<uint32_t>(lane) < boxes && k < end ? tree_place(P, r, k) : 0u;
+            };
+            uint32_t yv = 0, yk = 0, next = row_at(place);  // the tiles of V, of K, and the next one's
             // K(0), then K(t + 1) and V(t) by turns
-            for (uint32_t i = 0; i < 2 * tiles; ++i) {
-                const bool v = i == 2 * tiles - 1 || (i && !(i & 1));
-                const uint32_t t = v ? (i - 1) / 2 : (i + 1) / 2;
+#pragma unroll 1
+            for (uint32_t i = 0; i <= last; ++i) {
+                const bool v = i == last || (i && !(i & 1));
                 if (!v) {
-                    const uint32_t place = d[kPlace] - t * C::KT, k = place + lane * box;
                     // (tiles of history may be read while the prep kernel still runs)
-                    if (!waited && place + C::KT > d[kPast]) {
+                    if (!waited && place + C::KT > past) {
                         grid_dependency_wait();
                         waited = true;
                     }
-                    const uint32_t row = static_cast<uint32_t>(lane) < boxes && k < end ? tree_place(P, d[kReq], k) : 0u;
-                    y[0] = t & 1 ? y[0] : row;
-                    y[1] = t & 1 ? row : y[1];
+                    yv = yk;
+                    yk = next;
+                    place -= C::KT;
+                    if (i + (i ? 2 : 1) < last) next = row_at(place);
                 }
-                const uint32_t yt = t & 1 ? y[1] : y[0];
-                const int pieces = v ? C::VP : C::KP;
+                // this lane's box of the first piece: its key, and what there is of it
+                uint32_t k = lane * (v ? vbox : box), x = x0;
+                const uint32_t y = !v || i == last ? yk : yv, off = sbase + C::OFF_RING + k * (v ? C::VD * 4 : 128);
+                const bool mine = static_cast<uint32_t>(lane) < (v ? vboxes : boxes);
+                const CUtensorMap* map = v ? &tmV : &tmK;
+                static_assert(C::KP == C::VP, "pieces");
 #pragma unroll 1
-                for (int j = 0; j < pieces; ++j, ++pc) {
-                    const uint32_t sl = pc % NSLOT, bit = 1u << sl;
-                    if (pc >= NSLOT) {
-                        const bool w = was_v & bit;
-                        ok = warp_wait((w ? VE : KE) + 8 * sl, (w ? ve : ke) & bit ? 1 : 0) && ok;
-                        (w ? ve : ke) ^= bit;
-                    }
-                    // the row of this lane's box of the piece
-                    const uint32_t k = v ? j / C::DH * C::VK + lane * vbox : lane * box;
-                    const uint32_t row = __shfl_sync(0xffffffffu, yt, (k / box) & 31) + k % box;
-                    if (!ok) continue;
-                    const uint32_t bar = (v ? VL : KF) + 8 * sl;
-                    was_v = v ? was_v | bit : was_v & ~bit;
-                    const uint32_t sent = v ? bit << 16 : bit;
-                    if (filled & sent) (v ? vl : kf) ^= bit;
-                    filled |= sent;
-                    if (lane == 0) mbar_expect_tx(bar, C::PIECE);
+                for (int j = 0; j < C::KP; ++j) {
+                    const uint32_t row = __shfl_sync(0xffffffffu, y, k >> lb & 31) + (k & (box - 1));
+                    ok = ok && warp_wait(RE + 8 * sl, phase);
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(RF + 8 * sl, C::PIECE);
                     __syncwarp();
-                    const uint32_t dst = sbase + C::OFF_RING + sl * C::PIECE + lane * (v ? vbox * C::VD * 4 : box * 128);
-                    if (static_cast<uint32_t>(lane) < (v ? vboxes : boxes))
-                        tma_load_2d(dst, v ? &tmV : &tmK, static_cast<int>(x0 + (v ? j % C::DH * C::VD : 32 * j)),
-                                    static_cast<int>(row), bar);
+                    if (mine)
+                        tma_load_2d(off + sl * C::PIECE, map, static_cast<int>(x), static_cast<int>(row), RF + 8 * sl);
+                    ++sent;
+                    if (++sl == NSLOT) sl = 0, phase ^= 1;
+                    if (!v) {
+                        x += 32;
+                    } else if (C::DH == 1 || (j & 1)) {
+                        k += C::VK;
+                        x = x0;
+                    } else {
+                        x += C::VD;
+                    }
                 }
             }
             done(u);
         }
         grid_launch_dependents();
         if (misc[0])  // copies that may still be in flight
-            for (uint32_t sl = 0; sl < NSLOT; ++sl) {
-                if (filled >> sl & 1) mbar_wait(KF + 8 * sl, kf >> sl & 1, 1ll << 28);
-                if (filled >> (16 + sl) & 1) mbar_wait(VL + 8 * sl, vl >> sl & 1, 1ll << 28);
-            }
+            for (uint32_t s = 0; s < NSLOT && s < sent; ++s)
+                mbar_wait(RF + 8 * s, (sent - 1 - s) / NSLOT & 1, 1ll << 28);
     } else if (warp == 31) {
         // ------------------------------------------------------------ units
         regs_decrease<kRegAux>();
@@ -1370,6 +1378,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 29) tc::tmem_dealloc(tb, C::TMEM_COLS);
+    if (tid == 0 && misc[0]) atomicOr(P.status, kDevTimeout);
 }
 
 // ------------------------------------------------------------------ combine
