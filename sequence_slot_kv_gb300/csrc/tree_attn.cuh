@@ -38,13 +38,13 @@ __device__ __forceinline__ uint32_t tree_place(const TreeParams& P, uint32_t r, 
 // depth that of the node it points at and doubles the distance, so a chain of
 // 256 takes 8 rounds).  Part 0 does the same with the sets of ancestors and
 // writes, for every node, the set of the nodes that attend it.  The other parts
-// form the request's vectors, one warp per (node, kTreeQHeads query heads or
-// kTreeKvHeads kv heads): q' = RoPE(RMSnorm(q) w) scale log2(e) into the
+// form the request's vectors, one warp per (node, P.prep_heads query heads or half
+// as many kv heads): q' = RoPE(RMSnorm(q) w) scale log2(e) into the
 // workspace, k' and v into the node's cache row, with the decode kernel's
 // vector routines (so the same bits as a decode step's at that position).  A
 // call is bound by its dependent loads here; a warp's first rows are on their
 // way while the tree is looked at.
-constexpr int kTreeQHeads = 8, kTreeKvHeads = 4, kPrepThreads = 128, kPrepWarps = kPrepThreads / 32;
+constexpr int kPrepHeads = 8, kPrepCtas = 4, kPrepThreads = 128, kPrepWarps = kPrepThreads / 32;
 
 __device__ __forceinline__ void tree_cp_async16(void* smem_dst, const void* gmem_src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)), "l"(gmem_src)
@@ -69,11 +69,6 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, uint32_t r)
 }
 
 template <int HD>
-constexpr int tree_prep_smem() {
-    return kPrepWarps * kTreeQHeads * HD * 4;
-}
-
-template <int HD>
 __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const TreeParams P) {
     extern __shared__ __align__(16) uint8_t prep_smem[];
     __shared__ uint32_t set[kTreeNodes][kTreeWords];
@@ -86,10 +81,11 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
     const TreeReq q = tree_request(P, r);
     if (q.n == 0) return;
     // this warp's rows of item it, on their way
-    const uint32_t qg = (P.n_head + kTreeQHeads - 1) / kTreeQHeads;
-    const uint32_t groups = qg + (P.n_kv_head + kTreeKvHeads - 1) / kTreeKvHeads;
-    float* rows = reinterpret_cast<float*>(prep_smem) + warp * kTreeQHeads * HD;
-    float* vrows = rows + kTreeKvHeads * HD;
+    const uint32_t qh = P.prep_heads, kvh = (qh + 1) / 2;
+    const uint32_t qg = (P.n_head + qh - 1) / qh;
+    const uint32_t groups = qg + (P.n_kv_head + kvh - 1) / kvh;
+    float* rows = reinterpret_cast<float*>(prep_smem) + warp * 2 * kvh * HD;
+    float* vrows = rows + kvh * HD;
     struct Item {
         uint32_t node, x0, nx;
         bool is_q;
@@ -99,8 +95,8 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
         const uint32_t grp = it % groups;
         m.node = it / groups;
         m.is_q = grp < qg;
-        m.x0 = m.is_q ? grp * kTreeQHeads : (grp - qg) * kTreeKvHeads;
-        const uint32_t left = (m.is_q ? P.n_head : P.n_kv_head) - m.x0, most = m.is_q ? kTreeQHeads : kTreeKvHeads;
+        m.x0 = m.is_q ? grp * qh : (grp - qg) * kvh;
+        const uint32_t left = (m.is_q ? P.n_head : P.n_kv_head) - m.x0, most = m.is_q ? qh : kvh;
         m.nx = left < most ? left : most;
         return m;
     };
@@ -1387,16 +1383,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 constexpr int kJoinThreads = 256;
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const TreeParams P) {
-    grid_dependency_wait();
-    grid_launch_dependents();
     constexpr int RB = TreeCfg<HD>::RB, E = HD / 32;
     const int lane = threadIdx.x & 31;
     const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const uint32_t tok = static_cast<uint32_t>(w / P.n_head), h = static_cast<uint32_t>(w % P.n_head);
     if (tok >= P.n_tok) return;
-    const uint32_t r = P.req_of[tok];
-    if (r >= P.n_req) return;
-    const TreeShape x = tree_shape<RB>(P, r);
+    // The request, where that takes one look at the lengths, and its shape while the attention
+    // kernel still runs (they are inputs of the call); after that what prep says of the node.
+    uint32_t r = kTreeSkip;
+    TreeShape x = {};
+    if (P.n_req <= 32) {
+        const uint32_t s0 = static_cast<uint32_t>(lane) < P.n_req ? __ldg(P.starts + lane) : 0u;
+        const uint32_t s1 = static_cast<uint32_t>(lane) < P.n_req ? __ldg(P.starts + lane + 1) : 0u;
+        const uint32_t here = __ballot_sync(0xffffffffu, s0 <= tok && tok < s1);
+        if (here) {
+            r = __ffs(here) - 1;
+            x = tree_shape<RB>(P, r);
+        }
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const uint32_t owner = __ldcg(P.req_of + tok);
+    if (owner >= P.n_req) return;
+    if (owner != r) {
+        r = owner;
+        x = tree_shape<RB>(P, r);
+    }
     if (x.nb == 0 || tok < x.q.s0 || tok - x.q.s0 >= x.q.n) return;  // (left from an earlier call)
     const uint32_t G = P.n_head / P.n_kv_head, g = h / G;
     const uint32_t row = (tok - x.q.s0) * G + h % G, b = row / RB;
@@ -1424,6 +1436,7 @@ __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float den = 0.f, acc[E] = {};
+#pragma unroll 4
     for (uint32_t c = c0; c <= c1; ++c) {
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(c));
         const float f = fmaxf(tree_exp2(ml.x - m), 1.17549435e-38f);  // (see the raise)
@@ -1439,7 +1452,7 @@ __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const
 }
 
 template <int HD>
-int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, uint32_t sms,
+int launch_tree_hd(TreeParams p, const CUtensorMap& tmK, const CUtensorMap& tmV, uint32_t sms,
                    cudaStream_t stream) {
     using C = TreeCfg<HD>;
     static std::atomic<uint64_t> configured{0};
@@ -1469,14 +1482,19 @@ int launch_tree_hd(const TreeParams& p, const CUtensorMap& tmK, const CUtensorMa
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // parts: about one item per warp for requests of the mean size
-    const uint32_t groups = (p.n_head + kTreeQHeads - 1) / kTreeQHeads +
-                            (p.n_kv_head + kTreeKvHeads - 1) / kTreeKvHeads;
+    // parts: about one item per warp for requests of the mean size; a warp's heads come one
+    // after the other, so as few as leave no SM more than kPrepCtas CTAs
     const uint64_t mean = (p.n_tok + p.n_req - 1) / p.n_req;
-    const uint64_t parts = (mean * groups + kPrepWarps - 1) / kPrepWarps;
+    uint64_t parts = 0;
+    for (p.prep_heads = 1;; p.prep_heads *= 2) {
+        const uint32_t kvh = (p.prep_heads + 1) / 2;
+        const uint32_t groups = (p.n_head + p.prep_heads - 1) / p.prep_heads + (p.n_kv_head + kvh - 1) / kvh;
+        parts = (mean * groups + kPrepWarps - 1) / kPrepWarps;
+        if (p.prep_heads == kPrepHeads || p.n_req * (1 + parts) <= static_cast<uint64_t>(kPrepCtas) * sms) break;
+    }
     cfg.gridDim = dim3(p.n_req, 1 + static_cast<unsigned>(parts < 256 ? parts : 256));
     cfg.blockDim = dim3(kPrepThreads);
-    cfg.dynamicSmemBytes = tree_prep_smem<HD>();
+    cfg.dynamicSmemBytes = kPrepWarps * 2 * ((p.prep_heads + 1) / 2) * HD * 4;
     if ((e = cudaLaunchKernelEx(&cfg, slotkv_tree_prep_kernel<HD>, p)) != cudaSuccess) return static_cast<int>(e);
     cfg.gridDim = dim3(tree_grid(sms));
     cfg.blockDim = dim3(kTreeThreads);

@@ -39,6 +39,7 @@ struct TreeParams {
     uint32_t* plan;          // workspace [4][4]: of each size the tiles (64 bits), groups, first CTA
     uint32_t* status;        // sticky SLOTKV_DEV_* flags
     uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
+    uint32_t prep_heads;     // query heads of one warp of the prep kernel (the launcher's choice)
     uint32_t box_keys;       // keys of one TMA box of K: a power of two, at most 128
     float eps;
     float scale_log2;        // softmax scale * log2(e)
