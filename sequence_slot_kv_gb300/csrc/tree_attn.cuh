@@ -298,12 +298,10 @@ struct TreeCfg {
     static constexpr int QBYTES = 2 * RB * HD * 4, PBYTES = 2 * RB * KT * 4;
     static constexpr int OFF_P = QBYTES, OFF_RING = QBYTES + PBYTES;
     static constexpr int NSLOT = (224 * 1024 - OFF_RING) / PIECE;  // 8, 6, 8
-    static constexpr int NK = 2, NV = 2;                // buffers of K and of V^T
-    // tensor memory columns
-    static constexpr int C_S = 0, C_O = 2 * RB, C_K = C_O + DH * 2 * RB, C_V = C_K + NK * 64;
-    // a K buffer: hi | lo, 32 dims each; a V^T buffer: hi | lo, 32 keys each (FOLD: 64 keys)
-    static constexpr int VCOLS = 64;
-    static_assert(C_V + NV * VCOLS <= 512, "tensor memory");
+    static constexpr int NB = 4;                        // buffers of pieces in tensor memory
+    // tensor memory columns; a buffer: K's hi | lo, 32 dims each, or V^T's, 32 keys each (FOLD: 64 keys)
+    static constexpr int C_S = 0, C_O = 2 * RB, C_B = C_O + DH * 2 * RB, BCOLS = 64;
+    static_assert(C_B + NB * BCOLS <= 512, "tensor memory");
     static constexpr int TMEM_COLS = 512;
     // shared memory behind the ring: row data, scratch of the maxima, barriers, flags
     static constexpr int OFF_M = OFF_RING + NSLOT * PIECE;      // running maxima [2 units][RB]
@@ -314,10 +312,10 @@ struct TreeCfg {
     static constexpr int OFF_MAX = OFF_NODE + RB;          // a warp's maxima, its sums [4][RB]
     static constexpr int OFF_DESC = OFF_MAX + 4 * RB * 4;       // what the roles need to know of a unit [2]
     static constexpr int OFF_BAR = OFF_DESC + 2 * 12 * 4;
-    // piece landed, slot empty [NSLOT]; K converted, its buffer empty [NK]; V^T converted, its buffer
-    // empty [NV]; S full, empty; P full, empty [4]; tile done with; O full, empty; Q full; unit's end;
-    // drain [2]; unit known, done with [2]
-    static constexpr int NBAR = 2 * NSLOT + 2 * NK + 2 * NV + 21;
+    // piece landed, slot empty [NSLOT]; K in a buffer, V^T in it, the buffer empty [NB] (each kind's
+    // issuer has to see every phase of the barrier that it waits at); S full, empty; P full, empty [4];
+    // tile done with; O full, empty; Q full; unit's end; drain [2]; unit known, done with [2]
+    static constexpr int NBAR = 2 * NSLOT + 3 * NB + 21;
     static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
     static constexpr int SMEM = OFF_MISC + 64;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -524,21 +522,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // V value that is not finite in that block of 32 keys, [12 + softmax warpgroup] the last
     // with a raise
     const uint32_t bar0 = sbase + C::OFF_BAR;
-    const uint32_t RF = bar0, RE = RF + 8 * NSLOT, KLF = RE + 8 * NSLOT, KLE = KLF + 8 * C::NK, VF = KLE + 8 * C::NK, VFE = VF + 8 * C::NV, SF = VFE + 8 * C::NV,
-                   SE = SF + 8, PF = SE + 8, PE = PF + 32, FX = PE + 32, OF = FX + 8, OE = OF + 8, QF = OE + 8,
-                   UE = QF + 8, DRAIN = UE + 8, GF = DRAIN + 16, GE = GF + 16;
+    const uint32_t RF = bar0, RE = RF + 8 * NSLOT, KF = RE + 8 * NSLOT, VF = KF + 8 * C::NB, BE = VF + 8 * C::NB,
+                   SF = BE + 8 * C::NB, SE = SF + 8, PF = SE + 8, PE = PF + 32, FX = PE + 32, OF = FX + 8,
+                   OE = OF + 8, QF = OE + 8, UE = QF + 8, DRAIN = UE + 8, GF = DRAIN + 16, GE = GF + 16;
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(RF + 8 * i, 1);
             mbar_init(RE + 8 * i, 4);
         }
-        for (int i = 0; i < C::NK; ++i) {
-            mbar_init(KLF + 8 * i, 4);
-            mbar_init(KLE + 8 * i, 1);
-        }
-        for (int i = 0; i < C::NV; ++i) {
+        for (int i = 0; i < C::NB; ++i) {
+            mbar_init(KF + 8 * i, 4);
             mbar_init(VF + 8 * i, 4);
-            mbar_init(VFE + 8 * i, 1);
+            mbar_init(BE + 8 * i, 1);
         }
         mbar_init(SF, 1);
         mbar_init(SE, 16);
@@ -980,14 +975,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // ------------------------------------------------------------ converters
         // The two warpgroups take the pieces by turns; with an even number of
         // slots, of a tile's pieces and of buffers, each sees every phase of its
-        // own barriers.
-        static_assert(NSLOT % 2 == 0 && C::KP % 2 == 0 && C::VP % 2 == 0 && C::NK == 2 && C::NV == 2, "turns");
+        // own barriers.  Pieces go round the buffers in order, K's and V's alike, so
+        // a warpgroup fills one buffer while the MMAs read its other one.
+        static_assert(NSLOT % 2 == 0 && C::KP % 2 == 0 && C::VP % 2 == 0 && C::NB == 4, "turns");
         regs_decrease<kRegConv>();
         const uint32_t turn = warp < 24 ? 0u : 1u;
         const int w = warp & 3, me = w * 32 + lane;
         const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
-        // this warpgroup's slot and the parity of its piece, pieces of K and of V so far, tiles
-        uint32_t sl = turn, phase = 0, nk = 0, nv = 0, gt = 0;
+        // this warpgroup's slot and the parity of its piece, its buffer and the parity of that
+        // being empty, tiles
+        uint32_t sl = turn, phase = 0, buf = turn, empty = 1, gt = 0;
         bool ok = true;
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
@@ -1017,14 +1014,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 sl += 2;
                 if (sl >= NSLOT) sl = turn, phase ^= 1;
             };
+            // the piece's stores are on their way; the next one goes into the other buffer
+            auto stored = [&](uint32_t full) {
+                read();
+                handed = full + 8 * buf;
+                buf ^= 2;
+                if (buf == turn) empty ^= 1;
+            };
             // K(0), then K(t + 1) and V(t) by turns
             for (uint32_t i = 0; i <= last; ++i) {
                 if (i == last || (i && !(i & 1))) {
 #pragma unroll 1
-                    for (int j = static_cast<int>(turn); j < C::VP; j += 2, ++nv) {
+                    for (int j = static_cast<int>(turn); j < C::VP; j += 2) {
                         landed();
                         const float* src = reinterpret_cast<const float*>(smem + C::OFF_RING + sl * C::PIECE) + me % C::VD;
-                        const uint32_t dst = tlane + C::C_V + C::VCOLS * turn;
+                        const uint32_t dst = tlane + C::C_B + C::BCOLS * buf;
 #pragma unroll 1
                         for (int h = 0; h < C::VK / 32; ++h) {  // 32 keys at a time
                             const uint32_t k0 = j / C::DH * C::VK + 32 * h;
@@ -1038,7 +1042,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             }
                             if (h == 0) {
                                 hand_over();
-                                if (nv) ok = warp_wait(VFE + 8 * turn, (nv - 1) & 1) && ok;
+                                ok = warp_wait(BE + 8 * buf, empty) && ok;
                                 tc::fence_after_sync();
                             }
                             // the landed values are their own high parts
@@ -1073,14 +1077,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 }
                             }
                         }
-                        read();
-                        handed = VF + 8 * turn;
+                        stored(VF);
                     }
                     ++gt;
                     end += C::KT;
                 } else {
 #pragma unroll 1
-                    for (int j = static_cast<int>(turn); j < C::KP; j += 2, ++nk) {
+                    for (int j = static_cast<int>(turn); j < C::KP; j += 2) {
                         landed();
                         const uint8_t* src = smem + C::OFF_RING + sl * C::PIECE + me * 128;
                         uint32_t x[32];
@@ -1093,9 +1096,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             x[4 * c + 3] = y.w;
                         }
                         hand_over();
-                        if (nk) ok = warp_wait(KLE + 8 * turn, (nk - 1) & 1) && ok;
+                        ok = warp_wait(BE + 8 * buf, empty) && ok;
                         tc::fence_after_sync();
-                        const uint32_t dst = tlane + C::C_K + 64 * turn;
+                        const uint32_t dst = tlane + C::C_B + C::BCOLS * buf;
                         tc::tmem_st32(dst, x);  // (the landed values are their own high parts)
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
@@ -1104,8 +1107,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             x[k + 1] = __float_as_uint(lo.y);
                         }
                         tc::tmem_st32(dst + 32, x);
-                        read();
-                        handed = KLF + 8 * turn;
+                        stored(KF);
                     }
                 }
             }
@@ -1282,7 +1284,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         regs_decrease<kRegAux>();
         const bool lead = tc::elect_one();
         bool ok = true;
-        uint32_t n_piece = 0, tiles = 0;  // this warp's pieces, its tiles
+        uint32_t full = 0, tiles = 0;  // the parities of its pieces in the buffers, its tiles
         for (uint32_t u = 0;; ++u) {
             ok = known(u) && ok;
             const volatile uint32_t* d = words(u);
@@ -1300,14 +1302,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 ok = warp_wait(QF, u & 1) && ok;
                 for (uint32_t t = 0; t < n; ++t, ++tiles) {
                     if (tiles) ok = warp_wait(SE, (tiles - 1) & 1) && ok;
+                    uint32_t b = t ? C::KP % C::NB : 0;  // K(t) comes behind 2 t - 1 others
 #pragma unroll 1
-                    for (int j = 0; j < C::KP; ++j, ++n_piece) {
-                        const uint32_t b = n_piece % C::NK;
-                        ok = warp_wait(KLF + 8 * b, (n_piece / C::NK) & 1) && ok;
+                    for (int j = 0; j < C::KP; ++j, b = (b + 1) % C::NB) {
+                        ok = warp_wait(KF + 8 * b, full >> b & 1) && ok;
+                        full ^= 1u << b;
                         if (!ok) continue;
                         tc::fence_after_sync();
                         const uint64_t qd = qdesc0 + j * block;
-                        const uint32_t k = tb + C::C_K + 64 * b, kle = KLE + 8 * b;
+                        const uint32_t k = tb + C::C_B + C::BCOLS * b, free = BE + 8 * b;
                         const uint32_t more = j ? 1u : 0u;
                         if (lead) {
 #pragma unroll
@@ -1316,7 +1319,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 tc::mma_tf32_ts(sl2, k + 32 + 8 * kk, qd + 2 * kk, i1, 1u);
-                            tc::mma_commit(kle);
+                            tc::mma_commit(free);
                         }
                         __syncwarp();
                     }
@@ -1328,21 +1331,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const uint64_t pdesc0 = tc::smem_desc(sbase + C::OFF_P, 16, 1024, tc::kSwizzle128B);
                 for (uint32_t t = 0; t < n; ++t, ++tiles) {
                     if (tiles) ok = warp_wait(OE, (tiles - 1) & 1) && ok;
+                    uint32_t b = t == n - 1 ? C::VP % C::NB : 0;  // V(t) comes behind 2 t + 2, the last behind 2 n - 1
 #pragma unroll 1
-                    for (int j = 0; j < C::VP; ++j, ++n_piece) {
-                        const uint32_t b = n_piece % C::NV;
+                    for (int j = 0; j < C::VP; ++j, b = (b + 1) % C::NB) {
                         if (j % C::DH == 0)
 #pragma unroll
                             for (int h = 0; h < C::VK / 32; ++h)
                                 ok = warp_wait(PF + 8 * (j / C::DH * (C::VK / 32) + h), tiles & 1) && ok;
-                        ok = warp_wait(VF + 8 * b, (n_piece / C::NV) & 1) && ok;
+                        ok = warp_wait(VF + 8 * b, full >> b & 1) && ok;
+                        full ^= 1u << b;
                         if (!ok) continue;
                         tc::fence_after_sync();
-                        const uint32_t a = tb + C::C_V + C::VCOLS * b, o = tb + C::C_O + j % C::DH * 2 * RB;
+                        const uint32_t a = tb + C::C_B + C::BCOLS * b, o = tb + C::C_O + j % C::DH * 2 * RB;
                         const uint32_t ol = o + Rp;
                         const uint64_t pd = pdesc0 + j / C::DH * (C::VK / 32) * block, pd2 = pd + block;
                         const uint32_t more = j >= C::DH ? 1u : 0u;
-                        const uint32_t vfe = VFE + 8 * b, pe = PE + 8 * (j / C::DH * (C::VK / 32));
+                        const uint32_t free = BE + 8 * b, pe = PE + 8 * (j / C::DH * (C::VK / 32));
                         const bool last = j % C::DH == C::DH - 1;
                         if (lead) {
 #pragma unroll
@@ -1352,7 +1356,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                             for (int kk = 0; kk < (C::FOLD ? 0 : 4); ++kk)
                                 tc::mma_tf32_ts(ol, a + 32 + 8 * kk, pd + 2 * kk, i1, 1u);
-                            tc::mma_commit(vfe);
+                            tc::mma_commit(free);
                             if (last)
 #pragma unroll
                                 for (int h = 0; h < C::VK / 32; ++h) tc::mma_commit(pe + 8 * h);
