@@ -1455,10 +1455,10 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     if (((uintptr_t)starts | (uintptr_t)parents | (uintptr_t)sinks) & 3)
         return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
     slotkv::TreeParams P;
-    const size_t R = h->max_rows;
+    const size_t R = h->max_rows, joins = slotkv::kTreeJoin * (size_t)slotkv::tree_grid(sm_total(h));
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, s, "tree workspace (q)");
     if (rc == SLOTKV_OK)
-        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), 16 + 8 * R + R * (2 + slotkv::kTreeWords), s,
+        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), joins + R * (2 + slotkv::kTreeWords), s,
                        "tree workspace (nodes)");
     const size_t pr = slotkv::tree_partial_rows((int)h->head_dim, sm_total(h));
     if (rc == SLOTKV_OK)
@@ -1481,9 +1481,8 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     P.K = h->K;
     P.V = h->V;
     P.q_rot = h->sc_q;
-    P.plan = h->tree_idx;  // (read 16 bytes at a time, the first tiles 8 at a time)
-    P.base = reinterpret_cast<uint64_t*>(h->tree_idx + 16);
-    P.below = h->tree_idx + 16 + 8 * R;
+    P.join = h->tree_idx;  // (read 16 bytes at a time)
+    P.below = P.join + joins;
     P.req_of = P.below + R * slotkv::kTreeWords;
     P.part = h->tree_part;
     P.part_ml = P.part + pr * h->head_dim;

@@ -1207,7 +1207,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         walk.k = 0;
         walk.r = walk.member = 0;
         walk.off = walk.left = 0;
-        uint64_t u0 = 0;
+        uint64_t u0 = 0, u1 = 0;
+        uint32_t groups = 1;
+        uint64_t total = 1;
 #pragma unroll
         for (int k = 0; k < kSetSizes; ++k) {
             const uint32_t c = blockIdx.x - plan.first[k];
@@ -1215,55 +1217,54 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             walk.k = k;
             walk.member = c & ((1u << k) - 1u);
             u0 = tree_first(plan.total[k], plan.groups[k], c >> k);
-            walk.left = tree_first(plan.total[k], plan.groups[k], (c >> k) + 1) - u0;
+            u1 = tree_first(plan.total[k], plan.groups[k], (c >> k) + 1);
+            walk.left = u1 - u0;
+            groups = plan.groups[k];
+            total = plan.total[k];
         }
         // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
         if (sbase & 1023u) {
             walk.left = 0;
             if (lane == 0) atomicOr(P.status, kDevTimeout);
         }
-        // the request that the part begins in; CTA 0 writes all requests' first tiles, for the
-        // combine kernel
-        const bool tell = blockIdx.x == 0;
-        for (int k = 0; k < kSetSizes; ++k) {
-            if (!tell && k != walk.k) continue;
-            uint64_t at = 0;
-            for (uint32_t r0 = 0; r0 < P.n_req; r0 += 32) {
-                const TreeShape x = !r0 ? first : r0 + lane < P.n_req ? tree_shape<RB>(P, r0 + lane) : TreeShape{};
-                const uint64_t n = x.tiles(P.n_kv_head, k);
-                uint64_t incl = n;
+        // the request that the part begins in
+        uint64_t at = 0;
+        for (uint32_t r0 = 0; walk.left && r0 < P.n_req; r0 += 32) {
+            const TreeShape x = !r0 ? first : r0 + lane < P.n_req ? tree_shape<RB>(P, r0 + lane) : TreeShape{};
+            const uint64_t n = x.tiles(P.n_kv_head, walk.k);
+            uint64_t incl = n;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                const uint64_t begin = at + incl - n;
-                if (tell && r0 + lane < P.n_req) P.base[static_cast<size_t>(k) * P.n_req + r0 + lane] = begin;
-                const uint32_t here =
-                    __ballot_sync(0xffffffffu, k == walk.k && walk.left && begin <= u0 && u0 < begin + n);
-                if (here) {
-                    const int from = __ffs(here) - 1;
-                    walk.r = r0 + from;
-                    walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
-                    if (!tell) break;
-                }
-                at += __shfl_sync(0xffffffffu, incl, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
             }
+            const uint64_t begin = at + incl - n;
+            const uint32_t here = __ballot_sync(0xffffffffu, begin <= u0 && u0 < begin + n);
+            if (here) {
+                const int from = __ffs(here) - 1;
+                walk.r = r0 + from;
+                walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (tell && lane < kSetSizes) {
-#pragma unroll
-            for (int k = 0; k < kSetSizes; ++k)
-                if (lane == k) {
-                    P.plan[4 * k] = static_cast<uint32_t>(plan.total[k]);
-                    P.plan[4 * k + 1] = static_cast<uint32_t>(plan.total[k] >> 32);
-                    P.plan[4 * k + 2] = plan.groups[k];
-                    P.plan[4 * k + 3] = plan.first[k];
-                }
-        }
+        // nothing for the combine kernel to join from here on, unless there turns out to be
+        uint32_t* join = P.join + kTreeJoin * blockIdx.x;
+        if (lane == 0) join[kJoinRows] = 0u;
         for (uint32_t u = 0;; ++u) {
             uint32_t d[12];
             const bool more = walk.next(P, d);
             if (!more) d[kMore] = 0u;
+            if (more && d[kStart] && !d[kWhole] && lane == 0) {  // (the CTA's last; ends in another one)
+                const uint64_t first_tile = u1 - d[kTiles], last_tile = first_tile + walk.x.tl - 1;
+                join[kJoinTok] = d[kRow];
+                join[kJoinRow0] = d[kRow0];
+                join[kJoinRows] = d[kRows];
+                join[kJoinKvHead] = d[kKvHead];
+                join[kJoinReq] = d[kReq];
+                join[kJoinStep] = 1u << walk.k;
+                join[kJoinParts] = tree_owner(total, groups, last_tile) - tree_owner(total, groups, first_tile) + 1;
+            }
             if (u >= 2 && !warp_wait(GE + 8 * (u & 1), ((u >> 1) - 1) & 1)) break;
             if (lane == 0) {
                 volatile uint32_t* to = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_DESC) + 12 * (u & 1);
@@ -1382,70 +1383,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// One warp per (node, query head): the partial results of a unit that lies in
-// several CTAs, in CTA order; the others are done already.
+// The units that lie in several CTAs, of which there is one at most that begins in
+// a CTA: its partial results in the CTAs' order, a warp per row.
 constexpr int kJoinThreads = 256;
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const TreeParams P) {
-    constexpr int RB = TreeCfg<HD>::RB, E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    const uint32_t tok = static_cast<uint32_t>(w / P.n_head), h = static_cast<uint32_t>(w % P.n_head);
-    if (tok >= P.n_tok) return;
-    // The request, where that takes one look at the lengths, and its shape while the attention
-    // kernel still runs (they are inputs of the call); after that what prep says of the node.
-    uint32_t r = kTreeSkip;
-    TreeShape x = {};
-    if (P.n_req <= 32) {
-        const uint32_t s0 = static_cast<uint32_t>(lane) < P.n_req ? __ldg(P.starts + lane) : 0u;
-        const uint32_t s1 = static_cast<uint32_t>(lane) < P.n_req ? __ldg(P.starts + lane + 1) : 0u;
-        const uint32_t here = __ballot_sync(0xffffffffu, s0 <= tok && tok < s1);
-        if (here) {
-            r = __ffs(here) - 1;
-            x = tree_shape<RB>(P, r);
-        }
-    }
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t owner = __ldcg(P.req_of + tok);
-    if (owner >= P.n_req) return;
-    if (owner != r) {
-        r = owner;
-        x = tree_shape<RB>(P, r);
-    }
-    if (x.nb == 0 || tok < x.q.s0 || tok - x.q.s0 >= x.q.n) return;  // (left from an earlier call)
-    const uint32_t G = P.n_head / P.n_kv_head, g = h / G;
-    const uint32_t row = (tok - x.q.s0) * G + h % G, b = row / RB;
-    // the row block's set, and where its tiles are
-    int k = 0;
-#pragma unroll
-    for (int i = kSetSizes - 1; i > 0; --i)
-        if (b < (x.nb & ~((1u << i) - 1u))) {
-            k = i;
-            break;
-        }
-    const uint32_t in = b - tree_set_block(x.nb, k), sets = tree_sets(x.nb, k);
-    const uint4 plan = __ldcg(reinterpret_cast<const uint4*>(P.plan) + k);  // tiles, groups, first CTA
-    const uint64_t total = static_cast<uint64_t>(plan.y) << 32 | plan.x;
-    const uint64_t a = __ldcg(P.base + static_cast<size_t>(k) * P.n_req + r) +
-                       (static_cast<uint64_t>(g) * sets + (in >> k)) * x.tl;
-    const uint32_t c0 = tree_owner(total, plan.z, a), c1 = tree_owner(total, plan.z, a + x.tl - 1);
-    if (c0 == c1) return;
-    auto slot = [&](uint32_t c) {
-        const uint32_t cta = plan.w + (c << k) + (in & ((1u << k) - 1u));
-        return (2 * static_cast<size_t>(cta) + (c == c0 ? 1 : 0)) * RB + row % RB;
+    constexpr int RB = TreeCfg<HD>::RB, E = HD / 32;
+    const int lane = threadIdx.x & 31;
+    const uint32_t row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const uint4* join = reinterpret_cast<const uint4*>(P.join + kTreeJoin * blockIdx.x);
+    const uint4 j0 = __ldcg(join), j1 = __ldcg(join + 1);
+    const uint32_t rows = j0.z, step = j1.y, parts = j1.z;
+    if (row >= rows) return;
+    const uint32_t G = P.n_head / P.n_kv_head, at = j0.y + row;
+    const uint32_t tok = j0.x + at / G, h = j0.w * G + at % G;
+    // part i's row: the first CTA's last unit, the others' first one
+    auto slot = [&](uint32_t i) {
+        return (2 * static_cast<size_t>(blockIdx.x + i * step) + (i ? 0 : 1)) * RB + row;
     };
-    float m = -1e30f;
-    for (uint32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(P.part_ml + 2 * slot(c)));
+    float2 ml = make_float2(-1e30f, 0.f);
+    if (static_cast<uint32_t>(lane) < parts) ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(lane));
+    if (__ldcg(P.req_of + tok) != j1.x) return;  // (refused)
+    float m = ml.x;
+    for (uint32_t i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(P.part_ml + 2 * slot(i)));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float den = 0.f, acc[E] = {};
 #pragma unroll 4
-    for (uint32_t c = c0; c <= c1; ++c) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(c));
-        const float f = fmaxf(tree_exp2(ml.x - m), 1.17549435e-38f);  // (see the raise)
-        den = fmaf(ml.y, f, den);
-        const float* src = P.part + slot(c) * HD + lane;
+    for (uint32_t i = 0; i < parts; ++i) {
+        if (i && i % 32 == 0)
+            ml = i + lane < parts ? __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(i + lane))
+                                  : make_float2(-1e30f, 0.f);
+        const float mi = __shfl_sync(0xffffffffu, ml.x, i % 32), li = __shfl_sync(0xffffffffu, ml.y, i % 32);
+        const float f = fmaxf(tree_exp2(mi - m), 1.17549435e-38f);  // (see the raise)
+        den = fmaf(li, f, den);
+        const float* src = P.part + slot(i) * HD + lane;
 #pragma unroll
         for (int j = 0; j < E; ++j) acc[j] = fmaf(__ldcg(src + 32 * j), f, acc[j]);
     }
@@ -1507,8 +1481,7 @@ int launch_tree_hd(TreeParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
     e = rule ? cudaLaunchKernelEx(&cfg, slotkv_tree_attn_kernel<HD, true>, tmK, tmV, p)
              : cudaLaunchKernelEx(&cfg, slotkv_tree_attn_kernel<HD, false>, tmK, tmV, p);
     if (e != cudaSuccess) return static_cast<int>(e);
-    const uint64_t warps = static_cast<uint64_t>(p.n_tok) * p.n_head;
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.gridDim = dim3(tree_grid(sms), C::RB / (kJoinThreads / 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     return static_cast<int>(cudaLaunchKernelEx(&cfg, slotkv_tree_combine_kernel<HD>, p));

@@ -35,8 +35,7 @@ struct TreeParams {
                              // request's nodes are not written)
     float* part;             // workspace: partial results, two of a unit's rows per CTA [rows][hd]
     float* part_ml;          // and their (m, l)
-    uint64_t* base;          // workspace [4][n_req]: the requests' first tiles, by the size of the sets
-    uint32_t* plan;          // workspace [4][4]: of each size the tiles (64 bits), groups, first CTA
+    uint32_t* join;          // workspace [CTAs][kTreeJoin]: the unit that begins in a CTA and ends in another
     uint32_t* status;        // sticky SLOTKV_DEV_* flags
     uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
     uint32_t prep_heads;     // query heads of one warp of the prep kernel (the launcher's choice)
@@ -47,6 +46,10 @@ struct TreeParams {
     ScoreRule rule;          // doc_start: [n_req]
 };
 constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
+// A unit to join: its first node and row, rows (0: none), kv head, request, the step from one
+// of its CTAs to the next, and their number.
+constexpr uint32_t kTreeJoin = 8;
+enum TreeJoinWord { kJoinTok, kJoinRow0, kJoinRows, kJoinKvHead, kJoinReq, kJoinStep, kJoinParts };
 
 // Rows of a block (a unit of work), and the keys and dims of a piece of V.
 __host__ __device__ constexpr uint32_t tree_rows(int hd) { return hd == 256 ? 32u : 64u; }
