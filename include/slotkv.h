@@ -521,7 +521,7 @@ int slot_kv_extend_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
  *
  * Skipped with SLOTKV_DEV_RANGE, nothing of them written: a request with
  * nodes whose slot is >= n_slots, whose past[r] + n passes slot_ctx (bt_stride
- * * block_size), one of whose used table entries is >= n_blocks, with more than
+ * * block_size, or 2^31 - 256 where that is less), one of whose used table entries is >= n_blocks, with more than
  * SLOTKV_MAX_TREE nodes, with starts that decrease or pass n_tok, or with a
  * parent that is neither below its node nor 0xFFFFFFFF.  Keys that a row does
  * not attend never affect it, whatever they hold (another branch's or another

@@ -18,6 +18,7 @@ namespace {
 constexpr uint32_t kRange = 1u;  // SLOTKV_DEV_RANGE
 constexpr int kCopyThreads = 256;
 constexpr uint32_t kBatch = 8;   // 16-byte pieces a thread has in flight
+constexpr uint32_t kMaxPlaces = 0x7FFFFF00u;  // places of a request (a table may name more)
 
 __device__ __forceinline__ void begin_dependent() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -31,7 +32,7 @@ __device__ __forceinline__ uint32_t blocks_of(uint32_t keys, uint32_t block) {
 // n float4s from src to dst, by the threads i0, i0 + step, ...; the ranges do
 // not overlap.
 __device__ __forceinline__ void copy_float4(const float4* __restrict__ src,
-                                            float4* __restrict__ dst, uint32_t n, uint32_t i0,
+                                            float4* __restrict__ dst, uint64_t n, uint32_t i0,
                                             uint32_t step) {
     for (uint64_t i = i0; i < n; i += static_cast<uint64_t>(kBatch) * step) {
         float4 x[kBatch];
@@ -61,7 +62,8 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_keep_path_kernel(const Ke
     const uint32_t s0 = __ldg(P.starts + r), s1 = __ldg(P.starts + r + 1);
     const uint32_t n = __ldg(P.n_keep + r), past = __ldg(P.past + r);
     if (n == 0) return;
-    const uint64_t limit = P.slots ? P.pool.block : static_cast<uint64_t>(P.bt_stride) * P.pool.block;
+    uint64_t limit = P.slots ? P.pool.block : static_cast<uint64_t>(P.bt_stride) * P.pool.block;
+    limit = limit < kMaxPlaces ? limit : kMaxPlaces;
     bool ok = s0 <= s1 && s1 <= P.n_tok && s1 - s0 <= kMaxTree && n <= s1 - s0 &&
               static_cast<uint64_t>(past) + (s1 - s0) <= limit;
     const uint32_t slot = P.slots ? __ldg(P.slots + r) : 0u;
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_fork_tables_kernel(const 
             }
             if (good && id != old) {
                 const size_t block4 = static_cast<size_t>(P.pool.block) * (P.pool.kv_dim / 4);
-                const uint32_t n = rest * (P.pool.kv_dim / 4);
+                const uint64_t n = static_cast<uint64_t>(rest) * (P.pool.kv_dim / 4);
                 const uint32_t t = blockIdx.y * kCopyThreads + threadIdx.x;
                 const uint32_t step = gridDim.y * kCopyThreads;
                 copy_float4(reinterpret_cast<const float4*>(P.pool.K) + old * block4,
@@ -615,16 +617,16 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_compact_move_kernel(const
     begin_dependent();
     const CompactScratch S = compact_scratch(P.scratch, P.pool.n_blocks);
     const uint32_t moves = __ldcg(S.counts + 1), L = __ldcg(S.counts);
-    const uint32_t n4 = P.pool.block * (P.pool.kv_dim / 4);
+    const uint64_t n4 = static_cast<uint64_t>(P.pool.block) * (P.pool.kv_dim / 4);
     const uint64_t work = static_cast<uint64_t>(moves) * parts;
     for (uint64_t i = blockIdx.x; i < work; i += gridDim.x) {
         const uint32_t k = static_cast<uint32_t>(i / parts), part = static_cast<uint32_t>(i % parts);
         const uint32_t src = __ldcg(S.movers + k), dst = __ldcg(S.holes + k);
         const uint32_t t = part * kCopyThreads + threadIdx.x, step = parts * kCopyThreads;
-        copy_float4(reinterpret_cast<const float4*>(P.pool.K) + static_cast<size_t>(src) * n4,
-                    reinterpret_cast<float4*>(P.pool.K) + static_cast<size_t>(dst) * n4, n4, t, step);
-        copy_float4(reinterpret_cast<const float4*>(P.pool.V) + static_cast<size_t>(src) * n4,
-                    reinterpret_cast<float4*>(P.pool.V) + static_cast<size_t>(dst) * n4, n4, t, step);
+        copy_float4(reinterpret_cast<const float4*>(P.pool.K) + src * n4,
+                    reinterpret_cast<float4*>(P.pool.K) + dst * n4, n4, t, step);
+        copy_float4(reinterpret_cast<const float4*>(P.pool.V) + src * n4,
+                    reinterpret_cast<float4*>(P.pool.V) + dst * n4, n4, t, step);
         if (P.shares && part == 0 && threadIdx.x == 0) {
             P.shares[dst] = P.shares[src];
             P.shares[src] = 0;
@@ -675,11 +677,11 @@ int launch_keep_path(const KeepPathParams& p, cudaStream_t stream) {
 
 int launch_fork_tables(const ForkTablesParams& p, uint32_t sms, cudaStream_t stream) {
     // enough parts for few forks to fill the GPU, none smaller than one batch of every thread
-    const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
+    const uint64_t most = (static_cast<uint64_t>(p.pool.block) * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
                           (kBatch * kCopyThreads);
     const uint32_t forks = p.n_fork ? p.n_fork : 1u;
     uint32_t parts = (4 * sms + forks - 1) / forks;
-    parts = parts < most ? parts : most;
+    parts = parts < most ? parts : static_cast<uint32_t>(most);
     parts = parts < 64u ? parts : 64u;
     return launch_dependent(slotkv_fork_tables_kernel, dim3(forks, parts ? parts : 1u), kCopyThreads,
                             0, stream, p);
@@ -714,9 +716,9 @@ int launch_compact_pool(const CompactPoolParams& p, uint32_t sms, cudaStream_t s
         rc = launch_dependent(slotkv_compact_plan_kernel, dim3(ctas), kListThreads, ctas, stream, p);
     }
     if (rc != 0) return rc;
-    const uint32_t most = (p.pool.block * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
+    const uint64_t most = (static_cast<uint64_t>(p.pool.block) * (p.pool.kv_dim / 4) + kBatch * kCopyThreads - 1) /
                           (kBatch * kCopyThreads);
-    const uint32_t parts = most < 8u ? most : 8u;
+    const uint32_t parts = most < 8u ? static_cast<uint32_t>(most) : 8u;
     return launch_dependent(slotkv_compact_move_kernel, dim3(4 * sms), kCopyThreads, 0, stream, p, parts);
 }
 

@@ -62,7 +62,8 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, uint32_t r)
     q.s0 = __ldg(P.starts + r);
     q.past = __ldg(P.past + r);
     q.n = s1 - q.s0;
-    const uint64_t cap = P.block_tables ? static_cast<uint64_t>(P.bt_stride) * P.slot_ctx : P.slot_ctx;
+    uint64_t cap = P.block_tables ? static_cast<uint64_t>(P.bt_stride) * P.slot_ctx : P.slot_ctx;
+    cap = cap < kTreePlaces ? cap : kTreePlaces;
     q.ok = q.s0 <= s1 && s1 <= P.n_tok && q.n <= kTreeNodes && static_cast<uint64_t>(q.past) + q.n <= cap;
     if (!P.block_tables) q.ok = q.ok && __ldg(P.slots + r) < P.n_slots;
     return q;

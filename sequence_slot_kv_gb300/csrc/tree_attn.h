@@ -46,6 +46,8 @@ struct TreeParams {
     ScoreRule rule;          // doc_start: [n_req]
 };
 constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
+// Places of a request that 32-bit arithmetic on them leaves room for (a table may name more).
+constexpr uint32_t kTreePlaces = 0x7FFFFF00u;
 // A unit to join: its first node and row, rows (0: none), kv head, request, the step from one
 // of its CTAs to the next, and their number.
 constexpr uint32_t kTreeJoin = 8;

@@ -232,6 +232,27 @@ def test_requests_out_of_range(block, kind):
     kv.free()
 
 
+@pytest.mark.parametrize("past", [2**32 - 4, 2**32 - 2, 2**31 - 256, 2**31])
+def test_places_past_32_bits_are_refused(past):
+    """A table may name more places than 32 bits count; a request there is refused
+    (its places' sum must not wrap), the other one is served."""
+    c = Case([(5, [-1, 0, 1, 1]), (9, [-1, 0])], 1, 1, 64, block=64)
+    K0, V0 = c.K.clone(), c.V.clone()
+    wide = torch.zeros(2, 2**26 + 3, dtype=torch.int32, device="cuda")
+    wide[:, :c.tables.shape[1]] = c.tables
+    c.tables = wide
+    c.past[0] = past if past < 2**31 else past - 2**32
+    kv = c.handle()
+    c.run(kv)
+    c.check(K0, V0, skip={0})
+    assert kv.get_status() == skv.DEV_RANGE
+    want = c.K.clone()
+    kv.keep_path_paged(c.tables, c.past, c.starts, i32([2, 1]), i32([0, 3, 0, 0, 0, 0]))
+    assert kv.get_status() == skv.DEV_RANGE
+    assert torch.equal(c.K, want)
+    kv.free()
+
+
 def test_more_nodes_than_a_tree_may_have():
     c = Case([(5, list(range(-1, 256))), (9, [-1, 0])], 1, 1, 64)
     K0, V0 = c.K.clone(), c.V.clone()
