@@ -43,7 +43,11 @@ __device__ __forceinline__ uint32_t tree_place(const TreeParams& P, uint32_t r, 
 // workspace, k' and v into the node's cache row, with the decode kernel's
 // vector routines (so the same bits as a decode step's at that position).  A
 // call is bound by its dependent loads here; a warp's first rows are on their
-// way while the tree is looked at.
+// way while the tree is looked at.  A warp's heads come one after the other (0.4 us
+// each, 1.6 at head dim 256), so it has as few as keep the grid at kPrepCtas CTAs an SM:
+// 14 nodes of 8 heads 21.0 -> 19.4 us against 8 heads a warp, 27 nodes of 8 heads of
+// 256 137 -> 132 (whole calls); calls too large for that keep 8, whose angles, table
+// and tree are looked at once for all of them (620 nodes of 32 heads: 14 us, cold).
 constexpr int kPrepHeads = 8, kPrepCtas = 4, kPrepThreads = 128, kPrepWarps = kPrepThreads / 32;
 
 __device__ __forceinline__ void tree_cp_async16(void* smem_dst, const void* gmem_src) {
@@ -251,9 +255,9 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 //         of 8 rows.  Q rows into shared memory at a unit's start; then per tile S
 //         from tensor memory, the rule and the masks, P^T (hi, lo) into shared
 //         memory, the rows' sums in registers.  The running maxima are raised
-//         lazily (by 2^8), the 128 threads agreeing at a named barrier.  (The MMAs
-//         take most of what shared memory gives, so these loads and stores have
-//         long latencies, which more warps hide.)
+//         lazily (by 2^8), the 128 threads agreeing at a named barrier.  (Beside the
+//         MMAs shared memory answers after 200 cycles and more, which more warps
+//         hide.)
 //   4     accumulators: a thread per dim.  Every tile's O^T starts anew in
 //         tensor memory (its chain of sums is cut toward zero at each step) and
 //         is added to registers with rounded adds.  At the end out, or the
@@ -262,10 +266,13 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 //   7     producer (16 KB pieces of K, 128 keys x 32 dims, swizzled, and of V by TMA
 //         into a ring), two MMA issuers, and a warp that finds the CTA's units and
 //         tells the others.
-// The pieces go K(0), K(1), V(0), K(2), V(1), ...: S(t + 1) is formed while the
-// softmax of tile t runs.  P is handed over by blocks of 32 keys (a warp of each
-// softmax warpgroup writes one), so tile t + 1's first blocks are written while
-// the MMAs read tile t's last ones.  A unit's tiles go from its last keys to its first, so
+// The pieces go K(0), K(1), V(0), K(2), V(1), ... through the ring and through four
+// buffers of tensor memory: S(t + 1) is formed while the softmax of tile t runs.
+// (With two buffers for K's pieces and two for V's a converting warpgroup waited for
+// the MMAs after every piece: 32 requests of 64 nodes took 2.64 ms, now 2.22.)
+// P is handed over by blocks of 32 keys (a warp of each softmax warpgroup
+// writes one), so tile t + 1's first blocks are written while the MMAs read
+// tile t's last ones. A unit's tiles go from its last keys to its first, so
 // that a distance bias raises no maximum tile after tile.
 //
 // A request's row blocks all read the same keys, so they are given out in sets of
@@ -276,6 +283,18 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // (tree_plan; every CTA finds its own range from the lengths).  So a unit may lie
 // in several CTAs; each leaves (m, l, O) then, and slotkv_tree_combine_kernel
 // joins them in the groups' order.
+//
+// What bounds it.  24 requests of 4000 keys, 8 kv heads of 128: 8 rows a kv head in
+// 147 us, 5.4 TB/s (HBM, at 79 % of what a copy has with all of the call's three
+// kernels counted); 64 rows 166; 128 rows 274; 256 rows 517, 512 rows 1035: 3.2 us for a
+// tile of 64 rows and 128 keys, 6200 cycles, of which the MMAs alone take 3450 (they
+// are active 53 % of the time).  The rest is the converters, 80 % busy with latencies
+// (shared memory that the MMAs, TMA, P and they share, tensor memory, barriers), in
+// issue slots that are 62 % used; what waits on them fills the other roles' time.
+// 256 rows read 838 MB from HBM, K and V once (3.2 GB without the sets above).
+// Code size counts: the roles run different code side by side, and what does not fit the
+// instruction caches is fetched again every tile (the producer's loop unrolled costs
+// 5 to 15 %).
 //
 // Keys past the request's last are zeros in V; a masked key's P is -0.  A V value
 // that is not finite is a 0 to the tensor core, and the accumulators add it to
@@ -450,7 +469,8 @@ struct TreeWalk {
         const uint32_t unit = static_cast<uint32_t>(divide(off, x.tl)), sets = tree_sets(x.nb, k);
         const uint32_t t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
         const uint32_t n = left < x.tl - t0 ? static_cast<uint32_t>(left) : x.tl - t0;
-        const uint32_t row0 = (tree_set_block(x.nb, k) + (unit % sets << k) + member) * RB, all = x.q.n * (P.n_head / P.n_kv_head) - row0;
+        const uint32_t row0 = (tree_set_block(x.nb, k) + (unit % sets << k) + member) * RB;
+        const uint32_t all = x.q.n * (P.n_head / P.n_kv_head) - row0;
         d[kReq] = r;
         d[kRow] = x.q.s0;
         d[kNodes] = x.q.n;
@@ -489,7 +509,10 @@ __device__ __forceinline__ float tree_exp2(float x) {
 }
 __device__ __forceinline__ uint4 lds4(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 // A word of shared memory at addr + at.
@@ -807,7 +830,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     if (u && left == d[kTiles]) ok = warp_wait(UE, (u - 1) & 1) && ok;
                 }
                 // P^T: [32-key blocks][hi rows | lo rows][128 B], 16-byte pieces swizzled by the row
-                const uint32_t dst = sbase + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
+                const uint32_t dst = sbase + C::OFF_P + wq * (2 * Rp * 128) + 8 * sg * 128 + (lane >> 2) * 16 +
+                                     (lane & 3) * 4;
                 const uint32_t dst2 = dst + Rp * 128;
 #pragma unroll
                 for (int c = 0; c < CW; c += 2) {
@@ -888,7 +912,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     if (misc[4 + 4 * (gt & 1) + kb] != gt + 1) continue;
                     const uint32_t k0 = place + 32 * kb, end = d[kPast] + d[kNodes];
                     for (uint32_t k = 0; k < 32 && k0 + k < end; ++k) {
-                        const size_t at = (static_cast<size_t>(tree_place(P, d[kReq], k0 + k)) * P.n_kv_head + d[kKvHead]) * HD;
+                        const size_t key = tree_place(P, d[kReq], k0 + k);
+                        const size_t at = (key * P.n_kv_head + d[kKvHead]) * HD;
 #pragma unroll
                         for (int h = 0; h < C::DH; ++h) {
                             const float v = P.V[at + h * C::VD + me];
@@ -1386,6 +1411,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // ------------------------------------------------------------------ combine
 // The units that lie in several CTAs, of which there is one at most that begins in
 // a CTA: its partial results in the CTAs' order, a warp per row.
+//   m = max_i m_i,  out = sum_i O_i 2^(m_i - m) / (sum_i l_i 2^(m_i - m) + e^sink 2^-m)
+// Three dependent loads and at most 2 x 152 x 64 rows; a warp for each of the call's
+// rows, most of which have nothing to join, took 10 us more for 20 thousand rows.
 constexpr int kJoinThreads = 256;
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const TreeParams P) {
@@ -1461,8 +1489,7 @@ int launch_tree_hd(TreeParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // parts: about one item per warp for requests of the mean size; a warp's heads come one
-    // after the other, so as few as leave no SM more than kPrepCtas CTAs
+    // parts: about one item per warp for requests of the mean size
     const uint64_t mean = (p.n_tok + p.n_req - 1) / p.n_req;
     uint64_t parts = 0;
     for (p.prep_heads = 1;; p.prep_heads *= 2) {
