@@ -1455,10 +1455,11 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     if (((uintptr_t)starts | (uintptr_t)parents | (uintptr_t)sinks) & 3)
         return fail(SLOTKV_ERR_ARG, "tensor pointers must be 4-byte aligned");
     slotkv::TreeParams P;
-    const size_t R = h->max_rows, joins = slotkv::kTreeJoin * (size_t)slotkv::tree_grid(sm_total(h));
+    const size_t R = h->max_rows, ctas = slotkv::tree_grid(sm_total(h));
+    const size_t plans = slotkv::kTreePlan * ctas, joins = slotkv::kTreeJoin * ctas;
     int rc = first_use(&h->sc_q, R * h->max_n_head * h->head_dim, s, "tree workspace (q)");
     if (rc == SLOTKV_OK)
-        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), joins + R * (2 + slotkv::kTreeWords), s,
+        rc = first_use(reinterpret_cast<float**>(&h->tree_idx), plans + joins + R * (2 + slotkv::kTreeWords), s,
                        "tree workspace (nodes)");
     const size_t pr = slotkv::tree_partial_rows((int)h->head_dim, sm_total(h));
     if (rc == SLOTKV_OK)
@@ -1481,7 +1482,9 @@ static int tree_call(slotkv_t h, uint32_t n_req, uint32_t n_tok, uint32_t n_head
     P.K = h->K;
     P.V = h->V;
     P.q_rot = h->sc_q;
-    P.join = h->tree_idx;  // (read 16 bytes at a time)
+    P.ctas = (uint32_t)ctas;
+    P.plan = h->tree_idx;  // (read 16 bytes at a time, as the units to join)
+    P.join = P.plan + plans;
     P.below = P.join + joins;
     P.req_of = P.below + R * slotkv::kTreeWords;
     P.part = h->tree_part;

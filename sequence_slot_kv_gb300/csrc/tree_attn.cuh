@@ -33,7 +33,8 @@ __device__ __forceinline__ uint32_t tree_place(const TreeParams& P, uint32_t r, 
 }
 
 // ------------------------------------------------------------------ prep
-// CTA (request, part).  Every part checks the request and finds its nodes' depths
+// CTA (request, part), behind a column of CTAs whose first ones plan the attention
+// kernel's work (tree_plan_ctas).  Every part checks the request and finds its nodes' depths
 // by pointer doubling over the tree in shared memory (a round adds to a node's
 // depth that of the node it points at and doubles the distance, so a chain of
 // 256 takes 8 rounds).  Part 0 does the same with the sets of ancestors and
@@ -73,6 +74,274 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& P, uint32_t r)
     return q;
 }
 
+// ------------------------------------------------------------------ units
+// What a role reads of a unit (or the part of it that the CTA has), in words of
+// shared memory.  Tiles go from the last keys to the first: tile t of the part
+// begins at place d[kPlace] - 128 t.
+enum TreeWord { kReq, kRow, kNodes, kPast, kKvHead, kRow0, kRows, kPlace, kTiles, kStart, kWhole, kMore };
+
+// The sets of 1 << k blocks of a request of nb, and the first block of the first.
+constexpr int kSetSizes = 4;
+__device__ __forceinline__ uint32_t tree_sets(uint32_t nb, int k) {
+    return k == kSetSizes - 1 ? nb >> k : nb >> k & 1u;
+}
+__device__ __forceinline__ uint32_t tree_set_block(uint32_t nb, int k) {
+    return k == kSetSizes - 1 ? 0u : nb & ~((2u << k) - 1u);
+}
+// A request's shape: row blocks, first tile, tiles; 0 blocks: nothing to do.
+struct TreeShape {
+    TreeReq q;
+    uint32_t nb, tile0, tl;
+    // tiles of its sets of 1 << k blocks
+    __device__ uint64_t tiles(uint32_t n_kv_head, int k) const {
+        return static_cast<uint64_t>(tree_sets(nb, k)) * tl * n_kv_head;
+    }
+};
+template <int RB>
+__device__ __forceinline__ TreeShape tree_shape(const TreeParams& P, uint32_t r) {
+    TreeShape x;
+    x.q = tree_request(P, r);
+    x.nb = x.tile0 = x.tl = 0;
+    if (!x.q.ok || x.q.n == 0) return x;
+    const uint32_t last = x.q.past + x.q.n - 1, lo = rule_first(P.rule, r, x.q.past);
+    x.nb = (x.q.n * (P.n_head / P.n_kv_head) + RB - 1) / RB;
+    x.tile0 = (lo < last ? lo : last) / 128;
+    x.tl = last / 128 - x.tile0 + 1;
+    return x;
+}
+
+// The tiles of the sets of each size (one row block's), the groups of CTAs that
+// share them, and the first CTA of the groups.
+struct TreePlan {
+    uint64_t total[kSetSizes];
+    uint32_t groups[kSetSizes], first[kSetSizes];
+};
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {  // (of 32 bits where they do)
+    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+// As many groups as fit, so that the longest range is as short as may be.
+__device__ __forceinline__ void tree_plan(TreePlan& p, uint32_t ctas) {
+    uint64_t work = 0;
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) work += p.total[k] << k;
+    int left = static_cast<int>(ctas);
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) {
+        uint64_t g = p.total[k] ? divide(p.total[k] * ctas, work) : 0u;
+        g = g < p.total[k] ? g : p.total[k];
+        p.groups[k] = p.total[k] ? (g ? static_cast<uint32_t>(g) : 1u) : 0u;
+        left -= static_cast<int>(p.groups[k] << k);
+    }
+    for (;;) {
+        // the size with the longest ranges gets another group, or, where the groups of at
+        // least one are too many, the one with the shortest loses one
+        int best = -1;
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k) {
+            const bool can = left >= 0 ? (1 << k) <= left && p.groups[k] && p.groups[k] < p.total[k] : p.groups[k] > 1;
+            if (!can) continue;
+            if (best >= 0) {
+                uint64_t a = 0, b = 0;  // total[k] / groups[k] against the best one's
+#pragma unroll
+                for (int x = 0; x < kSetSizes; ++x)
+                    if (x == best) a = p.total[k] * p.groups[x], b = p.total[x] * p.groups[k];
+                if (left >= 0 ? a <= b : a >= b) continue;
+            }
+            best = k;
+        }
+        if (best < 0) break;
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k)
+            if (k == best) p.groups[k] += left >= 0 ? 1u : -1u;
+        left -= left >= 0 ? 1 << best : -(1 << best);
+    }
+    uint32_t at = 0;
+#pragma unroll
+    for (int k = 0; k < kSetSizes; ++k) {
+        p.first[k] = at;
+        at += p.groups[k] << k;
+    }
+}
+// Every group has each tiles, the first over groups one more; the group of tile x.
+__device__ __forceinline__ uint32_t tree_owner(uint64_t each, uint32_t over, uint64_t x) {
+    const uint64_t cut = over * (each + 1);
+    return static_cast<uint32_t>(x < cut ? divide(x, each + 1) : over + divide(x - cut, each));
+}
+
+// A CTA's parts of units, in order.
+template <int RB>
+struct TreeWalk {
+    int k;               // the sets' size, 1 << k, and the block of a set that is this CTA's
+    uint32_t member;
+    uint32_t r;
+    uint64_t off, left;  // tiles into request r, tiles left
+    TreeShape x;
+    bool known;
+    __device__ bool next(const TreeParams& P, uint32_t (&d)[12]) {
+        if (left == 0) return false;
+        for (;;) {
+            if (!known) {
+                if (r >= P.n_req) return false;
+                x = tree_shape<RB>(P, r);
+                known = true;
+            }
+            const uint64_t n = x.tiles(P.n_kv_head, k);
+            if (off < n) break;
+            off -= n;
+            ++r;
+            known = false;
+        }
+        const uint32_t unit = static_cast<uint32_t>(divide(off, x.tl)), sets = tree_sets(x.nb, k);
+        const uint32_t t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
+        const uint32_t n = left < x.tl - t0 ? static_cast<uint32_t>(left) : x.tl - t0;
+        const uint32_t row0 = (tree_set_block(x.nb, k) + (unit % sets << k) + member) * RB;
+        const uint32_t all = x.q.n * (P.n_head / P.n_kv_head) - row0;
+        d[kReq] = r;
+        d[kRow] = x.q.s0;
+        d[kNodes] = x.q.n;
+        d[kPast] = x.q.past;
+        d[kKvHead] = unit / sets;
+        d[kRow0] = row0;
+        d[kRows] = all < RB ? all : RB;
+        d[kPlace] = (x.tile0 + x.tl - 1 - t0) * 128;
+        d[kTiles] = n;
+        d[kStart] = t0 == 0 ? 1u : 0u;
+        d[kWhole] = n == x.tl ? 1u : 0u;
+        d[kMore] = 1u;
+        off += n;
+        left -= n;
+        return true;
+    }
+};
+
+// Where every CTA of the attention kernel begins, by the first CTAs of the prep kernel,
+// a thread per CTA: the totals of the sizes, the plan, then the requests' first tiles,
+// 128 requests at a time, among which a CTA finds its own.  (When each CTA of the
+// attention kernel did this for itself, its first unit was known 3 to 9 us after prep's
+// end: the code runs once, from cold instruction caches.)
+template <int RB>
+__device__ void tree_plan_ctas(const TreeParams& P) {
+    constexpr uint32_t NT = kPrepThreads, NW = NT / 32;
+    static_assert(NT == 128, "a power of two that the search halves");
+    __shared__ uint64_t begin[kSetSizes][NT];  // the requests' first tiles
+    __shared__ uint64_t sums[kSetSizes][NW], totals[kSetSizes], each[kSetSizes];
+    __shared__ uint32_t over[kSetSizes], groups[kSetSizes], first_cta[kSetSizes];
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const TreeShape first = tid < P.n_req ? tree_shape<RB>(P, tid) : TreeShape{};
+    // (loops over the sizes stay loops where they can: this code runs once, from cold
+    // instruction caches)
+#pragma unroll 1
+    for (int k = 0; k < kSetSizes; ++k) {
+        uint64_t all = first.tiles(P.n_kv_head, k);
+        for (uint32_t r = tid + NT; r < P.n_req; r += NT) all += tree_shape<RB>(P, r).tiles(P.n_kv_head, k);
+        if (__any_sync(0xffffffffu, all != 0))
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (lane == 0) sums[k][warp] = all;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        TreePlan plan;
+#pragma unroll
+        for (int k = 0; k < kSetSizes; ++k) {
+            plan.total[k] = 0;
+#pragma unroll
+            for (uint32_t w = 0; w < NW; ++w) plan.total[k] += sums[k][w];
+        }
+        tree_plan(plan, P.ctas);
+        uint64_t t = 0;
+        uint32_t g = 0, f = 0;  // this lane's size
+#pragma unroll
+        for (uint32_t k = 0; k < kSetSizes; ++k)
+            if (lane == k) t = plan.total[k], g = plan.groups[k], f = plan.first[k];
+        const uint64_t q = divide(t, g ? g : 1u);
+        if (lane < kSetSizes) {
+            totals[lane] = t;
+            each[lane] = q;
+            over[lane] = static_cast<uint32_t>(t - q * g);
+            groups[lane] = g;
+            first_cta[lane] = f;
+        }
+    }
+    __syncthreads();
+    for (uint32_t c0 = blockIdx.y * NT; c0 < P.ctas; c0 += gridDim.y * NT) {
+        const uint32_t cta = c0 + tid;
+        TreeWalk<RB> walk;
+        walk.known = false;
+        walk.k = 0;
+        walk.r = walk.member = 0;
+        walk.off = walk.left = 0;
+        uint64_t u0 = 0;
+#pragma unroll 1
+        for (int k = 0; k < kSetSizes; ++k) {
+            const uint32_t c = cta - first_cta[k], group = c >> k;
+            if (cta >= P.ctas || cta < first_cta[k] || group >= groups[k]) continue;
+            walk.k = k;
+            walk.member = c & ((1u << k) - 1u);
+            u0 = group * each[k] + min(group, over[k]);
+            walk.left = each[k] + (group < over[k] ? 1u : 0u);
+        }
+        const uint64_t u1 = u0 + walk.left;
+        bool found = walk.left == 0;
+        uint64_t at = 0;  // of this CTA's size, up to this 128 requests
+        for (uint32_t r0 = 0; r0 < P.n_req; r0 += NT) {
+            const uint32_t r = r0 + tid;
+            const TreeShape x = !r0 ? first : r < P.n_req ? tree_shape<RB>(P, r) : TreeShape{};
+            __syncthreads();  // (the last ones have been searched)
+#pragma unroll 1
+            for (int k = 0; k < kSetSizes; ++k) {
+                if (totals[k] == 0) continue;
+                const uint64_t n = x.tiles(P.n_kv_head, k);
+                uint64_t incl = n;
+#pragma unroll
+                for (uint32_t o = 1; o < 32; o <<= 1) {
+                    const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                begin[k][tid] = incl - n;  // in the warp
+                if (lane == 31) sums[k][warp] = incl;
+            }
+            __syncthreads();
+            // the warp that this CTA's first tile is in, and the request there
+            uint64_t before = at;
+            uint32_t w = 0;
+            for (; w < NW && !found; ++w) {
+                if (u0 < before + sums[walk.k][w]) break;
+                before += sums[walk.k][w];
+            }
+            if (!found && w < NW) {
+                uint32_t i = 32 * w;  // the last one that begins there or before
+#pragma unroll
+                for (uint32_t o = 16; o > 0; o >>= 1)
+                    if (before + begin[walk.k][i + o] <= u0) i += o;
+                walk.r = r0 + i;
+                walk.off = u0 - before - begin[walk.k][i];
+                found = true;
+            }
+            at = before;
+            if (__syncthreads_and(found)) break;
+        }
+        if (cta >= P.ctas) continue;
+        uint32_t d[12] = {};
+        uint32_t* to = P.plan + kTreePlan * static_cast<size_t>(cta);
+        d[kMore] = walk.next(P, d) ? 1u : 0u;
+#pragma unroll
+        for (int i = 0; i < 12; ++i) to[i] = d[i];
+        to[kPlanUnitTiles] = d[kMore] ? walk.x.tl : 0u;
+        to[kPlanSize] = walk.k;
+        to[kPlanMember] = walk.member;
+        to[kPlanReq] = walk.r;
+        to[kPlanOver] = over[walk.k];
+        const uint64_t wide[4] = {walk.off, walk.left, u1, each[walk.k]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            to[kPlanOff + 2 * i] = static_cast<uint32_t>(wide[i]);
+            to[kPlanOff + 2 * i + 1] = static_cast<uint32_t>(wide[i] >> 32);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ prep kernel
 template <int HD>
 __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const TreeParams P) {
     extern __shared__ __align__(16) uint8_t prep_smem[];
@@ -81,7 +350,11 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t r = blockIdx.x;
+    if (blockIdx.x == 0) {
+        if (blockIdx.y * kPrepThreads < P.ctas) tree_plan_ctas<static_cast<int>(tree_rows(HD))>(P);
+        return;
+    }
+    const uint32_t r = blockIdx.x - 1;
     const bool sets = blockIdx.y == 0;
     const TreeReq q = tree_request(P, r);
     if (q.n == 0) return;
@@ -264,8 +537,8 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 //         unit's partial result.
 //   5, 6  converters, a piece each by turns: K and V^T (hi, lo) into tensor memory.
 //   7     producer (16 KB pieces of K, 128 keys x 32 dims, swizzled, and of V by TMA
-//         into a ring), two MMA issuers, and a warp that finds the CTA's units and
-//         tells the others.
+//         into a ring), two MMA issuers, and a warp that goes through the CTA's
+//         units from there on and tells the others.
 // The pieces go K(0), K(1), V(0), K(2), V(1), ... through the ring and through four
 // buffers of tensor memory: S(t + 1) is formed while the softmax of tile t runs.
 // (With two buffers for K's pieces and two for V's a converting warpgroup waited for
@@ -280,7 +553,7 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // the blocks of a set side by side, tile for tile, and the keys come from memory
 // once for all of them.  The tiles of all sets of one size, in order, are cut into
 // one equal range per group, the CTAs divided among the sizes by their work
-// (tree_plan; every CTA finds its own range from the lengths).  So a unit may lie
+// (tree_plan; the prep kernel finds where each CTA begins).  So a unit may lie
 // in several CTAs; each leaves (m, l, O) then, and slotkv_tree_combine_kernel
 // joins them in the groups' order.
 //
@@ -347,147 +620,6 @@ constexpr int kTreeWarps = 32, kTreeThreads = 32 * kTreeWarps;
 constexpr int kTreeRegs = 64, kRegAcc = 112, kRegConv = 48, kRegAux = 48;
 static_assert(4 * kTreeRegs + kRegAcc + 2 * kRegConv + kRegAux == kTreeWarps / 4 * kTreeRegs,
               "register hand-over must add up to the launch's registers");
-
-// What a role reads of a unit (or the part of it that the CTA has), in words of
-// shared memory.  Tiles go from the last keys to the first: tile t of the part
-// begins at place d[kPlace] - 128 t.
-enum TreeWord { kReq, kRow, kNodes, kPast, kKvHead, kRow0, kRows, kPlace, kTiles, kStart, kWhole, kMore };
-
-// The sets of 1 << k blocks of a request of nb, and the first block of the first.
-constexpr int kSetSizes = 4;
-__device__ __forceinline__ uint32_t tree_sets(uint32_t nb, int k) {
-    return k == kSetSizes - 1 ? nb >> k : nb >> k & 1u;
-}
-__device__ __forceinline__ uint32_t tree_set_block(uint32_t nb, int k) {
-    return k == kSetSizes - 1 ? 0u : nb & ~((2u << k) - 1u);
-}
-// A request's shape: row blocks, first tile, tiles; 0 blocks: nothing to do.
-struct TreeShape {
-    TreeReq q;
-    uint32_t nb, tile0, tl;
-    // tiles of its sets of 1 << k blocks
-    __device__ uint64_t tiles(uint32_t n_kv_head, int k) const {
-        return static_cast<uint64_t>(tree_sets(nb, k)) * tl * n_kv_head;
-    }
-};
-template <int RB>
-__device__ __forceinline__ TreeShape tree_shape(const TreeParams& P, uint32_t r) {
-    TreeShape x;
-    x.q = tree_request(P, r);
-    x.nb = x.tile0 = x.tl = 0;
-    if (!x.q.ok || x.q.n == 0) return x;
-    const uint32_t last = x.q.past + x.q.n - 1, lo = rule_first(P.rule, r, x.q.past);
-    x.nb = (x.q.n * (P.n_head / P.n_kv_head) + RB - 1) / RB;
-    x.tile0 = (lo < last ? lo : last) / 128;
-    x.tl = last / 128 - x.tile0 + 1;
-    return x;
-}
-
-// The tiles of the sets of each size (one row block's), the groups of CTAs that
-// share them, and the first CTA of the groups.
-struct TreePlan {
-    uint64_t total[kSetSizes];
-    uint32_t groups[kSetSizes], first[kSetSizes];
-};
-__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {  // (of 32 bits where they do)
-    return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-}
-// As many groups as fit, so that the longest range is as short as may be.
-__device__ __forceinline__ void tree_plan(TreePlan& p, uint32_t ctas) {
-    uint64_t work = 0;
-#pragma unroll
-    for (int k = 0; k < kSetSizes; ++k) work += p.total[k] << k;
-    int left = static_cast<int>(ctas);
-#pragma unroll
-    for (int k = 0; k < kSetSizes; ++k) {
-        uint64_t g = p.total[k] ? divide(p.total[k] * ctas, work) : 0u;
-        g = g < p.total[k] ? g : p.total[k];
-        p.groups[k] = p.total[k] ? (g ? static_cast<uint32_t>(g) : 1u) : 0u;
-        left -= static_cast<int>(p.groups[k] << k);
-    }
-    for (;;) {
-        // the size with the longest ranges gets another group, or, where the groups of at
-        // least one are too many, the one with the shortest loses one
-        int best = -1;
-#pragma unroll
-        for (int k = 0; k < kSetSizes; ++k) {
-            const bool can = left >= 0 ? (1 << k) <= left && p.groups[k] && p.groups[k] < p.total[k] : p.groups[k] > 1;
-            if (!can) continue;
-            if (best >= 0) {
-                uint64_t a = 0, b = 0;  // total[k] / groups[k] against the best one's
-#pragma unroll
-                for (int x = 0; x < kSetSizes; ++x)
-                    if (x == best) a = p.total[k] * p.groups[x], b = p.total[x] * p.groups[k];
-                if (left >= 0 ? a <= b : a >= b) continue;
-            }
-            best = k;
-        }
-        if (best < 0) break;
-#pragma unroll
-        for (int k = 0; k < kSetSizes; ++k)
-            if (k == best) p.groups[k] += left >= 0 ? 1u : -1u;
-        left -= left >= 0 ? 1 << best : -(1 << best);
-    }
-    uint32_t at = 0;
-#pragma unroll
-    for (int k = 0; k < kSetSizes; ++k) {
-        p.first[k] = at;
-        at += p.groups[k] << k;
-    }
-}
-// The first tile of group c of n, and the group of tile x.
-__device__ __forceinline__ uint64_t tree_first(uint64_t total, uint32_t n, uint32_t c) {
-    return divide(total * c, n);
-}
-__device__ __forceinline__ uint32_t tree_owner(uint64_t total, uint32_t n, uint64_t x) {
-    return static_cast<uint32_t>(divide((x + 1) * n - 1, total));
-}
-
-// A CTA's parts of units, in order.
-template <int RB>
-struct TreeWalk {
-    int k;               // the sets' size, 1 << k, and the block of a set that is this CTA's
-    uint32_t member;
-    uint32_t r;
-    uint64_t off, left;  // tiles into request r, tiles left
-    TreeShape x;
-    bool known;
-    __device__ bool next(const TreeParams& P, uint32_t (&d)[12]) {
-        if (left == 0) return false;
-        for (;;) {
-            if (!known) {
-                if (r >= P.n_req) return false;
-                x = tree_shape<RB>(P, r);
-                known = true;
-            }
-            const uint64_t n = x.tiles(P.n_kv_head, k);
-            if (off < n) break;
-            off -= n;
-            ++r;
-            known = false;
-        }
-        const uint32_t unit = static_cast<uint32_t>(divide(off, x.tl)), sets = tree_sets(x.nb, k);
-        const uint32_t t0 = static_cast<uint32_t>(off - static_cast<uint64_t>(unit) * x.tl);
-        const uint32_t n = left < x.tl - t0 ? static_cast<uint32_t>(left) : x.tl - t0;
-        const uint32_t row0 = (tree_set_block(x.nb, k) + (unit % sets << k) + member) * RB;
-        const uint32_t all = x.q.n * (P.n_head / P.n_kv_head) - row0;
-        d[kReq] = r;
-        d[kRow] = x.q.s0;
-        d[kNodes] = x.q.n;
-        d[kPast] = x.q.past;
-        d[kKvHead] = unit / sets;
-        d[kRow0] = row0;
-        d[kRows] = all < RB ? all : RB;
-        d[kPlace] = (x.tile0 + x.tl - 1 - t0) * 128;
-        d[kTiles] = n;
-        d[kStart] = t0 == 0 ? 1u : 0u;
-        d[kWhole] = n == x.tl ? 1u : 0u;
-        d[kMore] = 1u;
-        off += n;
-        left -= n;
-        return true;
-    }
-};
 
 __device__ __forceinline__ bool bar_or(int id, bool p) {
     uint32_t r;
@@ -1143,7 +1275,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == 28) {
         // ------------------------------------------------------------ producer
         regs_decrease<kRegAux>();
-        bool ok = true, waited = false;
+        grid_dependency_wait();
+        bool ok = true;
         uint32_t sl = 0, phase = 1, sent = 0;  // the slot, the parity of its being empty, pieces sent
         const uint32_t box = P.box_keys, lb = 31 - __clz(box), boxes = C::KT >> lb;
         const uint32_t vbox = min(box, static_cast<uint32_t>(C::VK)), vboxes = max(C::VK >> lb, 1);
@@ -1151,7 +1284,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             ok = known(u) && ok;
             const volatile uint32_t* d = words(u);
             if (!ok || !d[kMore]) break;
-            const uint32_t last = 2 * d[kTiles] - 1, x0 = d[kKvHead] * HD, end = d[kPast] + d[kNodes], past = d[kPast];
+            const uint32_t last = 2 * d[kTiles] - 1, x0 = d[kKvHead] * HD, end = d[kPast] + d[kNodes];
             const uint32_t r = d[kReq];
             uint32_t place = d[kPlace];
             // the row of this lane's box of the tile at p
@@ -1165,11 +1298,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (uint32_t i = 0; i <= last; ++i) {
                 const bool v = i == last || (i && !(i & 1));
                 if (!v) {
-                    // (tiles of history may be read while the prep kernel still runs)
-                    if (!waited && place + C::KT > past) {
-                        grid_dependency_wait();
-                        waited = true;
-                    }
                     yv = yk;
                     yk = next;
                     place -= C::KT;
@@ -1211,97 +1339,63 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == 31) {
         // ------------------------------------------------------------ units
         regs_decrease<kRegAux>();
-        // what there is to do, by the size of the sets, and this CTA's part of it
-        TreePlan plan;
-        const TreeShape first = lane < P.n_req ? tree_shape<RB>(P, lane) : TreeShape{};
+        // the prep kernel's plan says where this CTA's part begins
+        grid_dependency_wait();
+        const uint4* from = reinterpret_cast<const uint4*>(P.plan + kTreePlan * static_cast<size_t>(blockIdx.x));
+        uint32_t d[kTreePlan];
 #pragma unroll
-        for (int k = 0; k < kSetSizes; ++k) plan.total[k] = first.tiles(P.n_kv_head, k);
-#pragma unroll 2
-        for (uint32_t r = lane + 32; r < P.n_req; r += 32) {
-            const TreeShape x = tree_shape<RB>(P, r);
-#pragma unroll
-            for (int k = 0; k < kSetSizes; ++k) plan.total[k] += x.tiles(P.n_kv_head, k);
+        for (uint32_t i = 0; i < kTreePlan / 4; ++i) {
+            const uint4 x = __ldcg(from + i);
+            d[4 * i] = x.x;
+            d[4 * i + 1] = x.y;
+            d[4 * i + 2] = x.z;
+            d[4 * i + 3] = x.w;
         }
-#pragma unroll
-        for (int k = 0; k < kSetSizes; ++k)
-            if (__any_sync(0xffffffffu, plan.total[k] != 0))
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) plan.total[k] += __shfl_xor_sync(0xffffffffu, plan.total[k], o);
-        tree_plan(plan, gridDim.x);
+        auto wide = [&](int i) { return static_cast<uint64_t>(d[i + 1]) << 32 | d[i]; };
         TreeWalk<RB> walk;
         walk.known = false;
-        walk.k = 0;
-        walk.r = walk.member = 0;
-        walk.off = walk.left = 0;
-        uint64_t u0 = 0, u1 = 0;
-        uint32_t groups = 1;
-        uint64_t total = 1;
+        walk.k = static_cast<int>(d[kPlanSize]);
+        walk.member = d[kPlanMember];
+        walk.r = d[kPlanReq];
+        walk.off = wide(kPlanOff);
+        walk.left = wide(kPlanLeft);
+        const uint64_t u1 = wide(kPlanEnd), each = wide(kPlanEach);
+        const uint32_t over = d[kPlanOver];
+        uint32_t unit_tiles = d[kPlanUnitTiles], u[12];
 #pragma unroll
-        for (int k = 0; k < kSetSizes; ++k) {
-            const uint32_t c = blockIdx.x - plan.first[k];
-            if (blockIdx.x < plan.first[k] || c >> k >= plan.groups[k]) continue;
-            walk.k = k;
-            walk.member = c & ((1u << k) - 1u);
-            u0 = tree_first(plan.total[k], plan.groups[k], c >> k);
-            u1 = tree_first(plan.total[k], plan.groups[k], (c >> k) + 1);
-            walk.left = u1 - u0;
-            groups = plan.groups[k];
-            total = plan.total[k];
-        }
+        for (int i = 0; i < 12; ++i) u[i] = d[i];
         // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
         if (sbase & 1023u) {
-            walk.left = 0;
+            u[kMore] = 0u;
             if (lane == 0) atomicOr(P.status, kDevTimeout);
-        }
-        // the request that the part begins in
-        uint64_t at = 0;
-        for (uint32_t r0 = 0; walk.left && r0 < P.n_req; r0 += 32) {
-            const TreeShape x = !r0 ? first : r0 + lane < P.n_req ? tree_shape<RB>(P, r0 + lane) : TreeShape{};
-            const uint64_t n = x.tiles(P.n_kv_head, walk.k);
-            uint64_t incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const uint64_t begin = at + incl - n;
-            const uint32_t here = __ballot_sync(0xffffffffu, begin <= u0 && u0 < begin + n);
-            if (here) {
-                const int from = __ffs(here) - 1;
-                walk.r = r0 + from;
-                walk.off = u0 - __shfl_sync(0xffffffffu, begin, from);
-                break;
-            }
-            at += __shfl_sync(0xffffffffu, incl, 31);
         }
         // nothing for the combine kernel to join from here on, unless there turns out to be
         uint32_t* join = P.join + kTreeJoin * blockIdx.x;
         if (lane == 0) join[kJoinRows] = 0u;
-        for (uint32_t u = 0;; ++u) {
-            uint32_t d[12];
-            const bool more = walk.next(P, d);
-            if (!more) d[kMore] = 0u;
-            if (more && d[kStart] && !d[kWhole] && lane == 0) {  // (the CTA's last; ends in another one)
-                const uint64_t first_tile = u1 - d[kTiles], last_tile = first_tile + walk.x.tl - 1;
-                join[kJoinTok] = d[kRow];
-                join[kJoinRow0] = d[kRow0];
-                join[kJoinRows] = d[kRows];
-                join[kJoinKvHead] = d[kKvHead];
-                join[kJoinReq] = d[kReq];
-                join[kJoinStep] = 1u << walk.k;
-                join[kJoinParts] = tree_owner(total, groups, last_tile) - tree_owner(total, groups, first_tile) + 1;
-            }
-            if (u >= 2 && !warp_wait(GE + 8 * (u & 1), ((u >> 1) - 1) & 1)) break;
+        for (uint32_t n = 0;; ++n) {
+            if (n >= 2 && !warp_wait(GE + 8 * (n & 1), ((n >> 1) - 1) & 1)) break;
             if (lane == 0) {
-                volatile uint32_t* to = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_DESC) + 12 * (u & 1);
-                if (more)
+                volatile uint32_t* to = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_DESC) + 12 * (n & 1);
+                if (u[kMore])
 #pragma unroll
-                    for (int i = 0; i < 11; ++i) to[i] = d[i];
-                to[kMore] = d[kMore];
-                mbar_arrive(GF + 8 * (u & 1));
+                    for (int i = 0; i < 11; ++i) to[i] = u[i];
+                to[kMore] = u[kMore];
+                mbar_arrive(GF + 8 * (n & 1));
             }
             __syncwarp();
-            if (!more) break;
+            if (!u[kMore]) break;
+            if (u[kStart] && !u[kWhole] && lane == 0) {  // (the CTA's last; ends in another one)
+                const uint64_t first_tile = u1 - u[kTiles], last_tile = first_tile + unit_tiles - 1;
+                join[kJoinTok] = u[kRow];
+                join[kJoinRow0] = u[kRow0];
+                join[kJoinRows] = u[kRows];
+                join[kJoinKvHead] = u[kKvHead];
+                join[kJoinReq] = u[kReq];
+                join[kJoinStep] = 1u << walk.k;
+                join[kJoinParts] = tree_owner(each, over, last_tile) - tree_owner(each, over, first_tile) + 1;
+            }
+            if (!walk.next(P, u)) u[kMore] = 0u;
+            unit_tiles = walk.x.tl;
         }
     } else {
         // ------------------------------------------------------------ MMA issuers
@@ -1498,7 +1592,7 @@ int launch_tree_hd(TreeParams p, const CUtensorMap& tmK, const CUtensorMap& tmV,
         parts = (mean * groups + kPrepWarps - 1) / kPrepWarps;
         if (p.prep_heads == kPrepHeads || p.n_req * (1 + parts) <= static_cast<uint64_t>(kPrepCtas) * sms) break;
     }
-    cfg.gridDim = dim3(p.n_req, 1 + static_cast<unsigned>(parts < 256 ? parts : 256));
+    cfg.gridDim = dim3(p.n_req + 1, 1 + static_cast<unsigned>(parts < 256 ? parts : 256));
     cfg.blockDim = dim3(kPrepThreads);
     cfg.dynamicSmemBytes = kPrepWarps * 2 * ((p.prep_heads + 1) / 2) * HD * 4;
     if ((e = cudaLaunchKernelEx(&cfg, slotkv_tree_prep_kernel<HD>, p)) != cudaSuccess) return static_cast<int>(e);

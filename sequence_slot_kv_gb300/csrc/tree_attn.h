@@ -35,9 +35,11 @@ struct TreeParams {
                              // request's nodes are not written)
     float* part;             // workspace: partial results, two of a unit's rows per CTA [rows][hd]
     float* part_ml;          // and their (m, l)
+    uint32_t* plan;          // workspace [CTAs][kTreePlan]: where each CTA's part of the work begins
     uint32_t* join;          // workspace [CTAs][kTreeJoin]: the unit that begins in a CTA and ends in another
     uint32_t* status;        // sticky SLOTKV_DEV_* flags
     uint32_t n_slots, slot_ctx, bt_stride, n_head, n_kv_head, n_req, n_tok;
+    uint32_t ctas;           // of the attention kernel (tree_grid)
     uint32_t prep_heads;     // query heads of one warp of the prep kernel (the launcher's choice)
     uint32_t box_keys;       // keys of one TMA box of K: a power of two, at most 128
     float eps;
@@ -51,6 +53,13 @@ constexpr uint32_t kTreePlaces = 0x7FFFFF00u;
 // A unit to join: its first node and row, rows (0: none), kv head, request, the step from one
 // of its CTAs to the next, and their number.
 constexpr uint32_t kTreeJoin = 8;
+// A CTA's plan: what its roles need to know of its first unit (TreeWord) and that unit's
+// tiles, then where to go on: size of the sets, block of a set, request, groups of the size
+// with one tile more than the others; tiles into the request, tiles left, the part's end,
+// tiles of a group (64 bits each).
+constexpr uint32_t kTreePlan = 28;
+enum TreePlanWord { kPlanUnitTiles = 12, kPlanSize, kPlanMember, kPlanReq, kPlanOver, kPlanOff = 18, kPlanLeft = 20,
+                    kPlanEnd = 22, kPlanEach = 24 };
 enum TreeJoinWord { kJoinTok, kJoinRow0, kJoinRows, kJoinKvHead, kJoinReq, kJoinStep, kJoinParts };
 
 // Rows of a block (a unit of work), and the keys and dims of a piece of V.
