@@ -272,6 +272,31 @@ def test_many_requests(hd, block):
     go(Case([(p, tree(r, n, 3)) for p, n in lens], 2, 2, hd, block=block, seed=1, pad=1))
 
 
+def test_thousands_of_requests():
+    """More than the planning looks at at once, many times over, of one block of rows and of several."""
+    r = random.Random(2)
+    lens = [(r.choice([0, 3, 130]), r.choice([0, 0, 1, 1, 2, 70 if i % 500 == 0 else 1])) for i in range(2500)]
+    go(Case([(p, tree(r, n, 3)) for p, n in lens], 1, 2, 64, seed=4))
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_sums_do_not_shrink(hd):
+    """The tensor core cuts every sum toward zero; what that takes on average is put back, so
+    the outputs are not smaller than they should be by more than what the estimate leaves:
+    of O 2 of up to 4 units of 2^-23, half a unit each of both roundings, of S a unit per
+    e-fold of the scores here (log2 units up to 12 times 2^-24 ln 2): below 5e-7."""
+    r = random.Random(hd)
+    c = Case([(3000, tree(r, 20, 4)), (777, tree(r, 9, 2))], 2, 4, hd, seed=7)
+    c.K *= 3.0
+    K0, V0 = c.K.clone(), c.V.clone()
+    kv = c.handle()
+    c.run(kv)
+    want = torch.stack(c.check(K0, V0)).flatten()
+    got = c.out[:c.rows].double().flatten()
+    assert abs(float(((got - want) * want).sum() / want.pow(2).sum())) <= 5e-7
+    kv.free()
+
+
 @pytest.mark.parametrize("hd,block", [(64, 0), (128, 128), (256, 0)])
 def test_long_history(hd, block):
     """One request over many keys (split over the GPU), beside short ones."""
