@@ -636,8 +636,9 @@ int slot_kv_free_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
  * and the share counts follow (share counts from L on become 0).  The free
  * list becomes L .. n_blocks - 1 in order, its last entries, and head[0]
  * points at its first (a list of fewer entries takes the first ids and raises
- * SLOTKV_DEV_RANGE).  Every block in use has to be named in block_tables:
- * others count as free.  shares may be NULL.  A request with more blocks than
+ * SLOTKV_DEV_RANGE).  Every row that lives on has to be in block_tables, forks
+ * beside the rows they came from: a block that no row here names counts as
+ * free, and a table elsewhere keeps ids that have moved.  shares may be NULL.  A request with more blocks than
  * bt_stride counts with all its entries, an entry >= n_blocks is left as it
  * is; each raises SLOTKV_DEV_RANGE.  n_req * bt_stride <= 2^30.  The first
  * call allocates a workspace: make one before capturing into a graph.

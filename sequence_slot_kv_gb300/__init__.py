@@ -818,7 +818,9 @@ class SlotKV:
     def compact_pool(self, past, block_tables, shares, free_blocks, head, stream=None):
         """slot_kv_compact_pool: the blocks that block_tables' rows use moved to
         the ids 0 .. L - 1; K, V, tables, shares (or None), the free list and
-        head follow, all in place.  int32 CUDA tensors."""
+        head follow, all in place.  Every row that lives on has to be in
+        block_tables: a block that none of them names counts as free.  int32
+        CUDA tensors."""
         c, name = _compiled(), "slot_kv_compact_pool"
         if c and _done(c.slot_kv_compact_pool(self._h.value, self.n_slots, past, block_tables,
                                               shares, free_blocks, head, _stream_arg(stream)),
