@@ -615,7 +615,11 @@ int slot_kv_fork_tables(slotkv_t handle, uint32_t n_fork, const uint32_t* src, u
  * nobody left goes back on the free list.  The k-th of the F blocks that do,
  * in the order of their first entries given up (request by request), is
  * written to free_blocks[head[0] - F + k]; head_out receives head[0] - F.
- * The tables are left as they are.
+ * The tables are left as they are: a row that goes back into a block that
+ * others share (keep[r] no multiple of bs) still ends in it, and room in a
+ * block is not ownership, so such a row is not extended or written as it is.
+ * Fork it (slot_kv_fork_tables with past = keep: the keys in use of that block
+ * are copied into one of its own), free the old row, and go on with the fork.
  *   keep    device u32[n_req], or NULL: 0.
  *   shares  or NULL for a pool without shared blocks (every entry then goes
  *           back on the list).

@@ -796,7 +796,9 @@ class SlotKV:
         """slot_kv_free_tables: the blocks of block_tables' rows past their first
         keep[r] keys (None: all) given up; those that nobody shares go back to
         free_blocks, below head.  shares None: no block is shared.  head_out
-        None moves ``head`` itself.  int32 CUDA tensors."""
+        None moves ``head`` itself.  A row rolled back into a shared block has
+        to be forked (fork_tables with the new length) before it is written.
+        int32 CUDA tensors."""
         if head_out is None:
             head_out = head
         c, name = _compiled(), "slot_kv_free_tables"

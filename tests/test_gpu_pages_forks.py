@@ -1,4 +1,5 @@
-"""Forks beside the rows they came from, and compaction over all of them."""
+"""Forks beside the rows they came from: compaction over all of them, and a
+roll-back into a block that a fork shares."""
 import os
 import random
 import re
@@ -83,4 +84,41 @@ def test_the_readme_example_keeps_its_forks():
         assert all(torch.equal(got[i], got[0]) for i in (2, 3))
     assert kv.get_status() == 0
     check_pool(every, past, names["shares"], names["free_blocks"], names["head"], n, bs)
+    kv.free()
+
+
+@pytest.mark.parametrize("length", [1, 63, 64, 65, 128, 150, 200, 230])
+def test_a_row_rolled_back_into_a_shared_block_is_forked_first(length):
+    """A row that goes back into a block that another row shares gets a copy of it
+    by a fork, and only then goes on writing: the sharer keeps its bits."""
+    bs, n, stride, n_kv, hd, past = 64, 32, 6, 2, 64, 230
+    kv, K, V = pool(n, bs, n_kv, hd)
+    Kf, Vf = kv.kv_tensors()
+    Kf.normal_(), Vf.normal_()
+    mine = [9, 30, 2, 17]
+    every = u32([0] * (3 * stride)).view(3, stride)
+    every[0, :4] = u32(mine)
+    shares = u32([0] * n)
+    free, head = u32([0] * 4 + [b for b in range(n) if b not in mine]), u32([4])
+    kv.fork_tables(u32([0]), u32([past]), every[:1], every[1:2], shares, free, head)
+    # row 1 back to `length` keys: its blocks behind go, the one that it ends in stays
+    kv.free_tables(u32([past]), every[1:2], shares, free, head, keep=u32([length]))
+    # so it is forked before it is written, and given up
+    kv.fork_tables(u32([0]), u32([length]), every[1:2], every[2:], shares, free, head)
+    kv.free_tables(u32([length]), every[1:2], shares, free, head)
+    check_pool(every[[0, 2]], [past, length], shares, free, head, n, bs)
+    first, keys = [X[mine].clone() for X in (K, V)], rows_of(K, every, [past], bs)[0]
+    fresh = 70
+    kv.extend_tables(u32([length]), u32([fresh]), every[2:], free, head)
+    q, k, v = (torch.randn(fresh, h, hd, device="cuda") for h in (n_kv, n_kv, n_kv))
+    w, f = torch.ones(hd, device="cuda"), torch.ones(hd // 2, device="cuda")
+    kv.tree_batch_attn_paged(q, k, v, every[2:], u32([length]), u32([0, fresh]),
+                             u32([2 ** 32 - 1] + list(range(fresh - 1))), w, w, f, None, None,
+                             torch.empty_like(q), 1e-6, hd ** -0.5)
+    assert all(torch.equal(X[mine], x) for X, x in zip((K, V), first))
+    assert torch.equal(rows_of(K, every[2:], [length], bs)[0], keys[:length])
+    got = rows_of(V, every[2:], [length + fresh], bs)[0]
+    assert torch.equal(got[length:], v.view(torch.int32))
+    check_pool(every[[0, 2]], [past, length + fresh], shares, free, head, n, bs)
+    assert kv.get_status() == 0
     kv.free()
