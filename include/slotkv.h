@@ -530,6 +530,9 @@ int slot_kv_extend_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
  * zeros.  The results agree with one decode step per node in f32 rounding;
  * they may differ in the last bits between batches.
  *
+ * A call that ends with SLOTKV_DEV_TIMEOUT has left alone every row of out
+ * that a CTA which gave up has a part of; its nodes' K and V are in the cache.
+ *
  * The workspace is allocated by the handle's first such call, at the size of
  * max_rows and max_n_head: make one before capturing into a graph (a call
  * under capture that would have to allocate returns SLOTKV_ERR_STATE).
@@ -907,8 +910,9 @@ int slot_kv_call_shape(slotkv_t handle, uint32_t B, uint32_t bt_stride, uint32_t
  *                             so the consumers' bounded wait expires (after
  *                             about a second), every CTA abandons its work
  *                             and the call ends with SLOTKV_DEV_TIMEOUT set,
- *                             having written nothing.  The context stays
- *                             usable; clear the flags with
+ *                             having written nothing (the tree calls: no
+ *                             row of out; their K and V come before).  The
+ *                             context stays usable; clear the flags with
  *                             slot_kv_get_status and the option with
  *                             slot_kv_set_options(handle, 0).
  * 0 (the default) is the plain form of decode_batch_attn.  SLOTKV_ERR_ARG for

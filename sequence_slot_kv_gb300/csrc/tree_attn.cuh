@@ -587,7 +587,10 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // Every wait is bounded.  Where one runs out, its CTA raises SLOTKV_DEV_TIMEOUT
 // and sets a flag that ends all its other waits at once; the roles go through
 // the rest of their loops without doing anything, so they meet at their barriers
-// and at the end as ever.
+// and at the end as ever.  Such a CTA writes nothing from there on (a role that
+// gave up hands on what it has not formed, so the accumulators look at the flag,
+// not at their own waits alone) and says so beside its unit to join; the
+// combine kernel leaves the rows alone that such a CTA has a part of.
 template <int HD>
 struct TreeCfg {
     static constexpr int KT = 128;                      // keys per tile
@@ -1108,7 +1111,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // the unit's end: O through P's buffer (at head dim 64 with the products of V's low
             // parts beside it), then a factor for every row, and out or the partial result
             float* stage = reinterpret_cast<float*>(smem + C::OFF_P);
-            const bool write = !bar_or(5, !ok) && P.req_of[d[kRow]] == d[kReq];
+            const bool write = !bar_or(5, !ok || misc[0] != 0u) && P.req_of[d[kRow]] == d[kReq];
 #pragma unroll
             for (int h = 0; h < C::DH; ++h)
 #pragma unroll
@@ -1386,11 +1389,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // (the swizzled tiles need the 1 KB alignment that dynamic shared memory starts at)
         if (sbase & 1023u) {
             u[kMore] = 0u;
-            if (lane == 0) atomicOr(P.status, kDevTimeout);
+            misc[0] = 1;
         }
         // nothing for the combine kernel to join from here on, unless there turns out to be
         uint32_t* join = P.join + kTreeJoin * blockIdx.x;
-        if (lane == 0) join[kJoinRows] = 0u;
+        if (lane == 0) join[kJoinRows] = join[kJoinGaveUp] = 0u;
         for (uint32_t n = 0;; ++n) {
             if (n >= 2 && !warp_wait(GE + 8 * (n & 1), ((n >> 1) - 1) & 1)) break;
             if (lane == 0) {
@@ -1518,7 +1521,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 29) tc::tmem_dealloc(tb, C::TMEM_COLS);
-    if (tid == 0 && misc[0]) atomicOr(P.status, kDevTimeout);
+    if (tid == 0 && misc[0]) {
+        atomicOr(P.status, kDevTimeout);
+        P.join[kTreeJoin * blockIdx.x + kJoinGaveUp] = 1u;
+    }
 }
 
 // ------------------------------------------------------------------ combine
@@ -1545,11 +1551,21 @@ __global__ void __launch_bounds__(kJoinThreads) slotkv_tree_combine_kernel(const
     auto slot = [&](uint32_t i) {
         return (2 * static_cast<size_t>(blockIdx.x + i * step) + (i ? 0 : 1)) * RB + row;
     };
+    // whether part i's CTA gave up
+    auto gave_up = [&](uint32_t i) { return __ldcg(P.join + kTreeJoin * (blockIdx.x + i * step) + kJoinGaveUp); };
     float2 ml = make_float2(-1e30f, 0.f);
-    if (static_cast<uint32_t>(lane) < parts) ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(lane));
+    uint32_t lost = 0;
+    if (static_cast<uint32_t>(lane) < parts) {
+        ml = __ldcg(reinterpret_cast<const float2*>(P.part_ml) + slot(lane));
+        lost = gave_up(lane);
+    }
     if (__ldcg(P.req_of + tok) != j1.x) return;  // (refused)
     float m = ml.x;
-    for (uint32_t i = lane + 32; i < parts; i += 32) m = fmaxf(m, __ldcg(P.part_ml + 2 * slot(i)));
+    for (uint32_t i = lane + 32; i < parts; i += 32) {
+        m = fmaxf(m, __ldcg(P.part_ml + 2 * slot(i)));
+        lost |= gave_up(i);
+    }
+    if (__any_sync(0xffffffffu, lost != 0u)) return;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float den = 0.f, acc[E] = {};

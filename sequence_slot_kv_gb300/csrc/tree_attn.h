@@ -51,7 +51,7 @@ constexpr uint32_t kTreeSkip = 0xFFFFFFFFu;
 // Places of a request that 32-bit arithmetic on them leaves room for (a table may name more).
 constexpr uint32_t kTreePlaces = 0x7FFFFF00u;
 // A unit to join: its first node and row, rows (0: none), kv head, request, the step from one
-// of its CTAs to the next, and their number.
+// of its CTAs to the next, and their number; and whether the CTA gave up.
 constexpr uint32_t kTreeJoin = 8;
 // A CTA's plan: what its roles need to know of its first unit (TreeWord) and that unit's
 // tiles, then where to go on: size of the sets, block of a set, request, groups of the size
@@ -60,7 +60,8 @@ constexpr uint32_t kTreeJoin = 8;
 constexpr uint32_t kTreePlan = 28;
 enum TreePlanWord { kPlanUnitTiles = 12, kPlanSize, kPlanMember, kPlanReq, kPlanOver, kPlanOff = 18, kPlanLeft = 20,
                     kPlanEnd = 22, kPlanEach = 24 };
-enum TreeJoinWord { kJoinTok, kJoinRow0, kJoinRows, kJoinKvHead, kJoinReq, kJoinStep, kJoinParts };
+enum TreeJoinWord { kJoinTok, kJoinRow0, kJoinRows, kJoinKvHead, kJoinReq, kJoinStep, kJoinParts,
+                    kJoinGaveUp };
 
 // Rows of a block (a unit of work), and the keys and dims of a piece of V.
 __host__ __device__ constexpr uint32_t tree_rows(int hd) { return hd == 256 ? 32u : 64u; }
