@@ -131,11 +131,32 @@ __device__ __forceinline__ bool fork_needs(const ForkTablesParams& P, uint32_t j
     return ok && past % P.pool.block != 0u;
 }
 
+// The forks of each run of kForkRun that take a block, for calls of more than kForkOne.
+__global__ void __launch_bounds__(kCopyThreads) slotkv_fork_count_kernel(const ForkTablesParams P) {
+    __shared__ uint32_t count;
+    begin_dependent();
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const uint32_t j0 = blockIdx.x * kForkRun, j1 = P.n_fork - j0 < kForkRun ? P.n_fork : j0 + kForkRun;
+    uint32_t n = 0;
+    for (uint32_t j = j0 + threadIdx.x; j < j1; j += kCopyThreads) {
+        bool ok;
+        uint32_t s, past;
+        n += fork_needs(P, j, ok, s, past);
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0 && n) atomicAdd(&count, n);
+    __syncthreads();
+    if (threadIdx.x == 0) P.counts[blockIdx.x] = count;
+}
+
 // CTA (fork, part): counts the forks before its own that take a block, which
 // names its own; part 0 writes the fork's table, and every part copies its
 // share of the partial block.  Every CTA reads the lengths of the forks before it,
 // so that nothing waits: one kernel, and partial blocks at the copy's rate (192 MB in
 // 30 us, 6.4 TB/s; what a call of few rows takes is its four dependent loads).
+// With RUNS it reads those before it in its run, and the counts of the runs before that.
+template <bool RUNS>
 __global__ void __launch_bounds__(kCopyThreads) slotkv_fork_tables_kernel(const ForkTablesParams P) {
     __shared__ uint32_t count;
     begin_dependent();
@@ -145,7 +166,9 @@ __global__ void __launch_bounds__(kCopyThreads) slotkv_fork_tables_kernel(const 
     if (threadIdx.x == 0) count = 0;
     __syncthreads();
     uint32_t before = 0;
-    for (uint32_t j = threadIdx.x; j < i; j += kCopyThreads) {
+    if (RUNS)
+        for (uint32_t c = threadIdx.x; c < i / kForkRun; c += kCopyThreads) before += __ldcg(P.counts + c);
+    for (uint32_t j = threadIdx.x + (RUNS ? i / kForkRun * kForkRun : 0u); j < i; j += kCopyThreads) {
         bool ok;
         uint32_t s, past;
         before += fork_needs(P, j, ok, s, past);
@@ -684,6 +707,11 @@ uint32_t list_ctas(uint64_t n) { return n <= kListWarps ? 1u : kListCtas; }
 // launch against four: 5.8 us against 8.5 at 8 items, 9.0 / 9.3 at 64, 9.7 / 9.8 at
 // 256, 13.5 / 10.1 at 512, 73 / 17 at 4096.
 constexpr uint64_t kListItems = kListWarps * kListCtas;
+// Forks up to which every CTA reads all lengths before its own (forks of two full
+// blocks: 16.7 us against 16.9 with the count kernel at 2048, 20.7 / 17.9 at 2500, 40 / 28
+// at 4096, 5355 / 354 at 65536), and the forks of a run beyond (with 2048 as one run
+// 34 us at 4096, 433 at 65536).
+constexpr uint32_t kForkOne = 2048;
 
 }  // namespace
 
@@ -701,8 +729,13 @@ int launch_fork_tables(const ForkTablesParams& p, uint32_t sms, cudaStream_t str
     uint32_t parts = (4 * sms + forks - 1) / forks;
     parts = parts < most ? parts : static_cast<uint32_t>(most);
     parts = parts < 64u ? parts : 64u;
-    return launch_dependent(slotkv_fork_tables_kernel, dim3(forks, parts ? parts : 1u), kCopyThreads,
-                            0, stream, p);
+    const dim3 grid(forks, parts ? parts : 1u);
+    if (forks <= kForkOne)
+        return launch_dependent(slotkv_fork_tables_kernel<false>, grid, kCopyThreads, 0, stream, p);
+    const int rc = launch_dependent(slotkv_fork_count_kernel, dim3((forks + kForkRun - 1) / kForkRun), kCopyThreads,
+                                    0, stream, p);
+    if (rc != 0) return rc;
+    return launch_dependent(slotkv_fork_tables_kernel<true>, grid, kCopyThreads, 0, stream, p);
 }
 
 int launch_free_tables(const FreeTablesParams& p, uint32_t sms, cudaStream_t stream) {

@@ -37,8 +37,10 @@ struct ForkTablesParams {
     const uint32_t* head;          // [1]
     uint32_t* head_out;            // [1], may be head
     uint32_t* scratch;             // handle-owned: [0] CTAs done (0 between calls), [1] new head
+    uint32_t* counts;              // handle-owned: one per kForkRun forks
     uint32_t n_fork, n_rows, bt_stride, n_free;
 };
+constexpr uint32_t kForkRun = 1024;  // forks that are counted together
 
 struct FreeTablesParams {
     PoolView pool;

@@ -1626,8 +1626,9 @@ int slot_kv_fork_tables(slotkv_t h, uint32_t n_fork, const uint32_t* src, uint32
     }
     const slotkv::ForkTablesParams P{pool_view(h), src,         past, block_tables,
                                      out_tables,   shares,      free_blocks, head,
-                                     head_out,     h->map_scratch, n_fork, n_rows,
-                                     bt_stride,    n_free};
+                                     head_out,     h->map_scratch, h->map_scratch + 2,
+                                     n_fork,       n_rows,      bt_stride, n_free};
+    static_assert(SLOTKV_MAX_REQUESTS / slotkv::kForkRun <= slotkv::kFreeCtas, "counts of the runs");
     const int e = slotkv::launch_fork_tables(P, sm_total(h), (cudaStream_t)stream);
     if (e != 0) return cuda_fail((cudaError_t)e, "fork tables kernel launch");
     return SLOTKV_OK;
