@@ -517,14 +517,25 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // high part.
 //   All of these cuts are toward zero, so they do not average out: left alone the
 // outputs were 0.6, 0.85 and 1.2e-6 too small at head dims 64, 128 and 256, most of
-// their error.  A step of a chain of n (eight products each) cuts its sum by half a
+// their error.  For O what is put back goes by what was cut, so that a row gets
+// its V to the bit where nothing is (one key, or keys of one weight, and V of 11
+// bits).  P's high part is cut from P (1 + 0.36 2^-10): where half of its last place
+// is on average, so that P's low part has both signs, and neither the bits cut off
+// that nor its product with V's low part, which is left out, adds up.  (A P of 11
+// bits stays: 0.36 2^-10 of it is below its last place.)  Of V's 13 low bits 11 are
+// read: of 4094.6 units that is on average 0.875 too few (3/2 where bit 12 is the
+// highest, 1/2 where 11 is), so the sums of products with a low part count 1 +
+// 0.875 / 4094.6 times.
+//   S: a step of a chain of n (eight products each) cuts its sum by half a
 // unit in the last place, 0.36 2^-23 of it on average; a dominant key's score grows
 // evenly, so it ends 0.18 (n + 1) 2^-23 too small, n = hd / 8, which joining the two
-// sums multiplies back.  O's terms have both signs, and its P and V lose (0.69
-// 2^-11)^2 in each of three places (two low parts cut, their product left out): 2 to 4
-// 2^-23 together, fewer where few keys are attended; 2 are put back.  Over 80 drawn
-// cases the outputs' relative error (root mean square) is 1.6 to 5.9e-7 since (up to
-// 1.4e-6 before; the plain f32 form's goes up to 1.6e-6).
+// sums multiplies back.  That is one factor for all scores, so it moves a weight
+// by that part of its distance from the row's highest score; between a key whose
+// product with q grows evenly and one that has it in the last channels, which
+// loses nothing, what was cut from the first remains, with the factor or without.
+//   Over 80 drawn cases the outputs' relative error (root mean square) is 0.8 to
+// 5.5e-7, between 2.6e-7 too small and 0.8e-7 too large (left alone up to 1.4e-6; the
+// plain f32 form's goes up to 1.4e-6).
 //   The A operands come from tensor memory, where a warp's lanes are
 // the operand's rows: K is written there by the thread that owns the key, V^T by
 // the thread that owns the dim, which makes the transposition free (and K's
@@ -610,9 +621,10 @@ struct TreeCfg {
     static constexpr int C_S = 0, C_O = 2 * RB, C_B = C_O + DH * 2 * RB, BCOLS = 64;
     static_assert(C_B + NB * BCOLS <= 512, "tensor memory");
     static constexpr int TMEM_COLS = 512;
-    // what a sum of high products loses on average, put back (see above)
+    // what a chain of S's high products loses on average, and V's low parts (see above)
     static constexpr float ULP = 1.1920929e-7f;
-    static constexpr float UNCUT_S = 1.f + static_cast<int>(0.18 * (HD / 8 + 1) + 0.5) * ULP, UNCUT_O = 1.f + 2 * ULP;
+    static constexpr float UNCUT_S = 1.f + static_cast<int>(0.18 * (HD / 8 + 1) + 0.5) * ULP;
+    static constexpr float UNCUT_V = 1.f + 0.875f / 4094.625f;
     // shared memory behind the ring: row data, scratch of the maxima, barriers, flags
     static constexpr int OFF_M = OFF_RING + NSLOT * PIECE;      // running maxima [2 units][RB]
     static constexpr int OFF_F = OFF_M + 2 * RB * 4;            // factors of a raise, of the end [RB]
@@ -673,15 +685,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
     return __ffma2_rn(b, make_float2(-1.f, -1.f), a);
 }
-// The sums of the high products and of those with a low part, the first times uncut.
-__device__ __forceinline__ float2 join2(float2 hi, float2 lo, float uncut) {
-    return __ffma2_rn(hi, make_float2(uncut, uncut), lo);
+// a times uncut, and b.
+__device__ __forceinline__ float2 join2(float2 a, float2 b, float uncut) {
+    return __ffma2_rn(a, make_float2(uncut, uncut), b);
 }
 // x without its low 13 mantissa bits: what the tensor core reads of it.
 __device__ __forceinline__ uint32_t tf32_part(float x) { return __float_as_uint(x) & 0xFFFFE000u; }
 // The low parts of two values.
 __device__ __forceinline__ float2 low2(float x, float y) {
     return sub2(make_float2(x, y), make_float2(__uint_as_float(tf32_part(x)), __uint_as_float(tf32_part(y))));
+}
+// What the tensor core reads as P's high parts (see above).
+__device__ __forceinline__ float2 near2(float x, float y) {
+    return __ffma2_rn(make_float2(x, y), make_float2(0.36f / 1024.f, 0.36f / 1024.f), make_float2(x, y));
 }
 
 template <int HD, bool SC>
@@ -990,11 +1006,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c += 2) {
                     if (4 * (c / 8 * 8) + 8 * sg < static_cast<int>(Rp)) {
-                        const float2 lo = low2(x[c], x[c + 1]);
+                        const float2 hi = near2(x[c], x[c + 1]);
+                        const float2 lo = sub2(make_float2(x[c], x[c + 1]), make_float2(__uint_as_float(tf32_part(hi.x)),
+                                                                                       __uint_as_float(tf32_part(hi.y))));
                         const int at = (32 * (c / 8) + c % 8) * 128;
-                        sts(dst ^ (c % 8) << 4, at, x[c]);
+                        sts(dst ^ (c % 8) << 4, at, hi.x);
                         sts(dst2 ^ (c % 8) << 4, at, lo.x);
-                        sts(dst ^ (c % 8 + 1) << 4, at + 128, x[c + 1]);
+                        sts(dst ^ (c % 8 + 1) << 4, at + 128, hi.y);
                         sts(dst2 ^ (c % 8 + 1) << 4, at + 128, lo.y);
                     }
                 }
@@ -1028,6 +1046,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t tlane = tb + (static_cast<uint32_t>(w) << 21);
         float* fs = reinterpret_cast<float*>(smem + C::OFF_F);
         const float* sums = reinterpret_cast<const float*>(smem + C::OFF_MAX);
+        const float uncut = C::FOLD && me >= 64 ? C::UNCUT_V : 1.f;  // (FOLD: V's low parts have lanes of their own)
         bool ok = true;
         uint32_t gt = 0;
         for (uint32_t u = 0;; ++u) {
@@ -1098,7 +1117,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         for (int k = 0; k < 16; k += 2) {
                             const float2 hi = make_float2(__uint_as_float(a[k]), __uint_as_float(a[k + 1]));
                             const float2 lo = make_float2(__uint_as_float(b[k]), __uint_as_float(b[k + 1]));
-                            const float2 y = add2(make_float2(o[h][16 * c + k], o[h][16 * c + k + 1]), join2(hi, lo, C::UNCUT_O));
+                            const float2 was = make_float2(o[h][16 * c + k], o[h][16 * c + k + 1]);
+                            const float2 y = C::FOLD ? join2(add2(hi, lo), was, uncut) : add2(join2(lo, hi, C::UNCUT_V), was);
                             o[h][16 * c + k] = y.x;
                             o[h][16 * c + k + 1] = y.y;
                         }
