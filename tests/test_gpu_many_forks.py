@@ -44,3 +44,24 @@ def test_the_time_of_a_call_is_linear_in_the_forks():
     assert shares.tolist() == [0, 0, 0, 4 * (n + n // 16), 0, 4 * (n + n // 16), 0, 0]
     assert bool((out == tables).all()) and kv.get_status() == 0
     kv.free()
+
+
+def test_many_forks_captured_and_replayed():
+    """The call's two kernels in a graph, head advanced in place by every replay."""
+    n, bs, blocks = 3000, 4, 3 * 1500 + 40
+    kv, K, V = pool(blocks, bs, 1, 64)
+    src, past = u32([i % 2 for i in range(n)]), u32([8, 6])
+    tables, out = u32([3, 5, 9, 1]).view(2, 2), u32([0] * (2 * n)).view(n, 2)
+    ids = [b for b in range(blocks) if b not in (3, 5, 9, 1)]
+    shares, free, head = u32([0] * blocks), u32(ids), u32([0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.fork_tables(src, past, tables, out, shares, free, head)
+    for i in range(3):
+        g.replay()
+        took = ids[1500 * i:1500 * (i + 1)]
+        assert out[::2].tolist() == [[3, 5]] * 1500 and out[1::2].tolist() == [[9, b] for b in took]
+        assert int(head) == 1500 * (i + 1)
+        assert all(torch.equal(X[took, :2], X[1, :2].expand(1500, -1, -1, -1)) for X in (K, V))
+    assert [int(shares[b]) for b in (3, 5, 9, 1)] == [4500, 4500, 4500, 0] and kv.get_status() == 0
+    kv.free()
