@@ -112,9 +112,10 @@ struct slotkv_s {
     float* sc_part[2] = {};           // acc then (m, l), each of partial_rows() head rows
     uint32_t* map_scratch = nullptr;  // table calls: CTA counter, new head, counts
     // tree calls: views of the buffers for slots [0] and pages [1], keys of a
-    // box of K in each (0: no pages); per-node words (request, depth,
-    // ancestors) and the requests' first tiles, and partial results, allocated by
-    // the first one (their rotated q is sc_q); slot_kv_compact_pool's map of ids
+    // box of K in each (0: no pages); where each CTA's work begins, the units to
+    // join and per-node words (the nodes that attend it, request, depth), and
+    // partial results, allocated by the first one (their rotated q is sc_q);
+    // slot_kv_compact_pool's map of ids
     CUtensorMap tmKt[2], tmVt[2];
     uint32_t tree_box[2] = {};
     uint32_t* tree_idx = nullptr;

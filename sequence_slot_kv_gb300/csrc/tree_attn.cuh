@@ -580,16 +580,22 @@ __global__ void __launch_bounds__(kPrepThreads) slotkv_tree_prep_kernel(const Tr
 // joins them in the groups' order.
 //
 // What bounds it.  24 requests of 4000 keys, 8 kv heads of 128: 8 rows a kv head in
-// 147 us, 5.4 TB/s (HBM, at 79 % of what a copy has with all of the call's three
-// kernels counted); 64 rows 166; 128 rows 274; 256 rows 517, 512 rows 1035: 3.2 us for a
+// 144 us, 5.5 TB/s (HBM, at 81 % of what a copy has with all of the call's three
+// kernels counted); 64 rows 163; 128 rows 276; 256 rows 517, 512 rows 1038: 3.2 us for a
 // tile of 64 rows and 128 keys, 6200 cycles, of which the MMAs alone take 3450 (they
-// are active 53 % of the time).  The rest is the converters, 80 % busy with latencies
-// (shared memory that the MMAs, TMA, P and they share, tensor memory, barriers), in
-// issue slots that are 62 % used; what waits on them fills the other roles' time.
-// 256 rows read 838 MB from HBM, K and V once (3.2 GB without the sets above).
-// Code size counts: the roles run different code side by side, and what does not fit the
+// are active 55 % of the kernel's time).  The rest is the converters, 81 % busy with
+// latencies (shared memory that the MMAs, TMA, P and they share, tensor memory,
+// barriers), in issue slots that are 64 % used; what waits on them fills the other
+// roles' time.  256 rows read 837 MB from HBM, K and V once (3.2 GB without the sets above).
+//   8 kv heads of 64: 8 rows 104 us, 64 rows 124, 256 rows 398, 512 rows 806: 2.5 us a
+// tile of 64 rows, MMAs 40 %, converters 83 %, issue slots 69 %.  4 kv heads of 256: 8 rows
+// 139 us (5.7 TB/s), 32 rows 147, 54 rows 194, 256 rows 707: 4.4 us a tile of 32 rows, twice
+// the bytes of one of 128, each block's CTA converting all of them (54 rows: MMAs
+// 36 %, issue slots 53 %).
+//   Code size counts: the roles run different code side by side, and what does not fit the
 // instruction caches is fetched again every tile (the producer's loop unrolled costs
-// 5 to 15 %).
+// 5 to 15 %).  In the 64 registers of the launch 20 words of a thread are spilled at head
+// dim 128, 13 at 64 and none at 256.
 //
 // Keys past the request's last are zeros in V; a masked key's P is -0.  A V value
 // that is not finite is a 0 to the tensor core, and the accumulators add it to
