@@ -531,7 +531,7 @@ int slot_kv_extend_tables(slotkv_t handle, uint32_t n_req, const uint32_t* past,
  * they may differ in the last bits between batches.
  *
  * A call that ends with SLOTKV_DEV_TIMEOUT has left alone every row of out
- * that a CTA which gave up has a part of; its nodes' K and V are in the cache.
+ * whose attention did not end; its nodes' K and V are in the cache.
  *
  * The workspace is allocated by the handle's first such call, at the size of
  * max_rows and max_n_head: make one before capturing into a graph (a call
